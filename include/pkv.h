@@ -106,6 +106,49 @@ int pt_assign(pkv_pt *pt, int seq_len, int *slot_out);
 int pt_reserve(pkv_pt *pt, int slot, int seq_len);
 /* release a live slot and its pages */
 int pt_free(pkv_pt *pt, int slot);
+/* ---------------------------------------------------------------------
+ * Sharing, taking back and moving pages. Each page counts the slots that
+ * hold it; pt_free and pt_truncate let go of a slot's hold, and a page goes
+ * back to the free stack when its last holder lets go. The calls that move
+ * tokens to other pages return (source, destination) page pairs, int32
+ * [n][2] in host memory, for kv_copy_pages: issue that copy on the handle's
+ * stream before the next call that reads or writes the caches (and before
+ * another pt_* call whose pairs could start from these destinations).
+ * Destinations are pages that were free, so they are never sources of the
+ * same call. All are all-or-nothing, and write the device table as
+ * pt_reserve does.
+ *
+ * pt_fork — `count` new slots that hold the first seq_len tokens of a live
+ * slot (a prompt's group of samples): the floor(seq_len / page_size) full
+ * pages are shared; when a partly filled page follows, each new slot gets a
+ * page of its own for it and a pair to copy (count pairs, else none). The
+ * source keeps its pages. seq_len <= the source's capacity; a new slot's
+ * capacity is its pages. A shared page must not be written: no slot may
+ * append at a position below a seq_len it was forked at (or forked others
+ * at) without pt_unshare first. Errors: PKV_E_BAD_SLOT, PKV_E_NO_SLOT,
+ * PKV_E_NO_PAGES, PKV_E_BAD_ARG.
+ *
+ * pt_unshare — gives the slot pages of its own for the shared pages under
+ * its tokens [begin, end), end <= capacity, with a pair for each (before a
+ * rewritten token, e.g. after a rewind behind a fork).
+ *
+ * pt_truncate — keeps the pages of the first seq_len tokens (<= capacity)
+ * and lets go of the rest, last page first; the table entries become -1.
+ *
+ * pt_compact — with U pages in use, moves those numbered above U to the free
+ * pages among 1..U (both ascending), in every slot that holds them; the free
+ * stack becomes [n_pages-1 .. U+1], so the used pages are exactly 1..U.
+ * pairs_out NULL: only counts the pairs (nothing changes).
+ *
+ * pt_page_refs — the number of slots that hold a page (0: free).
+ * ------------------------------------------------------------------- */
+int pt_fork(pkv_pt *pt, int src_slot, int seq_len, int count, int *slots_out,
+            int32_t *pairs_out, int max_pairs, int *n_pairs);
+int pt_unshare(pkv_pt *pt, int slot, int begin, int end, int32_t *pairs_out,
+               int max_pairs, int *n_pairs);
+int pt_truncate(pkv_pt *pt, int slot, int seq_len);
+int pt_compact(pkv_pt *pt, int32_t *pairs_out, int max_pairs, int *n_pairs);
+int pt_page_refs(const pkv_pt *pt, int page, int *n);
 /* tokens reserved for a slot (0 for a free slot) */
 int pt_capacity(const pkv_pt *pt, int slot, int *tokens);
 /* pages of a slot in logical order (host mirror); *n receives the count */
@@ -142,6 +185,25 @@ int kv_append_prefill(const pkv_bf16 *k, const pkv_bf16 *v, const int32_t *batch
                       int n_slots, int max_pages_per_seq, int page_size, int n_pages,
                       pkv_bf16 *k_cache, pkv_bf16 *v_cache, int Hkv, int D,
                       int32_t *err_word, void *stream);
+
+/* ---------------------------------------------------------------------
+ * kv_copy_pages — copies pages inside caches: for every cache c, head h <
+ * heads[c] and pair (a, b), page b of the head becomes page a. A cache is
+ * heads[c] x n_pages pages of page_bytes[c] contiguous bytes each, any
+ * element type: a bf16 cache (page_size * D * 2 bytes a page), an 8-bit one
+ * (page_size * D) or its scales (page_size / scale_block * 4), all the layers
+ * of a model in one call. caches, heads, page_bytes ([n_caches]) and pairs
+ * (int32 [n_pairs][2]) are host arrays, read before the call returns; the
+ * cache pointers are device memory. Refused with PKV_E_BAD_ARG: a page
+ * outside [0, n_pages), a destination named twice or also a source (the
+ * copies run in any order), NULL pointers, sizes below 1, and a cache of
+ * 2^46 bytes or more. Any alignment is accepted; 16-byte aligned
+ * caches and page sizes copy fastest. n_pairs 0 launches nothing. A captured
+ * call repeats the same pairs.
+ * ------------------------------------------------------------------- */
+int kv_copy_pages(void *const *caches, const int *heads, const int64_t *page_bytes,
+                  int n_caches, int n_pages, const int32_t *pairs, int n_pairs,
+                  void *stream);
 
 /* ---------------------------------------------------------------------
  * qk_norm_rope — per-head RMSNorm then RoPE, in place ([P1] attention

@@ -70,6 +70,14 @@ _SIGS = {
     "pt_assign": (_c_int, [_c_p, _c_int, ctypes.POINTER(_c_int)]),
     "pt_reserve": (_c_int, [_c_p, _c_int, _c_int]),
     "pt_free": (_c_int, [_c_p, _c_int]),
+    "pt_fork": (_c_int, [_c_p, _c_int, _c_int, _c_int, ctypes.POINTER(_c_int), _c_ip, _c_int,
+                         ctypes.POINTER(_c_int)]),
+    "pt_unshare": (_c_int, [_c_p, _c_int, _c_int, _c_int, _c_ip, _c_int,
+                            ctypes.POINTER(_c_int)]),
+    "pt_truncate": (_c_int, [_c_p, _c_int, _c_int]),
+    "pt_compact": (_c_int, [_c_p, _c_ip, _c_int, ctypes.POINTER(_c_int)]),
+    "pt_page_refs": (_c_int, [_c_p, _c_int, ctypes.POINTER(_c_int)]),
+    "kv_copy_pages": (_c_int, [_c_p, _c_p, _c_p, _c_int, _c_int, _c_p, _c_int, _c_p]),
     "pt_capacity": (_c_int, [_c_p, _c_int, ctypes.POINTER(_c_int)]),
     "pt_pages": (_c_int, [_c_p, _c_int, _c_ip, _c_int, ctypes.POINTER(_c_int)]),
     "pt_free_pages": (_c_int, [_c_p, ctypes.POINTER(_c_int)]),
@@ -214,6 +222,53 @@ def pt_free(h: int, slot: int) -> None:
     _check(load_library().pt_free(h, slot), "pt_free")
 
 
+def _pairs(n: int) -> torch.Tensor:
+    return torch.empty((n, 2), dtype=torch.int32)
+
+
+def pt_fork(h: int, src_slot: int, seq_len: int, count: int = 1):
+    """`count` new slots holding the first seq_len tokens of src_slot; returns
+    (slots, pairs): the pages to copy with kv_copy_pages (CPU int32 [n][2])."""
+    slots = (_c_int * max(count, 1))()
+    pairs = _pairs(max(count, 1))
+    n = _c_int()
+    _check(load_library().pt_fork(h, src_slot, seq_len, count, slots,
+                                  ctypes.cast(pairs.data_ptr(), _c_ip), pairs.shape[0],
+                                  ctypes.byref(n)), "pt_fork")
+    return list(slots), pairs[:n.value]
+
+
+def pt_unshare(h: int, slot: int, begin: int, end: int) -> torch.Tensor:
+    """Pages of the slot's own under tokens [begin, end); returns the pairs."""
+    pairs = _pairs(len(pt_pages(h, slot)))
+    n = _c_int()
+    _check(load_library().pt_unshare(h, slot, begin, end,
+                                     ctypes.cast(pairs.data_ptr(), _c_ip), pairs.shape[0],
+                                     ctypes.byref(n)), "pt_unshare")
+    return pairs[:n.value]
+
+
+def pt_truncate(h: int, slot: int, seq_len: int) -> None:
+    _check(load_library().pt_truncate(h, slot, seq_len), "pt_truncate")
+
+
+def pt_compact(h: int) -> torch.Tensor:
+    """Moves the used pages to the lowest numbers; returns the pairs."""
+    lib = load_library()
+    n = _c_int()
+    _check(lib.pt_compact(h, None, 0, ctypes.byref(n)), "pt_compact")
+    pairs = _pairs(max(n.value, 1))
+    _check(lib.pt_compact(h, ctypes.cast(pairs.data_ptr(), _c_ip), pairs.shape[0],
+                          ctypes.byref(n)), "pt_compact")
+    return pairs[:n.value]
+
+
+def pt_page_refs(h: int, page: int) -> int:
+    n = _c_int()
+    _check(load_library().pt_page_refs(h, page, ctypes.byref(n)), "pt_page_refs")
+    return n.value
+
+
 def pt_capacity(h: int, slot: int) -> int:
     n = _c_int()
     _check(load_library().pt_capacity(h, slot, ctypes.byref(n)), "pt_capacity")
@@ -286,6 +341,21 @@ class PageTable:
     def free(self, slot):
         pt_free(self.handle, slot)
 
+    def fork(self, slot, seq_len, count=1):
+        return pt_fork(self.handle, slot, seq_len, count)
+
+    def unshare(self, slot, begin, end):
+        return pt_unshare(self.handle, slot, begin, end)
+
+    def truncate(self, slot, seq_len):
+        pt_truncate(self.handle, slot, seq_len)
+
+    def compact(self):
+        return pt_compact(self.handle)
+
+    def page_refs(self, page):
+        return pt_page_refs(self.handle, page)
+
     def capacity(self, slot):
         return pt_capacity(self.handle, slot)
 
@@ -324,6 +394,32 @@ def kv_append_prefill(k, v, batch_idx, input_pos, dev_table, n_slots, max_pages_
         _ptr(k), _ptr(v), _ptr(batch_idx), _ptr(input_pos), L, _ptr(dev_table), n_slots,
         max_pages_per_seq, page_size, n_pages, _ptr(k_cache), _ptr(v_cache), Hkv, D,
         _ptr(err_word), _stream(stream)), "kv_append_prefill")
+
+
+def kv_copy_pages(caches, n_pages, pairs, stream=None) -> None:
+    """Copies page pairs[i][0] to page pairs[i][1] of every head of every cache
+    in `caches` (contiguous device tensors [heads][...], each head n_pages
+    pages: K and V caches, scales, any number of layers). pairs: CPU int32
+    [n][2], as pt_fork, pt_unshare and pt_compact return, or a sequence of
+    (source, destination)."""
+    if not isinstance(pairs, torch.Tensor):
+        pairs = torch.tensor(list(pairs), dtype=torch.int32).reshape(-1, 2)
+    if (pairs.device.type != "cpu" or pairs.dtype != torch.int32 or pairs.dim() != 2
+            or pairs.shape[1] != 2):
+        raise BadArgError("kv_copy_pages: pairs must be a CPU int32 tensor [n][2]")
+    pairs = pairs.contiguous()
+    n = len(caches)
+    ptrs, heads, nbytes = (_c_p * n)(), (_c_int * n)(), (ctypes.c_int64 * n)()
+    for i, c in enumerate(caches):
+        if not c.is_contiguous() or c.dim() < 2:
+            raise BadArgError("kv_copy_pages: caches must be contiguous tensors [heads][...]")
+        ptrs[i], heads[i] = c.data_ptr(), c.shape[0]
+        size = c.numel() * c.element_size()
+        nbytes[i] = size // max(heads[i] * n_pages, 1)
+        if nbytes[i] * heads[i] * n_pages != size:
+            raise BadArgError("kv_copy_pages: a head of a cache must be n_pages equal pages")
+    _check(load_library().kv_copy_pages(ptrs, heads, nbytes, n, n_pages, pairs.data_ptr(),
+                                        pairs.shape[0], _stream(stream)), "kv_copy_pages")
 
 
 def qk_norm_rope(q, k, gamma_q, gamma_k, pos, theta: float, eps: float = 1e-6,

@@ -13,6 +13,8 @@
 //     logical blocks, or fails with no change;
 //   - erase pushes the slot and appends its pages in reverse order; the
 //     device row stays stale until the slot is allocated again.
+// Pages may be shared by several slots (pt_fork): each page counts the slots
+// that hold it and returns to the free stack when the last one lets go.
 // The host keeps the authoritative copy so no call reads device memory.
 #include <cuda_runtime.h>
 
@@ -33,6 +35,7 @@ struct pkv_pt {
   std::vector<int32_t> table;              // [n_slots][max_pages]
   std::vector<int> capacity;               // tokens per slot
   std::vector<std::vector<int32_t>> pages; // pages per slot, logical order
+  std::vector<int32_t> refs;               // slots holding each page (0: free)
   std::vector<int32_t> free_pages;         // back = next taken
   std::vector<int> free_slots;             // back = next popped
   std::vector<char> live;                  // slot allocated?
@@ -52,6 +55,11 @@ int write_row_range(pkv_pt *pt, int slot, int begin, int count) {
                                  sizeof(int32_t) * count,
                                  cudaMemcpyHostToDevice, pt->stream));
   return PKV_OK;
+}
+
+// Lets go of one hold on page p.
+void release_page(pkv_pt *pt, int32_t p) {
+  if (--pt->refs[p] == 0) pt->free_pages.push_back(p);
 }
 
 bool valid_live(const pkv_pt *pt, int slot) {
@@ -87,6 +95,8 @@ int pt_create(int max_batch_size, int page_size, int n_pages,
   pt->capacity.assign(pt->n_slots, 0);
   pt->pages.assign(pt->n_slots, {});
   pt->live.assign(pt->n_slots, 0);
+  pt->refs.assign(n_pages, 0);
+  pt->free_pages.reserve(n_pages);
   for (int p = n_pages - 1; p >= 1; --p) pt->free_pages.push_back(p);
   for (int s = max_batch_size; s >= 1; --s) pt->free_slots.push_back(s);
   int st = write_row_range(pt, 0, 0, pt->n_slots * max_pages_per_seq);
@@ -148,6 +158,7 @@ static int reserve_impl(pkv_pt *pt, int slot, int seq_len) {
     int32_t p = pt->free_pages[first + i];
     row[start + i] = p;
     pt->pages[slot].push_back(p);
+    pt->refs[p] = 1;
   }
   pt->free_pages.resize(first);
   pt->capacity[slot] = cap + k * pt->page_size;
@@ -203,9 +214,185 @@ int pt_free(pkv_pt *pt, int slot) {
   pt->free_slots.push_back(slot);
   pt->live[slot] = 0;
   auto &pg = pt->pages[slot];
-  for (auto it = pg.rbegin(); it != pg.rend(); ++it) pt->free_pages.push_back(*it);
+  for (auto it = pg.rbegin(); it != pg.rend(); ++it) release_page(pt, *it);
   pg.clear();
   pt->capacity[slot] = 0;
+  return pkv::ok();
+}
+
+// The new slots share the pages that seq_len tokens fill; each gets a page of
+// its own for the partly filled last one, which the caller copies (pairs).
+int pt_fork(pkv_pt *pt, int src_slot, int seq_len, int count, int *slots_out,
+            int32_t *pairs_out, int max_pairs, int *n_pairs) {
+  if (!pt || !slots_out || !n_pairs) return pkv::fail(PKV_E_BAD_ARG, "pt_fork: NULL");
+  if (!valid_live(pt, src_slot))
+    return pkv::fail(PKV_E_BAD_SLOT, "pt_fork: slot %d not allocated", src_slot);
+  if (count < 1) return pkv::fail(PKV_E_BAD_ARG, "pt_fork: count must be >= 1");
+  if (seq_len < 0 || seq_len > pt->capacity[src_slot])
+    return pkv::fail(PKV_E_BAD_ARG, "pt_fork: %d tokens, slot %d holds %d", seq_len, src_slot,
+                     pt->capacity[src_slot]);
+  if (count > static_cast<int>(pt->free_slots.size()))
+    return pkv::fail(PKV_E_NO_SLOT, "pt_fork: need %d slots, %zu free", count,
+                     pt->free_slots.size());
+  const int shared = seq_len / pt->page_size;
+  const bool tail = seq_len % pt->page_size != 0;
+  const int need = tail ? count : 0;
+  if (need > static_cast<int>(pt->free_pages.size()))
+    return pkv::fail(PKV_E_NO_PAGES, "pt_fork: need %d pages, %zu free", need,
+                     pt->free_pages.size());
+  if (need > 0 && (!pairs_out || max_pairs < need))
+    return pkv::fail(PKV_E_BAD_ARG, "pt_fork: room for %d pairs needed", need);
+  try {   // room first, so that nothing below can throw
+    for (int i = 0; i < count; ++i)
+      pt->pages[pt->free_slots[pt->free_slots.size() - 1 - i]].reserve(shared + 1);
+  } catch (...) {
+    return pkv::fail(PKV_E_BAD_ARG, "pt_fork: out of host memory");
+  }
+  const int32_t *from = pt->table.data() + static_cast<size_t>(src_slot) * pt->max_pages;
+  for (int i = 0; i < count; ++i) {
+    const int slot = pt->free_slots.back();
+    pt->free_slots.pop_back();
+    pt->live[slot] = 1;
+    int32_t *row = pt->table.data() + static_cast<size_t>(slot) * pt->max_pages;
+    std::fill(row, row + pt->max_pages, -1);
+    pt->pages[slot].clear();
+    for (int b = 0; b < shared; ++b) {
+      row[b] = from[b];
+      pt->pages[slot].push_back(from[b]);
+      ++pt->refs[from[b]];
+    }
+    if (tail) {
+      const int32_t p = pt->free_pages.back();
+      pt->free_pages.pop_back();
+      pt->refs[p] = 1;
+      row[shared] = p;
+      pt->pages[slot].push_back(p);
+      pairs_out[2 * i] = from[shared];
+      pairs_out[2 * i + 1] = p;
+    }
+    pt->capacity[slot] = static_cast<int>(pt->pages[slot].size()) * pt->page_size;
+    slots_out[i] = slot;
+  }
+  *n_pairs = need;
+  for (int i = 0; i < count; ++i) {
+    const int st = write_row_range(pt, slots_out[i], 0, pt->max_pages);
+    if (st != PKV_OK) return st;
+  }
+  return pkv::ok();
+}
+
+// Gives the slot pages of its own for the shared ones under tokens [begin, end).
+int pt_unshare(pkv_pt *pt, int slot, int begin, int end, int32_t *pairs_out, int max_pairs,
+               int *n_pairs) {
+  if (!pt || !n_pairs) return pkv::fail(PKV_E_BAD_ARG, "pt_unshare: NULL");
+  if (!valid_live(pt, slot))
+    return pkv::fail(PKV_E_BAD_SLOT, "pt_unshare: slot %d not allocated", slot);
+  if (begin < 0 || end < begin || end > pt->capacity[slot])
+    return pkv::fail(PKV_E_BAD_ARG, "pt_unshare: tokens [%d, %d), slot %d holds %d", begin, end,
+                     slot, pt->capacity[slot]);
+  const int b0 = begin / pt->page_size;
+  const int b1 = end > begin ? (end - 1) / pt->page_size + 1 : b0;
+  int need = 0;
+  for (int b = b0; b < b1; ++b) need += pt->refs[pt->pages[slot][b]] > 1;
+  if (need > static_cast<int>(pt->free_pages.size()))
+    return pkv::fail(PKV_E_NO_PAGES, "pt_unshare: need %d pages, %zu free", need,
+                     pt->free_pages.size());
+  if (need > 0 && (!pairs_out || max_pairs < need))
+    return pkv::fail(PKV_E_BAD_ARG, "pt_unshare: room for %d pairs needed", need);
+  int32_t *row = pt->table.data() + static_cast<size_t>(slot) * pt->max_pages;
+  int n = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int32_t old = pt->pages[slot][b];
+    if (pt->refs[old] <= 1) continue;
+    const int32_t p = pt->free_pages.back();
+    pt->free_pages.pop_back();
+    pt->refs[p] = 1;
+    --pt->refs[old];
+    pt->pages[slot][b] = row[b] = p;
+    pairs_out[2 * n] = old;
+    pairs_out[2 * n + 1] = p;
+    ++n;
+  }
+  *n_pairs = n;
+  if (n > 0) {
+    const int st = write_row_range(pt, slot, b0, b1 - b0);
+    if (st != PKV_OK) return st;
+  }
+  return pkv::ok();
+}
+
+int pt_truncate(pkv_pt *pt, int slot, int seq_len) {
+  if (!pt) return pkv::fail(PKV_E_BAD_ARG, "pt_truncate: NULL handle");
+  if (!valid_live(pt, slot))
+    return pkv::fail(PKV_E_BAD_SLOT, "pt_truncate: slot %d not allocated", slot);
+  if (seq_len < 0 || seq_len > pt->capacity[slot])
+    return pkv::fail(PKV_E_BAD_ARG, "pt_truncate: %d tokens, slot %d holds %d", seq_len, slot,
+                     pt->capacity[slot]);
+  const int keep = pages_needed(0, seq_len, pt->page_size);
+  auto &pg = pt->pages[slot];
+  const int had = static_cast<int>(pg.size());
+  if (keep == had) return pkv::ok();
+  int32_t *row = pt->table.data() + static_cast<size_t>(slot) * pt->max_pages;
+  while (static_cast<int>(pg.size()) > keep) {
+    release_page(pt, pg.back());
+    pg.pop_back();
+    row[pg.size()] = -1;
+  }
+  pt->capacity[slot] = keep * pt->page_size;
+  const int st = write_row_range(pt, slot, keep, had - keep);
+  if (st != PKV_OK) return st;
+  return pkv::ok();
+}
+
+// With U pages in use, those numbered above U move to the free pages among
+// 1..U, both taken in ascending order.
+int pt_compact(pkv_pt *pt, int32_t *pairs_out, int max_pairs, int *n_pairs) {
+  if (!pt || !n_pairs) return pkv::fail(PKV_E_BAD_ARG, "pt_compact: NULL");
+  const int used = pt->n_pages - 1 - static_cast<int>(pt->free_pages.size());
+  int moves = 0;
+  for (int p = used + 1; p < pt->n_pages; ++p) moves += pt->refs[p] > 0;
+  *n_pairs = moves;
+  if (!pairs_out) return pkv::ok();   // the count alone
+  if (max_pairs < moves)
+    return pkv::fail(PKV_E_BAD_ARG, "pt_compact: room for %d pairs needed", moves);
+  std::vector<int32_t> to;
+  try {
+    to.assign(pt->n_pages, 0);
+  } catch (...) {
+    return pkv::fail(PKV_E_BAD_ARG, "pt_compact: out of host memory");
+  }
+  int dst = 1, n = 0;
+  for (int p = used + 1; p < pt->n_pages; ++p) {
+    if (pt->refs[p] == 0) continue;
+    while (pt->refs[dst] != 0) ++dst;   // as many free pages below as used ones above
+    to[p] = dst;
+    pt->refs[dst] = pt->refs[p];
+    pt->refs[p] = 0;
+    pairs_out[2 * n] = p;
+    pairs_out[2 * n + 1] = dst;
+    ++n;
+  }
+  for (int s = 1; s < pt->n_slots; ++s) {
+    int32_t *row = pt->table.data() + static_cast<size_t>(s) * pt->max_pages;
+    for (size_t b = 0; b < pt->pages[s].size(); ++b) {
+      const int32_t p = pt->pages[s][b];
+      if (to[p]) pt->pages[s][b] = row[b] = to[p];
+    }
+  }
+  pt->free_pages.clear();   // its room was reserved when the table was made
+  for (int p = pt->n_pages - 1; p > used; --p) pt->free_pages.push_back(p);
+  if (n > 0) {
+    const int st = write_row_range(pt, 0, 0, pt->n_slots * pt->max_pages);
+    if (st != PKV_OK) return st;
+  }
+  return pkv::ok();
+}
+
+int pt_page_refs(const pkv_pt *pt, int page, int *n) {
+  if (!pt || !n) return pkv::fail(PKV_E_BAD_ARG, "pt_page_refs: NULL");
+  if (page < 0 || page >= pt->n_pages)
+    return pkv::fail(PKV_E_BAD_ARG, "pt_page_refs: page %d out of range", page);
+  *n = pt->refs[page];
   return pkv::ok();
 }
 
