@@ -42,6 +42,12 @@
  * The page table is int32 [n_slots][max_pages_per_seq], row-major, with
  * n_slots = max_batch_size + 1; entry [s][j] is the physical page holding
  * logical tokens [j*page_size, (j+1)*page_size) of slot s, or -1.
+ *
+ * 8-bit cache: k_cache and v_cache are pkv_e4m3 of the same shape, each with
+ * fp32 scales [Hkv][n_pages * page_size / scale_block]: scale i of a head
+ * belongs to its rows [i * scale_block, (i + 1) * scale_block), and a row's
+ * value is code * scale. scale_block is a power of two that divides
+ * page_size (1: a scale for each token).
  */
 #ifndef PKV_H
 #define PKV_H
@@ -54,6 +60,7 @@ extern "C" {
 #endif
 
 typedef uint16_t pkv_bf16;
+typedef uint8_t pkv_e4m3;
 typedef struct pkv_pt pkv_pt;
 
 /* status codes */
@@ -70,6 +77,7 @@ typedef struct pkv_pt pkv_pt;
 #define PKV_ERR_PAGE_NEG 4     /* table entry < 0 (unreserved block) */
 #define PKV_ERR_SLOT 8         /* batch index outside [0, n_slots) */
 #define PKV_ERR_TIMEOUT 16     /* a bounded wait on a copy gave up */
+#define PKV_ERR_ORDER 32       /* 8-bit append: tokens of one scale block apart in the call */
 
 /* ---------------------------------------------------------------------
  * PageTable allocator (host) — [P3] PageTable.__init__ / can_reserve /
@@ -185,6 +193,45 @@ int kv_append_prefill(const pkv_bf16 *k, const pkv_bf16 *v, const int32_t *batch
                       int n_slots, int max_pages_per_seq, int page_size, int n_pages,
                       pkv_bf16 *k_cache, pkv_bf16 *v_cache, int Hkv, int D,
                       int32_t *err_word, void *stream);
+
+/* ---------------------------------------------------------------------
+ * kv_append_q8 — kv_append into the 8-bit cache. For each (kv head, scale
+ * block) that the call's tokens fall in, K and V each on their own:
+ *   a    = the largest finite |x| of the call's tokens in the block,
+ *   need = the smallest power of two with a / need <= 448 (at least 2^-126),
+ *   s    = need when the tokens include the block's first row, which starts
+ *          the block anew, else max(the scale held, need),
+ *   code = e4m3(x / s), to the nearest, ties to even, clamped to +-448 (so
+ *          infinities become +-448; NaN stays NaN),
+ * and where s exceeds the scale held, the block's rows before the call's first
+ * become e4m3(code * held / s) (exact but for values that leave e4m3's normal
+ * range). Scales so written are powers of two; one held that is not is
+ * rounded up to one first, and one that is not finite and positive counts as
+ * 0, which clears the rows before. Rows of the block behind the call's
+ * tokens are not rescaled: appending in the middle of a block drops what it
+ * held behind. Rows on slot 0 (padding) are skipped.
+ * The tokens of one block must stand next to each other in the call, at
+ * ascending positions (as a packed prompt's do). A call whose tokens do not
+ * (or name a position twice) sets PKV_ERR_ORDER and leaves the blocks
+ * concerned unspecified. Other errors as in kv_append.
+ * k, v: bf16 [B][Hkv][D]. Requires D % 16 == 0 and 16-byte aligned k, v and
+ * caches. One kernel, no workspace.
+ * ------------------------------------------------------------------- */
+int kv_append_q8(const pkv_bf16 *k, const pkv_bf16 *v, const int32_t *batch_idx,
+                 const int32_t *input_pos, int B, const int32_t *dev_table,
+                 int n_slots, int max_pages_per_seq, int page_size, int n_pages,
+                 int scale_block, pkv_e4m3 *k_cache, pkv_e4m3 *v_cache,
+                 float *k_scale, float *v_scale, int Hkv, int D,
+                 int32_t *err_word, void *stream);
+/* kv_append_prefill_q8 — the same with k and v head-major bf16 [Hkv][L][D]
+ * (kv_append_prefill's layout). */
+int kv_append_prefill_q8(const pkv_bf16 *k, const pkv_bf16 *v,
+                         const int32_t *batch_idx, const int32_t *input_pos, int L,
+                         const int32_t *dev_table, int n_slots,
+                         int max_pages_per_seq, int page_size, int n_pages,
+                         int scale_block, pkv_e4m3 *k_cache, pkv_e4m3 *v_cache,
+                         float *k_scale, float *v_scale, int Hkv, int D,
+                         int32_t *err_word, void *stream);
 
 /* ---------------------------------------------------------------------
  * kv_copy_pages — copies pages inside caches: for every cache c, head h <
@@ -309,6 +356,35 @@ int paged_decode_attn_splits(int B, int Hkv, int D, int max_pages_per_seq,
                              int page_size, int window, int *num_splits);
 /* workspace bytes for up to num_splits parts per row (0 when num_splits <= 1) */
 size_t paged_decode_attn_workspace(int B, int Hq, int D, int num_splits);
+
+/* ---------------------------------------------------------------------
+ * paged_decode_attn_q8 — paged_decode_attn over the 8-bit cache, with
+ * k_j = k_code_j * k_scale, v_j = v_code_j * v_scale of row j's block (any
+ * finite scales >= 0, powers of two or not):
+ *   out[b][h] = sum_j softmax_j(scale * q[b][h] . k_j) v_j
+ * Keys, rows without keys, windows, GQA, table errors and argument limits are
+ * paged_decode_attn's; q must be finite. Values at positions outside a row's
+ * keys are never used (codes there may be NaN, scales anything). Scores,
+ * softmax statistics and outputs are accumulated in fp32; the weights
+ * p_j * v_scale_j enter the product with V as fp16, relative to the row's
+ * largest.
+ * The work is cut over the GPU as in the automatic mode. The workspace must
+ * hold paged_decode_attn_q8_workspace(Hq, Hkv, D) bytes (16-byte aligned),
+ * whatever the batch and the lengths; zero it once before its first use.
+ * Every call leaves its counters zero again, except one that reports
+ * PKV_ERR_TIMEOUT. Calls sharing one workspace must not overlap on the GPU.
+ * ------------------------------------------------------------------- */
+int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache,
+                         const pkv_e4m3 *v_cache, const float *k_scale,
+                         const float *v_scale, const int32_t *dev_table,
+                         int n_slots, int max_pages_per_seq, int page_size,
+                         int n_pages, int scale_block, const int32_t *batch_idx,
+                         const int32_t *seq_lens, int window, float scale, int B,
+                         int Hq, int Hkv, int D, void *workspace,
+                         size_t workspace_bytes, pkv_bf16 *out,
+                         int32_t *err_word, void *stream);
+/* workspace bytes of paged_decode_attn_q8 (0 for sizes it refuses) */
+size_t paged_decode_attn_q8_workspace(int Hq, int Hkv, int D);
 
 /* ---------------------------------------------------------------------
  * paged_decode_step — one decode layer step in one pass: the write-then-

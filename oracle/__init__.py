@@ -11,6 +11,8 @@ computes, written from the pages' statement of the method:
     with length and sliding-window masking, plus its log-sum-exp.
   * ``block_mask`` — logical -> physical conversion of a block mask's kv
     indices through the page table;
+  * ``paged_q8``   — the 8-bit cache: e4m3 rounding, power-of-two scales per block
+    of tokens, the quantising append;
   * ``prefill``    — document-causal (optionally sliding) attention over packed
     prefill tokens, and its block mask (full / partial key blocks).
 
@@ -29,6 +31,8 @@ from .paged_kv import (physical_row, kv_append, gather_pages,
 from .norm_rope import rms_norm, rope, qk_norm_rope, inv_freq, v_norm
 from .attention import decode_attention, decode_attention_row
 from .prefill import prefill_attention, prefill_block_mask, keep_matrix
+from .paged_q8 import (kv_append_q8, dequantise, round_e4m3, need_scale, pow2_at_least,
+                       ERR_ORDER)
 from .block_mask import convert_logical_block_mask
 
 __all__ = [
@@ -38,4 +42,5 @@ __all__ = [
     "rms_norm", "rope", "qk_norm_rope", "inv_freq", "v_norm", "prefill_attention",
     "prefill_block_mask", "keep_matrix", "convert_logical_block_mask",
     "decode_attention", "decode_attention_row",
+    "kv_append_q8", "dequantise", "round_e4m3", "need_scale", "pow2_at_least", "ERR_ORDER",
 ]

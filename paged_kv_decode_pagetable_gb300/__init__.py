@@ -31,6 +31,7 @@ PKV_ERR_PAGE_RANGE = 2
 PKV_ERR_PAGE_NEG = 4
 PKV_ERR_SLOT = 8
 PKV_ERR_TIMEOUT = 16
+PKV_ERR_ORDER = 32
 
 
 class PkvError(RuntimeError):
@@ -87,6 +88,15 @@ _SIGS = {
                            _c_int, _c_p, _c_p, _c_int, _c_int, _c_p, _c_p]),
     "kv_append_prefill": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_int, _c_p, _c_int, _c_int, _c_int,
                                    _c_int, _c_p, _c_p, _c_int, _c_int, _c_p, _c_p]),
+    "kv_append_q8": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_int, _c_p, _c_int, _c_int, _c_int, _c_int,
+                              _c_int, _c_p, _c_p, _c_p, _c_p, _c_int, _c_int, _c_p, _c_p]),
+    "kv_append_prefill_q8": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_int, _c_p, _c_int, _c_int, _c_int,
+                                      _c_int, _c_int, _c_p, _c_p, _c_p, _c_p, _c_int, _c_int,
+                                      _c_p, _c_p]),
+    "paged_decode_attn_q8": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_int, _c_int, _c_int,
+                                      _c_int, _c_int, _c_p, _c_p, _c_int, _c_f, _c_int, _c_int,
+                                      _c_int, _c_int, _c_p, _c_sz, _c_p, _c_p, _c_p]),
+    "paged_decode_attn_q8_workspace": (_c_sz, [_c_int, _c_int, _c_int]),
     "prefill_block_mask": (_c_int, [_c_p, _c_int, _c_int, _c_p, _c_p, _c_p, _c_p, _c_p]),
     "convert_logical_block_mask": (_c_int, [_c_p, _c_int, _c_int, _c_p, _c_int, _c_int, _c_int,
                                             _c_int, _c_p, _c_int, _c_p, _c_p, _c_p]),
@@ -396,6 +406,61 @@ def kv_append_prefill(k, v, batch_idx, input_pos, dev_table, n_slots, max_pages_
         _ptr(err_word), _stream(stream)), "kv_append_prefill")
 
 
+def _q8_cache(k_cache, v_cache, k_scale, v_scale, n_rows: int) -> int:
+    """Checks an 8-bit cache's tensors; returns the tokens that share a scale."""
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype != torch.float8_e4m3fn or not t.is_contiguous() or t.dim() != 3:
+            raise BadArgError(f"{name} must be a contiguous float8_e4m3fn tensor "
+                              "[Hkv][n_pages * page_size][D]")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t.dtype != torch.float32 or not t.is_contiguous() or t.dim() != 2:
+            raise BadArgError(f"{name} must be a contiguous float32 tensor "
+                              "[Hkv][n_pages * page_size / scale_block]")
+    if v_cache.shape != k_cache.shape or k_cache.shape[1] != n_rows:
+        raise BadArgError("k_cache and v_cache must both hold n_pages * page_size rows")
+    n = k_scale.shape[1]
+    if v_scale.shape != k_scale.shape or k_scale.shape[0] != k_cache.shape[0] or n < 1 \
+            or n_rows % n:
+        raise BadArgError("k_scale and v_scale must both be [Hkv][n_pages * page_size / "
+                          "scale_block]")
+    return n_rows // n
+
+
+def kv_append_q8(k, v, batch_idx, input_pos, dev_table, n_slots, max_pages_per_seq, page_size,
+                 n_pages, k_cache, v_cache, k_scale, v_scale, err_word=None,
+                 stream=None) -> None:
+    """kv_append into the 8-bit cache (float8_e4m3fn codes, fp32 scales
+    [Hkv][n_pages * page_size / scale_block]); k and v are bf16 [B][Hkv][D]."""
+    _bf16(k, "k"), _bf16(v, "v")
+    _i32(batch_idx, "batch_idx"), _i32(input_pos, "input_pos"), _i32(dev_table, "dev_table")
+    block = _q8_cache(k_cache, v_cache, k_scale, v_scale, n_pages * page_size)
+    B, Hkv, D = k.shape
+    if v.shape != k.shape or (Hkv, D) != (k_cache.shape[0], k_cache.shape[2]):
+        raise BadArgError("kv_append_q8: k, v and the caches differ in heads or head dim")
+    _check(load_library().kv_append_q8(
+        _ptr(k), _ptr(v), _ptr(batch_idx), _ptr(input_pos), B, _ptr(dev_table), n_slots,
+        max_pages_per_seq, page_size, n_pages, block, _ptr(k_cache), _ptr(v_cache),
+        _ptr(k_scale), _ptr(v_scale), Hkv, D, _ptr(err_word), _stream(stream)), "kv_append_q8")
+
+
+def kv_append_prefill_q8(k, v, batch_idx, input_pos, dev_table, n_slots, max_pages_per_seq,
+                         page_size, n_pages, k_cache, v_cache, k_scale, v_scale, err_word=None,
+                         stream=None) -> None:
+    """kv_append_q8 of L packed prefill tokens; k and v are head-major
+    [Hkv][L][D]."""
+    _bf16(k, "k"), _bf16(v, "v")
+    _i32(batch_idx, "batch_idx"), _i32(input_pos, "input_pos"), _i32(dev_table, "dev_table")
+    block = _q8_cache(k_cache, v_cache, k_scale, v_scale, n_pages * page_size)
+    Hkv, L, D = k.shape
+    if v.shape != k.shape or (Hkv, D) != (k_cache.shape[0], k_cache.shape[2]):
+        raise BadArgError("kv_append_prefill_q8: k, v and the caches differ in heads or head dim")
+    _check(load_library().kv_append_prefill_q8(
+        _ptr(k), _ptr(v), _ptr(batch_idx), _ptr(input_pos), L, _ptr(dev_table), n_slots,
+        max_pages_per_seq, page_size, n_pages, block, _ptr(k_cache), _ptr(v_cache),
+        _ptr(k_scale), _ptr(v_scale), Hkv, D, _ptr(err_word), _stream(stream)),
+        "kv_append_prefill_q8")
+
+
 def kv_copy_pages(caches, n_pages, pairs, stream=None) -> None:
     """Copies page pairs[i][0] to page pairs[i][1] of every head of every cache
     in `caches` (contiguous device tensors [heads][...], each head n_pages
@@ -487,6 +552,30 @@ def paged_decode_attn(q, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq
         page_size, n_pages, _ptr(batch_idx), _ptr(seq_lens), int(window), float(scale), B, Hq,
         Hkv, D, int(num_splits), _ptr(workspace), ws_bytes, _ptr(out), _ptr(err_word),
         _stream(stream)), "paged_decode_attn")
+
+
+def paged_decode_attn_q8_workspace(Hq, Hkv, D) -> int:
+    return int(load_library().paged_decode_attn_q8_workspace(Hq, Hkv, D))
+
+
+def paged_decode_attn_q8(q, k_cache, v_cache, k_scale, v_scale, dev_table, n_slots,
+                         max_pages_per_seq, page_size, n_pages, batch_idx, seq_lens, window,
+                         scale, workspace, out, err_word=None, stream=None) -> None:
+    """paged_decode_attn over the 8-bit cache (see kv_append_q8). workspace: a
+    zeroed byte tensor of paged_decode_attn_q8_workspace(Hq, Hkv, D)."""
+    _bf16(q, "q"), _bf16(out, "out")
+    _i32(dev_table, "dev_table"), _i32(batch_idx, "batch_idx"), _i32(seq_lens, "seq_lens")
+    block = _q8_cache(k_cache, v_cache, k_scale, v_scale, n_pages * page_size)
+    B, Hq, D = q.shape
+    Hkv = k_cache.shape[0]
+    if D != k_cache.shape[2] or out.shape != q.shape:
+        raise BadArgError("paged_decode_attn_q8: q, out and the caches differ in shape")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load_library().paged_decode_attn_q8(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(dev_table),
+        n_slots, max_pages_per_seq, page_size, n_pages, block, _ptr(batch_idx), _ptr(seq_lens),
+        int(window), float(scale), B, Hq, Hkv, D, _ptr(workspace), ws_bytes, _ptr(out),
+        _ptr(err_word), _stream(stream)), "paged_decode_attn_q8")
 
 
 def paged_decode_step(q, k, v, gamma_q, gamma_k, batch_idx, input_pos, theta, eps, dev_table,

@@ -21,7 +21,8 @@ import dataclasses
 import numpy as np
 import torch
 
-from . import (PageTable, kv_append, paged_decode_attn, paged_decode_attn_splits,
+from . import (NoPagesError, NoSlotError, PageTable, kv_append, kv_append_q8, kv_copy_pages, paged_decode_attn,
+               paged_decode_attn_q8, paged_decode_attn_q8_workspace, paged_decode_attn_splits,
                paged_decode_attn_workspace, paged_decode_step, paged_decode_step_ex,
                qk_norm_rope, qkv_norm_rope)
 
@@ -54,6 +55,27 @@ def alloc_cache(Hkv: int, n_pages: int, page_size: int, D: int, device, fill: st
     return k, v
 
 
+def alloc_cache_q8(Hkv: int, n_pages: int, page_size: int, D: int, device,
+                   scale_block: int = 16):
+    """K and V caches in 8 bits with a scale per kv head and scale_block tokens:
+    (k, v, k_scale, v_scale), e4m3 [Hkv][n_pages * page_size][D] and fp32
+    [Hkv][n_pages * page_size / scale_block], zeroed."""
+    rows = n_pages * page_size
+    k, v = (torch.zeros((Hkv, rows, D), dtype=torch.uint8, device=device)
+            .view(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.zeros((Hkv, rows // scale_block), device=device) for _ in range(2))
+    return k, v, ks, vs
+
+
+class AttnWorkspaceQ8:
+    """Workspace of the 8-bit cache's attention: sized by the heads alone, zeroed
+    once."""
+
+    def __init__(self, Hq, Hkv, D, device):
+        self.buf = torch.zeros(paged_decode_attn_q8_workspace(Hq, Hkv, D), dtype=torch.uint8,
+                               device=device)
+
+
 class AttnWorkspace:
     """Split mode and workspace for one (B, Hq, Hkv, D, table, window) shape.
 
@@ -74,8 +96,12 @@ class AttnWorkspace:
 def decode_layer_step(spec: LayerSpec, pt: PageTable, k_cache, v_cache, q, k, v, batch_idx,
                       input_pos, seq_lens, out, ws: AttnWorkspace, gamma_q=None, gamma_k=None,
                       eps: float = 1e-6, scale: float | None = None, err=None, stream=None,
-                      table=None, fused: bool = True):
+                      table=None, fused: bool = True, k_scale=None, v_scale=None):
     """One layer's decode step: q/k norm + RoPE, K/V append, attention.
+
+    k_scale and v_scale given: the caches are 8-bit ones (alloc_cache_q8) and ws an
+    AttnWorkspaceQ8; the step is then the chain qk_norm_rope (qkv_norm_rope) ->
+    kv_append_q8 -> paged_decode_attn_q8.
 
     fused (default, rotary layers): one paged_decode_step(_ex) call; q, k and
     v are read only and seq_lens must equal input_pos + 1 (the kernel derives
@@ -91,7 +117,10 @@ def decode_layer_step(spec: LayerSpec, pt: PageTable, k_cache, v_cache, q, k, v,
     gk = gamma_k if spec.qk_norm else None
     if spec.gemma_options and not spec.rope:
         raise ValueError("rotary_dims, v_norm and k_eq_v need a rotary layer")
-    if fused and spec.rope:
+    q8 = k_scale is not None
+    if q8 != (v_scale is not None):
+        raise ValueError("give both k_scale and v_scale, or neither")
+    if fused and spec.rope and not q8:
         if spec.gemma_options:
             paged_decode_step_ex(q, k, v, gq, gk, batch_idx, input_pos, spec.theta, eps,
                                  spec.rotary_dims or None, spec.v_norm, spec.k_eq_v, table,
@@ -111,6 +140,14 @@ def decode_layer_step(spec: LayerSpec, pt: PageTable, k_cache, v_cache, q, k, v,
                       spec.rotary_dims or None, stream=stream)
     elif spec.rope:
         qk_norm_rope(q, k, gq, gk, input_pos, spec.theta, eps, stream=stream)
+    if q8:
+        kv_append_q8(k, v, batch_idx, input_pos, table, pt.n_slots, pt.max_pages_per_seq,
+                     pt.page_size, pt.n_pages, k_cache, v_cache, k_scale, v_scale, err,
+                     stream=stream)
+        paged_decode_attn_q8(q, k_cache, v_cache, k_scale, v_scale, table, pt.n_slots,
+                             pt.max_pages_per_seq, pt.page_size, pt.n_pages, batch_idx, seq_lens,
+                             spec.window, scale, ws.buf, out, err, stream=stream)
+        return
     kv_append(k, v, batch_idx, input_pos, table, pt.n_slots, pt.max_pages_per_seq,
               pt.page_size, pt.n_pages, k_cache, v_cache, err, stream=stream)
     paged_decode_attn(q, k_cache, v_cache, table, pt.n_slots, pt.max_pages_per_seq,
@@ -277,11 +314,44 @@ class ContinuousBatcher:
                 self.running.append(s)
         return True
 
+    def fork(self, s: Sequence, rids, caches, stream=None) -> list:
+        """Adds a sample of the running sequence `s` for each of `rids` (the group
+        of a prompt, called once it is prefilled): each starts with the tokens s
+        has, on a slot that shares its full pages. `caches` lists every tensor the
+        pages live in (K and V of all layers; with 8-bit caches their scales
+        too); the partly filled pages are copied in one call. Samples that find
+        no slot or page wait to be admitted like any other sequence. Returns the
+        new sequences."""
+        if s not in self.running:
+            raise ValueError(f"sequence {s.rid} is not running")
+        cached = s.total_length - 1      # the last token is appended by the next decode
+        new, pairs = [], []
+        for rid in rids:
+            f = Sequence(rid, s.prompt_len, s.max_new_tokens, s.generated)
+            try:
+                slots, copies = self.pt.fork(s.slot, cached)
+                f.slot = slots[0]
+                pairs += copies.tolist()
+                self.running.append(f)
+                self.events.append(("fork", s.rid, rid))
+            except (NoSlotError, NoPagesError):
+                self.waiting.append(f)
+            new.append(f)
+        kv_copy_pages(caches, self.pt.n_pages, pairs, stream=stream)
+        return new
+
     def run(self, max_steps: int = 100000) -> list:
         for _ in range(max_steps):
             if not self.step():
                 return self.done
         raise RuntimeError("scheduler did not drain")
+
+
+def compact_cache(pt: PageTable, caches, stream=None) -> int:
+    """Moves the used pages to the front of the caches; returns how many moved."""
+    pairs = pt.compact()
+    kv_copy_pages(caches, pt.n_pages, pairs, stream=stream)
+    return len(pairs)
 
 
 class DecodeGraphs:
@@ -290,12 +360,15 @@ class DecodeGraphs:
     copying the step's inputs in). A batch of B rows replays the smallest
     bucket >= B; rows B.. of the bucket are padding rows on slot 0 (the
     reserved slot: no keys, zero output, their append lands in the reserved
-    page 0). The page table is read through pt.dev_table, which the host
-    allocator updates between steps."""
+    page 0; an 8-bit cache skips it). The page table is read through
+    pt.dev_table, which the host allocator updates between steps. With k_scale
+    and v_scale the caches are 8-bit ones."""
 
     def __init__(self, spec: LayerSpec, pt: PageTable, k_cache, v_cache, Hq: int, max_bs: int,
-                 device, gamma_q=None, gamma_k=None, eps: float = 1e-6, ladder=None):
+                 device, gamma_q=None, gamma_k=None, eps: float = 1e-6, ladder=None,
+                 k_scale=None, v_scale=None):
         self.spec, self.pt, self.kc, self.vc = spec, pt, k_cache, v_cache
+        self.ks, self.vs = k_scale, v_scale
         self.gq, self.gk, self.eps = gamma_q, gamma_k, eps
         self.ladder = ladder or bucket_ladder(max_bs)
         Hkv, D = k_cache.shape[0], k_cache.shape[2]
@@ -309,8 +382,11 @@ class DecodeGraphs:
         self.input_pos = torch.zeros(max_bs, **i32)
         self.seq_lens = torch.ones(max_bs, **i32)
         self.err = torch.zeros(1, **i32)
-        self.ws = {b: AttnWorkspace(b, Hq, Hkv, D, pt.max_pages_per_seq, pt.page_size,
-                                    spec.window, device) for b in self.ladder}
+        if k_scale is None:
+            self.ws = {b: AttnWorkspace(b, Hq, Hkv, D, pt.max_pages_per_seq, pt.page_size,
+                                        spec.window, device) for b in self.ladder}
+        else:
+            self.ws = {b: AttnWorkspaceQ8(Hq, Hkv, D, device) for b in self.ladder}
         self.graphs = {}
         for b in reversed(self.ladder):
             self._call(b)                  # eager first use of every kernel
@@ -325,7 +401,7 @@ class DecodeGraphs:
         decode_layer_step(self.spec, self.pt, self.kc, self.vc, self.q[:b], self.k[:b],
                           self.v[:b], self.batch_idx[:b], self.input_pos[:b],
                           self.seq_lens[:b], self.out[:b], self.ws[b], self.gq, self.gk,
-                          self.eps, err=self.err)
+                          self.eps, err=self.err, k_scale=self.ks, v_scale=self.vs)
 
     def step(self, q, k, v, batch_idx, input_pos):
         """Device tensors for B rows; returns the B rows of the output (a view
