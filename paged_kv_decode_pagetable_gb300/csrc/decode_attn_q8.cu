@@ -1,108 +1,903 @@
-// paged_decode_attn_q8: GQA single-token decode attention over the paged 8-bit
-// cache (e4m3 codes, one scale per kv head and block of tokens).
+// paged_decode_attn_q8: split-KV GQA decode attention over the paged 8-bit cache
+// (e4m3 codes, one fp32 scale per kv head and block of tokens).
 //
-// One CTA per (row, query head): its warps take every fourth key, each with
-// an online softmax of its own (running maximum, sum and output in fp32), and
-// join at the end.
+//   s_j = scale * sk_j * (q . ck_j),  out = sum_j softmax(s)_j sv_j cv_j
+//
+// Bound by reading the codes and scales of every key once. Design (GB300):
+//   * work: the 64-key tiles of every (row, kv head), plus one position for each
+//     start of a (row, head), laid on one line from the actual lengths; every
+//     persistent CTA takes an equal share of it. A (row, head) that straddles
+//     CTAs leaves fp32 partials (each CTA has at most one that began before its
+//     share and one that goes on after it, so the workspace is 2 records a CTA);
+//     the CTA that finishes last, found by a counter, joins them in part order,
+//     so no CTA waits for another and the result does not depend on timing;
+//   * one producer warp streams query rows (cp.async.bulk), K and V tiles
+//     (cp.async.bulk.tensor into a swizzled ring) and the tiles' scales
+//     (cp.async) ahead of four consumer warps, looking up the next unit's pages
+//     while the current one moves;
+//   * each consumer warp owns 16 keys of every tile and keeps its own online
+//     softmax over the whole (row, head), so a tile needs no barrier between
+//     warps; the four states are joined once per unit. Keys are the M rows of
+//     S^T = K q^T and head-dim is the M rows of O^T = V^T P^T (mma.sync m16n8k16,
+//     fp16 in, fp32 out), the <= 8 query heads of the group are N; P goes from
+//     one product to the other through movmatrix;
+//   * codes become fp16 in registers (exact). q is scaled by a power of two to
+//     its row's largest magnitude, so it is exact in fp16 too (elements below
+//     2^-14 of the largest lose at most 2^-25 of it). The scale of v is part of
+//     the softmax weight: w_j = 2^(s_j + log2 sv_j - M) with M the running
+//     maximum of that sum, so w is at most 1 and as precise as fp16 allows where
+//     it matters however far the scales lie apart; the denominator keeps a
+//     running maximum of its own, per lane;
+//   * every mbarrier wait is bounded; a wait that gives up sets PKV_ERR_TIMEOUT,
+//     the CTA drains its copies and exits. Invalid table entries are reported
+//     and never dereferenced.
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <mutex>
 
 #include "pkv_internal.h"
 
 namespace {
 
-constexpr int kMaxG = 8;         // query heads per kv head
-constexpr int kMaxRows = 512;
-constexpr int kMaxCtas = 1024;   // CTAs the workspace has room for
+constexpr int kT = 64;               // keys per tile
+constexpr int kCWarps = 4;           // consumer warps, 16 keys of a tile each
+constexpr int kCThreads = kCWarps * 32;
+constexpr int kThreads = kCThreads + 32;   // + producer warp
+constexpr int kMaxG = 8;             // query heads per kv head (MMA N)
+constexpr int kMaxRows = 512;        // rows per call (row cache kept in smem)
+constexpr int kMaxCtas = 1024;       // CTAs the workspace has room for
+constexpr int kSpinLimit = 1 << 22;
+constexpr int kMergeCols = 128;      // columns joined per round of a unit's end
+constexpr int kMergeRow = kMergeCols + 4;   // padded: conflict-free 8-byte stores
 
+template <int D>
+struct Cfg {
+  static constexpr int CTAS_PER_SM = D <= 256 ? 2 : 1;
+  static constexpr int NS = D == 64 ? 8 : D == 128 ? 5 : 2;   // ring stages
+  static constexpr int COLS = D < 128 ? D : 128;   // bytes of a row in one box
+  static constexpr int CHUNKS = D / COLS;
+  static constexpr int CHUNK_BYTES = kT * COLS;
+  static constexpr int TILE_BYTES = kT * D;
+  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;   // K, then V
+  static constexpr int Q_ROW = D * 2 + 32;   // padded: conflict-free 8-byte loads
+  static constexpr int Q_STAGE = kMaxG * Q_ROW;
+  static constexpr int OFF_Q = NS * STAGE_BYTES;
+  static constexpr int OFF_SCALE = OFF_Q + 2 * Q_STAGE;          // [NS][2][kT] f32
+  static constexpr int OFF_MERGE = OFF_SCALE + NS * 2 * kT * 4;  // [4][8][kMergeRow] f32
+  static constexpr int OFF_STAT = OFF_MERGE + kCWarps * kMaxG * kMergeRow * 4;  // [3][4][8] f32
+  static constexpr int OFF_QS = OFF_STAT + 3 * kCWarps * kMaxG * 4;             // [2][8] f32
+  static constexpr int OFF_BAR = OFF_QS + 2 * kMaxG * 4;
+  static constexpr int N_BARS = 2 * NS + 4;
+  static constexpr int OFF_TILE = OFF_BAR + N_BARS * 8;   // [NS] u32: box mask, row offset
+  static constexpr int OFF_MISC = OFF_TILE + NS * 4;      // abort flag, last-arrival flag
+  static constexpr int OFF_DESC = (OFF_MISC + 8 + 15) & ~15;       // Unit [2]
+  static constexpr int OFF_ROWS = OFF_DESC + 2 * 48;               // int2 [kMaxRows]
+  static constexpr int OFF_PRE = OFF_ROWS + kMaxRows * 8;          // int [kMaxRows + 1]
+  static constexpr int SMEM = OFF_PRE + (kMaxRows + 1) * 4 + 1024;  // + alignment
+};
+// shared memory per SM on sm_103a: 228 KB, of which 1 KB is reserved per CTA
+static_assert(Cfg<64>::CTAS_PER_SM * (Cfg<64>::SMEM + 1024) <= 228 * 1024, "D=64 residency");
+static_assert(Cfg<128>::CTAS_PER_SM * (Cfg<128>::SMEM + 1024) <= 228 * 1024, "D=128 residency");
+static_assert(Cfg<256>::CTAS_PER_SM * (Cfg<256>::SMEM + 1024) <= 228 * 1024, "D=256 residency");
+static_assert(Cfg<512>::SMEM <= 227 * 1024, "D=512 smem per CTA");
+
+// ---------------------------------------------------------------- PTX ----
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait: gives up after kSpinLimit polls (each may suspend the thread for
+// a hardware-defined time) or as soon as the CTA aborts.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
+                                          volatile int *abort_flag) {
+  for (int i = 0; i < kSpinLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 63 && *abort_flag) return false;
+  }
+  return false;
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm, int x, int y,
+                                            int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void copy_word(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src))
+               : "memory");
+}
+// Arrives on the barrier once this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void consumer_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kCThreads) : "memory");
+}
+// consumer_sync that also returns the OR of `v` over the consumer threads
+__device__ __forceinline__ bool consumer_sync_or(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, 1, %2, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "n"(kCThreads)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The e4m3 codes in the low and the high half of a word as fp16 pairs (exact).
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float exp2i(int k) {   // 2^k, -126 <= k <= 127
+  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+}
+
+// Where 16-byte unit u of tile row r lies in a tile written by a swizzled copy:
+// row_base(r) ^ unit_bits(u). Rows of 128 bytes (and their 128-byte chunks, each a
+// [kT][128 B] block) XOR the unit with the row mod 8; rows of 64 bytes with
+// (row / 2) mod 4.
+template <int D>
+__device__ __forceinline__ uint32_t row_base(int r) {
+  return D == 64 ? r * 64 + (((r >> 1) & 3) << 4) : r * 128 + ((r & 7) << 4);
+}
+template <int D>
+__device__ __forceinline__ uint32_t unit_addr(uint32_t tile, uint32_t base, int u) {
+  return D == 64 ? tile + (base ^ (u << 4))
+                 : tile + (u >> 3) * Cfg<D>::CHUNK_BYTES + (base ^ ((u & 7) << 4));
+}
+
+// ------------------------------------------------------- row geometry ----
 struct Problem {
   const __nv_bfloat16 *q;
-  const uint8_t *k_cache, *v_cache;
   const float *k_scale, *v_scale;
   const int32_t *table, *batch_idx, *seq_lens;
   int n_slots, max_pages, log2_ps, n_pages, log2_block, window, B, Hq, Hkv, G;
   float scale_log2;
+  int *counters;           // [kMaxCtas], zero between calls
+  float *o_part, *st_part; // [kMaxCtas][2] records of G * D and G * 3 floats
   __nv_bfloat16 *out;
   int32_t *err;
 };
 
+struct RowInfo {
+  int slot, L, lo, t_first, n_tiles;
+};
+__device__ __forceinline__ RowInfo row_keys(const Problem &p, int slot, int L) {
+  RowInfo r;
+  r.slot = slot;
+  r.L = L;
+  r.lo = p.window > 0 ? max(0, L - p.window) : 0;
+  r.t_first = r.lo / kT;
+  r.n_tiles = (slot <= 0 || L <= 0) ? 0 : (L + kT - 1) / kT - r.t_first;
+  return r;
+}
+// Row b's slot (0 when invalid) and clamped length; `bits` gets its errors.
+__device__ __forceinline__ int2 row_read(const Problem &p, int b, int &bits) {
+  int slot = p.batch_idx ? p.batch_idx[b] : b;
+  int L = p.seq_lens[b];
+  bits = 0;
+  if (slot < 0 || slot >= p.n_slots) {
+    bits |= PKV_ERR_SLOT;
+    slot = 0;
+  }
+  const int most = p.max_pages << p.log2_ps;
+  if (L < 0 || L > most) {
+    bits |= PKV_ERR_POS;
+    L = L < 0 ? 0 : most;
+  }
+  return make_int2(slot, L);
+}
+
+// The line of work: a (row, head) with n > 0 tiles takes n + 1 positions, its start
+// and its tiles; pre[b] is the prefix sum of n + 1 over rows, (b, g)'s positions
+// begin at Hkv * pre[b] + g * (n + 1). CTA c of the `ctas` that share the line's
+// `total` positions owns [bound(c), bound(c + 1)); ctas <= total, so every share
+// has a position and every CTA between a (row, head)'s first and last has tiles of it.
+struct Line {
+  int total, ctas;
+  __device__ __forceinline__ int bound(int c) const {
+    return static_cast<int>(static_cast<long long>(c) * total / ctas);
+  }
+  __device__ __forceinline__ int owner(int x) const {
+    return static_cast<int>((static_cast<long long>(x + 1) * ctas - 1) / total);
+  }
+};
+
+// A run of tiles [ta, tb) of one (row, kv head), keys [k0, k1), the part-th of
+// `parts`; b < 0: no more work.
+struct Unit {
+  int b, g, slot, ta, tb, k0, k1, part, parts, first_cta;
+};
+static_assert(sizeof(Unit) <= 48, "unit descriptor slot");
+
+// The next unit from position x on (advanced past it); false at the share's end.
+// The whole converged producer warp calls it with uniform arguments.
+__device__ __forceinline__ bool next_unit(const Problem &p, const Line &line, const int2 *rows,
+                                          const int *pre, int end, int &x, Unit &w, int lane) {
+  while (x < end) {
+    int b = -1;   // the last row whose positions begin at or before x
+    for (int base = 0; base < p.B; base += 32) {
+      const int i = base + lane;
+      const unsigned le = __ballot_sync(0xffffffffu, i < p.B && p.Hkv * pre[i] <= x);
+      b += __popc(le);
+      if (le != 0xffffffffu) break;
+    }
+    const int width = pre[b + 1] - pre[b];
+    const int within = x - p.Hkv * pre[b];
+    const int g = within / width, r = within - g * width;
+    const int n = min(end - x, width - r);
+    x += n;
+    const int t0 = max(r, 1) - 1, t1 = r + n - 1;   // tiles of the row: [t0, t1)
+    if (t1 <= t0) continue;                          // only the start's position
+    const int2 rc = rows[b];
+    const RowInfo ri = row_keys(p, rc.x, rc.y);
+    const int start = p.Hkv * pre[b] + g * width;
+    w.b = b;
+    w.g = g;
+    w.slot = ri.slot;
+    w.ta = ri.t_first + t0;
+    w.tb = ri.t_first + t1;
+    w.k0 = max(ri.lo, w.ta * kT);
+    w.k1 = min(ri.L, w.tb * kT);
+    w.first_cta = line.owner(start + 1);
+    w.parts = line.owner(start + width - 1) - w.first_cta + 1;
+    w.part = static_cast<int>(blockIdx.x) - w.first_cta;
+    return true;
+  }
+  return false;
+}
+
+// ------------------------------------------------------------- kernel ----
 template <int D>
-__global__ void __launch_bounds__(128) decode_q8_kernel(const Problem p) {
-  constexpr int E = D / 32;   // elements a lane holds
+__global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
+    decode_q8_kernel(const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const Problem p) {
+  using Cf = Cfg<D>;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t s0 = smem_u32(sm);
+  const uint32_t full = s0 + Cf::OFF_BAR, empty = full + 8 * Cf::NS,
+                 fullQ = empty + 8 * Cf::NS, emptyQ = fullQ + 16;
+  uint32_t *tile_word = reinterpret_cast<uint32_t *>(sm + Cf::OFF_TILE);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OFF_MISC);
+  int *last_flag = reinterpret_cast<int *>(sm + Cf::OFF_MISC) + 1;
+  Unit *udesc = reinterpret_cast<Unit *>(sm + Cf::OFF_DESC);
+  int2 *rows = reinterpret_cast<int2 *>(sm + Cf::OFF_ROWS);
+  int *pre = reinterpret_cast<int *>(sm + Cf::OFF_PRE);
+
+  // ---- set-up, before the dependency wait: barriers, row cache, prefix sums.
+  // It reads only seq_lens and batch_idx (the producer also the table), which no
+  // kernel that may still run writes (the header's rule).
+  if (tid == 0) {
+    for (int i = 0; i < Cf::NS; ++i) {
+      mbar_init(full + 8 * i, 1 + 32);   // the copies' arrival, and every lane's scale words
+      mbar_init(empty + 8 * i, kCWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(fullQ + 8 * i, 1);
+      mbar_init(emptyQ + 8 * i, kCWarps);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async();
+  }
+  int row_bits = 0;
+  for (int b = tid; tid < kCThreads && b < p.B; b += kCThreads) {
+    int bits;
+    const int2 rc = row_read(p, b, bits);
+    row_bits |= bits;
+    const RowInfo r = row_keys(p, rc.x, rc.y);
+    rows[b] = rc;
+    pre[b + 1] = r.n_tiles > 0 ? r.n_tiles + 1 : 0;
+  }
+  __syncthreads();
+  if (warp == 0) {   // inclusive scan of pre[1 .. B]
+    int carry = 0;
+#pragma unroll 1
+    for (int base = 0; base < p.B; base += 32) {
+      const int i = base + lane;
+      int v = i < p.B ? pre[i + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+      }
+      if (i < p.B) pre[i + 1] = v + carry;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) pre[0] = 0;
+  }
+  __syncthreads();
+  Line line;
+  line.total = p.Hkv * pre[p.B];
+  line.ctas = min(static_cast<int>(gridDim.x), line.total);
+
+  const int ps = 1 << p.log2_ps;
+  const int log2_box = min(p.log2_ps, 6);
+  const int box_rows = 1 << log2_box;          // rows of one copy
+  const int boxes = kT >> log2_box;            // copies a tile
+  const int log2_sc = min(p.log2_block, 6);    // keys of a tile that share a scale word
+  const int scales = kT >> log2_sc;            // scale words of a tile, for K and for V
+
+  if (warp == kCWarps) {
+    // ======================== producer (one warp) ========================
+    // Lane j looks up box j of a unit (a page's segment of one tile). box_page only
+    // issues the table load; box_row checks the entry when it is used, so a
+    // look-ahead load never stalls the warp.
+    auto box_key = [&](const Unit &u, int j) -> int {   // first key of box j, -1 if unused
+      if (j >= (u.tb - u.ta) * boxes) return -1;
+      const int key = u.ta * kT + j * box_rows;
+      return key + box_rows <= u.k0 || key >= u.k1 ? -1 : key;
+    };
+    auto box_page = [&](const Unit &u, int j) -> int {
+      const int key = box_key(u, j);
+      return key < 0 ? -1
+                     : __ldg(p.table + static_cast<size_t>(u.slot) * p.max_pages +
+                             (key >> p.log2_ps));
+    };
+    auto box_row = [&](const Unit &u, int j, int page) -> int {   // the box's first cache row
+      const int key = box_key(u, j);
+      if (key < 0) return -1;
+      if (page < 0 || page >= p.n_pages) {
+        if (p.err) atomicOr(p.err, page < 0 ? PKV_ERR_PAGE_NEG : PKV_ERR_PAGE_RANGE);
+        return -1;
+      }
+      return ((u.g * p.n_pages + page) << p.log2_ps) + (key & (ps - 1));
+    };
+    int x = 0, end = 0;
+    if (static_cast<int>(blockIdx.x) < line.ctas) {
+      x = line.bound(blockIdx.x);
+      end = line.bound(blockIdx.x + 1);
+    }
+    Unit w, wn;
+    int it = 0, it_q = 0;
+    bool ok = true;
+    bool have = next_unit(p, line, rows, pre, end, x, w, lane);
+    int page_first = have ? box_page(w, lane) : -1;
+    pkv_wait_prior_grid();
+    while (ok && have) {
+      bool have_next = false, looked_ahead = false;
+      int page_next = -1;
+      {   // the query rows of the group, and the unit itself
+        const int qs = it_q & 1;
+        if (lane == 0) {
+          ok = mbar_wait(emptyQ + 8 * qs, ((it_q >> 1) & 1) ^ 1, abort_flag);
+          if (ok) {
+            udesc[qs] = w;   // published by the arrive
+            mbar_expect_tx(fullQ + 8 * qs, static_cast<uint32_t>(p.G * D * 2));
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (lane < p.G)
+          bulk_load(s0 + Cf::OFF_Q + qs * Cf::Q_STAGE + lane * Cf::Q_ROW,
+                    p.q + (static_cast<size_t>(w.b) * p.Hq + w.g * p.G + lane) * D,
+                    static_cast<uint32_t>(D * 2), fullQ + 8 * qs);
+        ++it_q;
+      }
+      const int n_boxes = (w.tb - w.ta) * boxes;
+      for (int base = 0; base < n_boxes && ok; base += 32) {
+        const int row = box_row(w, base + lane, base == 0 ? page_first : box_page(w, base + lane));
+        const int tiles_here = min(32, n_boxes - base) / boxes;
+        for (int tt = 0; tt < tiles_here; ++tt) {
+          const int t = w.ta + base / boxes + tt;
+          const int st = it % Cf::NS;
+          ok = mbar_wait(empty + 8 * st, ((it / Cf::NS) & 1) ^ 1, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t mask =
+              (__ballot_sync(0xffffffffu, row >= 0) >> (tt * boxes)) & ((1u << boxes) - 1u);
+          // One box per tile (pages of >= 64 keys): a tile whose keys end or start
+          // inside it is loaded as the 64 rows that end at its last key or start
+          // at its first; rows outside the page are zero-filled by the copy and
+          // never read from memory. Tile row r then holds key t * 64 + r + off.
+          int off = 0;
+          if (boxes == 1) {
+            const int lo_r = max(w.k0 - t * kT, 0), hi_r = min(w.k1 - t * kT, kT);
+            if (hi_r < kT && (lo_r == 0 || hi_r <= kT - lo_r)) off = hi_r - kT;
+            else if (lo_r > 0) off = lo_r;
+          }
+          const uint32_t bar = full + 8 * st;
+          const uint32_t dst = s0 + st * Cf::STAGE_BYTES;
+          if (lane == 0) {
+            tile_word[st] = mask | (static_cast<uint32_t>(off & 0xff) << 8);
+            mbar_expect_tx(bar, 2u * __popc(mask) * box_rows * D);
+          }
+          __syncwarp();
+          if (lane >= tt * boxes && lane < (tt + 1) * boxes && row >= 0) {
+            const int i = lane - tt * boxes;
+            const int y = (row & (ps - 1)) + off, z = row >> p.log2_ps;
+#pragma unroll
+            for (int cc = 0; cc < Cf::CHUNKS; ++cc) {
+              const uint32_t d = dst + cc * Cf::CHUNK_BYTES + i * box_rows * Cf::COLS;
+              tma_load_3d(d, &tmK, cc * Cf::COLS, y, z, bar);
+              tma_load_3d(d + Cf::TILE_BYTES, &tmV, cc * Cf::COLS, y, z, bar);
+            }
+          }
+          for (int e0 = 0; e0 < 2 * scales; e0 += 32) {
+            const int e = e0 + lane, ee = e & (scales - 1);
+            const int key = ee << log2_sc;   // within the tile
+            const int r = __shfl_sync(0xffffffffu, row, (tt * boxes + (key >> log2_box)) & 31);
+            if (e < 2 * scales && r >= 0) {
+              const int idx = (r + (key & (box_rows - 1))) >> p.log2_block;
+              copy_word(s0 + Cf::OFF_SCALE + ((st * 2 + (e >= scales)) * kT + ee) * 4,
+                        (e >= scales ? p.v_scale : p.k_scale) + idx);
+            }
+          }
+          copies_arrive(bar);
+          ++it;
+          if (!looked_ahead) {   // the next unit's lookups, once this one is moving
+            looked_ahead = true;
+            have_next = next_unit(p, line, rows, pre, end, x, wn, lane);
+            page_next = have_next ? box_page(wn, lane) : -1;
+          }
+        }
+      }
+      w = wn;
+      page_first = page_next;
+      have = have_next;
+    }
+    if (ok && lane == 0) {   // end of work, in the next Q stage
+      const int qs = it_q & 1;
+      ok = mbar_wait(emptyQ + 8 * qs, ((it_q >> 1) & 1) ^ 1, abort_flag);
+      if (ok) {
+        udesc[qs].b = -1;
+        mbar_arrive(fullQ + 8 * qs);
+        ++it_q;
+      }
+    }
+    copies_wait();
+    __syncwarp();
+    if (lane != 0) return;
+    if (!ok) {
+      *abort_flag = 1;
+      if (p.err) atomicOr(p.err, PKV_ERR_TIMEOUT);
+    }
+    // drain: the last phase armed on every stage must land before exit
+    volatile int no_abort = 0;
+    for (int s = 0; s < Cf::NS; ++s)
+      if (it > s) (void)mbar_wait(full + 8 * s, ((it - 1 - s) / Cf::NS) & 1, &no_abort);
+    for (int s = 0; s < 2; ++s)
+      if (it_q > s) (void)mbar_wait(fullQ + 8 * s, ((it_q - 1 - s) / 2) & 1, &no_abort);
+    return;
+  }
+
+  // ============================== consumers ==============================
   pkv_wait_prior_grid();
   pkv_allow_next_grid();
-  const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, g = hq / p.G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
-  const int slot = p.batch_idx ? p.batch_idx[b] : b;
-  int L = p.seq_lens[b];
-  const int Lmax = p.max_pages << p.log2_ps;
-  int bits = 0;
-  if (slot < 0 || slot >= p.n_slots) bits |= PKV_ERR_SLOT;
-  if (L > Lmax || L < 0) bits |= PKV_ERR_POS;
-  if (bits && hq == 0 && threadIdx.x == 0 && p.err) atomicOr(p.err, bits);
-  L = min(L, Lmax);
-  if (slot <= 0 || slot >= p.n_slots) L = 0;
-  const int lo = p.window > 0 ? max(0, L - p.window) : 0;
-  const __nv_bfloat16 *q = p.q + (static_cast<long long>(b) * p.Hq + hq) * D + lane * E;
-  float qf[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    qf[i] = __bfloat162float(q[i]);
-    o[i] = 0.f;
+  if (blockIdx.x == 0 && row_bits && p.err) atomicOr(p.err, row_bits);
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {   // rows without keys: zeros
+    if (pre[b + 1] != pre[b]) continue;
+    uint4 *o = reinterpret_cast<uint4 *>(p.out + static_cast<size_t>(b) * p.Hq * D);
+    for (int i = tid; i < p.Hq * D / 8; i += kCThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  for (int j = lo + warp; j < L; j += 4) {
-    const int page = p.table[static_cast<long long>(slot) * p.max_pages + (j >> p.log2_ps)];
-    if (page < 0 || page >= p.n_pages) {
-      if (lane == 0 && p.err) atomicOr(p.err, page < 0 ? PKV_ERR_PAGE_NEG : PKV_ERR_PAGE_RANGE);
-      continue;
+
+  const int gid = lane >> 2, tig = lane & 3;
+  const int h0 = 2 * tig, h1 = h0 + 1;
+  constexpr int KS = D / 16;      // 16-byte units of a row = MMA steps over D = m-tiles of O^T
+  constexpr bool Q_REGS = D <= 256;
+  constexpr int QK = Q_REGS ? KS : 1;
+  float *merge = reinterpret_cast<float *>(sm + Cf::OFF_MERGE);
+  float *stat = reinterpret_cast<float *>(sm + Cf::OFF_STAT);   // m, l, M: [3][4][8]
+  const int ldsm_row = 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7);
+  const uint32_t ldsm_base = row_base<D>(ldsm_row);
+  const int ldsm_unit = lane >> 4;
+  int it = 0, it_q = 0;
+  bool failed = false;
+
+  while (true) {
+    const int qs = it_q & 1;
+    const bool q_ok = mbar_wait(fullQ + 8 * qs, (it_q >> 1) & 1, abort_flag);
+    Unit w;
+    w.b = -1;
+    if (q_ok) w = udesc[qs];
+    if (!q_ok) {
+      *abort_flag = 1;
+      if (lane == 0 && p.err) atomicOr(p.err, PKV_ERR_TIMEOUT);
     }
-    const long long row = ((static_cast<long long>(g) * p.n_pages + page) << p.log2_ps) +
-                          (j & ((1 << p.log2_ps) - 1));
-    const uint8_t *kc = p.k_cache + row * D + lane * E, *vc = p.v_cache + row * D + lane * E;
-    float s = 0.f;
+    if (w.b >= 0) {
+      // q rows to fp16, in place, each scaled by a power of two to its largest
+      for (int h = warp; h < p.G; h += kCWarps) {
+        uint32_t *row = reinterpret_cast<uint32_t *>(sm + Cf::OFF_Q + qs * Cf::Q_STAGE +
+                                                     h * Cf::Q_ROW);
+        uint32_t v[D / 64], m = 0;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      __nv_fp8_e4m3 c;
-      c.__x = kc[i];
-      s = fmaf(qf[i], static_cast<float>(c), s);
+        for (int j = 0; j < D / 64; ++j) {
+          v[j] = row[lane + 32 * j];
+          m = __vmaxu2(m, v[j] & 0x7fff7fffu);
+        }
+        m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+        const int e = min(max(static_cast<int>(m >> 7) - 127, -126), 126);
+        const float f = exp2i(-e);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+          row[lane + 32 * j] = pack_f16(__uint_as_float(v[j] << 16) * f,
+                                        __uint_as_float(v[j] & 0xffff0000u) * f);
+        if (lane == 0)
+          reinterpret_cast<float *>(sm + Cf::OFF_QS)[qs * kMaxG + h] = p.scale_log2 * exp2i(e);
+      }
+      fence_proxy_async();
     }
+    // all consumer threads leave the loop together (end of work, or a wait gave up)
+    if (consumer_sync_or(w.b < 0)) break;
+    const uint8_t *qrow = sm + Cf::OFF_Q + qs * Cf::Q_STAGE + gid * Cf::Q_ROW + tig * 8;
+    uint2 qb[QK];
+    const bool hv = gid < p.G;
+    if constexpr (Q_REGS) {
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    s *= p.scale_log2 * p.k_scale[row >> p.log2_block];
-    const float mn = fmaxf(m, s), al = exp2f(m - mn), pr = exp2f(s - mn);
-    const float wv = pr * p.v_scale[row >> p.log2_block];
-    l = l * al + pr;
-    m = mn;
+      for (int c = 0; c < KS; ++c)
+        qb[c] = hv ? *reinterpret_cast<const uint2 *>(qrow + 32 * c) : make_uint2(0u, 0u);
+    }
+    const float *qscale = reinterpret_cast<const float *>(sm + Cf::OFF_QS) + qs * kMaxG;
+    const float sc0 = h0 < p.G ? qscale[h0] : 0.f, sc1 = h1 < p.G ? qscale[h1] : 0.f;
+    if constexpr (Q_REGS) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(emptyQ + 8 * qs);
+    }
+    ++it_q;
+
+    float o[KS][4];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      __nv_fp8_e4m3 c;
-      c.__x = vc[i];
-      o[i] = fmaf(wv, static_cast<float>(c), o[i] * al);
+    for (int u = 0; u < KS; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // this lane's keys
+    float M0 = -INFINITY, M1 = -INFINITY;                       // the warp's keys
+
+    for (int t = w.ta; t < w.tb; ++t, ++it) {
+      const int st = it % Cf::NS;
+      if (!mbar_wait(full + 8 * st, (it / Cf::NS) & 1, abort_flag)) {
+        failed = true;
+        *abort_flag = 1;
+        if (lane == 0 && p.err) atomicOr(p.err, PKV_ERR_TIMEOUT);
+      }
+      const uint32_t tw = tile_word[st];
+      const int off = static_cast<int8_t>((tw >> 8) & 0xffu);
+      const int tlo = max(w.k0, t * kT), thi = min(w.k1, t * kT + kT);
+      const uint32_t kbase = s0 + st * Cf::STAGE_BYTES, vbase = kbase + Cf::TILE_BYTES;
+      // tile row r holds a key of the unit?
+      auto valid = [&](int r) -> bool {
+        const int key = t * kT + r + off;
+        return key >= tlo && key < thi && ((tw >> (r >> log2_box)) & 1u);
+      };
+
+      // ---- S^T [16 keys x 8 heads] ----
+      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < KS; c += 2) {
+        uint32_t r[4], a0, a1, a2, a3;
+        ldsm_x4(unit_addr<D>(kbase, ldsm_base, c + ldsm_unit), r);
+        uint2 q0, q1;
+        if constexpr (Q_REGS) {
+          q0 = qb[c];
+          q1 = qb[c + 1];
+        } else {
+          q0 = hv ? *reinterpret_cast<const uint2 *>(qrow + 32 * c) : make_uint2(0u, 0u);
+          q1 = hv ? *reinterpret_cast<const uint2 *>(qrow + 32 * c + 32) : make_uint2(0u, 0u);
+        }
+        codes_to_f16(r[0], a0, a2);
+        codes_to_f16(r[1], a1, a3);
+        mma_f16(sa, a0, a1, a2, a3, q0.x, q0.y);
+        codes_to_f16(r[2], a0, a2);
+        codes_to_f16(r[3], a1, a3);
+        mma_f16(sb, a0, a1, a2, a3, q1.x, q1.y);
+      }
+      // ---- online softmax; lane: keys r_lo, r_hi of the tile, heads h0, h1 ----
+      const int r_lo = 16 * warp + gid, r_hi = r_lo + 8;
+      const float *ks = reinterpret_cast<const float *>(sm + Cf::OFF_SCALE) + st * 2 * kT;
+      const int i_lo = ((r_lo + off) & (kT - 1)) >> log2_sc;
+      const int i_hi = ((r_hi + off) & (kT - 1)) >> log2_sc;
+      const bool v_lo = valid(r_lo), v_hi = valid(r_hi);
+      const float k_lo = ks[i_lo], k_hi = ks[i_hi];
+      const float g_lo = __log2f(ks[kT + i_lo]), g_hi = __log2f(ks[kT + i_hi]);
+      const float s00 = v_lo ? (sa[0] + sb[0]) * (k_lo * sc0) : -INFINITY;
+      const float s01 = v_lo ? (sa[1] + sb[1]) * (k_lo * sc1) : -INFINITY;
+      const float s10 = v_hi ? (sa[2] + sb[2]) * (k_hi * sc0) : -INFINITY;
+      const float s11 = v_hi ? (sa[3] + sb[3]) * (k_hi * sc1) : -INFINITY;
+      const float z00 = v_lo ? s00 + g_lo : -INFINITY, z01 = v_lo ? s01 + g_lo : -INFINITY;
+      const float z10 = v_hi ? s10 + g_hi : -INFINITY, z11 = v_hi ? s11 + g_hi : -INFINITY;
+      {
+        const float n0 = fmaxf(m0, fmaxf(s00, s10)), n1 = fmaxf(m1, fmaxf(s01, s11));
+        const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
+        l0 = l0 * exp2f(m0 - u0) + (exp2f(s00 - u0) + exp2f(s10 - u0));
+        l1 = l1 * exp2f(m1 - u1) + (exp2f(s01 - u1) + exp2f(s11 - u1));
+        m0 = n0;
+        m1 = n1;
+      }
+      float x0 = fmaxf(z00, z10), x1 = fmaxf(z01, z11);
+#pragma unroll
+      for (int i = 4; i < 32; i <<= 1) {
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, i));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, i));
+      }
+      if (__any_sync(0xffffffffu, x0 > M0 || x1 > M1)) {
+        const float N0 = fmaxf(M0, x0), N1 = fmaxf(M1, x1);
+        const float a0 = M0 == -INFINITY ? 0.f : exp2f(M0 - N0);
+        const float a1 = M1 == -INFINITY ? 0.f : exp2f(M1 - N1);
+        M0 = N0;
+        M1 = N1;
+#pragma unroll
+        for (int u = 0; u < KS; ++u) {
+          o[u][0] *= a0;
+          o[u][1] *= a1;
+          o[u][2] *= a0;
+          o[u][3] *= a1;
+        }
+      }
+      const float U0 = M0 == -INFINITY ? 0.f : M0, U1 = M1 == -INFINITY ? 0.f : M1;
+      const uint32_t b0 = transpose8x8(pack_f16(exp2f(z00 - U0), exp2f(z01 - U1)));
+      const uint32_t b1 = transpose8x8(pack_f16(exp2f(z10 - U0), exp2f(z11 - U1)));
+      // ---- O^T [D x 8 heads] += V^T P^T; codes of keys outside the unit count 0 ----
+      const int c_lo = 16 * warp + 2 * tig;
+      const uint32_t keep_lo = (valid(c_lo) ? 0xffffu : 0u) | (valid(c_lo + 1) ? 0xffff0000u : 0u);
+      const uint32_t keep_hi =
+          (valid(c_lo + 8) ? 0xffffu : 0u) | (valid(c_lo + 9) ? 0xffff0000u : 0u);
+#pragma unroll
+      for (int u = 0; u < KS; u += 2) {
+        uint32_t r[4], a0, a1, a2, a3;
+        ldsm_x4_t(unit_addr<D>(vbase, ldsm_base, u + ldsm_unit), r);
+        // a word holds two columns of two keys; pair the keys of each column
+        codes_to_f16(__byte_perm(r[0] & keep_lo, 0, 0x3120), a0, a1);
+        codes_to_f16(__byte_perm(r[1] & keep_hi, 0, 0x3120), a2, a3);
+        mma_f16(o[u], a0, a1, a2, a3, b0, b1);
+        codes_to_f16(__byte_perm(r[2] & keep_lo, 0, 0x3120), a0, a1);
+        codes_to_f16(__byte_perm(r[3] & keep_hi, 0, 0x3120), a2, a3);
+        mma_f16(o[u + 1], a0, a1, a2, a3, b0, b1);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * st);
+    }
+    if constexpr (!Q_REGS) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(emptyQ + 8 * qs);
+    }
+
+    // ---- the unit's end: join the four warps' states ----
+    {
+      float n0 = m0, n1 = m1;
+#pragma unroll
+      for (int i = 4; i < 32; i <<= 1) {
+        n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, i));
+        n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, i));
+      }
+      float t0 = m0 == -INFINITY ? 0.f : l0 * exp2f(m0 - n0);
+      float t1 = m1 == -INFINITY ? 0.f : l1 * exp2f(m1 - n1);
+      if (l0 != l0) t0 = l0;   // a NaN score leaves m behind
+      if (l1 != l1) t1 = l1;
+#pragma unroll
+      for (int i = 4; i < 32; i <<= 1) {
+        t0 += __shfl_xor_sync(0xffffffffu, t0, i);
+        t1 += __shfl_xor_sync(0xffffffffu, t1, i);
+      }
+      if (gid == 0) {
+        float *s = stat + warp * kMaxG;
+        s[h0] = n0;
+        s[h1] = n1;
+        s[32 + h0] = t0;
+        s[32 + h1] = t1;
+        s[64 + h0] = M0;
+        s[64 + h1] = M1;
+      }
+    }
+    const bool cut = w.parts > 1;
+    const size_t rec = static_cast<size_t>(blockIdx.x) * 2 + (w.part == 0 ? 1 : 0);
+    constexpr int COLS = D < kMergeCols ? D : kMergeCols;
+    constexpr int HSTEP = kCThreads / COLS;      // heads handled at once
+    const int col = tid % COLS;
+    bool bad = false;
+#pragma unroll
+    for (int c0 = 0; c0 < D; c0 += COLS) {
+      if (c0 > 0) consumer_sync();   // the columns before have been read
+#pragma unroll
+      for (int u = 0; u < COLS / 16; ++u) {
+        const float(&f)[4] = o[c0 / 16 + u];
+        float *d = merge + (warp * kMaxG + h0) * kMergeRow + 16 * u + 2 * gid;
+        *reinterpret_cast<float2 *>(d) = make_float2(f[0], f[2]);
+        *reinterpret_cast<float2 *>(d + kMergeRow) = make_float2(f[1], f[3]);
+      }
+      if (c0 == 0) bad = consumer_sync_or(failed);
+      else consumer_sync();
+      if (bad) continue;
+      for (int h = tid / COLS; h < p.G; h += HSTEP) {
+        float M = -INFINITY, m = -INFINITY, l = 0.f, acc = 0.f;
+#pragma unroll
+        for (int i = 0; i < kCWarps; ++i) {
+          M = fmaxf(M, stat[64 + i * kMaxG + h]);
+          m = fmaxf(m, stat[i * kMaxG + h]);
+        }
+#pragma unroll
+        for (int i = 0; i < kCWarps; ++i) {
+          const float Mi = stat[64 + i * kMaxG + h], mi = stat[i * kMaxG + h];
+          const float li = stat[32 + i * kMaxG + h];
+          if (Mi != -INFINITY) acc += merge[(i * kMaxG + h) * kMergeRow + col] * exp2f(Mi - M);
+          if (mi != -INFINITY || li != li) l += li * (mi == m ? 1.f : exp2f(mi - m));
+        }
+        if (cut) {
+          __stcg(p.o_part + (rec * p.G + h) * D + c0 + col, acc);
+          if (c0 + col == 0) {
+            float *s = p.st_part + (rec * p.G + h) * 3;
+            __stcg(s, m);
+            __stcg(s + 1, l);
+            __stcg(s + 2, M);
+          }
+        } else {
+          const float v = M == -INFINITY || l == 0.f ? 0.f : acc * exp2f(M - m) / l;
+          p.out[(static_cast<size_t>(w.b) * p.Hq + w.g * p.G + h) * D + c0 + col] =
+              __float2bfloat16_rn(l != l ? l : v);
+        }
+      }
+    }
+    if (bad || !cut) continue;
+    // ---- a cut (row, head): the CTA that arrives last joins the parts ----
+    __threadfence();
+    consumer_sync();
+    if (tid == 0) *last_flag = atomicAdd(p.counters + w.first_cta, 1) == w.parts - 1;
+    consumer_sync();
+    if (!*last_flag) continue;
+    __threadfence();
+    if (tid == 0) p.counters[w.first_cta] = 0;
+    auto record = [&](int j) -> size_t {   // part j's record: CTA first_cta + j's
+      return static_cast<size_t>(w.first_cta + j) * 2 + (j == 0 ? 1 : 0);
+    };
+    for (int i = tid; i < p.G * D; i += kCThreads) {
+      const int h = i / D;
+      float M = -INFINITY, m = -INFINITY, l = 0.f, acc = 0.f;
+      for (int j = 0; j < w.parts; ++j) {
+        const float *s = p.st_part + (record(j) * p.G + h) * 3;
+        const float mj = __ldcg(s), lj = __ldcg(s + 1), Mj = __ldcg(s + 2);
+        const float v = __ldcg(p.o_part + record(j) * p.G * D + i);
+        const float mn = fmaxf(m, mj), Mn = fmaxf(M, Mj);
+        if (mn != -INFINITY) l = l * exp2f(m - mn) + (mj == mn ? lj : lj * exp2f(mj - mn));
+        if (lj != lj) l = lj;
+        if (Mn != -INFINITY)
+          acc = acc * exp2f(M - Mn) + (Mj == -INFINITY ? 0.f : v * exp2f(Mj - Mn));
+        m = mn;
+        M = Mn;
+      }
+      const float v = M == -INFINITY || l == 0.f ? 0.f : acc * exp2f(M - m) / l;
+      p.out[(static_cast<size_t>(w.b) * p.Hq + w.g * p.G) * D + i] =
+          __float2bfloat16_rn(l != l ? l : v);
     }
   }
-  if (lane == 0) {
-    sm_m[warp] = m;
-    sm_l[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < E; ++i) sm_o[warp][lane * E + i] = o[i];
-  __syncthreads();
-  const float mt = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float sum = 0.f, acc = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float f = sm_m[w] == -INFINITY ? 0.f : exp2f(sm_m[w] - mt);
-      sum += sm_l[w] * f;
-      acc += sm_o[w][d] * f;
+}
+
+// ------------------------------------------------------------- host ----
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static std::once_flag once;
+  static EncodeTiledFn fn = nullptr;
+  std::call_once(once, [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                         cudaEnableDefault, &qr) == cudaSuccess &&
+        qr == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+// Map over a cache of `pages` pages (all heads') of page_size rows of D bytes:
+// {column, row in page, page}, boxes of box_rows rows; rows outside the page read 0.
+int make_cache_map(CUtensorMap *tm, const void *base, long long pages, int page_size, int D,
+                   int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return pkv::fail(PKV_E_CUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page_size),
+                        static_cast<cuuint64_t>(pages)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(D) * page_size};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(D < 128 ? D : 128),
+                       static_cast<cuuint32_t>(box_rows), 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return pkv::fail(PKV_E_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return PKV_OK;
+}
+
+template <int D>
+int launch_q8(const CUtensorMap &tmK, const CUtensorMap &tmV, const Problem &p,
+              cudaStream_t stream) {
+  static std::mutex mu;
+  static bool done[64] = {false};
+  int dev = 0;
+  PKV_CUDA_CHECK(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return pkv::fail(PKV_E_CUDA, "device id out of range");
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      PKV_CUDA_CHECK(cudaFuncSetAttribute(
+          decode_q8_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM));
+      done[dev] = true;
     }
-    p.out[(static_cast<long long>(b) * p.Hq + hq) * D + d] =
-        __float2bfloat16_rn(sum != 0.f ? acc / sum : 0.f);
   }
+  const int sms = pkv::sm_count();
+  if (sms <= 0) return pkv::fail(PKV_E_CUDA, "paged_decode_attn_q8: no SM count");
+  const int most = sms * Cfg<D>::CTAS_PER_SM;
+  PKV_CUDA_CHECK(pkv::launch_pdl(decode_q8_kernel<D>, dim3(most < kMaxCtas ? most : kMaxCtas),
+                                 dim3(kThreads), Cfg<D>::SMEM, stream, tmK, tmV, p));
+  return pkv::ok();
 }
 
 bool good_heads(int Hq, int Hkv, int D) {
@@ -114,6 +909,8 @@ bool good_heads(int Hq, int Hkv, int D) {
 
 extern "C" {
 
+// Workspace: [kMaxCtas] counters, [kMaxCtas][2] records of G * D floats (partial
+// outputs), [kMaxCtas][2] records of G * 3 floats (running maxima and sum).
 size_t paged_decode_attn_q8_workspace(int Hq, int Hkv, int D) {
   if (!good_heads(Hq, Hkv, D)) return 0;
   const size_t G = Hq / Hkv;
@@ -152,11 +949,23 @@ int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e
   if (!pkv::aligned16(q) || !pkv::aligned16(out) || !pkv::aligned16(k_cache) ||
       !pkv::aligned16(v_cache))
     return pkv::fail(PKV_E_BAD_ARG, "%s: tensors must be 16-byte aligned", fn);
+  {
+    const long long row_tiles = (1LL * max_pages_per_seq * page_size + kT - 1) / kT + 2;
+    if (1LL * B * Hkv * row_tiles >= (1LL << 31))
+      return pkv::fail(PKV_E_BAD_ARG, "%s: B * Hkv * tiles per row too large", fn);
+  }
   const size_t need = paged_decode_attn_q8_workspace(Hq, Hkv, D);
   if (!workspace || workspace_bytes < need)
     return pkv::fail(PKV_E_BAD_ARG, "%s: workspace needs %zu bytes", fn, need);
   if (!pkv::aligned16(workspace))
     return pkv::fail(PKV_E_BAD_ARG, "%s: workspace must be 16-byte aligned", fn);
+  const long long pages = 1LL * Hkv * n_pages;
+  const int box_rows = page_size < kT ? page_size : kT;
+  CUtensorMap tmK, tmV;
+  int st = make_cache_map(&tmK, k_cache, pages, page_size, D, box_rows);
+  if (st != PKV_OK) return st;
+  st = make_cache_map(&tmV, v_cache, pages, page_size, D, box_rows);
+  if (st != PKV_OK) return st;
   auto log2i = [](int x) {
     int l = 0;
     while ((1 << l) < x) ++l;
@@ -164,8 +973,6 @@ int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e
   };
   Problem p;
   p.q = reinterpret_cast<const __nv_bfloat16 *>(q);
-  p.k_cache = k_cache;
-  p.v_cache = v_cache;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.table = dev_table;
@@ -182,15 +989,18 @@ int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.counters = static_cast<int *>(workspace);
+  p.o_part = reinterpret_cast<float *>(p.counters + kMaxCtas);
+  p.st_part = p.o_part + static_cast<size_t>(kMaxCtas) * 2 * p.G * D;
   p.out = reinterpret_cast<__nv_bfloat16 *>(out);
   p.err = err_word;
-  auto *kern = D == 64    ? decode_q8_kernel<64>
-               : D == 128 ? decode_q8_kernel<128>
-               : D == 256 ? decode_q8_kernel<256>
-                          : decode_q8_kernel<512>;
-  PKV_CUDA_CHECK(pkv::launch_pdl(kern, dim3(static_cast<unsigned>(B * Hq)), dim3(128), 0,
-                                 static_cast<cudaStream_t>(stream), p));
-  return pkv::ok();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (D) {
+    case 64: return launch_q8<64>(tmK, tmV, p, s);
+    case 128: return launch_q8<128>(tmK, tmV, p, s);
+    case 256: return launch_q8<256>(tmK, tmV, p, s);
+    default: return launch_q8<512>(tmK, tmV, p, s);
+  }
 }
 
 }  // extern "C"
