@@ -49,7 +49,7 @@ constexpr int kCThreads = kCWarps * 32;
 constexpr int kThreads = kCThreads + 32;   // + producer warp
 constexpr int kMaxG = 8;             // query heads per kv head (MMA N)
 constexpr int kMaxRows = 512;        // rows per call (row cache kept in smem)
-constexpr int kMaxCtas = 1024;       // CTAs the workspace has room for
+constexpr int kMaxCtas = 512;        // CTAs the workspace has room for
 constexpr int kSpinLimit = 1 << 22;
 constexpr int kMergeCols = 128;      // columns joined per round of a unit's end
 constexpr int kMergeRow = kMergeCols + 4;   // padded: conflict-free 8-byte stores
@@ -83,6 +83,8 @@ struct Cfg {
 static_assert(Cfg<64>::CTAS_PER_SM * (Cfg<64>::SMEM + 1024) <= 228 * 1024, "D=64 residency");
 static_assert(Cfg<128>::CTAS_PER_SM * (Cfg<128>::SMEM + 1024) <= 228 * 1024, "D=128 residency");
 static_assert(Cfg<256>::CTAS_PER_SM * (Cfg<256>::SMEM + 1024) <= 228 * 1024, "D=256 residency");
+// a unit's parts have their weights in the merge buffer
+static_assert(kMaxCtas * kMaxG <= kCWarps * kMaxG * kMergeRow, "merge buffer");
 static_assert(Cfg<512>::SMEM <= 227 * 1024, "D=512 smem per CTA");
 
 // ---------------------------------------------------------------- PTX ----
@@ -813,24 +815,71 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     auto record = [&](int j) -> size_t {   // part j's record: CTA first_cta + j's
       return static_cast<size_t>(w.first_cta + j) * 2 + (j == 0 ? 1 : 0);
     };
-    for (int i = tid; i < p.G * D; i += kCThreads) {
-      const int h = i / D;
-      float M = -INFINITY, m = -INFINITY, l = 0.f, acc = 0.f;
-      for (int j = 0; j < w.parts; ++j) {
+    // the parts' weights 2^(M_j - m) / l, one warp per head, lanes over parts
+    for (int h = warp; h < p.G; h += kCWarps) {
+      float M = -INFINITY, m = -INFINITY, l = 0.f;
+      for (int j = lane; j < w.parts; j += 32) {
         const float *s = p.st_part + (record(j) * p.G + h) * 3;
-        const float mj = __ldcg(s), lj = __ldcg(s + 1), Mj = __ldcg(s + 2);
-        const float v = __ldcg(p.o_part + record(j) * p.G * D + i);
-        const float mn = fmaxf(m, mj), Mn = fmaxf(M, Mj);
-        if (mn != -INFINITY) l = l * exp2f(m - mn) + (mj == mn ? lj : lj * exp2f(mj - mn));
+        const float mj = __ldcg(s), lj = __ldcg(s + 1);
+        merge[j * kMaxG + h] = __ldcg(s + 2);
+        const float mn = fmaxf(m, mj);
+        if (mn != -INFINITY) l = l * exp2f(m - mn) + lj * exp2f(mj - mn);
         if (lj != lj) l = lj;
-        if (Mn != -INFINITY)
-          acc = acc * exp2f(M - Mn) + (Mj == -INFINITY ? 0.f : v * exp2f(Mj - Mn));
         m = mn;
-        M = Mn;
+        M = fmaxf(M, merge[j * kMaxG + h]);
       }
-      const float v = M == -INFINITY || l == 0.f ? 0.f : acc * exp2f(M - m) / l;
-      p.out[(static_cast<size_t>(w.b) * p.Hq + w.g * p.G) * D + i] =
-          __float2bfloat16_rn(l != l ? l : v);
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) {
+        const float mo = __shfl_xor_sync(0xffffffffu, m, i), lo = __shfl_xor_sync(0xffffffffu, l, i);
+        const float mn = fmaxf(m, mo);
+        const float a = mn == -INFINITY ? 0.f : l * exp2f(m - mn);
+        const float c = mn == -INFINITY ? 0.f : lo * exp2f(mo - mn);
+        l = l != l ? l : lo != lo ? lo : a + c;
+        m = mn;
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
+      }
+      const float f = l != l ? l : M == -INFINITY || l == 0.f ? 0.f : exp2f(M - m) / l;
+      for (int j = lane; j < w.parts; j += 32) {
+        const float Mj = merge[j * kMaxG + h];
+        merge[j * kMaxG + h] = l != l ? l : Mj == -INFINITY ? 0.f : f * exp2f(Mj - M);
+      }
+    }
+    consumer_sync();
+    // four columns a thread and step, the loads of several parts in flight
+    constexpr int NI = D <= 128 ? 1 : 4;   // steps at once
+    const int items = p.G * D / 4;
+    __nv_bfloat16 *out = p.out + (static_cast<size_t>(w.b) * p.Hq + w.g * p.G) * D;
+    for (int i0 = tid; i0 < items; i0 += kCThreads * NI) {
+      float4 acc[NI];
+#pragma unroll
+      for (int k = 0; k < NI; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int j = 0; j < w.parts; ++j) {
+        const float4 *o4 = reinterpret_cast<const float4 *>(p.o_part + record(j) * p.G * D);
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+          const int i = i0 + k * kCThreads;
+          if (i < items) {
+            const float4 v = __ldcg(o4 + i);
+            const float f = merge[j * kMaxG + i / (D / 4)];
+            acc[k].x = fmaf(f, v.x, acc[k].x);
+            acc[k].y = fmaf(f, v.y, acc[k].y);
+            acc[k].z = fmaf(f, v.z, acc[k].z);
+            acc[k].w = fmaf(f, v.w, acc[k].w);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < NI; ++k) {
+        const int i = i0 + k * kCThreads;
+        if (i < items) {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[k].x, acc[k].y);
+          const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[k].z, acc[k].w);
+          *reinterpret_cast<uint2 *>(out + 4 * i) =
+              make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                         *reinterpret_cast<const uint32_t *>(&hi));
+        }
+      }
     }
   }
 }
