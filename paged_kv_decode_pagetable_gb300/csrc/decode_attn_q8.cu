@@ -7,17 +7,22 @@
 //   * work: the 64-key tiles of every (row, kv head), plus one position for each
 //     start of a (row, head), laid on one line from the actual lengths; every
 //     persistent CTA takes an equal share of it. A (row, head) that straddles
-//     CTAs leaves fp32 partials (each CTA has at most one that began before its
-//     share and one that goes on after it, so the workspace is 2 records a CTA);
-//     the CTA that finishes last, found by a counter, joins them in part order,
-//     so no CTA waits for another and the result does not depend on timing;
+//     CTAs is cut into parts; a CTA has at most one part that is not its (row,
+//     head)'s first, and that part is its first work, so the workspace is one fp32
+//     record and a flag a CTA. Parts are joined in a tree of eights (part j takes in
+//     j + 1 .. j + 7, then j + 8 ..) in a fixed order: results do not depend on
+//     timing. A first part is its CTA's last work, and a part that takes in others
+//     but is not first its CTA's only work, so they find the others written, or
+//     wait for CTAs launched after them that began with that very work;
 //   * one producer warp streams query rows (cp.async.bulk), K and V tiles
 //     (cp.async.bulk.tensor into a swizzled ring) and the tiles' scales
 //     (cp.async) ahead of four consumer warps, looking up the next unit's pages
 //     while the current one moves;
 //   * each consumer warp owns 16 keys of every tile and keeps its own online
-//     softmax over the whole (row, head), so a tile needs no barrier between
-//     warps; the four states are joined once per unit. Keys are the M rows of
+//     softmax over the whole unit, so no tile needs a barrier between warps. At a
+//     unit's end it leaves its state in shared memory and goes on; a joining warp
+//     adds the four states (and a cut row's other parts, which it fetches while the
+//     unit is still running) and writes the output or the partial. Keys are the M rows of
 //     S^T = K q^T and head-dim is the M rows of O^T = V^T P^T (mma.sync m16n8k16,
 //     fp16 in, fp32 out), the <= 8 query heads of the group are N; P goes from
 //     one product to the other through movmatrix;
@@ -28,7 +33,7 @@
 //     maximum of that sum, so w is at most 1 and as precise as fp16 allows where
 //     it matters however far the scales lie apart; the denominator keeps a
 //     running maximum of its own, per lane;
-//   * every mbarrier wait is bounded; a wait that gives up sets PKV_ERR_TIMEOUT,
+//   * every wait is bounded; one that gives up sets PKV_ERR_TIMEOUT,
 //     the CTA drains its copies and exits. Invalid table entries are reported
 //     and never dereferenced.
 #include <cuda.h>
@@ -46,12 +51,14 @@ namespace {
 constexpr int kT = 64;               // keys per tile
 constexpr int kCWarps = 4;           // consumer warps, 16 keys of a tile each
 constexpr int kCThreads = kCWarps * 32;
-constexpr int kThreads = kCThreads + 32;   // + producer warp
+constexpr int kThreads = kCThreads + 64;   // + producer warp and joining warp
 constexpr int kMaxG = 8;             // query heads per kv head (MMA N)
 constexpr int kMaxRows = 512;        // rows per call (row cache kept in smem)
 constexpr int kMaxCtas = 512;        // CTAs the workspace has room for
 constexpr int kSpinLimit = 1 << 22;
-constexpr int kMergeCols = 128;      // columns joined per round of a unit's end
+constexpr int kPollLimit = 1 << 20;
+constexpr int kFan = 8;              // parts joined at once in the tree of a cut row
+constexpr int kMergeCols = 128;      // columns handed to the joining warp at once
 constexpr int kMergeRow = kMergeCols + 4;   // padded: conflict-free 8-byte stores
 
 template <int D>
@@ -67,13 +74,15 @@ struct Cfg {
   static constexpr int Q_STAGE = kMaxG * Q_ROW;
   static constexpr int OFF_Q = NS * STAGE_BYTES;
   static constexpr int OFF_SCALE = OFF_Q + 2 * Q_STAGE;          // [NS][2][kT] f32
-  static constexpr int OFF_MERGE = OFF_SCALE + NS * 2 * kT * 4;  // [4][8][kMergeRow] f32
-  static constexpr int OFF_STAT = OFF_MERGE + kCWarps * kMaxG * kMergeRow * 4;  // [3][4][8] f32
-  static constexpr int OFF_QS = OFF_STAT + 3 * kCWarps * kMaxG * 4;             // [2][8] f32
+  // states handed over: [MS] slots of [4 warps][8 heads] rows, then m, l, M [4][8] each
+  static constexpr int MS = D == 512 ? 2 : 1;
+  static constexpr int MERGE_SLOT = (kCWarps * kMaxG * kMergeRow + 3 * kCWarps * kMaxG) * 4;
+  static constexpr int OFF_MERGE = OFF_SCALE + NS * 2 * kT * 4;
+  static constexpr int OFF_QS = OFF_MERGE + MS * MERGE_SLOT;                    // [2][8] f32
   static constexpr int OFF_BAR = OFF_QS + 2 * kMaxG * 4;
-  static constexpr int N_BARS = 2 * NS + 4;
+  static constexpr int N_BARS = 2 * NS + 4 + 2 * MS;
   static constexpr int OFF_TILE = OFF_BAR + N_BARS * 8;   // [NS] u32: box mask, row offset
-  static constexpr int OFF_MISC = OFF_TILE + NS * 4;      // abort flag, last-arrival flag
+  static constexpr int OFF_MISC = OFF_TILE + NS * 4;      // abort flag
   static constexpr int OFF_DESC = (OFF_MISC + 8 + 15) & ~15;       // Unit [2]
   static constexpr int OFF_ROWS = OFF_DESC + 2 * 48;               // int2 [kMaxRows]
   static constexpr int OFF_PRE = OFF_ROWS + kMaxRows * 8;          // int [kMaxRows + 1]
@@ -83,8 +92,6 @@ struct Cfg {
 static_assert(Cfg<64>::CTAS_PER_SM * (Cfg<64>::SMEM + 1024) <= 228 * 1024, "D=64 residency");
 static_assert(Cfg<128>::CTAS_PER_SM * (Cfg<128>::SMEM + 1024) <= 228 * 1024, "D=128 residency");
 static_assert(Cfg<256>::CTAS_PER_SM * (Cfg<256>::SMEM + 1024) <= 228 * 1024, "D=256 residency");
-// a unit's parts have their weights in the merge buffer
-static_assert(kMaxCtas * kMaxG <= kCWarps * kMaxG * kMergeRow, "merge buffer");
 static_assert(Cfg<512>::SMEM <= 227 * 1024, "D=512 smem per CTA");
 
 // ---------------------------------------------------------------- PTX ----
@@ -150,10 +157,7 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-__device__ __forceinline__ void consumer_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kCThreads) : "memory");
-}
-// consumer_sync that also returns the OR of `v` over the consumer threads
+// A barrier of the consumer threads that returns the OR of `v` over them.
 __device__ __forceinline__ bool consumer_sync_or(bool v) {
   uint32_t r;
   asm volatile(
@@ -229,8 +233,8 @@ struct Problem {
   const int32_t *table, *batch_idx, *seq_lens;
   int n_slots, max_pages, log2_ps, n_pages, log2_block, window, B, Hq, Hkv, G;
   float scale_log2;
-  int *counters;           // [kMaxCtas], zero between calls
-  float *o_part, *st_part; // [kMaxCtas][2] records of G * D and G * 3 floats
+  int *flags;              // [kMaxCtas], zero between calls: the CTA's part is written
+  float *o_part, *st_part; // [kMaxCtas] records of G * D and G * 3 floats
   __nv_bfloat16 *out;
   int32_t *err;
 };
@@ -323,6 +327,226 @@ __device__ __forceinline__ bool next_unit(const Problem &p, const Line &line, co
   return false;
 }
 
+// Exponent of the largest magnitude of a pair of bf16 halves' maxima.
+__device__ __forceinline__ int q_exponent(uint32_t m) {
+  return min(max(static_cast<int>(max(m & 0xffffu, m >> 16) >> 7) - 127, -126), 126);
+}
+__device__ __forceinline__ uint32_t bf16_to_f16(uint32_t v, float f) {
+  return pack_f16(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
+}
+// A sum l held relative to maximum m, relative to n >= m instead (a NaN stays one).
+__device__ __forceinline__ float sum_at(float l, float m, float n) {
+  return m == -INFINITY ? (l != l ? l : 0.f) : l * exp2f(m - n);
+}
+
+// ---------------------------------------------------------- joining ----
+// The softmax state of head lane & 7: m and l the maximum and the sum of the
+// weights 2^s, M the maximum of s + log2 sv that the output is relative to.
+struct State {
+  float m, l, M;
+};
+// Takes in four states, lane 8 k + h holding the k-th of head h. `fk` is what that
+// one's output counts, `fs` what the outputs so far count from now on.
+__device__ __forceinline__ void take_in(State &s, const State &x, float &fk, float &fs) {
+  float m = fmaxf(s.m, x.m), M = fmaxf(s.M, x.M);
+#pragma unroll
+  for (int i = 8; i < 32; i <<= 1) {
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
+  }
+  float l = sum_at(x.l, x.m, m);
+#pragma unroll
+  for (int i = 8; i < 32; i <<= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+  fk = x.M == -INFINITY ? 0.f : exp2f(x.M - M);
+  fs = s.M == -INFINITY ? 0.f : exp2f(s.M - M);
+  s.l = sum_at(s.l, s.m, m) + l;
+  s.m = m;
+  s.M = M;
+}
+__device__ __forceinline__ void fma4(float4 &a, float f, const float4 &v) {
+  a.x = fmaf(f, v.x, a.x);
+  a.y = fmaf(f, v.y, a.y);
+  a.z = fmaf(f, v.z, a.z);
+  a.w = fmaf(f, v.w, a.w);
+}
+__device__ __forceinline__ int ld_acquire(const int *a) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_release(int *a, int v) {
+  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(a), "r"(v) : "memory");
+}
+
+// The joining warp. A lane holds four columns of every head (D = 64: of every other
+// head) of each 128-column round.
+template <int D>
+__device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32_t fullQ,
+                                           uint32_t emptyQ, uint32_t fullM, uint32_t emptyM,
+                                           const Unit *udesc, volatile int *abort_flag,
+                                           int lane) {
+  using Cf = Cfg<D>;
+  constexpr int COLS = D < kMergeCols ? D : kMergeCols;
+  constexpr int ROUNDS = D / COLS;
+  constexpr int LPH = COLS / 4;            // lanes a head
+  constexpr int HPS = 32 / LPH;            // heads a step
+  constexpr int STEPS = kMaxG / HPS;
+  const int hs = lane / LPH, col = lane % LPH * 4;
+  const int sh = lane & 7;                 // the head whose state this lane holds
+  int it_q = 0, it_m = 0;
+  pkv_wait_prior_grid();
+  while (true) {
+    const int qs = it_q & 1;
+    const bool q_ok = mbar_wait(fullQ + 8 * qs, (it_q >> 1) & 1, abort_flag);
+    Unit w;
+    w.b = -1;
+    if (q_ok) w = udesc[qs];
+    __syncwarp();
+    if (__any_sync(0xffffffffu, w.b < 0)) return;
+    if (lane == 0) mbar_arrive(emptyQ + 8 * qs);
+    ++it_q;
+    float4 acc[ROUNDS][STEPS];
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r)
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) acc[r][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    State st = {-INFINITY, 0.f, -INFINITY};
+    bool bad = false;
+    // other parts of the row that this one takes in: at step s the parts
+    // part + s, ..., part + 7 s, if part is a multiple of 8 s
+    for (int s = 1; w.part % (kFan * s) == 0 && w.part + s < w.parts; s *= kFan) {
+      const int n = min(kFan - 1, (w.parts - 1 - w.part) / s);
+      const int cta0 = w.first_cta + w.part + s;   // the k-th one's CTA: cta0 + k s
+      bool there = lane >= n;
+      for (int i = 0; i < kPollLimit; ++i) {
+        there = there || ld_acquire(p.flags + cta0 + lane * s) != 0;
+        if (__all_sync(0xffffffffu, there) || __any_sync(0xffffffffu, *abort_flag)) break;
+      }
+      if (!__all_sync(0xffffffffu, there)) {
+        if (lane == 0 && p.err) atomicOr(p.err, PKV_ERR_TIMEOUT);
+        bad = true;
+        break;
+      }
+      if (lane < n) p.flags[cta0 + lane * s] = 0;
+      for (int k0 = 0; k0 < n; k0 += 4) {
+        const int k = k0 + (lane >> 3);
+        State x = {-INFINITY, 0.f, -INFINITY};
+        if (k < n && sh < p.G) {
+          const float *a = p.st_part + (static_cast<size_t>(cta0 + k * s) * p.G + sh) * 3;
+          x.m = __ldcg(a);
+          x.l = __ldcg(a + 1);
+          x.M = __ldcg(a + 2);
+        }
+        float fk, fs;
+        take_in(st, x, fk, fs);
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const int h = i * HPS + hs;
+          const float f = __shfl_sync(0xffffffffu, fs, h);
+          float fj[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) fj[j] = __shfl_sync(0xffffffffu, fk, 8 * j + h);
+          if (h < p.G) {
+#pragma unroll
+            for (int r = 0; r < ROUNDS; ++r) {
+              float4 v[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                v[j] = k0 + j < n
+                           ? __ldcg(reinterpret_cast<const float4 *>(
+                                 p.o_part +
+                                 (static_cast<size_t>(cta0 + (k0 + j) * s) * p.G + h) * D +
+                                 r * COLS + col))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+              float4 &a = acc[r][i];
+              a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) fma4(a, fj[j], v[j]);
+            }
+          }
+        }
+      }
+    }
+    // the unit's own four states
+    float fk = 0.f, fs = 0.f;
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r, ++it_m) {
+      const int ms = it_m % Cf::MS;
+      if (!mbar_wait(fullM + 8 * ms, (it_m / Cf::MS) & 1, abort_flag)) bad = true;
+      const float *merge =
+          reinterpret_cast<const float *>(sm + Cf::OFF_MERGE + ms * Cf::MERGE_SLOT);
+      if (r == 0) {
+        const float *a = merge + kCWarps * kMaxG * kMergeRow + lane;
+        const State x = {a[0], a[32], a[64]};
+        take_in(st, x, fk, fs);
+      }
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const int h = i * HPS + hs;
+        const float f = __shfl_sync(0xffffffffu, fs, h);
+        float fj[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fj[j] = __shfl_sync(0xffffffffu, fk, 8 * j + h);
+        if (h < p.G) {
+          float4 &a = acc[r][i];
+          a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+#pragma unroll
+          for (int j = 0; j < kCWarps; ++j)
+            fma4(a, fj[j], *reinterpret_cast<const float4 *>(merge + (j * kMaxG + h) * kMergeRow +
+                                                             col));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(emptyM + 8 * ms);
+    }
+    if (__any_sync(0xffffffffu, bad) || *abort_flag) continue;
+    if (w.part > 0) {   // a partial for the part that takes this one in
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const int h = i * HPS + hs;
+        if (h >= p.G) continue;
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r)
+          __stcg(reinterpret_cast<float4 *>(
+                     p.o_part + (static_cast<size_t>(blockIdx.x) * p.G + h) * D + r * COLS + col),
+                 acc[r][i]);
+      }
+      if (lane < p.G) {
+        float *a = p.st_part + (static_cast<size_t>(blockIdx.x) * p.G + lane) * 3;
+        __stcg(a, st.m);
+        __stcg(a + 1, st.l);
+        __stcg(a + 2, st.M);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        __threadfence();
+        st_release(p.flags + blockIdx.x, 1);
+      }
+      continue;
+    }
+    // no key of weight, or none at all: 0
+    const float inv = st.l != st.l ? st.l
+                      : st.M == -INFINITY || st.l == 0.f ? 0.f
+                                                         : exp2f(st.M - st.m) / st.l;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int h = i * HPS + hs;
+      const float f = __shfl_sync(0xffffffffu, inv, h);
+      if (h >= p.G) continue;
+      __nv_bfloat16 *out = p.out + (static_cast<size_t>(w.b) * p.Hq + w.g * p.G + h) * D + col;
+#pragma unroll
+      for (int r = 0; r < ROUNDS; ++r) {
+        const float4 a = acc[r][i];
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * f, a.y * f);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(a.z * f, a.w * f);
+        *reinterpret_cast<uint2 *>(out + r * COLS) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                       *reinterpret_cast<const uint32_t *>(&hi));
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------- kernel ----
 template <int D>
 __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
@@ -335,10 +559,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t s0 = smem_u32(sm);
   const uint32_t full = s0 + Cf::OFF_BAR, empty = full + 8 * Cf::NS,
-                 fullQ = empty + 8 * Cf::NS, emptyQ = fullQ + 16;
+                 fullQ = empty + 8 * Cf::NS, emptyQ = fullQ + 16, fullM = emptyQ + 16,
+                 emptyM = fullM + 8 * Cf::MS;
   uint32_t *tile_word = reinterpret_cast<uint32_t *>(sm + Cf::OFF_TILE);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OFF_MISC);
-  int *last_flag = reinterpret_cast<int *>(sm + Cf::OFF_MISC) + 1;
   Unit *udesc = reinterpret_cast<Unit *>(sm + Cf::OFF_DESC);
   int2 *rows = reinterpret_cast<int2 *>(sm + Cf::OFF_ROWS);
   int *pre = reinterpret_cast<int *>(sm + Cf::OFF_PRE);
@@ -353,7 +577,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(fullQ + 8 * i, 1);
-      mbar_init(emptyQ + 8 * i, kCWarps);
+      mbar_init(emptyQ + 8 * i, kCWarps + 1);   // the joining warp reads the unit too
+    }
+    for (int i = 0; i < Cf::MS; ++i) {
+      mbar_init(fullM + 8 * i, kCWarps);
+      mbar_init(emptyM + 8 * i, 1);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -540,6 +768,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     return;
   }
 
+  if (warp == kCWarps + 1) {
+    join_units<D>(p, sm, fullQ, emptyQ, fullM, emptyM, udesc, abort_flag, lane);
+    return;
+  }
+
   // ============================== consumers ==============================
   pkv_wait_prior_grid();
   pkv_allow_next_grid();
@@ -553,15 +786,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
   const int gid = lane >> 2, tig = lane & 3;
   const int h0 = 2 * tig, h1 = h0 + 1;
   constexpr int KS = D / 16;      // 16-byte units of a row = MMA steps over D = m-tiles of O^T
-  constexpr bool Q_REGS = D <= 256;
+  constexpr bool Q_REGS = D <= 256;   // the query stays in registers
   constexpr int QK = Q_REGS ? KS : 1;
-  float *merge = reinterpret_cast<float *>(sm + Cf::OFF_MERGE);
-  float *stat = reinterpret_cast<float *>(sm + Cf::OFF_STAT);   // m, l, M: [3][4][8]
   const int ldsm_row = 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7);
   const uint32_t ldsm_base = row_base<D>(ldsm_row);
   const int ldsm_unit = lane >> 4;
-  int it = 0, it_q = 0;
-  bool failed = false;
+  const bool hv = gid < p.G;
+  int it = 0, it_q = 0, it_m = 0;
+  auto give_up = [&]() {
+    *abort_flag = 1;
+    if (lane == 0 && p.err) atomicOr(p.err, PKV_ERR_TIMEOUT);
+  };
 
   while (true) {
     const int qs = it_q & 1;
@@ -569,48 +804,58 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     Unit w;
     w.b = -1;
     if (q_ok) w = udesc[qs];
-    if (!q_ok) {
-      *abort_flag = 1;
-      if (lane == 0 && p.err) atomicOr(p.err, PKV_ERR_TIMEOUT);
-    }
-    if (w.b >= 0) {
-      // q rows to fp16, in place, each scaled by a power of two to its largest
-      for (int h = warp; h < p.G; h += kCWarps) {
-        uint32_t *row = reinterpret_cast<uint32_t *>(sm + Cf::OFF_Q + qs * Cf::Q_STAGE +
-                                                     h * Cf::Q_ROW);
-        uint32_t v[D / 64], m = 0;
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          v[j] = row[lane + 32 * j];
-          m = __vmaxu2(m, v[j] & 0x7fff7fffu);
-        }
-        m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-        const int e = min(max(static_cast<int>(m >> 7) - 127, -126), 126);
-        const float f = exp2i(-e);
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j)
-          row[lane + 32 * j] = pack_f16(__uint_as_float(v[j] << 16) * f,
-                                        __uint_as_float(v[j] & 0xffff0000u) * f);
-        if (lane == 0)
-          reinterpret_cast<float *>(sm + Cf::OFF_QS)[qs * kMaxG + h] = p.scale_log2 * exp2i(e);
-      }
-      fence_proxy_async();
-    }
-    // all consumer threads leave the loop together (end of work, or a wait gave up)
-    if (consumer_sync_or(w.b < 0)) break;
+    else give_up();
+    // q to fp16, each row scaled by a power of two to its largest magnitude
     const uint8_t *qrow = sm + Cf::OFF_Q + qs * Cf::Q_STAGE + gid * Cf::Q_ROW + tig * 8;
     uint2 qb[QK];
-    const bool hv = gid < p.G;
-    if constexpr (Q_REGS) {
+    float sc0, sc1;
+    if constexpr (Q_REGS) {   // a warp's own copy: lane (gid, tig) holds head gid's fragments
+      if (__any_sync(0xffffffffu, w.b < 0)) break;
+      uint32_t m = 0;
 #pragma unroll
-      for (int c = 0; c < KS; ++c)
+      for (int c = 0; c < KS; ++c) {
         qb[c] = hv ? *reinterpret_cast<const uint2 *>(qrow + 32 * c) : make_uint2(0u, 0u);
-    }
-    const float *qscale = reinterpret_cast<const float *>(sm + Cf::OFF_QS) + qs * kMaxG;
-    const float sc0 = h0 < p.G ? qscale[h0] : 0.f, sc1 = h1 < p.G ? qscale[h1] : 0.f;
-    if constexpr (Q_REGS) {
+        m = __vmaxu2(m, __vmaxu2(qb[c].x & 0x7fff7fffu, qb[c].y & 0x7fff7fffu));
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(emptyQ + 8 * qs);
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int e = q_exponent(m);
+      const float f = exp2i(-e);
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        qb[c].x = bf16_to_f16(qb[c].x, f);
+        qb[c].y = bf16_to_f16(qb[c].y, f);
+      }
+      const float sc = p.scale_log2 * exp2i(e);
+      sc0 = __shfl_sync(0xffffffffu, sc, 8 * tig);       // head h0's, from lane (h0, 0)
+      sc1 = __shfl_sync(0xffffffffu, sc, 8 * tig + 4);
+    } else {                  // in place, once for the four warps
+      if (w.b >= 0) {
+        for (int h = warp; h < p.G; h += kCWarps) {
+          uint32_t *row = reinterpret_cast<uint32_t *>(sm + Cf::OFF_Q + qs * Cf::Q_STAGE +
+                                                       h * Cf::Q_ROW);
+          uint32_t v[D / 64], m = 0;
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            v[j] = row[lane + 32 * j];
+            m = __vmaxu2(m, v[j] & 0x7fff7fffu);
+          }
+          m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+          const int e = q_exponent(m);
+          const float f = exp2i(-e);
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) row[lane + 32 * j] = bf16_to_f16(v[j], f);
+          if (lane == 0)
+            reinterpret_cast<float *>(sm + Cf::OFF_QS)[qs * kMaxG + h] = p.scale_log2 * exp2i(e);
+        }
+        fence_proxy_async();
+      }
+      if (consumer_sync_or(w.b < 0)) break;
+      const float *qscale = reinterpret_cast<const float *>(sm + Cf::OFF_QS) + qs * kMaxG;
+      sc0 = h0 < p.G ? qscale[h0] : 0.f;
+      sc1 = h1 < p.G ? qscale[h1] : 0.f;
     }
     ++it_q;
 
@@ -622,11 +867,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
 
     for (int t = w.ta; t < w.tb; ++t, ++it) {
       const int st = it % Cf::NS;
-      if (!mbar_wait(full + 8 * st, (it / Cf::NS) & 1, abort_flag)) {
-        failed = true;
-        *abort_flag = 1;
-        if (lane == 0 && p.err) atomicOr(p.err, PKV_ERR_TIMEOUT);
-      }
+      if (!mbar_wait(full + 8 * st, (it / Cf::NS) & 1, abort_flag)) give_up();
       const uint32_t tw = tile_word[st];
       const int off = static_cast<int8_t>((tw >> 8) & 0xffu);
       const int tlo = max(w.k0, t * kT), thi = min(w.k1, t * kT + kT);
@@ -728,42 +969,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
       if (lane == 0) mbar_arrive(emptyQ + 8 * qs);
     }
 
-    // ---- the unit's end: join the four warps' states ----
-    {
-      float n0 = m0, n1 = m1;
+    // ---- the unit's end: this warp's state goes to the joining warp ----
+    float n0 = m0, n1 = m1;
 #pragma unroll
-      for (int i = 4; i < 32; i <<= 1) {
-        n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, i));
-        n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, i));
-      }
-      float t0 = m0 == -INFINITY ? 0.f : l0 * exp2f(m0 - n0);
-      float t1 = m1 == -INFINITY ? 0.f : l1 * exp2f(m1 - n1);
-      if (l0 != l0) t0 = l0;   // a NaN score leaves m behind
-      if (l1 != l1) t1 = l1;
-#pragma unroll
-      for (int i = 4; i < 32; i <<= 1) {
-        t0 += __shfl_xor_sync(0xffffffffu, t0, i);
-        t1 += __shfl_xor_sync(0xffffffffu, t1, i);
-      }
-      if (gid == 0) {
-        float *s = stat + warp * kMaxG;
-        s[h0] = n0;
-        s[h1] = n1;
-        s[32 + h0] = t0;
-        s[32 + h1] = t1;
-        s[64 + h0] = M0;
-        s[64 + h1] = M1;
-      }
+    for (int i = 4; i < 32; i <<= 1) {
+      n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, i));
+      n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, i));
     }
-    const bool cut = w.parts > 1;
-    const size_t rec = static_cast<size_t>(blockIdx.x) * 2 + (w.part == 0 ? 1 : 0);
-    constexpr int COLS = D < kMergeCols ? D : kMergeCols;
-    constexpr int HSTEP = kCThreads / COLS;      // heads handled at once
-    const int col = tid % COLS;
-    bool bad = false;
+    l0 = sum_at(l0, m0, n0);
+    l1 = sum_at(l1, m1, n1);
 #pragma unroll
-    for (int c0 = 0; c0 < D; c0 += COLS) {
-      if (c0 > 0) consumer_sync();   // the columns before have been read
+    for (int i = 4; i < 32; i <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, i);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, i);
+    }
+    constexpr int COLS = D < kMergeCols ? D : kMergeCols;
+#pragma unroll
+    for (int c0 = 0; c0 < D; c0 += COLS, ++it_m) {
+      const int ms = it_m % Cf::MS;
+      if (!mbar_wait(emptyM + 8 * ms, ((it_m / Cf::MS) & 1) ^ 1, abort_flag)) give_up();
+      float *merge = reinterpret_cast<float *>(sm + Cf::OFF_MERGE + ms * Cf::MERGE_SLOT);
 #pragma unroll
       for (int u = 0; u < COLS / 16; ++u) {
         const float(&f)[4] = o[c0 / 16 + u];
@@ -771,115 +996,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
         *reinterpret_cast<float2 *>(d) = make_float2(f[0], f[2]);
         *reinterpret_cast<float2 *>(d + kMergeRow) = make_float2(f[1], f[3]);
       }
-      if (c0 == 0) bad = consumer_sync_or(failed);
-      else consumer_sync();
-      if (bad) continue;
-      for (int h = tid / COLS; h < p.G; h += HSTEP) {
-        float M = -INFINITY, m = -INFINITY, l = 0.f, acc = 0.f;
-#pragma unroll
-        for (int i = 0; i < kCWarps; ++i) {
-          M = fmaxf(M, stat[64 + i * kMaxG + h]);
-          m = fmaxf(m, stat[i * kMaxG + h]);
-        }
-#pragma unroll
-        for (int i = 0; i < kCWarps; ++i) {
-          const float Mi = stat[64 + i * kMaxG + h], mi = stat[i * kMaxG + h];
-          const float li = stat[32 + i * kMaxG + h];
-          if (Mi != -INFINITY) acc += merge[(i * kMaxG + h) * kMergeRow + col] * exp2f(Mi - M);
-          if (mi != -INFINITY || li != li) l += li * (mi == m ? 1.f : exp2f(mi - m));
-        }
-        if (cut) {
-          __stcg(p.o_part + (rec * p.G + h) * D + c0 + col, acc);
-          if (c0 + col == 0) {
-            float *s = p.st_part + (rec * p.G + h) * 3;
-            __stcg(s, m);
-            __stcg(s + 1, l);
-            __stcg(s + 2, M);
-          }
-        } else {
-          const float v = M == -INFINITY || l == 0.f ? 0.f : acc * exp2f(M - m) / l;
-          p.out[(static_cast<size_t>(w.b) * p.Hq + w.g * p.G + h) * D + c0 + col] =
-              __float2bfloat16_rn(l != l ? l : v);
-        }
+      if (c0 == 0 && gid == 0) {
+        float *st = merge + kCWarps * kMaxG * kMergeRow + warp * kMaxG;
+        *reinterpret_cast<float2 *>(st + h0) = make_float2(n0, n1);
+        *reinterpret_cast<float2 *>(st + 32 + h0) = make_float2(l0, l1);
+        *reinterpret_cast<float2 *>(st + 64 + h0) = make_float2(M0, M1);
       }
-    }
-    if (bad || !cut) continue;
-    // ---- a cut (row, head): the CTA that arrives last joins the parts ----
-    __threadfence();
-    consumer_sync();
-    if (tid == 0) *last_flag = atomicAdd(p.counters + w.first_cta, 1) == w.parts - 1;
-    consumer_sync();
-    if (!*last_flag) continue;
-    __threadfence();
-    if (tid == 0) p.counters[w.first_cta] = 0;
-    auto record = [&](int j) -> size_t {   // part j's record: CTA first_cta + j's
-      return static_cast<size_t>(w.first_cta + j) * 2 + (j == 0 ? 1 : 0);
-    };
-    // the parts' weights 2^(M_j - m) / l, one warp per head, lanes over parts
-    for (int h = warp; h < p.G; h += kCWarps) {
-      float M = -INFINITY, m = -INFINITY, l = 0.f;
-      for (int j = lane; j < w.parts; j += 32) {
-        const float *s = p.st_part + (record(j) * p.G + h) * 3;
-        const float mj = __ldcg(s), lj = __ldcg(s + 1);
-        merge[j * kMaxG + h] = __ldcg(s + 2);
-        const float mn = fmaxf(m, mj);
-        if (mn != -INFINITY) l = l * exp2f(m - mn) + lj * exp2f(mj - mn);
-        if (lj != lj) l = lj;
-        m = mn;
-        M = fmaxf(M, merge[j * kMaxG + h]);
-      }
-#pragma unroll
-      for (int i = 16; i > 0; i >>= 1) {
-        const float mo = __shfl_xor_sync(0xffffffffu, m, i), lo = __shfl_xor_sync(0xffffffffu, l, i);
-        const float mn = fmaxf(m, mo);
-        const float a = mn == -INFINITY ? 0.f : l * exp2f(m - mn);
-        const float c = mn == -INFINITY ? 0.f : lo * exp2f(mo - mn);
-        l = l != l ? l : lo != lo ? lo : a + c;
-        m = mn;
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
-      }
-      const float f = l != l ? l : M == -INFINITY || l == 0.f ? 0.f : exp2f(M - m) / l;
-      for (int j = lane; j < w.parts; j += 32) {
-        const float Mj = merge[j * kMaxG + h];
-        merge[j * kMaxG + h] = l != l ? l : Mj == -INFINITY ? 0.f : f * exp2f(Mj - M);
-      }
-    }
-    consumer_sync();
-    // four columns a thread and step, the loads of several parts in flight
-    constexpr int NI = D <= 128 ? 1 : 4;   // steps at once
-    const int items = p.G * D / 4;
-    __nv_bfloat16 *out = p.out + (static_cast<size_t>(w.b) * p.Hq + w.g * p.G) * D;
-    for (int i0 = tid; i0 < items; i0 += kCThreads * NI) {
-      float4 acc[NI];
-#pragma unroll
-      for (int k = 0; k < NI; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int j = 0; j < w.parts; ++j) {
-        const float4 *o4 = reinterpret_cast<const float4 *>(p.o_part + record(j) * p.G * D);
-#pragma unroll
-        for (int k = 0; k < NI; ++k) {
-          const int i = i0 + k * kCThreads;
-          if (i < items) {
-            const float4 v = __ldcg(o4 + i);
-            const float f = merge[j * kMaxG + i / (D / 4)];
-            acc[k].x = fmaf(f, v.x, acc[k].x);
-            acc[k].y = fmaf(f, v.y, acc[k].y);
-            acc[k].z = fmaf(f, v.z, acc[k].z);
-            acc[k].w = fmaf(f, v.w, acc[k].w);
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < NI; ++k) {
-        const int i = i0 + k * kCThreads;
-        if (i < items) {
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[k].x, acc[k].y);
-          const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[k].z, acc[k].w);
-          *reinterpret_cast<uint2 *>(out + 4 * i) =
-              make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
-                         *reinterpret_cast<const uint32_t *>(&hi));
-        }
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(fullM + 8 * ms);
     }
   }
 }
@@ -958,12 +1082,12 @@ bool good_heads(int Hq, int Hkv, int D) {
 
 extern "C" {
 
-// Workspace: [kMaxCtas] counters, [kMaxCtas][2] records of G * D floats (partial
-// outputs), [kMaxCtas][2] records of G * 3 floats (running maxima and sum).
+// Workspace: [kMaxCtas] flags, [kMaxCtas] records of G * D floats (partial outputs),
+// [kMaxCtas] records of G * 3 floats (running maxima and sum).
 size_t paged_decode_attn_q8_workspace(int Hq, int Hkv, int D) {
   if (!good_heads(Hq, Hkv, D)) return 0;
   const size_t G = Hq / Hkv;
-  return kMaxCtas * (sizeof(int) + 2 * G * (D + 3) * sizeof(float));
+  return kMaxCtas * (sizeof(int) + G * (D + 3) * sizeof(float));
 }
 
 int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e4m3 *v_cache,
@@ -1038,9 +1162,9 @@ int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.counters = static_cast<int *>(workspace);
-  p.o_part = reinterpret_cast<float *>(p.counters + kMaxCtas);
-  p.st_part = p.o_part + static_cast<size_t>(kMaxCtas) * 2 * p.G * D;
+  p.flags = static_cast<int *>(workspace);
+  p.o_part = reinterpret_cast<float *>(p.flags + kMaxCtas);
+  p.st_part = p.o_part + static_cast<size_t>(kMaxCtas) * p.G * D;
   p.out = reinterpret_cast<__nv_bfloat16 *>(out);
   p.err = err_word;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
