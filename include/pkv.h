@@ -371,8 +371,8 @@ size_t paged_decode_attn_workspace(int B, int Hq, int D, int num_splits);
  * The work is cut over the GPU as in the automatic mode. The workspace must
  * hold paged_decode_attn_q8_workspace(Hq, Hkv, D) bytes (16-byte aligned),
  * whatever the batch and the lengths; zero it once before its first use.
- * Every call leaves its counters zero again, except one that reports
- * PKV_ERR_TIMEOUT. Calls sharing one workspace must not overlap on the GPU.
+ * Every call leaves it zero again, except one that reports PKV_ERR_TIMEOUT,
+ * after which it must be zeroed again. Calls sharing one workspace must not overlap on the GPU.
  * ------------------------------------------------------------------- */
 int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache,
                          const pkv_e4m3 *v_cache, const float *k_scale,

@@ -9,20 +9,24 @@
 //     persistent CTA takes an equal share of it. A (row, head) that straddles
 //     CTAs is cut into parts; a CTA has at most one part that is not its (row,
 //     head)'s first, and that part is its first work, so the workspace is one fp32
-//     record and a flag a CTA. Parts are joined in a tree of eights (part j takes in
+//     record a CTA. Each word of a record is the complement of the value's bits, so
+//     a zero word is one not yet written: who takes a part in polls the words
+//     themselves (no flag, no fence) and clears them. Parts are joined in a tree of eights (part j takes in
 //     j + 1 .. j + 7, then j + 8 ..) in a fixed order: results do not depend on
 //     timing. A first part is its CTA's last work, and a part that takes in others
 //     but is not first its CTA's only work, so they find the others written, or
 //     wait for CTAs launched after them that began with that very work;
 //   * one producer warp streams query rows (cp.async.bulk), K and V tiles
-//     (cp.async.bulk.tensor into a swizzled ring) and the tiles' scales
-//     (cp.async) ahead of four consumer warps, looking up the next unit's pages
-//     while the current one moves;
-//   * each consumer warp owns 16 keys of every tile and keeps its own online
-//     softmax over the whole unit, so no tile needs a barrier between warps. At a
+//     (cp.async.bulk.tensor into a swizzled ring, K and V entries of their own) and
+//     the scales of up to 32 tiles at a time (cp.async) ahead of four consumer warps,
+//     looking up the next unit's pages while the current one moves;
+//   * a consumer warp owns 16 keys of every tile (D >= 256) or 32 keys of every
+//     other tile (two teams of two warps: twice the independent work between two
+//     steps of the softmax) and keeps its own online softmax over the whole unit, so
+//     no tile needs a barrier between warps. At a
 //     unit's end it leaves its state in shared memory and goes on; a joining warp
-//     adds the four states (and a cut row's other parts, which it fetches while the
-//     unit is still running) and writes the output or the partial. Keys are the M rows of
+//     adds the four states (and a cut row's other parts) and writes the output or the
+//     partial. Keys are the M rows of
 //     S^T = K q^T and head-dim is the M rows of O^T = V^T P^T (mma.sync m16n8k16,
 //     fp16 in, fp32 out), the <= 8 query heads of the group are N; P goes from
 //     one product to the other through movmatrix;
@@ -49,7 +53,8 @@
 namespace {
 
 constexpr int kT = 64;               // keys per tile
-constexpr int kCWarps = 4;           // consumer warps, 16 keys of a tile each
+constexpr int kCWarps = 4;           // consumer warps
+constexpr int kScaleWords = 512;     // scales of K (and of V) handed over at once
 constexpr int kCThreads = kCWarps * 32;
 constexpr int kThreads = kCThreads + 64;   // + producer warp and joining warp
 constexpr int kMaxG = 8;             // query heads per kv head (MMA N)
@@ -57,35 +62,43 @@ constexpr int kMaxRows = 512;        // rows per call (row cache kept in smem)
 constexpr int kMaxCtas = 512;        // CTAs the workspace has room for
 constexpr int kSpinLimit = 1 << 22;
 constexpr int kPollLimit = 1 << 20;
-constexpr int kFan = 8;              // parts joined at once in the tree of a cut row
+constexpr int kFan = 8;              // fan-in of the tree that joins a cut row's parts
+constexpr int kMaxSources = 24;      // parts one part takes in, 7 a level, rounded up to 4
 constexpr int kMergeCols = 128;      // columns handed to the joining warp at once
 constexpr int kMergeRow = kMergeCols + 4;   // padded: conflict-free 8-byte stores
 
 template <int D>
 struct Cfg {
   static constexpr int CTAS_PER_SM = D <= 256 ? 2 : 1;
-  static constexpr int NS = D == 64 ? 8 : D == 128 ? 5 : 2;   // ring stages
+  static constexpr int MB = D <= 128 ? 2 : 1;      // 16-key blocks of a tile a warp owns
+  static constexpr int TEAM = kT / 16 / MB;        // warps that share a tile
+  static constexpr int TEAMS = kCWarps / TEAM;
+  // Ring entries, one K or V tile each. An entry always belongs to the same team: a
+  // wait for a phase of an entry is told from the phase before by parity alone, which
+  // holds only for who has waited for that one too.
+  static constexpr int NS = D == 64 ? 16 : D == 128 ? 8 : D == 256 ? 4 : 5;
+  static_assert(TEAMS == 1 || NS % (2 * TEAMS) == 0, "entries keep their team");
   static constexpr int COLS = D < 128 ? D : 128;   // bytes of a row in one box
   static constexpr int CHUNKS = D / COLS;
   static constexpr int CHUNK_BYTES = kT * COLS;
   static constexpr int TILE_BYTES = kT * D;
-  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;   // K, then V
   static constexpr int Q_ROW = D * 2 + 32;   // padded: conflict-free 8-byte loads
   static constexpr int Q_STAGE = kMaxG * Q_ROW;
-  static constexpr int OFF_Q = NS * STAGE_BYTES;
-  static constexpr int OFF_SCALE = OFF_Q + 2 * Q_STAGE;          // [NS][2][kT] f32
+  static constexpr int OFF_Q = NS * TILE_BYTES;
+  static constexpr int OFF_SCALE = OFF_Q + 2 * Q_STAGE;      // [2][2][kScaleWords] f32
   // states handed over: [MS] slots of [4 warps][8 heads] rows, then m, l, M [4][8] each
   static constexpr int MS = D == 512 ? 2 : 1;
   static constexpr int MERGE_SLOT = (kCWarps * kMaxG * kMergeRow + 3 * kCWarps * kMaxG) * 4;
-  static constexpr int OFF_MERGE = OFF_SCALE + NS * 2 * kT * 4;
+  static constexpr int OFF_MERGE = OFF_SCALE + 4 * kScaleWords * 4;
   static constexpr int OFF_QS = OFF_MERGE + MS * MERGE_SLOT;                    // [2][8] f32
-  static constexpr int OFF_BAR = OFF_QS + 2 * kMaxG * 4;
-  static constexpr int N_BARS = 2 * NS + 4 + 2 * MS;
+  static constexpr int OFF_SRC = OFF_QS + 2 * kMaxG * 4;   // weights of parts taken in, [kMaxSources][8]
+  static constexpr int OFF_BAR = OFF_SRC + kMaxSources * kMaxG * 4;
+  static constexpr int N_BARS = 2 * NS + 8 + 2 * MS;
   static constexpr int OFF_TILE = OFF_BAR + N_BARS * 8;   // [NS] u32: box mask, row offset
   static constexpr int OFF_MISC = OFF_TILE + NS * 4;      // abort flag
   static constexpr int OFF_DESC = (OFF_MISC + 8 + 15) & ~15;       // Unit [2]
-  static constexpr int OFF_ROWS = OFF_DESC + 2 * 48;               // int2 [kMaxRows]
-  static constexpr int OFF_PRE = OFF_ROWS + kMaxRows * 8;          // int [kMaxRows + 1]
+  static constexpr int OFF_LEN = OFF_DESC + 2 * 48;                // int [kMaxRows]
+  static constexpr int OFF_PRE = OFF_LEN + kMaxRows * 4;           // int [kMaxRows + 1]
   static constexpr int SMEM = OFF_PRE + (kMaxRows + 1) * 4 + 1024;  // + alignment
 };
 // shared memory per SM on sm_103a: 228 KB, of which 1 KB is reserved per CTA
@@ -149,6 +162,11 @@ __device__ __forceinline__ void copy_word(uint32_t dst, const void *src) {
                "l"(reinterpret_cast<uint64_t>(src))
                : "memory");
 }
+__device__ __forceinline__ void copy_words(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src))
+               : "memory");
+}
 // Arrives on the barrier once this thread's copies so far have landed.
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -208,6 +226,11 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
 }
+__device__ __forceinline__ float ex2(float x) {   // 2^x to 2 ulp; below 2^-126: 0
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ float exp2i(int k) {   // 2^k, -126 <= k <= 127
   return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
@@ -233,8 +256,8 @@ struct Problem {
   const int32_t *table, *batch_idx, *seq_lens;
   int n_slots, max_pages, log2_ps, n_pages, log2_block, window, B, Hq, Hkv, G;
   float scale_log2;
-  int *flags;              // [kMaxCtas], zero between calls: the CTA's part is written
-  float *o_part, *st_part; // [kMaxCtas] records of G * D and G * 3 floats
+  int scale_vec;           // scale words copied at once: 4 or 1
+  uint32_t *o_part, *st_part;   // [kMaxCtas] records of G * D and G * 3 words, zero between calls
   __nv_bfloat16 *out;
   int32_t *err;
 };
@@ -270,16 +293,18 @@ __device__ __forceinline__ int2 row_read(const Problem &p, int b, int &bits) {
 
 // The line of work: a (row, head) with n > 0 tiles takes n + 1 positions, its start
 // and its tiles; pre[b] is the prefix sum of n + 1 over rows, (b, g)'s positions
-// begin at Hkv * pre[b] + g * (n + 1). CTA c of the `ctas` that share the line's
-// `total` positions owns [bound(c), bound(c + 1)); ctas <= total, so every share
-// has a position and every CTA between a (row, head)'s first and last has tiles of it.
+// begin at Hkv * pre[b] + g * (n + 1). The `total` positions are shared by
+// min(CTAs, total) of them: the first `more` own each + 1, the others `each`, so every
+// share has a position and every CTA between a (row, head)'s first and last has tiles
+// of it.
 struct Line {
-  int total, ctas;
-  __device__ __forceinline__ int bound(int c) const {
-    return static_cast<int>(static_cast<long long>(c) * total / ctas);
+  uint32_t each, more;
+  __device__ __forceinline__ int bound(uint32_t c) const {
+    return static_cast<int>(c * each + min(c, more));
   }
-  __device__ __forceinline__ int owner(int x) const {
-    return static_cast<int>((static_cast<long long>(x + 1) * ctas - 1) / total);
+  __device__ __forceinline__ int owner(uint32_t x) const {
+    const uint32_t wide = more * (each + 1);
+    return static_cast<int>(x < wide ? x / (each + 1) : more + (x - wide) / each);
   }
 };
 
@@ -292,7 +317,7 @@ static_assert(sizeof(Unit) <= 48, "unit descriptor slot");
 
 // The next unit from position x on (advanced past it); false at the share's end.
 // The whole converged producer warp calls it with uniform arguments.
-__device__ __forceinline__ bool next_unit(const Problem &p, const Line &line, const int2 *rows,
+__device__ __forceinline__ bool next_unit(const Problem &p, const Line &line, const int *lens,
                                           const int *pre, int end, int &x, Unit &w, int lane) {
   while (x < end) {
     int b = -1;   // the last row whose positions begin at or before x
@@ -304,13 +329,14 @@ __device__ __forceinline__ bool next_unit(const Problem &p, const Line &line, co
     }
     const int width = pre[b + 1] - pre[b];
     const int within = x - p.Hkv * pre[b];
-    const int g = within / width, r = within - g * width;
+    const int g = static_cast<uint32_t>(within) / static_cast<uint32_t>(width);
+    const int r = within - g * width;
     const int n = min(end - x, width - r);
     x += n;
     const int t0 = max(r, 1) - 1, t1 = r + n - 1;   // tiles of the row: [t0, t1)
     if (t1 <= t0) continue;                          // only the start's position
-    const int2 rc = rows[b];
-    const RowInfo ri = row_keys(p, rc.x, rc.y);
+    // a row with tiles has a valid slot
+    const RowInfo ri = row_keys(p, p.batch_idx ? __ldg(p.batch_idx + b) : b, lens[b]);
     const int start = p.Hkv * pre[b] + g * width;
     w.b = b;
     w.g = g;
@@ -336,50 +362,54 @@ __device__ __forceinline__ uint32_t bf16_to_f16(uint32_t v, float f) {
 }
 // A sum l held relative to maximum m, relative to n >= m instead (a NaN stays one).
 __device__ __forceinline__ float sum_at(float l, float m, float n) {
-  return m == -INFINITY ? (l != l ? l : 0.f) : l * exp2f(m - n);
+  return m == -INFINITY ? (l != l ? l : 0.f) : l * ex2(m - n);
 }
 
 // ---------------------------------------------------------- joining ----
-// The softmax state of head lane & 7: m and l the maximum and the sum of the
-// weights 2^s, M the maximum of s + log2 sv that the output is relative to.
-struct State {
-  float m, l, M;
-};
-// Takes in four states, lane 8 k + h holding the k-th of head h. `fk` is what that
-// one's output counts, `fs` what the outputs so far count from now on.
-__device__ __forceinline__ void take_in(State &s, const State &x, float &fk, float &fs) {
-  float m = fmaxf(s.m, x.m), M = fmaxf(s.M, x.M);
-#pragma unroll
-  for (int i = 8; i < 32; i <<= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
-  }
-  float l = sum_at(x.l, x.m, m);
-#pragma unroll
-  for (int i = 8; i < 32; i <<= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
-  fk = x.M == -INFINITY ? 0.f : exp2f(x.M - M);
-  fs = s.M == -INFINITY ? 0.f : exp2f(s.M - M);
-  s.l = sum_at(s.l, s.m, m) + l;
-  s.m = m;
-  s.M = M;
-}
 __device__ __forceinline__ void fma4(float4 &a, float f, const float4 &v) {
   a.x = fmaf(f, v.x, a.x);
   a.y = fmaf(f, v.y, a.y);
   a.z = fmaf(f, v.z, a.z);
   a.w = fmaf(f, v.w, a.w);
 }
-__device__ __forceinline__ int ld_acquire(const int *a) {
-  int v;
-  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(a) : "memory");
+// Words of a partial: the complement of the value's bits, never 0 (the one float
+// whose complement is 0 is a NaN, stored as the canonical one).
+__device__ __forceinline__ uint32_t part_word(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return ~(u == 0xffffffffu ? 0x7fffffffu : u);
+}
+__device__ __forceinline__ float part_value(uint32_t w) { return __uint_as_float(~w); }
+__device__ __forceinline__ uint32_t ld_word(const uint32_t *a) {
+  uint32_t v;
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ void st_release(int *a, int v) {
-  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(a), "r"(v) : "memory");
+__device__ __forceinline__ void st_word(uint32_t *a, uint32_t v) {
+  asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint4 ld_words(const uint32_t *a) {
+  uint4 v;
+  asm volatile("ld.relaxed.gpu.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_words(uint32_t *a, uint4 v) {
+  asm volatile("st.relaxed.gpu.global.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(a), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ bool written(const uint4 &v) {
+  return v.x != 0u && v.y != 0u && v.z != 0u && v.w != 0u;
 }
 
-// The joining warp. A lane holds four columns of every head (D = 64: of every other
-// head) of each 128-column round.
+// The joining warp. A unit's result is a sum over states: its four consumer warps',
+// and, for a part that takes others in, theirs. A state has, per head, the maximum m
+// and the sum l of the weights 2^s, the maximum M of s + log2 sv, and the outputs
+// relative to M. Lanes are (state of four, head) for the statistics and (head, four
+// columns) for the outputs. Written as rolled loops: most of it runs once a CTA, and
+// then the fetching of its instructions is what it takes.
 template <int D>
 __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32_t fullQ,
                                            uint32_t emptyQ, uint32_t fullM, uint32_t emptyM,
@@ -390,9 +420,10 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
   constexpr int ROUNDS = D / COLS;
   constexpr int LPH = COLS / 4;            // lanes a head
   constexpr int HPS = 32 / LPH;            // heads a step
-  constexpr int STEPS = kMaxG / HPS;
+  constexpr int PAIR = ROUNDS == 1 ? 4 / HPS : 2;   // steps at once (four heads, or two)
   const int hs = lane / LPH, col = lane % LPH * 4;
-  const int sh = lane & 7;                 // the head whose state this lane holds
+  const int sh = lane & 7, sk = lane >> 3;
+  float *src_f = reinterpret_cast<float *>(sm + Cf::OFF_SRC);   // [kMaxSources][8]
   int it_q = 0, it_m = 0;
   pkv_wait_prior_grid();
   while (true) {
@@ -405,145 +436,173 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
     if (__any_sync(0xffffffffu, w.b < 0)) return;
     if (lane == 0) mbar_arrive(emptyQ + 8 * qs);
     ++it_q;
-    float4 acc[ROUNDS][STEPS];
-#pragma unroll
-    for (int r = 0; r < ROUNDS; ++r)
-#pragma unroll
-      for (int i = 0; i < STEPS; ++i) acc[r][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    State st = {-INFINITY, 0.f, -INFINITY};
-    bool bad = false;
-    // other parts of the row that this one takes in: at step s the parts
-    // part + s, ..., part + 7 s, if part is a multiple of 8 s
-    for (int s = 1; w.part % (kFan * s) == 0 && w.part + s < w.parts; s *= kFan) {
-      const int n = min(kFan - 1, (w.parts - 1 - w.part) / s);
-      const int cta0 = w.first_cta + w.part + s;   // the k-th one's CTA: cta0 + k s
-      bool there = lane >= n;
-      for (int i = 0; i < kPollLimit; ++i) {
-        there = there || ld_acquire(p.flags + cta0 + lane * s) != 0;
-        if (__all_sync(0xffffffffu, there) || __any_sync(0xffffffffu, *abort_flag)) break;
-      }
-      if (!__all_sync(0xffffffffu, there)) {
-        if (lane == 0 && p.err) atomicOr(p.err, PKV_ERR_TIMEOUT);
-        bad = true;
-        break;
-      }
-      if (lane < n) p.flags[cta0 + lane * s] = 0;
-      for (int k0 = 0; k0 < n; k0 += 4) {
-        const int k = k0 + (lane >> 3);
-        State x = {-INFINITY, 0.f, -INFINITY};
-        if (k < n && sh < p.G) {
-          const float *a = p.st_part + (static_cast<size_t>(cta0 + k * s) * p.G + sh) * 3;
-          x.m = __ldcg(a);
-          x.l = __ldcg(a + 1);
-          x.M = __ldcg(a + 2);
-        }
-        float fk, fs;
-        take_in(st, x, fk, fs);
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-          const int h = i * HPS + hs;
-          const float f = __shfl_sync(0xffffffffu, fs, h);
-          float fj[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) fj[j] = __shfl_sync(0xffffffffu, fk, 8 * j + h);
-          if (h < p.G) {
-#pragma unroll
-            for (int r = 0; r < ROUNDS; ++r) {
-              float4 v[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                v[j] = k0 + j < n
-                           ? __ldcg(reinterpret_cast<const float4 *>(
-                                 p.o_part +
-                                 (static_cast<size_t>(cta0 + (k0 + j) * s) * p.G + h) * D +
-                                 r * COLS + col))
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
-              float4 &a = acc[r][i];
-              a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) fma4(a, fj[j], v[j]);
-            }
-          }
-        }
-      }
+    // The parts this one takes in: at level s = 1, 8, 64 the parts part + s .. part + 7 s,
+    // if part is a multiple of 8 s. Lane q has the CTA of source q = 7 level + k - 1, if
+    // bit q of `takes` is set.
+    int my_cta = 0;
+    uint32_t takes = 0;
+    if (w.parts > 1) {
+      const int level = lane / 7, s = 1 << (3 * level), j = w.part + (lane % 7 + 1) * s;
+      const bool t = level < 3 && w.part % (kFan * s) == 0 && j < w.parts;
+      takes = __ballot_sync(0xffffffffu, t);
+      my_cta = w.first_cta + (t ? j : 0);
     }
-    // the unit's own four states
-    float fk = 0.f, fs = 0.f;
+    const int n_src = 32 - __clz(takes);
+    bool bad = false;
+    // ---- statistics: the unit's own in the merge slot, the sources' in their records ----
+    if (!mbar_wait(fullM + 8 * (it_m % Cf::MS), (it_m / Cf::MS) & 1, abort_flag)) bad = true;
+    const float *own = reinterpret_cast<const float *>(
+                           sm + Cf::OFF_MERGE + it_m % Cf::MS * Cf::MERGE_SLOT) +
+                       kCWarps * kMaxG * kMergeRow + lane;
+    const float own_m = own[0], own_l = own[32], own_M = own[64];
+    float m = own_m, l = own_l, M = own_M;   // this lane's states
+#pragma unroll 1
+    for (int k0 = 0; k0 < n_src; k0 += 4) {
+      const int k = k0 + sk;
+      const int cta = __shfl_sync(0xffffffffu, my_cta, k);
+      const bool mine = (takes >> k & 1u) && sh < p.G;
+      uint32_t *a = p.st_part + (static_cast<size_t>(cta) * p.G + sh) * 3;
+      uint32_t x0 = 0, x1 = 0, x2 = 0;
+      for (int i = 0;; ++i) {
+        if (mine) {
+          x0 = ld_word(a);
+          x1 = ld_word(a + 1);
+          x2 = ld_word(a + 2);
+        }
+        const bool there = !mine || (x0 != 0u && x1 != 0u && x2 != 0u);
+        if (__all_sync(0xffffffffu, there)) break;
+        if (i >= kPollLimit || __any_sync(0xffffffffu, *abort_flag)) {
+          bad = true;
+          break;
+        }
+      }
+      if (mine) {
+        st_word(a, 0u);
+        st_word(a + 1, 0u);
+        st_word(a + 2, 0u);
+      }
+      const float xm = mine ? part_value(x0) : -INFINITY, xM = mine ? part_value(x2) : -INFINITY;
+      src_f[k * kMaxG + sh] = xM;
+      const float mn = fmaxf(m, xm);
+      l = sum_at(l, m, mn) + sum_at(mine ? part_value(x1) : 0.f, xm, mn);
+      m = mn;
+      M = fmaxf(M, xM);
+    }
+    const float lane_m = m;
 #pragma unroll
+    for (int i = 8; i < 32; i <<= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
+    }
+    l = sum_at(l, lane_m, m);
+    const float own_f = own_M == -INFINITY ? 0.f : ex2(own_M - M);
+#pragma unroll 1
+    for (int k = sk; k < n_src; k += 4) {   // each lane the words it wrote
+      const float x = src_f[k * kMaxG + sh];
+      src_f[k * kMaxG + sh] = x == -INFINITY ? 0.f : ex2(x - M);
+    }
+#pragma unroll
+    for (int i = 8; i < 32; i <<= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+    // what the sum is multiplied by: 1 for a partial; no key of weight, or none: 0
+    const float last = w.part > 0 ? 1.f
+                       : l != l   ? l
+                       : M == -INFINITY || l == 0.f ? 0.f
+                                                    : ex2(M - m) / l;
+    __syncwarp();
+    // ---- outputs ----
+#pragma unroll 1
     for (int r = 0; r < ROUNDS; ++r, ++it_m) {
       const int ms = it_m % Cf::MS;
-      if (!mbar_wait(fullM + 8 * ms, (it_m / Cf::MS) & 1, abort_flag)) bad = true;
+      if (r > 0 && !mbar_wait(fullM + 8 * ms, (it_m / Cf::MS) & 1, abort_flag)) bad = true;
       const float *merge =
-          reinterpret_cast<const float *>(sm + Cf::OFF_MERGE + ms * Cf::MERGE_SLOT);
-      if (r == 0) {
-        const float *a = merge + kCWarps * kMaxG * kMergeRow + lane;
-        const State x = {a[0], a[32], a[64]};
-        take_in(st, x, fk, fs);
-      }
+          reinterpret_cast<const float *>(sm + Cf::OFF_MERGE + ms * Cf::MERGE_SLOT) + col;
+#pragma unroll 1
+      for (int i0 = 0; i0 < p.G; i0 += PAIR * HPS) {
+        float4 acc[PAIR];
 #pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        const int h = i * HPS + hs;
-        const float f = __shfl_sync(0xffffffffu, fs, h);
-        float fj[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) fj[j] = __shfl_sync(0xffffffffu, fk, 8 * j + h);
-        if (h < p.G) {
-          float4 &a = acc[r][i];
-          a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+        for (int i = 0; i < PAIR; ++i) {
+          const int h = (i0 + i * HPS + hs) & 7;
+          acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < kCWarps; ++j)
-            fma4(a, fj[j], *reinterpret_cast<const float4 *>(merge + (j * kMaxG + h) * kMergeRow +
-                                                             col));
+            fma4(acc[i], __shfl_sync(0xffffffffu, own_f, 8 * j + h),
+                 *reinterpret_cast<const float4 *>(merge + (j * kMaxG + h) * kMergeRow));
+        }
+#pragma unroll 1
+        for (int k0 = 0; k0 < n_src && !bad; k0 += 4) {
+          uint32_t *a[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            a[j] = p.o_part + (static_cast<size_t>(__shfl_sync(0xffffffffu, my_cta, k0 + j)) * p.G +
+                               i0 + hs) * D + r * COLS + col;
+          uint4 v[4][PAIR];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < PAIR; ++i)
+              v[j][i] = make_uint4(0u, 0u, 0u, 0u);
+          for (int n = 0;; ++n) {
+            bool there = true;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < PAIR; ++i)
+                if ((takes >> (k0 + j) & 1u) && i0 + i * HPS + hs < p.G && !written(v[j][i]))
+                  v[j][i] = ld_words(a[j] + i * HPS * D);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < PAIR; ++i)
+                there = there && (!(takes >> (k0 + j) & 1u) || i0 + i * HPS + hs >= p.G ||
+                                  written(v[j][i]));
+            if (__all_sync(0xffffffffu, there)) break;
+            if (n >= kPollLimit || __any_sync(0xffffffffu, *abort_flag)) {
+              bad = true;
+              break;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < PAIR; ++i) {
+              const int h = i0 + i * HPS + hs;
+              if ((takes >> (k0 + j) & 1u) && h < p.G) {
+                st_words(a[j] + i * HPS * D, make_uint4(0u, 0u, 0u, 0u));
+                fma4(acc[i], src_f[(k0 + j) * kMaxG + h],
+                     make_float4(part_value(v[j][i].x), part_value(v[j][i].y),
+                                 part_value(v[j][i].z), part_value(v[j][i].w)));
+              }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PAIR; ++i) {
+          const int h = i0 + i * HPS + hs;
+          const float f = __shfl_sync(0xffffffffu, last, h & 7);
+          if (h >= p.G || bad || *abort_flag) continue;
+          const float4 &o = acc[i];
+          if (w.part > 0) {
+            st_words(p.o_part + (static_cast<size_t>(blockIdx.x) * p.G + h) * D + r * COLS + col,
+                     make_uint4(part_word(o.x), part_word(o.y), part_word(o.z), part_word(o.w)));
+          } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * f, o.y * f);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * f, o.w * f);
+            *reinterpret_cast<uint2 *>(
+                p.out + (static_cast<size_t>(w.b) * p.Hq + w.g * p.G + h) * D + r * COLS + col) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                           *reinterpret_cast<const uint32_t *>(&hi));
+          }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(emptyM + 8 * ms);
     }
-    if (__any_sync(0xffffffffu, bad) || *abort_flag) continue;
-    if (w.part > 0) {   // a partial for the part that takes this one in
-#pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        const int h = i * HPS + hs;
-        if (h >= p.G) continue;
-#pragma unroll
-        for (int r = 0; r < ROUNDS; ++r)
-          __stcg(reinterpret_cast<float4 *>(
-                     p.o_part + (static_cast<size_t>(blockIdx.x) * p.G + h) * D + r * COLS + col),
-                 acc[r][i]);
-      }
-      if (lane < p.G) {
-        float *a = p.st_part + (static_cast<size_t>(blockIdx.x) * p.G + lane) * 3;
-        __stcg(a, st.m);
-        __stcg(a + 1, st.l);
-        __stcg(a + 2, st.M);
-      }
-      __syncwarp();
-      if (lane == 0) {
-        __threadfence();
-        st_release(p.flags + blockIdx.x, 1);
-      }
-      continue;
+    if (w.part > 0 && !bad && !*abort_flag && lane < p.G) {
+      uint32_t *a = p.st_part + (static_cast<size_t>(blockIdx.x) * p.G + lane) * 3;
+      st_word(a, part_word(m));
+      st_word(a + 1, part_word(l));
+      st_word(a + 2, part_word(M));
     }
-    // no key of weight, or none at all: 0
-    const float inv = st.l != st.l ? st.l
-                      : st.M == -INFINITY || st.l == 0.f ? 0.f
-                                                         : exp2f(st.M - st.m) / st.l;
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int h = i * HPS + hs;
-      const float f = __shfl_sync(0xffffffffu, inv, h);
-      if (h >= p.G) continue;
-      __nv_bfloat16 *out = p.out + (static_cast<size_t>(w.b) * p.Hq + w.g * p.G + h) * D + col;
-#pragma unroll
-      for (int r = 0; r < ROUNDS; ++r) {
-        const float4 a = acc[r][i];
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * f, a.y * f);
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(a.z * f, a.w * f);
-        *reinterpret_cast<uint2 *>(out + r * COLS) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
-                       *reinterpret_cast<const uint32_t *>(&hi));
-      }
-    }
+    if (bad && lane == 0 && p.err) atomicOr(p.err, PKV_ERR_TIMEOUT);
   }
 }
 
@@ -560,11 +619,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
   const uint32_t s0 = smem_u32(sm);
   const uint32_t full = s0 + Cf::OFF_BAR, empty = full + 8 * Cf::NS,
                  fullQ = empty + 8 * Cf::NS, emptyQ = fullQ + 16, fullM = emptyQ + 16,
-                 emptyM = fullM + 8 * Cf::MS;
+                 emptyM = fullM + 8 * Cf::MS, fullS = emptyM + 8 * Cf::MS, emptyS = fullS + 16;
   uint32_t *tile_word = reinterpret_cast<uint32_t *>(sm + Cf::OFF_TILE);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OFF_MISC);
   Unit *udesc = reinterpret_cast<Unit *>(sm + Cf::OFF_DESC);
-  int2 *rows = reinterpret_cast<int2 *>(sm + Cf::OFF_ROWS);
+  int *lens = reinterpret_cast<int *>(sm + Cf::OFF_LEN);
   int *pre = reinterpret_cast<int *>(sm + Cf::OFF_PRE);
 
   // ---- set-up, before the dependency wait: barriers, row cache, prefix sums.
@@ -572,8 +631,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
   // kernel that may still run writes (the header's rule).
   if (tid == 0) {
     for (int i = 0; i < Cf::NS; ++i) {
-      mbar_init(full + 8 * i, 1 + 32);   // the copies' arrival, and every lane's scale words
-      mbar_init(empty + 8 * i, kCWarps);
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, Cf::TEAM);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(fullS + 8 * i, 32);
+      mbar_init(emptyS + 8 * i, kCWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(fullQ + 8 * i, 1);
@@ -593,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     const int2 rc = row_read(p, b, bits);
     row_bits |= bits;
     const RowInfo r = row_keys(p, rc.x, rc.y);
-    rows[b] = rc;
+    lens[b] = rc.y;
     pre[b + 1] = r.n_tiles > 0 ? r.n_tiles + 1 : 0;
   }
   __syncthreads();
@@ -614,9 +677,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     if (lane == 0) pre[0] = 0;
   }
   __syncthreads();
-  Line line;
-  line.total = p.Hkv * pre[p.B];
-  line.ctas = min(static_cast<int>(gridDim.x), line.total);
+  const uint32_t total = p.Hkv * pre[p.B], ctas = min(gridDim.x, max(total, 1u));
+  const Line line = {total / ctas, total % ctas};
 
   const int ps = 1 << p.log2_ps;
   const int log2_box = min(p.log2_ps, 6);
@@ -624,6 +686,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
   const int boxes = kT >> log2_box;            // copies a tile
   const int log2_sc = min(p.log2_block, 6);    // keys of a tile that share a scale word
   const int scales = kT >> log2_sc;            // scale words of a tile, for K and for V
+  const int batch = min(32 / boxes, kScaleWords / scales);   // tiles looked up at once
 
   if (warp == kCWarps) {
     // ======================== producer (one warp) ========================
@@ -651,14 +714,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
       return ((u.g * p.n_pages + page) << p.log2_ps) + (key & (ps - 1));
     };
     int x = 0, end = 0;
-    if (static_cast<int>(blockIdx.x) < line.ctas) {
+    if (blockIdx.x < ctas) {
       x = line.bound(blockIdx.x);
       end = line.bound(blockIdx.x + 1);
     }
     Unit w, wn;
-    int it = 0, it_q = 0;
+    int it = 0, it_q = 0, it_s = 0;
     bool ok = true;
-    bool have = next_unit(p, line, rows, pre, end, x, w, lane);
+    bool have = next_unit(p, line, lens, pre, end, x, w, lane);
     int page_first = have ? box_page(w, lane) : -1;
     pkv_wait_prior_grid();
     while (ok && have) {
@@ -681,16 +744,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
                     static_cast<uint32_t>(D * 2), fullQ + 8 * qs);
         ++it_q;
       }
-      const int n_boxes = (w.tb - w.ta) * boxes;
-      for (int base = 0; base < n_boxes && ok; base += 32) {
-        const int row = box_row(w, base + lane, base == 0 ? page_first : box_page(w, base + lane));
-        const int tiles_here = min(32, n_boxes - base) / boxes;
+      const int n_tiles = w.tb - w.ta;
+      for (int base = 0; base < n_tiles && ok; base += batch) {
+        const int j0 = base * boxes;
+        const int row = box_row(w, j0 + lane, base == 0 ? page_first : box_page(w, j0 + lane));
+        const int tiles_here = min(batch, n_tiles - base);
         for (int tt = 0; tt < tiles_here; ++tt) {
-          const int t = w.ta + base / boxes + tt;
-          const int st = it % Cf::NS;
-          ok = mbar_wait(empty + 8 * st, ((it / Cf::NS) & 1) ^ 1, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+          const int t = w.ta + base + tt;
           const uint32_t mask =
               (__ballot_sync(0xffffffffu, row >= 0) >> (tt * boxes)) & ((1u << boxes) - 1u);
           // One box per tile (pages of >= 64 keys): a tile whose keys end or start
@@ -703,38 +763,59 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
             if (hi_r < kT && (lo_r == 0 || hi_r <= kT - lo_r)) off = hi_r - kT;
             else if (lo_r > 0) off = lo_r;
           }
-          const uint32_t bar = full + 8 * st;
-          const uint32_t dst = s0 + st * Cf::STAGE_BYTES;
-          if (lane == 0) {
-            tile_word[st] = mask | (static_cast<uint32_t>(off & 0xff) << 8);
-            mbar_expect_tx(bar, 2u * __popc(mask) * box_rows * D);
-          }
-          __syncwarp();
-          if (lane >= tt * boxes && lane < (tt + 1) * boxes && row >= 0) {
-            const int i = lane - tt * boxes;
-            const int y = (row & (ps - 1)) + off, z = row >> p.log2_ps;
 #pragma unroll
-            for (int cc = 0; cc < Cf::CHUNKS; ++cc) {
-              const uint32_t d = dst + cc * Cf::CHUNK_BYTES + i * box_rows * Cf::COLS;
-              tma_load_3d(d, &tmK, cc * Cf::COLS, y, z, bar);
-              tma_load_3d(d + Cf::TILE_BYTES, &tmV, cc * Cf::COLS, y, z, bar);
+          for (int kv = 0; kv < 2; ++kv) {
+            const int st = it % Cf::NS;
+            ok = ok && mbar_wait(empty + 8 * st, ((it / Cf::NS) & 1) ^ 1, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint32_t bar = full + 8 * st;
+            const uint32_t dst = s0 + st * Cf::TILE_BYTES;
+            if (lane == 0) {
+              tile_word[st] = mask | (static_cast<uint32_t>(off & 0xff) << 8);
+              mbar_expect_tx(bar, __popc(mask) * box_rows * D);
             }
-          }
-          for (int e0 = 0; e0 < 2 * scales; e0 += 32) {
-            const int e = e0 + lane, ee = e & (scales - 1);
-            const int key = ee << log2_sc;   // within the tile
-            const int r = __shfl_sync(0xffffffffu, row, (tt * boxes + (key >> log2_box)) & 31);
-            if (e < 2 * scales && r >= 0) {
-              const int idx = (r + (key & (box_rows - 1))) >> p.log2_block;
-              copy_word(s0 + Cf::OFF_SCALE + ((st * 2 + (e >= scales)) * kT + ee) * 4,
-                        (e >= scales ? p.v_scale : p.k_scale) + idx);
+            __syncwarp();
+            if (lane >= tt * boxes && lane < (tt + 1) * boxes && row >= 0) {
+              const int i = lane - tt * boxes;
+              const int y = (row & (ps - 1)) + off, z = row >> p.log2_ps;
+#pragma unroll
+              for (int cc = 0; cc < Cf::CHUNKS; ++cc)
+                tma_load_3d(dst + cc * Cf::CHUNK_BYTES + i * box_rows * Cf::COLS,
+                            kv ? &tmV : &tmK, cc * Cf::COLS, y, z, bar);
             }
+            ++it;
           }
-          copies_arrive(bar);
-          ++it;
+          if (!ok) break;
+          if (tt == 0) {   // the scales of all tiles here, once the first tile is moving
+            const int ss = it_s & 1;
+            ok = mbar_wait(emptyS + 8 * ss, ((it_s >> 1) & 1) ^ 1, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const int log2_items = 31 - __clz(scales / p.scale_vec);   // a tile's copies
+            const int items = tiles_here << log2_items;
+            for (int e0 = 0; e0 < 2 * items; e0 += 32) {
+              const int e = e0 + lane, kv = e >= items, ee = kv ? e - items : e;
+              const int tile = ee >> log2_items;
+              const int word = (ee & ((1 << log2_items) - 1)) * p.scale_vec;
+              const int key = word << log2_sc;   // within the tile
+              const int r =
+                  __shfl_sync(0xffffffffu, row, (tile * boxes + (key >> log2_box)) & 31);
+              if (e < 2 * items && r >= 0) {
+                const uint32_t dst = s0 + Cf::OFF_SCALE +
+                                     ((ss * 2 + kv) * kScaleWords + tile * scales + word) * 4;
+                const float *src = (kv ? p.v_scale : p.k_scale) +
+                                   ((r + (key & (box_rows - 1))) >> p.log2_block);
+                if (p.scale_vec == 4) copy_words(dst, src);
+                else copy_word(dst, src);
+              }
+            }
+            copies_arrive(fullS + 8 * ss);
+            ++it_s;
+          }
           if (!looked_ahead) {   // the next unit's lookups, once this one is moving
             looked_ahead = true;
-            have_next = next_unit(p, line, rows, pre, end, x, wn, lane);
+            have_next = next_unit(p, line, lens, pre, end, x, wn, lane);
             page_next = have_next ? box_page(wn, lane) : -1;
           }
         }
@@ -763,8 +844,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     volatile int no_abort = 0;
     for (int s = 0; s < Cf::NS; ++s)
       if (it > s) (void)mbar_wait(full + 8 * s, ((it - 1 - s) / Cf::NS) & 1, &no_abort);
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < 2; ++s) {
       if (it_q > s) (void)mbar_wait(fullQ + 8 * s, ((it_q - 1 - s) / 2) & 1, &no_abort);
+      if (it_s > s) (void)mbar_wait(fullS + 8 * s, ((it_s - 1 - s) / 2) & 1, &no_abort);
+    }
     return;
   }
 
@@ -788,11 +871,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
   constexpr int KS = D / 16;      // 16-byte units of a row = MMA steps over D = m-tiles of O^T
   constexpr bool Q_REGS = D <= 256;   // the query stays in registers
   constexpr int QK = Q_REGS ? KS : 1;
-  const int ldsm_row = 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7);
-  const uint32_t ldsm_base = row_base<D>(ldsm_row);
+  constexpr int MB = Cf::MB;
+  const int team = warp / Cf::TEAM, key0 = 16 * MB * (warp % Cf::TEAM);   // this warp's tile rows
+  // 16-byte units of rows key0 .. key0 + 15 for ldmatrix (the next 16: a constant on)
+  const uint32_t ldsm_base = row_base<D>(key0 + ((lane >> 3) & 1) * 8 + (lane & 7));
+  constexpr uint32_t ROWS16 = 16 * Cf::COLS;
   const int ldsm_unit = lane >> 4;
   const bool hv = gid < p.G;
-  int it = 0, it_q = 0, it_m = 0;
+  int tile = 0, it_q = 0, it_m = 0, it_s = 0;   // tile: tiles of the units before
   auto give_up = [&]() {
     *abort_flag = 1;
     if (lane == 0 && p.err) atomicOr(p.err, PKV_ERR_TIMEOUT);
@@ -865,105 +951,163 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // this lane's keys
     float M0 = -INFINITY, M1 = -INFINITY;                       // the warp's keys
 
-    for (int t = w.ta; t < w.tb; ++t, ++it) {
-      const int st = it % Cf::NS;
-      if (!mbar_wait(full + 8 * st, (it / Cf::NS) & 1, abort_flag)) give_up();
-      const uint32_t tw = tile_word[st];
-      const int off = static_cast<int8_t>((tw >> 8) & 0xffu);
-      const int tlo = max(w.k0, t * kT), thi = min(w.k1, t * kT + kT);
-      const uint32_t kbase = s0 + st * Cf::STAGE_BYTES, vbase = kbase + Cf::TILE_BYTES;
-      // tile row r holds a key of the unit?
-      auto valid = [&](int r) -> bool {
-        const int key = t * kT + r + off;
-        return key >= tlo && key < thi && ((tw >> (r >> log2_box)) & 1u);
+    for (int t0 = w.ta; t0 < w.tb; t0 += batch, ++it_s) {   // tiles whose scales come together
+      const int t1 = min(t0 + batch, w.tb);
+      const int ss = it_s & 1;
+      const float *scale_words =
+          reinterpret_cast<const float *>(sm + Cf::OFF_SCALE) + ss * 2 * kScaleWords;
+      bool have_scales = false;
+      auto wait_scales = [&]() {
+        if (have_scales) return;
+        have_scales = true;
+        if (!mbar_wait(fullS + 8 * ss, (it_s >> 1) & 1, abort_flag)) give_up();
+        __syncwarp();
       };
+      const int t_team = Cf::TEAMS == 2 ? t0 + (((tile + t0 - w.ta) ^ team) & 1) : t0;
+      for (int t = t_team; t < t1; t += Cf::TEAMS) {
+        const int ent = 2 * (tile + t - w.ta);   // ring entries: K, then V
+        int st = ent % Cf::NS;
+        if (!mbar_wait(full + 8 * st, (ent / Cf::NS) & 1, abort_flag)) give_up();
+        __syncwarp();
+        const uint32_t tw = tile_word[st];
+        const int off = static_cast<int8_t>((tw >> 8) & 0xffu);
+        const int tlo = max(w.k0 - t * kT, 0) - off, thi = min(w.k1 - t * kT, kT) - off;
+        // tile row r holds a key of the unit?
+        auto valid = [&](int r) -> bool {
+          return r >= tlo && r < thi && ((tw >> (r >> log2_box)) & 1u);
+        };
+        const bool whole = tlo == 0 && thi == kT && (tw & 0xffu) == (1u << boxes) - 1u;
+        uint32_t base = s0 + st * Cf::TILE_BYTES;
 
-      // ---- S^T [16 keys x 8 heads] ----
-      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+        // ---- S^T [16 MB keys x 8 heads]: lane's keys key0 + gid + 8 i, heads h0, h1.
+        // Two chains of MMAs: the two key blocks, or even and odd 16-byte units of one.
+        float sa[2][4];
 #pragma unroll
-      for (int c = 0; c < KS; c += 2) {
-        uint32_t r[4], a0, a1, a2, a3;
-        ldsm_x4(unit_addr<D>(kbase, ldsm_base, c + ldsm_unit), r);
-        uint2 q0, q1;
-        if constexpr (Q_REGS) {
-          q0 = qb[c];
-          q1 = qb[c + 1];
-        } else {
-          q0 = hv ? *reinterpret_cast<const uint2 *>(qrow + 32 * c) : make_uint2(0u, 0u);
-          q1 = hv ? *reinterpret_cast<const uint2 *>(qrow + 32 * c + 32) : make_uint2(0u, 0u);
+        for (int i = 0; i < 2; ++i) sa[i][0] = sa[i][1] = sa[i][2] = sa[i][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < KS; c += 2) {
+          uint2 q0, q1;
+          if constexpr (Q_REGS) {
+            q0 = qb[c];
+            q1 = qb[c + 1];
+          } else {
+            q0 = hv ? *reinterpret_cast<const uint2 *>(qrow + 32 * c) : make_uint2(0u, 0u);
+            q1 = hv ? *reinterpret_cast<const uint2 *>(qrow + 32 * c + 32) : make_uint2(0u, 0u);
+          }
+#pragma unroll
+          for (int i = 0; i < MB; ++i) {
+            uint32_t r[4], a0, a1, a2, a3;
+            ldsm_x4(unit_addr<D>(base, ldsm_base, c + ldsm_unit) + i * ROWS16, r);
+            codes_to_f16(r[0], a0, a2);
+            codes_to_f16(r[1], a1, a3);
+            mma_f16(sa[i], a0, a1, a2, a3, q0.x, q0.y);
+            codes_to_f16(r[2], a0, a2);
+            codes_to_f16(r[3], a1, a3);
+            mma_f16(sa[MB == 2 ? i : 1], a0, a1, a2, a3, q1.x, q1.y);
+          }
         }
-        codes_to_f16(r[0], a0, a2);
-        codes_to_f16(r[1], a1, a3);
-        mma_f16(sa, a0, a1, a2, a3, q0.x, q0.y);
-        codes_to_f16(r[2], a0, a2);
-        codes_to_f16(r[3], a1, a3);
-        mma_f16(sb, a0, a1, a2, a3, q1.x, q1.y);
-      }
-      // ---- online softmax; lane: keys r_lo, r_hi of the tile, heads h0, h1 ----
-      const int r_lo = 16 * warp + gid, r_hi = r_lo + 8;
-      const float *ks = reinterpret_cast<const float *>(sm + Cf::OFF_SCALE) + st * 2 * kT;
-      const int i_lo = ((r_lo + off) & (kT - 1)) >> log2_sc;
-      const int i_hi = ((r_hi + off) & (kT - 1)) >> log2_sc;
-      const bool v_lo = valid(r_lo), v_hi = valid(r_hi);
-      const float k_lo = ks[i_lo], k_hi = ks[i_hi];
-      const float g_lo = __log2f(ks[kT + i_lo]), g_hi = __log2f(ks[kT + i_hi]);
-      const float s00 = v_lo ? (sa[0] + sb[0]) * (k_lo * sc0) : -INFINITY;
-      const float s01 = v_lo ? (sa[1] + sb[1]) * (k_lo * sc1) : -INFINITY;
-      const float s10 = v_hi ? (sa[2] + sb[2]) * (k_hi * sc0) : -INFINITY;
-      const float s11 = v_hi ? (sa[3] + sb[3]) * (k_hi * sc1) : -INFINITY;
-      const float z00 = v_lo ? s00 + g_lo : -INFINITY, z01 = v_lo ? s01 + g_lo : -INFINITY;
-      const float z10 = v_hi ? s10 + g_hi : -INFINITY, z11 = v_hi ? s11 + g_hi : -INFINITY;
-      {
-        const float n0 = fmaxf(m0, fmaxf(s00, s10)), n1 = fmaxf(m1, fmaxf(s01, s11));
+        if constexpr (MB == 1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sa[0][i] += sa[1][i];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + 8 * st);   // the K entry is free
+        wait_scales();
+        // ---- online softmax ----
+        const float *kw = scale_words + (t - t0) * scales, *vw = kw + kScaleWords;
+        float sx[2 * MB][2], lv[2 * MB];
+#pragma unroll
+        for (int i = 0; i < 2 * MB; ++i) {
+          const int r = key0 + gid + 8 * i;
+          const int w0 = ((r + off) & (kT - 1)) >> log2_sc;
+          const float k = kw[w0];
+          lv[i] = __log2f(vw[w0]);
+          sx[i][0] = sa[i >> 1][(i & 1) * 2] * (k * sc0);
+          sx[i][1] = sa[i >> 1][(i & 1) * 2 + 1] * (k * sc1);
+          if (!whole && !valid(r)) {
+            sx[i][0] = sx[i][1] = -INFINITY;
+            lv[i] = 0.f;
+          }
+        }
+        float n0 = m0, n1 = m1, x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 2 * MB; ++i) {
+          n0 = fmaxf(n0, sx[i][0]);
+          n1 = fmaxf(n1, sx[i][1]);
+          x0 = fmaxf(x0, sx[i][0] + lv[i]);
+          x1 = fmaxf(x1, sx[i][1] + lv[i]);
+        }
         const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
-        l0 = l0 * exp2f(m0 - u0) + (exp2f(s00 - u0) + exp2f(s10 - u0));
-        l1 = l1 * exp2f(m1 - u1) + (exp2f(s01 - u1) + exp2f(s11 - u1));
+        l0 *= ex2(m0 - u0);
+        l1 *= ex2(m1 - u1);
         m0 = n0;
         m1 = n1;
-      }
-      float x0 = fmaxf(z00, z10), x1 = fmaxf(z01, z11);
 #pragma unroll
-      for (int i = 4; i < 32; i <<= 1) {
-        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, i));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, i));
-      }
-      if (__any_sync(0xffffffffu, x0 > M0 || x1 > M1)) {
-        const float N0 = fmaxf(M0, x0), N1 = fmaxf(M1, x1);
-        const float a0 = M0 == -INFINITY ? 0.f : exp2f(M0 - N0);
-        const float a1 = M1 == -INFINITY ? 0.f : exp2f(M1 - N1);
-        M0 = N0;
-        M1 = N1;
-#pragma unroll
-        for (int u = 0; u < KS; ++u) {
-          o[u][0] *= a0;
-          o[u][1] *= a1;
-          o[u][2] *= a0;
-          o[u][3] *= a1;
+        for (int i = 0; i < 2 * MB; ++i) {
+          l0 += ex2(sx[i][0] - u0);
+          l1 += ex2(sx[i][1] - u1);
         }
-      }
-      const float U0 = M0 == -INFINITY ? 0.f : M0, U1 = M1 == -INFINITY ? 0.f : M1;
-      const uint32_t b0 = transpose8x8(pack_f16(exp2f(z00 - U0), exp2f(z01 - U1)));
-      const uint32_t b1 = transpose8x8(pack_f16(exp2f(z10 - U0), exp2f(z11 - U1)));
-      // ---- O^T [D x 8 heads] += V^T P^T; codes of keys outside the unit count 0 ----
-      const int c_lo = 16 * warp + 2 * tig;
-      const uint32_t keep_lo = (valid(c_lo) ? 0xffffu : 0u) | (valid(c_lo + 1) ? 0xffff0000u : 0u);
-      const uint32_t keep_hi =
-          (valid(c_lo + 8) ? 0xffffu : 0u) | (valid(c_lo + 9) ? 0xffff0000u : 0u);
 #pragma unroll
-      for (int u = 0; u < KS; u += 2) {
-        uint32_t r[4], a0, a1, a2, a3;
-        ldsm_x4_t(unit_addr<D>(vbase, ldsm_base, u + ldsm_unit), r);
-        // a word holds two columns of two keys; pair the keys of each column
-        codes_to_f16(__byte_perm(r[0] & keep_lo, 0, 0x3120), a0, a1);
-        codes_to_f16(__byte_perm(r[1] & keep_hi, 0, 0x3120), a2, a3);
-        mma_f16(o[u], a0, a1, a2, a3, b0, b1);
-        codes_to_f16(__byte_perm(r[2] & keep_lo, 0, 0x3120), a0, a1);
-        codes_to_f16(__byte_perm(r[3] & keep_hi, 0, 0x3120), a2, a3);
-        mma_f16(o[u + 1], a0, a1, a2, a3, b0, b1);
+        for (int i = 4; i < 32; i <<= 1) {
+          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, i));
+          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, i));
+        }
+        if (__any_sync(0xffffffffu, x0 > M0 || x1 > M1)) {
+          const float N0 = fmaxf(M0, x0), N1 = fmaxf(M1, x1);
+          const float a0 = M0 == -INFINITY ? 0.f : ex2(M0 - N0);
+          const float a1 = M1 == -INFINITY ? 0.f : ex2(M1 - N1);
+          M0 = N0;
+          M1 = N1;
+#pragma unroll
+          for (int u = 0; u < KS; ++u) {
+            o[u][0] *= a0;
+            o[u][1] *= a1;
+            o[u][2] *= a0;
+            o[u][3] *= a1;
+          }
+        }
+        const float U0 = M0 == -INFINITY ? 0.f : M0, U1 = M1 == -INFINITY ? 0.f : M1;
+        uint32_t pb[2 * MB], keep[2 * MB];
+#pragma unroll
+        for (int i = 0; i < 2 * MB; ++i) {
+          pb[i] = transpose8x8(pack_f16(ex2(sx[i][0] + lv[i] - U0), ex2(sx[i][1] + lv[i] - U1)));
+          keep[i] = 0xffffffffu;
+        }
+        if (!whole) {   // codes of keys outside the unit count 0, whatever they are
+#pragma unroll
+          for (int i = 0; i < 2 * MB; ++i) {
+            const int r = key0 + 2 * tig + 8 * i;
+            keep[i] = (valid(r) ? 0xffffu : 0u) | (valid(r + 1) ? 0xffff0000u : 0u);
+          }
+        }
+        // ---- O^T [D x 8 heads] += V^T P^T ----
+        st = (ent + 1) % Cf::NS;
+        if (!mbar_wait(full + 8 * st, ((ent + 1) / Cf::NS) & 1, abort_flag)) give_up();
+        __syncwarp();
+        base = s0 + st * Cf::TILE_BYTES;
+#pragma unroll
+        for (int u = 0; u < KS; u += 2) {
+#pragma unroll
+          for (int i = 0; i < MB; ++i) {
+            uint32_t r[4], a0, a1, a2, a3;
+            ldsm_x4_t(unit_addr<D>(base, ldsm_base, u + ldsm_unit) + i * ROWS16, r);
+            // a word holds two columns of two keys; pair the keys of each column
+            codes_to_f16(__byte_perm(r[0] & keep[2 * i], 0, 0x3120), a0, a1);
+            codes_to_f16(__byte_perm(r[1] & keep[2 * i + 1], 0, 0x3120), a2, a3);
+            mma_f16(o[u], a0, a1, a2, a3, pb[2 * i], pb[2 * i + 1]);
+            codes_to_f16(__byte_perm(r[2] & keep[2 * i], 0, 0x3120), a0, a1);
+            codes_to_f16(__byte_perm(r[3] & keep[2 * i + 1], 0, 0x3120), a2, a3);
+            mma_f16(o[u + 1], a0, a1, a2, a3, pb[2 * i], pb[2 * i + 1]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + 8 * st);
       }
+      wait_scales();   // a warp without a tile here keeps step too
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty + 8 * st);
+      if (lane == 0) mbar_arrive(emptyS + 8 * ss);
     }
+    tile += w.tb - w.ta;
     if constexpr (!Q_REGS) {
       __syncwarp();
       if (lane == 0) mbar_arrive(emptyQ + 8 * qs);
@@ -1082,12 +1226,12 @@ bool good_heads(int Hq, int Hkv, int D) {
 
 extern "C" {
 
-// Workspace: [kMaxCtas] flags, [kMaxCtas] records of G * D floats (partial outputs),
-// [kMaxCtas] records of G * 3 floats (running maxima and sum).
+// Workspace: [kMaxCtas] records of G * D words (partial outputs), [kMaxCtas] records of
+// G * 3 words (running maxima and sum).
 size_t paged_decode_attn_q8_workspace(int Hq, int Hkv, int D) {
   if (!good_heads(Hq, Hkv, D)) return 0;
   const size_t G = Hq / Hkv;
-  return kMaxCtas * (sizeof(int) + G * (D + 3) * sizeof(float));
+  return kMaxCtas * G * (D + 3) * sizeof(float);
 }
 
 int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e4m3 *v_cache,
@@ -1162,8 +1306,10 @@ int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.flags = static_cast<int *>(workspace);
-  p.o_part = reinterpret_cast<float *>(p.flags + kMaxCtas);
+  // four scales at once where the rows of one copy have as many, 16-byte aligned
+  p.scale_vec = box_rows / scale_block >= 4 && pkv::aligned16(k_scale) && pkv::aligned16(v_scale)
+                    ? 4 : 1;
+  p.o_part = static_cast<uint32_t *>(workspace);
   p.st_part = p.o_part + static_cast<size_t>(kMaxCtas) * p.G * D;
   p.out = reinterpret_cast<__nv_bfloat16 *>(out);
   p.err = err_word;
