@@ -25,8 +25,9 @@
 //     steps of the softmax) and keeps its own online softmax over the whole unit, so
 //     no tile needs a barrier between warps. At a
 //     unit's end it leaves its state in shared memory and goes on; a joining warp
-//     adds the four states (and a cut row's other parts) and writes the output or the
-//     partial. Keys are the M rows of
+//     adds the four states and writes the output or the partial. A part that takes
+//     others in is its CTA's last work: there the consumer warps themselves add
+//     everything up, all loads of the other parts in flight at once. Keys are the M rows of
 //     S^T = K q^T and head-dim is the M rows of O^T = V^T P^T (mma.sync m16n8k16,
 //     fp16 in, fp32 out), the <= 8 query heads of the group are N; P goes from
 //     one product to the other through movmatrix;
@@ -91,8 +92,14 @@ struct Cfg {
   static constexpr int MERGE_SLOT = (kCWarps * kMaxG * kMergeRow + 3 * kCWarps * kMaxG) * 4;
   static constexpr int OFF_MERGE = OFF_SCALE + 4 * kScaleWords * 4;
   static constexpr int OFF_QS = OFF_MERGE + MS * MERGE_SLOT;                    // [2][8] f32
-  static constexpr int OFF_SRC = OFF_QS + 2 * kMaxG * 4;   // weights of parts taken in, [kMaxSources][8]
-  static constexpr int OFF_BAR = OFF_SRC + kMaxSources * kMaxG * 4;
+  // weights of the states added up: the warps' and the parts' taken in
+  static constexpr int OFF_SRC = OFF_QS + 2 * kMaxG * 4;   // [4 + kMaxSources][8] f32
+  static constexpr int OFF_BAR = OFF_SRC + (4 + kMaxSources) * kMaxG * 4;
+  // the warps' states of a part that takes others in, where the ring was:
+  // [4][8][DUMP_ROW] f32, then m, l, M [4][8] each
+  static constexpr int DUMP_ROW = D + 4;
+  static constexpr int DUMP_STATS = kCWarps * kMaxG * DUMP_ROW;
+  static_assert((DUMP_STATS + 3 * kCWarps * kMaxG) * 4 <= NS * TILE_BYTES, "states fit the ring");
   static constexpr int N_BARS = 2 * NS + 8 + 2 * MS;
   static constexpr int OFF_TILE = OFF_BAR + N_BARS * 8;   // [NS] u32: box mask, row offset
   static constexpr int OFF_MISC = OFF_TILE + NS * 4;      // abort flag
@@ -404,12 +411,34 @@ __device__ __forceinline__ bool written(const uint4 &v) {
   return v.x != 0u && v.y != 0u && v.z != 0u && v.w != 0u;
 }
 
-// The joining warp. A unit's result is a sum over states: its four consumer warps',
-// and, for a part that takes others in, theirs. A state has, per head, the maximum m
-// and the sum l of the weights 2^s, the maximum M of s + log2 sv, and the outputs
-// relative to M. Lanes are (state of four, head) for the statistics and (head, four
-// columns) for the outputs. Written as rolled loops: most of it runs once a CTA, and
-// then the fetching of its instructions is what it takes.
+// The parts a part takes in: at level s = 1, 8, 64 the parts part + s .. part + 7 s, if
+// part is a multiple of 8 s and there are as many. Bit q of the mask: source q =
+// 7 level + k - 1; lane q gets its CTA.
+__device__ __forceinline__ uint32_t sources(const Unit &w, int lane, int &cta) {
+  const int level = lane / 7, s = 1 << (3 * min(level, 3)), j = w.part + (lane % 7 + 1) * s;
+  const bool t = level < 3 && w.part % (kFan * s) == 0 && j < w.parts;
+  cta = w.first_cta + (t ? j : 0);
+  return __ballot_sync(0xffffffffu, t);
+}
+__device__ __forceinline__ bool takes_others(const Unit &w) {
+  return w.part % kFan == 0 && w.part + 1 < w.parts;
+}
+// What a sum of outputs relative to M is multiplied by: 1 for a partial, else
+// 2^(M - m) / l (no key of weight, or no key: 0; a NaN stays one).
+__device__ __forceinline__ float last_factor(bool partial, float m, float l, float M) {
+  return partial ? 1.f : l != l ? l : M == -INFINITY || l == 0.f ? 0.f : ex2(M - m) / l;
+}
+__device__ __forceinline__ uint2 pack4_bf16(const float4 &v, float f) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * f, v.w * f);
+  return make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                    *reinterpret_cast<const uint32_t *>(&hi));
+}
+
+// The joining warp: adds up the states of the four consumer warps at the end of every
+// unit that takes no others in. Lanes are (warp, head) for the statistics and (head,
+// four columns) for the outputs. Rolled loops: what runs once or twice a CTA takes the
+// time of fetching its instructions.
 template <int D>
 __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32_t fullQ,
                                            uint32_t emptyQ, uint32_t fullM, uint32_t emptyM,
@@ -420,10 +449,7 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
   constexpr int ROUNDS = D / COLS;
   constexpr int LPH = COLS / 4;            // lanes a head
   constexpr int HPS = 32 / LPH;            // heads a step
-  constexpr int PAIR = ROUNDS == 1 ? 4 / HPS : 2;   // steps at once (four heads, or two)
   const int hs = lane / LPH, col = lane % LPH * 4;
-  const int sh = lane & 7, sk = lane >> 3;
-  float *src_f = reinterpret_cast<float *>(sm + Cf::OFF_SRC);   // [kMaxSources][8]
   int it_q = 0, it_m = 0;
   pkv_wait_prior_grid();
   while (true) {
@@ -436,53 +462,108 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
     if (__any_sync(0xffffffffu, w.b < 0)) return;
     if (lane == 0) mbar_arrive(emptyQ + 8 * qs);
     ++it_q;
-    // The parts this one takes in: at level s = 1, 8, 64 the parts part + s .. part + 7 s,
-    // if part is a multiple of 8 s. Lane q has the CTA of source q = 7 level + k - 1, if
-    // bit q of `takes` is set.
-    int my_cta = 0;
-    uint32_t takes = 0;
-    if (w.parts > 1) {
-      const int level = lane / 7, s = 1 << (3 * level), j = w.part + (lane % 7 + 1) * s;
-      const bool t = level < 3 && w.part % (kFan * s) == 0 && j < w.parts;
-      takes = __ballot_sync(0xffffffffu, t);
-      my_cta = w.first_cta + (t ? j : 0);
+    if (takes_others(w)) continue;
+    const bool partial = w.part > 0;
+    float f = 0.f, last = 0.f, m = 0.f, l = 0.f, M = 0.f;
+#pragma unroll 1
+    for (int r = 0; r < ROUNDS; ++r, ++it_m) {
+      const int ms = it_m % Cf::MS;
+      bool ok = mbar_wait(fullM + 8 * ms, (it_m / Cf::MS) & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+      const float *merge =
+          reinterpret_cast<const float *>(sm + Cf::OFF_MERGE + ms * Cf::MERGE_SLOT);
+      if (r == 0) {
+        const float *a = merge + kCWarps * kMaxG * kMergeRow + lane;
+        const float own_m = a[0], own_l = a[32], own_M = a[64];
+        m = own_m;
+        M = own_M;
+#pragma unroll
+        for (int i = 8; i < 32; i <<= 1) {
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+          M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
+        }
+        l = sum_at(own_l, own_m, m);
+#pragma unroll
+        for (int i = 8; i < 32; i <<= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+        f = own_M == -INFINITY ? 0.f : ex2(own_M - M);
+        last = last_factor(partial, m, l, M);
+      }
+#pragma unroll 1
+      for (int i0 = 0; i0 < p.G; i0 += HPS) {
+        const int h = (i0 + hs) & 7;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < kCWarps; ++j)
+          fma4(acc, __shfl_sync(0xffffffffu, f, 8 * j + h),
+               *reinterpret_cast<const float4 *>(merge + (j * kMaxG + h) * kMergeRow + col));
+        const float fl = __shfl_sync(0xffffffffu, last, h);
+        if (i0 + hs >= p.G || !ok) continue;
+        const int at = r * COLS + col;
+        if (partial)
+          st_words(p.o_part + (static_cast<size_t>(blockIdx.x) * p.G + h) * D + at,
+                   make_uint4(part_word(acc.x), part_word(acc.y), part_word(acc.z),
+                              part_word(acc.w)));
+        else
+          *reinterpret_cast<uint2 *>(
+              p.out + (static_cast<size_t>(w.b) * p.Hq + w.g * p.G + h) * D + at) =
+              pack4_bf16(acc, fl);
+      }
+      if (partial && r == 0 && ok && lane < p.G) {
+        uint32_t *a = p.st_part + (static_cast<size_t>(blockIdx.x) * p.G + lane) * 3;
+        st_word(a, part_word(m));
+        st_word(a + 1, part_word(l));
+        st_word(a + 2, part_word(M));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(emptyM + 8 * ms);
     }
-    const int n_src = 32 - __clz(takes);
-    bool bad = false;
-    // ---- statistics: the unit's own in the merge slot, the sources' in their records ----
-    if (!mbar_wait(fullM + 8 * (it_m % Cf::MS), (it_m / Cf::MS) & 1, abort_flag)) bad = true;
-    const float *own = reinterpret_cast<const float *>(
-                           sm + Cf::OFF_MERGE + it_m % Cf::MS * Cf::MERGE_SLOT) +
-                       kCWarps * kMaxG * kMergeRow + lane;
-    const float own_m = own[0], own_l = own[32], own_M = own[64];
-    float m = own_m, l = own_l, M = own_M;   // this lane's states
+  }
+}
+
+// The end of a part that takes others in, by the consumer warps, whose states lie where
+// the ring was: warp 0 gathers the statistics and weighs the states, then every thread
+// adds up four columns of a head at a time.
+template <int D>
+__device__ __forceinline__ void join_parts(const Problem &p, uint8_t *sm, const Unit &w,
+                                           volatile int *abort_flag, int warp, int lane) {
+  using Cf = Cfg<D>;
+  const int tid = warp * 32 + lane;
+  const float *dump = reinterpret_cast<const float *>(sm);
+  float *weight = reinterpret_cast<float *>(sm + Cf::OFF_SRC);   // [4 + kMaxSources][8]
+  int my_cta;
+  const uint32_t takes = sources(w, lane, my_cta);
+  const int n_src = 32 - __clz(takes);
+  const bool partial = w.part > 0;
+  bool bad = false;
+  if (warp == 0) {
+    const int sh = lane & 7, sk = lane >> 3;
+    const float *a = dump + Cf::DUMP_STATS + lane;
+    const float own_M = a[64];
+    float m = a[0], l = a[32], M = own_M;   // of this lane's states
 #pragma unroll 1
     for (int k0 = 0; k0 < n_src; k0 += 4) {
       const int k = k0 + sk;
       const int cta = __shfl_sync(0xffffffffu, my_cta, k);
       const bool mine = (takes >> k & 1u) && sh < p.G;
-      uint32_t *a = p.st_part + (static_cast<size_t>(cta) * p.G + sh) * 3;
+      uint32_t *s = p.st_part + (static_cast<size_t>(cta) * p.G + sh) * 3;
       uint32_t x0 = 0, x1 = 0, x2 = 0;
-      for (int i = 0;; ++i) {
-        if (mine) {
-          x0 = ld_word(a);
-          x1 = ld_word(a + 1);
-          x2 = ld_word(a + 2);
-        }
-        const bool there = !mine || (x0 != 0u && x1 != 0u && x2 != 0u);
-        if (__all_sync(0xffffffffu, there)) break;
-        if (i >= kPollLimit || __any_sync(0xffffffffu, *abort_flag)) {
+      for (int i = 0; mine; ++i) {
+        x0 = ld_word(s);
+        x1 = ld_word(s + 1);
+        x2 = ld_word(s + 2);
+        if (x0 != 0u && x1 != 0u && x2 != 0u) break;
+        if (i >= kPollLimit || *abort_flag) {
           bad = true;
           break;
         }
       }
       if (mine) {
-        st_word(a, 0u);
-        st_word(a + 1, 0u);
-        st_word(a + 2, 0u);
+        st_word(s, 0u);
+        st_word(s + 1, 0u);
+        st_word(s + 2, 0u);
       }
       const float xm = mine ? part_value(x0) : -INFINITY, xM = mine ? part_value(x2) : -INFINITY;
-      src_f[k * kMaxG + sh] = xM;
+      weight[(4 + k) * kMaxG + sh] = xM;
       const float mn = fmaxf(m, xm);
       l = sum_at(l, m, mn) + sum_at(mine ? part_value(x1) : 0.f, xm, mn);
       m = mn;
@@ -495,115 +576,98 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
       M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
     }
     l = sum_at(l, lane_m, m);
-    const float own_f = own_M == -INFINITY ? 0.f : ex2(own_M - M);
-#pragma unroll 1
-    for (int k = sk; k < n_src; k += 4) {   // each lane the words it wrote
-      const float x = src_f[k * kMaxG + sh];
-      src_f[k * kMaxG + sh] = x == -INFINITY ? 0.f : ex2(x - M);
-    }
 #pragma unroll
     for (int i = 8; i < 32; i <<= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
-    // what the sum is multiplied by: 1 for a partial; no key of weight, or none: 0
-    const float last = w.part > 0 ? 1.f
-                       : l != l   ? l
-                       : M == -INFINITY || l == 0.f ? 0.f
-                                                    : ex2(M - m) / l;
-    __syncwarp();
-    // ---- outputs ----
+    const float last = last_factor(partial, m, l, M);
+    weight[lane] = own_M == -INFINITY ? 0.f : last * ex2(own_M - M);
 #pragma unroll 1
-    for (int r = 0; r < ROUNDS; ++r, ++it_m) {
-      const int ms = it_m % Cf::MS;
-      if (r > 0 && !mbar_wait(fullM + 8 * ms, (it_m / Cf::MS) & 1, abort_flag)) bad = true;
-      const float *merge =
-          reinterpret_cast<const float *>(sm + Cf::OFF_MERGE + ms * Cf::MERGE_SLOT) + col;
+    for (int k = 4 + sk; k < 4 + n_src; k += 4) {   // each lane the words it wrote
+      const float x = weight[k * kMaxG + sh];
+      weight[k * kMaxG + sh] = x == -INFINITY ? 0.f : last * ex2(x - M);
+    }
+    if (partial && !bad && lane < p.G) {
+      uint32_t *s = p.st_part + (static_cast<size_t>(blockIdx.x) * p.G + lane) * 3;
+      st_word(s, part_word(m));
+      st_word(s + 1, part_word(l));
+      st_word(s + 2, part_word(M));
+    }
+  }
+  bad = consumer_sync_or(bad || *abort_flag);
+  constexpr int IB = D <= 128 ? 2 : 4;   // places at once, of four parts each
+  const int places = p.G * D / 4;
+  __nv_bfloat16 *out = p.out + (static_cast<size_t>(w.b) * p.Hq + w.g * p.G) * D;
 #pragma unroll 1
-      for (int i0 = 0; i0 < p.G; i0 += PAIR * HPS) {
-        float4 acc[PAIR];
+  for (int i0 = tid; i0 - tid < places && !bad; i0 += kCThreads * IB) {
+    float4 acc[IB];
+    int h[IB];
 #pragma unroll
-        for (int i = 0; i < PAIR; ++i) {
-          const int h = (i0 + i * HPS + hs) & 7;
-          acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < IB; ++i) {
+      const int at = min(i0 + i * kCThreads, places - 1);
+      h[i] = at / (D / 4);
+      acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int j = 0; j < kCWarps; ++j)
-            fma4(acc[i], __shfl_sync(0xffffffffu, own_f, 8 * j + h),
-                 *reinterpret_cast<const float4 *>(merge + (j * kMaxG + h) * kMergeRow));
-        }
+      for (int j = 0; j < kCWarps; ++j)
+        fma4(acc[i], weight[j * kMaxG + h[i]],
+             *reinterpret_cast<const float4 *>(dump + (j * kMaxG + h[i]) * Cf::DUMP_ROW +
+                                               at % (D / 4) * 4));
+    }
 #pragma unroll 1
-        for (int k0 = 0; k0 < n_src && !bad; k0 += 4) {
-          uint32_t *a[4];
+    for (int k0 = 0; k0 < n_src; k0 += 4) {
+      uint32_t *a[4];
+      uint4 v[4][IB];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            a[j] = p.o_part + (static_cast<size_t>(__shfl_sync(0xffffffffu, my_cta, k0 + j)) * p.G +
-                               i0 + hs) * D + r * COLS + col;
-          uint4 v[4][PAIR];
+      for (int j = 0; j < 4; ++j) {
+        const int cta = __shfl_sync(0xffffffffu, my_cta, k0 + j);
+        a[j] = p.o_part + static_cast<size_t>(cta) * p.G * D + 4 * i0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < IB; ++i)
+          v[j][i] = (takes >> (k0 + j) & 1u) && i0 + i * kCThreads < places
+                        ? make_uint4(0u, 0u, 0u, 0u)
+                        : make_uint4(~0u, ~0u, ~0u, ~0u);
+      }
+      for (int n = 0;; ++n) {
+        bool there = true;
 #pragma unroll
-            for (int i = 0; i < PAIR; ++i)
-              v[j][i] = make_uint4(0u, 0u, 0u, 0u);
-          for (int n = 0;; ++n) {
-            bool there = true;
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+          for (int i = 0; i < IB; ++i)
+            if (!written(v[j][i])) v[j][i] = ld_words(a[j] + 4 * i * kCThreads);
 #pragma unroll
-              for (int i = 0; i < PAIR; ++i)
-                if ((takes >> (k0 + j) & 1u) && i0 + i * HPS + hs < p.G && !written(v[j][i]))
-                  v[j][i] = ld_words(a[j] + i * HPS * D);
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int i = 0; i < PAIR; ++i)
-                there = there && (!(takes >> (k0 + j) & 1u) || i0 + i * HPS + hs >= p.G ||
-                                  written(v[j][i]));
-            if (__all_sync(0xffffffffu, there)) break;
-            if (n >= kPollLimit || __any_sync(0xffffffffu, *abort_flag)) {
-              bad = true;
-              break;
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < PAIR; ++i) {
-              const int h = i0 + i * HPS + hs;
-              if ((takes >> (k0 + j) & 1u) && h < p.G) {
-                st_words(a[j] + i * HPS * D, make_uint4(0u, 0u, 0u, 0u));
-                fma4(acc[i], src_f[(k0 + j) * kMaxG + h],
-                     make_float4(part_value(v[j][i].x), part_value(v[j][i].y),
-                                 part_value(v[j][i].z), part_value(v[j][i].w)));
-              }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < PAIR; ++i) {
-          const int h = i0 + i * HPS + hs;
-          const float f = __shfl_sync(0xffffffffu, last, h & 7);
-          if (h >= p.G || bad || *abort_flag) continue;
-          const float4 &o = acc[i];
-          if (w.part > 0) {
-            st_words(p.o_part + (static_cast<size_t>(blockIdx.x) * p.G + h) * D + r * COLS + col,
-                     make_uint4(part_word(o.x), part_word(o.y), part_word(o.z), part_word(o.w)));
-          } else {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * f, o.y * f);
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * f, o.w * f);
-            *reinterpret_cast<uint2 *>(
-                p.out + (static_cast<size_t>(w.b) * p.Hq + w.g * p.G + h) * D + r * COLS + col) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
-                           *reinterpret_cast<const uint32_t *>(&hi));
-          }
+          for (int i = 0; i < IB; ++i) there = there && written(v[j][i]);
+        if (there) break;
+        if (n >= kPollLimit || *abort_flag) {
+          bad = true;
+          break;
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(emptyM + 8 * ms);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < IB; ++i)
+          if ((takes >> (k0 + j) & 1u) && i0 + i * kCThreads < places) {
+            st_words(a[j] + 4 * i * kCThreads, make_uint4(0u, 0u, 0u, 0u));
+            fma4(acc[i], weight[(4 + k0 + j) * kMaxG + h[i]],
+                 make_float4(part_value(v[j][i].x), part_value(v[j][i].y),
+                             part_value(v[j][i].z), part_value(v[j][i].w)));
+          }
     }
-    if (w.part > 0 && !bad && !*abort_flag && lane < p.G) {
-      uint32_t *a = p.st_part + (static_cast<size_t>(blockIdx.x) * p.G + lane) * 3;
-      st_word(a, part_word(m));
-      st_word(a + 1, part_word(l));
-      st_word(a + 2, part_word(M));
+    bad = __any_sync(0xffffffffu, bad);
+#pragma unroll
+    for (int i = 0; i < IB; ++i) {
+      const int at = i0 + i * kCThreads;
+      if (at >= places || bad) continue;
+      const float4 &o = acc[i];
+      if (partial)
+        st_words(p.o_part + static_cast<size_t>(blockIdx.x) * p.G * D + 4 * at,
+                 make_uint4(part_word(o.x), part_word(o.y), part_word(o.z), part_word(o.w)));
+      else
+        *reinterpret_cast<uint2 *>(out + 4 * at) = pack4_bf16(o, 1.f);
     }
-    if (bad && lane == 0 && p.err) atomicOr(p.err, PKV_ERR_TIMEOUT);
   }
+  if (bad && lane == 0 && p.err) atomicOr(p.err, PKV_ERR_TIMEOUT);
 }
 
 // ------------------------------------------------------------- kernel ----
@@ -1126,6 +1190,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     for (int i = 4; i < 32; i <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, i);
       l1 += __shfl_xor_sync(0xffffffffu, l1, i);
+    }
+    if (takes_others(w)) {   // the CTA's last work: the ring is free once all are here
+      (void)consumer_sync_or(false);
+      float *dump = reinterpret_cast<float *>(sm);
+#pragma unroll
+      for (int u = 0; u < KS; ++u) {
+        float *d = dump + (warp * kMaxG + h0) * Cf::DUMP_ROW + 16 * u + 2 * gid;
+        *reinterpret_cast<float2 *>(d) = make_float2(o[u][0], o[u][2]);
+        *reinterpret_cast<float2 *>(d + Cf::DUMP_ROW) = make_float2(o[u][1], o[u][3]);
+      }
+      if (gid == 0) {
+        float *st = dump + Cf::DUMP_STATS + warp * kMaxG + h0;
+        *reinterpret_cast<float2 *>(st) = make_float2(n0, n1);
+        *reinterpret_cast<float2 *>(st + 32) = make_float2(l0, l1);
+        *reinterpret_cast<float2 *>(st + 64) = make_float2(M0, M1);
+      }
+      (void)consumer_sync_or(false);
+      join_parts<D>(p, sm, w, abort_flag, warp, lane);
+      continue;
     }
     constexpr int COLS = D < kMergeCols ? D : kMergeCols;
 #pragma unroll
