@@ -4,7 +4,7 @@
 //   s_j = scale * sk_j * (q . ck_j),  out = sum_j softmax(s)_j sv_j cv_j
 //
 // Bound by reading the codes and scales of every key once. Design (GB300):
-//   * work: the 64-key tiles of every (row, kv head), plus one position for each
+//   * work: the 64-key tiles of every (row, kv head), plus START positions for each
 //     start of a (row, head), laid on one line from the actual lengths; every
 //     persistent CTA takes an equal share of it. A (row, head) that straddles
 //     CTAs is cut into parts; a CTA has at most one part that is not its (row,
@@ -71,6 +71,10 @@ constexpr int kMergeRow = kMergeCols + 4;   // padded: conflict-free 8-byte stor
 template <int D>
 struct Cfg {
   static constexpr int CTAS_PER_SM = D <= 256 ? 2 : 1;
+  // What starting a (row, head) costs, in tiles (a unit's state, its query and the part
+  // of its last tile not used). Rollout batch, D = 128: 1 21.6 us, 2 19.9, 3 19.7, 4 20.1;
+  // D = 512: 25.9, 24.8, 25.9, 26.0.
+  static constexpr int START = D <= 256 ? 3 : 2;
   static constexpr int MB = D <= 128 ? 2 : 1;      // 16-key blocks of a tile a warp owns
   static constexpr int TEAM = kT / 16 / MB;        // warps that share a tile
   static constexpr int TEAMS = kCWarps / TEAM;
@@ -105,7 +109,8 @@ struct Cfg {
   static constexpr int OFF_MISC = OFF_TILE + NS * 4;      // abort flag
   static constexpr int OFF_DESC = (OFF_MISC + 8 + 15) & ~15;       // Unit [2]
   static constexpr int OFF_LEN = OFF_DESC + 2 * 48;                // int [kMaxRows]
-  static constexpr int OFF_PRE = OFF_LEN + kMaxRows * 4;           // int [kMaxRows + 1]
+  static constexpr int OFF_SLOT = OFF_LEN + kMaxRows * 4;          // int [kMaxRows]
+  static constexpr int OFF_PRE = OFF_SLOT + kMaxRows * 4;          // int [kMaxRows + 1]
   static constexpr int SMEM = OFF_PRE + (kMaxRows + 1) * 4 + 1024;  // + alignment
 };
 // shared memory per SM on sm_103a: 228 KB, of which 1 KB is reserved per CTA
@@ -181,6 +186,13 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *tm) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
+}
+// All warps meet once the mbarriers are set up.
+__device__ __forceinline__ void setup_sync() {
+  asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
 }
 // A barrier of the consumer threads that returns the OR of `v` over them.
 __device__ __forceinline__ bool consumer_sync_or(bool v) {
@@ -298,12 +310,18 @@ __device__ __forceinline__ int2 row_read(const Problem &p, int b, int &bits) {
   return make_int2(slot, L);
 }
 
-// The line of work: a (row, head) with n > 0 tiles takes n + 1 positions, its start
-// and its tiles; pre[b] is the prefix sum of n + 1 over rows, (b, g)'s positions
-// begin at Hkv * pre[b] + g * (n + 1). The `total` positions are shared by
+// The line of work: a (row, head) with n > 0 tiles takes START + n positions, its start
+// and its tiles; pre[b] is the prefix sum of that over rows, (b, g)'s positions begin
+// at Hkv * pre[b] + g * (START + n). The `total` positions are shared by
 // min(CTAs, total) of them: the first `more` own each + 1, the others `each`, so every
 // share has a position and every CTA between a (row, head)'s first and last has tiles
 // of it.
+// x / d for a quotient below 2^20: the approximate one is at most one off.
+__device__ __forceinline__ uint32_t small_quotient(uint32_t x, uint32_t d) {
+  const uint32_t q = static_cast<uint32_t>(__fdividef(__uint2float_rz(x), __uint2float_rz(d)));
+  const int r = static_cast<int>(x - q * d);
+  return r < 0 ? q - 1 : r >= static_cast<int>(d) ? q + 1 : q;
+}
 struct Line {
   uint32_t each, more;
   __device__ __forceinline__ int bound(uint32_t c) const {
@@ -311,7 +329,8 @@ struct Line {
   }
   __device__ __forceinline__ int owner(uint32_t x) const {
     const uint32_t wide = more * (each + 1);
-    return static_cast<int>(x < wide ? x / (each + 1) : more + (x - wide) / each);
+    return static_cast<int>(x < wide ? small_quotient(x, each + 1)
+                                     : more + small_quotient(x - wide, each));
   }
 };
 
@@ -322,9 +341,13 @@ struct Unit {
 };
 static_assert(sizeof(Unit) <= 48, "unit descriptor slot");
 
-// The next unit from position x on (advanced past it); false at the share's end.
+// The next unit from position x on (advanced past it); false at the share's end. Which
+// part of its (row, head) it is comes later (which_part): `first_cta` and `parts` hold
+// the (row, head)'s first position and width until then, `part` whether its first
+// (bit 0) and last tile (bit 1) are this unit's.
 // The whole converged producer warp calls it with uniform arguments.
-__device__ __forceinline__ bool next_unit(const Problem &p, const Line &line, const int *lens,
+template <int START>
+__device__ __forceinline__ bool next_unit(const Problem &p, const int *slots, const int *lens,
                                           const int *pre, int end, int &x, Unit &w, int lane) {
   while (x < end) {
     int b = -1;   // the last row whose positions begin at or before x
@@ -336,15 +359,13 @@ __device__ __forceinline__ bool next_unit(const Problem &p, const Line &line, co
     }
     const int width = pre[b + 1] - pre[b];
     const int within = x - p.Hkv * pre[b];
-    const int g = static_cast<uint32_t>(within) / static_cast<uint32_t>(width);
+    const int g = static_cast<int>(small_quotient(within, width));
     const int r = within - g * width;
     const int n = min(end - x, width - r);
     x += n;
-    const int t0 = max(r, 1) - 1, t1 = r + n - 1;   // tiles of the row: [t0, t1)
-    if (t1 <= t0) continue;                          // only the start's position
-    // a row with tiles has a valid slot
-    const RowInfo ri = row_keys(p, p.batch_idx ? __ldg(p.batch_idx + b) : b, lens[b]);
-    const int start = p.Hkv * pre[b] + g * width;
+    const int t0 = max(r, START) - START, t1 = r + n - START;   // tiles of the row: [t0, t1)
+    if (t1 <= t0) continue;                          // only positions of the start
+    const RowInfo ri = row_keys(p, slots[b], lens[b]);
     w.b = b;
     w.g = g;
     w.slot = ri.slot;
@@ -352,12 +373,19 @@ __device__ __forceinline__ bool next_unit(const Problem &p, const Line &line, co
     w.tb = ri.t_first + t1;
     w.k0 = max(ri.lo, w.ta * kT);
     w.k1 = min(ri.L, w.tb * kT);
-    w.first_cta = line.owner(start + 1);
-    w.parts = line.owner(start + width - 1) - w.first_cta + 1;
-    w.part = static_cast<int>(blockIdx.x) - w.first_cta;
+    w.first_cta = p.Hkv * pre[b] + g * width;
+    w.parts = width;
+    w.part = (r <= START ? 1 : 0) | (r + n == width ? 2 : 0);
     return true;
   }
   return false;
+}
+template <int START>
+__device__ __forceinline__ void which_part(const Line &line, Unit &w) {
+  const int me = static_cast<int>(blockIdx.x), start = w.first_cta, last = start + w.parts - 1;
+  w.first_cta = w.part & 1 ? me : line.owner(start + START);
+  w.parts = (w.part & 2 ? me : line.owner(last)) - w.first_cta + 1;
+  w.part = me - w.first_cta;
 }
 
 // Exponent of the largest magnitude of a pair of bf16 halves' maxima.
@@ -535,11 +563,29 @@ __device__ __forceinline__ void join_parts(const Problem &p, uint8_t *sm, const 
   const int n_src = 32 - __clz(takes);
   const bool partial = w.part > 0;
   bool bad = false;
+  constexpr int IB = D <= 128 ? 2 : 4;   // places (four columns of a head) at once, of four parts
+  const int places = p.G * D / 4;
+  uint32_t *a[4];
+  uint4 v[4][IB];
+  // sources k0 .. k0 + 3 at places i0 + i * kCThreads: what there is to wait for
+  auto start_loads = [&](int i0, int k0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int cta = __shfl_sync(0xffffffffu, my_cta, k0 + j);
+      a[j] = p.o_part + static_cast<size_t>(cta) * p.G * D + 4 * i0;
+#pragma unroll
+      for (int i = 0; i < IB; ++i)
+        v[j][i] = (takes >> (k0 + j) & 1u) && i0 + i * kCThreads < places
+                      ? ld_words(a[j] + 4 * i * kCThreads)
+                      : make_uint4(~0u, ~0u, ~0u, ~0u);
+    }
+  };
+  start_loads(tid, 0);   // on their way while the statistics come in
   if (warp == 0) {
     const int sh = lane & 7, sk = lane >> 3;
-    const float *a = dump + Cf::DUMP_STATS + lane;
-    const float own_M = a[64];
-    float m = a[0], l = a[32], M = own_M;   // of this lane's states
+    const float *own = dump + Cf::DUMP_STATS + lane;
+    const float own_M = own[64];
+    float m = own[0], l = own[32], M = own_M;   // of this lane's states
 #pragma unroll 1
     for (int k0 = 0; k0 < n_src; k0 += 4) {
       const int k = k0 + sk;
@@ -593,8 +639,6 @@ __device__ __forceinline__ void join_parts(const Problem &p, uint8_t *sm, const 
     }
   }
   bad = consumer_sync_or(bad || *abort_flag);
-  constexpr int IB = D <= 128 ? 2 : 4;   // places at once, of four parts each
-  const int places = p.G * D / 4;
   __nv_bfloat16 *out = p.out + (static_cast<size_t>(w.b) * p.Hq + w.g * p.G) * D;
 #pragma unroll 1
   for (int i0 = tid; i0 - tid < places && !bad; i0 += kCThreads * IB) {
@@ -613,25 +657,9 @@ __device__ __forceinline__ void join_parts(const Problem &p, uint8_t *sm, const 
     }
 #pragma unroll 1
     for (int k0 = 0; k0 < n_src; k0 += 4) {
-      uint32_t *a[4];
-      uint4 v[4][IB];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int cta = __shfl_sync(0xffffffffu, my_cta, k0 + j);
-        a[j] = p.o_part + static_cast<size_t>(cta) * p.G * D + 4 * i0;
-#pragma unroll
-        for (int i = 0; i < IB; ++i)
-          v[j][i] = (takes >> (k0 + j) & 1u) && i0 + i * kCThreads < places
-                        ? make_uint4(0u, 0u, 0u, 0u)
-                        : make_uint4(~0u, ~0u, ~0u, ~0u);
-      }
+      if (i0 != tid || k0 != 0) start_loads(i0, k0);
       for (int n = 0;; ++n) {
         bool there = true;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < IB; ++i)
-            if (!written(v[j][i])) v[j][i] = ld_words(a[j] + 4 * i * kCThreads);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -641,6 +669,11 @@ __device__ __forceinline__ void join_parts(const Problem &p, uint8_t *sm, const 
           bad = true;
           break;
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < IB; ++i)
+            if (!written(v[j][i])) v[j][i] = ld_words(a[j] + 4 * i * kCThreads);
       }
       __syncwarp();
 #pragma unroll
@@ -688,61 +721,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OFF_MISC);
   Unit *udesc = reinterpret_cast<Unit *>(sm + Cf::OFF_DESC);
   int *lens = reinterpret_cast<int *>(sm + Cf::OFF_LEN);
+  int *slots = reinterpret_cast<int *>(sm + Cf::OFF_SLOT);
   int *pre = reinterpret_cast<int *>(sm + Cf::OFF_PRE);
-
-  // ---- set-up, before the dependency wait: barriers, row cache, prefix sums.
-  // It reads only seq_lens and batch_idx (the producer also the table), which no
-  // kernel that may still run writes (the header's rule).
-  if (tid == 0) {
-    for (int i = 0; i < Cf::NS; ++i) {
-      mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, Cf::TEAM);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(fullS + 8 * i, 32);
-      mbar_init(emptyS + 8 * i, kCWarps);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(fullQ + 8 * i, 1);
-      mbar_init(emptyQ + 8 * i, kCWarps + 1);   // the joining warp reads the unit too
-    }
-    for (int i = 0; i < Cf::MS; ++i) {
-      mbar_init(fullM + 8 * i, kCWarps);
-      mbar_init(emptyM + 8 * i, 1);
-    }
-    *abort_flag = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    fence_proxy_async();
-  }
-  int row_bits = 0;
-  for (int b = tid; tid < kCThreads && b < p.B; b += kCThreads) {
-    int bits;
-    const int2 rc = row_read(p, b, bits);
-    row_bits |= bits;
-    const RowInfo r = row_keys(p, rc.x, rc.y);
-    lens[b] = rc.y;
-    pre[b + 1] = r.n_tiles > 0 ? r.n_tiles + 1 : 0;
-  }
-  __syncthreads();
-  if (warp == 0) {   // inclusive scan of pre[1 .. B]
-    int carry = 0;
-#pragma unroll 1
-    for (int base = 0; base < p.B; base += 32) {
-      const int i = base + lane;
-      int v = i < p.B ? pre[i + 1] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += t;
-      }
-      if (i < p.B) pre[i + 1] = v + carry;
-      carry += __shfl_sync(0xffffffffu, v, 31);
-    }
-    if (lane == 0) pre[0] = 0;
-  }
-  __syncthreads();
-  const uint32_t total = p.Hkv * pre[p.B], ctas = min(gridDim.x, max(total, 1u));
-  const Line line = {total / ctas, total % ctas};
 
   const int ps = 1 << p.log2_ps;
   const int log2_box = min(p.log2_ps, 6);
@@ -754,6 +734,42 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
 
   if (warp == kCWarps) {
     // ======================== producer (one warp) ========================
+    // Set-up, before the dependency wait: row cache, prefix sums, the first unit and
+    // its pages. It reads only seq_lens, batch_idx and the table, which no kernel that
+    // may still run writes (the header's rule).
+    int row_bits = 0, carry = 0;
+#pragma unroll 1
+    for (int base = 0; base < p.B; base += 64) {
+      int2 rc[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int b = base + 32 * i + lane;
+        int bits = 0;
+        rc[i] = b < p.B ? row_read(p, b, bits) : make_int2(0, 0);
+        row_bits |= bits;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int b = base + 32 * i + lane;
+        const int n = row_keys(p, rc[i].x, rc[i].y).n_tiles;
+        int v = n > 0 ? Cf::START + n : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += t;
+        }
+        if (b < p.B) {
+          slots[b] = rc[i].x;
+          lens[b] = rc[i].y;
+          pre[b + 1] = carry + v;
+        }
+        carry += __shfl_sync(0xffffffffu, v, 31);
+      }
+    }
+    if (lane == 0) pre[0] = 0;
+    __syncwarp();
+    const uint32_t total = p.Hkv * carry, ctas = min(gridDim.x, max(total, 1u));
+    const Line line = {total / ctas, total % ctas};
     // Lane j looks up box j of a unit (a page's segment of one tile). box_page only
     // issues the table load; box_row checks the entry when it is used, so a
     // look-ahead load never stalls the warp.
@@ -785,9 +801,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     Unit w, wn;
     int it = 0, it_q = 0, it_s = 0;
     bool ok = true;
-    bool have = next_unit(p, line, lens, pre, end, x, w, lane);
+    bool have = next_unit<Cf::START>(p, slots, lens, pre, end, x, w, lane);
     int page_first = have ? box_page(w, lane) : -1;
+    if (have) which_part<Cf::START>(line, w);
+    setup_sync();
     pkv_wait_prior_grid();
+    if (blockIdx.x == 0 && row_bits && p.err) atomicOr(p.err, row_bits);
     while (ok && have) {
       bool have_next = false, looked_ahead = false;
       int page_next = -1;
@@ -851,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
             ++it;
           }
           if (!ok) break;
-          if (tt == 0) {   // the scales of all tiles here, once the first tile is moving
+          if (tt == 0) {   // the scales of all tiles here
             const int ss = it_s & 1;
             ok = mbar_wait(emptyS + 8 * ss, ((it_s >> 1) & 1) ^ 1, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
@@ -879,8 +898,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
           }
           if (!looked_ahead) {   // the next unit's lookups, once this one is moving
             looked_ahead = true;
-            have_next = next_unit(p, line, lens, pre, end, x, wn, lane);
+            have_next = next_unit<Cf::START>(p, slots, lens, pre, end, x, wn, lane);
             page_next = have_next ? box_page(wn, lane) : -1;
+            if (have_next) which_part<Cf::START>(line, wn);
           }
         }
       }
@@ -915,17 +935,40 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     return;
   }
 
-  if (warp == kCWarps + 1) {
+  if (warp == kCWarps + 1) {   // a lane sets up an mbarrier
+    for (int i = lane; i < Cf::N_BARS; i += 32) {
+      constexpr int Q0 = 2 * Cf::NS, M0 = Q0 + 4, S0 = M0 + 2 * Cf::MS;
+      const int count = i < Cf::NS        ? 1              // full
+                        : i < Q0          ? Cf::TEAM       // empty
+                        : i < Q0 + 2      ? 1              // fullQ
+                        : i < M0          ? kCWarps + 1    // emptyQ: the joining warp reads too
+                        : i < M0 + Cf::MS ? kCWarps        // fullM
+                        : i < S0          ? 1              // emptyM
+                        : i < S0 + 2      ? 32             // fullS
+                                          : kCWarps;       // emptyS
+      mbar_init(full + 8 * i, count);
+    }
+    if (lane == 0) {
+      *abort_flag = 0;
+      prefetch_map(&tmK);
+      prefetch_map(&tmV);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async();
+    __syncwarp();
+    setup_sync();
     join_units<D>(p, sm, fullQ, emptyQ, fullM, emptyM, udesc, abort_flag, lane);
     return;
   }
 
   // ============================== consumers ==============================
+  setup_sync();
   pkv_wait_prior_grid();
   pkv_allow_next_grid();
-  if (blockIdx.x == 0 && row_bits && p.err) atomicOr(p.err, row_bits);
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {   // rows without keys: zeros
-    if (pre[b + 1] != pre[b]) continue;
+    int bits;
+    const int2 rc = row_read(p, b, bits);
+    if (row_keys(p, rc.x, rc.y).n_tiles > 0) continue;
     uint4 *o = reinterpret_cast<uint4 *>(p.out + static_cast<size_t>(b) * p.Hq * D);
     for (int i = tid; i < p.Hq * D / 8; i += kCThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
   }
@@ -1350,7 +1393,7 @@ int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e
       !pkv::aligned16(v_cache))
     return pkv::fail(PKV_E_BAD_ARG, "%s: tensors must be 16-byte aligned", fn);
   {
-    const long long row_tiles = (1LL * max_pages_per_seq * page_size + kT - 1) / kT + 2;
+    const long long row_tiles = (1LL * max_pages_per_seq * page_size + kT - 1) / kT + 1 + Cfg<64>::START;
     if (1LL * B * Hkv * row_tiles >= (1LL << 31))
       return pkv::fail(PKV_E_BAD_ARG, "%s: B * Hkv * tiles per row too large", fn);
   }
