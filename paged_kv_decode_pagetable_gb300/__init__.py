@@ -166,9 +166,15 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# the current stream's handle without building a torch.cuda.Stream (about 4 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        if torch.cuda.is_available() and torch.cuda.is_initialized():
+        if torch.cuda.is_initialized():
+            if _raw_stream is not None:
+                return _raw_stream(torch.cuda.current_device())
             return torch.cuda.current_stream().cuda_stream
         return None
     if isinstance(stream, int):
@@ -188,6 +194,14 @@ def _i32(t, name):
         if t.dtype != torch.int32 or not t.is_contiguous():
             raise BadArgError(f"{name} must be a contiguous int32 tensor")
     return t
+
+
+def _on_device(*tensors) -> None:
+    """Refuses tensors that are not on the current CUDA device (None passes)."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    for t in tensors:
+        if t is not None and type(t) is not int and t.get_device() != dev:
+            raise BadArgError("every tensor must be on the current CUDA device")
 
 
 # --------------------------------------------------------------------------
@@ -406,24 +420,55 @@ def kv_append_prefill(k, v, batch_idx, input_pos, dev_table, n_slots, max_pages_
         _ptr(err_word), _stream(stream)), "kv_append_prefill")
 
 
+_E4M3 = torch.float8_e4m3fn
+
+
 def _q8_cache(k_cache, v_cache, k_scale, v_scale, n_rows: int) -> int:
     """Checks an 8-bit cache's tensors; returns the tokens that share a scale."""
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype != torch.float8_e4m3fn or not t.is_contiguous() or t.dim() != 3:
+        if t.dtype is not _E4M3 or not t.is_contiguous() or t.dim() != 3:
             raise BadArgError(f"{name} must be a contiguous float8_e4m3fn tensor "
                               "[Hkv][n_pages * page_size][D]")
     for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t.dtype != torch.float32 or not t.is_contiguous() or t.dim() != 2:
+        if t.dtype is not torch.float32 or not t.is_contiguous() or t.dim() != 2:
             raise BadArgError(f"{name} must be a contiguous float32 tensor "
                               "[Hkv][n_pages * page_size / scale_block]")
-    if v_cache.shape != k_cache.shape or k_cache.shape[1] != n_rows:
+    shape, scales = k_cache.shape, k_scale.shape
+    if v_cache.shape != shape or shape[1] != n_rows:
         raise BadArgError("k_cache and v_cache must both hold n_pages * page_size rows")
-    n = k_scale.shape[1]
-    if v_scale.shape != k_scale.shape or k_scale.shape[0] != k_cache.shape[0] or n < 1 \
-            or n_rows % n:
+    n = scales[1]
+    if v_scale.shape != scales or scales[0] != shape[0] or n < 1 or n_rows % n:
         raise BadArgError("k_scale and v_scale must both be [Hkv][n_pages * page_size / "
                           "scale_block]")
     return n_rows // n
+
+
+def _append_q8(name, head_major, k, v, batch_idx, input_pos, dev_table, n_slots,
+               max_pages_per_seq, page_size, n_pages, k_cache, v_cache, k_scale, v_scale,
+               err_word, stream) -> None:
+    _bf16(k, "k"), _bf16(v, "v")
+    _i32(batch_idx, "batch_idx"), _i32(input_pos, "input_pos"), _i32(dev_table, "dev_table")
+    block = _q8_cache(k_cache, v_cache, k_scale, v_scale, n_pages * page_size)
+    if k.dim() != 3 or v.shape != k.shape:
+        raise BadArgError(f"{name}: k and v must have one shape of three dimensions")
+    if head_major:
+        Hkv, N, D = k.shape
+    else:
+        N, Hkv, D = k.shape
+    if Hkv != k_cache.shape[0] or D != k_cache.shape[2]:
+        raise BadArgError(f"{name}: k, v and the caches differ in heads or head dim")
+    if input_pos is None or input_pos.numel() < N or (
+            batch_idx is not None and batch_idx.numel() < N):
+        raise BadArgError(f"{name}: batch_idx and input_pos must hold a value for every token")
+    if dev_table is None or dev_table.numel() < n_slots * max_pages_per_seq:
+        raise BadArgError(f"{name}: dev_table must be [n_slots][max_pages_per_seq]")
+    _on_device(k, v, batch_idx, input_pos, dev_table, k_cache, v_cache, k_scale, v_scale, err_word)
+    lib = load_library()
+    fn = lib.kv_append_prefill_q8 if head_major else lib.kv_append_q8
+    _check(fn(k.data_ptr(), v.data_ptr(), _ptr(batch_idx), input_pos.data_ptr(), N,
+              dev_table.data_ptr(), n_slots, max_pages_per_seq, page_size, n_pages, block,
+              k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), Hkv,
+              D, _ptr(err_word), _stream(stream)), name)
 
 
 def kv_append_q8(k, v, batch_idx, input_pos, dev_table, n_slots, max_pages_per_seq, page_size,
@@ -431,16 +476,9 @@ def kv_append_q8(k, v, batch_idx, input_pos, dev_table, n_slots, max_pages_per_s
                  stream=None) -> None:
     """kv_append into the 8-bit cache (float8_e4m3fn codes, fp32 scales
     [Hkv][n_pages * page_size / scale_block]); k and v are bf16 [B][Hkv][D]."""
-    _bf16(k, "k"), _bf16(v, "v")
-    _i32(batch_idx, "batch_idx"), _i32(input_pos, "input_pos"), _i32(dev_table, "dev_table")
-    block = _q8_cache(k_cache, v_cache, k_scale, v_scale, n_pages * page_size)
-    B, Hkv, D = k.shape
-    if v.shape != k.shape or (Hkv, D) != (k_cache.shape[0], k_cache.shape[2]):
-        raise BadArgError("kv_append_q8: k, v and the caches differ in heads or head dim")
-    _check(load_library().kv_append_q8(
-        _ptr(k), _ptr(v), _ptr(batch_idx), _ptr(input_pos), B, _ptr(dev_table), n_slots,
-        max_pages_per_seq, page_size, n_pages, block, _ptr(k_cache), _ptr(v_cache),
-        _ptr(k_scale), _ptr(v_scale), Hkv, D, _ptr(err_word), _stream(stream)), "kv_append_q8")
+    _append_q8("kv_append_q8", False, k, v, batch_idx, input_pos, dev_table, n_slots,
+               max_pages_per_seq, page_size, n_pages, k_cache, v_cache, k_scale, v_scale,
+               err_word, stream)
 
 
 def kv_append_prefill_q8(k, v, batch_idx, input_pos, dev_table, n_slots, max_pages_per_seq,
@@ -448,17 +486,9 @@ def kv_append_prefill_q8(k, v, batch_idx, input_pos, dev_table, n_slots, max_pag
                          stream=None) -> None:
     """kv_append_q8 of L packed prefill tokens; k and v are head-major
     [Hkv][L][D]."""
-    _bf16(k, "k"), _bf16(v, "v")
-    _i32(batch_idx, "batch_idx"), _i32(input_pos, "input_pos"), _i32(dev_table, "dev_table")
-    block = _q8_cache(k_cache, v_cache, k_scale, v_scale, n_pages * page_size)
-    Hkv, L, D = k.shape
-    if v.shape != k.shape or (Hkv, D) != (k_cache.shape[0], k_cache.shape[2]):
-        raise BadArgError("kv_append_prefill_q8: k, v and the caches differ in heads or head dim")
-    _check(load_library().kv_append_prefill_q8(
-        _ptr(k), _ptr(v), _ptr(batch_idx), _ptr(input_pos), L, _ptr(dev_table), n_slots,
-        max_pages_per_seq, page_size, n_pages, block, _ptr(k_cache), _ptr(v_cache),
-        _ptr(k_scale), _ptr(v_scale), Hkv, D, _ptr(err_word), _stream(stream)),
-        "kv_append_prefill_q8")
+    _append_q8("kv_append_prefill_q8", True, k, v, batch_idx, input_pos, dev_table, n_slots,
+               max_pages_per_seq, page_size, n_pages, k_cache, v_cache, k_scale, v_scale,
+               err_word, stream)
 
 
 def kv_copy_pages(caches, n_pages, pairs, stream=None) -> None:
@@ -478,11 +508,12 @@ def kv_copy_pages(caches, n_pages, pairs, stream=None) -> None:
     for i, c in enumerate(caches):
         if not c.is_contiguous() or c.dim() < 2:
             raise BadArgError("kv_copy_pages: caches must be contiguous tensors [heads][...]")
-        ptrs[i], heads[i] = c.data_ptr(), c.shape[0]
-        size = c.numel() * c.element_size()
-        nbytes[i] = size // max(heads[i] * n_pages, 1)
-        if nbytes[i] * heads[i] * n_pages != size:
+        size, h = c.nbytes, c.shape[0]
+        each = size // max(h * n_pages, 1)
+        if each * h * n_pages != size:
             raise BadArgError("kv_copy_pages: a head of a cache must be n_pages equal pages")
+        ptrs[i], heads[i], nbytes[i] = c.data_ptr(), h, each
+    _on_device(*caches)
     _check(load_library().kv_copy_pages(ptrs, heads, nbytes, n, n_pages, pairs.data_ptr(),
                                         pairs.shape[0], _stream(stream)), "kv_copy_pages")
 
@@ -570,12 +601,22 @@ def paged_decode_attn_q8(q, k_cache, v_cache, k_scale, v_scale, dev_table, n_slo
     Hkv = k_cache.shape[0]
     if D != k_cache.shape[2] or out.shape != q.shape:
         raise BadArgError("paged_decode_attn_q8: q, out and the caches differ in shape")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if seq_lens is None or seq_lens.numel() < B or (
+            batch_idx is not None and batch_idx.numel() < B):
+        raise BadArgError("paged_decode_attn_q8: batch_idx and seq_lens must hold a value for "
+                          "every row")
+    if dev_table is None or dev_table.numel() < n_slots * max_pages_per_seq:
+        raise BadArgError("paged_decode_attn_q8: dev_table must be [n_slots][max_pages_per_seq]")
+    if workspace is None:
+        raise BadArgError("paged_decode_attn_q8: workspace is missing")
+    _on_device(q, k_cache, v_cache, k_scale, v_scale, dev_table, batch_idx, seq_lens, workspace,
+               out, err_word)
     _check(load_library().paged_decode_attn_q8(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(dev_table),
-        n_slots, max_pages_per_seq, page_size, n_pages, block, _ptr(batch_idx), _ptr(seq_lens),
-        int(window), float(scale), B, Hq, Hkv, D, _ptr(workspace), ws_bytes, _ptr(out),
-        _ptr(err_word), _stream(stream)), "paged_decode_attn_q8")
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), dev_table.data_ptr(), n_slots, max_pages_per_seq, page_size, n_pages,
+        block, _ptr(batch_idx), seq_lens.data_ptr(), window, scale, B, Hq, Hkv, D,
+        workspace.data_ptr(), workspace.nbytes, out.data_ptr(), _ptr(err_word),
+        _stream(stream)), "paged_decode_attn_q8")
 
 
 def paged_decode_step(q, k, v, gamma_q, gamma_k, batch_idx, input_pos, theta, eps, dev_table,

@@ -136,11 +136,13 @@ __global__ void __launch_bounds__(kWarps * 32) append_q8_kernel(const Args a) {
       n += more;
       if (more < 32) break;
     }
-    // a run's start also looks for tokens of its block elsewhere in the call:
-    // of two runs that meet in a block, one starts in a block of the other
-    if (reporter && (starts >> l & 1)) {
+    // A run's start also looks for tokens of its block elsewhere in the call (of two
+    // runs that meet in a block, one starts in a block of the other); the warps of all
+    // heads share the tokens to look at.
+    if (starts >> l & 1) {
       bool clash = false;
-      for (long long j = lane; j < a.N; j += 32) {
+#pragma unroll 8
+      for (long long j = which * 32 + lane; j < a.N; j += per_window * 32) {
         const int s = a.batch_idx ? a.batch_idx[j] : static_cast<int>(j);
         clash |= s == slot && (a.input_pos[j] & ~bmask) == (pos & ~bmask) && (j < i || j >= i + n);
       }

@@ -1,6 +1,8 @@
 """Sharing, taking back and moving pages (pt_fork, pt_unshare, pt_truncate,
 pt_compact) through the C ABI, host only: a worked example, a model of the
 policy that keeps token contents, and every refusal leaving the state as it was."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -200,10 +202,6 @@ def test_refusals_leave_the_state():
 def test_copy_refusals_need_no_gpu():
     """Pairs and shapes are refused on the host, before any launch."""
     cache = torch.zeros((2, 6 * 4, 8), dtype=torch.bfloat16)     # never reached
-    for pairs in ([(1, 6)], [(-1, 2)], [(6, 1)], [(1, -1)], [(1, 2), (3, 2)], [(1, 2), (2, 3)],
-                  [(2, 3), (1, 2)], [(4, 4)]):
-        with pytest.raises(pkv.BadArgError):
-            pkv.kv_copy_pages([cache], 6, pairs)
     with pytest.raises(pkv.BadArgError):
         pkv.kv_copy_pages([cache], 5, [(1, 2)])                  # 24 rows are not 5 pages
     with pytest.raises(pkv.BadArgError):
@@ -212,5 +210,27 @@ def test_copy_refusals_need_no_gpu():
         pkv.kv_copy_pages([cache], 6, torch.zeros((1, 2), dtype=torch.int64))
     with pytest.raises(pkv.BadArgError):
         pkv.kv_copy_pages([cache], 0, [(0, 0)])
-    pkv.kv_copy_pages([cache], 6, [])                            # nothing to do
-    pkv.kv_copy_pages([], 6, [(1, 2)])
+    with pytest.raises(pkv.BadArgError):
+        pkv.kv_copy_pages([cache], 6, [(1, 2)])                  # not on a CUDA device
+    pkv.kv_copy_pages([], 6, [(1, 2)])                           # nothing to do
+
+
+def test_copy_library_refusals():
+    """The library's own checks, on an address that nothing follows."""
+    lib = pkv.load_library()
+
+    def call(pairs, heads=2, page_bytes=64, n_pages=6, cache=1 << 20, n_pairs=None):
+        flat = (ctypes.c_int32 * max(2 * len(pairs), 1))(*[x for p in pairs for x in p])
+        return lib.kv_copy_pages((ctypes.c_void_p * 1)(cache), (ctypes.c_int * 1)(heads),
+                                 (ctypes.c_int64 * 1)(page_bytes), 1, n_pages, flat,
+                                 len(pairs) if n_pairs is None else n_pairs, None)
+
+    for pairs in ([(1, 6)], [(-1, 2)], [(6, 1)], [(1, -1)], [(1, 2), (3, 2)], [(1, 2), (2, 3)],
+                  [(2, 3), (1, 2)], [(4, 4)]):
+        assert call(pairs) == pkv.PKV_E_BAD_ARG, pairs
+    for kw in (dict(heads=0), dict(heads=65536), dict(page_bytes=0), dict(n_pages=0),
+               dict(cache=0), dict(n_pairs=-1), dict(page_bytes=1 << 45)):
+        assert call([(1, 2)], **kw) == pkv.PKV_E_BAD_ARG, kw
+    assert call([]) == pkv.PKV_OK
+    assert lib.kv_copy_pages(None, None, None, 0, 6, None, 3, None) == pkv.PKV_OK
+    assert lib.kv_copy_pages(None, None, None, 1, 6, None, 3, None) == pkv.PKV_E_BAD_ARG
