@@ -212,8 +212,9 @@ int kv_append_prefill(const pkv_bf16 *k, const pkv_bf16 *v, const int32_t *batch
  * held behind. Rows on slot 0 (padding) are skipped.
  * The tokens of one block must stand next to each other in the call, at
  * ascending positions (as a packed prompt's do). A call whose tokens do not
- * (or name a position twice) sets PKV_ERR_ORDER and leaves the blocks
- * concerned unspecified. Other errors as in kv_append.
+ * (or name a position twice) leaves the blocks concerned unspecified; if that
+ * shows among its first 4096 tokens it sets PKV_ERR_ORDER. Other errors as in
+ * kv_append.
  * k, v: bf16 [B][Hkv][D]. Requires D % 16 == 0 and 16-byte aligned k, v and
  * caches. One kernel, no workspace.
  * ------------------------------------------------------------------- */

@@ -7,11 +7,13 @@
 // plain exponent shifts, so a block filled token by token holds what one call
 // would have written, but for values below the codes' normal range.
 //
-// Work: the tokens of one block that the call brings stand next to each
-// other (a run); the warp that meets a run's first token in a block handles
-// the whole run there, for one head of K or V: the run's largest magnitude,
-// the block's scale, the rescaling of older codes if the scale grew, the new
-// codes. Bound by reading k and v and writing half their bytes.
+// Work: the tokens of one block that the call brings stand next to each other (a run).
+// A warp looks at a window of tokens for one head of K or V or both; the first token of
+// each run there is taken by a group of lanes (4 to 32, or the CTA's 128 threads, by the
+// size of a run), which finds the run's largest magnitude and the block's scale,
+// rescales older codes if the scale grew and writes the new ones. Extra CTAs look for
+// tokens of one block that stand apart. Bound by reading k and v and writing half their
+// bytes.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -21,38 +23,67 @@
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kKeep = 8;   // 16-byte vectors of a run a lane keeps between the two passes
+constexpr int kChecked = 4096; // tokens of a call that are looked at for their order
+constexpr int kTable = 2048;   // places of a checking CTA's table, for about 1024 blocks
 
 struct Args {
   const __nv_bfloat16 *k, *v;
   const int32_t *batch_idx, *input_pos, *table;
-  int N, n_slots, max_pages, page_size, n_pages, block;
+  int N, n_slots, max_pages, page_size, n_pages, block, log2_block;
   uint8_t *k_cache, *v_cache;
   float *k_scale, *v_scale;
   int Hkv, D;
   long long token_stride, head_stride;   // of k and v, in elements
-  int window;                            // tokens a warp looks at (1 .. 31)
+  int window;                            // tokens a task covers, looked at 31 at a time
+  int tensors;                           // 2: a warp does K and V of its head, 1: one of them
+  int group;                             // lanes a run: 4 .. 32 (unused when a CTA takes one)
+  int checkers;                          // CTAs that look for tokens of a block apart
   int32_t *err;
 };
 
-// Largest finite magnitude of 8 bf16, as the bits of the two halves' maxima.
-__device__ __forceinline__ uint32_t max_finite(uint32_t m, uint4 x) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = w[i] & 0x7fff7fffu;
-    m = __vmaxu2(m, a & __vcmpltu2(a, 0x7f807f80u));
-  }
-  return m;
+struct Unit {   // 16 bf16 values
+  uint4 lo, hi;
+};
+__device__ __forceinline__ Unit load_unit(const __nv_bfloat16 *x) {
+  const uint4 *a = reinterpret_cast<const uint4 *>(x);
+  return {a[0], a[1]};
+}
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) {
+  return *reinterpret_cast<const __nv_bfloat162 *>(&x);
+}
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) {
+  return *reinterpret_cast<const uint32_t *>(&x);
+}
+// Running maxima of |x| (a NaN counts nothing, an infinity does).
+__device__ __forceinline__ __nv_bfloat162 max_abs(__nv_bfloat162 m, const uint4 &x) {
+  m = __hmax2(m, __habs2(as_bf162(x.x)));
+  m = __hmax2(m, __habs2(as_bf162(x.y)));
+  m = __hmax2(m, __habs2(as_bf162(x.z)));
+  return __hmax2(m, __habs2(as_bf162(x.w)));
+}
+// The same over finite values alone.
+__device__ __forceinline__ uint32_t finite(uint32_t x) {
+  const uint32_t a = x & 0x7fff7fffu;
+  return a & __vcmpltu2(a, 0x7f807f80u);
+}
+__device__ __forceinline__ __nv_bfloat162 max_finite(__nv_bfloat162 m, const uint4 &x) {
+  return max_abs(m, make_uint4(finite(x.x), finite(x.y), finite(x.z), finite(x.w)));
 }
 
-__device__ __forceinline__ uint32_t quantise2(uint32_t x, float inv) {
-  const float lo = __uint_as_float(x << 16) * inv, hi = __uint_as_float(x & 0xffff0000u) * inv;
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+// Two values times a power of two (exact in bf16 but below 2^-126, which rounds to 0
+// in e4m3 all the same), to e4m3.
+__device__ __forceinline__ uint32_t quantise2(uint32_t x, __nv_bfloat162 inv) {
+  const uint32_t y = as_u32(__hmul2(as_bf162(x), inv));
+  return __nv_cvt_float2_to_fp8x2(
+      make_float2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u)), __NV_SATFINITE,
+      __NV_E4M3);
 }
-__device__ __forceinline__ uint2 quantise8(uint4 x, float inv) {
-  return make_uint2(quantise2(x.x, inv) | quantise2(x.y, inv) << 16,
-                    quantise2(x.z, inv) | quantise2(x.w, inv) << 16);
+__device__ __forceinline__ uint32_t quantise4(uint32_t a, uint32_t b, __nv_bfloat162 inv) {
+  return __byte_perm(quantise2(a, inv), quantise2(b, inv), 0x5410);
+}
+__device__ __forceinline__ uint4 quantise(const Unit &x, __nv_bfloat162 inv) {
+  return make_uint4(quantise4(x.lo.x, x.lo.y, inv), quantise4(x.lo.z, x.lo.w, inv),
+                    quantise4(x.hi.x, x.hi.y, inv), quantise4(x.hi.z, x.hi.w, inv));
 }
 __device__ __forceinline__ uint32_t rescale2(uint32_t c, float ratio) {
   const __half2 h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3);
@@ -74,139 +105,238 @@ __device__ __forceinline__ float exp2i(int k) {   // 2^k, -126 <= k <= 127
   return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
 
+__device__ __forceinline__ int slot_of(const Args &a, long long i) {
+  return a.batch_idx ? a.batch_idx[i] : static_cast<int>(i);
+}
+// Tokens of one block apart: then the block has two leading tokens, tokens that start a
+// run or are their block's first. So every leading token's (slot, block) must be new.
+// Each checking CTA looks at the first kChecked tokens and keeps the leading ones whose
+// hash is its share in a table in shared memory. (All tokens, by every checking CTA,
+// would take longer than the append itself: 256k tokens of one 64-wide head are 15 us.)
+__device__ __forceinline__ void check_order(const Args &a) {
+  __shared__ unsigned long long table[kTable];
+  const int bmask = a.block - 1, n = min(a.N, kChecked), lane = threadIdx.x & 31;
+  bool clash = false;
+  for (int i = threadIdx.x; i < kTable; i += blockDim.x) table[i] = 0;
+  __syncthreads();
+  constexpr int U = 8;   // tokens a thread has in flight
+#pragma unroll 1
+  for (int i0 = threadIdx.x; i0 - static_cast<int>(threadIdx.x) < n; i0 += U * kWarps * 32) {
+    int slots[U], poss[U], before_slot[U], before_pos[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kWarps * 32;
+      slots[u] = i < n ? slot_of(a, i) : -1;
+      poss[u] = i < n ? a.input_pos[i] : -1;
+      before_slot[u] = lane == 0 && i > 0 && i < n ? slot_of(a, i - 1) : -1;
+      before_pos[u] = lane == 0 && i > 0 && i < n ? a.input_pos[i - 1] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int slot = slots[u], pos = poss[u];
+      int prev_slot = __shfl_up_sync(0xffffffffu, slot, 1);
+      int prev_pos = __shfl_up_sync(0xffffffffu, pos, 1);
+      if (lane == 0) {
+        prev_slot = before_slot[u];
+        prev_pos = before_pos[u];
+      }
+      if (slot > 0 && slot < a.n_slots && pos >= 0 &&
+          ((pos & bmask) == 0 || prev_slot != slot || prev_pos != pos - 1)) {
+        const unsigned long long key =
+            static_cast<unsigned long long>(slot) << 32 | static_cast<uint32_t>(pos & ~bmask);
+        uint32_t h = static_cast<uint32_t>(pos & ~bmask) * 0x9e3779b1u + slot * 0x85ebca77u;
+        h = (h ^ h >> 15) * 0x2c1b3c6du;
+        h ^= h >> 13;
+        if (__umulhi(h, a.checkers) == blockIdx.x) {
+          uint32_t at = h * 0x297a2d39u >> 16;
+          for (int k = 0; k < kTable; ++k, ++at) {
+            const unsigned long long old = atomicCAS(table + at % kTable, 0ull, key);
+            clash |= old == key;
+            if (old == 0ull || old == key) break;
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+  if (__any_sync(0xffffffffu, clash) && lane == 0 && a.err) atomicOr(a.err, PKV_ERR_ORDER);
+}
+
+// CTA: one run at a time for the whole CTA, else for a group of lanes. KEEP: 16-value
+// units of a run that a lane keeps between the two passes.
+template <bool CTA, int KEEP>
 __global__ void __launch_bounds__(kWarps * 32) append_q8_kernel(const Args a) {
   pkv_wait_prior_grid();
   pkv_allow_next_grid();
+  if (static_cast<int>(blockIdx.x) < a.checkers) {
+    check_order(a);
+    return;
+  }
   const int lane = threadIdx.x & 31;
-  const long long task = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5);
-  const int per_window = 2 * a.Hkv;
+  const long long block = blockIdx.x - a.checkers;
+  const long long task = CTA ? block : block * kWarps + (threadIdx.x >> 5);
+  const int per_window = a.tensors == 2 ? a.Hkv : 2 * a.Hkv;
   const long long i0 = task / per_window * a.window;
   if (i0 >= a.N) return;
   const int which = static_cast<int>(task % per_window);
-  const bool is_v = which >= a.Hkv;
-  const int h = is_v ? which - a.Hkv : which;
+  const int kv0 = which >= a.Hkv ? 1 : 0;   // 0: K, 1: V
+  const int h = which - kv0 * a.Hkv;
   const bool reporter = which == 0;
   const int bmask = a.block - 1;
-
-  // lane l looks at token i0 + l - 1: the window's tokens and the one before
-  const long long mine = i0 + lane - 1;
-  const bool there = mine >= 0 && mine < a.N && lane <= a.window;
-  const int my_slot = there ? (a.batch_idx ? a.batch_idx[mine] : static_cast<int>(mine)) : -1;
-  const int my_pos = there ? a.input_pos[mine] : -1;
-  const int prev_slot = __shfl_up_sync(0xffffffffu, my_slot, 1);
-  const int prev_pos = __shfl_up_sync(0xffffffffu, my_pos, 1);
-  const bool follows = mine > 0 && prev_slot == my_slot && prev_pos >= 0 &&
-                       my_pos - 1 == prev_pos;
-  uint32_t leaders = __ballot_sync(
-      0xffffffffu, there && lane > 0 && (!follows || my_pos < 0 || (my_pos & bmask) == 0));
-  const uint32_t starts = __ballot_sync(0xffffffffu, !follows);
-
-  while (leaders) {
-    const int l = __ffs(leaders) - 1;
-    leaders &= leaders - 1;
-    const long long i = i0 + l - 1;
-    const int slot = __shfl_sync(0xffffffffu, my_slot, l);
-    const int pos = __shfl_sync(0xffffffffu, my_pos, l);
-    int bits = 0, page = 0;
-    if (slot < 0 || slot >= a.n_slots) {
-      bits = PKV_ERR_SLOT;
-    } else if (slot == 0) {
-      continue;                      // padding
-    } else if (pos < 0 || pos / a.page_size >= a.max_pages) {
-      bits = PKV_ERR_POS;
-    } else {
-      page = a.table[static_cast<long long>(slot) * a.max_pages + pos / a.page_size];
-      if (page < 0) bits = PKV_ERR_PAGE_NEG;
-      else if (page >= a.n_pages) bits = PKV_ERR_PAGE_RANGE;
-    }
-    if (bits) {
-      if (reporter && lane == 0 && a.err) atomicOr(a.err, bits);
-      continue;
-    }
-    // the run in this block: tokens i .. i + n - 1
-    const int first = pos & bmask, room = a.block - first;
-    int n = 1;
-    while (n < room) {
-      const long long j = i + n + lane;
-      const bool in = n + lane < room && j < a.N &&
-                      (a.batch_idx ? a.batch_idx[j] : static_cast<int>(j)) == slot &&
-                      a.input_pos[j] == pos + n + lane;
-      const uint32_t m = __ballot_sync(0xffffffffu, in);
-      const int more = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
-      n += more;
-      if (more < 32) break;
-    }
-    // A run's start also looks for tokens of its block elsewhere in the call (of two
-    // runs that meet in a block, one starts in a block of the other); the warps of all
-    // heads share the tokens to look at.
-    if (starts >> l & 1) {
-      bool clash = false;
-#pragma unroll 8
-      for (long long j = which * 32 + lane; j < a.N; j += per_window * 32) {
-        const int s = a.batch_idx ? a.batch_idx[j] : static_cast<int>(j);
-        clash |= s == slot && (a.input_pos[j] & ~bmask) == (pos & ~bmask) && (j < i || j >= i + n);
-      }
-      if (__any_sync(0xffffffffu, clash) && lane == 0 && a.err) atomicOr(a.err, PKV_ERR_ORDER);
-    }
-
-    const __nv_bfloat16 *x = (is_v ? a.v : a.k) + i * a.token_stride + h * a.head_stride;
-    const int chunks = a.D / 8;                 // 16-byte vectors a token
-    const long long row0 = static_cast<long long>(h) * a.n_pages * a.page_size +
-                           static_cast<long long>(page) * a.page_size + pos % a.page_size;
-    uint8_t *codes = (is_v ? a.v_cache : a.k_cache) + row0 * a.D;
-    float *scale = (is_v ? a.v_scale : a.k_scale) + row0 / a.block;
-    const float held_raw = first ? *scale : 0.f;
-    // pass 1: the largest magnitude; a lane's first kKeep vectors stay
-    uint4 keep[kKeep];
-    uint32_t m2 = 0;
-    const int total = n * chunks;
-    {
-      int tok = lane / chunks, c = lane % chunks;
+  const int units = a.D / 16;   // of a token
+  // this lane's place in its group
+  const int gs = CTA ? kWarps * 32 : a.group;
+  const int gw = CTA ? 32 : gs;                  // lanes of the group in this warp
+  const int g0 = lane & ~(gw - 1);               // the group's first lane here
+  const int gl = CTA ? threadIdx.x : lane - g0;
+  const uint32_t gmask = (gw == 32 ? 0xffffffffu : (1u << gw) - 1u) << g0;
+  __shared__ uint32_t part[2][kWarps];
+  int turn = 0;
+  auto group_max = [&](uint32_t v) -> uint32_t {
+    v = __reduce_max_sync(gmask, v);
+    if constexpr (CTA) {
+      turn ^= 1;
+      if (lane == 0) part[turn][threadIdx.x >> 5] = v;
+      __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kKeep; ++j) {
-        const int u = lane + 32 * j;
-        keep[j] = u < total ? *reinterpret_cast<const uint4 *>(x + tok * a.token_stride + 8 * c)
-                            : make_uint4(0u, 0u, 0u, 0u);
-        for (c += 32; c >= chunks; c -= chunks) ++tok;
+      for (int i = 0; i < kWarps; ++i) v = max(v, part[turn][i]);
+    }
+    return v;
+  };
+
+  const long long i1 = min(static_cast<long long>(a.N), i0 + a.window);
+  for (long long w0 = i0; w0 < i1; w0 += 31) {
+    const long long w1 = min(i1, w0 + 31);
+    // lane l looks at token w0 + l - 1: the one before the window, the window, and
+    // what a run that begins there goes on to
+    const long long mine = w0 + lane - 1;
+    const bool there = mine >= 0 && mine < a.N;
+    const int my_slot = there ? slot_of(a, mine) : -1;
+    const int my_pos = there ? a.input_pos[mine] : -1;
+    const int prev_slot = __shfl_up_sync(0xffffffffu, my_slot, 1);
+    const int prev_pos = __shfl_up_sync(0xffffffffu, my_pos, 1);
+    const uint32_t goes_on = __ballot_sync(
+        0xffffffffu, there && lane > 0 && mine > 0 && my_pos > 0 && prev_slot == my_slot &&
+                         prev_pos == my_pos - 1 && (my_pos & bmask) != 0);
+    // tokens of the window that lead a run of their block
+    uint32_t leaders = ~goes_on & __ballot_sync(0xffffffffu, there && lane > 0 && lane <= w1 - w0);
+
+    while (leaders) {
+      int l = 0;   // this group's: the groups take the next ones in turn
+      for (int q = 0; q < 32; q += gw) {
+        if (q == g0 && leaders) l = __ffs(leaders) - 1;
+        leaders &= leaders - 1;   // (0 stays 0)
       }
+      const int slot = __shfl_sync(0xffffffffu, my_slot, l);
+      const int pos = __shfl_sync(0xffffffffu, my_pos, l);
+      const long long i = w0 + l - 1;
+      if (l > 0 && slot != 0) {   // a leader, and not padding
+        int bits = 0;
+        if (slot < 0 || slot >= a.n_slots) bits = PKV_ERR_SLOT;
+        else if (pos < 0 || pos / a.page_size >= a.max_pages) bits = PKV_ERR_POS;
+        int page = 0, in_page = 0;
+        if (!bits) {
+          const int pb = pos / a.page_size;
+          in_page = pos - pb * a.page_size;
+          page = a.table[static_cast<long long>(slot) * a.max_pages + pb];
+        }
+        // the run in this block: tokens i .. i + n - 1
+        const int first = pos & bmask, room = a.block - first;
+        int n = 32 - l;   // tokens in sight
+        if (l < 31) {
+          const uint32_t after = ~goes_on >> (l + 1);   // a zero bit: that token goes on
+          if (after & (0x7fffffffu >> l)) n = __ffs(after);
+        }
+        if (n == 32 - l) {   // it may go on out of sight
+          while (n < room) {
+            const long long j = i + n + (lane - g0);
+            const bool in = n + (lane - g0) < room && j < a.N && slot_of(a, j) == slot &&
+                            a.input_pos[j] == pos + n + (lane - g0);
+            const uint32_t m = __ballot_sync(gmask, in) >> g0;
+            const int more = min(__ffs(~m) == 0 ? 32 : __ffs(~m) - 1, gw);
+            n += more;
+            if (more < gw) break;
+          }
+        }
+        const int total = n * units;
+        const bool flat = a.token_stride == a.D || n == 1;
+        for (int kv = kv0; kv < kv0 + a.tensors; ++kv) {
+          const __nv_bfloat16 *x = (kv ? a.v : a.k) + i * a.token_stride + h * a.head_stride;
+          auto unit = [&](int u) -> const __nv_bfloat16 * {
+            if (flat) return x + 16 * u;
+            const int t = u / units;
+            return x + t * a.token_stride + 16 * (u - t * units);
+          };
+          // pass 1: the largest magnitude; a lane's first KEEP units stay (their loads
+          // go out beside the table's)
+          Unit keep[KEEP];
 #pragma unroll
-      for (int j = 0; j < kKeep; ++j) m2 = max_finite(m2, keep[j]);
-      for (int u = lane + 32 * kKeep; u < total; u += 32) {
-        m2 = max_finite(m2, *reinterpret_cast<const uint4 *>(x + tok * a.token_stride + 8 * c));
-        for (c += 32; c >= chunks; c -= chunks) ++tok;
-      }
-    }
-    const uint32_t amax = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
-    const float held = held_raw > 0.f && held_raw < INFINITY ? held_raw : 0.f;
-    int e = need_exponent(amax);
-    if (held > 0.f) {   // the held scale, rounded up to a power of two
-      const uint32_t hb = __float_as_uint(held);
-      int he = static_cast<int>(hb >> 23) - 127 + ((hb & 0x7fffffu) ? 1 : 0);
-      he = min(max(he, -126), 126);
-      e = max(e, he);
-    }
-    const float s = exp2i(e), inv = exp2i(-e);
-    if (first && s != held_raw) {
-      const float ratio = held * inv;
-      uint2 *old = reinterpret_cast<uint2 *>(codes - static_cast<long long>(first) * a.D);
-      for (int u = lane; u < first * chunks; u += 32) {
-        const uint2 c = old[u];
-        old[u] = make_uint2(rescale4(c.x, ratio), rescale4(c.y, ratio));
-      }
-    }
-    if (lane == 0) *scale = s;
-    // pass 2: the codes
-    uint2 *dst = reinterpret_cast<uint2 *>(codes);
-    int tok = lane / chunks, c = lane % chunks;
+          for (int j = 0; j < KEEP; ++j) {
+            const int u = gl + gs * j;
+            if (u < total) keep[j] = load_unit(unit(u));
+            else keep[j].lo = keep[j].hi = make_uint4(0u, 0u, 0u, 0u);
+          }
+          if (!bits) {
+            if (page < 0) bits = PKV_ERR_PAGE_NEG;
+            else if (page >= a.n_pages) bits = PKV_ERR_PAGE_RANGE;
+          }
+          if (bits) break;
+          const long long row0 = static_cast<long long>(h) * a.n_pages * a.page_size +
+                                 static_cast<long long>(page) * a.page_size + in_page;
+          uint8_t *codes = (kv ? a.v_cache : a.k_cache) + row0 * a.D;
+          float *scale = (kv ? a.v_scale : a.k_scale) + (row0 >> a.log2_block);
+          const float held_raw = first ? *scale : 0.f;
+          __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
 #pragma unroll
-    for (int j = 0; j < kKeep; ++j) {
-      const int u = lane + 32 * j;
-      if (u < total) dst[u] = quantise8(keep[j], inv);
-      for (c += 32; c >= chunks; c -= chunks) ++tok;
-    }
-    for (int u = lane + 32 * kKeep; u < total; u += 32) {
-      dst[u] = quantise8(*reinterpret_cast<const uint4 *>(x + tok * a.token_stride + 8 * c), inv);
-      for (c += 32; c >= chunks; c -= chunks) ++tok;
+          for (int j = 0; j < KEEP; ++j) m2 = max_abs(max_abs(m2, keep[j].lo), keep[j].hi);
+#pragma unroll 4
+          for (int u = gl + gs * KEEP; u < total; u += gs) {
+            const Unit y = load_unit(unit(u));
+            m2 = max_abs(max_abs(m2, y.lo), y.hi);
+          }
+          uint32_t amax = group_max(max(as_u32(m2) & 0xffffu, as_u32(m2) >> 16));
+          if (amax >= 0x7f80u) {   // an infinity among them: the finite ones again
+            m2 = __float2bfloat162_rn(0.f);
+            for (int u = gl; u < total; u += gs) {
+              const Unit y = load_unit(unit(u));
+              m2 = max_finite(max_finite(m2, y.lo), y.hi);
+            }
+            amax = group_max(max(as_u32(m2) & 0xffffu, as_u32(m2) >> 16));
+          }
+          const float held = held_raw > 0.f && held_raw < INFINITY ? held_raw : 0.f;
+          int e = need_exponent(amax);
+          if (held > 0.f) {   // the held scale, rounded up to a power of two
+            const uint32_t hb = __float_as_uint(held);
+            int he = static_cast<int>(hb >> 23) - 127 + ((hb & 0x7fffffu) ? 1 : 0);
+            he = min(max(he, -126), 126);
+            e = max(e, he);
+          }
+          const float s = exp2i(e), inv = exp2i(-e);
+          if (first && s != held_raw) {
+            const float ratio = held * inv;
+            uint4 *old = reinterpret_cast<uint4 *>(codes - static_cast<long long>(first) * a.D);
+            for (int u = gl; u < first * units; u += gs) {
+              const uint4 c = old[u];
+              old[u] = make_uint4(rescale4(c.x, ratio), rescale4(c.y, ratio), rescale4(c.z, ratio),
+                                  rescale4(c.w, ratio));
+            }
+          }
+          if (gl == 0) *scale = s;   // (the group has read the held one before its maximum)
+          // pass 2: the codes
+          const __nv_bfloat162 inv2 = __float2bfloat162_rn(inv);
+          uint4 *dst = reinterpret_cast<uint4 *>(codes);
+#pragma unroll
+          for (int j = 0; j < KEEP; ++j) {
+            const int u = gl + gs * j;
+            if (u < total) dst[u] = quantise(keep[j], inv2);
+          }
+#pragma unroll 4
+          for (int u = gl + gs * KEEP; u < total; u += gs)
+            dst[u] = quantise(load_unit(unit(u)), inv2);
+        }
+        if (bits && reporter && gl == 0 && a.err) atomicOr(a.err, bits);
+      }
+      __syncwarp();
     }
   }
 }
@@ -245,6 +375,8 @@ int launch_append_q8(const char *fn, const pkv_bf16 *k, const pkv_bf16 *v,
   a.page_size = page_size;
   a.n_pages = n_pages;
   a.block = scale_block;
+  a.log2_block = 0;
+  while ((1 << a.log2_block) < scale_block) ++a.log2_block;
   a.k_cache = k_cache;
   a.v_cache = v_cache;
   a.k_scale = k_scale;
@@ -254,15 +386,27 @@ int launch_append_q8(const char *fn, const pkv_bf16 *k, const pkv_bf16 *v,
   a.token_stride = head_major ? D : 1LL * Hkv * D;
   a.head_stride = head_major ? 1LL * N * D : D;
   a.err = err_word;
-  // one token a warp while those warps fit the GPU at once (a decode step),
-  // else 16 (a packed prompt, where few tokens lead a run)
-  const long long pairs = 2LL * Hkv;
-  a.window = N * pairs <= 32LL * sms ? 1 : 16;
-  const long long tasks = (N + a.window - 1LL) / a.window * pairs;
-  const long long blocks = (tasks + kWarps - 1) / kWarps;
+  // A run's expected units of 16 values: a block's tokens in a prompt, one token else.
+  const long long run = 1LL * (head_major ? scale_block : 1) * D / 16;
+  // One token of K or V a warp while those warps fit the GPU twice over (a decode
+  // step), else windows of 16 tokens (a block's, for a CTA a run); two units of a run a lane, or a CTA for a run of
+  // 8 units a lane of a warp and more.
+  const bool few = 2LL * N * Hkv <= 64LL * sms;
+  const bool whole_cta = !few && run >= 256;
+  a.window = few ? 1 : whole_cta && scale_block > 16 ? scale_block : 16;
+  a.tensors = few || whole_cta ? 1 : 2;
+  a.group = 32;
+  if (!few)
+    while (a.group > 4 && a.group >= run) a.group /= 2;
+  a.checkers = ((N < kChecked ? N : kChecked) + 1023) / 1024;
+  const long long tasks = (N + a.window - 1LL) / a.window * Hkv * (3 - a.tensors);
+  const long long blocks = a.checkers + (whole_cta ? tasks : (tasks + kWarps - 1) / kWarps);
   if (blocks > 0x7fffffffLL) return pkv::fail(PKV_E_BAD_ARG, "%s: too large", fn);
-  PKV_CUDA_CHECK(pkv::launch_pdl(append_q8_kernel, dim3(static_cast<unsigned>(blocks)),
-                                 dim3(kWarps * 32), 0, static_cast<cudaStream_t>(stream), a));
+  auto *kern = whole_cta               ? append_q8_kernel<true, 4>
+               : run <= 2 * a.group ? append_q8_kernel<false, 2>
+                                    : append_q8_kernel<false, 4>;
+  PKV_CUDA_CHECK(pkv::launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kWarps * 32), 0,
+                                 static_cast<cudaStream_t>(stream), a));
   return pkv::ok();
 }
 
