@@ -1174,24 +1174,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
           }
         }
         const float U0 = M0 == -INFINITY ? 0.f : M0, U1 = M1 == -INFINITY ? 0.f : M1;
-        uint32_t pb[2 * MB], keep[2 * MB];
+        uint32_t pb[2 * MB];
 #pragma unroll
-        for (int i = 0; i < 2 * MB; ++i) {
+        for (int i = 0; i < 2 * MB; ++i)
           pb[i] = transpose8x8(pack_f16(ex2(sx[i][0] + lv[i] - U0), ex2(sx[i][1] + lv[i] - U1)));
-          keep[i] = 0xffffffffu;
-        }
-        if (!whole) {   // codes of keys outside the unit count 0, whatever they are
-#pragma unroll
-          for (int i = 0; i < 2 * MB; ++i) {
-            const int r = key0 + 2 * tig + 8 * i;
-            keep[i] = (valid(r) ? 0xffffu : 0u) | (valid(r + 1) ? 0xffff0000u : 0u);
-          }
-        }
         // ---- O^T [D x 8 heads] += V^T P^T ----
         st = (ent + 1) % Cf::NS;
         if (!mbar_wait(full + 8 * st, ((ent + 1) / Cf::NS) & 1, abort_flag)) give_up();
         __syncwarp();
         base = s0 + st * Cf::TILE_BYTES;
+        if (!whole) {   // codes of this warp's keys outside the unit count 0, whatever they are
+#pragma unroll 1
+          for (int i = lane; i < 16 * MB * KS; i += 32) {
+            const int r = key0 + i / KS;
+            if (!valid(r))
+              *reinterpret_cast<uint4 *>(sm + unit_addr<D>(st * Cf::TILE_BYTES, row_base<D>(r),
+                                                           i % KS)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async();   // the next copy into the entry comes after these stores
+          __syncwarp();
+        }
 #pragma unroll
         for (int u = 0; u < KS; u += 2) {
 #pragma unroll
@@ -1199,11 +1201,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
             uint32_t r[4], a0, a1, a2, a3;
             ldsm_x4_t(unit_addr<D>(base, ldsm_base, u + ldsm_unit) + i * ROWS16, r);
             // a word holds two columns of two keys; pair the keys of each column
-            codes_to_f16(__byte_perm(r[0] & keep[2 * i], 0, 0x3120), a0, a1);
-            codes_to_f16(__byte_perm(r[1] & keep[2 * i + 1], 0, 0x3120), a2, a3);
+            codes_to_f16(__byte_perm(r[0], 0, 0x3120), a0, a1);
+            codes_to_f16(__byte_perm(r[1], 0, 0x3120), a2, a3);
             mma_f16(o[u], a0, a1, a2, a3, pb[2 * i], pb[2 * i + 1]);
-            codes_to_f16(__byte_perm(r[2] & keep[2 * i], 0, 0x3120), a0, a1);
-            codes_to_f16(__byte_perm(r[3] & keep[2 * i + 1], 0, 0x3120), a2, a3);
+            codes_to_f16(__byte_perm(r[2], 0, 0x3120), a0, a1);
+            codes_to_f16(__byte_perm(r[3], 0, 0x3120), a2, a3);
             mma_f16(o[u + 1], a0, a1, a2, a3, pb[2 * i], pb[2 * i + 1]);
           }
         }
