@@ -83,7 +83,8 @@ struct Cfg {
   // holds only for who has waited for that one too.
   static constexpr int NS = D == 64 ? 16 : D == 128 ? 8 : D == 256 ? 4 : 5;
   static_assert(TEAMS == 1 || NS % (2 * TEAMS) == 0, "entries keep their team");
-  static constexpr int COLS = D < 128 ? D : 128;   // bytes of a row in one box
+  static constexpr int COLS = D < 128 ? D : 128;   // bytes of a token in one box
+  static constexpr int TOKENS = D < 128 ? 2 : 1;   // tokens in a 128-byte row of the copy
   static constexpr int CHUNKS = D / COLS;
   static constexpr int CHUNK_BYTES = kT * COLS;
   static constexpr int TILE_BYTES = kT * D;
@@ -91,9 +92,10 @@ struct Cfg {
   static constexpr int Q_STAGE = kMaxG * Q_ROW;
   static constexpr int OFF_Q = NS * TILE_BYTES;
   static constexpr int OFF_SCALE = OFF_Q + 2 * Q_STAGE;      // [2][2][kScaleWords] f32
-  // states handed over: [MS] slots of [4 warps][8 heads] rows, then m, l, M [4][8] each
-  static constexpr int MS = D == 512 ? 2 : 1;
-  static constexpr int MERGE_SLOT = (kCWarps * kMaxG * kMergeRow + 3 * kCWarps * kMaxG) * 4;
+  // states handed over: [MS] slots of [4 warps][8 heads] rows, then M [4][8], then m and l
+  // of every lane, [4 warps][8 lanes][8 heads] each
+  static constexpr int MS = 1;
+  static constexpr int MERGE_SLOT = (kCWarps * kMaxG * kMergeRow + 17 * kCWarps * kMaxG) * 4;
   static constexpr int OFF_MERGE = OFF_SCALE + 4 * kScaleWords * 4;
   static constexpr int OFF_QS = OFF_MERGE + MS * MERGE_SLOT;                    // [2][8] f32
   // weights of the states added up: the warps' and the parts' taken in
@@ -104,7 +106,7 @@ struct Cfg {
   static constexpr int DUMP_ROW = D + 4;
   static constexpr int DUMP_STATS = kCWarps * kMaxG * DUMP_ROW;
   static_assert((DUMP_STATS + 3 * kCWarps * kMaxG) * 4 <= NS * TILE_BYTES, "states fit the ring");
-  static constexpr int N_BARS = 2 * NS + 8 + 2 * MS;
+  static constexpr int N_BARS = 2 * NS + 10 + 2 * MS;
   static constexpr int OFF_TILE = OFF_BAR + N_BARS * 8;   // [NS] u32: box mask, row offset
   static constexpr int OFF_MISC = OFF_TILE + NS * 4;      // abort flag
   static constexpr int OFF_DESC = (OFF_MISC + 8 + 15) & ~15;       // Unit [2]
@@ -254,13 +256,14 @@ __device__ __forceinline__ float exp2i(int k) {   // 2^k, -126 <= k <= 127
   return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
 
-// Where 16-byte unit u of tile row r lies in a tile written by a swizzled copy:
-// row_base(r) ^ unit_bits(u). Rows of 128 bytes (and their 128-byte chunks, each a
-// [kT][128 B] block) XOR the unit with the row mod 8; rows of 64 bytes with
-// (row / 2) mod 4.
+// Where 16-byte unit u of tile row r lies in a tile written by the swizzled copy:
+// row_base(r) ^ unit_bits(u). The copy's rows are 128 bytes (D = 64: two tokens; above
+// 128: one of the 128-byte chunks, each a [kT][128 B] block), whose units are XORed with
+// the row mod 8.
 template <int D>
 __device__ __forceinline__ uint32_t row_base(int r) {
-  return D == 64 ? r * 64 + (((r >> 1) & 3) << 4) : r * 128 + ((r & 7) << 4);
+  if (D == 64) return (r >> 1) * 128 + ((((r & 1) << 2) ^ ((r >> 1) & 7)) << 4);
+  return r * 128 + ((r & 7) << 4);
 }
 template <int D>
 __device__ __forceinline__ uint32_t unit_addr(uint32_t tile, uint32_t base, int u) {
@@ -336,7 +339,7 @@ struct Line {
 
 // A run of tiles [ta, tb) of one (row, kv head), keys [k0, k1), the part-th of
 // `parts`; b < 0: no more work.
-struct Unit {
+struct alignas(16) Unit {
   int b, g, slot, ta, tb, k0, k1, part, parts, first_cta;
 };
 static_assert(sizeof(Unit) <= 48, "unit descriptor slot");
@@ -388,13 +391,6 @@ __device__ __forceinline__ void which_part(const Line &line, Unit &w) {
   w.part = me - w.first_cta;
 }
 
-// Exponent of the largest magnitude of a pair of bf16 halves' maxima.
-__device__ __forceinline__ int q_exponent(uint32_t m) {
-  return min(max(static_cast<int>(max(m & 0xffffu, m >> 16) >> 7) - 127, -126), 126);
-}
-__device__ __forceinline__ uint32_t bf16_to_f16(uint32_t v, float f) {
-  return pack_f16(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
-}
 // A sum l held relative to maximum m, relative to n >= m instead (a NaN stays one).
 __device__ __forceinline__ float sum_at(float l, float m, float n) {
   return m == -INFINITY ? (l != l ? l : 0.f) : l * ex2(m - n);
@@ -469,9 +465,9 @@ __device__ __forceinline__ uint2 pack4_bf16(const float4 &v, float f) {
 // time of fetching its instructions.
 template <int D>
 __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32_t fullQ,
-                                           uint32_t emptyQ, uint32_t fullM, uint32_t emptyM,
-                                           const Unit *udesc, volatile int *abort_flag,
-                                           int lane) {
+                                           uint32_t readyQ, uint32_t emptyQ, uint32_t fullM,
+                                           uint32_t emptyM, const Unit *udesc,
+                                           volatile int *abort_flag, int lane) {
   using Cf = Cfg<D>;
   constexpr int COLS = D < kMergeCols ? D : kMergeCols;
   constexpr int ROUNDS = D / COLS;
@@ -480,16 +476,51 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
   const int hs = lane / LPH, col = lane % LPH * 4;
   int it_q = 0, it_m = 0;
   pkv_wait_prior_grid();
-  while (true) {
+  // The next unit: its query rows become fp16 in place, each scaled by a power of two
+  // to its largest magnitude, before the consumer warps need them.
+  auto receive = [&](Unit &w) {
     const int qs = it_q & 1;
     const bool q_ok = mbar_wait(fullQ + 8 * qs, (it_q >> 1) & 1, abort_flag);
-    Unit w;
     w.b = -1;
     if (q_ok) w = udesc[qs];
     __syncwarp();
-    if (__any_sync(0xffffffffu, w.b < 0)) return;
-    if (lane == 0) mbar_arrive(emptyQ + 8 * qs);
+    if (__any_sync(0xffffffffu, w.b < 0)) w.b = -1;
+    if (w.b >= 0) {
+#pragma unroll 1
+      for (int h = 0; h < p.G; ++h) {
+        uint32_t *row = reinterpret_cast<uint32_t *>(sm + Cf::OFF_Q + qs * Cf::Q_STAGE +
+                                                     h * Cf::Q_ROW);
+        uint32_t v[D / 64], m = 0;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+          v[j] = row[lane + 32 * j];
+          m = __vmaxu2(m, v[j] & 0x7fff7fffu);
+        }
+        m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+        const int e = min(max(static_cast<int>(m >> 7) - 127, -126), 126);
+        const float f = exp2i(-e);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+          row[lane + 32 * j] = pack_f16(__uint_as_float(v[j] << 16) * f,
+                                        __uint_as_float(v[j] & 0xffff0000u) * f);
+        if (lane == 0)
+          reinterpret_cast<float *>(sm + Cf::OFF_QS)[qs * kMaxG + h] = p.scale_log2 * exp2i(e);
+      }
+      fence_proxy_async();   // the next copy into the stage comes after these stores
+    }
+    __syncwarp();
+    if (lane == 0) {
+      if (q_ok) mbar_arrive(readyQ + 8 * qs);
+      if (w.b >= 0) mbar_arrive(emptyQ + 8 * qs);
+    }
     ++it_q;
+  };
+  Unit w, next;
+  receive(next);
+  while (true) {
+    w = next;
+    if (w.b < 0) return;
+    receive(next);
     if (takes_others(w)) continue;
     const bool partial = w.part > 0;
     float f = 0.f, last = 0.f, m = 0.f, l = 0.f, M = 0.f;
@@ -501,8 +532,14 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
       const float *merge =
           reinterpret_cast<const float *>(sm + Cf::OFF_MERGE + ms * Cf::MERGE_SLOT);
       if (r == 0) {
-        const float *a = merge + kCWarps * kMaxG * kMergeRow + lane;
-        const float own_m = a[0], own_l = a[32], own_M = a[64];
+        const float *a = merge + kCWarps * kMaxG * kMergeRow;
+        const float own_M = a[lane];
+        a += 32 + (lane >> 3) * 64 + (lane & 7);   // the warp's lanes, for this head
+        float own_m = -INFINITY, own_l = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) own_m = fmaxf(own_m, a[8 * i]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) own_l += sum_at(a[256 + 8 * i], a[8 * i], own_m);
         m = own_m;
         M = own_M;
 #pragma unroll
@@ -716,7 +753,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
   const uint32_t s0 = smem_u32(sm);
   const uint32_t full = s0 + Cf::OFF_BAR, empty = full + 8 * Cf::NS,
                  fullQ = empty + 8 * Cf::NS, emptyQ = fullQ + 16, fullM = emptyQ + 16,
-                 emptyM = fullM + 8 * Cf::MS, fullS = emptyM + 8 * Cf::MS, emptyS = fullS + 16;
+                 emptyM = fullM + 8 * Cf::MS, fullS = emptyM + 8 * Cf::MS, emptyS = fullS + 16,
+                 readyQ = emptyS + 16;
   uint32_t *tile_word = reinterpret_cast<uint32_t *>(sm + Cf::OFF_TILE);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OFF_MISC);
   Unit *udesc = reinterpret_cast<Unit *>(sm + Cf::OFF_DESC);
@@ -845,6 +883,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
             const int lo_r = max(w.k0 - t * kT, 0), hi_r = min(w.k1 - t * kT, kT);
             if (hi_r < kT && (lo_r == 0 || hi_r <= kT - lo_r)) off = hi_r - kT;
             else if (lo_r > 0) off = lo_r;
+            off = off / Cf::TOKENS * Cf::TOKENS;   // whole rows of the copy, towards the tile's
           }
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
@@ -861,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
             __syncwarp();
             if (lane >= tt * boxes && lane < (tt + 1) * boxes && row >= 0) {
               const int i = lane - tt * boxes;
-              const int y = (row & (ps - 1)) + off, z = row >> p.log2_ps;
+              const int y = ((row & (ps - 1)) + off) / Cf::TOKENS, z = row >> p.log2_ps;
 #pragma unroll
               for (int cc = 0; cc < Cf::CHUNKS; ++cc)
                 tma_load_3d(dst + cc * Cf::CHUNK_BYTES + i * box_rows * Cf::COLS,
@@ -945,7 +984,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
                         : i < M0 + Cf::MS ? kCWarps        // fullM
                         : i < S0          ? 1              // emptyM
                         : i < S0 + 2      ? 32             // fullS
-                                          : kCWarps;       // emptyS
+                        : i < S0 + 4      ? kCWarps        // emptyS
+                                          : 1;             // readyQ
       mbar_init(full + 8 * i, count);
     }
     if (lane == 0) {
@@ -957,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     fence_proxy_async();
     __syncwarp();
     setup_sync();
-    join_units<D>(p, sm, fullQ, emptyQ, fullM, emptyM, udesc, abort_flag, lane);
+    join_units<D>(p, sm, fullQ, readyQ, emptyQ, fullM, emptyM, udesc, abort_flag, lane);
     return;
   }
 
@@ -993,62 +1033,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
 
   while (true) {
     const int qs = it_q & 1;
-    const bool q_ok = mbar_wait(fullQ + 8 * qs, (it_q >> 1) & 1, abort_flag);
+    const bool q_ok = mbar_wait(readyQ + 8 * qs, (it_q >> 1) & 1, abort_flag);
     Unit w;
     w.b = -1;
     if (q_ok) w = udesc[qs];
     else give_up();
-    // q to fp16, each row scaled by a power of two to its largest magnitude
+    if (__any_sync(0xffffffffu, w.b < 0)) break;
+    // lane (gid, tig) holds head gid's fragments
     const uint8_t *qrow = sm + Cf::OFF_Q + qs * Cf::Q_STAGE + gid * Cf::Q_ROW + tig * 8;
+    const float *qscale = reinterpret_cast<const float *>(sm + Cf::OFF_QS) + qs * kMaxG;
+    const float sc0 = h0 < p.G ? qscale[h0] : 0.f, sc1 = h1 < p.G ? qscale[h1] : 0.f;
     uint2 qb[QK];
-    float sc0, sc1;
-    if constexpr (Q_REGS) {   // a warp's own copy: lane (gid, tig) holds head gid's fragments
-      if (__any_sync(0xffffffffu, w.b < 0)) break;
-      uint32_t m = 0;
+    if constexpr (Q_REGS) {
 #pragma unroll
-      for (int c = 0; c < KS; ++c) {
+      for (int c = 0; c < KS; ++c)
         qb[c] = hv ? *reinterpret_cast<const uint2 *>(qrow + 32 * c) : make_uint2(0u, 0u);
-        m = __vmaxu2(m, __vmaxu2(qb[c].x & 0x7fff7fffu, qb[c].y & 0x7fff7fffu));
-      }
       __syncwarp();
       if (lane == 0) mbar_arrive(emptyQ + 8 * qs);
-      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const int e = q_exponent(m);
-      const float f = exp2i(-e);
-#pragma unroll
-      for (int c = 0; c < KS; ++c) {
-        qb[c].x = bf16_to_f16(qb[c].x, f);
-        qb[c].y = bf16_to_f16(qb[c].y, f);
-      }
-      const float sc = p.scale_log2 * exp2i(e);
-      sc0 = __shfl_sync(0xffffffffu, sc, 8 * tig);       // head h0's, from lane (h0, 0)
-      sc1 = __shfl_sync(0xffffffffu, sc, 8 * tig + 4);
-    } else {                  // in place, once for the four warps
-      if (w.b >= 0) {
-        for (int h = warp; h < p.G; h += kCWarps) {
-          uint32_t *row = reinterpret_cast<uint32_t *>(sm + Cf::OFF_Q + qs * Cf::Q_STAGE +
-                                                       h * Cf::Q_ROW);
-          uint32_t v[D / 64], m = 0;
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            v[j] = row[lane + 32 * j];
-            m = __vmaxu2(m, v[j] & 0x7fff7fffu);
-          }
-          m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-          const int e = q_exponent(m);
-          const float f = exp2i(-e);
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j) row[lane + 32 * j] = bf16_to_f16(v[j], f);
-          if (lane == 0)
-            reinterpret_cast<float *>(sm + Cf::OFF_QS)[qs * kMaxG + h] = p.scale_log2 * exp2i(e);
-        }
-        fence_proxy_async();
-      }
-      if (consumer_sync_or(w.b < 0)) break;
-      const float *qscale = reinterpret_cast<const float *>(sm + Cf::OFF_QS) + qs * kMaxG;
-      sc0 = h0 < p.G ? qscale[h0] : 0.f;
-      sc1 = h1 < p.G ? qscale[h1] : 0.f;
     }
     ++it_q;
 
@@ -1222,20 +1223,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
       if (lane == 0) mbar_arrive(emptyQ + 8 * qs);
     }
 
-    // ---- the unit's end: this warp's state goes to the joining warp ----
-    float n0 = m0, n1 = m1;
-#pragma unroll
-    for (int i = 4; i < 32; i <<= 1) {
-      n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, i));
-      n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, i));
-    }
-    l0 = sum_at(l0, m0, n0);
-    l1 = sum_at(l1, m1, n1);
-#pragma unroll
-    for (int i = 4; i < 32; i <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, i);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, i);
-    }
+    // ---- the unit's end ----
     if (takes_others(w)) {   // the CTA's last work: the ring is free once all are here
       (void)consumer_sync_or(false);
       float *dump = reinterpret_cast<float *>(sm);
@@ -1244,6 +1232,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
         float *d = dump + (warp * kMaxG + h0) * Cf::DUMP_ROW + 16 * u + 2 * gid;
         *reinterpret_cast<float2 *>(d) = make_float2(o[u][0], o[u][2]);
         *reinterpret_cast<float2 *>(d + Cf::DUMP_ROW) = make_float2(o[u][1], o[u][3]);
+      }
+      float n0 = m0, n1 = m1;
+#pragma unroll
+      for (int i = 4; i < 32; i <<= 1) {
+        n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, i));
+        n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, i));
+      }
+      l0 = sum_at(l0, m0, n0);
+      l1 = sum_at(l1, m1, n1);
+#pragma unroll
+      for (int i = 4; i < 32; i <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, i);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, i);
       }
       if (gid == 0) {
         float *st = dump + Cf::DUMP_STATS + warp * kMaxG + h0;
@@ -1268,11 +1269,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
         *reinterpret_cast<float2 *>(d) = make_float2(f[0], f[2]);
         *reinterpret_cast<float2 *>(d + kMergeRow) = make_float2(f[1], f[3]);
       }
-      if (c0 == 0 && gid == 0) {
-        float *st = merge + kCWarps * kMaxG * kMergeRow + warp * kMaxG;
-        *reinterpret_cast<float2 *>(st + h0) = make_float2(n0, n1);
-        *reinterpret_cast<float2 *>(st + 32 + h0) = make_float2(l0, l1);
-        *reinterpret_cast<float2 *>(st + 64 + h0) = make_float2(M0, M1);
+      if (c0 == 0) {
+        float *st = merge + kCWarps * kMaxG * kMergeRow + h0;
+        if (gid == 0) *reinterpret_cast<float2 *>(st + warp * kMaxG) = make_float2(M0, M1);
+        st += 32 + (warp * 8 + gid) * kMaxG;
+        *reinterpret_cast<float2 *>(st) = make_float2(m0, m1);
+        *reinterpret_cast<float2 *>(st + 256) = make_float2(l0, l1);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(fullM + 8 * ms);
@@ -1302,19 +1304,19 @@ EncodeTiledFn encode_fn() {
 
 // Map over a cache of `pages` pages (all heads') of page_size rows of D bytes:
 // {column, row in page, page}, boxes of box_rows rows; rows outside the page read 0.
+// D = 64: two rows of the cache make one of the map.
 int make_cache_map(CUtensorMap *tm, const void *base, long long pages, int page_size, int D,
                    int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return pkv::fail(PKV_E_CUDA, "cuTensorMapEncodeTiled unavailable");
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page_size),
+  const int width = D < 128 ? 128 : D, rows = page_size * D / width;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(pages)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(D) * page_size};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(D < 128 ? D : 128),
-                       static_cast<cuuint32_t>(box_rows), 1u};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(D) * page_size};
+  cuuint32_t box[3] = {128u, static_cast<cuuint32_t>(box_rows * D / width), 1u};
   cuuint32_t estr[3] = {1u, 1u, 1u};
   CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return pkv::fail(PKV_E_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
