@@ -244,8 +244,8 @@ int kv_append_prefill_q8(const pkv_bf16 *k, const pkv_bf16 *v,
  * (int32 [n_pairs][2]) are host arrays, read before the call returns; the
  * cache pointers are device memory. Refused with PKV_E_BAD_ARG: a page
  * outside [0, n_pages), a destination named twice or also a source (the
- * copies run in any order), NULL pointers, sizes below 1, and a cache of
- * 2^46 bytes or more. Any alignment is accepted; 16-byte aligned
+ * copies run in any order), NULL pointers, sizes below 1, more than 65535
+ * heads, a page above 2^31 bytes and a cache of 2^46 or more. Any alignment is accepted; 16-byte aligned
  * caches and page sizes copy fastest. n_pairs 0 launches nothing. A captured
  * call repeats the same pairs.
  * ------------------------------------------------------------------- */
