@@ -245,9 +245,10 @@ int kv_append_prefill_q8(const pkv_bf16 *k, const pkv_bf16 *v,
  * cache pointers are device memory. Refused with PKV_E_BAD_ARG: a page
  * outside [0, n_pages), a destination named twice or also a source (the
  * copies run in any order), NULL pointers, sizes below 1, more than 65535
- * heads, a page above 2^31 bytes and a cache of 2^46 or more. Any alignment is accepted; 16-byte aligned
- * caches and page sizes copy fastest. n_pairs 0 launches nothing. A captured
- * call repeats the same pairs.
+ * heads, a page above 2^31 bytes and a cache of 2^46 or more. Any alignment
+ * is accepted; 16-byte aligned caches and page sizes copy fastest. n_pairs 0
+ * checks the caches and launches nothing (pairs may be NULL). A captured call
+ * repeats the same pairs.
  * ------------------------------------------------------------------- */
 int kv_copy_pages(void *const *caches, const int *heads, const int64_t *page_bytes,
                   int n_caches, int n_pages, const int32_t *pairs, int n_pairs,
@@ -364,16 +365,17 @@ size_t paged_decode_attn_workspace(int B, int Hq, int D, int num_splits);
  * finite scales >= 0, powers of two or not):
  *   out[b][h] = sum_j softmax_j(scale * q[b][h] . k_j) v_j
  * Keys, rows without keys, windows, GQA, table errors and argument limits are
- * paged_decode_attn's; q must be finite. Values at positions outside a row's
- * keys are never used (codes there may be NaN, scales anything). Scores,
- * softmax statistics and outputs are accumulated in fp32; the weights
- * p_j * v_scale_j enter the product with V as fp16, relative to the row's
- * largest.
+ * paged_decode_attn's, with Hkv <= 65535; q must be finite and the scores
+ * within fp32's range. Values at positions outside a row's keys are never
+ * used (codes there may be NaN, scales anything). Scores, softmax statistics
+ * and outputs are accumulated in fp32; the weights p_j * v_scale_j enter the
+ * product with V as fp16, relative to the row's largest.
  * The work is cut over the GPU as in the automatic mode. The workspace must
  * hold paged_decode_attn_q8_workspace(Hq, Hkv, D) bytes (16-byte aligned),
  * whatever the batch and the lengths; zero it once before its first use.
  * Every call leaves it zero again, except one that reports PKV_ERR_TIMEOUT,
- * after which it must be zeroed again. Calls sharing one workspace must not overlap on the GPU.
+ * after which it must be zeroed again. Calls sharing one workspace must not
+ * overlap on the GPU.
  * ------------------------------------------------------------------- */
 int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache,
                          const pkv_e4m3 *v_cache, const float *k_scale,

@@ -123,8 +123,8 @@ extern "C" int kv_copy_pages(void *const *caches, const int *heads, const int64_
                              void *stream) {
   if (n_caches < 0 || n_pairs < 0 || n_pages < 1)
     return pkv::fail(PKV_E_BAD_ARG, "kv_copy_pages: bad size argument");
-  if (n_caches == 0 || n_pairs == 0) return pkv::ok();
-  if (!caches || !heads || !page_bytes || !pairs)
+  if (n_caches == 0) return pkv::ok();
+  if (!caches || !heads || !page_bytes || (n_pairs > 0 && !pairs))
     return pkv::fail(PKV_E_BAD_ARG, "kv_copy_pages: NULL pointer");
   for (int c = 0; c < n_caches; ++c) {
     if (!caches[c]) return pkv::fail(PKV_E_BAD_ARG, "kv_copy_pages: NULL cache");
@@ -132,6 +132,7 @@ extern "C" int kv_copy_pages(void *const *caches, const int *heads, const int64_
         page_bytes[c] > (1LL << 31) || page_bytes[c] >= (1LL << 46) / n_pages / heads[c])
       return pkv::fail(PKV_E_BAD_ARG, "kv_copy_pages: cache %d: bad heads or page_bytes", c);
   }
+  if (n_pairs == 0) return pkv::ok();
   std::vector<unsigned char> role;   // 1: a source, 2: a destination
   try {
     role.assign(n_pages, 0);

@@ -21,8 +21,8 @@ import dataclasses
 import numpy as np
 import torch
 
-from . import (NoPagesError, NoSlotError, PageTable, kv_append, kv_append_q8, kv_copy_pages, paged_decode_attn,
-               paged_decode_attn_q8, paged_decode_attn_q8_workspace, paged_decode_attn_splits,
+from . import (NoPagesError, NoSlotError, PageTable, kv_append, kv_append_q8, kv_copy_pages,
+               paged_decode_attn, paged_decode_attn_q8, paged_decode_attn_q8_workspace, paged_decode_attn_splits,
                paged_decode_attn_workspace, paged_decode_step, paged_decode_step_ex,
                qk_norm_rope, qkv_norm_rope)
 
@@ -324,6 +324,8 @@ class ContinuousBatcher:
         new sequences."""
         if s not in self.running:
             raise ValueError(f"sequence {s.rid} is not running")
+        rids = list(rids)
+        kv_copy_pages(caches, self.pt.n_pages, [])   # refuses them before anything changes
         cached = s.total_length - 1      # the last token is appended by the next decode
         new, pairs = [], []
         for rid in rids:
@@ -349,6 +351,7 @@ class ContinuousBatcher:
 
 def compact_cache(pt: PageTable, caches, stream=None) -> int:
     """Moves the used pages to the front of the caches; returns how many moved."""
+    kv_copy_pages(caches, pt.n_pages, [])   # refuses them before anything moves
     pairs = pt.compact()
     kv_copy_pages(caches, pt.n_pages, pairs, stream=stream)
     return len(pairs)

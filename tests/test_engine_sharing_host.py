@@ -2,6 +2,7 @@
 prompt's pages, wait when nothing fits, and give every page back (host only)."""
 import numpy as np
 import pytest
+import torch
 
 pkv = pytest.importorskip("paged_kv_decode_pagetable_gb300")
 from paged_kv_decode_pagetable_gb300 import engine  # noqa: E402
@@ -77,3 +78,24 @@ def test_compact_cache_counts_moves():
     assert engine.compact_cache(pt, []) == len([p for p in range(6, 9)])
     assert sorted(pt.pages(b)) == [1, 2, 3]
     assert engine.compact_cache(pt, []) == 0
+
+
+def test_refused_caches_change_nothing():
+    """Caches that cannot be copied are refused before pages change hands."""
+    pt = pkv.PageTable(3, 4, 20, 8)
+    cb = engine.ContinuousBatcher(pt, [engine.Sequence(0, 9, 4)])
+    assert cb.step()
+    s = cb.running[0]
+    bad = torch.zeros((2, 19 * 4, 8))                 # 76 rows are not 20 pages
+    for caches in ([bad], [torch.zeros((2, 80, 8))]):   # ... and not on a CUDA device
+        with pytest.raises(pkv.BadArgError):
+            cb.fork(s, [1, 2], caches)
+        assert list(cb.running) == [s] and not cb.waiting
+        assert [pt.page_refs(p) for p in pt.pages(s.slot)] == [1, 1, 1]
+    a = pt.assign(20)
+    b = pt.assign(8)
+    pt.free(a)
+    before = pt.pages(b)
+    with pytest.raises(pkv.BadArgError):
+        engine.compact_cache(pt, [bad])
+    assert pt.pages(b) == before

@@ -234,3 +234,16 @@ def test_copy_library_refusals():
     assert call([]) == pkv.PKV_OK
     assert lib.kv_copy_pages(None, None, None, 0, 6, None, 3, None) == pkv.PKV_OK
     assert lib.kv_copy_pages(None, None, None, 1, 6, None, 3, None) == pkv.PKV_E_BAD_ARG
+
+
+def test_copy_of_no_pairs_checks_the_caches():
+    """n_pairs 0 launches nothing, but refuses what any copy of these caches would."""
+    lib = pkv.load_library()
+
+    def call(cache=1 << 20, heads=2, page_bytes=64):
+        return lib.kv_copy_pages((ctypes.c_void_p * 1)(cache), (ctypes.c_int * 1)(heads),
+                                 (ctypes.c_int64 * 1)(page_bytes), 1, 6, None, 0, None)
+
+    assert call() == pkv.PKV_OK
+    for kw in (dict(cache=0), dict(heads=0), dict(page_bytes=0)):
+        assert call(**kw) == pkv.PKV_E_BAD_ARG, kw
