@@ -1348,7 +1348,7 @@ int launch_q8(const CUtensorMap &tmK, const CUtensorMap &tmV, const Problem &p,
 }
 
 bool good_heads(int Hq, int Hkv, int D) {
-  return (D == 64 || D == 128 || D == 256 || D == 512) && Hkv >= 1 && Hq >= Hkv &&
+  return (D == 64 || D == 128 || D == 256 || D == 512) && Hkv >= 1 && Hkv <= 65535 && Hq >= Hkv &&
          Hq % Hkv == 0 && Hq / Hkv <= kMaxG;
 }
 
@@ -1375,7 +1375,7 @@ int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e
   if (D != 64 && D != 128 && D != 256 && D != 512)
     return pkv::fail(PKV_E_BAD_ARG, "%s: D must be 64, 128, 256 or 512", fn);
   if (!good_heads(Hq, Hkv, D))
-    return pkv::fail(PKV_E_BAD_ARG, "%s: need Hq %% Hkv == 0 and Hq/Hkv <= %d", fn, kMaxG);
+    return pkv::fail(PKV_E_BAD_ARG, "%s: need Hkv <= 65535, Hq %% Hkv == 0 and Hq/Hkv <= %d", fn, kMaxG);
   if (!pkv::is_pow2(page_size) || page_size < 8)
     return pkv::fail(PKV_E_BAD_ARG, "%s: page_size must be a power of two >= 8", fn);
   if (!pkv::is_pow2(scale_block) || scale_block > page_size)

@@ -150,3 +150,8 @@ def test_workspace_size(lib):
         assert 0 < a < b and a % 4 == 0
         assert b == pkv.paged_decode_attn_q8_workspace(64, 8, D)   # by the group alone
     assert lib.paged_decode_attn_q8(*{**ATTN, "B": 0}.values()) == pkv.PKV_OK
+
+
+def test_more_heads_than_a_call_takes(lib):
+    assert pkv.paged_decode_attn_q8_workspace(65535, 65535, 64) > 0
+    assert pkv.paged_decode_attn_q8_workspace(65536, 65536, 64) == 0
