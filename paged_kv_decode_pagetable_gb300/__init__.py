@@ -166,15 +166,17 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-# the current stream's handle without building a torch.cuda.Stream (about 4 us)
+# the current stream's handle without building a torch.cuda.Stream (about 4 us), and the
+# current device without torch.cuda's own look at its initialisation
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int | None:
     if stream is None:
         if torch.cuda.is_initialized():
             if _raw_stream is not None:
-                return _raw_stream(torch.cuda.current_device())
+                return _raw_stream(_raw_device())
             return torch.cuda.current_stream().cuda_stream
         return None
     if isinstance(stream, int):
@@ -182,23 +184,26 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+_E4M3, _F32, _BF16, _I32 = torch.float8_e4m3fn, torch.float32, torch.bfloat16, torch.int32
+
+
 def _bf16(t, name):
     if t is not None and not isinstance(t, int):
-        if t.dtype != torch.bfloat16 or not t.is_contiguous():
+        if t.dtype is not _BF16 or not t.is_contiguous():
             raise BadArgError(f"{name} must be a contiguous bfloat16 tensor")
     return t
 
 
 def _i32(t, name):
     if t is not None and not isinstance(t, int):
-        if t.dtype != torch.int32 or not t.is_contiguous():
+        if t.dtype is not _I32 or not t.is_contiguous():
             raise BadArgError(f"{name} must be a contiguous int32 tensor")
     return t
 
 
 def _on_device(*tensors) -> None:
     """Refuses tensors that are not on the current CUDA device (None passes)."""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    dev = _raw_device() if torch.cuda.is_initialized() else None
     for t in tensors:
         if t is not None and type(t) is not int and t.get_device() != dev:
             raise BadArgError("every tensor must be on the current CUDA device")
@@ -420,27 +425,27 @@ def kv_append_prefill(k, v, batch_idx, input_pos, dev_table, n_slots, max_pages_
         _ptr(err_word), _stream(stream)), "kv_append_prefill")
 
 
-_E4M3 = torch.float8_e4m3fn
-
-
-def _q8_cache(k_cache, v_cache, k_scale, v_scale, n_rows: int) -> int:
-    """Checks an 8-bit cache's tensors; returns the tokens that share a scale."""
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype is not _E4M3 or not t.is_contiguous() or t.dim() != 3:
+def _q8_cache(k_cache, v_cache, k_scale, v_scale, n_rows: int) -> tuple:
+    """Checks an 8-bit cache's tensors; returns the kv heads, the head dim and the
+    tokens that share a scale."""
+    shape, v_shape, scales, v_scales = (k_cache.shape, v_cache.shape, k_scale.shape,
+                                        v_scale.shape)
+    for t, size, name in ((k_cache, shape, "k_cache"), (v_cache, v_shape, "v_cache")):
+        if t.dtype is not _E4M3 or len(size) != 3 or not t.is_contiguous():
             raise BadArgError(f"{name} must be a contiguous float8_e4m3fn tensor "
                               "[Hkv][n_pages * page_size][D]")
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t.dtype is not torch.float32 or not t.is_contiguous() or t.dim() != 2:
+    for t, size, name in ((k_scale, scales, "k_scale"), (v_scale, v_scales, "v_scale")):
+        if t.dtype is not _F32 or len(size) != 2 or not t.is_contiguous():
             raise BadArgError(f"{name} must be a contiguous float32 tensor "
                               "[Hkv][n_pages * page_size / scale_block]")
-    shape, scales = k_cache.shape, k_scale.shape
-    if v_cache.shape != shape or shape[1] != n_rows:
+    Hkv, rows, D = shape
+    if v_shape != shape or rows != n_rows:
         raise BadArgError("k_cache and v_cache must both hold n_pages * page_size rows")
-    n = scales[1]
-    if v_scale.shape != scales or scales[0] != shape[0] or n < 1 or n_rows % n:
+    heads, n = scales
+    if v_scales != scales or heads != Hkv or n < 1 or n_rows % n:
         raise BadArgError("k_scale and v_scale must both be [Hkv][n_pages * page_size / "
                           "scale_block]")
-    return n_rows // n
+    return Hkv, D, n_rows // n
 
 
 def _append_q8(name, head_major, k, v, batch_idx, input_pos, dev_table, n_slots,
@@ -448,14 +453,15 @@ def _append_q8(name, head_major, k, v, batch_idx, input_pos, dev_table, n_slots,
                err_word, stream) -> None:
     _bf16(k, "k"), _bf16(v, "v")
     _i32(batch_idx, "batch_idx"), _i32(input_pos, "input_pos"), _i32(dev_table, "dev_table")
-    block = _q8_cache(k_cache, v_cache, k_scale, v_scale, n_pages * page_size)
-    if k.dim() != 3 or v.shape != k.shape:
+    Hkv, D, block = _q8_cache(k_cache, v_cache, k_scale, v_scale, n_pages * page_size)
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape:
         raise BadArgError(f"{name}: k and v must have one shape of three dimensions")
     if head_major:
-        Hkv, N, D = k.shape
+        heads, N, width = shape
     else:
-        N, Hkv, D = k.shape
-    if Hkv != k_cache.shape[0] or D != k_cache.shape[2]:
+        N, heads, width = shape
+    if heads != Hkv or width != D:
         raise BadArgError(f"{name}: k, v and the caches differ in heads or head dim")
     if input_pos is None or input_pos.numel() < N or (
             batch_idx is not None and batch_idx.numel() < N):
@@ -596,10 +602,10 @@ def paged_decode_attn_q8(q, k_cache, v_cache, k_scale, v_scale, dev_table, n_slo
     zeroed byte tensor of paged_decode_attn_q8_workspace(Hq, Hkv, D)."""
     _bf16(q, "q"), _bf16(out, "out")
     _i32(dev_table, "dev_table"), _i32(batch_idx, "batch_idx"), _i32(seq_lens, "seq_lens")
-    block = _q8_cache(k_cache, v_cache, k_scale, v_scale, n_pages * page_size)
-    B, Hq, D = q.shape
-    Hkv = k_cache.shape[0]
-    if D != k_cache.shape[2] or out.shape != q.shape:
+    Hkv, D, block = _q8_cache(k_cache, v_cache, k_scale, v_scale, n_pages * page_size)
+    shape = q.shape
+    B, Hq, width = shape
+    if width != D or out.shape != shape:
         raise BadArgError("paged_decode_attn_q8: q, out and the caches differ in shape")
     if seq_lens is None or seq_lens.numel() < B or (
             batch_idx is not None and batch_idx.numel() < B):
