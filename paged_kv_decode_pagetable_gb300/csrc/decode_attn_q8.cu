@@ -3,7 +3,15 @@
 //
 //   s_j = scale * sk_j * (q . ck_j),  out = sum_j softmax(s)_j sv_j cv_j
 //
-// Bound by reading the codes and scales of every key once. Design (GB300):
+// Bound by reading the codes and scales of every key once. Measured against the measured
+// 6789 GB/s: 16 rows of 16k to 32k tokens (8 heads of 128, blocks of 16) 122.6 us, 0.97;
+// 256 rows of 500 to 1500 tokens 88 us, 0.89; 64 rows of 100 to 1024 tokens 18.8 us, 0.59;
+// the same with 512-wide heads (one of them, blocks of 64) 25.2 us, 0.45; one row of 32k
+// tokens 19.8 us, 0.50; 64-wide heads, 16 rows of 8k to 16k tokens 51 us, 0.58. Without
+// its arithmetic the kernel takes 16.5, 22.6 and 40 us for the 64 rows, the 512-wide and
+// the 64-wide ones: what small calls cost beyond their bytes is the start (launch, row
+// set-up, page lookups, the first tiles' latency: about 5 us) and the joins (2 to 5 us).
+// Design (GB300):
 //   * work: the 64-key tiles of every (row, kv head), plus START positions for each
 //     start of a (row, head), laid on one line from the actual lengths; every
 //     persistent CTA takes an equal share of it. A (row, head) that straddles
@@ -11,8 +19,9 @@
 //     head)'s first, and that part is its first work, so the workspace is one fp32
 //     record a CTA. Each word of a record is the complement of the value's bits, so
 //     a zero word is one not yet written: who takes a part in polls the words
-//     themselves (no flag, no fence) and clears them. Parts are joined in a tree of eights (part j takes in
-//     j + 1 .. j + 7, then j + 8 ..) in a fixed order: results do not depend on
+//     themselves (no flag, no fence) and clears them. Parts are joined in a tree of
+//     eights (part j takes in j + 1 .. j + 7, then j + 8 ..; a tree of sixteens: one
+//     row of 32k tokens 19.9 -> 22.9 us) in a fixed order: results do not depend on
 //     timing. A first part is its CTA's last work, and a part that takes in others
 //     but is not first its CTA's only work, so they find the others written, or
 //     wait for CTAs launched after them that began with that very work;
@@ -23,14 +32,18 @@
 //   * a consumer warp owns 16 keys of every tile (D >= 256) or 32 keys of every
 //     other tile (two teams of two warps: twice the independent work between two
 //     steps of the softmax) and keeps its own online softmax over the whole unit, so
-//     no tile needs a barrier between warps. At a
-//     unit's end it leaves its state in shared memory and goes on; a joining warp
-//     adds the four states and writes the output or the partial. A part that takes
-//     others in is its CTA's last work: there the consumer warps themselves add
-//     everything up, all loads of the other parts in flight at once. Keys are the M rows of
-//     S^T = K q^T and head-dim is the M rows of O^T = V^T P^T (mma.sync m16n8k16,
-//     fp16 in, fp32 out), the <= 8 query heads of the group are N; P goes from
-//     one product to the other through movmatrix;
+//     no tile needs a barrier between warps. At a unit's end it leaves its state in
+//     shared memory and goes on; a joining warp adds the four states and writes the
+//     output or the partial. A part that takes others in is its CTA's last work: there
+//     the consumer warps themselves add everything up, the loads of several parts in
+//     flight at once;
+//   * keys are the M rows of S^T = K q^T and head-dim is the M rows of O^T = V^T P^T
+//     (mma.sync m16n8k16, fp16 in, fp32 out), the <= 8 query heads of the group are N;
+//     P goes from one product to the other through movmatrix. The products are 4 G
+//     FLOP a code byte and busy the tensor pipe about a tenth of the time, so
+//     tcgen05.mma has no rate to add: its operands come from shared memory, where the
+//     codes would have to be written back as fp16 first (with q and P in e4m3 instead,
+//     the result would lose most of q's and P's bits);
 //   * codes become fp16 in registers (exact). q is scaled by a power of two to
 //     its row's largest magnitude, so it is exact in fp16 too (elements below
 //     2^-14 of the largest lose at most 2^-25 of it). The scale of v is part of
@@ -70,12 +83,18 @@ constexpr int kMergeRow = kMergeCols + 4;   // padded: conflict-free 8-byte stor
 
 template <int D>
 struct Cfg {
+  // One CTA per SM, at the same shared memory a CTA: D = 128 rollout batch 18.8 -> 24.8 us, 16
+  // long rows 124 -> 168; D = 256 mixed (16 rows of 8k to 16k tokens 40.4 -> 43.0, 64 rows of
+  // 256 to 2048 16.5 -> 15.3, sliding 11.8 -> 12.1); D = 512 has room for one. Three at
+  // D = 64: 16 rows of 8k to 16k tokens 51.5 -> 49.2, one short row 3.62 -> 3.70.
   static constexpr int CTAS_PER_SM = D <= 256 ? 2 : 1;
   // What starting a (row, head) costs, in tiles (a unit's state, its query and the part
   // of its last tile not used). Rollout batch, D = 128: 1 21.6 us, 2 19.9, 3 19.7, 4 20.1;
   // D = 512: 25.9, 24.8, 25.9, 26.0.
   static constexpr int START = D <= 256 ? 3 : 2;
-  static constexpr int MB = D <= 128 ? 2 : 1;      // 16-key blocks of a tile a warp owns
+  // 16-key blocks of a tile a warp owns. D = 128: 1 rollout batch 20.3 us, 256 rows 95.2;
+  // 2 18.8, 89.1; 4 22.2, 94.9. D = 256: 1 and 2 alike (sliding 11.8, 12.1).
+  static constexpr int MB = D <= 128 ? 2 : 1;
   static constexpr int TEAM = kT / 16 / MB;        // warps that share a tile
   static constexpr int TEAMS = kCWarps / TEAM;
   // Ring entries, one K or V tile each. An entry always belongs to the same team: a
@@ -92,12 +111,11 @@ struct Cfg {
   static constexpr int Q_STAGE = kMaxG * Q_ROW;
   static constexpr int OFF_Q = NS * TILE_BYTES;
   static constexpr int OFF_SCALE = OFF_Q + 2 * Q_STAGE;      // [2][2][kScaleWords] f32
-  // states handed over: [MS] slots of [4 warps][8 heads] rows, then M [4][8], then m and l
-  // of every lane, [4 warps][8 lanes][8 heads] each
-  static constexpr int MS = 1;
-  static constexpr int MERGE_SLOT = (kCWarps * kMaxG * kMergeRow + 17 * kCWarps * kMaxG) * 4;
+  // states handed over: [4 warps][8 heads] rows, then M [4][8], then m and l of every
+  // lane, [4 warps][8 lanes][8 heads] each
+  static constexpr int MERGE_BYTES = (kCWarps * kMaxG * kMergeRow + 17 * kCWarps * kMaxG) * 4;
   static constexpr int OFF_MERGE = OFF_SCALE + 4 * kScaleWords * 4;
-  static constexpr int OFF_QS = OFF_MERGE + MS * MERGE_SLOT;                    // [2][8] f32
+  static constexpr int OFF_QS = OFF_MERGE + MERGE_BYTES;   // [2][8] f32
   // weights of the states added up: the warps' and the parts' taken in
   static constexpr int OFF_SRC = OFF_QS + 2 * kMaxG * 4;   // [4 + kMaxSources][8] f32
   static constexpr int OFF_BAR = OFF_SRC + (4 + kMaxSources) * kMaxG * 4;
@@ -106,7 +124,7 @@ struct Cfg {
   static constexpr int DUMP_ROW = D + 4;
   static constexpr int DUMP_STATS = kCWarps * kMaxG * DUMP_ROW;
   static_assert((DUMP_STATS + 3 * kCWarps * kMaxG) * 4 <= NS * TILE_BYTES, "states fit the ring");
-  static constexpr int N_BARS = 2 * NS + 10 + 2 * MS;
+  static constexpr int N_BARS = 2 * NS + 12;
   static constexpr int OFF_TILE = OFF_BAR + N_BARS * 8;   // [NS] u32: box mask, row offset
   static constexpr int OFF_MISC = OFF_TILE + NS * 4;      // abort flag
   static constexpr int OFF_DESC = (OFF_MISC + 8 + 15) & ~15;       // Unit [2]
@@ -526,11 +544,9 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
     float f = 0.f, last = 0.f, m = 0.f, l = 0.f, M = 0.f;
 #pragma unroll 1
     for (int r = 0; r < ROUNDS; ++r, ++it_m) {
-      const int ms = it_m % Cf::MS;
-      bool ok = mbar_wait(fullM + 8 * ms, (it_m / Cf::MS) & 1, abort_flag);
+      bool ok = mbar_wait(fullM, it_m & 1, abort_flag);
       ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-      const float *merge =
-          reinterpret_cast<const float *>(sm + Cf::OFF_MERGE + ms * Cf::MERGE_SLOT);
+      const float *merge = reinterpret_cast<const float *>(sm + Cf::OFF_MERGE);
       if (r == 0) {
         const float *a = merge + kCWarps * kMaxG * kMergeRow;
         const float own_M = a[lane];
@@ -580,7 +596,7 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
         st_word(a + 2, part_word(M));
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(emptyM + 8 * ms);
+      if (lane == 0) mbar_arrive(emptyM);
     }
   }
 }
@@ -753,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
   const uint32_t s0 = smem_u32(sm);
   const uint32_t full = s0 + Cf::OFF_BAR, empty = full + 8 * Cf::NS,
                  fullQ = empty + 8 * Cf::NS, emptyQ = fullQ + 16, fullM = emptyQ + 16,
-                 emptyM = fullM + 8 * Cf::MS, fullS = emptyM + 8 * Cf::MS, emptyS = fullS + 16,
+                 emptyM = fullM + 8, fullS = emptyM + 8, emptyS = fullS + 16,
                  readyQ = emptyS + 16;
   uint32_t *tile_word = reinterpret_cast<uint32_t *>(sm + Cf::OFF_TILE);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OFF_MISC);
@@ -976,12 +992,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
 
   if (warp == kCWarps + 1) {   // a lane sets up an mbarrier
     for (int i = lane; i < Cf::N_BARS; i += 32) {
-      constexpr int Q0 = 2 * Cf::NS, M0 = Q0 + 4, S0 = M0 + 2 * Cf::MS;
+      constexpr int Q0 = 2 * Cf::NS, M0 = Q0 + 4, S0 = M0 + 2;
       const int count = i < Cf::NS        ? 1              // full
                         : i < Q0          ? Cf::TEAM       // empty
                         : i < Q0 + 2      ? 1              // fullQ
                         : i < M0          ? kCWarps + 1    // emptyQ: the joining warp reads too
-                        : i < M0 + Cf::MS ? kCWarps        // fullM
+                        : i < M0 + 1      ? kCWarps        // fullM
                         : i < S0          ? 1              // emptyM
                         : i < S0 + 2      ? 32             // fullS
                         : i < S0 + 4      ? kCWarps        // emptyS
@@ -1259,9 +1275,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     constexpr int COLS = D < kMergeCols ? D : kMergeCols;
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += COLS, ++it_m) {
-      const int ms = it_m % Cf::MS;
-      if (!mbar_wait(emptyM + 8 * ms, ((it_m / Cf::MS) & 1) ^ 1, abort_flag)) give_up();
-      float *merge = reinterpret_cast<float *>(sm + Cf::OFF_MERGE + ms * Cf::MERGE_SLOT);
+      if (!mbar_wait(emptyM, (it_m & 1) ^ 1, abort_flag)) give_up();
+      float *merge = reinterpret_cast<float *>(sm + Cf::OFF_MERGE);
 #pragma unroll
       for (int u = 0; u < COLS / 16; ++u) {
         const float(&f)[4] = o[c0 / 16 + u];
@@ -1277,7 +1292,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
         *reinterpret_cast<float2 *>(st + 256) = make_float2(l0, l1);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(fullM + 8 * ms);
+      if (lane == 0) mbar_arrive(fullM);
     }
   }
 }
@@ -1375,7 +1390,8 @@ int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e
   if (D != 64 && D != 128 && D != 256 && D != 512)
     return pkv::fail(PKV_E_BAD_ARG, "%s: D must be 64, 128, 256 or 512", fn);
   if (!good_heads(Hq, Hkv, D))
-    return pkv::fail(PKV_E_BAD_ARG, "%s: need Hkv <= 65535, Hq %% Hkv == 0 and Hq/Hkv <= %d", fn, kMaxG);
+    return pkv::fail(PKV_E_BAD_ARG, "%s: need Hkv <= 65535, Hq %% Hkv == 0 and Hq/Hkv <= %d", fn,
+                     kMaxG);
   if (!pkv::is_pow2(page_size) || page_size < 8)
     return pkv::fail(PKV_E_BAD_ARG, "%s: page_size must be a power of two >= 8", fn);
   if (!pkv::is_pow2(scale_block) || scale_block > page_size)
@@ -1397,7 +1413,8 @@ int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e
       !pkv::aligned16(v_cache))
     return pkv::fail(PKV_E_BAD_ARG, "%s: tensors must be 16-byte aligned", fn);
   {
-    const long long row_tiles = (1LL * max_pages_per_seq * page_size + kT - 1) / kT + 1 + Cfg<64>::START;
+    const long long row_tiles =
+        (1LL * max_pages_per_seq * page_size + kT - 1) / kT + 1 + Cfg<64>::START;
     if (1LL * B * Hkv * row_tiles >= (1LL << 31))
       return pkv::fail(PKV_E_BAD_ARG, "%s: B * Hkv * tiles per row too large", fn);
   }
@@ -1436,7 +1453,8 @@ int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
   p.scale_log2 = scale * 1.4426950408889634f;
-  // four scales at once where the rows of one copy have as many, 16-byte aligned
+  // four scales at once where the rows of one copy have as many, 16-byte aligned (217 short
+  // rows with a scale a token 19.6 us, word by word 21.3)
   p.scale_vec = box_rows / scale_block >= 4 && pkv::aligned16(k_scale) && pkv::aligned16(v_scale)
                     ? 4 : 1;
   p.o_part = static_cast<uint32_t *>(workspace);

@@ -13,7 +13,10 @@
 // size of a run), which finds the run's largest magnitude and the block's scale,
 // rescales older codes if the scale grew and writes the new ones. Extra CTAs look for
 // tokens of one block that stand apart. Bound by reading k and v and writing half their
-// bytes.
+// bytes: 16411 tokens of 16 prompts (8 heads of 128, blocks of 16; 101 MB) take 22.0 us,
+// 0.67 of the measured 6789 GB/s (an elementwise copy of as many bytes: 16.1 us; the warps
+// issue in 44% of the cycles and wait for loads in most others), a decode step of 8 rows
+// 2.8 us, one of 512 rows 5.2 us, both the latency of index, table, token and store.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -388,9 +391,22 @@ int launch_append_q8(const char *fn, const pkv_bf16 *k, const pkv_bf16 *v,
   a.err = err_word;
   // A run's expected units of 16 values: a block's tokens in a prompt, one token else.
   const long long run = 1LL * (head_major ? scale_block : 1) * D / 16;
-  // One token of K or V a warp while those warps fit the GPU twice over (a decode
-  // step), else windows of 16 tokens (a block's, for a CTA a run); two units of a run a lane, or a CTA for a run of
-  // 8 units a lane of a warp and more.
+  // Measured, in us (16411 tokens of 8 heads of 128 in blocks of 16 / 64 / 1; 200003 tokens
+  // of one head of 64 in blocks of 16; 8200 tokens of 2 heads of 512 in blocks of 16):
+  // - few: one token of K or V a warp while the GPU holds all those warps at once, for the
+  //   shortest latency. 8 and 512 rows: 2.8 and 5.2, without it 4.3 and 11.9; used for all
+  //   calls 95 / 112 / 207, 162, 30 instead of the below; up to four times the warps: 30
+  //   instead of 12.6 for the last.
+  // - whole_cta: a CTA a run of 8 units a lane of a warp and more. 25.8 (blocks of 64) and
+  //   12.6 (512 wide); never: 35.9 and 32.5; from half that size on: 49 instead of 22.0
+  //   for the first.
+  // - window: 16 tokens 22.0 / - / 29.3, 22.3; 8: 22.6 / - / 31.5, 30.7; 31: 23.3 / - /
+  //   33.8, 23.9. A CTA takes a block's tokens: 25.8 for 64; 16 of them: 33.5.
+  // - tensors: K and V one after the other, which share what is looked up: 22.0 / - / 29.3,
+  //   22.3; a warp each: 23.9 / - / 35.3, 28.0. (A CTA or a lone token: one, for more warps.)
+  // - group: two units of a run a lane, four lanes at least: 29.3 (blocks of 1); one unit
+  //   a lane 41; always a whole warp 119.
+  // - KEEP: room for two units where a run fits that: 29.3 and 22.3, for four 30.3 and 23.0.
   const bool few = 2LL * N * Hkv <= 64LL * sms;
   const bool whole_cta = !few && run >= 256;
   a.window = few ? 1 : whole_cta && scale_block > 16 ? scale_block : 16;
