@@ -6,8 +6,8 @@
 // Bound by reading the codes and scales of every key once. Measured against the measured
 // 6789 GB/s: 16 rows of 16k to 32k tokens (8 heads of 128, blocks of 16) 122.6 us, 0.97;
 // 256 rows of 500 to 1500 tokens 88 us, 0.89; 64 rows of 100 to 1024 tokens 18.8 us, 0.59;
-// the same with 512-wide heads (one of them, blocks of 64) 25.2 us, 0.45; one row of 32k
-// tokens 19.8 us, 0.50; 64-wide heads, 16 rows of 8k to 16k tokens 51 us, 0.58. Without
+// the same with 512-wide heads (one of them, blocks of 64) 25.0 us, 0.45; one row of 32k
+// tokens 19.0 us, 0.52; 64-wide heads, 16 rows of 8k to 16k tokens 50 us, 0.60. Without
 // its arithmetic the kernel takes 16.5, 22.6 and 40 us for the 64 rows, the 512-wide and
 // the 64-wide ones: what small calls cost beyond their bytes is the start (launch, row
 // set-up, page lookups, the first tiles' latency: about 5 us) and the joins (2 to 5 us).
@@ -34,9 +34,10 @@
 //     steps of the softmax) and keeps its own online softmax over the whole unit, so
 //     no tile needs a barrier between warps. At a unit's end it leaves its state in
 //     shared memory and goes on; a joining warp adds the four states and writes the
-//     output or the partial. A part that takes others in is its CTA's last work: there
-//     the consumer warps themselves add everything up, the loads of several parts in
-//     flight at once;
+//     output or the partial. A part that is its CTA's last work, as every part that takes
+//     others in is, is added up by the consumer warps themselves, the loads of several
+//     parts in flight at once (last parts that take none in, too: sliding 11.8 -> 11.2 us,
+//     B = 8 9.5 -> 9.2; whole rows stay with the joining warp: one short row 3.5, not 4.0);
 //   * keys are the M rows of S^T = K q^T and head-dim is the M rows of O^T = V^T P^T
 //     (mma.sync m16n8k16, fp16 in, fp32 out), the <= 8 query heads of the group are N;
 //     P goes from one product to the other through movmatrix. The products are 4 G
@@ -119,7 +120,7 @@ struct Cfg {
   // weights of the states added up: the warps' and the parts' taken in
   static constexpr int OFF_SRC = OFF_QS + 2 * kMaxG * 4;   // [4 + kMaxSources][8] f32
   static constexpr int OFF_BAR = OFF_SRC + (4 + kMaxSources) * kMaxG * 4;
-  // the warps' states of a part that takes others in, where the ring was:
+  // the warps' states of a part that is the CTA's last work, where the ring was:
   // [4][8][DUMP_ROW] f32, then m, l, M [4][8] each
   static constexpr int DUMP_ROW = D + 4;
   static constexpr int DUMP_STATS = kCWarps * kMaxG * DUMP_ROW;
@@ -359,6 +360,7 @@ struct Line {
 // `parts`; b < 0: no more work.
 struct alignas(16) Unit {
   int b, g, slot, ta, tb, k0, k1, part, parts, first_cta;
+  int last;   // the CTA's last work
 };
 static_assert(sizeof(Unit) <= 48, "unit descriptor slot");
 
@@ -397,6 +399,7 @@ __device__ __forceinline__ bool next_unit(const Problem &p, const int *slots, co
     w.first_cta = p.Hkv * pre[b] + g * width;
     w.parts = width;
     w.part = (r <= START ? 1 : 0) | (r + n == width ? 2 : 0);
+    w.last = end - x <= START;   // no room for a tile of another (row, head)
     return true;
   }
   return false;
@@ -462,9 +465,9 @@ __device__ __forceinline__ uint32_t sources(const Unit &w, int lane, int &cta) {
   cta = w.first_cta + (t ? j : 0);
   return __ballot_sync(0xffffffffu, t);
 }
-__device__ __forceinline__ bool takes_others(const Unit &w) {
-  return w.part % kFan == 0 && w.part + 1 < w.parts;
-}
+// Whether the consumer warps join a unit themselves. (A part that takes others in goes on
+// in the next CTA, so it is the last.)
+__device__ __forceinline__ bool joined_by_all(const Unit &w) { return w.last && w.parts > 1; }
 // What a sum of outputs relative to M is multiplied by: 1 for a partial, else
 // 2^(M - m) / l (no key of weight, or no key: 0; a NaN stays one).
 __device__ __forceinline__ float last_factor(bool partial, float m, float l, float M) {
@@ -478,7 +481,7 @@ __device__ __forceinline__ uint2 pack4_bf16(const float4 &v, float f) {
 }
 
 // The joining warp: adds up the states of the four consumer warps at the end of every
-// unit that takes no others in. Lanes are (warp, head) for the statistics and (head,
+// unit that they do not join themselves. Lanes are (warp, head) for the statistics and (head,
 // four columns) for the outputs. Rolled loops: what runs once or twice a CTA takes the
 // time of fetching its instructions.
 template <int D>
@@ -539,7 +542,7 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
     w = next;
     if (w.b < 0) return;
     receive(next);
-    if (takes_others(w)) continue;
+    if (joined_by_all(w)) continue;
     const bool partial = w.part > 0;
     float f = 0.f, last = 0.f, m = 0.f, l = 0.f, M = 0.f;
 #pragma unroll 1
@@ -601,10 +604,10 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
   }
 }
 
-// The end of a part that takes others in, by the consumer warps, whose states lie where
+// The end of a part that is the CTA's last work, by the consumer warps, whose states lie where
 // the ring was: warp 0 gathers the statistics and weighs the states, then every thread
-// adds up four columns of a head at a time.
-template <int D>
+// adds up IB places (four columns of a head) at once, of SRC parts.
+template <int D, int IB, int SRC>
 __device__ __forceinline__ void join_parts(const Problem &p, uint8_t *sm, const Unit &w,
                                            volatile int *abort_flag, int warp, int lane) {
   using Cf = Cfg<D>;
@@ -616,14 +619,13 @@ __device__ __forceinline__ void join_parts(const Problem &p, uint8_t *sm, const 
   const int n_src = 32 - __clz(takes);
   const bool partial = w.part > 0;
   bool bad = false;
-  constexpr int IB = D <= 128 ? 2 : 4;   // places (four columns of a head) at once, of four parts
   const int places = p.G * D / 4;
-  uint32_t *a[4];
-  uint4 v[4][IB];
-  // sources k0 .. k0 + 3 at places i0 + i * kCThreads: what there is to wait for
+  uint32_t *a[SRC];
+  uint4 v[SRC][IB];
+  // sources k0 .. k0 + SRC - 1 at places i0 + i * kCThreads: what there is to wait for
   auto start_loads = [&](int i0, int k0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < SRC; ++j) {
       const int cta = __shfl_sync(0xffffffffu, my_cta, k0 + j);
       a[j] = p.o_part + static_cast<size_t>(cta) * p.G * D + 4 * i0;
 #pragma unroll
@@ -709,12 +711,12 @@ __device__ __forceinline__ void join_parts(const Problem &p, uint8_t *sm, const 
                                                at % (D / 4) * 4));
     }
 #pragma unroll 1
-    for (int k0 = 0; k0 < n_src; k0 += 4) {
+    for (int k0 = 0; k0 < n_src; k0 += SRC) {
       if (i0 != tid || k0 != 0) start_loads(i0, k0);
       for (int n = 0;; ++n) {
         bool there = true;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < SRC; ++j)
 #pragma unroll
           for (int i = 0; i < IB; ++i) there = there && written(v[j][i]);
         if (there) break;
@@ -723,14 +725,14 @@ __device__ __forceinline__ void join_parts(const Problem &p, uint8_t *sm, const 
           break;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < SRC; ++j)
 #pragma unroll
           for (int i = 0; i < IB; ++i)
             if (!written(v[j][i])) v[j][i] = ld_words(a[j] + 4 * i * kCThreads);
       }
       __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < SRC; ++j)
 #pragma unroll
         for (int i = 0; i < IB; ++i)
           if ((takes >> (k0 + j) & 1u) && i0 + i * kCThreads < places) {
@@ -1240,7 +1242,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     }
 
     // ---- the unit's end ----
-    if (takes_others(w)) {   // the CTA's last work: the ring is free once all are here
+    if (joined_by_all(w)) {   // the ring is free once all are here
       (void)consumer_sync_or(false);
       float *dump = reinterpret_cast<float *>(sm);
 #pragma unroll
@@ -1269,7 +1271,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
         *reinterpret_cast<float2 *>(st + 64) = make_float2(M0, M1);
       }
       (void)consumer_sync_or(false);
-      join_parts<D>(p, sm, w, abort_flag, warp, lane);
+      // As many places as 8 heads have (D = 512 at once instead of half of them: 17.2 ->
+      // 15.7 us for 10 rows of 1000 tokens), and as many parts as registers allow. Up to
+      // 4 heads have half the places: at D = 128 one place of 8 parts instead of two of 4
+      // (B = 8 9.1 -> 8.6 us, one row of 32k tokens 19.6 -> 19.0); at D = 512 no gain.
+      constexpr int IB = D / 64, SRC = D <= 128 ? 8 / IB : D == 256 ? 4 : 2;
+      bool done = false;
+      if constexpr (D == 128) {
+        done = p.G <= kMaxG / 2;
+        if (done) join_parts<D, 1, 8>(p, sm, w, abort_flag, warp, lane);
+      }
+      if (!done) join_parts<D, IB, SRC>(p, sm, w, abort_flag, warp, lane);
       continue;
     }
     constexpr int COLS = D < kMergeCols ? D : kMergeCols;
