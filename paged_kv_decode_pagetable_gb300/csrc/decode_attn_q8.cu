@@ -6,10 +6,9 @@
 // Bound by reading the codes and scales of every key once. Measured against the measured
 // 6789 GB/s: 16 rows of 16k to 32k tokens (8 heads of 128, blocks of 16) 122.6 us, 0.97;
 // 256 rows of 500 to 1500 tokens 88 us, 0.89; 64 rows of 100 to 1024 tokens 18.8 us, 0.59;
-// the same with 512-wide heads (one of them, blocks of 64) 25.0 us, 0.45; one row of 32k
+// the same with 512-wide heads (one of them, blocks of 64) 23.4 us, 0.48; one row of 32k
 // tokens 19.0 us, 0.52; 64-wide heads, 16 rows of 8k to 16k tokens 50 us, 0.60. Without
-// its arithmetic the kernel takes 16.5, 22.6 and 40 us for the 64 rows, the 512-wide and
-// the 64-wide ones: what small calls cost beyond their bytes is the start (launch, row
+// its arithmetic the kernel takes 16.5 and 40 us for the 64 rows and the 64-wide ones: what small calls cost beyond their bytes is the start (launch, row
 // set-up, page lookups, the first tiles' latency: about 5 us) and the joins (2 to 5 us).
 // Design (GB300):
 //   * work: the 64-key tiles of every (row, kv head), plus START positions for each
@@ -37,7 +36,8 @@
 //     output or the partial. A part that is its CTA's last work, as every part that takes
 //     others in is, is added up by the consumer warps themselves, the loads of several
 //     parts in flight at once (last parts that take none in, too: sliding 11.8 -> 11.2 us,
-//     B = 8 9.5 -> 9.2; whole rows stay with the joining warp: one short row 3.5, not 4.0);
+//     B = 8 9.5 -> 9.2; whole rows stay with the joining warp: one short row 3.5, not 4.0).
+//     At D = 512 the consumer warps join every unit;
 //   * keys are the M rows of S^T = K q^T and head-dim is the M rows of O^T = V^T P^T
 //     (mma.sync m16n8k16, fp16 in, fp32 out), the <= 8 query heads of the group are N;
 //     P goes from one product to the other through movmatrix. The products are 4 G
@@ -91,8 +91,8 @@ struct Cfg {
   static constexpr int CTAS_PER_SM = D <= 256 ? 2 : 1;
   // What starting a (row, head) costs, in tiles (a unit's state, its query and the part
   // of its last tile not used). Rollout batch, D = 128: 1 21.6 us, 2 19.9, 3 19.7, 4 20.1;
-  // D = 512: 25.9, 24.8, 25.9, 26.0.
-  static constexpr int START = D <= 256 ? 3 : 2;
+  // 64 rows at D = 512: 1 25.0, 2 23.7, 3 23.4.
+  static constexpr int START = 3;
   // 16-key blocks of a tile a warp owns. D = 128: 1 rollout batch 20.3 us, 256 rows 95.2;
   // 2 18.8, 89.1; 4 22.2, 94.9. D = 256: 1 and 2 alike (sliding 11.8, 12.1).
   static constexpr int MB = D <= 128 ? 2 : 1;
@@ -122,13 +122,17 @@ struct Cfg {
   static constexpr int OFF_BAR = OFF_SRC + (4 + kMaxSources) * kMaxG * 4;
   // the warps' states of a part that is the CTA's last work, where the ring was:
   // [4][8][DUMP_ROW] f32, then m, l, M [4][8] each
+  // Whether the consumer warps join whole units and first works too, round by round. At
+  // D = 512 they would wait for four rounds of the joining warp, 1.2 us each: 64 rows 25.0 ->
+  // 23.7 us, 226 rows of 58 to 227 tokens 23.9 -> 19.5. At D = 256 no difference.
+  static constexpr bool SELF = D == 512;
   static constexpr int DUMP_ROW = D + 4;
   static constexpr int DUMP_STATS = kCWarps * kMaxG * DUMP_ROW;
   static_assert((DUMP_STATS + 3 * kCWarps * kMaxG) * 4 <= NS * TILE_BYTES, "states fit the ring");
   static constexpr int N_BARS = 2 * NS + 12;
   static constexpr int OFF_TILE = OFF_BAR + N_BARS * 8;   // [NS] u32: box mask, row offset
-  static constexpr int OFF_MISC = OFF_TILE + NS * 4;      // abort flag
-  static constexpr int OFF_DESC = (OFF_MISC + 8 + 15) & ~15;       // Unit [2]
+  static constexpr int OFF_MISC = OFF_TILE + NS * 4;      // abort flag, admitted units [2]
+  static constexpr int OFF_DESC = (OFF_MISC + 12 + 15) & ~15;      // Unit [2]
   static constexpr int OFF_LEN = OFF_DESC + 2 * 48;                // int [kMaxRows]
   static constexpr int OFF_SLOT = OFF_LEN + kMaxRows * 4;          // int [kMaxRows]
   static constexpr int OFF_PRE = OFF_SLOT + kMaxRows * 4;          // int [kMaxRows + 1]
@@ -211,11 +215,20 @@ __device__ __forceinline__ void fence_proxy_async() {
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *tm) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
 }
+// The consumer warps' wait for the joining warp's word on their next unit, which comes
+// within a few of its own bounded waits: the limit lies beyond them, so that all consumer
+// warps get the same word.
+__device__ __forceinline__ bool mbar_wait_word(uint32_t bar, uint32_t parity) {
+  for (int i = 0; i < 16 * kSpinLimit; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
 // All warps meet once the mbarriers are set up.
 __device__ __forceinline__ void setup_sync() {
   asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
 }
-// A barrier of the consumer threads that returns the OR of `v` over them.
+// A barrier of the consumer threads that returns the OR of `v` over them. All their warps
+// pass the same ones: they work through the units that the joining warp admits.
 __device__ __forceinline__ bool consumer_sync_or(bool v) {
   uint32_t r;
   asm volatile(
@@ -496,6 +509,7 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
   constexpr int HPS = 32 / LPH;            // heads a step
   const int hs = lane / LPH, col = lane % LPH * 4;
   int it_q = 0, it_m = 0;
+  volatile int *admitted = abort_flag + 1;
   pkv_wait_prior_grid();
   // The next unit: its query rows become fp16 in place, each scaled by a power of two
   // to its largest magnitude, before the consumer warps need them.
@@ -531,7 +545,12 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
     }
     __syncwarp();
     if (lane == 0) {
-      if (q_ok) mbar_arrive(readyQ + 8 * qs);
+      if (!q_ok) {
+        *abort_flag = 1;
+        if (p.err) atomicOr(p.err, PKV_ERR_TIMEOUT);
+      }
+      admitted[qs] = w.b >= 0;
+      mbar_arrive(readyQ + 8 * qs);   // whatever came, for the consumer warps wait for it
       if (w.b >= 0) mbar_arrive(emptyQ + 8 * qs);
     }
     ++it_q;
@@ -542,7 +561,7 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
     w = next;
     if (w.b < 0) return;
     receive(next);
-    if (joined_by_all(w)) continue;
+    if (Cf::SELF || joined_by_all(w)) continue;
     const bool partial = w.part > 0;
     float f = 0.f, last = 0.f, m = 0.f, l = 0.f, M = 0.f;
 #pragma unroll 1
@@ -1051,12 +1070,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
 
   while (true) {
     const int qs = it_q & 1;
-    const bool q_ok = mbar_wait(readyQ + 8 * qs, (it_q >> 1) & 1, abort_flag);
-    Unit w;
-    w.b = -1;
-    if (q_ok) w = udesc[qs];
-    else give_up();
-    if (__any_sync(0xffffffffu, w.b < 0)) break;
+    const bool go = mbar_wait_word(readyQ + 8 * qs, (it_q >> 1) & 1) && abort_flag[1 + qs];
+    if (!__all_sync(0xffffffffu, go)) break;
+    const Unit w = udesc[qs];
     // lane (gid, tig) holds head gid's fragments
     const uint8_t *qrow = sm + Cf::OFF_Q + qs * Cf::Q_STAGE + gid * Cf::Q_ROW + tig * 8;
     const float *qscale = reinterpret_cast<const float *>(sm + Cf::OFF_QS) + qs * kMaxG;
@@ -1242,15 +1258,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     }
 
     // ---- the unit's end ----
-    if (joined_by_all(w)) {   // the ring is free once all are here
-      (void)consumer_sync_or(false);
-      float *dump = reinterpret_cast<float *>(sm);
+    auto hand_over = [&](float *to, int c0) {   // kMergeCols columns of the warp's state
 #pragma unroll
-      for (int u = 0; u < KS; ++u) {
-        float *d = dump + (warp * kMaxG + h0) * Cf::DUMP_ROW + 16 * u + 2 * gid;
-        *reinterpret_cast<float2 *>(d) = make_float2(o[u][0], o[u][2]);
-        *reinterpret_cast<float2 *>(d + Cf::DUMP_ROW) = make_float2(o[u][1], o[u][3]);
+      for (int u = 0; u < (D < kMergeCols ? D : kMergeCols) / 16; ++u) {
+        const float(&f)[4] = o[c0 / 16 + u];
+        float *d = to + (warp * kMaxG + h0) * kMergeRow + 16 * u + 2 * gid;
+        *reinterpret_cast<float2 *>(d) = make_float2(f[0], f[2]);
+        *reinterpret_cast<float2 *>(d + kMergeRow) = make_float2(f[1], f[3]);
       }
+    };
+    auto write_stats = [&](float *to) {   // the warp's m, l and M: [3][4][8]
       float n0 = m0, n1 = m1;
 #pragma unroll
       for (int i = 4; i < 32; i <<= 1) {
@@ -1265,11 +1282,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
         l1 += __shfl_xor_sync(0xffffffffu, l1, i);
       }
       if (gid == 0) {
-        float *st = dump + Cf::DUMP_STATS + warp * kMaxG + h0;
-        *reinterpret_cast<float2 *>(st) = make_float2(n0, n1);
-        *reinterpret_cast<float2 *>(st + 32) = make_float2(l0, l1);
-        *reinterpret_cast<float2 *>(st + 64) = make_float2(M0, M1);
+        to += warp * kMaxG + h0;
+        *reinterpret_cast<float2 *>(to) = make_float2(n0, n1);
+        *reinterpret_cast<float2 *>(to + 32) = make_float2(l0, l1);
+        *reinterpret_cast<float2 *>(to + 64) = make_float2(M0, M1);
       }
+    };
+    if (joined_by_all(w)) {   // the ring is free once all are here
+      (void)consumer_sync_or(false);
+      float *dump = reinterpret_cast<float *>(sm);
+#pragma unroll
+      for (int u = 0; u < KS; ++u) {
+        float *d = dump + (warp * kMaxG + h0) * Cf::DUMP_ROW + 16 * u + 2 * gid;
+        *reinterpret_cast<float2 *>(d) = make_float2(o[u][0], o[u][2]);
+        *reinterpret_cast<float2 *>(d + Cf::DUMP_ROW) = make_float2(o[u][1], o[u][3]);
+      }
+      write_stats(dump + Cf::DUMP_STATS);
       (void)consumer_sync_or(false);
       // As many places as 8 heads have (D = 512 at once instead of half of them: 17.2 ->
       // 15.7 us for 10 rows of 1000 tokens), and as many parts as registers allow. Up to
@@ -1285,26 +1313,74 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
       continue;
     }
     constexpr int COLS = D < kMergeCols ? D : kMergeCols;
+    float *merge = reinterpret_cast<float *>(sm + Cf::OFF_MERGE);
+    if constexpr (Cf::SELF) {
+      // round by round, a thread four columns of heads warp and warp + 4
+      float f[2][kCWarps];
+      const bool partial = w.part > 0;
 #pragma unroll
-    for (int c0 = 0; c0 < D; c0 += COLS, ++it_m) {
-      if (!mbar_wait(emptyM, (it_m & 1) ^ 1, abort_flag)) give_up();
-      float *merge = reinterpret_cast<float *>(sm + Cf::OFF_MERGE);
+      for (int c0 = 0; c0 < D; c0 += COLS) {
+        hand_over(merge, c0);
+        if (c0 == 0) write_stats(merge + kCWarps * kMaxG * kMergeRow);
+        const bool bad = consumer_sync_or(*abort_flag);
 #pragma unroll
-      for (int u = 0; u < COLS / 16; ++u) {
-        const float(&f)[4] = o[c0 / 16 + u];
-        float *d = merge + (warp * kMaxG + h0) * kMergeRow + 16 * u + 2 * gid;
-        *reinterpret_cast<float2 *>(d) = make_float2(f[0], f[2]);
-        *reinterpret_cast<float2 *>(d + kMergeRow) = make_float2(f[1], f[3]);
+        for (int i = 0; i < 2; ++i) {
+          const int h = warp + 4 * i;
+          if (h >= p.G) break;
+          if (c0 == 0) {
+            const float *a = merge + kCWarps * kMaxG * kMergeRow + h;
+            float m = a[0], l = 0.f, M = a[64];
+#pragma unroll
+            for (int j = 1; j < kCWarps; ++j) {
+              m = fmaxf(m, a[8 * j]);
+              M = fmaxf(M, a[64 + 8 * j]);
+            }
+#pragma unroll
+            for (int j = 0; j < kCWarps; ++j) l += sum_at(a[32 + 8 * j], a[8 * j], m);
+            const float last = last_factor(partial, m, l, M);
+#pragma unroll
+            for (int j = 0; j < kCWarps; ++j)
+              f[i][j] = a[64 + 8 * j] == -INFINITY ? 0.f : last * ex2(a[64 + 8 * j] - M);
+            if (partial && !bad && lane == 0) {
+              uint32_t *st = p.st_part + (static_cast<size_t>(blockIdx.x) * p.G + h) * 3;
+              st_word(st, part_word(m));
+              st_word(st + 1, part_word(l));
+              st_word(st + 2, part_word(M));
+            }
+          }
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < kCWarps; ++j)
+            fma4(acc, f[i][j],
+                 *reinterpret_cast<const float4 *>(merge + (j * kMaxG + h) * kMergeRow + 4 * lane));
+          const int at = c0 + 4 * lane;
+          if (bad) continue;
+          if (partial)
+            st_words(p.o_part + (static_cast<size_t>(blockIdx.x) * p.G + h) * D + at,
+                     make_uint4(part_word(acc.x), part_word(acc.y), part_word(acc.z),
+                                part_word(acc.w)));
+          else
+            *reinterpret_cast<uint2 *>(
+                p.out + (static_cast<size_t>(w.b) * p.Hq + w.g * p.G + h) * D + at) =
+                pack4_bf16(acc, 1.f);
+        }
+        (void)consumer_sync_or(false);   // before the buffer is written again
       }
-      if (c0 == 0) {
-        float *st = merge + kCWarps * kMaxG * kMergeRow + h0;
-        if (gid == 0) *reinterpret_cast<float2 *>(st + warp * kMaxG) = make_float2(M0, M1);
-        st += 32 + (warp * 8 + gid) * kMaxG;
-        *reinterpret_cast<float2 *>(st) = make_float2(m0, m1);
-        *reinterpret_cast<float2 *>(st + 256) = make_float2(l0, l1);
+    } else {
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += COLS, ++it_m) {
+        if (!mbar_wait(emptyM, (it_m & 1) ^ 1, abort_flag)) give_up();
+        hand_over(merge, c0);
+        if (c0 == 0) {
+          float *st = merge + kCWarps * kMaxG * kMergeRow + h0;
+          if (gid == 0) *reinterpret_cast<float2 *>(st + warp * kMaxG) = make_float2(M0, M1);
+          st += 32 + (warp * 8 + gid) * kMaxG;
+          *reinterpret_cast<float2 *>(st) = make_float2(m0, m1);
+          *reinterpret_cast<float2 *>(st + 256) = make_float2(l0, l1);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(fullM);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(fullM);
     }
   }
 }
