@@ -8,8 +8,9 @@
 // 256 rows of 500 to 1500 tokens 88 us, 0.89; 64 rows of 100 to 1024 tokens 18.8 us, 0.59;
 // the same with 512-wide heads (one of them, blocks of 64) 23.4 us, 0.48; one row of 32k
 // tokens 19.0 us, 0.52; 64-wide heads, 16 rows of 8k to 16k tokens 50 us, 0.60. Without
-// its arithmetic the kernel takes 16.5 and 40 us for the 64 rows and the 64-wide ones: what small calls cost beyond their bytes is the start (launch, row
-// set-up, page lookups, the first tiles' latency: about 5 us) and the joins (2 to 5 us).
+// its arithmetic the kernel takes 16.5 and 40 us for the 64 rows and the 64-wide ones: what
+// small calls cost beyond their bytes is the start (launch, row set-up, page lookups, the
+// first tiles' latency: about 5 us) and the joins (2 to 5 us).
 // Design (GB300):
 //   * work: the 64-key tiles of every (row, kv head), plus START positions for each
 //     start of a (row, head), laid on one line from the actual lengths; every

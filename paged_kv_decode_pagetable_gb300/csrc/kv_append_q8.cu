@@ -13,10 +13,10 @@
 // size of a run), which finds the run's largest magnitude and the block's scale,
 // rescales older codes if the scale grew and writes the new ones. Extra CTAs look for
 // tokens of one block that stand apart. Bound by reading k and v and writing half their
-// bytes: 16411 tokens of 16 prompts (8 heads of 128, blocks of 16; 101 MB) take 22.0 us,
-// 0.67 of the measured 6789 GB/s (an elementwise copy of as many bytes: 16.1 us; the warps
+// bytes: 16411 tokens of 16 prompts (8 heads of 128, blocks of 16; 101 MB) take 21.2 us,
+// 0.70 of the measured 6789 GB/s (an elementwise copy of as many bytes: 16.1 us; the warps
 // issue in 44% of the cycles and wait for loads in most others), a decode step of 8 rows
-// 2.8 us, one of 512 rows 5.2 us, both the latency of index, table, token and store.
+// 2.9 us, one of 512 rows 4.7 us, both the latency of index, table, token and store.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -166,9 +166,13 @@ __device__ __forceinline__ void check_order(const Args &a) {
 }
 
 // CTA: one run at a time for the whole CTA, else for a group of lanes. KEEP: 16-value
-// units of a run that a lane keeps between the two passes.
+// units of a run that a lane keeps between the two passes. CTAs an SM, by the registers
+// left to them (us for the cases named at the launch): KEEP 2: 5 29.3 (blocks of 1), 22.3
+// (one head); 7 24.5, 19.4; 8 24.6, 19.3; 9 26.6, 20.4. KEEP 4: 4 23.7; 5 22.0; 6 21.6;
+// 7 22.6. A CTA a run: 5 25.8; 8 25.2.
 template <bool CTA, int KEEP>
-__global__ void __launch_bounds__(kWarps * 32) append_q8_kernel(const Args a) {
+__global__ void __launch_bounds__(kWarps * 32, CTA || KEEP == 2 ? 8 : 6)
+    append_q8_kernel(const Args a) {
   pkv_wait_prior_grid();
   pkv_allow_next_grid();
   if (static_cast<int>(blockIdx.x) < a.checkers) {
@@ -292,7 +296,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_q8_kernel(const Args a) {
           __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
 #pragma unroll
           for (int j = 0; j < KEEP; ++j) m2 = max_abs(max_abs(m2, keep[j].lo), keep[j].hi);
-#pragma unroll 4
+#pragma unroll 2
           for (int u = gl + gs * KEEP; u < total; u += gs) {
             const Unit y = load_unit(unit(u));
             m2 = max_abs(max_abs(m2, y.lo), y.hi);
@@ -333,7 +337,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_q8_kernel(const Args a) {
             const int u = gl + gs * j;
             if (u < total) dst[u] = quantise(keep[j], inv2);
           }
-#pragma unroll 4
+#pragma unroll 1
           for (int u = gl + gs * KEEP; u < total; u += gs)
             dst[u] = quantise(load_unit(unit(u)), inv2);
         }
@@ -394,19 +398,20 @@ int launch_append_q8(const char *fn, const pkv_bf16 *k, const pkv_bf16 *v,
   // Measured, in us (16411 tokens of 8 heads of 128 in blocks of 16 / 64 / 1; 200003 tokens
   // of one head of 64 in blocks of 16; 8200 tokens of 2 heads of 512 in blocks of 16):
   // - few: one token of K or V a warp while the GPU holds all those warps at once, for the
-  //   shortest latency. 8 and 512 rows: 2.8 and 5.2, without it 4.3 and 11.9; used for all
+  //   shortest latency. 8 and 512 rows: 2.9 and 4.7, without it 4.4 and 12.7; used for all
   //   calls 95 / 112 / 207, 162, 30 instead of the below; up to four times the warps: 30
-  //   instead of 12.6 for the last.
-  // - whole_cta: a CTA a run of 8 units a lane of a warp and more. 25.8 (blocks of 64) and
-  //   12.6 (512 wide); never: 35.9 and 32.5; from half that size on: 49 instead of 22.0
+  //   instead of 12.5 for the last.
+  // - whole_cta: a CTA a run of 8 units a lane of a warp and more. 25.2 (blocks of 64) and
+  //   12.5 (512 wide); never: 37.0 and 33.7; from half that size on: 47 instead of 21.8
   //   for the first.
-  // - window: 16 tokens 22.0 / - / 29.3, 22.3; 8: 22.6 / - / 31.5, 30.7; 31: 23.3 / - /
-  //   33.8, 23.9. A CTA takes a block's tokens: 25.8 for 64; 16 of them: 33.5.
-  // - tensors: K and V one after the other, which share what is looked up: 22.0 / - / 29.3,
-  //   22.3; a warp each: 23.9 / - / 35.3, 28.0. (A CTA or a lone token: one, for more warps.)
-  // - group: two units of a run a lane, four lanes at least: 29.3 (blocks of 1); one unit
-  //   a lane 41; always a whole warp 119.
-  // - KEEP: room for two units where a run fits that: 29.3 and 22.3, for four 30.3 and 23.0.
+  // - window: 16 tokens 21.8 / - / 24.6, 19.3; 8: 22.1 / - / 25.4, 25.2; 31: 23.4 / - /
+  //   25.2, 21.1. A CTA takes a block's tokens: 25.2 for 64; 16 of them: 31.3.
+  // - tensors: K and V one after the other, which share what is looked up: 21.8 / - / 24.6,
+  //   19.3; a warp each: 22.9 / - / 28.2, 22.1. (A CTA or a lone token: one, for more warps.)
+  // - group: two units of a run a lane, four lanes at least: 24.6 (blocks of 1); one unit
+  //   a lane 33.9; always a whole warp 103.
+  // - KEEP: room for two units where a run fits that: 24.6 and 19.3, for four 31.1 and 22.5;
+  //   for two only, with the others read again: 27.9 instead of 21.8.
   const bool few = 2LL * N * Hkv <= 64LL * sms;
   const bool whole_cta = !few && run >= 256;
   a.window = few ? 1 : whole_cta && scale_block > 16 ? scale_block : 16;
