@@ -5,12 +5,15 @@
 // descriptions travel as kernel parameters, so a call uploads nothing and can be
 // captured. A cache's pages to copy, head by head, are laid end to end and cut into
 // equal tiles of 16-byte vectors (smaller words where a cache is not so aligned), one a
-// CTA, whatever the page size; a thread has four loads in flight before it stores (two or
-// eight: no faster, and 54.8 -> 59.8 us where the sources repeat).
+// CTA, whatever the page size; a thread has four loads in flight before it stores. CTAs of
+// 128 threads, four words each: 43.7 us where the sources repeat and 2.2 for one page; 256
+// threads 45.0 and 2.5, 512 47.7 and 2.9; 256 with two words 48.5 and 2.0, with eight 47.7
+// and 3.4; larger copies alike to 1%.
 // Measured against a copy at 6789 GB/s: 1311 pages of two bf16 layers moved together 197 us
-// (1.03 of it), 448 pages of 64 forked prompts on four 8-bit layers 54.8 us (sources read
-// once), 2000 pages of 1 KB x 8 heads x 8 caches 40.6 us (0.95); one page 2.8 us, the
-// latency of a launch and of a load behind another.
+// (1.03 of it), 448 pages of 64 forked prompts on four 8-bit layers 43.7 us (1.58: each
+// source is read from memory once; 0.91 by the bytes that move), 2000 pages of 1 KB x 8
+// heads x 8 caches 40.4 us (0.96); one page 2.2 us, the latency of a launch and of a load
+// behind another.
 #include <cuda_runtime.h>
 
 #include <vector>
@@ -19,14 +22,29 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kEach = 4;                      // words a thread copies
 constexpr int kTile = kThreads * kEach;
 
+// Division of n < 2^31 by d >= 1 as a multiplication (Granlund and Montgomery, Division by
+// Invariant Integers using Multiplication): with l = ceil(log2 d) and m = ceil(2^(31+l) / d),
+// the quotient is floor(m n / 2^(31+l)). With divisions in the kernel, copies whose sources
+// repeat are bound by issuing them (54.7 instead of 45.0 us, at 256 threads).
+struct Divisor {
+  uint32_t d, m, l;
+  void set(uint32_t divisor) {
+    d = divisor;
+    for (l = 0; (1ull << l) < d;) ++l;
+    m = static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t quotient(uint32_t n) const {
+    return static_cast<uint32_t>((static_cast<uint64_t>(m) * n) >> (31 + l));
+  }
+};
 struct Cache {
   unsigned char *base;
   long long head_bytes;   // from one head to the next
-  uint32_t page_words;    // words of `vec` bytes in a page
+  Divisor page_words;     // words of `vec` bytes in a page
   int vec;                // 16, 4 or 1
   uint32_t block0;        // CTAs of the caches before this one
   uint32_t rows;          // pages to copy: pairs x heads
@@ -39,7 +57,8 @@ constexpr int kMaxPairs = 3500;
 template <int NP>
 struct CopyArgs {
   Cache cache[kMaxCaches];
-  int n_caches, n_pairs;
+  int n_caches;
+  Divisor n_pairs;
   int2 pair[NP];
 };
 static_assert(sizeof(CopyArgs<kMaxPairs>) <= 32000, "kernel parameters");
@@ -47,7 +66,8 @@ static_assert(sizeof(CopyArgs<kMaxPairs>) <= 32000, "kernel parameters");
 template <typename T, int NP>
 __device__ __forceinline__ void copy_tile(const CopyArgs<NP> &a, const Cache &k) {
   const uint64_t first = static_cast<uint64_t>(blockIdx.x - k.block0) * kTile + threadIdx.x;
-  const uint64_t words = static_cast<uint64_t>(k.rows) * k.page_words;
+  const uint32_t page_words = k.page_words.d;
+  const uint64_t words = static_cast<uint64_t>(k.rows) * page_words;
   T v[kEach];
   T *to[kEach];
 #pragma unroll
@@ -55,15 +75,15 @@ __device__ __forceinline__ void copy_tile(const CopyArgs<NP> &a, const Cache &k)
     const uint64_t w = first + i * kThreads;
     to[i] = nullptr;
     if (w < words) {
-      // (32-bit division while it reaches: 2^32 words are 64 GB of vectors)
-      const uint32_t row = words >> 32 ? static_cast<uint32_t>(w / k.page_words)
-                                       : static_cast<uint32_t>(w) / k.page_words;
-      const uint32_t in = static_cast<uint32_t>(w - static_cast<uint64_t>(row) * k.page_words);
-      const uint32_t head = row / a.n_pairs;
-      const int2 pr = a.pair[row - head * a.n_pairs];
+      // (2^31 words are 32 GB of vectors)
+      const uint32_t row = words >> 31 ? static_cast<uint32_t>(w / page_words)
+                                       : k.page_words.quotient(static_cast<uint32_t>(w));
+      const uint32_t in = static_cast<uint32_t>(w) - row * page_words;
+      const uint32_t head = a.n_pairs.quotient(row);
+      const int2 pr = a.pair[row - head * a.n_pairs.d];
       T *page0 = reinterpret_cast<T *>(k.base + head * k.head_bytes) + in;
-      v[i] = page0[static_cast<size_t>(pr.x) * k.page_words];
-      to[i] = page0 + static_cast<size_t>(pr.y) * k.page_words;
+      v[i] = page0[static_cast<uint64_t>(static_cast<uint32_t>(pr.x)) * page_words];
+      to[i] = page0 + static_cast<uint64_t>(static_cast<uint32_t>(pr.y)) * page_words;
     }
   }
 #pragma unroll
@@ -89,8 +109,9 @@ int launch_copy(void *const *caches, const int *heads, const int64_t *page_bytes
                 int n_pages, const int32_t *pairs, int n_pairs, cudaStream_t stream) {
   CopyArgs<NP> a;
   for (int p0 = 0; p0 < n_pairs; p0 += NP) {
-    a.n_pairs = n_pairs - p0 < NP ? n_pairs - p0 : NP;
-    for (int i = 0; i < a.n_pairs; ++i)
+    const int here = n_pairs - p0 < NP ? n_pairs - p0 : NP;
+    a.n_pairs.set(here);
+    for (int i = 0; i < here; ++i)
       a.pair[i] = make_int2(pairs[2 * (p0 + i)], pairs[2 * (p0 + i) + 1]);
     for (int c0 = 0; c0 < n_caches;) {
       long long blocks = 0;
@@ -101,11 +122,11 @@ int launch_copy(void *const *caches, const int *heads, const int64_t *page_bytes
         const int64_t bytes = page_bytes[c0 + n];
         const uintptr_t both = reinterpret_cast<uintptr_t>(k.base) | bytes;
         k.vec = both % 16 == 0 ? 16 : both % 4 == 0 ? 4 : 1;
-        k.page_words = static_cast<uint32_t>(bytes / k.vec);
+        k.page_words.set(static_cast<uint32_t>(bytes / k.vec));
         k.head_bytes = bytes * n_pages;
-        k.rows = static_cast<uint32_t>(heads[c0 + n]) * a.n_pairs;
+        k.rows = static_cast<uint32_t>(heads[c0 + n]) * here;
         k.block0 = static_cast<uint32_t>(blocks);
-        const uint64_t words = static_cast<uint64_t>(k.rows) * k.page_words;
+        const uint64_t words = static_cast<uint64_t>(k.rows) * k.page_words.d;
         const long long more = static_cast<long long>((words + kTile - 1) / kTile);
         if (n > 0 && blocks + more > 0x7fffffffLL) break;
         if (more > 0x7fffffffLL)

@@ -173,3 +173,15 @@ def test_forked_compacted_and_unshared_sequences_attend_alike(dev):
         v2[:, (1 + 4 * i) * ps:(1 + 4 * i) * ps + 50] = seq[s][1].transpose(0, 1)
     want = attend(own, 4, k2, v2, 13, torch.arange(1, 4, dtype=torch.int32, device=dev))
     assert torch.equal(got, want)
+
+
+def test_more_words_than_31_bits_count(dev):
+    """2100 pages of 2^20 + 1 bytes, copied byte by byte."""
+    n, nb = 2100, (1 << 20) + 1
+    P = 2 * n + 3
+    cache = torch.empty((1, P, nb), dtype=torch.uint8, device=dev).random_(0, 256)
+    before = cache[0, n:n + 3].clone()
+    pairs = torch.stack([torch.arange(n - 1, -1, -1), torch.arange(n + 3, P)], 1).int()
+    pkv.kv_copy_pages([cache], P, pairs)
+    assert torch.equal(cache[0, :n].flip(0), cache[0, n + 3:])
+    assert torch.equal(cache[0, n:n + 3], before)
