@@ -33,6 +33,7 @@ struct Args {
   const __nv_bfloat16 *k, *v;
   const int32_t *batch_idx, *input_pos, *table;
   int N, n_slots, max_pages, page_size, n_pages, block, log2_block;
+  pkv::Divisor page;   // by page_size
   uint8_t *k_cache, *v_cache;
   float *k_scale, *v_scale;
   int Hkv, D;
@@ -180,12 +181,13 @@ __global__ void __launch_bounds__(kWarps * 32, CTA || KEEP == 2 ? 8 : 6)
     return;
   }
   const int lane = threadIdx.x & 31;
-  const long long block = blockIdx.x - a.checkers;
-  const long long task = CTA ? block : block * kWarps + (threadIdx.x >> 5);
-  const int per_window = a.tensors == 2 ? a.Hkv : 2 * a.Hkv;
-  const long long i0 = task / per_window * a.window;
+  const uint32_t block = blockIdx.x - a.checkers;
+  const uint32_t task = CTA ? block : block * kWarps + (threadIdx.x >> 5);
+  const uint32_t per_window = a.tensors == 2 ? a.Hkv : 2 * a.Hkv;
+  const uint32_t window = task / per_window;
+  const long long i0 = static_cast<long long>(window) * a.window;
   if (i0 >= a.N) return;
-  const int which = static_cast<int>(task % per_window);
+  const int which = static_cast<int>(task - window * per_window);
   const int kv0 = which >= a.Hkv ? 1 : 0;   // 0: K, 1: V
   const int h = which - kv0 * a.Hkv;
   const bool reporter = which == 0;
@@ -240,10 +242,10 @@ __global__ void __launch_bounds__(kWarps * 32, CTA || KEEP == 2 ? 8 : 6)
       if (l > 0 && slot != 0) {   // a leader, and not padding
         int bits = 0;
         if (slot < 0 || slot >= a.n_slots) bits = PKV_ERR_SLOT;
-        else if (pos < 0 || pos / a.page_size >= a.max_pages) bits = PKV_ERR_POS;
+        else if (pos < 0 || a.page.quotient(pos) >= a.max_pages) bits = PKV_ERR_POS;
         int page = 0, in_page = 0;
         if (!bits) {
-          const int pb = pos / a.page_size;
+          const int pb = a.page.quotient(pos);
           in_page = pos - pb * a.page_size;
           page = a.table[static_cast<long long>(slot) * a.max_pages + pb];
         }
@@ -380,6 +382,7 @@ int launch_append_q8(const char *fn, const pkv_bf16 *k, const pkv_bf16 *v,
   a.n_slots = n_slots;
   a.max_pages = max_pages_per_seq;
   a.page_size = page_size;
+  a.page.set(page_size);
   a.n_pages = n_pages;
   a.block = scale_block;
   a.log2_block = 0;
@@ -422,7 +425,7 @@ int launch_append_q8(const char *fn, const pkv_bf16 *k, const pkv_bf16 *v,
   a.checkers = ((N < kChecked ? N : kChecked) + 1023) / 1024;
   const long long tasks = (N + a.window - 1LL) / a.window * Hkv * (3 - a.tensors);
   const long long blocks = a.checkers + (whole_cta ? tasks : (tasks + kWarps - 1) / kWarps);
-  if (blocks > 0x7fffffffLL) return pkv::fail(PKV_E_BAD_ARG, "%s: too large", fn);
+  if (blocks > 0x7fffffffLL || tasks > 0xfffffff0LL) return pkv::fail(PKV_E_BAD_ARG, "%s: too large", fn);
   auto *kern = whole_cta               ? append_q8_kernel<true, 4>
                : run <= 2 * a.group ? append_q8_kernel<false, 2>
                                     : append_q8_kernel<false, 4>;

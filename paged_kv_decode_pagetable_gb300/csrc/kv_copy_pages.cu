@@ -11,7 +11,8 @@
 // and 3.4; larger copies alike to 1%.
 // Measured against a copy at 6789 GB/s: 1311 pages of two bf16 layers moved together 197 us
 // (1.03 of it), 448 pages of 64 forked prompts on four 8-bit layers 43.7 us (1.58: each
-// source is read from memory once; 0.91 by the bytes that move), 2000 pages of 1 KB x 8
+// source is read from memory once; 0.91 by the bytes that move; bound by issuing its
+// instructions, 54.7 us, when it divided by numbers only known at run time), 2000 pages of 1 KB x 8
 // heads x 8 caches 40.4 us (0.96); one page 2.2 us, the latency of a launch and of a load
 // behind another.
 #include <cuda_runtime.h>
@@ -26,25 +27,10 @@ constexpr int kThreads = 128;
 constexpr int kEach = 4;                      // words a thread copies
 constexpr int kTile = kThreads * kEach;
 
-// Division of n < 2^31 by d >= 1 as a multiplication (Granlund and Montgomery, Division by
-// Invariant Integers using Multiplication): with l = ceil(log2 d) and m = ceil(2^(31+l) / d),
-// the quotient is floor(m n / 2^(31+l)). With divisions in the kernel, copies whose sources
-// repeat are bound by issuing them (54.7 instead of 45.0 us, at 256 threads).
-struct Divisor {
-  uint32_t d, m, l;
-  void set(uint32_t divisor) {
-    d = divisor;
-    for (l = 0; (1ull << l) < d;) ++l;
-    m = static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d);
-  }
-  __device__ __forceinline__ uint32_t quotient(uint32_t n) const {
-    return static_cast<uint32_t>((static_cast<uint64_t>(m) * n) >> (31 + l));
-  }
-};
 struct Cache {
   unsigned char *base;
   long long head_bytes;   // from one head to the next
-  Divisor page_words;     // words of `vec` bytes in a page
+  pkv::Divisor page_words;     // words of `vec` bytes in a page
   int vec;                // 16, 4 or 1
   uint32_t block0;        // CTAs of the caches before this one
   uint32_t rows;          // pages to copy: pairs x heads
@@ -58,7 +44,7 @@ template <int NP>
 struct CopyArgs {
   Cache cache[kMaxCaches];
   int n_caches;
-  Divisor n_pairs;
+  pkv::Divisor n_pairs;
   int2 pair[NP];
 };
 static_assert(sizeof(CopyArgs<kMaxPairs>) <= 32000, "kernel parameters");

@@ -68,6 +68,21 @@ inline bool aligned16(const void *p) {
 }
 inline bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
+// Division of n < 2^31 by d >= 1 as a multiplication (Granlund and Montgomery, Division by
+// Invariant Integers using Multiplication): with l = ceil(log2 d) and m = ceil(2^(31+l) / d),
+// the quotient is floor(m n / 2^(31+l)).
+struct Divisor {
+  uint32_t d, m, l;
+  void set(uint32_t divisor) {
+    d = divisor;
+    for (l = 0; (1ull << l) < d;) ++l;
+    m = static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t quotient(uint32_t n) const {
+    return static_cast<uint32_t>((static_cast<uint64_t>(m) * n) >> (31 + l));
+  }
+};
+
 // Launches a kernel that may begin while the previous kernel of the stream
 // is still running (programmatic dependent launch). Every kernel launched
 // this way executes griddepcontrol.wait before it touches global memory, so
