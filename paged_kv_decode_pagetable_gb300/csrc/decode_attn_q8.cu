@@ -543,7 +543,7 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
         if (lane == 0)
           reinterpret_cast<float *>(sm + Cf::OFF_QS)[qs * kMaxG + h] = p.scale_log2 * exp2i(e);
       }
-      fence_proxy_async();   // the next copy into the stage comes after these stores
+      fence_proxy_async();   // the next copy into the stage comes after these accesses
     }
     __syncwarp();
     if (lane == 0) {
@@ -1072,6 +1072,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     if (lane == 0 && p.err) atomicOr(p.err, PKV_ERR_TIMEOUT);
   };
 
+  // Hands memory back to the producer warp. What this warp has read there with plain loads
+  // comes before what the copies (another proxy) write: without the fence a load still in
+  // flight could read the next tile (seen at D = 256, two CTAs an SM: one call in ten of
+  // three rows of 30k tokens).
+  auto release = [&](uint32_t bar) {
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+
   while (true) {
     const int qs = it_q & 1;
     const bool go = mbar_wait_word(readyQ + 8 * qs, (it_q >> 1) & 1) && abort_flag[1 + qs];
@@ -1086,8 +1096,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
 #pragma unroll
       for (int c = 0; c < KS; ++c)
         qb[c] = hv ? *reinterpret_cast<const uint2 *>(qrow + 32 * c) : make_uint2(0u, 0u);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(emptyQ + 8 * qs);
+      release(emptyQ + 8 * qs);
     }
     ++it_q;
 
@@ -1156,8 +1165,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
 #pragma unroll
           for (int i = 0; i < 4; ++i) sa[0][i] += sa[1][i];
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + 8 * st);   // the K entry is free
+        release(empty + 8 * st);   // the K entry
         wait_scales();
         // ---- online softmax ----
         const float *kw = scale_words + (t - t0) * scales, *vw = kw + kScaleWords;
@@ -1230,8 +1238,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
               *reinterpret_cast<uint4 *>(sm + unit_addr<D>(st * Cf::TILE_BYTES, row_base<D>(r),
                                                            i % KS)) = make_uint4(0u, 0u, 0u, 0u);
           }
-          fence_proxy_async();   // the next copy into the entry comes after these stores
-          __syncwarp();
+          __syncwarp();   // (the entry's release fences these stores too)
         }
 #pragma unroll
         for (int u = 0; u < KS; u += 2) {
@@ -1248,8 +1255,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
             mma_f16(o[u + 1], a0, a1, a2, a3, pb[2 * i], pb[2 * i + 1]);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + 8 * st);
+        release(empty + 8 * st);
       }
       wait_scales();   // a warp without a tile here keeps step too
       __syncwarp();
@@ -1257,8 +1263,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     }
     tile += w.tb - w.ta;
     if constexpr (!Q_REGS) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(emptyQ + 8 * qs);
+      release(emptyQ + 8 * qs);
     }
 
     // ---- the unit's end ----

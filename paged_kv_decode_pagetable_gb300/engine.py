@@ -22,9 +22,9 @@ import numpy as np
 import torch
 
 from . import (NoPagesError, NoSlotError, PageTable, kv_append, kv_append_q8, kv_copy_pages,
-               paged_decode_attn, paged_decode_attn_q8, paged_decode_attn_q8_workspace, paged_decode_attn_splits,
-               paged_decode_attn_workspace, paged_decode_step, paged_decode_step_ex,
-               qk_norm_rope, qkv_norm_rope)
+               paged_decode_attn, paged_decode_attn_q8, paged_decode_attn_q8_workspace,
+               paged_decode_attn_splits, paged_decode_attn_workspace, paged_decode_step,
+               paged_decode_step_ex, qk_norm_rope, qkv_norm_rope)
 
 
 @dataclasses.dataclass(frozen=True)

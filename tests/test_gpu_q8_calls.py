@@ -198,3 +198,18 @@ def test_ones_own_key_alone_is_its_value(dev):
             r = c.table[c.slots[b], 0] * 8
             want = np.repeat(c.c[1][:, r] * c.s[1][:, r][:, None], 2, 0)
             assert np.array_equal(got[b], want), (D, b)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+def test_full_rings_are_read_before_they_are_refilled(dev, D):
+    """Long rows keep every ring entry in use; a tile read after its entry was refilled
+    shows as calls that differ (at D = 256, one in ten)."""
+    rng = np.random.default_rng(63)
+    c = Case(rng, 3, 24, 3, D, 64, 2, [29952, 28480, 29803]).device(dev)
+    outs = torch.full((200,) + c.out.shape, float("nan"), dtype=torch.bfloat16, device=dev)
+    for o in outs:
+        call(c, out=o)
+    assert torch.isfinite(outs).all()
+    assert all(torch.equal(o, outs[0]) for o in outs[1:])
+    c.out = outs[0]
+    c.check(rows=[1])
