@@ -4,10 +4,10 @@
 //   s_j = scale * sk_j * (q . ck_j),  out = sum_j softmax(s)_j sv_j cv_j
 //
 // Bound by reading the codes and scales of every key once. Measured against the measured
-// 6789 GB/s: 16 rows of 16k to 32k tokens (8 heads of 128, blocks of 16) 122.6 us, 0.97;
-// 256 rows of 500 to 1500 tokens 88 us, 0.89; 64 rows of 100 to 1024 tokens 18.8 us, 0.59;
-// the same with 512-wide heads (one of them, blocks of 64) 23.4 us, 0.48; one row of 32k
-// tokens 19.0 us, 0.52; 64-wide heads, 16 rows of 8k to 16k tokens 50 us, 0.60. Without
+// 6789 GB/s: 16 rows of 16k to 32k tokens (8 heads of 128, blocks of 32) 124.2 us, 0.96;
+// 256 rows of 500 to 1500 tokens 89 us, 0.88; 64 rows of 100 to 1024 tokens 19.0 us, 0.58;
+// 64 rows of 256 to 2048 tokens with one 512-wide head 23.5 us, 0.48; one row of 32k
+// tokens 18.9 us, 0.52; 64-wide heads, 16 rows of 8k to 16k tokens 50.6 us, 0.59. Without
 // its arithmetic the kernel takes 16.5 and 40 us for the 64 rows and the 64-wide ones: what
 // small calls cost beyond their bytes is the start (launch, row set-up, page lookups, the
 // first tiles' latency: about 5 us) and the joins (2 to 5 us).

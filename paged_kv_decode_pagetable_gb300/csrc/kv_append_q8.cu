@@ -13,10 +13,10 @@
 // size of a run), which finds the run's largest magnitude and the block's scale,
 // rescales older codes if the scale grew and writes the new ones. Extra CTAs look for
 // tokens of one block that stand apart. Bound by reading k and v and writing half their
-// bytes: 16411 tokens of 16 prompts (8 heads of 128, blocks of 16; 101 MB) take 21.2 us,
+// bytes: 16411 tokens of 16 prompts (8 heads of 128, blocks of 16; 101 MB) take 21.3 us,
 // 0.70 of the measured 6789 GB/s (an elementwise copy of as many bytes: 16.1 us; the warps
-// issue in 44% of the cycles and wait for loads in most others), a decode step of 8 rows
-// 2.9 us, one of 512 rows 4.7 us, both the latency of index, table, token and store.
+// issue in 43% of the cycles and wait for loads in most others), a decode step of 8 rows
+// 2.7 us, one of 512 rows 4.4 us, both the latency of index, table, token and store.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
