@@ -213,3 +213,23 @@ def test_full_rings_are_read_before_they_are_refilled(dev, D):
     assert all(torch.equal(o, outs[0]) for o in outs[1:])
     c.out = outs[0]
     c.check(rows=[1])
+
+
+def test_calls_beside_a_busy_stream(dev):
+    """Other work holds SMs, so that not all CTAs of a call are resident at once: parts
+    wait for ones that start later, and all finish."""
+    rng = np.random.default_rng(64)
+    cases = [Case(rng, 1, 32, 8, 128, 64, 16, [30000]).device(dev),
+             Case(rng, 9, 8, 1, 512, 64, 64, rng.integers(500, 9000, 9)).device(dev)]
+    want = [c.run().clone() for c in cases]
+    a = torch.randn((4096, 4096), dtype=torch.bfloat16, device=dev)
+    other, b = torch.cuda.Stream(), torch.empty_like(a)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        for _ in range(200):
+            torch.mm(a, a, out=b)
+    outs = [[call(c) for _ in range(100)] for c in cases]
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(x, w) for x in o)
+    assert all(not c.ws.any() for c in cases)
