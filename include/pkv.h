@@ -366,7 +366,8 @@ size_t paged_decode_attn_workspace(int B, int Hq, int D, int num_splits);
  *   out[b][h] = sum_j softmax_j(scale * q[b][h] . k_j) v_j
  * Keys, rows without keys, windows, GQA, table errors and argument limits are
  * paged_decode_attn's, with Hkv <= 65535; q must be finite and the scores
- * within fp32's range. Values at positions outside a row's keys are never
+ * below 2^26 in magnitude (fp32 tells larger ones apart by 4 and more; there
+ * the output is some mean of the values, or 0). Values at positions outside a row's keys are never
  * used (codes there may be NaN, scales anything). Scores, softmax statistics
  * and outputs are accumulated in fp32; the weights p_j * v_scale_j enter the
  * product with V as fp16, relative to the row's largest.

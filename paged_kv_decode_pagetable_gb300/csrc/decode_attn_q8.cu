@@ -52,7 +52,9 @@
 //     the softmax weight: w_j = 2^(s_j + log2 sv_j - M) with M the running
 //     maximum of that sum, so w is at most 1 and as precise as fp16 allows where
 //     it matters however far the scales lie apart; the denominator keeps a
-//     running maximum of its own, per lane;
+//     running maximum of its own, per lane. The sum is rounded up for M alone and w taken
+//     as 2^((s_j - M) + log2 sv_j), whose difference is exact where w counts: added to a
+//     score of 10^5 the logarithm would keep 7 bits behind the point;
 //   * every wait is bounded; one that gives up sets PKV_ERR_TIMEOUT,
 //     the CTA drains its copies and exits. Invalid table entries are reported
 //     and never dereferenced.
@@ -1188,8 +1190,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
         for (int i = 0; i < 2 * MB; ++i) {
           n0 = fmaxf(n0, sx[i][0]);
           n1 = fmaxf(n1, sx[i][1]);
-          x0 = fmaxf(x0, sx[i][0] + lv[i]);
-          x1 = fmaxf(x1, sx[i][1] + lv[i]);
+          x0 = fmaxf(x0, __fadd_ru(sx[i][0], lv[i]));
+          x1 = fmaxf(x1, __fadd_ru(sx[i][1], lv[i]));
         }
         const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
         l0 *= ex2(m0 - u0);
@@ -1224,7 +1226,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
         uint32_t pb[2 * MB];
 #pragma unroll
         for (int i = 0; i < 2 * MB; ++i)
-          pb[i] = transpose8x8(pack_f16(ex2(sx[i][0] + lv[i] - U0), ex2(sx[i][1] + lv[i] - U1)));
+          pb[i] = transpose8x8(pack_f16(ex2(sx[i][0] - U0 + lv[i]), ex2(sx[i][1] - U1 + lv[i])));
         // ---- O^T [D x 8 heads] += V^T P^T ----
         st = (ent + 1) % Cf::NS;
         if (!mbar_wait(full + 8 * st, ((ent + 1) / Cf::NS) & 1, abort_flag)) give_up();
