@@ -370,7 +370,8 @@ size_t paged_decode_attn_workspace(int B, int Hq, int D, int num_splits);
  * the output is some mean of the values, or 0). Values at positions outside a row's keys are never
  * used (codes there may be NaN, scales anything). Scores, softmax statistics
  * and outputs are accumulated in fp32; the weights p_j * v_scale_j enter the
- * product with V as fp16, relative to the row's largest.
+ * product with V as fp16: to 11 bits down to 2^-29 of the row's largest, and
+ * as 0 below 2^-40 of it.
  * The work is cut over the GPU as in the automatic mode. The workspace must
  * hold paged_decode_attn_q8_workspace(Hq, Hkv, D) bytes (16-byte aligned),
  * whatever the batch and the lengths; zero it once before its first use.

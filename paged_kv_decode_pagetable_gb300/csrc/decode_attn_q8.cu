@@ -50,9 +50,11 @@
 //     its row's largest magnitude, so it is exact in fp16 too (elements below
 //     2^-14 of the largest lose at most 2^-25 of it). The scale of v is part of
 //     the softmax weight: w_j = 2^(s_j + log2 sv_j - M) with M the running
-//     maximum of that sum, so w is at most 1 and as precise as fp16 allows where
-//     it matters however far the scales lie apart; the denominator keeps a
-//     running maximum of its own, per lane. The sum is rounded up for M alone and w taken
+//     maximum of that sum, so w is at most 1 however far the scales lie
+//     apart; the denominator keeps a running maximum of its own, per lane. w enters the
+//     product as fp16 times 2^15, so that weights down to 2^-29 keep 11 bits and none above
+//     2^-40 is lost (times 1, a key 2^-25 as heavy as its warp's heaviest would add nothing);
+//     the factor goes where the warps' states are joined. The sum is rounded up for M alone and w taken
 //     as 2^((s_j - M) + log2 sv_j), whose difference is exact where w counts: added to a
 //     score of 10^5 the logarithm would keep 7 bits behind the point;
 //   * every wait is bounded; one that gives up sets PKV_ERR_TIMEOUT,
@@ -76,6 +78,8 @@ constexpr int kScaleWords = 512;     // scales of K (and of V) handed over at on
 constexpr int kCThreads = kCWarps * 32;
 constexpr int kThreads = kCThreads + 64;   // + producer warp and joining warp
 constexpr int kMaxG = 8;             // query heads per kv head (MMA N)
+constexpr float kLift = 15.f;        // log2 of the weights' factor in the product with V
+constexpr float kUnlift = 1.f / 32768.f;
 constexpr int kMaxRows = 512;        // rows per call (row cache kept in smem)
 constexpr int kMaxCtas = 512;        // CTAs the workspace has room for
 constexpr int kSpinLimit = 1 << 22;
@@ -592,7 +596,7 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
         l = sum_at(own_l, own_m, m);
 #pragma unroll
         for (int i = 8; i < 32; i <<= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
-        f = own_M == -INFINITY ? 0.f : ex2(own_M - M);
+        f = own_M == -INFINITY ? 0.f : kUnlift * ex2(own_M - M);
         last = last_factor(partial, m, l, M);
       }
 #pragma unroll 1
@@ -1225,8 +1229,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
         const float U0 = M0 == -INFINITY ? 0.f : M0, U1 = M1 == -INFINITY ? 0.f : M1;
         uint32_t pb[2 * MB];
 #pragma unroll
-        for (int i = 0; i < 2 * MB; ++i)
-          pb[i] = transpose8x8(pack_f16(ex2(sx[i][0] - U0 + lv[i]), ex2(sx[i][1] - U1 + lv[i])));
+        for (int i = 0; i < 2 * MB; ++i) {   // at most 2^15: (s - M) <= -lv
+          const float lift = lv[i] + kLift;
+          pb[i] = transpose8x8(pack_f16(ex2(sx[i][0] - U0 + lift), ex2(sx[i][1] - U1 + lift)));
+        }
         // ---- O^T [D x 8 heads] += V^T P^T ----
         st = (ent + 1) % Cf::NS;
         if (!mbar_wait(full + 8 * st, ((ent + 1) / Cf::NS) & 1, abort_flag)) give_up();
@@ -1274,8 +1280,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
       for (int u = 0; u < (D < kMergeCols ? D : kMergeCols) / 16; ++u) {
         const float(&f)[4] = o[c0 / 16 + u];
         float *d = to + (warp * kMaxG + h0) * kMergeRow + 16 * u + 2 * gid;
-        *reinterpret_cast<float2 *>(d) = make_float2(f[0], f[2]);
-        *reinterpret_cast<float2 *>(d + kMergeRow) = make_float2(f[1], f[3]);
+        // (the joining warp's weights of the states take the factor back at D <= 256)
+        constexpr float F = Cf::SELF ? kUnlift : 1.f;
+        *reinterpret_cast<float2 *>(d) = make_float2(f[0] * F, f[2] * F);
+        *reinterpret_cast<float2 *>(d + kMergeRow) = make_float2(f[1] * F, f[3] * F);
       }
     };
     auto write_stats = [&](float *to) {   // the warp's m, l and M: [3][4][8]
@@ -1305,8 +1313,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
 #pragma unroll
       for (int u = 0; u < KS; ++u) {
         float *d = dump + (warp * kMaxG + h0) * Cf::DUMP_ROW + 16 * u + 2 * gid;
-        *reinterpret_cast<float2 *>(d) = make_float2(o[u][0], o[u][2]);
-        *reinterpret_cast<float2 *>(d + Cf::DUMP_ROW) = make_float2(o[u][1], o[u][3]);
+        *reinterpret_cast<float2 *>(d) = make_float2(o[u][0] * kUnlift, o[u][2] * kUnlift);
+        *reinterpret_cast<float2 *>(d + Cf::DUMP_ROW) =
+            make_float2(o[u][1] * kUnlift, o[u][3] * kUnlift);
       }
       write_stats(dump + Cf::DUMP_STATS);
       (void)consumer_sync_or(false);
