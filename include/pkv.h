@@ -368,7 +368,9 @@ size_t paged_decode_attn_workspace(int B, int Hq, int D, int num_splits);
  * paged_decode_attn's, with Hkv <= 65535; q must be finite and the scores
  * below 2^26 in magnitude (fp32 tells larger ones apart by 4 and more; there
  * the output is some mean of the values, or 0). Values at positions outside a row's keys are never
- * used (codes there may be NaN, scales anything). Scores, softmax statistics
+ * used (codes there may be NaN, scales anything). A query row enters the
+ * product with K as fp16 scaled to its largest element: exact but for elements
+ * below 2^-29 of that one, which lose 2^-40 of it. Scores, softmax statistics
  * and outputs are accumulated in fp32; the weights p_j * v_scale_j enter the
  * product with V as fp16: to 11 bits down to 2^-29 of the row's largest, and
  * as 0 below 2^-40 of it.

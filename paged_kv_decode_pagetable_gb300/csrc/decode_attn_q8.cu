@@ -46,9 +46,9 @@
 //     tcgen05.mma has no rate to add: its operands come from shared memory, where the
 //     codes would have to be written back as fp16 first (with q and P in e4m3 instead,
 //     the result would lose most of q's and P's bits);
-//   * codes become fp16 in registers (exact). q is scaled by a power of two to
-//     its row's largest magnitude, so it is exact in fp16 too (elements below
-//     2^-14 of the largest lose at most 2^-25 of it). The scale of v is part of
+//   * codes become fp16 in registers (exact). q is scaled by a power of two that
+//     brings its row's largest magnitude to 2^15 .. 2^16, so it is exact in fp16 too (elements
+//     below 2^-29 of the largest lose at most 2^-40 of it). The scale of v is part of
 //     the softmax weight: w_j = 2^(s_j + log2 sv_j - M) with M the running
 //     maximum of that sum, so w is at most 1 however far the scales lie
 //     apart; the denominator keeps a running maximum of its own, per lane. w enters the
@@ -520,7 +520,8 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
   volatile int *admitted = abort_flag + 1;
   pkv_wait_prior_grid();
   // The next unit: its query rows become fp16 in place, each scaled by a power of two
-  // to its largest magnitude, before the consumer warps need them.
+  // that brings its largest magnitude to 2^15 .. 2^16 (65280 at most, below fp16's largest),
+  // before the consumer warps need them.
   auto receive = [&](Unit &w) {
     const int qs = it_q & 1;
     const bool q_ok = mbar_wait(fullQ + 8 * qs, (it_q >> 1) & 1, abort_flag);
@@ -540,7 +541,7 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
           m = __vmaxu2(m, v[j] & 0x7fff7fffu);
         }
         m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-        const int e = min(max(static_cast<int>(m >> 7) - 127, -126), 126);
+        const int e = max(static_cast<int>(m >> 7) - 127 - 15, -126);
         const float f = exp2i(-e);
 #pragma unroll
         for (int j = 0; j < D / 64; ++j)

@@ -1,6 +1,6 @@
 """paged_decode_attn_q8 where its 32- and 16-bit arithmetic could lose what matters:
 scores of any size, keys of very little weight beside a heavy one, scales of V at the
-ends of their range.
+ends of their range, queries with one very large element.
 
 Bounds: test_gpu_q8's; for light keys with the absolute part of a weight's rounding that
 the header states: weights enter the product with V times 2^15, so half a step below
@@ -96,3 +96,16 @@ def test_scales_of_v_at_their_ends(dev):
         c.s[1] = c.s[1] * 2.0 ** (e + 7)
         c.device(dev).run()
         c.check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+@pytest.mark.parametrize("large", [8, 14, 20])
+def test_one_large_query_element(dev, D, large):
+    """q has an element of 2^large where every key is 0: the scores come from the others,
+    and the bound knows only those."""
+    rng = np.random.default_rng(D + large)
+    c = Case(rng, 3, 8, 2, D, 64, 16, [500, 64, 131])
+    c.c[0][:, :, 5] = np.where(np.isnan(c.c[0][:, :, 5]), np.nan, 0.0)
+    c.q[:, :, 5] = 2.0 ** large
+    c.device(dev).run()
+    c.check()
