@@ -105,6 +105,8 @@ int pt_create(int max_batch_size, int page_size, int n_pages,
               pkv_pt **out);
 int pt_destroy(pkv_pt *pt);
 int pt_set_stream(pkv_pt *pt, void *stream);
+/* the stream of the table's copies (as given to pt_create or pt_set_stream) */
+int pt_get_stream(const pkv_pt *pt, void **stream);
 /* slot < 0: can a new request of seq_len tokens be admitted (a free slot
  * and enough pages)?  slot >= 1: can that live slot grow to seq_len? */
 int pt_can_reserve(const pkv_pt *pt, int seq_len, int slot, int *ok);

@@ -67,6 +67,7 @@ _SIGS = {
     "pt_create": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_p, _c_p, ctypes.POINTER(_c_p)]),
     "pt_destroy": (_c_int, [_c_p]),
     "pt_set_stream": (_c_int, [_c_p, _c_p]),
+    "pt_get_stream": (_c_int, [_c_p, ctypes.POINTER(_c_p)]),
     "pt_can_reserve": (_c_int, [_c_p, _c_int, _c_int, ctypes.POINTER(_c_int)]),
     "pt_assign": (_c_int, [_c_p, _c_int, ctypes.POINTER(_c_int)]),
     "pt_reserve": (_c_int, [_c_p, _c_int, _c_int]),
@@ -229,6 +230,13 @@ def pt_destroy(h: int) -> None:
 
 def pt_set_stream(h: int, stream=None) -> None:
     _check(load_library().pt_set_stream(h, _stream(stream)), "pt_set_stream")
+
+
+def pt_get_stream(h: int) -> int:
+    """The handle's stream (0: the default stream)."""
+    s = _c_p()
+    _check(load_library().pt_get_stream(h, ctypes.byref(s)), "pt_get_stream")
+    return s.value or 0
 
 
 def pt_can_reserve(h: int, seq_len: int, slot: int = -1) -> bool:

@@ -119,6 +119,12 @@ int pt_set_stream(pkv_pt *pt, void *stream) {
   return pkv::ok();
 }
 
+int pt_get_stream(const pkv_pt *pt, void **stream) {
+  if (!pt || !stream) return pkv::fail(PKV_E_BAD_ARG, "pt_get_stream: NULL");
+  *stream = pt->stream;
+  return pkv::ok();
+}
+
 int pt_can_reserve(const pkv_pt *pt, int seq_len, int slot, int *ok) {
   if (!pt || !ok) return pkv::fail(PKV_E_BAD_ARG, "pt_can_reserve: NULL");
   if (slot < 0) {

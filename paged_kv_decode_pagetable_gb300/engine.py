@@ -21,10 +21,11 @@ import dataclasses
 import numpy as np
 import torch
 
-from . import (NoPagesError, NoSlotError, PageTable, kv_append, kv_append_q8, kv_copy_pages,
-               paged_decode_attn, paged_decode_attn_q8, paged_decode_attn_q8_workspace,
-               paged_decode_attn_splits, paged_decode_attn_workspace, paged_decode_step,
-               paged_decode_step_ex, qk_norm_rope, qkv_norm_rope)
+from . import (NoPagesError, NoSlotError, PageTable, _stream, kv_append, kv_append_q8,
+               kv_copy_pages, paged_decode_attn, paged_decode_attn_q8,
+               paged_decode_attn_q8_workspace, paged_decode_attn_splits,
+               paged_decode_attn_workspace, paged_decode_step, paged_decode_step_ex,
+               pt_get_stream, qk_norm_rope, qkv_norm_rope)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -231,6 +232,34 @@ class Sequence:
         return self.prompt_len + self.generated
 
 
+def _after(stream: int, other: int) -> None:
+    """What `stream` is given from here on waits for what `other` has been given."""
+    def of(handle):
+        return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+    done = torch.cuda.Event()
+    done.record(of(other))
+    of(stream).wait_event(done)
+
+
+def _move_pages(pt: PageTable, caches, move, stream):
+    """Calls `move`, which changes the table and returns page pairs, and copies them. The
+    copy has to stand behind the table's upload and before the next append or attention,
+    and the pages it writes may still be read: it runs on the table's stream, behind all
+    that `stream` (None: the current one) has been given, and what `stream` is given
+    afterwards waits for it."""
+    kv_copy_pages(caches, pt.n_pages, [])   # refuses them before anything changes
+    use = _stream(stream) or 0
+    own = use if pt.dev_table is None else pt_get_stream(pt.handle)
+    if own != use:
+        _after(own, use)
+    pairs = move()
+    kv_copy_pages(caches, pt.n_pages, pairs, stream=own)
+    if own != use:
+        _after(use, own)
+    return pairs
+
+
 class ContinuousBatcher:
     """The scheduling of the pages' generate loop ("unsloth: compare
     main...flex-moe-qwen3" · flex_gemma4_moe.py · generate) over a PageTable:
@@ -321,25 +350,31 @@ class ContinuousBatcher:
         pages live in (K and V of all layers; with 8-bit caches their scales
         too); the partly filled pages are copied in one call. Samples that find
         no slot or page wait to be admitted like any other sequence. Returns the
-        new sequences."""
+        new sequences. `stream` (None: the current one) is the one that appends
+        to and reads the caches, besides the page table's: both see the samples'
+        pages in order."""
         if s not in self.running:
             raise ValueError(f"sequence {s.rid} is not running")
         rids = list(rids)
-        kv_copy_pages(caches, self.pt.n_pages, [])   # refuses them before anything changes
         cached = s.total_length - 1      # the last token is appended by the next decode
-        new, pairs = [], []
-        for rid in rids:
-            f = Sequence(rid, s.prompt_len, s.max_new_tokens, s.generated)
-            try:
-                slots, copies = self.pt.fork(s.slot, cached)
-                f.slot = slots[0]
-                pairs += copies.tolist()
-                self.running.append(f)
-                self.events.append(("fork", s.rid, rid))
-            except (NoSlotError, NoPagesError):
-                self.waiting.append(f)
-            new.append(f)
-        kv_copy_pages(caches, self.pt.n_pages, pairs, stream=stream)
+        new = []
+
+        def move():
+            pairs = []
+            for rid in rids:
+                f = Sequence(rid, s.prompt_len, s.max_new_tokens, s.generated)
+                try:
+                    slots, copies = self.pt.fork(s.slot, cached)
+                    f.slot = slots[0]
+                    pairs += copies.tolist()
+                    self.running.append(f)
+                    self.events.append(("fork", s.rid, rid))
+                except (NoSlotError, NoPagesError):
+                    self.waiting.append(f)
+                new.append(f)
+            return pairs
+
+        _move_pages(self.pt, caches, move, stream)
         return new
 
     def run(self, max_steps: int = 100000) -> list:
@@ -350,11 +385,10 @@ class ContinuousBatcher:
 
 
 def compact_cache(pt: PageTable, caches, stream=None) -> int:
-    """Moves the used pages to the front of the caches; returns how many moved."""
-    kv_copy_pages(caches, pt.n_pages, [])   # refuses them before anything moves
-    pairs = pt.compact()
-    kv_copy_pages(caches, pt.n_pages, pairs, stream=stream)
-    return len(pairs)
+    """Moves the used pages to the front of the caches; returns how many moved. `stream`
+    (None: the current one) is the one that appends to and reads the caches, besides the
+    page table's: both see the pages move in order."""
+    return len(_move_pages(pt, caches, pt.compact, stream))
 
 
 class DecodeGraphs:
