@@ -76,7 +76,7 @@ typedef struct pkv_pt pkv_pt;
 #define PKV_ERR_PAGE_RANGE 2   /* table entry >= n_pages */
 #define PKV_ERR_PAGE_NEG 4     /* table entry < 0 (unreserved block) */
 #define PKV_ERR_SLOT 8         /* batch index outside [0, n_slots) */
-#define PKV_ERR_TIMEOUT 16     /* a bounded wait on a copy gave up */
+#define PKV_ERR_TIMEOUT 16     /* a bounded wait (for a copy, or for another part of a row) gave up */
 #define PKV_ERR_ORDER 32       /* 8-bit append: tokens of one scale block apart in the call */
 
 /* ---------------------------------------------------------------------
@@ -337,6 +337,9 @@ int qk_norm_rope_append(pkv_bf16 *q, pkv_bf16 *k, const pkv_bf16 *v,
  * Every call leaves it zero again, except a call that reports
  * PKV_ERR_TIMEOUT in the error word, after which the workspace must be
  * zeroed again. Calls sharing one workspace must not overlap on the GPU.
+ * In the automatic mode a first part waits for parts of CTAs started after its
+ * own: a call that other work leaves a single CTA's place for about a second
+ * reports PKV_ERR_TIMEOUT.
  * q: bf16 [B][Hq][D], out: bf16 [B][Hq][D], caches and table as above.
  * Requires D in {64, 128, 256, 512}, 1 <= Hq/Hkv <= 8, Hq % Hkv == 0,
  * page_size a power of two >= 8, B <= 512, and 16-byte aligned q, out,

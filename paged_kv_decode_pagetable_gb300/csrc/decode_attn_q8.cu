@@ -24,7 +24,11 @@
 //     row of 32k tokens 19.9 -> 22.9 us) in a fixed order: results do not depend on
 //     timing. A first part is its CTA's last work, and a part that takes in others
 //     but is not first its CTA's only work, so they find the others written, or
-//     wait for CTAs launched after them that began with that very work;
+//     wait for CTAs that began with that very work. The shares are given out from the
+//     line's end: a part's takers lie before it on the line, so a CTA waits only for CTAs
+//     with lower block numbers, which were started before it, and a call ends however few
+//     CTAs can be resident beside other work (given out from the front, three or four CTAs
+//     that each wait for one not started could hold all there is);
 //   * one producer warp streams query rows (cp.async.bulk), K and V tiles
 //     (cp.async.bulk.tensor into a swizzled ring, K and V entries of their own) and
 //     the scales of up to 32 tiles at a time (cp.async) ahead of four consumer warps,
@@ -355,9 +359,10 @@ __device__ __forceinline__ int2 row_read(const Problem &p, int b, int &bits) {
 // The line of work: a (row, head) with n > 0 tiles takes START + n positions, its start
 // and its tiles; pre[b] is the prefix sum of that over rows, (b, g)'s positions begin
 // at Hkv * pre[b] + g * (START + n). The `total` positions are shared by
-// min(CTAs, total) of them: the first `more` own each + 1, the others `each`, so every
-// share has a position and every CTA between a (row, head)'s first and last has tiles
-// of it.
+// min(CTAs, total) of them: the first `few` own `each`, the others, which are started
+// earlier, each + 1 (64 rows of 100 to 1024 tokens 19.3 us; the larger shares first on the
+// line 19.8), so every share has a position and every CTA between a (row, head)'s first and
+// last has tiles of it.
 // x / d for a quotient below 2^20: the approximate one is at most one off.
 __device__ __forceinline__ uint32_t small_quotient(uint32_t x, uint32_t d) {
   const uint32_t q = static_cast<uint32_t>(__fdividef(__uint2float_rz(x), __uint2float_rz(d)));
@@ -365,14 +370,14 @@ __device__ __forceinline__ uint32_t small_quotient(uint32_t x, uint32_t d) {
   return r < 0 ? q - 1 : r >= static_cast<int>(d) ? q + 1 : q;
 }
 struct Line {
-  uint32_t each, more;
+  uint32_t each, few;
   __device__ __forceinline__ int bound(uint32_t c) const {
-    return static_cast<int>(c * each + min(c, more));
+    return static_cast<int>(c * each + max(c, few) - few);
   }
   __device__ __forceinline__ int owner(uint32_t x) const {
-    const uint32_t wide = more * (each + 1);
-    return static_cast<int>(x < wide ? small_quotient(x, each + 1)
-                                     : more + small_quotient(x - wide, each));
+    const uint32_t narrow = few * each;
+    return static_cast<int>(x < narrow ? small_quotient(x, each)
+                                       : few + small_quotient(x - narrow, each + 1));
   }
 };
 
@@ -425,13 +430,17 @@ __device__ __forceinline__ bool next_unit(const Problem &p, const int *slots, co
   }
   return false;
 }
+// `me` is the share's number on the line.
 template <int START>
-__device__ __forceinline__ void which_part(const Line &line, Unit &w) {
-  const int me = static_cast<int>(blockIdx.x), start = w.first_cta, last = start + w.parts - 1;
+__device__ __forceinline__ void which_part(const Line &line, int me, Unit &w) {
+  const int start = w.first_cta, last = start + w.parts - 1;
   w.first_cta = w.part & 1 ? me : line.owner(start + START);
   w.parts = (w.part & 2 ? me : line.owner(last)) - w.first_cta + 1;
   w.part = me - w.first_cta;
 }
+
+// The record of a part that is not first: its share's.
+__device__ __forceinline__ size_t own_record(const Unit &w) { return w.first_cta + w.part; }
 
 // A sum l held relative to maximum m, relative to n >= m instead (a NaN stays one).
 __device__ __forceinline__ float sum_at(float l, float m, float n) {
@@ -612,7 +621,7 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
         if (i0 + hs >= p.G || !ok) continue;
         const int at = r * COLS + col;
         if (partial)
-          st_words(p.o_part + (static_cast<size_t>(blockIdx.x) * p.G + h) * D + at,
+          st_words(p.o_part + (own_record(w) * p.G + h) * D + at,
                    make_uint4(part_word(acc.x), part_word(acc.y), part_word(acc.z),
                               part_word(acc.w)));
         else
@@ -621,7 +630,7 @@ __device__ __forceinline__ void join_units(const Problem &p, uint8_t *sm, uint32
               pack4_bf16(acc, fl);
       }
       if (partial && r == 0 && ok && lane < p.G) {
-        uint32_t *a = p.st_part + (static_cast<size_t>(blockIdx.x) * p.G + lane) * 3;
+        uint32_t *a = p.st_part + (own_record(w) * p.G + lane) * 3;
         st_word(a, part_word(m));
         st_word(a + 1, part_word(l));
         st_word(a + 2, part_word(M));
@@ -715,7 +724,7 @@ __device__ __forceinline__ void join_parts(const Problem &p, uint8_t *sm, const 
       weight[k * kMaxG + sh] = x == -INFINITY ? 0.f : last * ex2(x - M);
     }
     if (partial && !bad && lane < p.G) {
-      uint32_t *s = p.st_part + (static_cast<size_t>(blockIdx.x) * p.G + lane) * 3;
+      uint32_t *s = p.st_part + (own_record(w) * p.G + lane) * 3;
       st_word(s, part_word(m));
       st_word(s + 1, part_word(l));
       st_word(s + 2, part_word(M));
@@ -777,7 +786,7 @@ __device__ __forceinline__ void join_parts(const Problem &p, uint8_t *sm, const 
       if (at >= places || bad) continue;
       const float4 &o = acc[i];
       if (partial)
-        st_words(p.o_part + static_cast<size_t>(blockIdx.x) * p.G * D + 4 * at,
+        st_words(p.o_part + own_record(w) * p.G * D + 4 * at,
                  make_uint4(part_word(o.x), part_word(o.y), part_word(o.z), part_word(o.w)));
       else
         *reinterpret_cast<uint2 *>(out + 4 * at) = pack4_bf16(o, 1.f);
@@ -853,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     if (lane == 0) pre[0] = 0;
     __syncwarp();
     const uint32_t total = p.Hkv * carry, ctas = min(gridDim.x, max(total, 1u));
-    const Line line = {total / ctas, total % ctas};
+    const Line line = {total / ctas, ctas - total % ctas};
     // Lane j looks up box j of a unit (a page's segment of one tile). box_page only
     // issues the table load; box_row checks the entry when it is used, so a
     // look-ahead load never stalls the warp.
@@ -878,9 +887,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
       return ((u.g * p.n_pages + page) << p.log2_ps) + (key & (ps - 1));
     };
     int x = 0, end = 0;
+    const int me = static_cast<int>(ctas - 1 - blockIdx.x);   // this CTA's share of the line
     if (blockIdx.x < ctas) {
-      x = line.bound(blockIdx.x);
-      end = line.bound(blockIdx.x + 1);
+      x = line.bound(me);
+      end = line.bound(me + 1);
     }
     Unit w, wn;
     w.b = 0;
@@ -888,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
     bool ok = true;
     bool have = next_unit<Cf::START>(p, slots, lens, pre, end, x, w, lane);
     int page_first = have ? box_page(w, lane) : -1;
-    if (have) which_part<Cf::START>(line, w);
+    if (have) which_part<Cf::START>(line, me, w);
     setup_sync();
     pkv_wait_prior_grid();
     if (blockIdx.x == 0 && row_bits && p.err) atomicOr(p.err, row_bits);
@@ -987,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
             wn.b = w.b;
             have_next = next_unit<Cf::START>(p, slots, lens, pre, end, x, wn, lane);
             page_next = have_next ? box_page(wn, lane) : -1;
-            if (have_next) which_part<Cf::START>(line, wn);
+            if (have_next) which_part<Cf::START>(line, me, wn);
           }
         }
       }
@@ -1363,7 +1373,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
             for (int j = 0; j < kCWarps; ++j)
               f[i][j] = a[64 + 8 * j] == -INFINITY ? 0.f : last * ex2(a[64 + 8 * j] - M);
             if (partial && !bad && lane == 0) {
-              uint32_t *st = p.st_part + (static_cast<size_t>(blockIdx.x) * p.G + h) * 3;
+              uint32_t *st = p.st_part + (own_record(w) * p.G + h) * 3;
               st_word(st, part_word(m));
               st_word(st + 1, part_word(l));
               st_word(st + 2, part_word(M));
@@ -1377,7 +1387,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
           const int at = c0 + 4 * lane;
           if (bad) continue;
           if (partial)
-            st_words(p.o_part + (static_cast<size_t>(blockIdx.x) * p.G + h) * D + at,
+            st_words(p.o_part + (own_record(w) * p.G + h) * D + at,
                      make_uint4(part_word(acc.x), part_word(acc.y), part_word(acc.z),
                                 part_word(acc.w)));
           else
