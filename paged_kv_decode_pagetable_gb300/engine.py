@@ -21,11 +21,11 @@ import dataclasses
 import numpy as np
 import torch
 
-from . import (NoPagesError, NoSlotError, PageTable, _stream, kv_append, kv_append_q8,
-               kv_copy_pages, paged_decode_attn, paged_decode_attn_q8,
+from . import (NoPagesError, NoSlotError, PageTable, PKV_ERR_TIMEOUT, _stream, kv_append,
+               kv_append_q8, kv_copy_pages, paged_decode_attn, paged_decode_attn_q8,
                paged_decode_attn_q8_workspace, paged_decode_attn_splits,
                paged_decode_attn_workspace, paged_decode_step, paged_decode_step_ex,
-               pt_get_stream, qk_norm_rope, qkv_norm_rope)
+               pkv_read_error_word, pt_get_stream, qk_norm_rope, qkv_norm_rope)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -76,6 +76,11 @@ class AttnWorkspaceQ8:
         self.buf = torch.zeros(paged_decode_attn_q8_workspace(Hq, Hkv, D), dtype=torch.uint8,
                                device=device)
 
+    def reset(self):
+        """Zeroes it again (on the current stream), as after a call that reported
+        PKV_ERR_TIMEOUT."""
+        self.buf.zero_()
+
 
 class AttnWorkspace:
     """Split mode and workspace for one (B, Hq, Hkv, D, table, window) shape.
@@ -93,6 +98,12 @@ class AttnWorkspace:
         n = paged_decode_attn_workspace(B, Hq, D, self.max_parts)
         self.buf = torch.zeros(n, dtype=torch.uint8, device=device) if n else None
 
+    def reset(self):
+        """Zeroes it again (on the current stream), as after a call that reported
+        PKV_ERR_TIMEOUT."""
+        if self.buf is not None:
+            self.buf.zero_()
+
 
 def decode_layer_step(spec: LayerSpec, pt: PageTable, k_cache, v_cache, q, k, v, batch_idx,
                       input_pos, seq_lens, out, ws: AttnWorkspace, gamma_q=None, gamma_k=None,
@@ -102,7 +113,10 @@ def decode_layer_step(spec: LayerSpec, pt: PageTable, k_cache, v_cache, q, k, v,
 
     k_scale and v_scale given: the caches are 8-bit ones (alloc_cache_q8) and ws an
     AttnWorkspaceQ8; the step is then the chain qk_norm_rope (qkv_norm_rope) ->
-    kv_append_q8 -> paged_decode_attn_q8.
+    kv_append_q8 -> paged_decode_attn_q8, whatever `fused` is (q and k are rotated in place).
+
+    err: an int32 word for the kernels' error bits. After PKV_ERR_TIMEOUT the workspace
+    must be reset (ws.reset()) before its next use.
 
     fused (default, rotary layers): one paged_decode_step(_ex) call; q, k and
     v are read only and seq_lens must equal input_pos + 1 (the kernel derives
@@ -440,9 +454,22 @@ class DecodeGraphs:
                           self.seq_lens[:b], self.out[:b], self.ws[b], self.gq, self.gk,
                           self.eps, err=self.err, k_scale=self.ks, v_scale=self.vs)
 
+    def errors(self) -> int:
+        """The error bits of the steps since the last look, on the current stream,
+        which it waits for. Clears them, and after PKV_ERR_TIMEOUT (a step's output
+        is then unspecified) the workspaces, which the next step needs zero."""
+        bits = pkv_read_error_word(self.err)
+        if bits:
+            self.err.zero_()
+        if bits & PKV_ERR_TIMEOUT:
+            for w in self.ws.values():
+                w.reset()
+        return bits
+
     def step(self, q, k, v, batch_idx, input_pos):
         """Device tensors for B rows; returns the B rows of the output (a view
-        of the static buffer, valid until the next step)."""
+        of the static buffer, valid until the next step). What a step could not
+        do is told by errors()."""
         B = q.shape[0]
         b = bucket_for(B, self.ladder)
         self.q[:B].copy_(q)
