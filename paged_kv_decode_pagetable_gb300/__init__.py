@@ -512,21 +512,32 @@ def kv_copy_pages(caches, n_pages, pairs, stream=None) -> None:
     [n][2], as pt_fork, pt_unshare and pt_compact return, or a sequence of
     (source, destination)."""
     if not isinstance(pairs, torch.Tensor):
-        pairs = torch.tensor(list(pairs), dtype=torch.int32).reshape(-1, 2)
+        try:
+            given = torch.tensor(list(pairs))
+            pairs = given.to(torch.int32).reshape(-1, 2)
+            if given.numel() and (given.dtype != torch.int64 or (given.reshape(-1, 2) != pairs).any()):
+                raise ValueError("not whole numbers of 32 bits")
+        except (TypeError, ValueError, RuntimeError) as e:
+            raise BadArgError(f"kv_copy_pages: pairs must be (source, destination)s: {e}") from None
     if (pairs.device.type != "cpu" or pairs.dtype != torch.int32 or pairs.dim() != 2
             or pairs.shape[1] != 2):
         raise BadArgError("kv_copy_pages: pairs must be a CPU int32 tensor [n][2]")
     pairs = pairs.contiguous()
-    n = len(caches)
-    ptrs, heads, nbytes = (_c_p * n)(), (_c_int * n)(), (ctypes.c_int64 * n)()
-    for i, c in enumerate(caches):
-        if not c.is_contiguous() or c.dim() < 2:
-            raise BadArgError("kv_copy_pages: caches must be contiguous tensors [heads][...]")
-        size, h = c.nbytes, c.shape[0]
-        each = size // max(h * n_pages, 1)
-        if each * h * n_pages != size:
-            raise BadArgError("kv_copy_pages: a head of a cache must be n_pages equal pages")
-        ptrs[i], heads[i], nbytes[i] = c.data_ptr(), h, each
+    try:
+        if isinstance(caches, torch.Tensor):
+            raise TypeError
+        n = len(caches)
+        ptrs, heads, nbytes = (_c_p * n)(), (_c_int * n)(), (ctypes.c_int64 * n)()
+        for i, c in enumerate(caches):
+            if not c.is_contiguous() or c.dim() < 2:
+                raise BadArgError("kv_copy_pages: caches must be contiguous tensors [heads][...]")
+            size, h = c.nbytes, c.shape[0]
+            each = size // max(h * n_pages, 1)
+            if each * h * n_pages != size:
+                raise BadArgError("kv_copy_pages: a head of a cache must be n_pages equal pages")
+            ptrs[i], heads[i], nbytes[i] = c.data_ptr(), h, each
+    except (AttributeError, TypeError):
+        raise BadArgError("kv_copy_pages: caches must be a list of tensors") from None
     _on_device(*caches)
     _check(load_library().kv_copy_pages(ptrs, heads, nbytes, n, n_pages, pairs.data_ptr(),
                                         pairs.shape[0], _stream(stream)), "kv_copy_pages")
