@@ -190,14 +190,22 @@ _E4M3, _F32, _BF16, _I32 = torch.float8_e4m3fn, torch.float32, torch.bfloat16, t
 
 def _bf16(t, name):
     if t is not None and not isinstance(t, int):
-        if t.dtype is not _BF16 or not t.is_contiguous():
+        try:
+            good = t.dtype is _BF16 and t.is_contiguous()
+        except AttributeError:
+            good = False
+        if not good:
             raise BadArgError(f"{name} must be a contiguous bfloat16 tensor")
     return t
 
 
 def _i32(t, name):
     if t is not None and not isinstance(t, int):
-        if t.dtype is not _I32 or not t.is_contiguous():
+        try:
+            good = t.dtype is _I32 and t.is_contiguous()
+        except AttributeError:
+            good = False
+        if not good:
             raise BadArgError(f"{name} must be a contiguous int32 tensor")
     return t
 
@@ -433,11 +441,21 @@ def kv_append_prefill(k, v, batch_idx, input_pos, dev_table, n_slots, max_pages_
         _ptr(err_word), _stream(stream)), "kv_append_prefill")
 
 
+def _word(t) -> None:
+    """Refuses an error word that is not one (None and addresses pass)."""
+    if t is not None and type(t) is not int and (
+            not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.numel() < 1):
+        raise BadArgError("err_word must be an int32 tensor")
+
+
 def _q8_cache(k_cache, v_cache, k_scale, v_scale, n_rows: int) -> tuple:
     """Checks an 8-bit cache's tensors; returns the kv heads, the head dim and the
     tokens that share a scale."""
-    shape, v_shape, scales, v_scales = (k_cache.shape, v_cache.shape, k_scale.shape,
-                                        v_scale.shape)
+    try:
+        shape, v_shape, scales, v_scales = (k_cache.shape, v_cache.shape, k_scale.shape,
+                                            v_scale.shape)
+    except AttributeError:
+        raise BadArgError("k_cache, v_cache, k_scale and v_scale must be tensors") from None
     for t, size, name in ((k_cache, shape, "k_cache"), (v_cache, v_shape, "v_cache")):
         if t.dtype is not _E4M3 or len(size) != 3 or not t.is_contiguous():
             raise BadArgError(f"{name} must be a contiguous float8_e4m3fn tensor "
@@ -461,21 +479,28 @@ def _append_q8(name, head_major, k, v, batch_idx, input_pos, dev_table, n_slots,
                err_word, stream) -> None:
     _bf16(k, "k"), _bf16(v, "v")
     _i32(batch_idx, "batch_idx"), _i32(input_pos, "input_pos"), _i32(dev_table, "dev_table")
+    if err_word is not None:
+        _word(err_word)
     Hkv, D, block = _q8_cache(k_cache, v_cache, k_scale, v_scale, n_pages * page_size)
-    shape = k.shape
-    if len(shape) != 3 or v.shape != shape:
-        raise BadArgError(f"{name}: k and v must have one shape of three dimensions")
-    if head_major:
-        heads, N, width = shape
-    else:
-        N, heads, width = shape
-    if heads != Hkv or width != D:
-        raise BadArgError(f"{name}: k, v and the caches differ in heads or head dim")
-    if input_pos is None or input_pos.numel() < N or (
-            batch_idx is not None and batch_idx.numel() < N):
-        raise BadArgError(f"{name}: batch_idx and input_pos must hold a value for every token")
-    if dev_table is None or dev_table.numel() < n_slots * max_pages_per_seq:
-        raise BadArgError(f"{name}: dev_table must be [n_slots][max_pages_per_seq]")
+    try:
+        shape = k.shape
+        if len(shape) != 3 or v.shape != shape:
+            raise BadArgError(f"{name}: k and v must have one shape of three dimensions")
+        if head_major:
+            heads, N, width = shape
+        else:
+            N, heads, width = shape
+        if heads != Hkv or width != D:
+            raise BadArgError(f"{name}: k, v and the caches differ in heads or head dim")
+        if input_pos is None or input_pos.numel() < N or (
+                batch_idx is not None and batch_idx.numel() < N):
+            raise BadArgError(f"{name}: batch_idx and input_pos must hold a value for every "
+                              "token")
+        if dev_table is None or dev_table.numel() < n_slots * max_pages_per_seq:
+            raise BadArgError(f"{name}: dev_table must be [n_slots][max_pages_per_seq]")
+    except AttributeError:
+        raise BadArgError(f"{name}: k, v, batch_idx, input_pos and dev_table must be tensors"
+                          ) from None
     _on_device(k, v, batch_idx, input_pos, dev_table, k_cache, v_cache, k_scale, v_scale, err_word)
     lib = load_library()
     fn = lib.kv_append_prefill_q8 if head_major else lib.kv_append_q8
@@ -621,19 +646,28 @@ def paged_decode_attn_q8(q, k_cache, v_cache, k_scale, v_scale, dev_table, n_slo
     zeroed byte tensor of paged_decode_attn_q8_workspace(Hq, Hkv, D)."""
     _bf16(q, "q"), _bf16(out, "out")
     _i32(dev_table, "dev_table"), _i32(batch_idx, "batch_idx"), _i32(seq_lens, "seq_lens")
+    if err_word is not None:
+        _word(err_word)
     Hkv, D, block = _q8_cache(k_cache, v_cache, k_scale, v_scale, n_pages * page_size)
-    shape = q.shape
-    B, Hq, width = shape
-    if width != D or out.shape != shape:
-        raise BadArgError("paged_decode_attn_q8: q, out and the caches differ in shape")
-    if seq_lens is None or seq_lens.numel() < B or (
-            batch_idx is not None and batch_idx.numel() < B):
-        raise BadArgError("paged_decode_attn_q8: batch_idx and seq_lens must hold a value for "
-                          "every row")
-    if dev_table is None or dev_table.numel() < n_slots * max_pages_per_seq:
-        raise BadArgError("paged_decode_attn_q8: dev_table must be [n_slots][max_pages_per_seq]")
-    if workspace is None:
-        raise BadArgError("paged_decode_attn_q8: workspace is missing")
+    try:
+        shape = q.shape
+        if len(shape) != 3 or shape[2] != D or out.shape != shape:
+            raise BadArgError("paged_decode_attn_q8: q, out and the caches differ in shape")
+        B, Hq, _ = shape
+        if seq_lens is None or seq_lens.numel() < B or (
+                batch_idx is not None and batch_idx.numel() < B):
+            raise BadArgError("paged_decode_attn_q8: batch_idx and seq_lens must hold a value "
+                              "for every row")
+        if dev_table is None or dev_table.numel() < n_slots * max_pages_per_seq:
+            raise BadArgError("paged_decode_attn_q8: dev_table must be [n_slots]"
+                              "[max_pages_per_seq]")
+        if workspace is None:
+            raise BadArgError("paged_decode_attn_q8: workspace is missing")
+        if not workspace.is_contiguous():
+            raise BadArgError("paged_decode_attn_q8: workspace must be a contiguous tensor")
+    except AttributeError:
+        raise BadArgError("paged_decode_attn_q8: q, out, batch_idx, seq_lens, dev_table and "
+                          "workspace must be tensors") from None
     _on_device(q, k_cache, v_cache, k_scale, v_scale, dev_table, batch_idx, seq_lens, workspace,
                out, err_word)
     _check(load_library().paged_decode_attn_q8(
