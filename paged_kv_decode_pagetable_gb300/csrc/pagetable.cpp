@@ -45,10 +45,17 @@ namespace {
 
 int pages_needed(int cap, int seq_len, int ps) {
   if (seq_len <= cap) return 0;
-  return (seq_len - cap + ps - 1) / ps;
+  return static_cast<int>((static_cast<long long>(seq_len) - cap + ps - 1) / ps);
 }
 
-int write_row_range(pkv_pt *pt, int slot, int begin, int count) {
+// Whether a slot of `cap` tokens may have k more pages: the row has room and the capacity
+// stays within an int.
+bool row_holds(const pkv_pt *pt, int cap, int k) {
+  return static_cast<long long>(cap) / pt->page_size + k <= pt->max_pages &&
+         cap + static_cast<long long>(k) * pt->page_size <= 0x7fffffffLL;
+}
+
+int write_row_range(pkv_pt *pt, int slot, int begin, long long count) {
   if (!pt->dev_table || count <= 0) return PKV_OK;
   size_t off = static_cast<size_t>(slot) * pt->max_pages + begin;
   PKV_CUDA_CHECK(cudaMemcpyAsync(pt->dev_table + off, pt->table.data() + off,
@@ -74,7 +81,7 @@ int pt_create(int max_batch_size, int page_size, int n_pages,
               int max_pages_per_seq, int32_t *dev_table, void *stream,
               pkv_pt **out) {
   if (!out) return pkv::fail(PKV_E_BAD_ARG, "pt_create: out is NULL");
-  if (max_batch_size < 1 || page_size < 1 || n_pages < 2 ||
+  if (max_batch_size < 1 || max_batch_size == 0x7fffffff || page_size < 1 || n_pages < 2 ||
       max_pages_per_seq < 1)
     return pkv::fail(PKV_E_BAD_ARG,
                      "pt_create: need max_batch_size>=1, page_size>=1, "
@@ -90,16 +97,21 @@ int pt_create(int max_batch_size, int page_size, int n_pages,
   pt->max_pages = max_pages_per_seq;
   pt->dev_table = dev_table;
   pt->stream = static_cast<cudaStream_t>(stream);
-  pt->table.assign(static_cast<size_t>(pt->n_slots) * max_pages_per_seq, -1);
-  std::fill(pt->table.begin(), pt->table.begin() + max_pages_per_seq, 0);
-  pt->capacity.assign(pt->n_slots, 0);
-  pt->pages.assign(pt->n_slots, {});
-  pt->live.assign(pt->n_slots, 0);
-  pt->refs.assign(n_pages, 0);
-  pt->free_pages.reserve(n_pages);
-  for (int p = n_pages - 1; p >= 1; --p) pt->free_pages.push_back(p);
-  for (int s = max_batch_size; s >= 1; --s) pt->free_slots.push_back(s);
-  int st = write_row_range(pt, 0, 0, pt->n_slots * max_pages_per_seq);
+  try {
+    pt->table.assign(static_cast<size_t>(pt->n_slots) * max_pages_per_seq, -1);
+    std::fill(pt->table.begin(), pt->table.begin() + max_pages_per_seq, 0);
+    pt->capacity.assign(pt->n_slots, 0);
+    pt->pages.assign(pt->n_slots, {});
+    pt->live.assign(pt->n_slots, 0);
+    pt->refs.assign(n_pages, 0);
+    pt->free_pages.reserve(n_pages);
+    for (int p = n_pages - 1; p >= 1; --p) pt->free_pages.push_back(p);
+    for (int s = max_batch_size; s >= 1; --s) pt->free_slots.push_back(s);
+  } catch (...) {
+    delete pt;
+    return pkv::fail(PKV_E_BAD_ARG, "pt_create: out of host memory");
+  }
+  int st = write_row_range(pt, 0, 0, 1LL * pt->n_slots * max_pages_per_seq);
   if (st != PKV_OK) {
     delete pt;
     return st;
@@ -132,7 +144,7 @@ int pt_can_reserve(const pkv_pt *pt, int seq_len, int slot, int *ok) {
     *ok = !pt->free_slots.empty() &&
           static_cast<long long>(pt->free_pages.size()) * pt->page_size >=
               seq_len &&
-          k <= pt->max_pages;
+          row_holds(pt, 0, k);
     return pkv::ok();
   }
   if (!valid_live(pt, slot))
@@ -140,8 +152,7 @@ int pt_can_reserve(const pkv_pt *pt, int seq_len, int slot, int *ok) {
                      slot);
   int cap = pt->capacity[slot];
   int k = pages_needed(cap, seq_len, pt->page_size);
-  *ok = k <= static_cast<int>(pt->free_pages.size()) &&
-        cap / pt->page_size + k <= pt->max_pages;
+  *ok = k <= static_cast<int>(pt->free_pages.size()) && row_holds(pt, cap, k);
   return pkv::ok();
 }
 
@@ -150,13 +161,18 @@ static int reserve_impl(pkv_pt *pt, int slot, int seq_len) {
   int k = pages_needed(cap, seq_len, pt->page_size);
   if (k == 0) return PKV_OK;
   int start = cap / pt->page_size;
-  if (start + k > pt->max_pages)
+  if (!row_holds(pt, cap, k))
     return pkv::fail(PKV_E_BAD_ARG,
                      "reserve: %d tokens exceed the table row (%d pages)",
                      seq_len, pt->max_pages);
   if (k > static_cast<int>(pt->free_pages.size()))
     return pkv::fail(PKV_E_NO_PAGES, "reserve: need %d pages, %zu free", k,
                      pt->free_pages.size());
+  try {
+    pt->pages[slot].reserve(pt->pages[slot].size() + k);
+  } catch (...) {
+    return pkv::fail(PKV_E_BAD_ARG, "reserve: out of host memory");
+  }
   // take the tail free_pages[-k:] in list order for blocks start..start+k-1
   size_t first = pt->free_pages.size() - k;
   int32_t *row = pt->table.data() + static_cast<size_t>(slot) * pt->max_pages;
@@ -192,7 +208,7 @@ int pt_assign(pkv_pt *pt, int seq_len, int *slot_out) {
   if (pt->free_slots.empty())
     return pkv::fail(PKV_E_NO_SLOT, "pt_assign: no free slot");
   int k = pages_needed(0, seq_len, pt->page_size);
-  if (k > pt->max_pages)
+  if (!row_holds(pt, 0, k))
     return pkv::fail(PKV_E_BAD_ARG,
                      "pt_assign: %d tokens exceed the table row (%d pages)",
                      seq_len, pt->max_pages);
@@ -200,6 +216,11 @@ int pt_assign(pkv_pt *pt, int seq_len, int *slot_out) {
     return pkv::fail(PKV_E_NO_PAGES, "pt_assign: need %d pages, %zu free", k,
                      pt->free_pages.size());
   int slot = pt->free_slots.back();
+  try {   // room first, so that nothing below can fail
+    pt->pages[slot].reserve(k);
+  } catch (...) {
+    return pkv::fail(PKV_E_BAD_ARG, "pt_assign: out of host memory");
+  }
   pt->free_slots.pop_back();
   pt->live[slot] = 1;
   pt->capacity[slot] = 0;
@@ -388,7 +409,7 @@ int pt_compact(pkv_pt *pt, int32_t *pairs_out, int max_pairs, int *n_pairs) {
   pt->free_pages.clear();   // its room was reserved when the table was made
   for (int p = pt->n_pages - 1; p > used; --p) pt->free_pages.push_back(p);
   if (n > 0) {
-    const int st = write_row_range(pt, 0, 0, pt->n_slots * pt->max_pages);
+    const int st = write_row_range(pt, 0, 0, 1LL * pt->n_slots * pt->max_pages);
     if (st != PKV_OK) return st;
   }
   return pkv::ok();
