@@ -294,7 +294,9 @@ __global__ void __launch_bounds__(kWarps * 32, CTA || KEEP == 2 ? 8 : 6)
                                  static_cast<long long>(page) * a.page_size + in_page;
           uint8_t *codes = (kv ? a.v_cache : a.k_cache) + row0 * a.D;
           float *scale = (kv ? a.v_scale : a.k_scale) + (row0 >> a.log2_block);
-          const float held_raw = first ? *scale : 0.f;
+          // read by the lane that replaces it (the maximum's exchange orders no memory
+          // between lanes), or by all threads of a CTA, whose barrier does
+          float held_raw = first && (CTA || gl == 0) ? *scale : 0.f;
           __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
 #pragma unroll
           for (int j = 0; j < KEEP; ++j) m2 = max_abs(max_abs(m2, keep[j].lo), keep[j].hi);
@@ -312,6 +314,8 @@ __global__ void __launch_bounds__(kWarps * 32, CTA || KEEP == 2 ? 8 : 6)
             }
             amax = group_max(max(as_u32(m2) & 0xffffu, as_u32(m2) >> 16));
           }
+          if constexpr (!CTA)
+            if (first) held_raw = __shfl_sync(gmask, held_raw, g0);
           const float held = held_raw > 0.f && held_raw < INFINITY ? held_raw : 0.f;
           int e = need_exponent(amax);
           if (held > 0.f) {   // the held scale, rounded up to a power of two
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTA || KEEP == 2 ? 8 : 6)
                                   rescale4(c.w, ratio));
             }
           }
-          if (gl == 0) *scale = s;   // (the group has read the held one before its maximum)
+          if (gl == 0) *scale = s;
           // pass 2: the codes
           const __nv_bfloat162 inv2 = __float2bfloat162_rn(inv);
           uint4 *dst = reinterpret_cast<uint4 *>(codes);
