@@ -208,8 +208,8 @@ int kv_append_prefill(const pkv_bf16 *k, const pkv_bf16 *v, const int32_t *batch
  * and where s exceeds the scale held, the block's rows before the call's first
  * become e4m3(code * held / s) (exact but for values that leave e4m3's normal
  * range). Scales so written are powers of two; one held that is not is
- * rounded up to one first, and one that is not finite and positive counts as
- * 0, which clears the rows before. Rows of the block behind the call's
+ * rounded up to one first (2^126 at most), and one that is not finite and
+ * positive counts as 0, which clears the rows before. Rows of the block behind the call's
  * tokens are not rescaled: appending in the middle of a block drops what it
  * held behind. Rows on slot 0 (padding) are skipped.
  * The tokens of one block must stand next to each other in the call, at
@@ -371,8 +371,8 @@ size_t paged_decode_attn_workspace(int B, int Hq, int D, int num_splits);
  *   out[b][h] = sum_j softmax_j(scale * q[b][h] . k_j) v_j
  * Keys, rows without keys, windows, GQA, table errors and argument limits are
  * paged_decode_attn's, with Hkv <= 65535; q must be finite and the scores
- * below 2^26 in magnitude (fp32 tells larger ones apart by 4 and more; there
- * the output is some mean of the values, or 0). Values at positions outside a row's keys are never
+ * below 2^26 in magnitude (fp32 tells larger ones apart by 4 and more only).
+ * Values at positions outside a row's keys are never
  * used (codes there may be NaN, scales anything). A query row enters the
  * product with K as fp16 scaled to its largest element: exact but for elements
  * below 2^-29 of that one, which lose 2^-40 of it. Scores, softmax statistics

@@ -4,13 +4,14 @@
 //   s_j = scale * sk_j * (q . ck_j),  out = sum_j softmax(s)_j sv_j cv_j
 //
 // Bound by reading the codes and scales of every key once. Measured against the measured
-// 6789 GB/s: 16 rows of 16k to 32k tokens (8 heads of 128, blocks of 32) 124.2 us, 0.96;
-// 256 rows of 500 to 1500 tokens 89 us, 0.88; 64 rows of 100 to 1024 tokens 19.0 us, 0.58;
-// 64 rows of 256 to 2048 tokens with one 512-wide head 23.5 us, 0.48; one row of 32k
-// tokens 18.9 us, 0.52; 64-wide heads, 16 rows of 8k to 16k tokens 50.6 us, 0.59. Without
-// its arithmetic the kernel takes 16.5 and 40 us for the 64 rows and the 64-wide ones: what
-// small calls cost beyond their bytes is the start (launch, row set-up, page lookups, the
-// first tiles' latency: about 5 us) and the joins (2 to 5 us).
+// 6789 GB/s: 16 rows of 16k to 32k tokens (8 heads of 128, blocks of 32) 123.3 us, 0.96;
+// 256 rows of 500 to 1500 tokens 88.9 us, 0.88; 64 rows of 100 to 1024 tokens 19.2 us, 0.57;
+// 64 rows of 256 to 2048 tokens with one 512-wide head 23.4 us, 0.48; one row of 32k
+// tokens 19.0 us, 0.52; 64-wide heads, 16 rows of 8k to 16k tokens 51.5 us, 0.58. Without
+// its arithmetic (an earlier state, of 19.0 and 50.6) the kernel took 16.5 and 40 us for the
+// 64 rows and the 64-wide ones: what small calls cost beyond their bytes is the start (launch,
+// row set-up, page lookups, the first tiles' latency: about 5 us) and the joins (2 to 5 us);
+// at D = 64 the fixed work of a tile of 4 KB.
 // Design (GB300):
 //   * work: the 64-key tiles of every (row, kv head), plus START positions for each
 //     start of a (row, head), laid on one line from the actual lengths; every
@@ -54,13 +55,13 @@
 //     brings its row's largest magnitude to 2^15 .. 2^16, so it is exact in fp16 too (elements
 //     below 2^-29 of the largest lose at most 2^-40 of it). The scale of v is part of
 //     the softmax weight: w_j = 2^(s_j + log2 sv_j - M) with M the running
-//     maximum of that sum, so w is at most 1 however far the scales lie
-//     apart; the denominator keeps a running maximum of its own, per lane. w enters the
-//     product as fp16 times 2^15, so that weights down to 2^-29 keep 11 bits and none above
-//     2^-40 is lost (times 1, a key 2^-25 as heavy as its warp's heaviest would add nothing);
-//     the factor goes where the warps' states are joined. The sum is rounded up for M alone and w taken
-//     as 2^((s_j - M) + log2 sv_j), whose difference is exact where w counts: added to a
-//     score of 10^5 the logarithm would keep 7 bits behind the point;
+//     maximum of that sum, so w is at most 1 however far the scales lie apart; the
+//     denominator keeps a running maximum of its own, per lane. w enters the product as
+//     fp16 times 2^15, so that weights down to 2^-29 keep 11 bits and none above 2^-40 is
+//     lost (times 1, a key 2^-25 as heavy as its warp's heaviest would add nothing); the
+//     factor goes where the warps' states are joined. The sum is rounded up for M alone and
+//     w taken as 2^((s_j - M) + log2 sv_j), whose difference is exact where w counts: added
+//     to a score of 10^5 the logarithm would keep 7 bits behind the point;
 //   * every wait is bounded; one that gives up sets PKV_ERR_TIMEOUT,
 //     the CTA drains its copies and exits. Invalid table entries are reported
 //     and never dereferenced.
@@ -95,17 +96,18 @@ constexpr int kMergeRow = kMergeCols + 4;   // padded: conflict-free 8-byte stor
 
 template <int D>
 struct Cfg {
-  // One CTA per SM, at the same shared memory a CTA: D = 128 rollout batch 18.8 -> 24.8 us, 16
-  // long rows 124 -> 168; D = 256 mixed (16 rows of 8k to 16k tokens 40.4 -> 43.0, 64 rows of
-  // 256 to 2048 16.5 -> 15.3, sliding 11.8 -> 12.1); D = 512 has room for one. Three at
-  // D = 64: 16 rows of 8k to 16k tokens 51.5 -> 49.2, one short row 3.62 -> 3.70.
+  // One CTA per SM: D = 128 rollout batch 19.3 -> 24.9 us, 16 long rows 123 -> 169; D = 256
+  // mixed (16 rows of 8k to 16k tokens 39.7 -> 43.1, 64 rows of 256 to 2048 16.2 -> 14.9,
+  // sliding 11.2 -> 11.5); D = 512 has room for one. Three at D = 64, with half the ring: 16
+  // rows of 8k to 16k tokens 51.5 -> 48.0, one short row 3.6 -> 4.1.
   static constexpr int CTAS_PER_SM = D <= 256 ? 2 : 1;
   // What starting a (row, head) costs, in tiles (a unit's state, its query and the part
-  // of its last tile not used). Rollout batch, D = 128: 1 21.6 us, 2 19.9, 3 19.7, 4 20.1;
-  // 64 rows at D = 512: 1 25.0, 2 23.7, 3 23.4.
+  // of its last tile not used). 1, 2, 3, 4: rollout batch at D = 128 20.2, 18.8, 19.3, 19.7
+  // us; 64 rows at D = 256 17.4, 16.4, 16.2, 15.9, at D = 512 24.4, 23.8, 23.4, 23.9.
   static constexpr int START = 3;
-  // 16-key blocks of a tile a warp owns. D = 128: 1 rollout batch 20.3 us, 256 rows 95.2;
-  // 2 18.8, 89.1; 4 22.2, 94.9. D = 256: 1 and 2 alike (sliding 11.8, 12.1).
+  // 16-key blocks of a tile a warp owns. D = 128: 1 rollout batch 20.9 us, 256 rows 98.8;
+  // 2 19.3, 88.9 (4, in an earlier state: 22.2 and 94.9 against 18.8 and 89.1). D = 256: 1 and
+  // 2 alike (sliding 11.2, 11.5).
   static constexpr int MB = D <= 128 ? 2 : 1;
   static constexpr int TEAM = kT / 16 / MB;        // warps that share a tile
   static constexpr int TEAMS = kCWarps / TEAM;
@@ -134,8 +136,8 @@ struct Cfg {
   // the warps' states of a part that is the CTA's last work, where the ring was:
   // [4][8][DUMP_ROW] f32, then m, l, M [4][8] each
   // Whether the consumer warps join whole units and first works too, round by round. At
-  // D = 512 they would wait for four rounds of the joining warp, 1.2 us each: 64 rows 25.0 ->
-  // 23.7 us, 226 rows of 58 to 227 tokens 23.9 -> 19.5. At D = 256 no difference.
+  // D = 512 they would wait for four rounds of the joining warp, 1.2 us each: 64 rows 24.8 ->
+  // 23.4 us, 226 rows of 58 to 227 tokens 22.9 -> 19.5. At D = 256 no difference.
   static constexpr bool SELF = D == 512;
   static constexpr int DUMP_ROW = D + 4;
   static constexpr int DUMP_STATS = kCWarps * kMaxG * DUMP_ROW;
@@ -390,7 +392,7 @@ struct alignas(16) Unit {
 static_assert(sizeof(Unit) <= 48, "unit descriptor slot");
 
 // The next unit from position x on (advanced past it), in row w.b at the earliest (searched
-// from there: 217 short rows 20.1 -> 18.0 us); false at the share's end. Which
+// from there: 217 short rows 18.1 -> 17.1 us); false at the share's end. Which
 // part of its (row, head) it is comes later (which_part): `first_cta` and `parts` hold
 // the (row, head)'s first position and width until then, `part` whether its first
 // (bit 0) and last tile (bit 1) are this unit's.
@@ -1330,10 +1332,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS_PER_SM)
       }
       write_stats(dump + Cf::DUMP_STATS);
       (void)consumer_sync_or(false);
-      // As many places as 8 heads have (D = 512 at once instead of half of them: 17.2 ->
-      // 15.7 us for 10 rows of 1000 tokens), and as many parts as registers allow. Up to
+      // As many places as 8 heads have (D = 512 at once instead of half of them: 17.7 ->
+      // 16.0 us for 10 rows of 1000 tokens), and as many parts as registers allow. Up to
       // 4 heads have half the places: at D = 128 one place of 8 parts instead of two of 4
-      // (B = 8 9.1 -> 8.6 us, one row of 32k tokens 19.6 -> 19.0); at D = 512 no gain.
+      // (B = 8 9.2 -> 8.5 us, one row of 32k tokens 19.6 -> 19.0); at D = 512 no gain.
       constexpr int IB = D / 64, SRC = D <= 128 ? 8 / IB : D == 256 ? 4 : 2;
       bool done = false;
       if constexpr (D == 128) {
@@ -1573,7 +1575,7 @@ int paged_decode_attn_q8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e
   p.G = Hq / Hkv;
   p.scale_log2 = scale * 1.4426950408889634f;
   // four scales at once where the rows of one copy have as many, 16-byte aligned (217 short
-  // rows with a scale a token 19.6 us, word by word 21.3)
+  // rows with a scale a token 17.1 us, word by word 18.9)
   p.scale_vec = box_rows / scale_block >= 4 && pkv::aligned16(k_scale) && pkv::aligned16(v_scale)
                     ? 4 : 1;
   p.o_part = static_cast<uint32_t *>(workspace);

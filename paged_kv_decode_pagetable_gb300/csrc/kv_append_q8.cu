@@ -13,8 +13,8 @@
 // size of a run), which finds the run's largest magnitude and the block's scale,
 // rescales older codes if the scale grew and writes the new ones. Extra CTAs look for
 // tokens of one block that stand apart. Bound by reading k and v and writing half their
-// bytes: 16411 tokens of 16 prompts (8 heads of 128, blocks of 16; 101 MB) take 21.3 us,
-// 0.70 of the measured 6789 GB/s (an elementwise copy of as many bytes: 16.1 us; the warps
+// bytes: 16411 tokens of 16 prompts (8 heads of 128, blocks of 16; 101 MB) take 21.4 us,
+// 0.69 of the measured 6789 GB/s (an elementwise copy of as many bytes: 16.1 us; the warps
 // issue in 43% of the cycles and wait for loads in most others), a decode step of 8 rows
 // 2.7 us, one of 512 rows 4.4 us, both the latency of index, table, token and store.
 #include <cuda_bf16.h>
@@ -168,9 +168,9 @@ __device__ __forceinline__ void check_order(const Args &a) {
 
 // CTA: one run at a time for the whole CTA, else for a group of lanes. KEEP: 16-value
 // units of a run that a lane keeps between the two passes. CTAs an SM, by the registers
-// left to them (us for the cases named at the launch): KEEP 2: 5 29.3 (blocks of 1), 22.3
-// (one head); 7 24.5, 19.4; 8 24.6, 19.3; 9 26.6, 20.4. KEEP 4: 4 23.7; 5 22.0; 6 21.6;
-// 7 22.6. A CTA a run: 5 25.8; 8 25.2.
+// left to them (us for the cases named at the launch): KEEP 2: 5 28.9 (blocks of 1), 21.5
+// (one head); 7 24.3, 19.1; 8 23.9, 18.7; 9 24.9, 19.4. KEEP 4: 4 23.3; 5 21.6; 6 21.4;
+// 7 21.6. A CTA a run: 5 29.3; 8 24.1.
 template <bool CTA, int KEEP>
 __global__ void __launch_bounds__(kWarps * 32, CTA || KEEP == 2 ? 8 : 6)
     append_q8_kernel(const Args a) {
@@ -404,21 +404,22 @@ int launch_append_q8(const char *fn, const pkv_bf16 *k, const pkv_bf16 *v,
   const long long run = 1LL * (head_major ? scale_block : 1) * D / 16;
   // Measured, in us (16411 tokens of 8 heads of 128 in blocks of 16 / 64 / 1; 200003 tokens
   // of one head of 64 in blocks of 16; 8200 tokens of 2 heads of 512 in blocks of 16):
-  // - few: one token of K or V a warp while the GPU holds all those warps at once, for the
-  //   shortest latency. 8 and 512 rows: 2.9 and 4.7, without it 4.4 and 12.7; used for all
-  //   calls 95 / 112 / 207, 162, 30 instead of the below; up to four times the warps: 30
-  //   instead of 12.5 for the last.
-  // - whole_cta: a CTA a run of 8 units a lane of a warp and more. 25.2 (blocks of 64) and
-  //   12.5 (512 wide); never: 37.0 and 33.7; from half that size on: 47 instead of 21.8
+  // - few: one token of K or V a warp, for the shortest latency, up to 64 warps an SM (24
+  //   to 32 of them resident at a time). 8 and 512 rows: 2.8 and 4.5, without it 4.7 and 13.0;
+  //   steps of 300, 512, 700 and 1200 rows of 8 heads of 128: 4.2, 6.2, 7.8 and 12.1, without
+  //   it 8.2, 8.2, 8.3 and 8.4; packed tokens, 300, 580, 700 and 1200: 3.6, 4.6, 5.1 and 7.1,
+  //   without it 5.3, 5.2, 5.7 and 5.4; used for all calls 78 / 92 / 147, 104, 27.
+  // - whole_cta: a CTA a run of 8 units a lane of a warp and more. 24.1 (blocks of 64) and
+  //   12.1 (512 wide); never: 34.2 and 33.0; from half that size on: 42 instead of 21.4
   //   for the first.
-  // - window: 16 tokens 21.8 / - / 24.6, 19.3; 8: 22.1 / - / 25.4, 25.2; 31: 23.4 / - /
-  //   25.2, 21.1. A CTA takes a block's tokens: 25.2 for 64; 16 of them: 31.3.
-  // - tensors: K and V one after the other, which share what is looked up: 21.8 / - / 24.6,
-  //   19.3; a warp each: 22.9 / - / 28.2, 22.1. (A CTA or a lone token: one, for more warps.)
-  // - group: two units of a run a lane, four lanes at least: 24.6 (blocks of 1); one unit
-  //   a lane 33.9; always a whole warp 103.
-  // - KEEP: room for two units where a run fits that: 24.6 and 19.3, for four 31.1 and 22.5;
-  //   for two only, with the others read again: 27.9 instead of 21.8.
+  // - window: 16 tokens 21.4 / - / 23.9, 18.7; 8: 21.5 / - / 24.5, 24.1; 31: 23.1 / - /
+  //   24.6, 20.5. A CTA takes a block's tokens: 24.1 for 64; 16 of them: 29.1.
+  // - tensors: K and V one after the other, which share what is looked up: 21.4 / - / 23.9,
+  //   18.7; a warp each: 22.2 / - / 27.2, 20.8. (A CTA or a lone token: one, for more warps.)
+  // - group: two units of a run a lane, four lanes at least: 23.9 (blocks of 1); one unit
+  //   a lane 33.5; always a whole warp 102.
+  // - KEEP: room for two units where a run fits that: 23.9 and 18.7, for four 30.6 and 21.9;
+  //   for two only, with the others read again: 26.9 instead of 21.4.
   const bool few = 2LL * N * Hkv <= 64LL * sms;
   const bool whole_cta = !few && run >= 256;
   a.window = few ? 1 : whole_cta && scale_block > 16 ? scale_block : 16;
