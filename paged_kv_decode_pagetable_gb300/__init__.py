@@ -540,7 +540,9 @@ def kv_copy_pages(caches, n_pages, pairs, stream=None) -> None:
         try:
             given = torch.tensor(list(pairs))
             pairs = given.to(torch.int32).reshape(-1, 2)
-            if given.numel() and (given.dtype != torch.int64 or (given.reshape(-1, 2) != pairs).any()):
+            if given.numel() and (given.dtype.is_floating_point or given.dtype.is_complex
+                                  or given.dtype == torch.bool
+                                  or (given.reshape(-1, 2) != pairs).any()):
                 raise ValueError("not whole numbers of 32 bits")
         except (TypeError, ValueError, RuntimeError) as e:
             raise BadArgError(f"kv_copy_pages: pairs must be (source, destination)s: {e}") from None

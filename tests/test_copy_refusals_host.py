@@ -1,4 +1,5 @@
 """Lists of caches and of pairs that kv_copy_pages refuses as bad arguments (no GPU needed)."""
+import numpy as np
 import pytest
 import torch
 
@@ -25,3 +26,11 @@ def test_caches(caches):
 def test_pairs(pairs):
     with pytest.raises(pkv.BadArgError, match="pairs"):
         pkv.kv_copy_pages([], 4, pairs)
+
+
+@pytest.mark.parametrize("pairs", [np.array([[1, 2], [3, 0]], np.int32), [(1, 2)], ((1, 2), (3, 0)),
+                                   np.array([[1, 2]]), [np.array([1, 2], np.int16)], [],
+                                   np.zeros((0, 2), np.int32), iter([(1, 2)]),
+                                   torch.tensor([[1, 2]], dtype=torch.int32)])
+def test_whole_numbers_of_any_kind_are_taken(pairs):
+    pkv.kv_copy_pages([], 4, pairs)
