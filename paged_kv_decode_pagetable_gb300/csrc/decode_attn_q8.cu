@@ -27,7 +27,7 @@
 //     but is not first its CTA's only work, so they find the others written, or
 //     wait for CTAs that began with that very work. The shares are given out from the
 //     line's end: a part's takers lie before it on the line, so a CTA waits only for CTAs
-//     with lower block numbers, which were started before it, and a call ends however few
+//     with lower block numbers, which are started before it, and a call ends however few
 //     CTAs can be resident beside other work (given out from the front, three or four CTAs
 //     that each wait for one not started could hold all there is);
 //   * one producer warp streams query rows (cp.async.bulk), K and V tiles
