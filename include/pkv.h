@@ -78,6 +78,8 @@ typedef struct pkv_pt pkv_pt;
 #define PKV_ERR_SLOT 8         /* batch index outside [0, n_slots) */
 #define PKV_ERR_TIMEOUT 16     /* a bounded wait (for a copy, or for another part of a row) gave up */
 #define PKV_ERR_ORDER 32       /* 8-bit append: tokens of one scale block apart in the call */
+#define PKV_ERR_TREE 64        /* drafted trees: row_start, parents or a path malformed */
+#define PKV_ERR_PROB 128       /* tree_verify: a row of probabilities without any, a token outside */
 
 /* ---------------------------------------------------------------------
  * PageTable allocator (host) — [P3] PageTable.__init__ / can_reserve /
@@ -555,6 +557,127 @@ int paged_decode_attn_noalloc(const pkv_bf16 *q, const pkv_bf16 *k_cache,
                               const int32_t *seq_lens, int window, float scale,
                               int B, int Hq, int Hkv, int D, int num_splits,
                               pkv_bf16 *out, int32_t *err_word, void *stream);
+
+/* ---------------------------------------------------------------------
+ * Speculative steps: several drafted tokens a row are appended, attended to
+ * and verified at once, and the accepted ones kept. The pages decode one token
+ * a step; these calls extend their attention forward ([P1]: norm, rotary,
+ * paged write, attention) to a tree of tokens.
+ *
+ * A row b has ctx_lens[b] tokens in the cache (all its committed tokens but
+ * the last) and up to PKV_TREE_MAX "nodes": node 0, the last committed token,
+ * and the drafts that may follow it. The nodes of all rows are packed: row b's
+ * are row_start[b] .. row_start[b + 1] - 1 of the N packed ones (row_start:
+ * int32 [B + 1], ascending). parents (int32 [N]) gives each node's parent by
+ * its index inside its row, lower than its own; -1 for a root (node 0; a
+ * further root sees the context only). Node i of a row is stored at cache
+ * position ctx + i and rotated for position ctx + depth(i), depth 0 for roots.
+ * A chain of drafts is parents -1, 0, 1, 2, .. .
+ *
+ * All four read this from device memory, so that a captured call serves any
+ * trees of up to B rows and N nodes: rows may be empty (row_start equal), and
+ * packed nodes outside every row are neither read nor written. A row whose
+ * nodes lie outside [0, N) or are more than PKV_TREE_MAX, a path that does not
+ * ascend (PKV_ERR_TREE), a bad slot (PKV_ERR_SLOT) or tokens beyond the table
+ * row (PKV_ERR_POS) are reported and the row skipped; a parent that does not
+ * lie before its node is reported (PKV_ERR_TREE) and counts as -1. Rows on
+ * slot 0 are padding. B <= 512 (65535 for tree_verify and kv_keep_path). Rows
+ * name distinct slots, and pages that a row's nodes fall on must be its own
+ * (pt_unshare). bf16 caches.
+ * ------------------------------------------------------------------- */
+#define PKV_TREE_MAX 64
+
+/* tree_qkv_norm_rope_append — the step's prologue, qkv_norm_rope and kv_append
+ * for trees in one kernel: q is normalised, rotated and written to q_out (bf16
+ * [N][Hq][D]; may be q itself when q_stride is Hq * D); k is normalised and
+ * rotated into the row's pages, v goes there as it is, or divided by its root
+ * mean square when v_norm != 0. v NULL: the value is the raw k (K = V). q, k
+ * and v are bf16 [N][heads][D] with q_stride, k_stride and v_stride elements
+ * from one token to the next (multiples of 8: parts of a fused projection's
+ * rows will do) and are only read. gamma_q / gamma_k: bf16 [D], both or
+ * neither (no norm of q and k). rotary_dims as in qkv_norm_rope. The rotation
+ * angle is exact to 2^-24 of a half turn at any position. Rows on slot 0 land
+ * in page 0. Requires D in {64, 128, 256, 512}, Hq >= 1, Hkv >= 1, theta
+ * finite and > 0, 16-byte aligned tensors. */
+int tree_qkv_norm_rope_append(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v,
+                              int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                              const pkv_bf16 *gamma_q, const pkv_bf16 *gamma_k,
+                              const int32_t *batch_idx, const int32_t *ctx_lens,
+                              const int32_t *row_start, const int32_t *parents, float theta,
+                              float eps, int rotary_dims, int v_norm, int B, int N, int Hq,
+                              int Hkv, int D, const int32_t *dev_table, int n_slots,
+                              int max_pages_per_seq, int page_size, int n_pages,
+                              pkv_bf16 *k_cache, pkv_bf16 *v_cache, pkv_bf16 *q_out,
+                              int32_t *err_word, void *stream);
+
+/* paged_tree_attn — paged_decode_attn for trees: node t's query sees the keys
+ * j < ctx of its row's context and those of the nodes on its path to its root,
+ * itself included (its nodes' keys and values are in the cache already); with
+ * a window W > 0 only keys less than W positions behind its own, a node's
+ * position being ctx + its depth.
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j
+ * q, out: bf16 [N][Hq][D]. Query head h reads kv head h / (Hq / Hkv). Nodes of
+ * slot 0 give zeros. Values that a node does not see never reach it, whatever
+ * they hold. Table entries that are negative or >= n_pages inside a row's key
+ * range set PKV_ERR_PAGE_* (that row's output is then unspecified). Requires
+ * D in {64, 128, 256, 512}, 1 <= Hq / Hkv <= 8, page_size a power of two >= 8,
+ * scale finite and > 0, 16-byte aligned tensors. The workspace (any contents,
+ * paged_tree_attn_workspace(Hq, Hkv, D) bytes, whatever the batch; 0 for sizes
+ * the call refuses) holds parts of rows during a call: calls that share one
+ * must not overlap on the GPU. */
+int paged_tree_attn(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,
+                    const int32_t *dev_table, int n_slots, int max_pages_per_seq,
+                    int page_size, int n_pages, const int32_t *batch_idx,
+                    const int32_t *ctx_lens, const int32_t *row_start,
+                    const int32_t *parents, int window, float scale, int B, int N,
+                    int Hq, int Hkv, int D, void *workspace, size_t workspace_bytes,
+                    pkv_bf16 *out, int32_t *err_word, void *stream);
+size_t paged_tree_attn_workspace(int Hq, int Hkv, int D);
+
+/* tree_verify — which drafts stay, and the token behind them. target_probs:
+ * fp32 [N][V] (target_stride words a row), the target's probabilities after
+ * each node; draft_probs: the same of the draft model (the distribution its
+ * children were drawn from), or NULL for drafts chosen without chance. tokens:
+ * int32 [N], each node's token. A row's walk starts at node 0 (other roots are
+ * not reached) and tries the current node's children in index order; with p
+ * and q the rows of the current node and k children refused so far,
+ *   w = max(p - a_k q, 0), S_k = sum of w, a_0 = 0, S_0 = 1, a_k+1 = a_k + S_k
+ * child c with token x is accepted when u_accept[c] q(x) S_k < w(x), and becomes
+ * the current node. Without q, w is p without the refused tokens, S_k is 1
+ * minus their sum and q(x) is 1. When no child is left the next token is the
+ * least i with w(0) + .. + w(i) > u_pick[row] * (the sum of all w); where that
+ * sum is 0, of p itself. So outputs are distributed as the target's if siblings
+ * are independent draws from q (or do not depend on chance).
+ * accepted (int32 [B]) receives the number of accepted drafts, path (int32 [B]
+ * [path_cols]) node 0 and theirs in order, then -1, next_token (int32 [B]) the
+ * token. Probabilities: in [0, 1], a row summing to 1 but for rounding (other
+ * values count as the nearest, NaN as 0; a sum of 4096 or more gives an
+ * unspecified token); u in [0, 1). Sums are exact to 2^-52 a term. An empty or
+ * reported row gives 0, -1s and -1; path_cols must hold every row's nodes
+ * (PKV_ERR_TREE). A token outside [0, V) is never accepted, and a p without any
+ * probability gives -1 (PKV_ERR_PROB). V <= 2^22. */
+int tree_verify(const float *target_probs, int64_t target_stride, const float *draft_probs,
+                int64_t draft_stride, const int32_t *tokens, const int32_t *row_start,
+                const int32_t *parents, const float *u_accept, const float *u_pick, int B,
+                int N, int V, int path_cols, int32_t *accepted, int32_t *path,
+                int32_t *next_token, int32_t *err_word, void *stream);
+
+/* kv_keep_path — after tree_verify, for t = 1 .. accepted[b] cache token
+ * ctx + path[b][t] of row b becomes its token ctx + t, in every cache: the
+ * context is then ctx + 1 + accepted tokens long (what lies behind is stale).
+ * A cache is heads[c] x n_pages * page_size tokens of token_bytes[c] contiguous
+ * bytes, any element type (for an 8-bit cache: one scale a token, the codes and
+ * the scales as caches of their own). caches, heads and token_bytes are host
+ * arrays; accepted and path as tree_verify writes them (path: int32 [B]
+ * [path_cols]). Table entries out of range set PKV_ERR_PAGE_* and the row is
+ * left as it is, in all caches. Any alignment; 16-byte aligned caches and
+ * tokens copy fastest. token_bytes <= 2^20. */
+int kv_keep_path(void *const *caches, const int *heads, const int64_t *token_bytes,
+                 int n_caches, const int32_t *dev_table, int n_slots,
+                 int max_pages_per_seq, int page_size, int n_pages,
+                 const int32_t *batch_idx, const int32_t *ctx_lens,
+                 const int32_t *accepted, const int32_t *path, int path_cols, int B,
+                 int32_t *err_word, void *stream);
 
 /* ---------------------------------------------------------------------
  * Utilities

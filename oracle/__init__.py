@@ -34,6 +34,7 @@ from .prefill import prefill_attention, prefill_block_mask, keep_matrix
 from .paged_q8 import (kv_append_q8, dequantise, round_e4m3, need_scale, pow2_at_least,
                        ERR_ORDER)
 from .block_mask import convert_logical_block_mask
+from . import tree
 
 __all__ = [
     "PageTableModel", "NoSlot", "NoPages", "BadSlot", "BadArg", "PageTableError",
@@ -43,4 +44,5 @@ __all__ = [
     "prefill_block_mask", "keep_matrix", "convert_logical_block_mask",
     "decode_attention", "decode_attention_row",
     "kv_append_q8", "dequantise", "round_e4m3", "need_scale", "pow2_at_least", "ERR_ORDER",
+    "tree",
 ]

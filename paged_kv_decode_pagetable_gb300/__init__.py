@@ -32,6 +32,8 @@ PKV_ERR_PAGE_NEG = 4
 PKV_ERR_SLOT = 8
 PKV_ERR_TIMEOUT = 16
 PKV_ERR_ORDER = 32
+PKV_ERR_TREE = 64
+PKV_ERR_PROB = 128
 
 
 class PkvError(RuntimeError):
@@ -61,6 +63,7 @@ class CudaError(PkvError):
 _ERRORS = {c.code: c for c in (NoSlotError, NoPagesError, BadSlotError, BadArgError, CudaError)}
 
 _c_int, _c_p, _c_f, _c_sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_float, ctypes.c_size_t
+_c_i64 = ctypes.c_int64
 _c_ip = ctypes.POINTER(ctypes.c_int32)
 
 _SIGS = {
@@ -127,6 +130,18 @@ _SIGS = {
                                    _c_int, _c_int, _c_int, _c_int, _c_p, _c_p, _c_int, _c_f,
                                    _c_int, _c_int, _c_int, _c_int, _c_int, _c_p, _c_sz, _c_p,
                                    _c_p, _c_p]),
+    "tree_qkv_norm_rope_append": (_c_int, [_c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p,
+                                           _c_p, _c_p, _c_p, _c_p, _c_f, _c_f, _c_int, _c_int,
+                                           _c_int, _c_int, _c_int, _c_int, _c_int, _c_p, _c_int,
+                                           _c_int, _c_int, _c_int, _c_p, _c_p, _c_p, _c_p, _c_p]),
+    "paged_tree_attn": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_int, _c_int, _c_int, _c_int, _c_p,
+                                 _c_p, _c_p, _c_p, _c_int, _c_f, _c_int, _c_int, _c_int, _c_int,
+                                 _c_int, _c_p, _c_sz, _c_p, _c_p, _c_p]),
+    "paged_tree_attn_workspace": (_c_sz, [_c_int, _c_int, _c_int]),
+    "tree_verify": (_c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_int,
+                             _c_int, _c_int, _c_int, _c_p, _c_p, _c_p, _c_p, _c_p]),
+    "kv_keep_path": (_c_int, [_c_p, _c_p, _c_p, _c_int, _c_p, _c_int, _c_int, _c_int, _c_int,
+                              _c_p, _c_p, _c_p, _c_p, _c_int, _c_int, _c_p, _c_p]),
     "pkv_read_error_word": (_c_int, [_c_p, _c_p, _c_ip]),
     "pkv_last_error": (ctypes.c_char_p, []),
 }
@@ -817,6 +832,218 @@ def prefill_attn(q, k, v, block_mask: PrefillBlockMask, scale, out, stream=None)
         _ptr(q), _ptr(k), _ptr(v), _ptr(bm.docs), _ptr(bm.kv_num_blocks), _ptr(bm.kv_indices),
         _ptr(bm.full_kv_num_blocks), _ptr(bm.full_kv_indices), L, Hq, Hkv, D, bm.window,
         float(scale), _ptr(out), _stream(stream)), "prefill_attn")
+
+
+# --------------------------------------------------------------------------
+# speculative steps: trees of drafted tokens
+# --------------------------------------------------------------------------
+
+TREE_MAX = 64
+
+
+def _is_tensor(name, **tensors) -> None:
+    """Refuses what is no tensor (missing ones too)."""
+    for what, t in tensors.items():
+        if not isinstance(t, torch.Tensor):
+            raise BadArgError(f"{name}: {what} must be a tensor")
+
+
+def _tree(name, N, row_start, parents) -> int:
+    """Checks the packed trees of a call; returns the number of rows."""
+    _at_least(name, "row_start", row_start, 1)
+    _at_least(name, "parents", parents, N)
+    return row_start.numel() - 1
+
+
+def _tree_rows(name, B, batch_idx, ctx_lens) -> None:
+    _at_least(name, "ctx_lens", ctx_lens, B)
+    if batch_idx is not None:
+        _at_least(name, "batch_idx", batch_idx, B)
+
+
+def _at_least(name, what, t, n) -> None:
+    _is_tensor(name, **{what: t})
+    _i32(t, what)
+    if t.numel() < n:
+        raise BadArgError(f"{name}: {what} must hold {n} values")
+
+
+def _tree_cache(name, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq, page_size,
+                n_pages) -> tuple:
+    _is_tensor(name, k_cache=k_cache, v_cache=v_cache, dev_table=dev_table)
+    _bf16(k_cache, "k_cache"), _bf16(v_cache, "v_cache"), _i32(dev_table, "dev_table")
+    if k_cache.dim() != 3 or v_cache.shape != k_cache.shape or (
+            k_cache.shape[1] != n_pages * page_size):
+        raise BadArgError(f"{name}: k_cache and v_cache must both be [Hkv][n_pages * page_size]"
+                          "[D]")
+    if dev_table.numel() < n_slots * max_pages_per_seq:
+        raise BadArgError(f"{name}: dev_table must be [n_slots][max_pages_per_seq]")
+    return k_cache.shape[0], k_cache.shape[2]
+
+
+def _tokens(name, what, t, heads, D) -> int:
+    """Checks bf16 tokens [N][heads][D] whose rows may stand apart; returns their stride."""
+    _is_tensor(name, **{what: t})
+    if t.dtype is not _BF16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise BadArgError(f"{name}: {what} must be a bfloat16 tensor [N][{heads}][{D}]")
+    if t.shape[0] > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+        raise BadArgError(f"{name}: {what}'s heads must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * D
+
+
+def tree_qkv_norm_rope_append(q, k, v, gamma_q, gamma_k, batch_idx, ctx_lens, row_start, parents,
+                              theta, eps, rotary_dims, v_norm, dev_table, n_slots,
+                              max_pages_per_seq, page_size, n_pages, k_cache, v_cache, q_out,
+                              err_word=None, stream=None) -> None:
+    """Norm, rotation at ctx + depth and the paged append of every row's tree of
+    drafted tokens (row_start int32 [B + 1], parents int32 [N]); q, k and v are
+    bf16 [N][heads][D], rows of any stride, and only read; the rotated q goes to
+    q_out. v None: the value is the raw k. rotary_dims None: all of D."""
+    name = "tree_qkv_norm_rope_append"
+    Hkv, D = _tree_cache(name, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq, page_size,
+                         n_pages)
+    _is_tensor(name, q=q, q_out=q_out)
+    if q.dim() != 3:
+        raise BadArgError(f"{name}: q must be [N][Hq][D]")
+    N, Hq, _ = q.shape
+    sq, sk = _tokens(name, "q", q, Hq, D), _tokens(name, "k", k, Hkv, D)
+    sv = 0 if v is None else _tokens(name, "v", v, Hkv, D)
+    _bf16(q_out, "q_out"), _bf16(gamma_q, "gamma_q"), _bf16(gamma_k, "gamma_k")
+    if k.shape[0] != N or (v is not None and v.shape[0] != N) or q_out.shape != q.shape:
+        raise BadArgError(f"{name}: q, k, v and q_out differ in tokens or heads")
+    for g in (gamma_q, gamma_k):
+        if g is not None and (not isinstance(g, torch.Tensor) or g.numel() != D):
+            raise BadArgError(f"{name}: gains must be [D]")
+    B = _tree(name, N, row_start, parents)
+    _tree_rows(name, B, batch_idx, ctx_lens)
+    _word(err_word)
+    _on_device(q, k, v, gamma_q, gamma_k, batch_idx, ctx_lens, row_start, parents, dev_table,
+               k_cache, v_cache, q_out, err_word)
+    _check(load_library().tree_qkv_norm_rope_append(
+        q.data_ptr(), k.data_ptr(), _ptr(v), sq, sk, sv, _ptr(gamma_q), _ptr(gamma_k),
+        _ptr(batch_idx), ctx_lens.data_ptr(), row_start.data_ptr(), parents.data_ptr(),
+        float(theta), float(eps), D if rotary_dims is None else int(rotary_dims),
+        int(bool(v_norm)), B, N, Hq, Hkv, D, dev_table.data_ptr(), n_slots, max_pages_per_seq,
+        page_size, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), q_out.data_ptr(),
+        _ptr(err_word), _stream(stream)), name)
+
+
+def paged_tree_attn_workspace(Hq, Hkv, D) -> int:
+    return int(load_library().paged_tree_attn_workspace(Hq, Hkv, D))
+
+
+def paged_tree_attn(q, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq, page_size, n_pages,
+                    batch_idx, ctx_lens, row_start, parents, window, scale, workspace, out,
+                    err_word=None, stream=None) -> None:
+    """Attention of every row's tree of drafted tokens (already appended) over the
+    paged cache: a node sees the context and its own path. q, out: bf16
+    [N][Hq][D]; workspace: a byte tensor of paged_tree_attn_workspace(Hq, Hkv,
+    D)."""
+    name = "paged_tree_attn"
+    Hkv, D = _tree_cache(name, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq, page_size,
+                         n_pages)
+    _is_tensor(name, q=q, out=out, workspace=workspace)
+    _bf16(q, "q"), _bf16(out, "out")
+    if q.dim() != 3 or q.shape[2] != D or out.shape != q.shape:
+        raise BadArgError(f"{name}: q, out and the caches differ in shape")
+    if not workspace.is_contiguous():
+        raise BadArgError(f"{name}: workspace must be a contiguous tensor")
+    N, Hq, _ = q.shape
+    B = _tree(name, N, row_start, parents)
+    _tree_rows(name, B, batch_idx, ctx_lens)
+    _word(err_word)
+    _on_device(q, k_cache, v_cache, dev_table, batch_idx, ctx_lens, row_start, parents, workspace,
+               out, err_word)
+    _check(load_library().paged_tree_attn(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), dev_table.data_ptr(), n_slots,
+        max_pages_per_seq, page_size, n_pages, _ptr(batch_idx), ctx_lens.data_ptr(),
+        row_start.data_ptr(), parents.data_ptr(), int(window), float(scale), B, N, Hq, Hkv, D,
+        workspace.data_ptr(), workspace.nbytes, out.data_ptr(), _ptr(err_word), _stream(stream)),
+        name)
+
+
+def _probs(name, what, t, N, V=None) -> int:
+    """Checks fp32 rows [N][V] that may stand apart; returns their stride."""
+    _is_tensor(name, **{what: t})
+    if t.dtype is not _F32 or t.dim() != 2 or t.shape[0] < N or (V is not None and t.shape[1] != V):
+        raise BadArgError(f"{name}: {what} must be a float32 tensor [N][V]")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise BadArgError(f"{name}: {what}'s rows must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def tree_verify(target_probs, draft_probs, tokens, row_start, parents, u_accept, u_pick, accepted,
+                path, next_token, err_word=None, stream=None) -> None:
+    """Which drafted tokens the target accepts, and the token behind them, from the
+    given uniform numbers. target_probs, draft_probs: fp32 [N][V], the
+    distribution after each node (draft_probs None: drafts chosen without
+    chance); tokens int32 [N]; u_accept fp32 [N], u_pick fp32 [B]. Writes accepted
+    int32 [B], path int32 [B][cols] (node 0 and the accepted drafts, then -1) and
+    next_token int32 [B]."""
+    name = "tree_verify"
+    _is_tensor(name, tokens=tokens)
+    N = tokens.numel()
+    _i32(tokens, "tokens")
+    sp = _probs(name, "target_probs", target_probs, N)
+    V = target_probs.shape[1]
+    sq = 0 if draft_probs is None else _probs(name, "draft_probs", draft_probs, N, V)
+    B = _tree(name, N, row_start, parents)
+    for what, t, n in (("u_accept", u_accept, N), ("u_pick", u_pick, B)):
+        _is_tensor(name, **{what: t})
+        if t.dtype is not _F32 or not t.is_contiguous() or t.numel() < n:
+            raise BadArgError(f"{name}: {what} must be a contiguous float32 tensor of {n} values")
+    _at_least(name, "accepted", accepted, B)
+    _at_least(name, "next_token", next_token, B)
+    _is_tensor(name, path=path)
+    _i32(path, "path")
+    if path.dim() != 2 or path.shape[0] < B or path.shape[1] < 1:
+        raise BadArgError(f"{name}: path must be [B][cols]")
+    _word(err_word)
+    _on_device(target_probs, draft_probs, tokens, row_start, parents, u_accept, u_pick, accepted,
+               path, next_token, err_word)
+    _check(load_library().tree_verify(
+        target_probs.data_ptr(), sp, _ptr(draft_probs), sq, tokens.data_ptr(),
+        row_start.data_ptr(), parents.data_ptr(), u_accept.data_ptr(), u_pick.data_ptr(), B, N, V,
+        path.shape[1], accepted.data_ptr(), path.data_ptr(), next_token.data_ptr(),
+        _ptr(err_word), _stream(stream)), name)
+
+
+def kv_keep_path(caches, dev_table, n_slots, max_pages_per_seq, page_size, n_pages, batch_idx,
+                 ctx_lens, accepted, path, err_word=None, stream=None) -> None:
+    """After tree_verify: the accepted nodes' tokens move to the positions behind the
+    context, in every head of every cache in `caches` (contiguous device tensors
+    [heads][n_pages * page_size][...], any element type, all the layers of a
+    model)."""
+    name = "kv_keep_path"
+    _is_tensor(name, dev_table=dev_table, path=path)
+    _i32(dev_table, "dev_table"), _i32(path, "path")
+    if path.dim() != 2 or path.shape[1] < 1:
+        raise BadArgError(f"{name}: path must be [B][cols]")
+    B = path.shape[0]
+    _at_least(name, "accepted", accepted, B)
+    _tree_rows(name, B, batch_idx, ctx_lens)
+    if dev_table.numel() < n_slots * max_pages_per_seq:
+        raise BadArgError(f"{name}: dev_table must be [n_slots][max_pages_per_seq]")
+    rows = n_pages * page_size
+    try:
+        if isinstance(caches, torch.Tensor):
+            raise TypeError
+        n = len(caches)
+        ptrs, heads, nbytes = (_c_p * n)(), (_c_int * n)(), (ctypes.c_int64 * n)()
+        for i, c in enumerate(caches):
+            if not c.is_contiguous() or c.dim() < 2 or c.shape[1] != rows:
+                raise BadArgError(f"{name}: caches must be contiguous tensors [heads][n_pages * "
+                                  "page_size][...]")
+            h = c.shape[0]
+            ptrs[i], heads[i], nbytes[i] = c.data_ptr(), h, c.nbytes // max(h * rows, 1)
+    except (AttributeError, TypeError):
+        raise BadArgError(f"{name}: caches must be a list of tensors") from None
+    _word(err_word)
+    _on_device(dev_table, batch_idx, ctx_lens, accepted, path, err_word, *caches)
+    _check(load_library().kv_keep_path(
+        ptrs, heads, nbytes, n, dev_table.data_ptr(), n_slots, max_pages_per_seq, page_size,
+        n_pages, _ptr(batch_idx), ctx_lens.data_ptr(), accepted.data_ptr(), path.data_ptr(),
+        path.shape[1], B, _ptr(err_word), _stream(stream)), name)
 
 
 def pkv_read_error_word(err_word, stream=None) -> int:

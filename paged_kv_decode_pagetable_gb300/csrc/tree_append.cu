@@ -1,0 +1,250 @@
+// tree_qkv_norm_rope_append: a speculative step's prologue in one pass over q, k and v:
+// per-head RMSNorm, rotate-half RoPE at ctx + depth, and the scatter of K and V to the cache
+// positions ctx + index (siblings share a rotation position, not a cache row).
+//
+//   r = x / sqrt(mean(x^2) + eps) * gamma
+//   y_i = r_i cos phi_i - r_{i+D/2} sin phi_i,  y_{i+D/2} = r_{i+D/2} cos phi_i + r_i sin phi_i
+//   phi_i = (ctx + depth) theta^(-2i/D)
+//
+// The order of "unsloth: compare main...flex-moe-qwen3" · flex_gemma4_moe.py · attention
+// forward (norm, rotary, then the paged write), as qkv_norm_rope and kv_append have it.
+//
+// The angle is kept as a fraction of a turn in 64-bit fixed point: with F_i = 2^64
+// theta^(-2i/D) / (2 pi), computed once on the host, position * F_i modulo 2^64 is the exact
+// fraction however far the position (in fp32 the angle of position 30000 is off by 10^-3
+// radians already, more than the output's rounding).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "pkv_internal.h"
+#include "tree.cuh"
+
+namespace {
+
+constexpr int kMaxThreads = 512;
+constexpr int kMaxD = 512;
+
+struct Turns {
+  uint64_t f[kMaxD / 2];
+};
+
+struct AppendArgs {
+  const __nv_bfloat16 *q, *k, *v, *gq, *gk;
+  long long sq, sk, sv;   // elements from one token to the next
+  const int32_t *batch_idx, *ctx_lens, *row_start, *parents, *table;
+  __nv_bfloat16 *k_cache, *v_cache, *q_out;
+  int32_t *err;
+  float eps;
+  int v_norm, B, N, Hq, Hkv, n_slots, max_pages, page_size, n_pages;
+};
+
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One CTA a node; D / 16 lanes a head, each with 8 rotation pairs (two 16-byte words).
+template <int D>
+__global__ void __launch_bounds__(kMaxThreads)
+    tree_append_kernel(const AppendArgs a, const __grid_constant__ Turns turns) {
+  constexpr int LANES = D / 16;
+  __shared__ int s_par[kTreeMax];
+  __shared__ float2 s_rot[D / 2];
+  __shared__ int s_row;
+  pkv_wait_prior_grid();
+  pkv_allow_next_grid();
+  const int node = blockIdx.x, tid = threadIdx.x;
+  const int heads = a.Hq + 2 * a.Hkv;
+  const int part = tid % LANES;
+  auto source = [&](int h) -> const __nv_bfloat16 * {
+    const long long n = node;
+    if (h < a.Hq) return a.q + n * a.sq + h * D;
+    if (h < a.Hq + a.Hkv) return a.k + n * a.sk + (h - a.Hq) * D;
+    return a.v + n * a.sv + (h - a.Hq - a.Hkv) * D;
+  };
+  // the first head's values are on their way while the row is looked up
+  int h = tid / LANES;
+  uint4 lo4 = make_uint4(0, 0, 0, 0), hi4 = lo4;
+  if (h < heads) {
+    const __nv_bfloat16 *x = source(h);
+    lo4 = *reinterpret_cast<const uint4 *>(x + 8 * part);
+    hi4 = *reinterpret_cast<const uint4 *>(x + D / 2 + 8 * part);
+  }
+  // the node's row: the last that starts at or before it
+  int before = 0;
+  for (int i0 = 0; i0 <= a.B; i0 += blockDim.x)
+    before += __syncthreads_count(i0 + tid <= a.B && a.row_start[i0 + tid] <= node);
+  const int b = before - 1;
+  if (b < 0 || b >= a.B) return;   // a node of no row
+  const TreeRow r = tree_row(b, a.N, a.row_start, a.batch_idx, a.ctx_lens, a.n_slots, a.max_pages,
+                             a.page_size);
+  const int i = node - r.n0;
+  if (r.bits || i < 0 || i >= r.n) {
+    if (tid == 0) tree_report(a.err, r.bits);
+    return;
+  }
+  const int at = r.ctx + i;
+  int page = -1, bits = 0;
+  if (tid == 0) {
+    page = a.table[static_cast<long long>(r.slot) * a.max_pages + at / a.page_size];
+    if (page < 0) bits = PKV_ERR_PAGE_NEG;
+    else if (page >= a.n_pages) bits = PKV_ERR_PAGE_RANGE;
+    s_row = bits ? -1 : page;
+  }
+  int pbits = 0;
+  for (int t = tid; t <= i; t += blockDim.x) s_par[t] = tree_parent(a.parents, r.n0, t, pbits);
+  tree_report(a.err, bits | pbits);
+  __syncthreads();
+  int depth = 0;
+  for (int t = s_par[i]; t >= 0; t = s_par[t]) ++depth;
+  const uint64_t pos = static_cast<uint64_t>(r.ctx + depth);
+  for (int t = tid; t < D / 2; t += blockDim.x) {
+    // the nearest half turn's fraction, in units of half a turn
+    const int32_t frac = static_cast<int32_t>((pos * turns.f[t]) >> 32);
+    float sn, cs;
+    sincospif(static_cast<float>(frac) * 0x1p-31f, &sn, &cs);
+    s_rot[t] = make_float2(cs, sn);
+  }
+  __syncthreads();
+  page = s_row;
+  const long long row = static_cast<long long>(page) * a.page_size + at % a.page_size;
+  const long long head_rows = static_cast<long long>(a.n_pages) * a.page_size;
+  // (whole warps go round together: the lanes of a head reduce with shuffles)
+  for (int h0 = 0; h0 < heads; h0 += blockDim.x / LANES, h += blockDim.x / LANES) {
+    if (h0 > 0 && h < heads) {
+      const __nv_bfloat16 *x = source(h);
+      lo4 = *reinterpret_cast<const uint4 *>(x + 8 * part);
+      hi4 = *reinterpret_cast<const uint4 *>(x + D / 2 + 8 * part);
+    }
+    const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
+    const __nv_bfloat16 *g = is_q ? a.gq : is_v ? nullptr : a.gk;
+    const bool norm = is_v ? a.v_norm != 0 : g != nullptr;
+    float lo[8], hi[8];
+    unpack8(lo4, lo);
+    unpack8(hi4, hi);
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(lo[e], lo[e], fmaf(hi[e], hi[e], ss));
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (h >= heads) continue;
+    if (norm) {
+      const float inv = rsqrtf(ss / D + a.eps);
+      float gl[8], gh[8];
+      if (g) {
+        unpack8(*reinterpret_cast<const uint4 *>(g + 8 * part), gl);
+        unpack8(*reinterpret_cast<const uint4 *>(g + D / 2 + 8 * part), gh);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        lo[e] *= g ? inv * gl[e] : inv;
+        hi[e] *= g ? inv * gh[e] : inv;
+      }
+    }
+    if (!is_v) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 w = s_rot[8 * part + e];
+        const float x1 = lo[e], x2 = hi[e];
+        lo[e] = x1 * w.x - x2 * w.y;
+        hi[e] = x2 * w.x + x1 * w.y;
+      }
+    }
+    __nv_bfloat16 *to;
+    if (is_q) {
+      to = a.q_out + (static_cast<long long>(node) * a.Hq + h) * D;
+    } else {
+      if (page < 0) continue;
+      const int hk = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
+      to = (is_v ? a.v_cache : a.k_cache) + (hk * head_rows + row) * D;
+    }
+    *reinterpret_cast<uint4 *>(to + 8 * part) = pack8(lo);
+    *reinterpret_cast<uint4 *>(to + D / 2 + 8 * part) = pack8(hi);
+  }
+}
+
+template <int D>
+cudaError_t launch(const AppendArgs &a, const Turns &t, cudaStream_t s) {
+  const int want = (a.Hq + 2 * a.Hkv) * (D / 16);
+  const int threads = want >= kMaxThreads ? kMaxThreads : (want + 31) / 32 * 32;
+  return pkv::launch_pdl(tree_append_kernel<D>, dim3(a.N), dim3(threads), 0, s, a, t);
+}
+
+}  // namespace
+
+extern "C" int tree_qkv_norm_rope_append(
+    const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, int64_t q_stride, int64_t k_stride,
+    int64_t v_stride, const pkv_bf16 *gamma_q, const pkv_bf16 *gamma_k, const int32_t *batch_idx,
+    const int32_t *ctx_lens, const int32_t *row_start, const int32_t *parents, float theta,
+    float eps, int rotary_dims, int v_norm, int B, int N, int Hq, int Hkv, int D,
+    const int32_t *dev_table, int n_slots, int max_pages_per_seq, int page_size, int n_pages,
+    pkv_bf16 *k_cache, pkv_bf16 *v_cache, pkv_bf16 *q_out, int32_t *err_word, void *stream) {
+  static const char *fn = "tree_qkv_norm_rope_append";
+  if (D != 64 && D != 128 && D != 256 && D != 512)
+    return pkv::fail(PKV_E_BAD_ARG, "%s: D must be 64, 128, 256 or 512", fn);
+  if (B < 0 || B > kTreeRows || N < 0 || Hq < 1 || Hq > 65535 || Hkv < 1 || Hkv > 65535)
+    return pkv::fail(PKV_E_BAD_ARG, "%s: bad shape (at most %d rows)", fn, kTreeRows);
+  if (page_size < 1 || n_pages < 1 || n_slots < 1 || max_pages_per_seq < 1)
+    return pkv::fail(PKV_E_BAD_ARG, "%s: bad table geometry", fn);
+  if (rotary_dims < 0 || rotary_dims > D || rotary_dims % 2)
+    return pkv::fail(PKV_E_BAD_ARG, "%s: rotary_dims must be even and in [0, D]", fn);
+  if (!(theta > 0.f) || std::isinf(theta))
+    return pkv::fail(PKV_E_BAD_ARG, "%s: theta must be finite and > 0", fn);
+  if (!(eps >= 0.f)) return pkv::fail(PKV_E_BAD_ARG, "%s: eps must be >= 0", fn);
+  if ((gamma_q == nullptr) != (gamma_k == nullptr))
+    return pkv::fail(PKV_E_BAD_ARG, "%s: give both gains or neither", fn);
+  if (B == 0 || N == 0) return pkv::ok();
+  if (!q || !k || !ctx_lens || !row_start || !parents || !dev_table || !k_cache || !v_cache ||
+      !q_out)
+    return pkv::fail(PKV_E_BAD_ARG, "%s: NULL tensor", fn);
+  if (!v) {   // the value is the raw key
+    v = k;
+    v_stride = k_stride;
+  }
+  if (!pkv::aligned16(q) || !pkv::aligned16(k) || !pkv::aligned16(v) || !pkv::aligned16(k_cache) ||
+      !pkv::aligned16(v_cache) || !pkv::aligned16(q_out) || !pkv::aligned16(gamma_q) ||
+      !pkv::aligned16(gamma_k))
+    return pkv::fail(PKV_E_BAD_ARG, "%s: tensors must be 16-byte aligned", fn);
+  const int64_t most = int64_t(1) << 40;
+  if (q_stride % 8 || k_stride % 8 || v_stride % 8 || q_stride < 0 || k_stride < 0 ||
+      v_stride < 0 || q_stride > most || k_stride > most || v_stride > most)
+    return pkv::fail(PKV_E_BAD_ARG, "%s: token strides must be multiples of 8 elements", fn);
+  Turns t;
+  for (int i = 0; i < D / 2; ++i) {
+    double f = i < rotary_dims / 2 ? pow(static_cast<double>(theta), -2.0 * i / D) / (2.0 * M_PI)
+                                   : 0.0;
+    f -= floor(f);
+    t.f[i] = f >= 1.0 ? 0 : static_cast<uint64_t>(ldexp(f, 64));
+  }
+  const AppendArgs a = {reinterpret_cast<const __nv_bfloat16 *>(q),
+                        reinterpret_cast<const __nv_bfloat16 *>(k),
+                        reinterpret_cast<const __nv_bfloat16 *>(v),
+                        reinterpret_cast<const __nv_bfloat16 *>(gamma_q),
+                        reinterpret_cast<const __nv_bfloat16 *>(gamma_k),
+                        q_stride, k_stride, v_stride, batch_idx, ctx_lens, row_start, parents,
+                        dev_table, reinterpret_cast<__nv_bfloat16 *>(k_cache),
+                        reinterpret_cast<__nv_bfloat16 *>(v_cache),
+                        reinterpret_cast<__nv_bfloat16 *>(q_out), err_word, eps, v_norm, B, N, Hq,
+                        Hkv, n_slots, max_pages_per_seq, page_size, n_pages};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  PKV_CUDA_CHECK(D == 64    ? launch<64>(a, t, s)
+                 : D == 128 ? launch<128>(a, t, s)
+                 : D == 256 ? launch<256>(a, t, s)
+                            : launch<512>(a, t, s));
+  return pkv::ok();
+}

@@ -22,10 +22,11 @@ import numpy as np
 import torch
 
 from . import (NoPagesError, NoSlotError, PageTable, PKV_ERR_TIMEOUT, _stream, kv_append,
-               kv_append_q8, kv_copy_pages, paged_decode_attn, paged_decode_attn_q8,
+               kv_append_q8, kv_copy_pages, kv_keep_path, paged_decode_attn, paged_decode_attn_q8,
                paged_decode_attn_q8_workspace, paged_decode_attn_splits,
                paged_decode_attn_workspace, paged_decode_step, paged_decode_step_ex,
-               pkv_read_error_word, pt_get_stream, qk_norm_rope, qkv_norm_rope)
+               paged_tree_attn, paged_tree_attn_workspace, pkv_read_error_word, pt_get_stream,
+               qk_norm_rope, qkv_norm_rope, tree_qkv_norm_rope_append, tree_verify)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -168,6 +169,54 @@ def decode_layer_step(spec: LayerSpec, pt: PageTable, k_cache, v_cache, q, k, v,
     paged_decode_attn(q, k_cache, v_cache, table, pt.n_slots, pt.max_pages_per_seq,
                       pt.page_size, pt.n_pages, batch_idx, seq_lens, spec.window, scale,
                       ws.splits, ws.buf, out, err, stream=stream)
+
+
+# --------------------------------------------------------------------------
+# Speculative steps: trees of drafted tokens
+# --------------------------------------------------------------------------
+
+class TreeWorkspace:
+    """Workspace of paged_tree_attn: sized by the heads alone, any contents."""
+
+    def __init__(self, Hq, Hkv, D, device):
+        self.buf = torch.empty(paged_tree_attn_workspace(Hq, Hkv, D), dtype=torch.uint8,
+                               device=device)
+
+
+def tree_layer_step(spec: LayerSpec, pt: PageTable, k_cache, v_cache, q, k, v, batch_idx, ctx_lens,
+                    row_start, parents, q_out, out, ws: TreeWorkspace, gamma_q=None, gamma_k=None,
+                    eps: float = 1e-6, scale: float | None = None, err=None, stream=None,
+                    table=None):
+    """One layer's step over trees of drafted tokens: tree_qkv_norm_rope_append, then
+    paged_tree_attn (decode_layer_step for several tokens a row). Row b's slot must have
+    capacity for ctx_lens[b] and its nodes (PageTable.reserve) and own the pages the nodes
+    fall on. q, k and v ([N][heads][D], rows of any stride) are read only; q_out and out are
+    [N][Hq][D]."""
+    table = pt.dev_table if table is None else table
+    scale = scale if scale is not None else spec.head_dim ** -0.5
+    if spec.gemma_options and not spec.rope:
+        raise ValueError("rotary_dims, v_norm and k_eq_v need a rotary layer")
+    geometry = (table, pt.n_slots, pt.max_pages_per_seq, pt.page_size, pt.n_pages)
+    tree_qkv_norm_rope_append(q, k, None if spec.k_eq_v else v, gamma_q if spec.qk_norm else None,
+                              gamma_k if spec.qk_norm else None, batch_idx, ctx_lens, row_start,
+                              parents, spec.theta, eps,
+                              (spec.rotary_dims or None) if spec.rope else 0, spec.v_norm,
+                              *geometry, k_cache, v_cache, q_out, err, stream=stream)
+    paged_tree_attn(q_out, k_cache, v_cache, *geometry, batch_idx, ctx_lens, row_start, parents,
+                    spec.window, scale, ws.buf, out, err, stream=stream)
+
+
+def accept_drafts(pt: PageTable, caches, target_probs, draft_probs, tokens, batch_idx, ctx_lens,
+                  row_start, parents, u_accept, u_pick, accepted, path, next_token, err=None,
+                  stream=None, table=None):
+    """After the last layer: tree_verify, then kv_keep_path on `caches` (K and V of every
+    layer). Row b's context is then ctx_lens[b] + 1 + accepted[b] tokens long and its next
+    tree begins with next_token[b]; nothing waits for the GPU."""
+    table = pt.dev_table if table is None else table
+    tree_verify(target_probs, draft_probs, tokens, row_start, parents, u_accept, u_pick, accepted,
+                path, next_token, err, stream=stream)
+    kv_keep_path(caches, table, pt.n_slots, pt.max_pages_per_seq, pt.page_size, pt.n_pages,
+                 batch_idx, ctx_lens, accepted, path, err, stream=stream)
 
 
 @dataclasses.dataclass
