@@ -15,8 +15,8 @@
 // In S^T a thread owns a key. Its columns' maxima run across threads, so they are not taken
 // tile by tile: a column keeps a reference, every thread checks that none of its scores passes
 // it by more than 2^8, and only where one does (a unit's first tile, and few others) the maxima
-// are reduced, the references moved and O scaled. The sums of the weights stay per thread until
-// a unit's end.
+// are reduced, the references moved and O scaled. The weights' sums are a third product, with ones
+// in V's place: every lane of TMEM has them, and no thread keeps a sum for each column.
 //
 // Work: the units' tiles, one more place for each unit's start, lie on one line, cut into equal
 // shares for one persistent CTA an SM from the lengths, on the device. A unit that is cut leaves
@@ -38,6 +38,7 @@
 
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "pkv_internal.h"
 #include "tcgen05.cuh"
@@ -46,9 +47,6 @@
 namespace {
 
 constexpr int kTile = 128;               // keys of a tile
-constexpr int kSoftWarps = 8;
-constexpr int kProdWarp = 8, kMmaWarp = 9, kPrepWarp = 10;
-constexpr int kThreads = 11 * 32;
 constexpr int kStart = 1;                // places on the line for a unit's start
 constexpr int kMaxCtas = 160;            // CTAs the workspace has room for
 constexpr float kLazyLog2 = 8.f;
@@ -57,29 +55,42 @@ constexpr int kJoinCols = 8;             // columns of a joining CTA
 
 template <int D>
 struct Cfg {
-  static constexpr int COLS = D <= 128 ? 128 : 64;      // columns of a unit, at most
-  static constexpr int HALF = COLS / 2;                 // of a softmax warp
-  static constexpr int BLOCKS = D <= 128 ? 1 : D / 128; // ring entries of a K or V tile
-  static constexpr int ATOMS = D == 64 ? 1 : 2;         // 64-column atoms of an entry
-  static constexpr int ATOM = kTile * 128;              // bytes
-  static constexpr int ENTRY = ATOMS * ATOM;
-  static constexpr int NS = D == 64 ? 8 : D == 256 ? 5 : 4;
+  static constexpr int COLS = 64;                       // columns of a unit, at most
+  // Units at work at a time, each with softmax warps, MMA warp, queries, P and TMEM of its own;
+  // where TMEM has room for one only, its softmax warps come in two groups of half the columns.
+  static constexpr int UNITS = D <= 128 ? 2 : 1;
+  static constexpr int GROUPS = 2 / UNITS;              // groups of four softmax warps a unit
+  static constexpr int HALF = COLS / GROUPS;            // columns of a softmax warp, at most
+  static constexpr int SOFT = 8;                        // softmax warps of all units
+  static constexpr int PROD = SOFT, PREP = SOFT + 1, MMA = SOFT + 2;
+  static constexpr int THREADS = (SOFT + 2 + UNITS) * 32;
+  // A ring entry: 64 columns of D of a K tile, or 64 keys' 128 columns of a V tile (two atoms
+  // of 64 columns; D = 64: all its keys).
+  static constexpr int ENTRY = kTile * 128;             // bytes
+  static constexpr int E = D / 64;                      // entries of a K tile, and of a V tile
+  static constexpr int BLOCKS = D <= 128 ? 1 : D / 128; // blocks of 128 rows of O^T
+  static constexpr int V_HALVES = D == 64 ? 1 : 2;      // entries of a V tile's block
+  static constexpr int NS = D == 128 ? 9 : D == 512 ? 8 : 10;
   static constexpr int Q_ATOM = COLS * 128;
-  static constexpr int OFF_Q = NS * ENTRY;
-  static constexpr int OFF_P = OFF_Q + (D / 64) * Q_ATOM;
-  static constexpr int P_ATOM = kTile * 128;            // 64 columns of every key
-  static constexpr int OFF_PREP = OFF_P + (COLS / 64) * P_ATOM;
-  static constexpr int S_COL = 0, O_COL = 2 * COLS;
-  static constexpr int TMEM_COLS = O_COL + BLOCKS * COLS <= 256 ? 256 : 512;
+  static constexpr int Q_BYTES = E * Q_ATOM;
+  static constexpr int P_BYTES = kTile * 128;
+  static constexpr int OFF_Q = NS * ENTRY;              // [UNITS]
+  static constexpr int OFF_P = OFF_Q + UNITS * Q_BYTES; // [UNITS]
+  static constexpr int OFF_ONES = OFF_P + UNITS * P_BYTES;  // one swizzle atom of ones
+  static constexpr int OFF_SMALL = OFF_ONES + 1024;
+  // of a unit: S of two tiles, O^T's blocks, the sums of the weights (in every lane)
+  static constexpr int S_COL = 0, O_COL = 2 * COLS, L_COL = O_COL + BLOCKS * COLS;
+  static constexpr int UNIT_COLS = 512 / UNITS;
+  static_assert(L_COL + COLS <= UNIT_COLS, "TMEM");
   static constexpr size_t RECORD = static_cast<size_t>(COLS) * (D + 2);   // floats of a part
 };
 
-// Which nodes see a key, of a unit's row.
+// Which of a unit's columns see a key, a bit each.
 struct Prep {
-  uint64_t below[kTreeMax];    // nodes that have node i on their path
-  uint64_t shallow[kTreeMax];  // nodes of depth <= i
+  uint64_t below[kTreeMax];    // those of the nodes that have node i on their path
+  uint64_t shallow[kTreeMax];  // those of the nodes of depth <= i
   int depth[kTreeMax];
-  unsigned poison[2];          // nodes that see a value that is not finite
+  unsigned poison[2];          // those that see some value that is not finite
 };
 
 // A unit cut into parts, for the joining kernel.
@@ -90,14 +101,16 @@ struct Cut {
 struct Small {
   Prep prep[2];
   long long pre[kTreeRows + 1];     // first place of every row on the line
-  int n0[kTreeRows], ctx[kTreeRows];
+  int ctx[kTreeRows], slot[kTreeRows];
   uint8_t n[kTreeRows];
-  float ref[128];                   // a column's reference, -inf: none yet
-  alignas(16) float mneg[128];                  // its negative, kUnset: none yet
-  float alpha[128];
-  float red[4][128];                // of the four warps of a half: maxima, sums
+  // of the columns, group g's from g * HALF on (the groups may be at different units)
+  alignas(16) float mneg[128];      // a column's reference's negative, kUnset: none yet
+  float ref[128];                   // its reference, -inf: none yet
+  float alpha[128];                 // what a new one scales O and sums by; NaN: poisoned
+  long long dst[128];               // its place in out, -1: none
+  float red[4][128];                // maxima of the four warps of a group
   int pages[2][16];
-  long long scan[kThreads / 32];
+  long long scan[12];
   uint64_t bars[48];
   uint32_t tmem;
   int abort;
@@ -105,7 +118,7 @@ struct Small {
 
 template <int D>
 constexpr size_t smem_bytes() {
-  return 1024 + Cfg<D>::OFF_PREP + sizeof(Small);
+  return 1024 + Cfg<D>::OFF_SMALL + sizeof(Small);
 }
 static_assert(smem_bytes<64>() <= 232448 && smem_bytes<128>() <= 232448 &&
                   smem_bytes<256>() <= 232448 && smem_bytes<512>() <= 232448,
@@ -117,7 +130,7 @@ struct Args {
   float *parts;
   Cut *cuts;
   int32_t *err;
-  int n_slots, max_pages, page_size, log_page, n_pages, window, B, N, Hq, Hkv, G, unit_tokens;
+  int n_slots, max_pages, page_size, log_page, n_pages, window, B, N, Hq, Hkv, G, unit_tokens, box_nodes;
   float scale_log2;
 };
 
@@ -134,19 +147,50 @@ __device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, f
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
 }
-// barrier of the 128 threads of a half, and whether any of them says yes
-__device__ __forceinline__ bool half_any(int half, bool mine) {
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(r));
+  return r != 0;
+}
+// barrier of the 128 threads of a group, and whether any of them says yes
+__device__ __forceinline__ bool group_any(int grp, bool mine) {
   uint32_t r;
   asm volatile(
       "{\n.reg .pred p, q;\nsetp.ne.b32 q, %1, 0;\n"
       "barrier.cta.red.or.pred p, %2, 128, q;\nselp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(mine)), "r"(1 + half)
+      : "r"(static_cast<uint32_t>(mine)), "r"(1 + grp)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void half_sync(int half) {
-  asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory");
+__device__ __forceinline__ void group_sync(int grp) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + grp) : "memory");
+}
+// The maximum of 16 columns over the 32 lanes: halves of the columns change places until every
+// pair of lanes has one, column_of(lane).
+__device__ __forceinline__ float column_max(float (&x)[16], int lane) {
+#pragma unroll
+  for (int o = 16, n = 8; o >= 2; o >>= 1, n >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (e < n) {
+        const float got = __shfl_xor_sync(0xffffffffu, up ? x[e] : x[e + n], o);
+        x[e] = fmaxf(up ? x[e + n] : x[e], got);
+      }
+    }
+  }
+  return fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
+}
+__device__ __forceinline__ int column_of(int lane) {
+  return (lane & 16 ? 8 : 0) + (lane & 8 ? 4 : 0) + (lane & 4 ? 2 : 0) + (lane & 2 ? 1 : 0);
+}
+
+// N of a unit's products: a multiple of 16 columns for each group of softmax warps
+template <int GROUPS>
+__device__ __forceinline__ int columns(int cols) {
+  return (cols + 16 * GROUPS - 1) / (16 * GROUPS) * (16 * GROUPS);
 }
 
 // A unit, or the part of it that this CTA has: tiles [t0, t1) of ntiles.
@@ -178,7 +222,7 @@ struct Line {
     if (pos >= end) return false;
     while (pos >= sm->pre[b + 1]) ++b;
     p.b = b;
-    p.n0 = sm->n0[b];
+    p.n0 = a->row_start[b];
     p.n = sm->n[b] & 127;
     p.ctx = sm->ctx[b];
     p.lo = a->window > 0 ? max(0, p.ctx - a->window + 1) : 0;
@@ -206,24 +250,34 @@ struct Line {
 __device__ __forceinline__ long long share(long long W, int c, int n) { return W * c / n; }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t raw[];
   uint8_t *sm = raw + ((1024u - (t_smem(raw) & 1023u)) & 1023u);
-  Small &s = *reinterpret_cast<Small *>(sm + C::OFF_PREP);
+  Small &s = *reinterpret_cast<Small *>(sm + C::OFF_SMALL);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
-  const uint32_t sRing = t_smem(sm), sQ = t_smem(sm + C::OFF_Q), sP = t_smem(sm + C::OFF_P);
+  const uint32_t sRing = t_smem(sm), sQ = t_smem(sm + C::OFF_Q), sP = t_smem(sm + C::OFF_P),
+                 sOnes = t_smem(sm + C::OFF_ONES);
   const uint32_t bars = t_smem(s.bars);
-  const uint32_t full = bars, empty = full + 8 * C::NS, sfull = empty + 8 * C::NS,
-                 sfree = sfull + 16, pfull = sfree + 16, pvdone = pfull + 8, ofree = pvdone + 8,
-                 qfull = ofree + 8, qempty = qfull + 8, prepfull = qempty + 8,
-                 prepempty = prepfull + 16, drain = prepempty + 16;
+  constexpr int U = C::UNITS;
+  // the ring's, then unit x's (S buffer b, preparation b)
+  const uint32_t full = bars, empty = full + 8 * C::NS, drain = empty + 8 * C::NS,
+                 prepfull = drain + 8 * U, prepempty = prepfull + 16, unit0 = prepempty + 16;
+  constexpr int UB = 10;
+  auto sfull = [&](int x, int b) { return unit0 + 8 * (UB * x + b); };
+  auto sfree = [&](int x, int b) { return unit0 + 8 * (UB * x + 2 + b); };
+  auto pfull = [&](int x) { return unit0 + 8 * (UB * x + 4); };
+  auto pvdone = [&](int x) { return unit0 + 8 * (UB * x + 5); };
+  auto ofree = [&](int x) { return unit0 + 8 * (UB * x + 6); };
+  auto qfull = [&](int x) { return unit0 + 8 * (UB * x + 7); };
+  auto qempty = [&](int x) { return unit0 + 8 * (UB * x + 8); };
+  auto turn = [&](int x) { return unit0 + 8 * (UB * x + 9); };
   volatile int *abort_flag = &s.abort;
-  static_assert(2 * C::NS + 14 <= 48, "barriers");
+  static_assert(2 * C::NS + 4 + U + U * UB <= 48, "barriers");
 
   if (tid == 0) {
     for (int i = 0; i < C::NS; ++i) {
@@ -231,24 +285,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       t_bar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      t_bar_init(sfull + 8 * i, 1);
-      t_bar_init(sfree + 8 * i, kSoftWarps);
       t_bar_init(prepfull + 8 * i, 1);
-      t_bar_init(prepempty + 8 * i, kSoftWarps);
+      t_bar_init(prepempty + 8 * i, C::SOFT / U);
     }
-    t_bar_init(pfull, kSoftWarps);
-    t_bar_init(pvdone, 1);
-    t_bar_init(ofree, kSoftWarps);
-    t_bar_init(qfull, 1);
-    t_bar_init(qempty, 1);
-    t_bar_init(drain, 1);
+    for (int x = 0; x < U; ++x) {
+      for (int b = 0; b < 2; ++b) {
+        t_bar_init(sfull(x, b), 1);
+        t_bar_init(sfree(x, b), C::SOFT / U);
+      }
+      t_bar_init(pfull(x), C::SOFT / U);
+      t_bar_init(pvdone(x), 1);
+      t_bar_init(ofree(x), C::SOFT / U);
+      t_bar_init(qfull(x), 1);
+      t_bar_init(qempty(x), 1);
+      t_bar_init(turn(x), 1);
+      t_bar_init(drain + 8 * x, 1);
+    }
     s.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  for (int i = tid; i < 256; i += C::THREADS)
+    reinterpret_cast<uint32_t *>(sm + C::OFF_ONES)[i] = 0x3f803f80u;
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      t_smem(&s.tmem)),
-                 "r"(C::TMEM_COLS));
+                 "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   pkv_wait_prior_grid();
@@ -256,17 +318,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // the line: places of every row, summed up over the rows
   {
-    long long mine[2];
+    constexpr int R = (kTreeRows + C::THREADS) / C::THREADS;   // rows of a thread, and the end
+    long long mine[R];
+    long long sum = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int b = 2 * tid + i;
+    for (int i = 0; i < R; ++i) {
+      const int b = R * tid + i;
       mine[i] = 0;
       if (b < a.B) {
         const TreeRow r = tree_row(b, a.N, a.row_start, a.batch_idx, a.ctx_lens, a.n_slots,
                                    a.max_pages, a.page_size);
         if (r.bits && cta == 0) tree_report(a.err, r.bits);
-        s.n0[b] = r.n0;
         s.ctx[b] = r.ctx;
+        s.slot[b] = r.slot;
         // the top bit: padding, only zeros to write
         s.n[b] = static_cast<uint8_t>(r.n | (r.slot == 0 ? 128 : 0));
         if (r.n > 0) {
@@ -276,8 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ((r.n + a.unit_tokens - 1) / a.unit_tokens);
         }
       }
+      sum += mine[i];
     }
-    long long sum = mine[0] + mine[1];
+    const long long own = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, sum, o);
@@ -287,10 +352,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     t_fence_before();
     __syncthreads();
     t_fence_after();
-    for (int w = 0; w < warp; ++w) sum += s.scan[w];
-    const int b = 2 * tid;
-    if (b <= a.B) s.pre[b] = sum - mine[0] - mine[1];
-    if (b + 1 <= a.B) s.pre[b + 1] = sum - mine[1];
+#pragma unroll
+    for (int w = 0; w < C::THREADS / 32 - 1; ++w) sum += w < warp ? s.scan[w] : 0;
+    sum -= own;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (R * tid + i <= a.B) s.pre[R * tid + i] = sum;
+      sum += mine[i];
+    }
     __syncthreads();
   }
   const uint32_t tmem = s.tmem;
@@ -303,48 +372,72 @@ __global__ void __launch_bounds__(kThreads, 1)
   Part p;
   if (tid == 0) a.cuts[cta].cols = 0;
 
-  if (warp == kProdWarp) {
+  if (warp == C::PROD) {
     // ============================ producer ============================
-    const int box_rows = min(a.page_size, kTile);
-    const int per_tile = kTile / box_rows;         // pages of a tile (1 where they are larger)
-    int g = 0;                                     // ring entries so far
+    const int k_rows = min(a.page_size, kTile);             // tokens of a K box
+    const int v_rows = min(a.page_size, kTile / C::V_HALVES);
+    const int per_tile = kTile / k_rows;         // pages of a tile (1 where they are larger)
+    int g = 0;                                   // ring entries so far
     int bits = 0;
     bool ok = true;
-    // one K or V tile: its pages' boxes, BLOCKS entries
-    auto load = [&](const CUtensorMap *tm, int which, int head, int j0, int first, int last) {
-      const int row0 = j0 & (a.page_size - 1);     // (page_size > 128: place inside the page)
-      for (int blk = 0; blk < C::BLOCKS && ok; ++blk, ++g) {
-        const int e = g % C::NS;
-        if (g >= C::NS && !t_wait_warp(empty + 8 * e, g / C::NS - 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0)
-          t_expect_tx(full + 8 * e, (last - first) * box_rows * 128 * C::ATOMS);
+    // room in the next entry, and how many bytes will come
+    auto take = [&](int boxes, int rows) -> int {
+      const int e = g % C::NS;
+      if (g >= C::NS && !t_wait_warp(empty + 8 * e, g / C::NS - 1, abort_flag)) {
+        ok = false;
+        return 0;
+      }
+      if (lane == 0) t_expect_tx(full + 8 * e, boxes * rows * 128);
+      __syncwarp();
+      ++g;
+      return e;
+    };
+    // a K tile: 64 columns of all its pages [first, last) an entry
+    auto load_k = [&](int which, int head, int j0, int first, int last) {
+      const int in_page = j0 & (a.page_size - 1);   // (pages larger than a tile)
+      for (int at = 0; at < C::E && ok; ++at) {
+        const int e = take(last - first, k_rows);
+        if (!ok) break;
+        if (lane >= first && lane < last)
+          t_tma_4d(sRing + e * C::ENTRY + lane * k_rows * 128, &tmK, 0,
+                   s.pages[which][lane] * a.page_size + in_page, head, at, full + 8 * e);
         __syncwarp();
-        if (lane >= first && lane < last) {
-          const int page = s.pages[which][lane];
-          const int row = page * a.page_size + (per_tile == 1 ? row0 : 0);
-#pragma unroll
-          for (int at = 0; at < C::ATOMS; ++at)
-            t_tma_4d(sRing + e * C::ENTRY + at * C::ATOM + lane * box_rows * 128, tm, 0, row, head,
-                     blk * C::ATOMS + at, full + 8 * e);
-        }
+      }
+    };
+    // a V tile: 128 columns of half its keys an entry, two atoms a page
+    auto load_v = [&](int which, int head, int j0, int first, int last) {
+      const int in_page = j0 & (a.page_size - 1);
+      constexpr int AT = D == 64 ? 1 : 2;
+      const int per = kTile / C::V_HALVES / v_rows;   // pages of an entry
+      for (int c = 0; c < C::E && ok; ++c) {
+        const int half = c % C::V_HALVES, blk = c / C::V_HALVES;
+        // pages [p0, p0 + per) of the tile; one larger than an entry serves both halves
+        const int p0 = per_tile == 1 ? 0 : half * per;
+        const int lo = max(first, p0), hi = min(last, p0 + per);
+        const int e = take(max(0, hi - lo) * AT, v_rows);
+        if (!ok) break;
+        const int pg = p0 + lane / AT, at = lane % AT;
+        if (pg >= lo && pg < hi)
+          t_tma_4d(sRing + e * C::ENTRY + at * (kTile / C::V_HALVES) * 128 +
+                       (pg - p0) * v_rows * 128,
+                   &tmV, 0,
+                   s.pages[which][pg] * a.page_size + in_page +
+                       (per_tile == 1 ? half * (kTile / C::V_HALVES) : 0),
+                   head, blk * AT + at, full + 8 * e);
         __syncwarp();
       }
     };
     while (ok && line.next(p)) {
       if (p.t0 == p.t1) continue;
-      const int slot = a.batch_idx ? a.batch_idx[p.b] : p.b;
-      const int32_t *row = a.table + static_cast<long long>(slot) * a.max_pages;
+      const int32_t *row = a.table + static_cast<long long>(s.slot[p.b]) * a.max_pages;
       const int last_page = (p.ctx + p.n - 1) >> a.log_page;
       const int first_page = p.lo >> a.log_page;
       // page numbers 32 at a time, the next ones on their way
-      const int base0 = ((p.tile0 + p.t0) * kTile) >> a.log_page;
       auto fetch = [&](int i) -> int {
         return i >= first_page && i <= last_page ? row[i] : 0;
       };
-      int base = base0, now = fetch(base + lane), then = fetch(base + 32 + lane);
+      int base = ((p.tile0 + p.t0) * kTile) >> a.log_page;
+      int now = fetch(base + lane), then = fetch(base + 32 + lane);
       int kf = 0, kl = 0;      // pages of the last K tile that are there
       for (int t = p.t0; t <= p.t1 && ok; ++t) {
         const int pf = kf, pl = kl;
@@ -367,10 +460,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             s.pages[t & 1][lane] = page;
           }
           __syncwarp();
-          load(&tmK, t & 1, p.head, j0, kf, kl);
+          load_k(t & 1, p.head, j0, kf, kl);
         }
-        if (t > p.t0 && ok)
-          load(&tmV, (t - 1) & 1, p.head, (p.tile0 + t - 1) * kTile, pf, pl);
+        if (t > p.t0 && ok) load_v((t - 1) & 1, p.head, (p.tile0 + t - 1) * kTile, pf, pl);
       }
     }
     tree_report(a.err, bits);
@@ -381,87 +473,123 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= C::MMA) {
     // ============================== MMA ===============================
-    if (lane == 0) {
-      int g = 0, tiles = 0, segs = 0, pv = 0;
-      bool ok = true;
-      auto entry = [&]() -> int {   // the next ring entry, once it is there
-        const int e = g % C::NS;
-        if (!t_wait(full + 8 * e, g / C::NS, abort_flag)) ok = false;
-        return e;
-      };
-      while (ok && line.next(p)) {
-        if (p.t0 == p.t1) continue;
-        const int N = (p.toks * a.G + 31) & ~31;
-        const uint32_t idS = idesc(N, false), idO = idesc(N, true);
-        if (!t_wait(qfull, segs, abort_flag)) break;
-        auto do_pv = [&](bool first) {
-          if (!t_wait(pfull, pv, abort_flag)) ok = false;
-          if (ok && first && segs >= 1 && !t_wait(ofree, segs - 1, abort_flag)) ok = false;
-          for (int blk = 0; blk < C::BLOCKS && ok; ++blk, ++g) {
-            const int e = entry();
-            if (!ok) break;
-            t_fence_after();
+    // The whole warp goes through the steps and one elected lane issues: so the compiler knows
+    // that descriptors and addresses are the warp's, and an MMA takes 42 to 50 cycles (its A
+    // operand's way from shared memory). Issued under a lane's own branch it took 90 to 150.
+    const int x = warp - C::MMA;     // this warp's units: every U-th
+    int g = 0, tiles = 0, segs = 0, own = 0;
+    bool ok = true;
+    const uint32_t tx = __shfl_sync(0xffffffffu, tmem + x * C::UNIT_COLS, 0);
+    const uint64_t dQ = t_desc(sQ + x * C::Q_BYTES, 16, 1024);
+    const uint64_t dP = t_desc(sP + x * C::P_BYTES, 0, 1024), dOne = t_desc(sOnes, 0, 0);
+    auto wait_entry = [&](int i) -> bool {
+      return t_wait_warp(full + 8 * (i % C::NS), i / C::NS, abort_flag);
+    };
+    // P V of a tile, and the weights' sums: a row of ones, 128 times
+    auto do_pv = [&](uint32_t id, int pv, bool first, bool last) {
+      if (U == 2 && last) {   // the unit's last entries: the other unit's turn
+        for (int c = 0; c < C::E && ok; ++c) ok = wait_entry(g + c);
+        if (ok && lane == 0) t_arrive(turn(x ^ 1));
+      }
+      ok = ok && t_wait_warp(pfull(x), pv, abort_flag);
+      if (first && own >= 1) ok = ok && t_wait_warp(ofree(x), own - 1, abort_flag);
+#pragma unroll 1
+      for (int c = 0; c < C::E && ok; ++c, ++g) {
+        if (!wait_entry(g)) {
+          ok = false;
+          break;
+        }
+        t_fence_after();
+        const int half = c % C::V_HALVES, blk = c / C::V_HALVES;
+        const uint32_t e = __shfl_sync(0xffffffffu, g % C::NS, 0);
+        const uint32_t to = tx + C::O_COL + blk * C::COLS;
+        // (D = 64: rows 64 .. 127 of the product repeat rows 0 .. 63)
+        const uint64_t va = t_desc(sRing + e * C::ENTRY, D == 64 ? 0 : kTile / 2 * 128, 1024);
+        const uint64_t pb = dP + half * (kTile / 2 * 128 >> 4);
+        const uint32_t add = half > 0 || !first;
+        if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k) {
-              // (D = 64: rows 64 .. 127 of the product repeat rows 0 .. 63)
-              const uint64_t va = t_desc(sRing + e * C::ENTRY + k * 2048,
-                                         C::ATOMS == 1 ? 0 : C::ATOM, 1024);
-              const uint64_t pb = t_desc(sP + k * 2048, C::P_ATOM, 1024);
-              t_mma(tmem + C::O_COL + blk * C::COLS, va, pb, idO, (k > 0 || !first) ? 1u : 0u);
-            }
-            t_commit(empty + 8 * e);
-          }
-          if (ok) t_commit(pvdone);
-          ++pv;
-        };
-        for (int t = p.t0; t < p.t1 && ok; ++t, ++tiles) {
-          const int buf = tiles & 1;
-          if (tiles >= 2 && !t_wait(sfree + 8 * buf, (tiles >> 1) - 1, abort_flag)) {
+          for (int k = 0; k < kTile / C::V_HALVES / 16; ++k)
+            t_mma(to, va + k * (2048 >> 4), pb + k * (2048 >> 4), id, k > 0 ? 1u : add);
+          t_commit(empty + 8 * e);
+        }
+        __syncwarp();
+      }
+      if (ok && elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          t_mma(tx + C::L_COL, dOne, dP + k * (2048 >> 4), id, k > 0 || !first ? 1u : 0u);
+        t_commit(pvdone(x));
+      }
+      __syncwarp();
+    };
+    while (ok && line.next(p)) {
+      if (p.t0 == p.t1) continue;
+      const int seg = segs++;
+      if (seg % U != x) {
+        g += 2 * (p.t1 - p.t0) * C::E;
+        continue;
+      }
+      // An entry's phase is told from the one before only. So a unit begins when all entries
+      // before its own have landed, which the other unit's warp has seen.
+      if (U == 2 && seg > 0 && !t_wait_warp(turn(x), (seg - 1) / 2, abort_flag)) break;
+      const int N = __shfl_sync(0xffffffffu, columns<C::GROUPS>(p.toks * a.G), 0);
+      const uint32_t idS = idesc(N, false), idO = idesc(N, true);
+      if (!t_wait_warp(qfull(x), own, abort_flag)) break;
+      for (int t = p.t0; t < p.t1 && ok; ++t, ++tiles) {
+        const int buf = tiles & 1;
+        if (tiles >= 2) ok = t_wait_warp(sfree(x, buf), (tiles >> 1) - 1, abort_flag);
+        const uint32_t to = __shfl_sync(0xffffffffu, tx + C::S_COL + buf * C::COLS, 0);
+#pragma unroll 1
+        for (int c = 0; c < C::E && ok; ++c, ++g) {
+          if (!wait_entry(g)) {
             ok = false;
             break;
           }
-          for (int blk = 0; blk < C::BLOCKS && ok; ++blk, ++g) {
-            const int e = entry();
-            if (!ok) break;
-            t_fence_after();
+          t_fence_after();
+          const uint32_t e = __shfl_sync(0xffffffffu, g % C::NS, 0);
+          const uint64_t ka = t_desc(sRing + e * C::ENTRY, 16, 1024);
+          const uint64_t qb = dQ + c * (C::Q_ATOM >> 4);
+          if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4 * C::ATOMS; ++k) {
-              const uint64_t ka =
-                  t_desc(sRing + e * C::ENTRY + (k >> 2) * C::ATOM + (k & 3) * 32, 16, 1024);
-              const uint64_t qb = t_desc(
-                  sQ + (blk * C::ATOMS + (k >> 2)) * C::Q_ATOM + (k & 3) * 32, 16, 1024);
-              t_mma(tmem + C::S_COL + buf * C::COLS, ka, qb, idS, (blk > 0 || k > 0) ? 1u : 0u);
-            }
+            for (int k = 0; k < 4; ++k) t_mma(to, ka + k * 2, qb + k * 2, idS, c > 0 || k > 0);
             t_commit(empty + 8 * e);
           }
-          if (!ok) break;
-          t_commit(sfull + 8 * buf);
-          if (t == p.t1 - 1) t_commit(qempty);
-          if (t > p.t0) do_pv(t == p.t0 + 1);
+          __syncwarp();
         }
-        if (ok) do_pv(p.t1 - p.t0 == 1);
-        ++segs;
+        if (!ok) break;
+        if (elect_one()) {
+          t_commit(sfull(x, buf));
+          if (t == p.t1 - 1) t_commit(qempty(x));
+        }
+        __syncwarp();
+        if (t > p.t0) do_pv(idO, tiles - 1, t == p.t0 + 1, false);
       }
-      t_commit(drain);
-      t_wait_drain(drain);
+      if (ok) do_pv(idO, tiles - 1, p.t1 - p.t0 == 1, true);
+      ++own;
     }
-  } else if (warp == kPrepWarp) {
+    if (elect_one()) {
+      t_commit(drain + 8 * x);
+      t_wait_drain(drain + 8 * x);
+    }
+    __syncwarp();
+  } else if (warp == C::PREP) {
     // ====================== queries and who sees whom ======================
     int segs = 0, bits = 0;
-    bool ok = true;
-    const int box = 8 * a.G * 128;      // bytes of 8 nodes' heads, one atom
-    while (ok && line.next(p)) {
+    const int box = a.box_nodes * a.G * 128;      // bytes of a box: nodes x heads, one atom
+    while (line.next(p)) {
       if (p.t0 == p.t1) continue;
-      if (segs >= 1 && !t_wait_warp(qempty, segs - 1, abort_flag)) break;
+      const int x = segs % U;
+      if (segs >= U && !t_wait_warp(qempty(x), segs / U - 1, abort_flag)) break;
       if (lane == 0) {
-        const int boxes = (p.toks + 7) / 8;
-        t_expect_tx(qfull, boxes * box * (D / 64));
+        const int boxes = (p.toks + a.box_nodes - 1) / a.box_nodes;
+        t_expect_tx(qfull(x), boxes * box * (D / 64));
         for (int i = 0; i < boxes; ++i)
           for (int at = 0; at < D / 64; ++at)
-            t_tma_4d(sQ + at * C::Q_ATOM + i * box, &tmQ, 0, p.head * a.G, p.n0 + p.tok0 + 8 * i, at,
-                     qfull);
+            t_tma_4d(sQ + x * C::Q_BYTES + at * C::Q_ATOM + i * box, &tmQ, 0, p.head * a.G,
+                     p.n0 + p.tok0 + a.box_nodes * i, at, qfull(x));
       }
       Prep &w = s.prep[segs & 1];
       if (segs >= 2 && !t_wait_warp(prepempty + 8 * (segs & 1), (segs >> 1) - 1, abort_flag)) break;
@@ -497,15 +625,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!more) break;
       }
       uint64_t below[2] = {0, 0}, shallow[2] = {0, 0};
-      int depth[2];
+      int depth[2] = {0, 0};
+      const uint64_t heads = (1ull << a.G) - 1;     // a node's columns
       for (int t = 0; t < p.n; ++t) {
         const uint64_t v = path[t];
         const int d = __popcll(v) - 1;
+        const int at = t - p.tok0;
+        const uint64_t mine = at >= 0 && at < p.toks ? heads << (at * a.G) : 0;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int i = lane + 32 * q;
-          below[q] |= ((v >> i) & 1) << t;
-          shallow[q] |= static_cast<uint64_t>(d <= i) << t;
+          below[q] |= (v >> i) & 1 ? mine : 0;
+          shallow[q] |= d <= i ? mine : 0;
           if (t == i) depth[q] = d;
         }
       }
@@ -514,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int q = 0; q < 2; ++q) {
         w.below[lane + 32 * q] = below[q];
         w.shallow[lane + 32 * q] = shallow[q];
-        w.depth[lane + 32 * q] = lane + 32 * q < p.n ? depth[q] : 0;
+        w.depth[lane + 32 * q] = depth[q];
       }
       if (lane < 2) w.poison[lane] = 0;
       __syncwarp();
@@ -524,46 +655,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     tree_report(a.err, bits);
   } else {
     // ============================ softmax =============================
-    const int quad = warp & 3, half = warp >> 2;
+    const int quad = warp & 3, sub = warp >> 2;      // (sub: which four warps)
+    const int x = U == 2 ? sub : 0, grp = U == 2 ? 0 : sub;   // unit, group of its columns
+    const uint32_t sfull_x = sfull(x, 0), sfree_x = sfree(x, 0), pvdone_x = pvdone(x);
     const int row = 32 * quad + lane;           // the key of a tile, or the column of D
-    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * quad) << 16);
-    int tiles = 0, segs = 0, g = 0;             // g: ring entries of the units so far
+    const uint32_t trow = tmem + x * C::UNIT_COLS + (static_cast<uint32_t>(32 * quad) << 16);
+    const int h0 = sub * C::HALF;               // where the warps' columns are in shared memory
+    uint8_t *pbuf = sm + C::OFF_P + x * C::P_BYTES + row * 128;
+    const int mine = 32 * quad + lane;          // the column that this thread looks after
+    int tiles = 0, segs = 0, seg = 0, g = 0;    // g: ring entries of the parts so far
     bool ok = true, gone = false;
-    float l[C::HALF];
-    while (!gone && line.next(p)) {
-      const int cols = p.toks * a.G;
-      if (p.ntiles == 0) {                      // padding
-        for (int i = warp; i < cols; i += kSoftWarps) {
-          const long long o = (static_cast<long long>(p.n0 + p.tok0 + i / a.G) * a.Hq +
-                               p.head * a.G + i % a.G) * D;
-          for (int d = 2 * lane; d < D; d += 64)
-            *reinterpret_cast<uint32_t *>(a.out + o + d) = 0;
-        }
-        continue;
-      }
-      if (p.t0 == p.t1) continue;
-      const int N = (cols + 31) & ~31;
-      const int hn = N / 2, c0 = half * hn;     // this warp's columns c0 .. c0 + hn
-      // (in shared memory from h0 on: the halves may be at different units)
-      const int h0 = half * C::HALF;
-      Prep &w = s.prep[segs & 1];
+    // a unit (or its part) with CH chunks of 16 columns a group
+    auto unit = [&](auto chunks) {
+      constexpr int CH = decltype(chunks)::value, HN = 16 * CH;
+      const int cols = p.toks * a.G, c0 = grp * HN;
+      Prep &w = s.prep[seg & 1];
       const int nt = p.t1 - p.t0;
+      // the columns in use of the warp's own
+      const uint64_t wide = cols >= 64 ? ~0ull : (1ull << cols) - 1;
       bool any_masked = false;
-#pragma unroll
-      for (int c = 0; c < C::HALF; ++c) l[c] = 0.f;
       for (int t = p.t0; t < p.t1; ++t, ++tiles) {
         const int buf = tiles & 1, i = t - p.t0;
         const int j0 = (p.tile0 + t) * kTile, j = j0 + row;
         const bool masked = j0 + kTile > p.ctx ||
                             (a.window > 0 && j0 <= p.ctx + p.n - 1 - a.window);
         const bool first = i == 0;
-        uint64_t sees = ~0ull;                  // nodes that see this thread's key
+        uint64_t sees = ~0ull;                  // the columns that see this thread's key
         any_masked |= masked;
+        // (S first: the unit's queries are there then, and the preparations before its own)
+        ok = ok && t_wait_warp(sfull_x + 8 * buf, tiles >> 1, abort_flag);
         if (masked) {
-          ok = ok && t_wait_warp(prepfull + 8 * (segs & 1), segs >> 1, abort_flag);
+          ok = ok && t_wait_warp(prepfull + 8 * (seg & 1), seg >> 1, abort_flag);
           const int node = j - p.ctx;
-          if (node >= p.n) sees = 0;
-          else if (node >= 0) {
+          if (node >= p.n) {
+            sees = 0;
+          } else if (node >= 0) {
             sees = w.below[node];
             if (a.window > 0)
               sees &= w.shallow[min(static_cast<long long>(kTreeMax - 1),
@@ -572,9 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int d = node + a.window - 1;
             sees = d < 0 ? 0 : w.shallow[min(d, kTreeMax - 1)];
           }
-          sees >>= p.tok0;
         }
-        ok = ok && t_wait_warp(sfull + 8 * buf, tiles >> 1, abort_flag);
         t_fence_after();
         const uint32_t scol = trow + C::S_COL + buf * C::COLS + c0;
         // 16 scores of this thread's key, -inf where a node does not see it
@@ -585,80 +709,52 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[e]);
           if (masked) {
-            int tok = (c0 + c) / a.G, k = (c0 + c) - tok * a.G;
+            const uint32_t bits = static_cast<uint32_t>(sees >> (c0 + c));
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              if (!((sees >> (tok & 63)) & 1)) x[e] = -INFINITY;
-              if (++k == a.G) {
-                k = 0;
-                ++tok;
-              }
-            }
+            for (int e = 0; e < 16; ++e) x[e] = bits & (1u << e) ? x[e] : -INFINITY;
           }
         };
-        uint32_t pk[C::HALF / 2];
+        uint32_t pk[HN / 2];
         // the weights under the references at hand; whether one is out of reach
         auto weights = [&]() -> bool {
           float top = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < C::HALF; c += 16) {
-            if (c < hn) {
-              float x[16];
-              scores(c, x);
-              const float4 *m4 = reinterpret_cast<const float4 *>(s.mneg + h0 + c);
+          for (int c = 0; c < HN; c += 16) {
+            float x[16];
+            scores(c, x);
+            const float4 *m4 = reinterpret_cast<const float4 *>(s.mneg + h0 + c);
 #pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                const float4 m = m4[e / 4];
-                fma2(x[e], x[e + 1], x[e], x[e + 1], a.scale_log2, m.x, m.y);
-                fma2(x[e + 2], x[e + 3], x[e + 2], x[e + 3], a.scale_log2, m.z, m.w);
-                top = t_max3(top, x[e], x[e + 1]);
-                top = t_max3(top, x[e + 2], x[e + 3]);
-              }
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                x[e] = t_ex2(x[e]);
-                x[e + 1] = t_ex2(x[e + 1]);
-                pk[(c + e) / 2] = t_pack(x[e], x[e + 1]);
-              }
+            for (int e = 0; e < 16; e += 4) {
+              const float4 m = m4[e / 4];
+              fma2(x[e], x[e + 1], x[e], x[e + 1], a.scale_log2, m.x, m.y);
+              fma2(x[e + 2], x[e + 3], x[e + 2], x[e + 3], a.scale_log2, m.z, m.w);
+              top = t_max3(top, x[e], x[e + 1]);
+              top = t_max3(top, x[e + 2], x[e + 3]);
             }
+#pragma unroll
+            for (int e = 0; e < 16; e += 2)
+              pk[(c + e) / 2] = t_pack(t_ex2(x[e]), t_ex2(x[e + 1]));
           }
           return top > kLazyLog2;
         };
-        bool slow = first;
+        bool slow = false;
         if (!first) slow = ok && weights();
-        if (half_any(half, slow || !ok)) {
-          if (half_any(half, !ok)) {
+        if (first || group_any(sub, slow || !ok)) {
+          if (group_any(sub, !ok)) {
             gone = true;
-            break;
+            return;
           }
           // the columns' maxima over the tile
-#pragma unroll
-          for (int c = 0; c < C::HALF; c += 16) {
-            if (c < hn) {
-              float x[16];
-              scores(c, x);
-              // 16 columns over 32 lanes: halves change places until a lane pair has one
-#pragma unroll
-              for (int o = 16, n = 8; o >= 2; o >>= 1, n >>= 1) {
-                const bool up = lane & o;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  if (e < n) {
-                    const float give = up ? x[e] : x[e + n];
-                    const float got = __shfl_xor_sync(0xffffffffu, give, o);
-                    x[e] = fmaxf(up ? x[e + n] : x[e], got);
-                  }
-                }
-              }
-              const float v = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
-              const int col = (lane & 16 ? 8 : 0) + (lane & 8 ? 4 : 0) + (lane & 4 ? 2 : 0) +
-                              (lane & 2 ? 1 : 0);
-              if (!(lane & 1)) s.red[quad][h0 + c + col] = v;
-            }
+#pragma unroll 1
+          for (int c = 0; c < HN; c += 16) {
+            float x[16];
+            scores(c, x);
+            const float v = column_max(x, lane);
+            if (!(lane & 1)) s.red[quad][h0 + c + column_of(lane)] = v;
           }
-          half_sync(half);
-          if (32 * quad + lane < hn) {
-            const int c = h0 + 32 * quad + lane;
+          group_sync(sub);
+          if (mine < HN) {
+            const int c = h0 + mine;
             const float old = first ? -INFINITY : s.ref[c];
             const float top = fmaxf(fmaxf(s.red[0][c], s.red[1][c]),
                                     fmaxf(s.red[2][c], s.red[3][c])) * a.scale_log2;
@@ -667,29 +763,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             s.mneg[c] = ref == -INFINITY ? kUnset : -ref;
             s.alpha[c] = old == ref ? 1.f : exp2f(old - ref);
           }
-          half_sync(half);
+          group_sync(sub);
           if (!first) {
-            ok = t_wait_warp(pvdone, tiles - 1, abort_flag);
+            ok = t_wait_warp(pvdone_x, tiles - 1, abort_flag);
             t_fence_after();
             if (ok) {
+#pragma unroll 1
+              for (int c = 0; c < HN; c += 16) {
+#pragma unroll 1
+                for (int blk = 0; blk <= C::BLOCKS; ++blk) {   // (the last: the sums)
+                  uint32_t r[16];
+                  const uint32_t at = trow + C::O_COL + blk * C::COLS + c0 + c;
+                  t_ld16(at, r);
+                  t_wait_ld();
 #pragma unroll
-              for (int c = 0; c < C::HALF; c += 16) {
-                if (c < hn) {
-                  float al[16];
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) al[e] = s.alpha[h0 + c + e];
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) l[c + e] *= al[e];
-                  for (int blk = 0; blk < C::BLOCKS; ++blk) {
-                    uint32_t r[16];
-                    const uint32_t at = trow + C::O_COL + blk * C::COLS + c0 + c;
-                    t_ld16(at, r);
-                    t_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                      r[e] = __float_as_uint(__uint_as_float(r[e]) * al[e]);
-                    t_st16(at, r);
-                  }
+                  for (int e = 0; e < 16; ++e)
+                    r[e] = __float_as_uint(__uint_as_float(r[e]) * s.alpha[h0 + c + e]);
+                  t_st16(at, r);
                 }
               }
               t_wait_st();
@@ -697,132 +787,117 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           weights();
         }
-        // the sums of the weights as they enter the product
-#pragma unroll
-        for (int c = 0; c < C::HALF; c += 2) {
-          if (c < hn)
-            t_add2(l[c], l[c + 1], __uint_as_float(pk[c / 2] << 16),
-                   __uint_as_float(pk[c / 2] & 0xffff0000u));
-        }
         t_fence_before();
         __syncwarp();
-        if (lane == 0) t_arrive(sfree + 8 * buf);
-        if (tiles >= 1) ok = ok && t_wait_warp(pvdone, tiles - 1, abort_flag);
-        // this key's columns in a row of 128 bytes for each 64, as the swizzle has them
+        if (lane == 0) t_arrive(sfree_x + 8 * buf);
+        if (tiles >= 1) ok = ok && t_wait_warp(pvdone_x, tiles - 1, abort_flag);
+        // this key's columns in a row of 128 bytes, as the swizzle has them
 #pragma unroll
-        for (int c = 0; c < C::HALF; c += 8) {
-          if (c < hn) {
-            const int col = c0 + c;
-            uint8_t *to = sm + C::OFF_P + (col >> 6) * C::P_ATOM + row * 128 +
-                          ((((col & 63) >> 3) ^ (row & 7)) << 4);
-            *reinterpret_cast<uint4 *>(to) =
-                make_uint4(pk[c / 2], pk[c / 2 + 1], pk[c / 2 + 2], pk[c / 2 + 3]);
-          }
-        }
+        for (int c = 0; c < HN; c += 8)
+          *reinterpret_cast<uint4 *>(pbuf + ((((c0 + c) >> 3) ^ (row & 7)) << 4)) =
+              make_uint4(pk[c / 2], pk[c / 2 + 1], pk[c / 2 + 2], pk[c / 2 + 3]);
         if (masked) {
-          // the tile's V entries: V(i) stands behind K(i + 1) in the ring. Rows seen by no node
+          // the tile's V entries: V(i) stands behind K(i + 1) in the ring. Rows seen by no column
           // are cleared, and those seen by some only if they are not finite
-          const int e0 = g + (2 * i + (i == nt - 1 ? 1 : 2)) * C::BLOCKS;
-          const uint64_t unit = ~0ull >> (kTreeMax - p.toks);
-          const bool some = (sees & unit) != 0, all = (sees & unit) == unit;
+          const int e0 = g + (2 * i + (i == nt - 1 ? 1 : 2)) * C::E;
+          const unsigned none = __ballot_sync(0xffffffffu, (sees & wide) == 0);
+          const unsigned part = __ballot_sync(0xffffffffu, (sees & wide) != 0 && (sees & wide) != wide);
           // a phase is told from the one before only, so the entries' previous tiles have to be
           // there: they stand at or before K(i) or V(i - 1) in the ring, whose products are done,
           // but for rings no longer than a tile, where they are K(i + 1)
-          static_assert(C::NS == C::BLOCKS || C::NS > 2 * C::BLOCKS, "previous tiles");
-          if (C::NS == C::BLOCKS && i < nt - 1)
-            ok = ok && t_wait_warp(sfull + 8 * (buf ^ 1), (tiles + 1) >> 1, abort_flag);
-          bool bad = false;
-          for (int blk = 0; blk < C::BLOCKS; ++blk) {
-            const int n = e0 + blk, e = n % C::NS, k = n / C::NS;
-            ok = ok && t_wait_warp(full + 8 * e, k, abort_flag);
-            // each half one atom; D = 64 has one, shared by halves of its row
-            constexpr int WORDS = C::ATOMS == 1 ? 4 : 8;
-            uint8_t *v = sm + e * C::ENTRY + (C::ATOMS == 1 ? 0 : half * C::ATOM) + row * 128 +
-                         (C::ATOMS == 1 ? half * 64 : 0);
-            if (some && !all) {
-#pragma unroll
-              for (int x = 0; x < WORDS; ++x) {
-                const uint4 y = *reinterpret_cast<const uint4 *>(v + 16 * x);
-                const uint32_t u[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                  bad |= (u[z] & 0x7f80u) == 0x7f80u || (u[z] & 0x7f800000u) == 0x7f800000u;
-              }
-            }
-          }
-          if (bad) {
-            const uint64_t who = (sees & unit) << p.tok0;
-            atomicOr(&w.poison[0], static_cast<unsigned>(who));
-            atomicOr(&w.poison[1], static_cast<unsigned>(who >> 32));
-          }
-          if ((bad || !some) && ok) {
+          static_assert(C::NS == C::E || C::NS >= 2 * C::E, "previous tiles");
+          if (none | part) {
+            if (C::NS == C::E && i < nt - 1)
+              ok = ok && t_wait_warp(sfull_x + 8 * (buf ^ 1), (tiles + 1) >> 1, abort_flag);
+            constexpr int KEYS = kTile / C::V_HALVES;    // of an entry
+            // this warp's share of a row of an entry: 8 lanes an atom, both atoms or its group's
+            constexpr int AT = D == 64 || C::GROUPS == 2 ? 1 : 2;
+            constexpr int STEP = 4 / AT;                 // rows at a time
+            const int in = (lane & 7) * 16 +
+                           ((C::GROUPS == 2 ? grp : AT == 2 ? (lane >> 3) & 1 : 0) * KEYS) * 128;
+            const int which = lane / (8 * AT);           // of the rows at a time
+#pragma unroll 1
             for (int blk = 0; blk < C::BLOCKS; ++blk) {
-              const int e = (e0 + blk) % C::NS;
-              constexpr int WORDS = C::ATOMS == 1 ? 4 : 8;
-              uint8_t *v = sm + e * C::ENTRY + (C::ATOMS == 1 ? 0 : half * C::ATOM) + row * 128 +
-                           (C::ATOMS == 1 ? half * 64 : 0);
-              for (int x = 0; x < WORDS; ++x)
-                *reinterpret_cast<uint4 *>(v + 16 * x) = make_uint4(0, 0, 0, 0);
+              const int n = e0 + blk * C::V_HALVES + 32 * quad / KEYS, e = n % C::NS;
+              ok = ok && t_wait_warp(full + 8 * e, n / C::NS, abort_flag);
+              if (!ok) break;
+              uint8_t *v = sm + e * C::ENTRY + in + (32 * quad % KEYS) * 128;
+              unsigned clear = none;
+              if (part) {
+#pragma unroll 1
+                for (int r = 0; r < 32; r += STEP) {
+                  if (!((part >> r) & ((1u << STEP) - 1))) continue;
+                  const uint4 y = *reinterpret_cast<const uint4 *>(v + (r + which) * 128);
+                  // 0 times what is finite stays 0
+                  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+                  __nv_bfloat162 z = zero;
+                  z = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&y.x), zero, z);
+                  z = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&y.y), zero, z);
+                  z = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&y.z), zero, z);
+                  z = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&y.w), zero, z);
+                  const bool bad = __isnan(__low2float(z)) || __isnan(__high2float(z));
+                  const unsigned who = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
+                  for (int q = 0; q < STEP; ++q)
+                    if ((who >> (8 * AT * q)) & ((1u << (8 * AT - 1) << 1) - 1))
+                      clear |= part & (1u << (r + q));
+                }
+              }
+              const unsigned poisoned = clear & part;
+              if (poisoned >> lane & 1) {
+                atomicOr(&w.poison[0], static_cast<unsigned>(sees & wide));
+                atomicOr(&w.poison[1], static_cast<unsigned>((sees & wide) >> 32));
+              }
+              if (clear) {
+#pragma unroll 1
+                for (int r = 0; r < 32; r += STEP)
+                  if (clear >> (r + which) & 1)
+                    *reinterpret_cast<uint4 *>(v + (r + which) * 128) = make_uint4(0, 0, 0, 0);
+              }
+              __syncwarp();
             }
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         t_fence_before();
         __syncwarp();
-        if (lane == 0) t_arrive(pfull);
+        if (lane == 0) t_arrive(pfull(x));
       }
-      if (gone) break;
-      g += 2 * nt * C::BLOCKS;
-      // the weights' sums of the columns, over the lanes and the half's warps
-#pragma unroll
-      for (int c = 0; c < C::HALF; c += 16) {
-        if (c < hn) {
-          float x[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = l[c + e];
-#pragma unroll
-          for (int o = 16, n = 8; o >= 2; o >>= 1, n >>= 1) {
-            const bool up = lane & o;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (e < n) {
-                const float give = up ? x[e] : x[e + n];
-                x[e] = (up ? x[e + n] : x[e]) + __shfl_xor_sync(0xffffffffu, give, o);
-              }
-            }
-          }
-          const float v = x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
-          const int col = (lane & 16 ? 8 : 0) + (lane & 8 ? 4 : 0) + (lane & 4 ? 2 : 0) +
-                          (lane & 2 ? 1 : 0);
-          if (!(lane & 1)) s.red[quad][h0 + c + col] = v;
-        }
-      }
-      ok = ok && t_wait_warp(pvdone, tiles - 1, abort_flag);
+      ok = ok && t_wait_warp(pvdone_x, tiles - 1, abort_flag);
       t_fence_after();
-      half_sync(half);
       const bool whole = p.whole();
-      const int place = 2 * cta + (p.t0 == 0 ? 1 : 0);
-      float *rec = a.parts + place * C::RECORD;
-      if (32 * quad + lane < hn) {
-        const int c = c0 + 32 * quad + lane, k = h0 + 32 * quad + lane;
-        float sum = (s.red[0][k] + s.red[1][k]) + (s.red[2][k] + s.red[3][k]);
-        if (c < cols) {
-          const int tok = p.tok0 + c / a.G;
-          if (any_masked && (w.poison[tok >> 5] >> (tok & 31) & 1)) sum = NAN;
-          if (!whole) {
-            rec[C::COLS * D + c] = s.ref[k];
-            rec[C::COLS * (D + 1) + c] = sum;
-          }
-        }
-        s.alpha[k] = sum == 0.f ? 0.f : 1.f / sum;
+      float *rec = a.parts + (2 * cta + (p.t0 == 0 ? 1 : 0)) * C::RECORD;
+      if (mine < HN) {
+        const int c = c0 + mine, k = h0 + mine, tok = p.tok0 + c / a.G;
+        const bool bad = any_masked && (w.poison[c >> 5] >> (c & 31) & 1);
+        s.dst[k] = c < cols ? (static_cast<long long>(p.n0 + tok) * a.Hq + p.head * a.G + c % a.G) * D
+                            : -1;
+        s.alpha[k] = bad ? NAN : 1.f;
+        if (!whole && c < cols) rec[C::COLS * D + c] = s.ref[k];
       }
-      half_sync(half);
+      group_sync(sub);
       if (ok) {
-#pragma unroll
-        for (int blk = 0; blk < C::BLOCKS; ++blk) {
-          const int d = blk * 128 + row;
 #pragma unroll 1
-          for (int c = 0; c < hn; c += 16) {
+        for (int c = 0; c < HN; c += 16) {
+          float l[16];
+          {
+            uint32_t r[16];
+            t_ld16(trow + C::L_COL + c0 + c, r);
+            t_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) l[e] = __uint_as_float(r[e]) * s.alpha[h0 + c + e];
+          }
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) l[e] = l[e] == 0.f ? 0.f : __fdividef(1.f, l[e]);
+          } else if (row == 0) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c0 + c + e < cols) rec[C::COLS * (D + 1) + c0 + c + e] = l[e];
+          }
+#pragma unroll 1
+          for (int blk = 0; blk < C::BLOCKS; ++blk) {
+            const int d = blk * 128 + row;
             uint32_t r[16];
             t_ld16(trow + C::O_COL + blk * C::COLS + c0 + c, r);
             t_wait_ld();
@@ -831,18 +906,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               // two columns a step: even lanes store one, odd lanes the other, two places each
 #pragma unroll
               for (int e = 0; e < 16; e += 2) {
-                const int col = c0 + c + e;
-                const float y0 = __uint_as_float(r[e]) * s.alpha[h0 + c + e];
-                const float y1 = __uint_as_float(r[e + 1]) * s.alpha[h0 + c + e + 1];
+                const float y0 = __uint_as_float(r[e]) * l[e];
+                const float y1 = __uint_as_float(r[e + 1]) * l[e + 1];
                 const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? y0 : y1, 1);
-                const int mine = col + (lane & 1);
                 const uint32_t v = lane & 1 ? t_pack(got, y1) : t_pack(y0, got);
-                if (mine < cols) {
-                  const int tok = mine / a.G;
-                  const long long o = static_cast<long long>(p.n0 + p.tok0 + tok) * a.Hq +
-                                      p.head * a.G + (mine - tok * a.G);
-                  *reinterpret_cast<uint32_t *>(a.out + o * D + (d & ~1)) = v;
-                }
+                const long long dst = s.dst[h0 + c + e + (lane & 1)];
+                if (dst >= 0) *reinterpret_cast<uint32_t *>(a.out + dst + (d & ~1)) = v;
               }
             } else {
 #pragma unroll
@@ -854,22 +923,48 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (tid == 0 && !whole && p.t0 == 0) {
+      if (warp == 4 * x && lane == 0 && !whole && p.t0 == 0) {
         // the CTA of the unit's last tile
         const long long at = p.start + kStart + p.ntiles - 1;
         int c = static_cast<int>(at * ctas / W);
         while (c > 0 && share(W, c, ctas) > at) --c;
         while (share(W, c + 1, ctas) <= at) ++c;
-        Cut cut = {p.n0 + p.tok0, cols, p.head, c - cta + 1};
+        const Cut cut = {p.n0 + p.tok0, cols, p.head, c - cta + 1};
         a.cuts[cta] = cut;
       }
       t_fence_before();
       __syncwarp();
       if (lane == 0) {
-        t_arrive(ofree);
-        t_arrive(prepempty + 8 * (segs & 1));
+        t_arrive(ofree(x));
+        t_arrive(prepempty + 8 * (seg & 1));
       }
-      ++segs;
+    };
+    while (!gone && line.next(p)) {
+      const int cols = p.toks * a.G;
+      if (p.ntiles == 0) {                      // padding
+        for (int i = warp; i < cols; i += C::SOFT) {   // all units' warps share them
+          const long long o = (static_cast<long long>(p.n0 + p.tok0 + i / a.G) * a.Hq +
+                               p.head * a.G + i % a.G) * D;
+          for (int d = 2 * lane; d < D; d += 64)
+            *reinterpret_cast<uint32_t *>(a.out + o + d) = 0;
+        }
+        continue;
+      }
+      if (p.t0 == p.t1) continue;
+      seg = segs++;
+      if (seg % U != x) {
+        g += 2 * (p.t1 - p.t0) * C::E;
+        continue;
+      }
+      // code of its own for every number of chunks: with tests around unused ones the warps
+      // wait for instructions more than for anything else
+      switch (columns<C::GROUPS>(cols) / (16 * C::GROUPS)) {
+        case 1: unit(std::integral_constant<int, 1>()); break;
+        case 2: unit(std::integral_constant<int, 2>()); break;
+        case 3: if (C::HALF >= 48) unit(std::integral_constant<int, C::HALF >= 48 ? 3 : 1>()); break;
+        default: if (C::HALF >= 64) unit(std::integral_constant<int, C::HALF >= 64 ? 4 : 1>());
+      }
+      g += 2 * (p.t1 - p.t0) * C::E;
     }
     if ((gone || !ok) && lane == 0) tree_report(a.err, PKV_ERR_TIMEOUT);
   }
@@ -878,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   t_fence_after();
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(C::TMEM_COLS));
+                 "r"(512));
 }
 
 // Joins the parts of the unit that CTA blockIdx.x began and others went on with: a warp a column.
@@ -957,16 +1052,21 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
   }
   const int sms = pkv::sm_count();
   const int grid = sms < 1 ? 1 : sms < kMaxCtas ? sms : kMaxCtas;
-  a.unit_tokens = C::COLS / (8 * a.G) * 8;
+  // a Q box is so many nodes that its rows fill whole swizzle atoms of 8
+  const int box_nodes = a.G % 8 == 0 ? 1 : a.G % 4 == 0 ? 2 : a.G % 2 == 0 ? 4 : 8;
+  a.unit_tokens = C::COLS / (box_nodes * a.G) * box_nodes;
+  a.box_nodes = box_nodes;
   a.cuts = static_cast<Cut *>(workspace);
   a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + kMaxCtas * sizeof(Cut));
   CUtensorMap tmQ, tmK, tmV;
-  const int rows = a.n_pages * a.page_size, box = a.page_size < kTile ? a.page_size : kTile;
-  int st = pkv::prefill_atoms_map(&tmQ, q, a.N, a.Hq, D, a.G, 8, 1);
-  if (st == PKV_OK) st = pkv::prefill_atoms_map(&tmK, k, a.Hkv, rows, D, box, 1, 1);
-  if (st == PKV_OK) st = pkv::prefill_atoms_map(&tmV, v, a.Hkv, rows, D, box, 1, 1);
+  const int rows = a.n_pages * a.page_size;
+  const int k_box = a.page_size < kTile ? a.page_size : kTile;
+  const int v_box = a.page_size < kTile / C::V_HALVES ? a.page_size : kTile / C::V_HALVES;
+  int st = pkv::prefill_atoms_map(&tmQ, q, a.N, a.Hq, D, a.G, box_nodes, 1);
+  if (st == PKV_OK) st = pkv::prefill_atoms_map(&tmK, k, a.Hkv, rows, D, k_box, 1, 1);
+  if (st == PKV_OK) st = pkv::prefill_atoms_map(&tmV, v, a.Hkv, rows, D, v_box, 1, 1);
   if (st != PKV_OK) return st;
-  PKV_CUDA_CHECK(pkv::launch_pdl(tree_attn_kernel<D>, dim3(grid), dim3(kThreads), smem_bytes<D>(),
+  PKV_CUDA_CHECK(pkv::launch_pdl(tree_attn_kernel<D>, dim3(grid), dim3(C::THREADS), smem_bytes<D>(),
                                  s, tmQ, tmK, tmV, a));
   PKV_CUDA_CHECK(pkv::launch_pdl(tree_join_kernel<D>, dim3(grid, C::COLS / kJoinCols),
                                  dim3(kJoinCols * 32), 0, s, static_cast<const float *>(a.parts),
