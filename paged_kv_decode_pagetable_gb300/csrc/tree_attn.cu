@@ -38,7 +38,6 @@
 
 #include <cmath>
 #include <mutex>
-#include <type_traits>
 
 #include "pkv_internal.h"
 #include "tcgen05.cuh"
@@ -50,6 +49,7 @@ constexpr int kTile = 128;               // keys of a tile
 constexpr int kStart = 1;                // places on the line for a unit's start
 constexpr int kMaxCtas = 160;            // CTAs the workspace has room for
 constexpr float kLazyLog2 = 8.f;
+constexpr int kMostPlaces = 0x7fffffff;  // as many and more are reported, not computed
 constexpr float kUnset = 1e30f;          // stands for -reference of a column without one
 constexpr int kJoinCols = 8;             // columns of a joining CTA
 
@@ -100,8 +100,8 @@ struct Cut {
 
 struct Small {
   Prep prep[2];
-  long long pre[kTreeRows + 1];     // first place of every row on the line
-  int ctx[kTreeRows], slot[kTreeRows];
+  int pre[kTreeRows + 1];           // first place of every row on the line
+  int n0[kTreeRows], ctx[kTreeRows], slot[kTreeRows];
   uint8_t n[kTreeRows];
   // of the columns, group g's from g * HALF on (the groups may be at different units)
   alignas(16) float mneg[128];      // a column's reference's negative, kUnset: none yet
@@ -110,10 +110,9 @@ struct Small {
   long long dst[128];               // its place in out, -1: none
   float red[4][128];                // maxima of the four warps of a group
   int pages[2][16];
-  long long scan[12];
+  int scan[12];
   uint64_t bars[48];
   uint32_t tmem;
-  int abort;
 };
 
 template <int D>
@@ -146,6 +145,21 @@ __device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, f
       "mov.b64 rc, {%5, %6};\nfma.rn.f32x2 rd, ra, rb, rc;\nmov.b64 {%0, %1}, rd;\n}"
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+// Waits for completion number k of a barrier's phases, by a whole warp with one answer; false if
+// it gave up, after about two seconds. (A loop of few instructions: the waits are many, and a
+// kernel that does not fit the instruction caches waits for its code instead.)
+__device__ __forceinline__ bool wait_for(uint32_t bar, int k) {
+  uint32_t done;
+  asm volatile(
+      "{\n.reg .pred p, q;\n.reg .u32 n;\nmov.u32 n, 0;\n"
+      "WAIT:\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1024;\n"
+      "@p bra DONE;\nadd.u32 n, n, 1;\nsetp.lt.u32 q, n, %3;\n@q bra WAIT;\n"
+      "DONE:\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(static_cast<uint32_t>(k) & 1u), "n"(1 << 21)
+      : "memory");
+  return __all_sync(0xffffffffu, done != 0);
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -193,24 +207,30 @@ __device__ __forceinline__ int columns(int cols) {
   return (cols + 16 * GROUPS - 1) / (16 * GROUPS) * (16 * GROUPS);
 }
 
+// sums of places stop at kMostPlaces
+__device__ __forceinline__ int add_places(int a, int b) {
+  return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b),
+                              static_cast<unsigned>(kMostPlaces)));
+}
+
 // A unit, or the part of it that this CTA has: tiles [t0, t1) of ntiles.
 struct Part {
   int b, head, tok0, toks, n0, n, ctx, lo, tile0, ntiles, t0, t1;
-  long long start;   // the unit's first place on the line
+  int start;   // the unit's first place on the line
   __device__ bool whole() const { return t0 == 0 && t1 == ntiles; }
 };
 
 struct Line {
   const Small *sm;
   const Args *a;
-  long long pos, end;
-  int b;
-  __device__ void begin(const Small &s, const Args &args, long long x0, long long x1) {
+  int pos, end, b;
+  __device__ void begin(const Small &s, const Args &args, int x0, int x1) {
     sm = &s;
     a = &args;
     pos = x0;
     end = x1;
     int l = 0, r = args.B;   // the last row that starts at or before x0
+#pragma unroll 1
     while (r - l > 1) {
       const int m = (l + r) / 2;
       if (s.pre[m] <= x0) l = m;
@@ -220,24 +240,23 @@ struct Line {
   }
   __device__ bool next(Part &p) {
     if (pos >= end) return false;
+#pragma unroll 1
     while (pos >= sm->pre[b + 1]) ++b;
     p.b = b;
-    p.n0 = a->row_start[b];
+    p.n0 = sm->n0[b];
     p.n = sm->n[b] & 127;
     p.ctx = sm->ctx[b];
     p.lo = a->window > 0 ? max(0, p.ctx - a->window + 1) : 0;
     p.tile0 = p.lo / kTile;
     p.ntiles = sm->n[b] & 128 ? 0 : (p.ctx + p.n - 1) / kTile - p.tile0 + 1;
     const int cost = p.ntiles + kStart;
-    const long long local = pos - sm->pre[b];
-    const long long u = (local >> 31) ? local / cost
-                                      : static_cast<uint32_t>(local) / static_cast<uint32_t>(cost);
+    const unsigned local = pos - sm->pre[b], u = local / static_cast<unsigned>(cost);
     const int off = static_cast<int>(local - u * cost);
     const int units = (p.n + a->unit_tokens - 1) / a->unit_tokens;
     p.head = static_cast<int>(u) / units;
     p.tok0 = (static_cast<int>(u) - p.head * units) * a->unit_tokens;
     p.toks = min(a->unit_tokens, p.n - p.tok0);
-    const int to = static_cast<int>(min(static_cast<long long>(cost), off + (end - pos)));
+    const int to = min(cost, off + (end - pos));
     p.t0 = max(0, off - kStart);
     p.t1 = max(0, to - kStart);
     p.start = pos - off;
@@ -246,8 +265,13 @@ struct Line {
   }
 };
 
-// first place of CTA c's share of W places among n CTAs
-__device__ __forceinline__ long long share(long long W, int c, int n) { return W * c / n; }
+// The line's W places in equal shares for n CTAs, the first ones one longer where need be: the
+// first place of CTA c's, and the CTA that has a place.
+__device__ __forceinline__ int share(int W, int c, int n) { return W / n * c + min(c, W % n); }
+__device__ __forceinline__ int share_of(int W, int at, int n) {
+  const int q = W / n, r = W % n, head = r * (q + 1);
+  return at < head ? at / (q + 1) : r + (at - head) / q;
+}
 
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
@@ -276,18 +300,20 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   auto qfull = [&](int x) { return unit0 + 8 * (UB * x + 7); };
   auto qempty = [&](int x) { return unit0 + 8 * (UB * x + 8); };
   auto turn = [&](int x) { return unit0 + 8 * (UB * x + 9); };
-  volatile int *abort_flag = &s.abort;
   static_assert(2 * C::NS + 4 + U + U * UB <= 48, "barriers");
 
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < C::NS; ++i) {
       t_bar_init(full + 8 * i, 1);
       t_bar_init(empty + 8 * i, 1);
     }
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       t_bar_init(prepfull + 8 * i, 1);
       t_bar_init(prepempty + 8 * i, C::SOFT / U);
     }
+#pragma unroll 1
     for (int x = 0; x < U; ++x) {
       for (int b = 0; b < 2; ++b) {
         t_bar_init(sfull(x, b), 1);
@@ -301,9 +327,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       t_bar_init(turn(x), 1);
       t_bar_init(drain + 8 * x, 1);
     }
-    s.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+#pragma unroll 1
   for (int i = tid; i < 256; i += C::THREADS)
     reinterpret_cast<uint32_t *>(sm + C::OFF_ONES)[i] = 0x3f803f80u;
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -319,8 +345,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   // the line: places of every row, summed up over the rows
   {
     constexpr int R = (kTreeRows + C::THREADS) / C::THREADS;   // rows of a thread, and the end
-    long long mine[R];
-    long long sum = 0;
+    int mine[R], sum = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int b = R * tid + i;
@@ -329,6 +354,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const TreeRow r = tree_row(b, a.N, a.row_start, a.batch_idx, a.ctx_lens, a.n_slots,
                                    a.max_pages, a.page_size);
         if (r.bits && cta == 0) tree_report(a.err, r.bits);
+        s.n0[b] = r.n0;
         s.ctx[b] = r.ctx;
         s.slot[b] = r.slot;
         // the top bit: padding, only zeros to write
@@ -336,37 +362,42 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (r.n > 0) {
           const int lo = a.window > 0 ? max(0, r.ctx - a.window + 1) : 0;
           const int tiles = r.slot == 0 ? 0 : (r.ctx + r.n - 1) / kTile - lo / kTile + 1;
-          mine[i] = static_cast<long long>(tiles + kStart) * a.Hkv *
-                    ((r.n + a.unit_tokens - 1) / a.unit_tokens);
+          mine[i] = static_cast<int>(min(static_cast<long long>(kMostPlaces),
+                                         static_cast<long long>(tiles + kStart) *
+                                             (a.Hkv * ((r.n + a.unit_tokens - 1) / a.unit_tokens))));
         }
       }
-      sum += mine[i];
+      sum = add_places(sum, mine[i]);
     }
-    const long long own = sum;
+    int upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto = add_places(upto, v);
     }
-    if (lane == 31) s.scan[warp] = sum;
+    if (lane == 31) s.scan[warp] = upto;
     t_fence_before();
     __syncthreads();
     t_fence_after();
 #pragma unroll
-    for (int w = 0; w < C::THREADS / 32 - 1; ++w) sum += w < warp ? s.scan[w] : 0;
-    sum -= own;
+    for (int w = 0; w < C::THREADS / 32 - 1; ++w)
+      upto = w < warp ? add_places(upto, s.scan[w]) : upto;
+    // (where the sum ran over, only its end counts)
+    sum = upto - sum;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (R * tid + i <= a.B) s.pre[R * tid + i] = sum;
-      sum += mine[i];
+      sum = add_places(sum, mine[i]);
     }
     __syncthreads();
   }
   const uint32_t tmem = s.tmem;
-  const long long W = s.pre[a.B];
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), W));
-  const long long x0 = cta < ctas ? share(W, cta, ctas) : 0;
-  const long long x1 = cta < ctas ? share(W, cta + 1, ctas) : 0;
+  const bool too_long = s.pre[a.B] == kMostPlaces;
+  const int W = too_long ? 0 : s.pre[a.B];
+  if (too_long && cta == 0 && tid == 0) tree_report(a.err, PKV_ERR_POS);
+  const int ctas = min(static_cast<int>(gridDim.x), W);
+  const int x0 = cta < ctas ? share(W, cta, ctas) : 0;
+  const int x1 = cta < ctas ? share(W, cta + 1, ctas) : 0;
   Line line;
   line.begin(s, a, x0, x1);
   Part p;
@@ -383,7 +414,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     // room in the next entry, and how many bytes will come
     auto take = [&](int boxes, int rows) -> int {
       const int e = g % C::NS;
-      if (g >= C::NS && !t_wait_warp(empty + 8 * e, g / C::NS - 1, abort_flag)) {
+      if (g >= C::NS && !wait_for(empty + 8 * e, g / C::NS - 1)) {
         ok = false;
         return 0;
       }
@@ -395,6 +426,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     // a K tile: 64 columns of all its pages [first, last) an entry
     auto load_k = [&](int which, int head, int j0, int first, int last) {
       const int in_page = j0 & (a.page_size - 1);   // (pages larger than a tile)
+#pragma unroll 1
       for (int at = 0; at < C::E && ok; ++at) {
         const int e = take(last - first, k_rows);
         if (!ok) break;
@@ -409,6 +441,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const int in_page = j0 & (a.page_size - 1);
       constexpr int AT = D == 64 ? 1 : 2;
       const int per = kTile / C::V_HALVES / v_rows;   // pages of an entry
+#pragma unroll 1
       for (int c = 0; c < C::E && ok; ++c) {
         const int half = c % C::V_HALVES, blk = c / C::V_HALVES;
         // pages [p0, p0 + per) of the tile; one larger than an entry serves both halves
@@ -439,6 +472,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       int base = ((p.tile0 + p.t0) * kTile) >> a.log_page;
       int now = fetch(base + lane), then = fetch(base + 32 + lane);
       int kf = 0, kl = 0;      // pages of the last K tile that are there
+#pragma unroll 1
       for (int t = p.t0; t <= p.t1 && ok; ++t) {
         const int pf = kf, pl = kl;
         if (t < p.t1) {
@@ -466,9 +500,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       }
     }
     tree_report(a.err, bits);
-    if (!ok || *abort_flag) {
+    if (!ok) {
       // what is on its way lands before the CTA leaves
+#pragma unroll 1
       for (int i = max(0, g - C::NS); i < g; ++i) {
+#pragma unroll 1
         for (int k = 0; k < kSpin && !t_test(full + 8 * (i % C::NS), i / C::NS); ++k) {
         }
       }
@@ -484,46 +520,55 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     const uint32_t tx = __shfl_sync(0xffffffffu, tmem + x * C::UNIT_COLS, 0);
     const uint64_t dQ = t_desc(sQ + x * C::Q_BYTES, 16, 1024);
     const uint64_t dP = t_desc(sP + x * C::P_BYTES, 0, 1024), dOne = t_desc(sOnes, 0, 0);
-    auto wait_entry = [&](int i) -> bool {
-      return t_wait_warp(full + 8 * (i % C::NS), i / C::NS, abort_flag);
+    // the next BT ring entries, once they are there: waits, fences and elections cost more than
+    // issuing the MMAs of one
+    constexpr int BT = C::E < 2 ? 1 : 2;
+    uint32_t entry[BT];
+    auto take = [&]() {
+#pragma unroll
+      for (int b = 0; b < BT; ++b, ++g) {
+        entry[b] = __shfl_sync(0xffffffffu, g % C::NS, 0);
+        ok = ok && wait_for(full + 8 * entry[b], g / C::NS);
+      }
+      t_fence_after();
     };
     // P V of a tile, and the weights' sums: a row of ones, 128 times
     auto do_pv = [&](uint32_t id, int pv, bool first, bool last) {
       if (U == 2 && last) {   // the unit's last entries: the other unit's turn
-        for (int c = 0; c < C::E && ok; ++c) ok = wait_entry(g + c);
+#pragma unroll 1
+        for (int c = 0; c < C::E; ++c)
+          ok = ok && wait_for(full + 8 * ((g + c) % C::NS), (g + c) / C::NS);
         if (ok && lane == 0) t_arrive(turn(x ^ 1));
       }
-      ok = ok && t_wait_warp(pfull(x), pv, abort_flag);
-      if (first && own >= 1) ok = ok && t_wait_warp(ofree(x), own - 1, abort_flag);
+      ok = ok && wait_for(pfull(x), pv);
+      if (first && own >= 1) ok = ok && wait_for(ofree(x), own - 1);
+      const uint32_t add = !first;
 #pragma unroll 1
-      for (int c = 0; c < C::E && ok; ++c, ++g) {
-        if (!wait_entry(g)) {
-          ok = false;
-          break;
-        }
-        t_fence_after();
-        const int half = c % C::V_HALVES, blk = c / C::V_HALVES;
-        const uint32_t e = __shfl_sync(0xffffffffu, g % C::NS, 0);
-        const uint32_t to = tx + C::O_COL + blk * C::COLS;
-        // (D = 64: rows 64 .. 127 of the product repeat rows 0 .. 63)
-        const uint64_t va = t_desc(sRing + e * C::ENTRY, D == 64 ? 0 : kTile / 2 * 128, 1024);
-        const uint64_t pb = dP + half * (kTile / 2 * 128 >> 4);
-        const uint32_t add = half > 0 || !first;
+      for (int c = 0; c < C::E && ok; c += BT) {
+        take();
+        if (!ok) break;
+        const uint32_t to = tx + C::O_COL + c / C::V_HALVES * C::COLS;
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kTile / C::V_HALVES / 16; ++k)
-            t_mma(to, va + k * (2048 >> 4), pb + k * (2048 >> 4), id, k > 0 ? 1u : add);
-          t_commit(empty + 8 * e);
+          for (int b = 0; b < BT; ++b) {
+            // (D = 64: rows 64 .. 127 of the product repeat rows 0 .. 63)
+            const uint64_t va =
+                t_desc(sRing + entry[b] * C::ENTRY, D == 64 ? 0 : kTile / 2 * 128, 1024);
+            const uint64_t pb = dP + b * (kTile / 2 * 128 >> 4);
+#pragma unroll
+            for (int k = 0; k < kTile / C::V_HALVES / 16; ++k)
+              t_mma(to, va + k * (2048 >> 4), pb + k * (2048 >> 4), id, b > 0 || k > 0 ? 1u : add);
+            t_commit(empty + 8 * entry[b]);
+          }
+          if (c + BT == C::E) {
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              t_mma(tx + C::L_COL, dOne, dP + k * (2048 >> 4), id, k > 0 ? 1u : add);
+            t_commit(pvdone(x));
+          }
         }
         __syncwarp();
       }
-      if (ok && elect_one()) {
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          t_mma(tx + C::L_COL, dOne, dP + k * (2048 >> 4), id, k > 0 || !first ? 1u : 0u);
-        t_commit(pvdone(x));
-      }
-      __syncwarp();
     };
     while (ok && line.next(p)) {
       if (p.t0 == p.t1) continue;
@@ -534,40 +579,42 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       }
       // An entry's phase is told from the one before only. So a unit begins when all entries
       // before its own have landed, which the other unit's warp has seen.
-      if (U == 2 && seg > 0 && !t_wait_warp(turn(x), (seg - 1) / 2, abort_flag)) break;
+      if (U == 2 && seg > 0 && !wait_for(turn(x), (seg - 1) / 2)) break;
       const int N = __shfl_sync(0xffffffffu, columns<C::GROUPS>(p.toks * a.G), 0);
       const uint32_t idS = idesc(N, false), idO = idesc(N, true);
-      if (!t_wait_warp(qfull(x), own, abort_flag)) break;
-      for (int t = p.t0; t < p.t1 && ok; ++t, ++tiles) {
-        const int buf = tiles & 1;
-        if (tiles >= 2) ok = t_wait_warp(sfree(x, buf), (tiles >> 1) - 1, abort_flag);
-        const uint32_t to = __shfl_sync(0xffffffffu, tx + C::S_COL + buf * C::COLS, 0);
+      if (!wait_for(qfull(x), own)) break;
 #pragma unroll 1
-        for (int c = 0; c < C::E && ok; ++c, ++g) {
-          if (!wait_entry(g)) {
-            ok = false;
-            break;
-          }
-          t_fence_after();
-          const uint32_t e = __shfl_sync(0xffffffffu, g % C::NS, 0);
-          const uint64_t ka = t_desc(sRing + e * C::ENTRY, 16, 1024);
-          const uint64_t qb = dQ + c * (C::Q_ATOM >> 4);
-          if (elect_one()) {
+      for (int t = p.t0; t <= p.t1 && ok; ++t) {
+        if (t < p.t1) {
+          const int buf = tiles & 1;
+          if (tiles >= 2) ok = wait_for(sfree(x, buf), (tiles >> 1) - 1);
+          const uint32_t to = __shfl_sync(0xffffffffu, tx + C::S_COL + buf * C::COLS, 0);
+#pragma unroll 1
+          for (int c = 0; c < C::E && ok; c += BT) {
+            take();
+            if (!ok) break;
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) t_mma(to, ka + k * 2, qb + k * 2, idS, c > 0 || k > 0);
-            t_commit(empty + 8 * e);
+              for (int b = 0; b < BT; ++b) {
+                const uint64_t ka = t_desc(sRing + entry[b] * C::ENTRY, 16, 1024);
+                const uint64_t qb = dQ + (c + b) * (C::Q_ATOM >> 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  t_mma(to, ka + k * 2, qb + k * 2, idS, c > 0 || b > 0 || k > 0);
+                t_commit(empty + 8 * entry[b]);
+              }
+              if (c + BT == C::E) {
+                t_commit(sfull(x, buf));
+                if (t == p.t1 - 1) t_commit(qempty(x));
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          ++tiles;
         }
-        if (!ok) break;
-        if (elect_one()) {
-          t_commit(sfull(x, buf));
-          if (t == p.t1 - 1) t_commit(qempty(x));
-        }
-        __syncwarp();
-        if (t > p.t0) do_pv(idO, tiles - 1, t == p.t0 + 1, false);
+        if (t > p.t0 && ok)
+          do_pv(idO, tiles - (t < p.t1 ? 2 : 1), t == p.t0 + 1, t == p.t1);
       }
-      if (ok) do_pv(idO, tiles - 1, p.t1 - p.t0 == 1, true);
       ++own;
     }
     if (elect_one()) {
@@ -582,17 +629,19 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     while (line.next(p)) {
       if (p.t0 == p.t1) continue;
       const int x = segs % U;
-      if (segs >= U && !t_wait_warp(qempty(x), segs / U - 1, abort_flag)) break;
+      if (segs >= U && !wait_for(qempty(x), segs / U - 1)) break;
       if (lane == 0) {
         const int boxes = (p.toks + a.box_nodes - 1) / a.box_nodes;
         t_expect_tx(qfull(x), boxes * box * (D / 64));
+#pragma unroll 1
         for (int i = 0; i < boxes; ++i)
+#pragma unroll 1
           for (int at = 0; at < D / 64; ++at)
             t_tma_4d(sQ + x * C::Q_BYTES + at * C::Q_ATOM + i * box, &tmQ, 0, p.head * a.G,
                      p.n0 + p.tok0 + a.box_nodes * i, at, qfull(x));
       }
       Prep &w = s.prep[segs & 1];
-      if (segs >= 2 && !t_wait_warp(prepempty + 8 * (segs & 1), (segs >> 1) - 1, abort_flag)) break;
+      if (segs >= 2 && !wait_for(prepempty + 8 * (segs & 1), (segs >> 1) - 1)) break;
       // paths: each node's set of ancestors and itself, twice as far every time
       uint64_t *path = w.below;
       int *jump = w.depth;
@@ -602,6 +651,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         jump[i] = i < p.n ? tree_parent(a.parents, p.n0, i, bits) : -1;
       }
       __syncwarp();
+#pragma unroll 1
       for (int r = 0; r < 6; ++r) {
         uint64_t v[2];
         int j[2];
@@ -627,6 +677,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       uint64_t below[2] = {0, 0}, shallow[2] = {0, 0};
       int depth[2] = {0, 0};
       const uint64_t heads = (1ull << a.G) - 1;     // a node's columns
+#pragma unroll 1
       for (int t = 0; t < p.n; ++t) {
         const uint64_t v = path[t];
         const int d = __popcll(v) - 1;
@@ -665,15 +716,17 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     const int mine = 32 * quad + lane;          // the column that this thread looks after
     int tiles = 0, segs = 0, seg = 0, g = 0;    // g: ring entries of the parts so far
     bool ok = true, gone = false;
-    // a unit (or its part) with CH chunks of 16 columns a group
-    auto unit = [&](auto chunks) {
-      constexpr int CH = decltype(chunks)::value, HN = 16 * CH;
-      const int cols = p.toks * a.G, c0 = grp * HN;
+    // A unit, or the part of it that is this CTA's. Loops over chunks of 16 columns stay loops:
+    // unrolled, the warps waited for instructions a third of the time.
+    auto unit = [&]() {
+      const int cols = p.toks * a.G;
+      const int hn = columns<C::GROUPS>(cols) / C::GROUPS, c0 = grp * hn;   // this warp's columns
       Prep &w = s.prep[seg & 1];
       const int nt = p.t1 - p.t0;
       // the columns in use of the warp's own
       const uint64_t wide = cols >= 64 ? ~0ull : (1ull << cols) - 1;
       bool any_masked = false;
+#pragma unroll 1
       for (int t = p.t0; t < p.t1; ++t, ++tiles) {
         const int buf = tiles & 1, i = t - p.t0;
         const int j0 = (p.tile0 + t) * kTile, j = j0 + row;
@@ -683,9 +736,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         uint64_t sees = ~0ull;                  // the columns that see this thread's key
         any_masked |= masked;
         // (S first: the unit's queries are there then, and the preparations before its own)
-        ok = ok && t_wait_warp(sfull_x + 8 * buf, tiles >> 1, abort_flag);
+        ok = ok && wait_for(sfull_x + 8 * buf, tiles >> 1);
         if (masked) {
-          ok = ok && t_wait_warp(prepfull + 8 * (seg & 1), seg >> 1, abort_flag);
+          ok = ok && wait_for(prepfull + 8 * (seg & 1), seg >> 1);
           const int node = j - p.ctx;
           if (node >= p.n) {
             sees = 0;
@@ -702,74 +755,52 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         t_fence_after();
         const uint32_t scol = trow + C::S_COL + buf * C::COLS + c0;
         // 16 scores of this thread's key, -inf where a node does not see it
-        auto scores = [&](int c, float (&x)[16]) {
+        auto scores = [&](int c, float (&y)[16]) {
           uint32_t r[16];
           t_ld16(scol + c, r);
           t_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[e]);
+          for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(r[e]);
           if (masked) {
             const uint32_t bits = static_cast<uint32_t>(sees >> (c0 + c));
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = bits & (1u << e) ? x[e] : -INFINITY;
+            for (int e = 0; e < 16; ++e) y[e] = bits & (1u << e) ? y[e] : -INFINITY;
           }
         };
-        uint32_t pk[HN / 2];
-        // the weights under the references at hand; whether one is out of reach
-        auto weights = [&]() -> bool {
-          float top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < HN; c += 16) {
-            float x[16];
-            scores(c, x);
-            const float4 *m4 = reinterpret_cast<const float4 *>(s.mneg + h0 + c);
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 m = m4[e / 4];
-              fma2(x[e], x[e + 1], x[e], x[e + 1], a.scale_log2, m.x, m.y);
-              fma2(x[e + 2], x[e + 3], x[e + 2], x[e + 3], a.scale_log2, m.z, m.w);
-              top = t_max3(top, x[e], x[e + 1]);
-              top = t_max3(top, x[e + 2], x[e + 3]);
+        // P's place is free once the tile before has been multiplied
+        if (tiles >= 1) {
+          ok = ok && wait_for(pvdone_x, tiles - 1);
+          t_fence_after();
+        }
+        // a first tile begins with the columns' maxima, others when a score is out of reach
+        for (bool exact = first;;) {
+          if (exact) {
+            if (group_any(sub, !ok)) {
+              gone = true;
+              return;
             }
-#pragma unroll
-            for (int e = 0; e < 16; e += 2)
-              pk[(c + e) / 2] = t_pack(t_ex2(x[e]), t_ex2(x[e + 1]));
-          }
-          return top > kLazyLog2;
-        };
-        bool slow = false;
-        if (!first) slow = ok && weights();
-        if (first || group_any(sub, slow || !ok)) {
-          if (group_any(sub, !ok)) {
-            gone = true;
-            return;
-          }
-          // the columns' maxima over the tile
 #pragma unroll 1
-          for (int c = 0; c < HN; c += 16) {
-            float x[16];
-            scores(c, x);
-            const float v = column_max(x, lane);
-            if (!(lane & 1)) s.red[quad][h0 + c + column_of(lane)] = v;
-          }
-          group_sync(sub);
-          if (mine < HN) {
-            const int c = h0 + mine;
-            const float old = first ? -INFINITY : s.ref[c];
-            const float top = fmaxf(fmaxf(s.red[0][c], s.red[1][c]),
-                                    fmaxf(s.red[2][c], s.red[3][c])) * a.scale_log2;
-            const float ref = fmaxf(old, top);
-            s.ref[c] = ref;
-            s.mneg[c] = ref == -INFINITY ? kUnset : -ref;
-            s.alpha[c] = old == ref ? 1.f : exp2f(old - ref);
-          }
-          group_sync(sub);
-          if (!first) {
-            ok = t_wait_warp(pvdone_x, tiles - 1, abort_flag);
-            t_fence_after();
-            if (ok) {
+            for (int c = 0; c < hn; c += 16) {
+              float y[16];
+              scores(c, y);
+              const float v = column_max(y, lane);
+              if (!(lane & 1)) s.red[quad][h0 + c + column_of(lane)] = v;
+            }
+            group_sync(sub);
+            if (mine < hn) {
+              const int c = h0 + mine;
+              const float old = first ? -INFINITY : s.ref[c];
+              const float top = fmaxf(fmaxf(s.red[0][c], s.red[1][c]),
+                                      fmaxf(s.red[2][c], s.red[3][c])) * a.scale_log2;
+              const float ref = fmaxf(old, top);
+              s.ref[c] = ref;
+              s.mneg[c] = ref == -INFINITY ? kUnset : -ref;
+              s.alpha[c] = old == ref ? 1.f : exp2f(old - ref);
+            }
+            group_sync(sub);
+            if (!first) {
 #pragma unroll 1
-              for (int c = 0; c < HN; c += 16) {
+              for (int c = 0; c < hn; c += 16) {
 #pragma unroll 1
                 for (int blk = 0; blk <= C::BLOCKS; ++blk) {   // (the last: the sums)
                   uint32_t r[16];
@@ -785,17 +816,39 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
               t_wait_st();
             }
           }
-          weights();
+          // the weights under the references at hand, a key's columns in a row of 128 bytes as
+          // the swizzle has them
+          float top = -INFINITY;
+          if (ok) {
+#pragma unroll 1
+            for (int c = 0; c < hn; c += 16) {
+              float y[16];
+              scores(c, y);
+              const float4 *m4 = reinterpret_cast<const float4 *>(s.mneg + h0 + c);
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const float4 m = m4[e / 4];
+                fma2(y[e], y[e + 1], y[e], y[e + 1], a.scale_log2, m.x, m.y);
+                fma2(y[e + 2], y[e + 3], y[e + 2], y[e + 3], a.scale_log2, m.z, m.w);
+                top = t_max3(top, y[e], y[e + 1]);
+                top = t_max3(top, y[e + 2], y[e + 3]);
+                w[e / 2] = t_pack(t_ex2(y[e]), t_ex2(y[e + 1]));
+                w[e / 2 + 1] = t_pack(t_ex2(y[e + 2]), t_ex2(y[e + 3]));
+              }
+              const int at = (c0 + c) >> 3;
+              *reinterpret_cast<uint4 *>(pbuf + ((at ^ (row & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4 *>(pbuf + (((at + 1) ^ (row & 7)) << 4)) =
+                  make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
+          if (exact || !group_any(sub, top > kLazyLog2 || !ok)) break;
+          exact = true;
         }
         t_fence_before();
         __syncwarp();
         if (lane == 0) t_arrive(sfree_x + 8 * buf);
-        if (tiles >= 1) ok = ok && t_wait_warp(pvdone_x, tiles - 1, abort_flag);
-        // this key's columns in a row of 128 bytes, as the swizzle has them
-#pragma unroll
-        for (int c = 0; c < HN; c += 8)
-          *reinterpret_cast<uint4 *>(pbuf + ((((c0 + c) >> 3) ^ (row & 7)) << 4)) =
-              make_uint4(pk[c / 2], pk[c / 2 + 1], pk[c / 2 + 2], pk[c / 2 + 3]);
         if (masked) {
           // the tile's V entries: V(i) stands behind K(i + 1) in the ring. Rows seen by no column
           // are cleared, and those seen by some only if they are not finite
@@ -808,7 +861,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           static_assert(C::NS == C::E || C::NS >= 2 * C::E, "previous tiles");
           if (none | part) {
             if (C::NS == C::E && i < nt - 1)
-              ok = ok && t_wait_warp(sfull_x + 8 * (buf ^ 1), (tiles + 1) >> 1, abort_flag);
+              ok = ok && wait_for(sfull_x + 8 * (buf ^ 1), (tiles + 1) >> 1);
             constexpr int KEYS = kTile / C::V_HALVES;    // of an entry
             // this warp's share of a row of an entry: 8 lanes an atom, both atoms or its group's
             constexpr int AT = D == 64 || C::GROUPS == 2 ? 1 : 2;
@@ -819,7 +872,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 #pragma unroll 1
             for (int blk = 0; blk < C::BLOCKS; ++blk) {
               const int n = e0 + blk * C::V_HALVES + 32 * quad / KEYS, e = n % C::NS;
-              ok = ok && t_wait_warp(full + 8 * e, n / C::NS, abort_flag);
+              ok = ok && wait_for(full + 8 * e, n / C::NS);
               if (!ok) break;
               uint8_t *v = sm + e * C::ENTRY + in + (32 * quad % KEYS) * 128;
               unsigned clear = none;
@@ -863,11 +916,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         __syncwarp();
         if (lane == 0) t_arrive(pfull(x));
       }
-      ok = ok && t_wait_warp(pvdone_x, tiles - 1, abort_flag);
+      ok = ok && wait_for(pvdone_x, tiles - 1);
       t_fence_after();
       const bool whole = p.whole();
       float *rec = a.parts + (2 * cta + (p.t0 == 0 ? 1 : 0)) * C::RECORD;
-      if (mine < HN) {
+      if (mine < hn) {
         const int c = c0 + mine, k = h0 + mine, tok = p.tok0 + c / a.G;
         const bool bad = any_masked && (w.poison[c >> 5] >> (c & 31) & 1);
         s.dst[k] = c < cols ? (static_cast<long long>(p.n0 + tok) * a.Hq + p.head * a.G + c % a.G) * D
@@ -878,7 +931,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       group_sync(sub);
       if (ok) {
 #pragma unroll 1
-        for (int c = 0; c < HN; c += 16) {
+        for (int c = 0; c < hn; c += 16) {
           float l[16];
           {
             uint32_t r[16];
@@ -889,7 +942,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           }
           if (whole) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) l[e] = l[e] == 0.f ? 0.f : __fdividef(1.f, l[e]);
+            for (int e = 0; e < 16; ++e) l[e] = __fdividef(1.f, l[e]);
           } else if (row == 0) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -925,10 +978,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       }
       if (warp == 4 * x && lane == 0 && !whole && p.t0 == 0) {
         // the CTA of the unit's last tile
-        const long long at = p.start + kStart + p.ntiles - 1;
-        int c = static_cast<int>(at * ctas / W);
-        while (c > 0 && share(W, c, ctas) > at) --c;
-        while (share(W, c + 1, ctas) <= at) ++c;
+        const int c = share_of(W, p.start + kStart + p.ntiles - 1, ctas);
         const Cut cut = {p.n0 + p.tok0, cols, p.head, c - cta + 1};
         a.cuts[cta] = cut;
       }
@@ -942,9 +992,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     while (!gone && line.next(p)) {
       const int cols = p.toks * a.G;
       if (p.ntiles == 0) {                      // padding
+#pragma unroll 1
         for (int i = warp; i < cols; i += C::SOFT) {   // all units' warps share them
           const long long o = (static_cast<long long>(p.n0 + p.tok0 + i / a.G) * a.Hq +
                                p.head * a.G + i % a.G) * D;
+#pragma unroll 1
           for (int d = 2 * lane; d < D; d += 64)
             *reinterpret_cast<uint32_t *>(a.out + o + d) = 0;
         }
@@ -956,14 +1008,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         g += 2 * (p.t1 - p.t0) * C::E;
         continue;
       }
-      // code of its own for every number of chunks: with tests around unused ones the warps
-      // wait for instructions more than for anything else
-      switch (columns<C::GROUPS>(cols) / (16 * C::GROUPS)) {
-        case 1: unit(std::integral_constant<int, 1>()); break;
-        case 2: unit(std::integral_constant<int, 2>()); break;
-        case 3: if (C::HALF >= 48) unit(std::integral_constant<int, C::HALF >= 48 ? 3 : 1>()); break;
-        default: if (C::HALF >= 64) unit(std::integral_constant<int, C::HALF >= 64 ? 4 : 1>());
-      }
+      unit();
       g += 2 * (p.t1 - p.t0) * C::E;
     }
     if ((gone || !ok) && lane == 0) tree_report(a.err, PKV_ERR_TIMEOUT);
