@@ -10,7 +10,9 @@ with ``python -c "import __graft_entry__ as g; g.build()"`` (or
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 
 import torch
@@ -840,6 +842,34 @@ def prefill_attn(q, k, v, block_mask: PrefillBlockMask, scale, out, stream=None)
 
 TREE_MAX = 64
 
+# Each call looks its tensors over in one go (_fits, _fits_i32, _fits_tokens: about 0.3 us a
+# tensor) and only where something does not fit finds out what, and raises, in its _refuse_
+# function (host time of a call with everything told apart first: append 13.9 us, attention
+# 8.3, verification 10.0, move of 48 caches 41.2).
+
+
+def _fits(t, dtype, shape, dev) -> bool:
+    return (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == dev)
+
+
+def _fits_i32(t, n, dev) -> bool:
+    return (t.dtype is _I32 and t.numel() >= n and t.is_contiguous()
+            and t.get_device() == dev)
+
+
+def _fits_tokens(t, heads, D, dev) -> bool:
+    """bf16 [N][heads][D], the rows possibly apart."""
+    return (t.dtype is _BF16 and t.shape[1:] == (heads, D) and t.stride()[1:] == (D, 1)
+            and t.get_device() == dev)
+
+
+def _stream_on(stream, dev) -> int | None:
+    """_stream of a call whose tensors are on the current device `dev`."""
+    if stream is None and dev >= 0 and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
+
 
 def _is_tensor(name, **tensors) -> None:
     """Refuses what is no tensor (missing ones too)."""
@@ -899,6 +929,51 @@ def tree_qkv_norm_rope_append(q, k, v, gamma_q, gamma_k, batch_idx, ctx_lens, ro
     drafted tokens (row_start int32 [B + 1], parents int32 [N]); q, k and v are
     bf16 [N][heads][D], rows of any stride, and only read; the rotated q goes to
     q_out. v None: the value is the raw k. rotary_dims None: all of D."""
+    try:
+        N, Hq, D = q.shape
+        Hkv = k_cache.shape[0]
+        rows = (Hkv, n_pages * page_size, D)
+        dev = _raw_device() if q.is_cuda else None
+        B = row_start.numel() - 1
+        fits = (_fits_tokens(q, Hq, D, dev) and _fits_tokens(k, Hkv, D, dev)
+                and (v is None or (_fits_tokens(v, Hkv, D, dev) and v.shape[0] == N))
+                and k.shape[0] == N and N > 1
+                and _fits(k_cache, _BF16, rows, dev) and _fits(v_cache, _BF16, rows, dev)
+                and _fits(q_out, _BF16, (N, Hq, D), dev)
+                and (gamma_q is None or _fits(gamma_q, _BF16, (D,), dev))
+                and (gamma_k is None or _fits(gamma_k, _BF16, (D,), dev))
+                and (batch_idx is None or _fits_i32(batch_idx, B, dev))
+                and _fits_i32(ctx_lens, B, dev) and _fits_i32(row_start, 1, dev)
+                and _fits_i32(parents, N, dev)
+                and _fits_i32(dev_table, n_slots * max_pages_per_seq, dev)
+                and (err_word is None or _fits_i32(err_word, 1, dev)))
+    except (AttributeError, TypeError, ValueError, IndexError):
+        fits = False
+    if fits:
+        sq, sk, sv = q.stride()[0], k.stride()[0], 0 if v is None else v.stride()[0]
+    else:
+        B, N, Hq, Hkv, D, sq, sk, sv, dev = _refuse_append(
+            q, k, v, gamma_q, gamma_k, batch_idx, ctx_lens, row_start, parents, dev_table, n_slots,
+            max_pages_per_seq, page_size, n_pages, k_cache, v_cache, q_out, err_word)
+    lib = load_library()
+    status = lib.tree_qkv_norm_rope_append(
+        q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(), sq, sk, sv,
+        None if gamma_q is None else gamma_q.data_ptr(),
+        None if gamma_k is None else gamma_k.data_ptr(),
+        None if batch_idx is None else batch_idx.data_ptr(), ctx_lens.data_ptr(),
+        row_start.data_ptr(), parents.data_ptr(), float(theta), float(eps),
+        D if rotary_dims is None else int(rotary_dims), 1 if v_norm else 0, B, N, Hq, Hkv, D,
+        dev_table.data_ptr(), n_slots, max_pages_per_seq, page_size, n_pages, k_cache.data_ptr(),
+        v_cache.data_ptr(), q_out.data_ptr(), None if err_word is None else err_word.data_ptr(),
+        _stream_on(stream, dev))
+    if status:
+        _check(status, "tree_qkv_norm_rope_append")
+
+
+def _refuse_append(q, k, v, gamma_q, gamma_k, batch_idx, ctx_lens, row_start, parents, dev_table,
+                   n_slots, max_pages_per_seq, page_size, n_pages, k_cache, v_cache, q_out,
+                   err_word):
+    """What is wrong with an append's tensors; their sizes where nothing is."""
     name = "tree_qkv_norm_rope_append"
     Hkv, D = _tree_cache(name, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq, page_size,
                          n_pages)
@@ -919,13 +994,7 @@ def tree_qkv_norm_rope_append(q, k, v, gamma_q, gamma_k, batch_idx, ctx_lens, ro
     _word(err_word)
     _on_device(q, k, v, gamma_q, gamma_k, batch_idx, ctx_lens, row_start, parents, dev_table,
                k_cache, v_cache, q_out, err_word)
-    _check(load_library().tree_qkv_norm_rope_append(
-        q.data_ptr(), k.data_ptr(), _ptr(v), sq, sk, sv, _ptr(gamma_q), _ptr(gamma_k),
-        _ptr(batch_idx), ctx_lens.data_ptr(), row_start.data_ptr(), parents.data_ptr(),
-        float(theta), float(eps), D if rotary_dims is None else int(rotary_dims),
-        int(bool(v_norm)), B, N, Hq, Hkv, D, dev_table.data_ptr(), n_slots, max_pages_per_seq,
-        page_size, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), q_out.data_ptr(),
-        _ptr(err_word), _stream(stream)), name)
+    return B, N, Hq, Hkv, D, sq, sk, sv, q.get_device()
 
 
 def paged_tree_attn_workspace(Hq, Hkv, D) -> int:
@@ -939,6 +1008,41 @@ def paged_tree_attn(q, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq, 
     paged cache: a node sees the context and its own path. q, out: bf16
     [N][Hq][D]; workspace: a byte tensor of paged_tree_attn_workspace(Hq, Hkv,
     D)."""
+    try:
+        N, Hq, D = q.shape
+        Hkv = k_cache.shape[0]
+        rows = (Hkv, n_pages * page_size, D)
+        dev = _raw_device() if q.is_cuda else None
+        B = row_start.numel() - 1
+        fits = (_fits(q, _BF16, (N, Hq, D), dev) and _fits(out, _BF16, (N, Hq, D), dev)
+                and _fits(k_cache, _BF16, rows, dev) and _fits(v_cache, _BF16, rows, dev)
+                and (batch_idx is None or _fits_i32(batch_idx, B, dev))
+                and _fits_i32(ctx_lens, B, dev) and _fits_i32(row_start, 1, dev)
+                and _fits_i32(parents, N, dev)
+                and _fits_i32(dev_table, n_slots * max_pages_per_seq, dev)
+                and workspace.is_contiguous() and workspace.get_device() == dev
+                and (err_word is None or _fits_i32(err_word, 1, dev)))
+    except (AttributeError, TypeError, ValueError):
+        fits = False
+    if not fits:
+        B, N, Hq, Hkv, D, dev = _refuse_attn(
+            q, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq, page_size, n_pages,
+            batch_idx, ctx_lens, row_start, parents, workspace, out, err_word)
+    lib = load_library()
+    status = lib.paged_tree_attn(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), dev_table.data_ptr(), n_slots,
+        max_pages_per_seq, page_size, n_pages,
+        None if batch_idx is None else batch_idx.data_ptr(), ctx_lens.data_ptr(),
+        row_start.data_ptr(), parents.data_ptr(), int(window), float(scale), B, N, Hq, Hkv, D,
+        workspace.data_ptr(), workspace.nbytes, out.data_ptr(),
+        None if err_word is None else err_word.data_ptr(), _stream_on(stream, dev))
+    if status:
+        _check(status, "paged_tree_attn")
+
+
+def _refuse_attn(q, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq, page_size, n_pages,
+                 batch_idx, ctx_lens, row_start, parents, workspace, out, err_word):
+    """What is wrong with an attention's tensors; their sizes where nothing is."""
     name = "paged_tree_attn"
     Hkv, D = _tree_cache(name, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq, page_size,
                          n_pages)
@@ -954,12 +1058,7 @@ def paged_tree_attn(q, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq, 
     _word(err_word)
     _on_device(q, k_cache, v_cache, dev_table, batch_idx, ctx_lens, row_start, parents, workspace,
                out, err_word)
-    _check(load_library().paged_tree_attn(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), dev_table.data_ptr(), n_slots,
-        max_pages_per_seq, page_size, n_pages, _ptr(batch_idx), ctx_lens.data_ptr(),
-        row_start.data_ptr(), parents.data_ptr(), int(window), float(scale), B, N, Hq, Hkv, D,
-        workspace.data_ptr(), workspace.nbytes, out.data_ptr(), _ptr(err_word), _stream(stream)),
-        name)
+    return B, N, Hq, Hkv, D, q.get_device()
 
 
 def _probs(name, what, t, N, V=None) -> int:
@@ -980,6 +1079,48 @@ def tree_verify(target_probs, draft_probs, tokens, row_start, parents, u_accept,
     chance); tokens int32 [N]; u_accept fp32 [N], u_pick fp32 [B]. Writes accepted
     int32 [B], path int32 [B][cols] (node 0 and the accepted drafts, then -1) and
     next_token int32 [B]."""
+    try:
+        N, B, V = tokens.numel(), row_start.numel() - 1, target_probs.shape[1]
+        dev = _raw_device() if tokens.is_cuda else None
+        sp, one = target_probs.stride()
+        fits = (target_probs.dtype is _F32 and one == 1 and target_probs.shape[0] >= N > 1
+                and target_probs.get_device() == dev
+                and _fits_i32(tokens, N, dev) and _fits_i32(row_start, 1, dev)
+                and _fits_i32(parents, N, dev) and _fits_i32(accepted, B, dev)
+                and _fits_i32(next_token, B, dev)
+                and u_accept.dtype is _F32 and u_accept.numel() >= N and u_accept.is_contiguous()
+                and u_accept.get_device() == dev
+                and u_pick.dtype is _F32 and u_pick.numel() >= B and u_pick.is_contiguous()
+                and u_pick.get_device() == dev
+                and (err_word is None or _fits_i32(err_word, 1, dev)))
+        cols = path.shape[1]
+        fits = fits and path.shape[0] >= B and cols > 0 and _fits_i32(path, 1, dev)
+        sq = 0
+        if draft_probs is not None:
+            sq, one = draft_probs.stride()
+            fits = (fits and draft_probs.dtype is _F32 and one == 1
+                    and draft_probs.shape[0] >= N and draft_probs.shape[1] == V
+                    and draft_probs.get_device() == dev)
+    except (AttributeError, TypeError, ValueError, IndexError):
+        fits = False
+    if not fits:
+        B, N, V, cols, sp, sq, dev = _refuse_verify(
+            target_probs, draft_probs, tokens, row_start, parents, u_accept, u_pick, accepted, path,
+            next_token, err_word)
+    lib = load_library()
+    status = lib.tree_verify(
+        target_probs.data_ptr(), sp, None if draft_probs is None else draft_probs.data_ptr(), sq,
+        tokens.data_ptr(), row_start.data_ptr(), parents.data_ptr(), u_accept.data_ptr(),
+        u_pick.data_ptr(), B, N, V, cols, accepted.data_ptr(), path.data_ptr(),
+        next_token.data_ptr(), None if err_word is None else err_word.data_ptr(),
+        _stream_on(stream, dev))
+    if status:
+        _check(status, "tree_verify")
+
+
+def _refuse_verify(target_probs, draft_probs, tokens, row_start, parents, u_accept, u_pick,
+                   accepted, path, next_token, err_word):
+    """What is wrong with a verification's tensors; their sizes where nothing is."""
     name = "tree_verify"
     _is_tensor(name, tokens=tokens)
     N = tokens.numel()
@@ -1001,11 +1142,7 @@ def tree_verify(target_probs, draft_probs, tokens, row_start, parents, u_accept,
     _word(err_word)
     _on_device(target_probs, draft_probs, tokens, row_start, parents, u_accept, u_pick, accepted,
                path, next_token, err_word)
-    _check(load_library().tree_verify(
-        target_probs.data_ptr(), sp, _ptr(draft_probs), sq, tokens.data_ptr(),
-        row_start.data_ptr(), parents.data_ptr(), u_accept.data_ptr(), u_pick.data_ptr(), B, N, V,
-        path.shape[1], accepted.data_ptr(), path.data_ptr(), next_token.data_ptr(),
-        _ptr(err_word), _stream(stream)), name)
+    return B, N, V, path.shape[1], sp, sq, tokens.get_device()
 
 
 def kv_keep_path(caches, dev_table, n_slots, max_pages_per_seq, page_size, n_pages, batch_idx,
@@ -1014,6 +1151,51 @@ def kv_keep_path(caches, dev_table, n_slots, max_pages_per_seq, page_size, n_pag
     context, in every head of every cache in `caches` (contiguous device tensors
     [heads][n_pages * page_size][...], any element type, all the layers of a
     model)."""
+    try:
+        B, cols = path.shape
+        dev = _raw_device() if path.is_cuda else None
+        fits = (cols > 0 and _fits_i32(path, 1, dev) and _fits_i32(accepted, B, dev)
+                and (batch_idx is None or _fits_i32(batch_idx, B, dev))
+                and _fits_i32(ctx_lens, B, dev)
+                and _fits_i32(dev_table, n_slots * max_pages_per_seq, dev)
+                and (err_word is None or _fits_i32(err_word, 1, dev)))
+        # the caches of a model are alike: each is told from the first by shape and type
+        n, first = len(caches), caches[0]
+        shape, rows = first.shape, n_pages * page_size
+        fits = (fits and shape[1] == rows and shape[0] > 0
+                and list(map(_T.size, caches)) == [shape] * n
+                and list(map(_dtype_of, caches)) == [first.dtype] * n
+                and all(map(_T.is_contiguous, caches))
+                and list(map(_T.get_device, caches)) == [dev] * n
+                and not isinstance(caches, _T))
+    except (AttributeError, TypeError, ValueError, IndexError):
+        fits = False
+    if fits:
+        ptrs = array.array("Q", map(_T.data_ptr, caches))
+        heads = array.array("i", shape[:1]) * n
+        nbytes = array.array("q", (first.nbytes // (shape[0] * rows),)) * n
+    else:
+        B, cols, n, ptrs, heads, nbytes, dev = _refuse_keep(
+            caches, dev_table, n_slots, max_pages_per_seq, page_size, n_pages, batch_idx, ctx_lens,
+            accepted, path, err_word)
+    lib = load_library()
+    status = lib.kv_keep_path(
+        ptrs.buffer_info()[0], heads.buffer_info()[0], nbytes.buffer_info()[0], n,
+        dev_table.data_ptr(), n_slots, max_pages_per_seq, page_size, n_pages,
+        None if batch_idx is None else batch_idx.data_ptr(), ctx_lens.data_ptr(),
+        accepted.data_ptr(), path.data_ptr(), cols, B,
+        None if err_word is None else err_word.data_ptr(), _stream_on(stream, dev))
+    if status:
+        _check(status, "kv_keep_path")
+
+
+_T = torch.Tensor
+_dtype_of = operator.attrgetter("dtype")
+
+
+def _refuse_keep(caches, dev_table, n_slots, max_pages_per_seq, page_size, n_pages, batch_idx,
+                 ctx_lens, accepted, path, err_word):
+    """What is wrong with a move's tensors; their sizes where nothing is."""
     name = "kv_keep_path"
     _is_tensor(name, dev_table=dev_table, path=path)
     _i32(dev_table, "dev_table"), _i32(path, "path")
@@ -1025,25 +1207,21 @@ def kv_keep_path(caches, dev_table, n_slots, max_pages_per_seq, page_size, n_pag
     if dev_table.numel() < n_slots * max_pages_per_seq:
         raise BadArgError(f"{name}: dev_table must be [n_slots][max_pages_per_seq]")
     rows = n_pages * page_size
+    ptrs, heads, nbytes = array.array("Q"), array.array("i"), array.array("q")
     try:
         if isinstance(caches, torch.Tensor):
             raise TypeError
-        n = len(caches)
-        ptrs, heads, nbytes = (_c_p * n)(), (_c_int * n)(), (ctypes.c_int64 * n)()
-        for i, c in enumerate(caches):
+        for c in caches:
             if not c.is_contiguous() or c.dim() < 2 or c.shape[1] != rows:
                 raise BadArgError(f"{name}: caches must be contiguous tensors [heads][n_pages * "
                                   "page_size][...]")
             h = c.shape[0]
-            ptrs[i], heads[i], nbytes[i] = c.data_ptr(), h, c.nbytes // max(h * rows, 1)
+            ptrs.append(c.data_ptr()), heads.append(h), nbytes.append(c.nbytes // max(h * rows, 1))
     except (AttributeError, TypeError):
         raise BadArgError(f"{name}: caches must be a list of tensors") from None
     _word(err_word)
     _on_device(dev_table, batch_idx, ctx_lens, accepted, path, err_word, *caches)
-    _check(load_library().kv_keep_path(
-        ptrs, heads, nbytes, n, dev_table.data_ptr(), n_slots, max_pages_per_seq, page_size,
-        n_pages, _ptr(batch_idx), ctx_lens.data_ptr(), accepted.data_ptr(), path.data_ptr(),
-        path.shape[1], B, _ptr(err_word), _stream(stream)), name)
+    return B, path.shape[1], len(ptrs), ptrs, heads, nbytes, path.get_device()
 
 
 def pkv_read_error_word(err_word, stream=None) -> int:

@@ -224,12 +224,20 @@ extern "C" int tree_qkv_norm_rope_append(
   if (q_stride % 8 || k_stride % 8 || v_stride % 8 || q_stride < 0 || k_stride < 0 ||
       v_stride < 0 || q_stride > most || k_stride > most || v_stride > most)
     return pkv::fail(PKV_E_BAD_ARG, "%s: token strides must be multiples of 8 elements", fn);
-  Turns t;
-  for (int i = 0; i < D / 2; ++i) {
-    double f = i < rotary_dims / 2 ? pow(static_cast<double>(theta), -2.0 * i / D) / (2.0 * M_PI)
-                                   : 0.0;
-    f -= floor(f);
-    t.f[i] = f >= 1.0 ? 0 : static_cast<uint64_t>(ldexp(f, 64));
+  // the table of the thread's last theta, D and rotary_dims (2 us of powers; a model's layers
+  // have one or two of them)
+  static thread_local Turns t;
+  static thread_local float t_theta = 0.f;
+  static thread_local int t_D = 0, t_rotary = -1;
+  if (theta != t_theta || D != t_D || rotary_dims != t_rotary) {
+    for (int i = 0; i < D / 2; ++i) {
+      double f = i < rotary_dims / 2
+                     ? pow(static_cast<double>(theta), -2.0 * i / D) / (2.0 * M_PI)
+                     : 0.0;
+      f -= floor(f);
+      t.f[i] = f >= 1.0 ? 0 : static_cast<uint64_t>(ldexp(f, 64));
+    }
+    t_theta = theta, t_D = D, t_rotary = rotary_dims;
   }
   const AppendArgs a = {reinterpret_cast<const __nv_bfloat16 *>(q),
                         reinterpret_cast<const __nv_bfloat16 *>(k),
