@@ -651,8 +651,9 @@ size_t paged_tree_attn_workspace(int Hq, int Hkv, int D);
  * accepted (int32 [B]) receives the number of accepted drafts, path (int32 [B]
  * [path_cols]) node 0 and theirs in order, then -1, next_token (int32 [B]) the
  * token. Probabilities: in [0, 1], a row summing to 1 but for rounding (other
- * values count as the nearest, NaN as 0; a sum of 4096 or more gives an
- * unspecified token); u in [0, 1). Sums are exact to 2^-52 a term. An empty or
+ * values count as the nearest, NaN as 0; a sum of 2^18 or more gives an
+ * unspecified token); u in [0, 1). In the sums each term is rounded to a whole
+ * multiple of 2^-43, so results depend on no order of summation. An empty or
  * reported row gives 0, -1s and -1; path_cols must hold every row's nodes
  * (PKV_ERR_TREE). A token outside [0, V) is never accepted, and a p without any
  * probability gives -1 (PKV_ERR_PROB). V <= 2^22. */

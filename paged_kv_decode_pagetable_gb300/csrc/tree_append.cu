@@ -23,8 +23,10 @@
 
 namespace {
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 384;
 constexpr int kMaxD = 512;
+constexpr int kEach = 4;      // nodes of a CTA where there are more than a few an SM
+constexpr int kAlone = 2;     // up to so many nodes an SM are CTAs of their own
 
 struct Turns {
   uint64_t f[kMaxD / 2];
@@ -58,123 +60,133 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One CTA a node; D / 16 lanes a head, each with 8 rotation pairs (two 16-byte words).
-template <int D>
-__global__ void __launch_bounds__(kMaxThreads)
-    tree_append_kernel(const AppendArgs a, const __grid_constant__ Turns turns) {
+// EACH nodes a CTA; D / 16 lanes a head, each with 8 rotation pairs (two 16-byte words) of every
+// node. A warp a node finds its row, pages and depth while the nodes' q, k and v are on their way.
+template <int D, int EACH>
+__global__ void __launch_bounds__(kMaxThreads, 2)
+    tree_append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Turns turns) {
   constexpr int LANES = D / 16;
-  __shared__ int s_par[kTreeMax];
-  __shared__ float2 s_rot[D / 2];
-  __shared__ int s_row;
+  __shared__ int s_par[EACH][kTreeMax];
+  __shared__ float2 s_rot[EACH][D / 2];
+  __shared__ int s_pos[EACH];           // rotation position, -1: no node of a row
+  __shared__ long long s_row[EACH];     // cache row, -1: none
   pkv_wait_prior_grid();
   pkv_allow_next_grid();
-  const int node = blockIdx.x, tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int node0 = blockIdx.x * EACH;
   const int heads = a.Hq + 2 * a.Hkv;
   const int part = tid % LANES;
-  auto source = [&](int h) -> const __nv_bfloat16 * {
-    const long long n = node;
-    if (h < a.Hq) return a.q + n * a.sq + h * D;
-    if (h < a.Hq + a.Hkv) return a.k + n * a.sk + (h - a.Hq) * D;
-    return a.v + n * a.sv + (h - a.Hq - a.Hkv) * D;
+  auto load = [&](int n, int h, uint4 &lo, uint4 &hi) {
+    const __nv_bfloat16 *x = h < a.Hq             ? a.q + n * a.sq + h * D
+                             : h < a.Hq + a.Hkv ? a.k + n * a.sk + (h - a.Hq) * D
+                                                : a.v + n * a.sv + (h - a.Hq - a.Hkv) * D;
+    lo = *reinterpret_cast<const uint4 *>(x + 8 * part);
+    hi = *reinterpret_cast<const uint4 *>(x + D / 2 + 8 * part);
   };
-  // the first head's values are on their way while the row is looked up
   int h = tid / LANES;
-  uint4 lo4 = make_uint4(0, 0, 0, 0), hi4 = lo4;
-  if (h < heads) {
-    const __nv_bfloat16 *x = source(h);
-    lo4 = *reinterpret_cast<const uint4 *>(x + 8 * part);
-    hi4 = *reinterpret_cast<const uint4 *>(x + D / 2 + 8 * part);
+  uint4 lo4[EACH], hi4[EACH];
+#pragma unroll
+  for (int j = 0; j < EACH; ++j) {
+    lo4[j] = hi4[j] = make_uint4(0, 0, 0, 0);
+    if (h < heads && node0 + j < a.N) load(node0 + j, h, lo4[j], hi4[j]);
   }
-  // the node's row: the last that starts at or before it
-  int before = 0;
-  for (int i0 = 0; i0 <= a.B; i0 += blockDim.x)
-    before += __syncthreads_count(i0 + tid <= a.B && a.row_start[i0 + tid] <= node);
-  const int b = before - 1;
-  if (b < 0 || b >= a.B) return;   // a node of no row
-  const TreeRow r = tree_row(b, a.N, a.row_start, a.batch_idx, a.ctx_lens, a.n_slots, a.max_pages,
-                             a.page_size);
-  const int i = node - r.n0;
-  if (r.bits || i < 0 || i >= r.n) {
-    if (tid == 0) tree_report(a.err, r.bits);
-    return;
+  for (int j = warp; j < EACH; j += blockDim.x / 32) {
+    const int node = node0 + j;
+    int before = 0;   // the node's row: the last that starts at or before it
+    for (int i = lane; i <= a.B; i += 32) before += a.row_start[i] <= node;
+    const int b = __reduce_add_sync(0xffffffffu, before) - 1;
+    int bits = 0, pos = -1;
+    long long to = -1;
+    if (node < a.N && b >= 0 && b < a.B) {   // (others are nodes of no row)
+      const TreeRow r = tree_row(b, a.N, a.row_start, a.batch_idx, a.ctx_lens, a.n_slots,
+                                 a.max_pages, a.page_size);
+      const int i = node - r.n0;
+      bits = r.bits;
+      if (!r.bits && i >= 0 && i < r.n) {
+        const int at = r.ctx + i;
+        const int page = a.table[static_cast<long long>(r.slot) * a.max_pages + at / a.page_size];
+        for (int t = lane; t <= i; t += 32) s_par[j][t] = tree_parent(a.parents, r.n0, t, bits);
+        __syncwarp();
+        pos = r.ctx;
+        for (int t = s_par[j][i]; t >= 0; t = s_par[j][t]) ++pos;
+        if (page < 0) bits |= PKV_ERR_PAGE_NEG;
+        else if (page >= a.n_pages) bits |= PKV_ERR_PAGE_RANGE;
+        else to = static_cast<long long>(page) * a.page_size + at % a.page_size;
+      }
+    }
+    tree_report(a.err, bits);
+    if (lane == 0) {
+      s_pos[j] = pos;
+      s_row[j] = to;
+    }
   }
-  const int at = r.ctx + i;
-  int page = -1, bits = 0;
-  if (tid == 0) {
-    page = a.table[static_cast<long long>(r.slot) * a.max_pages + at / a.page_size];
-    if (page < 0) bits = PKV_ERR_PAGE_NEG;
-    else if (page >= a.n_pages) bits = PKV_ERR_PAGE_RANGE;
-    s_row = bits ? -1 : page;
-  }
-  int pbits = 0;
-  for (int t = tid; t <= i; t += blockDim.x) s_par[t] = tree_parent(a.parents, r.n0, t, pbits);
-  tree_report(a.err, bits | pbits);
   __syncthreads();
-  int depth = 0;
-  for (int t = s_par[i]; t >= 0; t = s_par[t]) ++depth;
-  const uint64_t pos = static_cast<uint64_t>(r.ctx + depth);
-  for (int t = tid; t < D / 2; t += blockDim.x) {
+  for (int t = tid; t < EACH * (D / 2); t += blockDim.x) {
+    const int j = t / (D / 2), i = t % (D / 2);
     // the nearest half turn's fraction, in units of half a turn
-    const int32_t frac = static_cast<int32_t>((pos * turns.f[t]) >> 32);
+    const int32_t frac =
+        static_cast<int32_t>((static_cast<uint64_t>(s_pos[j]) * turns.f[i]) >> 32);
     float sn, cs;
     sincospif(static_cast<float>(frac) * 0x1p-31f, &sn, &cs);
-    s_rot[t] = make_float2(cs, sn);
+    s_rot[j][i] = make_float2(cs, sn);
   }
   __syncthreads();
-  page = s_row;
-  const long long row = static_cast<long long>(page) * a.page_size + at % a.page_size;
   const long long head_rows = static_cast<long long>(a.n_pages) * a.page_size;
   // (whole warps go round together: the lanes of a head reduce with shuffles)
   for (int h0 = 0; h0 < heads; h0 += blockDim.x / LANES, h += blockDim.x / LANES) {
-    if (h0 > 0 && h < heads) {
-      const __nv_bfloat16 *x = source(h);
-      lo4 = *reinterpret_cast<const uint4 *>(x + 8 * part);
-      hi4 = *reinterpret_cast<const uint4 *>(x + D / 2 + 8 * part);
-    }
     const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
     const __nv_bfloat16 *g = is_q ? a.gq : is_v ? nullptr : a.gk;
     const bool norm = is_v ? a.v_norm != 0 : g != nullptr;
-    float lo[8], hi[8];
-    unpack8(lo4, lo);
-    unpack8(hi4, hi);
-    float ss = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(lo[e], lo[e], fmaf(hi[e], hi[e], ss));
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (h >= heads) continue;
-    if (norm) {
-      const float inv = rsqrtf(ss / D + a.eps);
-      float gl[8], gh[8];
-      if (g) {
-        unpack8(*reinterpret_cast<const uint4 *>(g + 8 * part), gl);
-        unpack8(*reinterpret_cast<const uint4 *>(g + D / 2 + 8 * part), gh);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        lo[e] *= g ? inv * gl[e] : inv;
-        hi[e] *= g ? inv * gh[e] : inv;
-      }
+    uint4 gl4 = make_uint4(0, 0, 0, 0), gh4 = gl4;
+    if (g) {
+      gl4 = *reinterpret_cast<const uint4 *>(g + 8 * part);
+      gh4 = *reinterpret_cast<const uint4 *>(g + D / 2 + 8 * part);
     }
-    if (!is_v) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 w = s_rot[8 * part + e];
-        const float x1 = lo[e], x2 = hi[e];
-        lo[e] = x1 * w.x - x2 * w.y;
-        hi[e] = x2 * w.x + x1 * w.y;
+    for (int j = 0; j < EACH; ++j) {
+      const int pos = s_pos[j];
+      if (pos < 0) continue;
+      if (h0 > 0 && h < heads) load(node0 + j, h, lo4[j], hi4[j]);
+      float lo[8], hi[8];
+      unpack8(lo4[j], lo);
+      unpack8(hi4[j], hi);
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(lo[e], lo[e], fmaf(hi[e], hi[e], ss));
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (h >= heads) continue;
+      if (norm) {
+        const float inv = rsqrtf(ss / D + a.eps);
+        float gl[8], gh[8];
+        unpack8(gl4, gl);
+        unpack8(gh4, gh);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          lo[e] *= g ? inv * gl[e] : inv;
+          hi[e] *= g ? inv * gh[e] : inv;
+        }
       }
+      if (!is_v) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 w = s_rot[j][8 * part + e];
+          const float x1 = lo[e], x2 = hi[e];
+          lo[e] = x1 * w.x - x2 * w.y;
+          hi[e] = x2 * w.x + x1 * w.y;
+        }
+      }
+      __nv_bfloat16 *to;
+      if (is_q) {
+        to = a.q_out + (static_cast<long long>(node0 + j) * a.Hq + h) * D;
+      } else {
+        if (s_row[j] < 0) continue;
+        const int hk = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
+        to = (is_v ? a.v_cache : a.k_cache) + (hk * head_rows + s_row[j]) * D;
+      }
+      *reinterpret_cast<uint4 *>(to + 8 * part) = pack8(lo);
+      *reinterpret_cast<uint4 *>(to + D / 2 + 8 * part) = pack8(hi);
     }
-    __nv_bfloat16 *to;
-    if (is_q) {
-      to = a.q_out + (static_cast<long long>(node) * a.Hq + h) * D;
-    } else {
-      if (page < 0) continue;
-      const int hk = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
-      to = (is_v ? a.v_cache : a.k_cache) + (hk * head_rows + row) * D;
-    }
-    *reinterpret_cast<uint4 *>(to + 8 * part) = pack8(lo);
-    *reinterpret_cast<uint4 *>(to + D / 2 + 8 * part) = pack8(hi);
   }
 }
 
@@ -182,7 +194,10 @@ template <int D>
 cudaError_t launch(const AppendArgs &a, const Turns &t, cudaStream_t s) {
   const int want = (a.Hq + 2 * a.Hkv) * (D / 16);
   const int threads = want >= kMaxThreads ? kMaxThreads : (want + 31) / 32 * 32;
-  return pkv::launch_pdl(tree_append_kernel<D>, dim3(a.N), dim3(threads), 0, s, a, t);
+  if (a.N <= kAlone * pkv::sm_count())
+    return pkv::launch_pdl(tree_append_kernel<D, 1>, dim3(a.N), dim3(threads), 0, s, a, t);
+  return pkv::launch_pdl(tree_append_kernel<D, kEach>, dim3((a.N + kEach - 1) / kEach),
+                         dim3(threads), 0, s, a, t);
 }
 
 }  // namespace

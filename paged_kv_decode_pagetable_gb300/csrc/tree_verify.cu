@@ -11,14 +11,15 @@
 // The scheme keeps the target's distribution if a node's children are independent samples of q
 // (or, without q, any tokens that p does not depend on).
 //
-// Sums are kept in fixed point, 2^-52 a unit in 64 bits: exact (each term cut off once, below
-// what fp32 probabilities resolve), so they do not depend on how the vocabulary is divided, and
-// the row's CTAs, which all do the same walk, cannot disagree on a decision.
+// Sums are kept in fixed point, in units of 2^-43: each probability is rounded to one once (fp32
+// ones below 2^-20 lose up to 2^-44, far below what moves a threshold past a token), the sums
+// are whole numbers. So they do not depend on how the vocabulary is divided, and the row's CTAs,
+// which all do the same walk, cannot disagree on a decision.
 //
 // Bound by reading the last node's row of p (and of q where something was refused) once: a pass
 // over a row is one of the target's V words. A cluster of up to 8 CTAs shares a row: each sums
 // a contiguous part, the sums cross through distributed shared memory, and the warp whose part
-// holds the threshold reads it again for the token.
+// holds the threshold reads the group of words with it again for the token.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -34,7 +35,10 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kUnit = 128;      // words a warp reads at a time: four a lane
 constexpr int kDeep = 4;        // such reads in flight
-constexpr uint64_t kMaxA = uint64_t(127) << 52;   // a stays below 2^7 (64 refusals of 1)
+constexpr int kGroups = 32;     // sums that a warp keeps of its part
+constexpr int kBits = 43;       // sums are in units of 2^-43
+constexpr double kUnitSize = 1.0 / (1ull << kBits);
+constexpr uint64_t kMaxA = uint64_t(127) << kBits;   // a stays below 2^7 (64 refusals of 1)
 
 struct VerifyArgs {
   const float *p, *q;
@@ -46,26 +50,65 @@ struct VerifyArgs {
 };
 
 // probabilities outside [0, 1] and NaN count as the nearest of the two ends (NaN as 0)
-__device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
+__device__ __forceinline__ float clean(float x) { return __saturatef(x); }
 
-// x in [0, 1] in units of 2^-52, cut off: the significand shifted by the exponent
-__device__ __forceinline__ uint64_t fixed(float x) {
-  const uint32_t b = __float_as_uint(clean(x));
-  const int sh = static_cast<int>(b >> 23) - 98;   // 2^(e - 150) 2^52
-  const uint32_t m = (b & 0x7fffffu) | 0x800000u;
-  return sh >= 0 ? static_cast<uint64_t>(m) << sh : m >> min(-sh, 31);
+// x in [0, 1] in units of 2^-43, to the nearest, in two steps of fp32: added to 12, whose last
+// place is 2^-20, x leaves its rounding to that in the sum's last bits; what remains, exact, is
+// scaled and added to 1.5 * 2^23, whose last place is 1. hi and lo take the sums' bits, each
+// kHi0 or kLo0 too large.
+constexpr int kHi0 = 0x41400000, kLo0 = 0x4b400000;
+__device__ __forceinline__ void fixed(float x, int &hi, int &lo) {
+  const float y = __fadd_rn(x, 12.f);
+  const float rest = __fsub_rn(x, __fsub_rn(y, 12.f));
+  hi = __float_as_int(y);
+  lo = __float_as_int(__fmaf_rn(rest, 0x1p43f, 0x1.8p23f));
+}
+__device__ __forceinline__ int64_t fixed(float x) {
+  int hi, lo;
+  fixed(x, hi, lo);
+  return (static_cast<int64_t>(hi - kHi0) << 23) + (lo - kLo0);
 }
 
-// w of one token: p - a q, none below 0. a in units of 2^-52; exact below 2^-52
-template <bool RES>
-__device__ __forceinline__ uint64_t weight(float p, float q, uint64_t a, bool one) {
-  uint64_t w = fixed(p);
-  if (RES) {
-    uint64_t f = fixed(q);
-    if (!one) f = __umul64hi(f << 7, a << 5);
-    w = w > f ? w - f : 0;
+// How a pass weighs a token: p itself, p - q (a = 1, the first refusal), or p - a q; none below 0.
+enum { kPlain = 0, kFirst = 1, kLater = 2 };
+template <int KIND>
+__device__ __forceinline__ uint64_t weight(float p, float q, uint64_t a) {
+  p = clean(p), q = clean(q);
+  if (KIND == kPlain) return fixed(p);
+  if (KIND == kFirst) return p > q ? fixed(p) - fixed(q) : 0;
+  const uint64_t w = fixed(p), f = __umul64hi(static_cast<uint64_t>(fixed(q)) << 14, a << 7);
+  return w > f ? w - f : 0;
+}
+
+// Adds the weights of N tokens to s.
+template <int KIND, int N>
+__device__ __forceinline__ void add_weights(const float (&p)[N], const float (&q)[N], uint64_t a,
+                                            uint64_t &s) {
+  if (KIND == kLater) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s += weight<KIND>(p[i], q[i], a);
+    return;
   }
-  return w;
+  int hi = 0, lo = 0;   // (terms up to 2^20 and 2^23)
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float x = clean(p[i]);
+    int h, l;
+    if (KIND == kFirst) {
+      const float y = clean(q[i]);
+      const bool more = x > y;
+      int h2, l2;
+      fixed(more ? x : 0.f, h, l);
+      fixed(more ? y : 0.f, h2, l2);
+      hi += h - h2;
+      lo += l - l2;
+    } else {
+      fixed(x, h, l);
+      hi += h - kHi0;
+      lo += l - kLo0;
+    }
+  }
+  s += (static_cast<int64_t>(hi) << 23) + lo;
 }
 
 struct Row {
@@ -82,29 +125,6 @@ __device__ __forceinline__ float4 four(const float *row, bool vec, int i, int V)
   if (i + 2 < V) r.z = __ldg(row + i + 2);
   if (i + 3 < V) r.w = __ldg(row + i + 3);
   return r;
-}
-
-// Sum of the weights of units [u0, u1) over the warp (every lane gets its own share).
-template <bool RES>
-__device__ __forceinline__ uint64_t sum_units(const Row &r, uint64_t a, int u0, int u1, int V,
-                                              int lane) {
-  const bool one = a == 1ull << 52;
-  uint64_t s = 0;
-  for (int u = u0; u < u1; u += kDeep) {
-    float4 p[kDeep], q[kDeep];
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      const int i = u + d < u1 ? (u + d) * kUnit + 4 * lane : V;
-      p[d] = four(r.p, r.vec_p, i, V);
-      if (RES) q[d] = four(r.q, r.vec_q, i, V);
-    }
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      s += weight<RES>(p[d].x, q[d].x, a, one) + weight<RES>(p[d].y, q[d].y, a, one) +
-           weight<RES>(p[d].z, q[d].z, a, one) + weight<RES>(p[d].w, q[d].w, a, one);
-    }
-  }
-  return s;
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t s) {
@@ -127,40 +147,96 @@ struct Shared {
   float p[kTreeMax], q[kTreeMax], u[kTreeMax];
   int path[kTreeMax];
   int gone[kTreeMax];              // refused tokens of the current node (drafts without q)
-  uint64_t warp[kWarps];           // sums of this CTA's warps
+  uint64_t group[kWarps][kGroups]; // sums of the groups of units of this CTA's warps
+  uint64_t warp[kWarps];           // and of the warps
   uint64_t rank[2][kMaxCluster];   // sums of the row's CTAs, by turns
   uint64_t a;
-  int node, n_gone, last, n_path, bits;
+  int node, n_gone, last, n_path;
 };
 
-// Whether and where the warp's units hold the threshold, with the refused tokens left out.
-template <bool RES>
+// kDeep units from u on (below u1), all their reads in flight: what this lane has of them
+template <int KIND>
+__device__ __forceinline__ void read_units(const Row &r, int u, int u1, int V, int lane,
+                                           float (&p)[4 * kDeep], float (&q)[4 * kDeep]) {
+#pragma unroll
+  for (int d = 0; d < kDeep; ++d) {
+    const int i = u + d < u1 ? (u + d) * kUnit + 4 * lane : V;
+    const float4 x = four(r.p, r.vec_p, i, V);
+    p[4 * d] = x.x, p[4 * d + 1] = x.y, p[4 * d + 2] = x.z, p[4 * d + 3] = x.w;
+    if (KIND != kPlain) {
+      const float4 y = four(r.q, r.vec_q, i, V);
+      q[4 * d] = y.x, q[4 * d + 1] = y.y, q[4 * d + 2] = y.z, q[4 * d + 3] = y.w;
+    }
+  }
+}
+
+// Sums of the groups of `size` units that units [u0, u1) make up; returns their sum.
+template <int KIND>
+__device__ __forceinline__ uint64_t sum_units(const Row &r, uint64_t a, Shared &sh, int size, int u0,
+                                              int u1, int V, int warp, int lane) {
+  uint64_t total = 0;
+  int g = 0;
+  for (int first = u0; first < u1; first += size, ++g) {
+    const int end = min(u1, first + size);
+    uint64_t s = 0;
+    for (int u = first; u < end; u += kDeep) {
+      float p[4 * kDeep], q[4 * kDeep];
+      read_units<KIND>(r, u, end, V, lane, p, q);
+      add_weights<KIND>(p, q, a, s);
+    }
+    // refused tokens among them
+    for (int k = lane; k < sh.n_gone; k += 32) {
+      const int unit = sh.gone[k] / kUnit;
+      if (unit >= first && unit < end) s -= fixed(clean(r.p[sh.gone[k]]));
+    }
+    s = warp_sum(s);
+    if (lane == 0) sh.group[warp][g] = s;
+    total += s;
+  }
+  if (lane >= g) sh.group[warp][lane] = 0;
+  return total;
+}
+
+// The token on which the threshold t falls, among the warp's units.
+template <int KIND>
 __device__ __forceinline__ int find(const Row &r, uint64_t a, const Shared &sh, uint64_t before,
-                                    uint64_t t, int u0, int u1, int V, int lane) {
-  const bool one = a == 1ull << 52;
-  for (int u = u0; u < u1; ++u) {
-    const int i = u * kUnit + 4 * lane;
-    const float4 p = four(r.p, r.vec_p, i, V);
-    const float4 q = RES ? four(r.q, r.vec_q, i, V) : make_float4(0.f, 0.f, 0.f, 0.f);
-    uint64_t w[4] = {weight<RES>(p.x, q.x, a, one), weight<RES>(p.y, q.y, a, one),
-                     weight<RES>(p.z, q.z, a, one), weight<RES>(p.w, q.w, a, one)};
-    for (int g = 0; g < sh.n_gone; ++g) {
-      const int d = sh.gone[g] - i;
+                                    uint64_t t, int size, int u0, int u1, int V, int warp,
+                                    int lane) {
+  const uint64_t mine = sh.group[warp][lane];
+  const uint64_t start = before + warp_before(mine, lane);
+  const unsigned hit = __ballot_sync(0xffffffffu, t >= start && t < start + mine);
+  if (!hit) return -1;
+  const int g = __ffs(hit) - 1;
+  before = __shfl_sync(0xffffffffu, start, g);
+  const int first = u0 + g * size, end = min(u1, first + size);
+  for (int u = first; u < end; u += kDeep) {
+    float p[4 * kDeep], q[4 * kDeep];
+    read_units<KIND>(r, u, end, V, lane, p, q);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (d == e) w[e] = 0;
-    }
-    const uint64_t mine = w[0] + w[1] + w[2] + w[3];
-    uint64_t c = before + warp_before(mine, lane);
-    int hit = -1;
+    for (int d = 0; d < kDeep; ++d) {
+      const int i = (u + d) * kUnit + 4 * lane;
+      uint64_t w[4], sum = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      c += w[e];
-      if (hit < 0 && c > t) hit = i + e;
+      for (int e = 0; e < 4; ++e) w[e] = weight<KIND>(p[4 * d + e], q[4 * d + e], a);
+      for (int k = 0; k < sh.n_gone; ++k) {
+        const int at = sh.gone[k] - i;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (at == e) w[e] = 0;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum += w[e];
+      uint64_t c = before + warp_before(sum, lane);
+      int here = -1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c += w[e];
+        if (here < 0 && c > t) here = i + e;
+      }
+      const unsigned who = __ballot_sync(0xffffffffu, here >= 0);
+      if (who) return __shfl_sync(0xffffffffu, here, __ffs(who) - 1);
+      before = __shfl_sync(0xffffffffu, c, 31);
     }
-    const unsigned who = __ballot_sync(0xffffffffu, hit >= 0);
-    if (who) return __shfl_sync(0xffffffffu, hit, __ffs(who) - 1);
-    before = __shfl_sync(0xffffffffu, c, 31);
   }
   return -1;
 }
@@ -186,8 +262,6 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyAr
     }
     return;
   }
-  if (tid == 0) sh.bits = 0;
-  __syncthreads();
   if (tid < n) {
     int bits = 0;
     const int t = a.tokens[n0 + tid];
@@ -216,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyAr
   const int units = (a.V + kUnit - 1) / kUnit;
   const int each = (units + ranks * kWarps - 1) / (ranks * kWarps);
   const int u0 = min(units, (rank * kWarps + warp) * each), u1 = min(units, u0 + each);
+  const int size = (each + kGroups * kDeep - 1) / (kGroups * kDeep) * kDeep;   // of a group
 
   // state of the walk (warp 0's, the same in every CTA of the row)
   int cur = 0, i = 1, n_path = 1;
@@ -240,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyAr
         const double u = sh.u[c], p = sh.p[c], q = sh.q[c];
         bool good;
         if (a.q) {
-          const double w = fmax(p - static_cast<double>(a_k) * 0x1p-52 * q, 0.0);
+          const double w = fmax(p - static_cast<double>(a_k) * kUnitSize * q, 0.0);
           good = u * q * s_k < w;
         } else {
           bool twice = false;
@@ -264,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyAr
           n_gone = 0;
         } else if (a.q) {
           // what is left after this refusal
-          const uint64_t s = static_cast<uint64_t>(s_k * 0x1p52);
+          const uint64_t s = static_cast<uint64_t>(s_k * (1ull << kBits));
           a_k = a_k + s < kMaxA ? a_k + s : kMaxA;
           pass = true;
         }
@@ -289,14 +364,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyAr
     r.vec_p = (reinterpret_cast<uintptr_t>(r.p) & 15) == 0;
     r.vec_q = (reinterpret_cast<uintptr_t>(r.q) & 15) == 0;
     const bool last = sh.last;
-    uint64_t s = ak ? sum_units<true>(r, ak, u0, u1, a.V, lane)
-                    : sum_units<false>(r, ak, u0, u1, a.V, lane);
-    // refused tokens in this warp's part
-    for (int g = lane; g < sh.n_gone; g += 32) {
-      const int unit = sh.gone[g] / kUnit;
-      if (unit >= u0 && unit < u1) s -= fixed(r.p[sh.gone[g]]);
-    }
-    s = warp_sum(s);
+    const int kind = ak == 0 ? kPlain : ak == 1ull << kBits ? kFirst : kLater;
+    const uint64_t s =
+        kind == kPlain   ? sum_units<kPlain>(r, ak, sh, size, u0, u1, a.V, warp, lane)
+        : kind == kFirst ? sum_units<kFirst>(r, ak, sh, size, u0, u1, a.V, warp, lane)
+                         : sum_units<kLater>(r, ak, sh, size, u0, u1, a.V, warp, lane);
     if (lane == 0) sh.warp[warp] = s;
     __syncthreads();
     if (warp == 0) {
@@ -310,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyAr
       total += sh.rank[turn & 1][k];
     }
     if (!last) {
-      s_k = static_cast<double>(total) * 0x1p-52;
+      s_k = static_cast<double>(total) * kUnitSize;
       continue;
     }
     if (total == 0 && (ak || sh.n_gone)) {   // nothing left but rounding: the target's own row
@@ -337,8 +409,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyAr
     // this warp's part of the line
     for (int k = 0; k < warp; ++k) before += sh.warp[k];
     if (t >= before && t < before + sh.warp[warp]) {
-      const int tok = ak ? find<true>(r, ak, sh, before, t, u0, u1, a.V, lane)
-                         : find<false>(r, ak, sh, before, t, u0, u1, a.V, lane);
+      const int tok =
+          kind == kPlain   ? find<kPlain>(r, ak, sh, before, t, size, u0, u1, a.V, warp, lane)
+          : kind == kFirst ? find<kFirst>(r, ak, sh, before, t, size, u0, u1, a.V, warp, lane)
+                           : find<kLater>(r, ak, sh, before, t, size, u0, u1, a.V, warp, lane);
       if (lane == 0) a.next[b] = tok;
     }
     return;   // every CTA's words were read before the last cluster barrier, or are its own
