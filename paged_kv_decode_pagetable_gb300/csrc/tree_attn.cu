@@ -220,28 +220,13 @@ struct Part {
   __device__ bool whole() const { return t0 == 0 && t1 == ntiles; }
 };
 
+// Goes through a CTA's share of the line, part by part.
 struct Line {
   const Small *sm;
   const Args *a;
-  int pos, end, b;
-  __device__ void begin(const Small &s, const Args &args, int x0, int x1) {
-    sm = &s;
-    a = &args;
-    pos = x0;
-    end = x1;
-    int l = 0, r = args.B;   // the last row that starts at or before x0
-#pragma unroll 1
-    while (r - l > 1) {
-      const int m = (l + r) / 2;
-      if (s.pre[m] <= x0) l = m;
-      else r = m;
-    }
-    b = l;
-  }
-  __device__ bool next(Part &p) {
-    if (pos >= end) return false;
-#pragma unroll 1
-    while (pos >= sm->pre[b + 1]) ++b;
+  int pos, end, off;   // off: where in its unit pos is
+  Part p;              // the unit at pos (all but t0 and t1)
+  __device__ void row(int b) {
     p.b = b;
     p.n0 = sm->n0[b];
     p.n = sm->n[b] & 127;
@@ -249,18 +234,52 @@ struct Line {
     p.lo = a->window > 0 ? max(0, p.ctx - a->window + 1) : 0;
     p.tile0 = p.lo / kTile;
     p.ntiles = sm->n[b] & 128 ? 0 : (p.ctx + p.n - 1) / kTile - p.tile0 + 1;
-    const int cost = p.ntiles + kStart;
-    const unsigned local = pos - sm->pre[b], u = local / static_cast<unsigned>(cost);
-    const int off = static_cast<int>(local - u * cost);
-    const int units = (p.n + a->unit_tokens - 1) / a->unit_tokens;
-    p.head = static_cast<int>(u) / units;
-    p.tok0 = (static_cast<int>(u) - p.head * units) * a->unit_tokens;
+  }
+  __device__ void begin(const Small &s, const Args &args, int x0, int x1) {
+    sm = &s;
+    a = &args;
+    pos = x0;
+    end = x1;
+    off = 0;
+    if (x0 >= x1) return;
+    int l = 0, r = args.B;   // the last row that starts at or before x0
+#pragma unroll 1
+    while (r - l > 1) {
+      const int m = (l + r) / 2;
+      if (s.pre[m] <= x0) l = m;
+      else r = m;
+    }
+    row(l);
+    const int cost = p.ntiles + kStart, units = (p.n + args.unit_tokens - 1) / args.unit_tokens;
+    const int u = (x0 - s.pre[l]) / cost;
+    off = x0 - s.pre[l] - u * cost;
+    p.head = u / units;
+    p.tok0 = (u - p.head * units) * args.unit_tokens;
+  }
+  // the next part, in p
+  __device__ bool next() {
+    if (pos >= end) return false;
+    if (off == p.ntiles + kStart) {   // behind a unit: the next nodes, head or row with nodes
+      off = 0;
+      p.tok0 += a->unit_tokens;
+      if (p.tok0 >= p.n) {
+        p.tok0 = 0;
+        if (++p.head == a->Hkv) {
+          p.head = 0;
+          int b = p.b + 1;
+#pragma unroll 1
+          while (sm->pre[b + 1] == pos) ++b;
+          row(b);
+        }
+      }
+    }
     p.toks = min(a->unit_tokens, p.n - p.tok0);
-    const int to = min(cost, off + (end - pos));
+    const int to = min(p.ntiles + kStart, off + (end - pos));
     p.t0 = max(0, off - kStart);
     p.t1 = max(0, to - kStart);
     p.start = pos - off;
     pos += to - off;
+    off = to;
     return true;
   }
 };
@@ -339,7 +358,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                  "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  pkv_wait_prior_grid();
   pkv_allow_next_grid();
 
   // the line: places of every row, summed up over the rows
@@ -400,7 +418,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   const int x1 = cta < ctas ? share(W, cta + 1, ctas) : 0;
   Line line;
   line.begin(s, a, x0, x1);
-  Part p;
+  const Part &p = line.p;
+  // (what the prior kernel may write or read - caches, queries, workspace, output - from here on)
+  pkv_wait_prior_grid();
   if (tid == 0) a.cuts[cta].cols = 0;
 
   if (warp == C::PROD) {
@@ -460,7 +480,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         __syncwarp();
       }
     };
-    while (ok && line.next(p)) {
+    while (ok && line.next()) {
       if (p.t0 == p.t1) continue;
       const int32_t *row = a.table + static_cast<long long>(s.slot[p.b]) * a.max_pages;
       const int last_page = (p.ctx + p.n - 1) >> a.log_page;
@@ -543,6 +563,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       ok = ok && wait_for(pfull(x), pv);
       if (first && own >= 1) ok = ok && wait_for(ofree(x), own - 1);
       const uint32_t add = !first;
+      t_fence_after();
+      if (ok && elect_one()) {   // (they need no V, which may be on its way)
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          t_mma(tx + C::L_COL, dOne, dP + k * (2048 >> 4), id, k > 0 ? 1u : add);
+      }
+      __syncwarp();
 #pragma unroll 1
       for (int c = 0; c < C::E && ok; c += BT) {
         take();
@@ -561,16 +588,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             t_commit(empty + 8 * entry[b]);
           }
           if (c + BT == C::E) {
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              t_mma(tx + C::L_COL, dOne, dP + k * (2048 >> 4), id, k > 0 ? 1u : add);
             t_commit(pvdone(x));
           }
         }
         __syncwarp();
       }
     };
-    while (ok && line.next(p)) {
+    while (ok && line.next()) {
       if (p.t0 == p.t1) continue;
       const int seg = segs++;
       if (seg % U != x) {
@@ -626,7 +650,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     // ====================== queries and who sees whom ======================
     int segs = 0, bits = 0;
     const int box = a.box_nodes * a.G * 128;      // bytes of a box: nodes x heads, one atom
-    while (line.next(p)) {
+    while (line.next()) {
       if (p.t0 == p.t1) continue;
       const int x = segs % U;
       if (segs >= U && !wait_for(qempty(x), segs / U - 1)) break;
@@ -878,22 +902,28 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
               unsigned clear = none;
               if (part) {
 #pragma unroll 1
-                for (int r = 0; r < 32; r += STEP) {
-                  if (!((part >> r) & ((1u << STEP) - 1))) continue;
-                  const uint4 y = *reinterpret_cast<const uint4 *>(v + (r + which) * 128);
-                  // 0 times what is finite stays 0
-                  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
-                  __nv_bfloat162 z = zero;
-                  z = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&y.x), zero, z);
-                  z = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&y.y), zero, z);
-                  z = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&y.z), zero, z);
-                  z = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&y.w), zero, z);
-                  const bool bad = __isnan(__low2float(z)) || __isnan(__high2float(z));
-                  const unsigned who = __ballot_sync(0xffffffffu, bad);
+                for (int r0 = 0; r0 < 32; r0 += 4 * STEP) {
+                  if (!(part >> r0 & ((1u << (4 * STEP - 1) << 1) - 1))) continue;
+                  uint4 y[4];
 #pragma unroll
-                  for (int q = 0; q < STEP; ++q)
-                    if ((who >> (8 * AT * q)) & ((1u << (8 * AT - 1) << 1) - 1))
-                      clear |= part & (1u << (r + q));
+                  for (int i = 0; i < 4; ++i)
+                    y[i] = *reinterpret_cast<const uint4 *>(v + (r0 + i * STEP + which) * 128);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    // 0 times what is finite stays 0
+                    const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+                    __nv_bfloat162 z = zero;
+                    z = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&y[i].x), zero, z);
+                    z = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&y[i].y), zero, z);
+                    z = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&y[i].z), zero, z);
+                    z = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&y[i].w), zero, z);
+                    const unsigned who = __ballot_sync(
+                        0xffffffffu, (*reinterpret_cast<const uint32_t *>(&z) & 0x7fff7fffu) != 0);
+#pragma unroll
+                    for (int q = 0; q < STEP; ++q)
+                      if (who >> (8 * AT * q) & ((1u << (8 * AT - 1) << 1) - 1))
+                        clear |= part & (1u << (r0 + i * STEP + q));
+                  }
                 }
               }
               const unsigned poisoned = clear & part;
@@ -902,9 +932,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 atomicOr(&w.poison[1], static_cast<unsigned>((sees & wide) >> 32));
               }
               if (clear) {
-#pragma unroll 1
+                const unsigned mine_of = clear >> which;
+#pragma unroll
                 for (int r = 0; r < 32; r += STEP)
-                  if (clear >> (r + which) & 1)
+                  if (mine_of >> r & 1)
                     *reinterpret_cast<uint4 *>(v + (r + which) * 128) = make_uint4(0, 0, 0, 0);
               }
               __syncwarp();
@@ -989,7 +1020,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         t_arrive(prepempty + 8 * (seg & 1));
       }
     };
-    while (!gone && line.next(p)) {
+    while (!gone && line.next()) {
       const int cols = p.toks * a.G;
       if (p.ntiles == 0) {                      // padding
 #pragma unroll 1
