@@ -51,7 +51,7 @@ constexpr int kMaxCtas = 160;            // CTAs the workspace has room for
 constexpr float kLazyLog2 = 8.f;
 constexpr int kMostPlaces = 0x7fffffff;  // as many and more are reported, not computed
 constexpr float kUnset = 1e30f;          // stands for -reference of a column without one
-constexpr int kJoinCols = 8;             // columns of a joining CTA
+constexpr int kJoinWarps = 8;            // of a joining CTA
 
 template <int D>
 struct Cfg {
@@ -1052,60 +1052,81 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                  "r"(512));
 }
 
-// Joins the parts of the unit that CTA blockIdx.x began and others went on with: a warp a column.
+// Joins the parts of the unit that CTA blockIdx.x began and others went on with: a warp a
+// column, the reads of a few parts in flight with those of their weights.
 template <int D>
-__global__ void __launch_bounds__(kJoinCols * 32)
+__global__ void __launch_bounds__(kJoinWarps * 32)
     tree_join_kernel(const float *parts, const Cut *cuts, __nv_bfloat16 *out, int Hq, int G) {
   using C = Cfg<D>;
   pkv_wait_prior_grid();
   pkv_allow_next_grid();
   const Cut cut = cuts[blockIdx.x];
-  const int col = blockIdx.y * kJoinCols + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int item = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int col = item, d = 4 * lane;
   if (col >= cut.cols) return;
   auto rec = [&](int i) -> const float * {
     return parts + (2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * C::RECORD;
   };
-  float m = -INFINITY;
-  for (int i = lane; i < cut.parts; i += 32) m = fmaxf(m, rec(i)[C::COLS * D + col]);
+  constexpr int kAhead = C::BLOCKS > 2 ? 2 : 4;
+  float4 v[kAhead][C::BLOCKS];
+  auto read = [&](int i) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (m == -INFINITY) m = 0.f;
-  constexpr int E = D / 32;
-  float x[E], l = 0.f;
+    for (int j = 0; j < kAhead; ++j)
+      if (i + j < cut.parts && d < D)
 #pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = 0.f;
-  for (int i = 0; i < cut.parts; ++i) {
-    const float *r = rec(i);
-    const float w = exp2f(r[C::COLS * D + col] - m);
-    l = fmaf(w, r[C::COLS * (D + 1) + col], l);
-    const float *y = r + col * D + (E == 2 ? 2 : 4) * lane;
+        for (int b = 0; b < C::BLOCKS; ++b)
+          v[j][b] = *reinterpret_cast<const float4 *>(rec(i + j) + col * D + 128 * b + d);
+  };
+  read(0);
+  float top = -INFINITY, sum = 0.f, ref = -INFINITY, l = 0.f;
+  for (int i = lane; i < cut.parts; i += 32) {
+    ref = rec(i)[C::COLS * D + col];
+    l = rec(i)[C::COLS * (D + 1) + col];
+    top = fmaxf(top, ref);
+  }
 #pragma unroll
-    for (int e = 0; e < E; e += (E == 2 ? 2 : 4)) {
-      if (E == 2) {
-        const float2 v = *reinterpret_cast<const float2 *>(y);
-        x[0] = fmaf(w, v.x, x[0]);
-        x[1] = fmaf(w, v.y, x[1]);
-      } else {
-        const float4 v = *reinterpret_cast<const float4 *>(y + 32 * e);
-        x[e] = fmaf(w, v.x, x[e]);
-        x[e + 1] = fmaf(w, v.y, x[e + 1]);
-        x[e + 2] = fmaf(w, v.z, x[e + 2]);
-        x[e + 3] = fmaf(w, v.w, x[e + 3]);
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (top == -INFINITY) top = 0.f;
+  float4 x[C::BLOCKS];
+#pragma unroll
+  for (int b = 0; b < C::BLOCKS; ++b) x[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < cut.parts; i0 += 32) {
+    if (cut.parts > 32 && i0 + lane < cut.parts) {   // (else they are at hand)
+      ref = rec(i0 + lane)[C::COLS * D + col];
+      l = rec(i0 + lane)[C::COLS * (D + 1) + col];
+    }
+    const float w = i0 + lane < cut.parts ? exp2f(ref - top) : 0.f;
+    float s = i0 + lane < cut.parts ? w * l : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    sum += s;
+    const int n = min(32, cut.parts - i0);
+    for (int i = 0; i < n; i += kAhead) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, (i + j) & 31);
+        if (i + j < n) {
+#pragma unroll
+          for (int b = 0; b < C::BLOCKS; ++b) {
+            x[b].x = fmaf(wj, v[j][b].x, x[b].x);
+            x[b].y = fmaf(wj, v[j][b].y, x[b].y);
+            x[b].z = fmaf(wj, v[j][b].z, x[b].z);
+            x[b].w = fmaf(wj, v[j][b].w, x[b].w);
+          }
+        }
       }
+      read(i0 + i + kAhead);
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (d >= D) return;
+  const float inv = 1.f / sum;
   const int tok = col / G;
   __nv_bfloat16 *o = out + (static_cast<long long>(cut.token0 + tok) * Hq + cut.head * G +
                             (col - tok * G)) * D;
-  if (E == 2) {
-    *reinterpret_cast<uint32_t *>(o + 2 * lane) = t_pack(x[0] * inv, x[1] * inv);
-  } else {
 #pragma unroll
-    for (int e = 0; e < E; e += 4)
-      *reinterpret_cast<uint2 *>(o + 32 * e + 4 * lane) =
-          make_uint2(t_pack(x[e] * inv, x[e + 1] * inv), t_pack(x[e + 2] * inv, x[e + 3] * inv));
-  }
+  for (int b = 0; b < C::BLOCKS; ++b)
+    *reinterpret_cast<uint2 *>(o + 128 * b + d) =
+        make_uint2(t_pack(x[b].x * inv, x[b].y * inv), t_pack(x[b].z * inv, x[b].w * inv));
 }
 
 template <int D>
@@ -1144,8 +1165,8 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
   if (st != PKV_OK) return st;
   PKV_CUDA_CHECK(pkv::launch_pdl(tree_attn_kernel<D>, dim3(grid), dim3(C::THREADS), smem_bytes<D>(),
                                  s, tmQ, tmK, tmV, a));
-  PKV_CUDA_CHECK(pkv::launch_pdl(tree_join_kernel<D>, dim3(grid, C::COLS / kJoinCols),
-                                 dim3(kJoinCols * 32), 0, s, static_cast<const float *>(a.parts),
+  PKV_CUDA_CHECK(pkv::launch_pdl(tree_join_kernel<D>, dim3(grid, C::COLS / kJoinWarps),
+                                 dim3(kJoinWarps * 32), 0, s, static_cast<const float *>(a.parts),
                                  static_cast<const Cut *>(a.cuts), a.out, a.Hq, a.G));
   return pkv::ok();
 }
