@@ -53,12 +53,12 @@ constexpr int kMostPlaces = 0x7fffffff;  // as many and more are reported, not c
 constexpr float kUnset = 1e30f;          // stands for -reference of a column without one
 constexpr int kJoinWarps = 8;            // of a joining CTA
 
-template <int D>
+template <int D, int MOST>
 struct Cfg {
-  static constexpr int COLS = 64;                       // columns of a unit, at most
+  static constexpr int COLS = MOST;                     // columns of a unit, at most
   // Units at work at a time, each with softmax warps, MMA warp, queries, P and TMEM of its own;
-  // where TMEM has room for one only, its softmax warps come in two groups of half the columns.
-  static constexpr int UNITS = D <= 128 ? 2 : 1;
+  // where there is room for one only, its softmax warps come in two groups of half the columns.
+  static constexpr int UNITS = D <= 128 && COLS == 64 ? 2 : 1;
   static constexpr int GROUPS = 2 / UNITS;              // groups of four softmax warps a unit
   static constexpr int HALF = COLS / GROUPS;            // columns of a softmax warp, at most
   static constexpr int SOFT = 8;                        // softmax warps of all units
@@ -70,27 +70,36 @@ struct Cfg {
   static constexpr int E = D / 64;                      // entries of a K tile, and of a V tile
   static constexpr int BLOCKS = D <= 128 ? 1 : D / 128; // blocks of 128 rows of O^T
   static constexpr int V_HALVES = D == 64 ? 1 : 2;      // entries of a V tile's block
-  static constexpr int NS = D == 128 ? 9 : D == 512 ? 8 : 10;
+  // as many as shared memory holds
+  static constexpr int NS = D == 512                ? 8
+                            : D == 256              ? (COLS == 128 ? 6 : 9)
+                            : D == 128              ? (COLS == 128 ? 8 : 9)
+                            : COLS == 128           ? 9
+                                                    : 10;
   static constexpr int Q_ATOM = COLS * 128;
   static constexpr int Q_BYTES = E * Q_ATOM;
-  static constexpr int P_BYTES = kTile * 128;
+  static constexpr int P_ATOM = kTile * 128;            // 64 columns of every key
+  static constexpr int P_BYTES = COLS / 64 * P_ATOM;
   static constexpr int OFF_Q = NS * ENTRY;              // [UNITS]
   static constexpr int OFF_P = OFF_Q + UNITS * Q_BYTES; // [UNITS]
   static constexpr int OFF_ONES = OFF_P + UNITS * P_BYTES;  // one swizzle atom of ones
   static constexpr int OFF_SMALL = OFF_ONES + 1024;
-  // of a unit: S of two tiles, O^T's blocks, the sums of the weights (in every lane)
-  static constexpr int S_COL = 0, O_COL = 2 * COLS, L_COL = O_COL + BLOCKS * COLS;
+  // of a unit: S of two tiles (of one where TMEM has no room), O^T's blocks, the sums of the
+  // weights (in every lane)
+  static constexpr int SB = D == 256 && COLS == 128 ? 1 : 2;
+  static constexpr int S_COL = 0, O_COL = SB * COLS, L_COL = O_COL + BLOCKS * COLS;
   static constexpr int UNIT_COLS = 512 / UNITS;
   static_assert(L_COL + COLS <= UNIT_COLS, "TMEM");
   static constexpr size_t RECORD = static_cast<size_t>(COLS) * (D + 2);   // floats of a part
 };
 
-// Which of a unit's columns see a key, a bit each.
+// Which of a unit's columns see a key, a bit each, for each group of softmax warps its own.
+template <int GROUPS>
 struct Prep {
-  uint64_t below[kTreeMax];    // those of the nodes that have node i on their path
-  uint64_t shallow[kTreeMax];  // those of the nodes of depth <= i
+  uint64_t below[GROUPS][kTreeMax];    // those of the nodes that have node i on their path
+  uint64_t shallow[GROUPS][kTreeMax];  // those of the nodes of depth <= i
   int depth[kTreeMax];
-  unsigned poison[2];          // those that see some value that is not finite
+  unsigned poison[GROUPS][2];          // those that see some value that is not finite
 };
 
 // A unit cut into parts, for the joining kernel.
@@ -98,30 +107,34 @@ struct Cut {
   int token0, cols, head, parts;
 };
 
-struct Small {
-  Prep prep[2];
+struct Rows {
   int pre[kTreeRows + 1];           // first place of every row on the line
   int n0[kTreeRows], ctx[kTreeRows], slot[kTreeRows];
-  uint8_t n[kTreeRows];
+  uint8_t n[kTreeRows];             // (the top bit: padding, only zeros to write)
+};
+
+template <typename C>
+struct Small {
+  static constexpr int COLS = C::UNITS * C::COLS;
+  Prep<C::GROUPS> prep[2];
   // of the columns, group g's from g * HALF on (the groups may be at different units)
-  alignas(16) float mneg[128];      // a column's reference's negative, kUnset: none yet
-  float ref[128];                   // its reference, -inf: none yet
-  float alpha[128];                 // what a new one scales O and sums by; NaN: poisoned
-  long long dst[128];               // its place in out, -1: none
-  float red[4][128];                // maxima of the four warps of a group
+  alignas(16) float mneg[COLS];     // a column's reference's negative, kUnset: none yet
+  float ref[COLS];                  // its reference, -inf: none yet
+  float alpha[COLS];                // what a new one scales O and sums by; NaN: poisoned
+  long long dst[COLS];              // its place in out, -1: none
+  float red[4][COLS];               // maxima of the four warps of a group
   int pages[2][16];
   int scan[12];
   uint64_t bars[48];
   uint32_t tmem;
+  Rows rows;
 };
 
-template <int D>
+template <typename C>
 constexpr size_t smem_bytes() {
-  return 1024 + Cfg<D>::OFF_SMALL + sizeof(Small);
+  static_assert(1024 + C::OFF_SMALL + sizeof(Small<C>) <= 232448, "shared memory");
+  return 1024 + C::OFF_SMALL + sizeof(Small<C>);
 }
-static_assert(smem_bytes<64>() <= 232448 && smem_bytes<128>() <= 232448 &&
-                  smem_bytes<256>() <= 232448 && smem_bytes<512>() <= 232448,
-              "shared memory");
 
 struct Args {
   const int32_t *table, *batch_idx, *ctx_lens, *row_start, *parents;
@@ -222,7 +235,7 @@ struct Part {
 
 // Goes through a CTA's share of the line, part by part.
 struct Line {
-  const Small *sm;
+  const Rows *sm;
   const Args *a;
   int pos, end, off;   // off: where in its unit pos is
   Part p;              // the unit at pos (all but t0 and t1)
@@ -235,7 +248,7 @@ struct Line {
     p.tile0 = p.lo / kTile;
     p.ntiles = sm->n[b] & 128 ? 0 : (p.ctx + p.n - 1) / kTile - p.tile0 + 1;
   }
-  __device__ void begin(const Small &s, const Args &args, int x0, int x1) {
+  __device__ void begin(const Rows &s, const Args &args, int x0, int x1) {
     sm = &s;
     a = &args;
     pos = x0;
@@ -292,15 +305,16 @@ __device__ __forceinline__ int share_of(int W, int at, int n) {
   return at < head ? at / (q + 1) : r + (at - head) / q;
 }
 
-template <int D>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+template <int D, int MOST>
+__global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args a) {
-  using C = Cfg<D>;
+  using C = Cfg<D, MOST>;
   extern __shared__ uint8_t raw[];
   uint8_t *sm = raw + ((1024u - (t_smem(raw) & 1023u)) & 1023u);
-  Small &s = *reinterpret_cast<Small *>(sm + C::OFF_SMALL);
+  Small<C> &s = *reinterpret_cast<Small<C> *>(sm + C::OFF_SMALL);
+  Rows &rows = s.rows;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
   const uint32_t sRing = t_smem(sm), sQ = t_smem(sm + C::OFF_Q), sP = t_smem(sm + C::OFF_P),
@@ -372,11 +386,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const TreeRow r = tree_row(b, a.N, a.row_start, a.batch_idx, a.ctx_lens, a.n_slots,
                                    a.max_pages, a.page_size);
         if (r.bits && cta == 0) tree_report(a.err, r.bits);
-        s.n0[b] = r.n0;
-        s.ctx[b] = r.ctx;
-        s.slot[b] = r.slot;
-        // the top bit: padding, only zeros to write
-        s.n[b] = static_cast<uint8_t>(r.n | (r.slot == 0 ? 128 : 0));
+        rows.n0[b] = r.n0;
+        rows.ctx[b] = r.ctx;
+        rows.slot[b] = r.slot;
+        rows.n[b] = static_cast<uint8_t>(r.n | (r.slot == 0 ? 128 : 0));
         if (r.n > 0) {
           const int lo = a.window > 0 ? max(0, r.ctx - a.window + 1) : 0;
           const int tiles = r.slot == 0 ? 0 : (r.ctx + r.n - 1) / kTile - lo / kTile + 1;
@@ -404,20 +417,20 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     sum = upto - sum;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      if (R * tid + i <= a.B) s.pre[R * tid + i] = sum;
+      if (R * tid + i <= a.B) rows.pre[R * tid + i] = sum;
       sum = add_places(sum, mine[i]);
     }
     __syncthreads();
   }
   const uint32_t tmem = s.tmem;
-  const bool too_long = s.pre[a.B] == kMostPlaces;
-  const int W = too_long ? 0 : s.pre[a.B];
+  const bool too_long = rows.pre[a.B] == kMostPlaces;
+  const int W = too_long ? 0 : rows.pre[a.B];
   if (too_long && cta == 0 && tid == 0) tree_report(a.err, PKV_ERR_POS);
   const int ctas = min(static_cast<int>(gridDim.x), W);
   const int x0 = cta < ctas ? share(W, cta, ctas) : 0;
   const int x1 = cta < ctas ? share(W, cta + 1, ctas) : 0;
   Line line;
-  line.begin(s, a, x0, x1);
+  line.begin(rows, a, x0, x1);
   const Part &p = line.p;
   // (what the prior kernel may write or read - caches, queries, workspace, output - from here on)
   pkv_wait_prior_grid();
@@ -482,7 +495,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     };
     while (ok && line.next()) {
       if (p.t0 == p.t1) continue;
-      const int32_t *row = a.table + static_cast<long long>(s.slot[p.b]) * a.max_pages;
+      const int32_t *row = a.table + static_cast<long long>(rows.slot[p.b]) * a.max_pages;
       const int last_page = (p.ctx + p.n - 1) >> a.log_page;
       const int first_page = p.lo >> a.log_page;
       // page numbers 32 at a time, the next ones on their way
@@ -539,7 +552,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     bool ok = true;
     const uint32_t tx = __shfl_sync(0xffffffffu, tmem + x * C::UNIT_COLS, 0);
     const uint64_t dQ = t_desc(sQ + x * C::Q_BYTES, 16, 1024);
-    const uint64_t dP = t_desc(sP + x * C::P_BYTES, 0, 1024), dOne = t_desc(sOnes, 0, 0);
+    const uint64_t dP = t_desc(sP + x * C::P_BYTES, C::P_ATOM, 1024), dOne = t_desc(sOnes, 0, 0);
     // the next BT ring entries, once they are there: waits, fences and elections cost more than
     // issuing the MMAs of one
     constexpr int BT = C::E < 2 ? 1 : 2;
@@ -610,8 +623,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 #pragma unroll 1
       for (int t = p.t0; t <= p.t1 && ok; ++t) {
         if (t < p.t1) {
-          const int buf = tiles & 1;
-          if (tiles >= 2) ok = wait_for(sfree(x, buf), (tiles >> 1) - 1);
+          const int buf = tiles % C::SB;
+          if (tiles >= C::SB) ok = wait_for(sfree(x, buf), tiles / C::SB - 1);
           const uint32_t to = __shfl_sync(0xffffffffu, tx + C::S_COL + buf * C::COLS, 0);
 #pragma unroll 1
           for (int c = 0; c < C::E && ok; c += BT) {
@@ -664,10 +677,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             t_tma_4d(sQ + x * C::Q_BYTES + at * C::Q_ATOM + i * box, &tmQ, 0, p.head * a.G,
                      p.n0 + p.tok0 + a.box_nodes * i, at, qfull(x));
       }
-      Prep &w = s.prep[segs & 1];
+      Prep<C::GROUPS> &w = s.prep[segs & 1];
       if (segs >= 2 && !wait_for(prepempty + 8 * (segs & 1), (segs >> 1) - 1)) break;
       // paths: each node's set of ancestors and itself, twice as far every time
-      uint64_t *path = w.below;
+      uint64_t *path = w.below[0];
       int *jump = w.depth;
 #pragma unroll
       for (int i = lane; i < kTreeMax; i += 32) {
@@ -698,31 +711,42 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         __syncwarp();
         if (!more) break;
       }
-      uint64_t below[2] = {0, 0}, shallow[2] = {0, 0};
+      uint64_t below[2][2] = {{0, 0}, {0, 0}}, shallow[2][2] = {{0, 0}, {0, 0}};   // [group][node]
       int depth[2] = {0, 0};
-      const uint64_t heads = (1ull << a.G) - 1;     // a node's columns
+      const int hn = columns<C::GROUPS>(p.toks * a.G) / C::GROUPS;
 #pragma unroll 1
       for (int t = 0; t < p.n; ++t) {
         const uint64_t v = path[t];
         const int d = __popcll(v) - 1;
-        const int at = t - p.tok0;
-        const uint64_t mine = at >= 0 && at < p.toks ? heads << (at * a.G) : 0;
+        const int first = (t - p.tok0) * a.G;          // the node's columns
+        const bool here = t >= p.tok0 && t < p.tok0 + p.toks;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int i = lane + 32 * q;
-          below[q] |= (v >> i) & 1 ? mine : 0;
-          shallow[q] |= d <= i ? mine : 0;
-          if (t == i) depth[q] = d;
+        for (int q = 0; q < 2; ++q)
+          if (t == lane + 32 * q) depth[q] = d;
+#pragma unroll
+        for (int gr = 0; gr < C::GROUPS; ++gr) {
+          // those of them that are the group's
+          const int lo = max(0, first - gr * hn), hi = min(hn, first + a.G - gr * hn);
+          const uint64_t mine = here && lo < hi ? ((1ull << (hi - lo)) - 1) << lo : 0;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int i = lane + 32 * q;
+            below[gr][q] |= (v >> i) & 1 ? mine : 0;
+            shallow[gr][q] |= d <= i ? mine : 0;
+          }
         }
       }
       __syncwarp();
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        w.below[lane + 32 * q] = below[q];
-        w.shallow[lane + 32 * q] = shallow[q];
+#pragma unroll
+        for (int gr = 0; gr < C::GROUPS; ++gr) {
+          w.below[gr][lane + 32 * q] = below[gr][q];
+          w.shallow[gr][lane + 32 * q] = shallow[gr][q];
+        }
         w.depth[lane + 32 * q] = depth[q];
       }
-      if (lane < 2) w.poison[lane] = 0;
+      if (lane < 2 * C::GROUPS) w.poison[lane >> 1][lane & 1] = 0;
       __syncwarp();
       if (lane == 0) t_arrive(prepfull + 8 * (segs & 1));
       ++segs;
@@ -736,7 +760,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     const int row = 32 * quad + lane;           // the key of a tile, or the column of D
     const uint32_t trow = tmem + x * C::UNIT_COLS + (static_cast<uint32_t>(32 * quad) << 16);
     const int h0 = sub * C::HALF;               // where the warps' columns are in shared memory
-    uint8_t *pbuf = sm + C::OFF_P + x * C::P_BYTES + row * 128;
+    uint8_t *pbuf = sm + C::OFF_P + x * C::P_BYTES + row * 128;   // this key's row of P
     const int mine = 32 * quad + lane;          // the column that this thread looks after
     int tiles = 0, segs = 0, seg = 0, g = 0;    // g: ring entries of the parts so far
     bool ok = true, gone = false;
@@ -745,35 +769,41 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     auto unit = [&]() {
       const int cols = p.toks * a.G;
       const int hn = columns<C::GROUPS>(cols) / C::GROUPS, c0 = grp * hn;   // this warp's columns
-      Prep &w = s.prep[seg & 1];
+      Prep<C::GROUPS> &w = s.prep[seg & 1];
       const int nt = p.t1 - p.t0;
-      // the columns in use of the warp's own
-      const uint64_t wide = cols >= 64 ? ~0ull : (1ull << cols) - 1;
+      // a group's columns in use
+      auto used = [&](int gr) -> uint64_t {
+        const int k = min(hn, cols - gr * hn);
+        return k <= 0 ? 0 : ~0ull >> (64 - k);
+      };
       bool any_masked = false;
 #pragma unroll 1
       for (int t = p.t0; t < p.t1; ++t, ++tiles) {
-        const int buf = tiles & 1, i = t - p.t0;
+        const int buf = tiles % C::SB, i = t - p.t0;
         const int j0 = (p.tile0 + t) * kTile, j = j0 + row;
         const bool masked = j0 + kTile > p.ctx ||
                             (a.window > 0 && j0 <= p.ctx + p.n - 1 - a.window);
         const bool first = i == 0;
         uint64_t sees = ~0ull;                  // the columns that see this thread's key
+        bool none_sees = false, all_see = true;
         any_masked |= masked;
         // (S first: the unit's queries are there then, and the preparations before its own)
-        ok = ok && wait_for(sfull_x + 8 * buf, tiles >> 1);
+        ok = ok && wait_for(sfull_x + 8 * buf, tiles / C::SB);
         if (masked) {
           ok = ok && wait_for(prepfull + 8 * (seg & 1), seg >> 1);
           const int node = j - p.ctx;
-          if (node >= p.n) {
-            sees = 0;
-          } else if (node >= 0) {
-            sees = w.below[node];
-            if (a.window > 0)
-              sees &= w.shallow[min(static_cast<long long>(kTreeMax - 1),
-                                    static_cast<long long>(w.depth[node]) + a.window - 1)];
-          } else if (a.window > 0) {
-            const int d = node + a.window - 1;
-            sees = d < 0 ? 0 : w.shallow[min(d, kTreeMax - 1)];
+          const int reach = node < 0 ? node + a.window - 1
+                                     : min(static_cast<long long>(kTreeMax),
+                                           static_cast<long long>(w.depth[min(node, p.n - 1)]) +
+                                               a.window - 1);
+          none_sees = true;
+#pragma unroll
+          for (int gr = 0; gr < C::GROUPS; ++gr) {
+            uint64_t v = node >= p.n ? 0 : node >= 0 ? w.below[gr][node] : ~0ull;
+            if (a.window > 0) v &= reach < 0 ? 0 : w.shallow[gr][min(reach, kTreeMax - 1)];
+            if (gr == grp) sees = v;
+            none_sees = none_sees && !(v & used(gr));
+            all_see = all_see && !(~v & used(gr));
           }
         }
         t_fence_after();
@@ -786,7 +816,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(r[e]);
           if (masked) {
-            const uint32_t bits = static_cast<uint32_t>(sees >> (c0 + c));
+            const uint32_t bits = static_cast<uint32_t>(sees >> c);
 #pragma unroll
             for (int e = 0; e < 16; ++e) y[e] = bits & (1u << e) ? y[e] : -INFINITY;
           }
@@ -860,10 +890,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 w[e / 2] = t_pack(t_ex2(y[e]), t_ex2(y[e + 1]));
                 w[e / 2 + 1] = t_pack(t_ex2(y[e + 2]), t_ex2(y[e + 3]));
               }
-              const int at = (c0 + c) >> 3;
-              *reinterpret_cast<uint4 *>(pbuf + ((at ^ (row & 7)) << 4)) =
+              const int at = ((c0 + c) & 63) >> 3;
+              uint8_t *to = pbuf + (c0 + c) / 64 * C::P_ATOM;
+              *reinterpret_cast<uint4 *>(to + ((at ^ (row & 7)) << 4)) =
                   make_uint4(w[0], w[1], w[2], w[3]);
-              *reinterpret_cast<uint4 *>(pbuf + (((at + 1) ^ (row & 7)) << 4)) =
+              *reinterpret_cast<uint4 *>(to + (((at + 1) ^ (row & 7)) << 4)) =
                   make_uint4(w[4], w[5], w[6], w[7]);
             }
           }
@@ -877,21 +908,23 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           // the tile's V entries: V(i) stands behind K(i + 1) in the ring. Rows seen by no column
           // are cleared, and those seen by some only if they are not finite
           const int e0 = g + (2 * i + (i == nt - 1 ? 1 : 2)) * C::E;
-          const unsigned none = __ballot_sync(0xffffffffu, (sees & wide) == 0);
-          const unsigned part = __ballot_sync(0xffffffffu, (sees & wide) != 0 && (sees & wide) != wide);
+          const unsigned none = __ballot_sync(0xffffffffu, none_sees);
+          const unsigned part = __ballot_sync(0xffffffffu, !none_sees && !all_see);
           // a phase is told from the one before only, so the entries' previous tiles have to be
           // there: they stand at or before K(i) or V(i - 1) in the ring, whose products are done,
-          // but for rings no longer than a tile, where they are K(i + 1)
-          static_assert(C::NS == C::E || C::NS >= 2 * C::E, "previous tiles");
-          if (none | part) {
-            if (C::NS == C::E && i < nt - 1)
-              ok = ok && wait_for(sfull_x + 8 * (buf ^ 1), (tiles + 1) >> 1);
+          // but for rings shorter than two tiles, where some are K(i + 1)
+          // (a single atom is the first group's)
+          if ((none | part) && (D > 64 || grp == 0)) {
+            if (C::NS < 2 * C::E && i < nt - 1)
+              ok = ok && wait_for(sfull_x + 8 * ((tiles + 1) % C::SB), (tiles + 1) / C::SB);
             constexpr int KEYS = kTile / C::V_HALVES;    // of an entry
             // this warp's share of a row of an entry: 8 lanes an atom, both atoms or its group's
             constexpr int AT = D == 64 || C::GROUPS == 2 ? 1 : 2;
             constexpr int STEP = 4 / AT;                 // rows at a time
             const int in = (lane & 7) * 16 +
-                           ((C::GROUPS == 2 ? grp : AT == 2 ? (lane >> 3) & 1 : 0) * KEYS) * 128;
+                           (D == 64            ? 0
+                            : C::GROUPS == 2 ? grp
+                                             : (lane >> 3) & 1) * KEYS * 128;
             const int which = lane / (8 * AT);           // of the rows at a time
 #pragma unroll 1
             for (int blk = 0; blk < C::BLOCKS; ++blk) {
@@ -928,8 +961,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
               }
               const unsigned poisoned = clear & part;
               if (poisoned >> lane & 1) {
-                atomicOr(&w.poison[0], static_cast<unsigned>(sees & wide));
-                atomicOr(&w.poison[1], static_cast<unsigned>((sees & wide) >> 32));
+                // (this row's node, for all groups: each has looked at columns of D of its own)
+                const int node = j - p.ctx;
+                const int reach =
+                    node < 0 ? node + a.window - 1
+                             : min(kTreeMax - 1, w.depth[node] + min(a.window, kTreeMax) - 1);
+#pragma unroll
+                for (int gr = 0; gr < C::GROUPS; ++gr) {
+                  uint64_t u = node >= 0 ? w.below[gr][node] : ~0ull;
+                  if (a.window > 0) u &= w.shallow[gr][min(reach, kTreeMax - 1)];
+                  atomicOr(&w.poison[gr][0], static_cast<unsigned>(u));
+                  atomicOr(&w.poison[gr][1], static_cast<unsigned>(u >> 32));
+                }
               }
               if (clear) {
                 const unsigned mine_of = clear >> which;
@@ -953,7 +996,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       float *rec = a.parts + (2 * cta + (p.t0 == 0 ? 1 : 0)) * C::RECORD;
       if (mine < hn) {
         const int c = c0 + mine, k = h0 + mine, tok = p.tok0 + c / a.G;
-        const bool bad = any_masked && (w.poison[c >> 5] >> (c & 31) & 1);
+        const bool bad = any_masked && (w.poison[grp][mine >> 5] >> (mine & 31) & 1);
         s.dst[k] = c < cols ? (static_cast<long long>(p.n0 + tok) * a.Hq + p.head * a.G + c % a.G) * D
                             : -1;
         s.alpha[k] = bad ? NAN : 1.f;
@@ -1054,10 +1097,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 
 // Joins the parts of the unit that CTA blockIdx.x began and others went on with: a warp a
 // column, the reads of a few parts in flight with those of their weights.
-template <int D>
+template <int D, int MOST>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     tree_join_kernel(const float *parts, const Cut *cuts, __nv_bfloat16 *out, int Hq, int G) {
-  using C = Cfg<D>;
+  using C = Cfg<D, MOST>;
   pkv_wait_prior_grid();
   pkv_allow_next_grid();
   const Cut cut = cuts[blockIdx.x];
@@ -1129,10 +1172,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         make_uint2(t_pack(x[b].x * inv, x[b].y * inv), t_pack(x[b].z * inv, x[b].w * inv));
 }
 
-template <int D>
+template <int D, int MOST>
 int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void *workspace,
            cudaStream_t s) {
-  using C = Cfg<D>;
+  using C = Cfg<D, MOST>;
   static std::mutex mu;
   static bool done[64] = {false};
   int dev = 0;
@@ -1141,9 +1184,9 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
-      PKV_CUDA_CHECK(cudaFuncSetAttribute(tree_attn_kernel<D>,
+      PKV_CUDA_CHECK(cudaFuncSetAttribute(tree_attn_kernel<D, MOST>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          static_cast<int>(smem_bytes<D>())));
+                                          static_cast<int>(smem_bytes<C>())));
       done[dev] = true;
     }
   }
@@ -1163,20 +1206,25 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
   if (st == PKV_OK) st = pkv::prefill_atoms_map(&tmK, k, a.Hkv, rows, D, k_box, 1, 1);
   if (st == PKV_OK) st = pkv::prefill_atoms_map(&tmV, v, a.Hkv, rows, D, v_box, 1, 1);
   if (st != PKV_OK) return st;
-  PKV_CUDA_CHECK(pkv::launch_pdl(tree_attn_kernel<D>, dim3(grid), dim3(C::THREADS), smem_bytes<D>(),
+  PKV_CUDA_CHECK(pkv::launch_pdl(tree_attn_kernel<D, MOST>, dim3(grid), dim3(C::THREADS), smem_bytes<C>(),
                                  s, tmQ, tmK, tmV, a));
-  PKV_CUDA_CHECK(pkv::launch_pdl(tree_join_kernel<D>, dim3(grid, C::COLS / kJoinWarps),
+  PKV_CUDA_CHECK(pkv::launch_pdl(tree_join_kernel<D, MOST>, dim3(grid, C::COLS / kJoinWarps),
                                  dim3(kJoinWarps * 32), 0, s, static_cast<const float *>(a.parts),
                                  static_cast<const Cut *>(a.cuts), a.out, a.Hq, a.G));
   return pkv::ok();
 }
 
-size_t record_floats(int D) {
-  return D == 64    ? Cfg<64>::RECORD
-         : D == 128 ? Cfg<128>::RECORD
-         : D == 256 ? Cfg<256>::RECORD
-                    : Cfg<512>::RECORD;
+// Units of 128 columns where the rows have more than 64, by the packed nodes a row: the keys of
+// a row are then read half as often. At D = 512 TMEM holds 64.
+template <int D>
+int launch_for(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, const Args &a,
+               void *workspace, cudaStream_t s) {
+  if (D <= 256 && static_cast<long long>(a.N) * a.G > 64LL * a.B)
+    return launch<D, D <= 256 ? 128 : 64>(q, k, v, a, workspace, s);
+  return launch<D, 64>(q, k, v, a, workspace, s);
 }
+
+size_t record_floats(int D) { return static_cast<size_t>(D <= 256 ? 128 : 64) * (D + 2); }
 
 }  // namespace
 
@@ -1238,8 +1286,8 @@ extern "C" int paged_tree_attn(const pkv_bf16 *q, const pkv_bf16 *k_cache, const
   a.Hkv = Hkv;
   a.G = Hq / Hkv;
   a.scale_log2 = scale * 1.4426950408889634f;
-  return D == 64    ? launch<64>(q, k_cache, v_cache, a, workspace, s)
-         : D == 128 ? launch<128>(q, k_cache, v_cache, a, workspace, s)
-         : D == 256 ? launch<256>(q, k_cache, v_cache, a, workspace, s)
-                    : launch<512>(q, k_cache, v_cache, a, workspace, s);
+  return D == 64    ? launch_for<64>(q, k_cache, v_cache, a, workspace, s)
+         : D == 128 ? launch_for<128>(q, k_cache, v_cache, a, workspace, s)
+         : D == 256 ? launch_for<256>(q, k_cache, v_cache, a, workspace, s)
+                    : launch_for<512>(q, k_cache, v_cache, a, workspace, s);
 }

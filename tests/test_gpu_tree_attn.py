@@ -33,6 +33,28 @@ def test_nodes(D, nodes):
     TreeCase(rng, 8, 1, D, 32, [129, 40], trees).device(pkv).check(pkv)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("window", [0, 40])
+def test_more_columns_than_64(D, G, window):
+    """Rows of many nodes take units of 128 columns; heads of a node may fall to both halves,
+    rows of few nodes stand beside them."""
+    rng = rng_of(20, D, G, window)
+    ns = (64, 64, 61) if G <= 2 else (64, 30, 1, 41)
+    trees = [random_tree(rng, n, w) for n, w in zip(ns, (4, 1, 8, 2))]
+    c = TreeCase(rng, G, 1, D, 16, [300, 5, 131, 0][:len(ns)], trees, window=window)
+    c.device(pkv).check(pkv)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_and_long_rows_of_many_nodes(D):
+    rng = rng_of(21, D)
+    trees = [random_tree(rng, int(rng.integers(15, 40)), 3) for _ in range(60)]
+    TreeCase(rng, 8, 1, D, 32, rng.integers(0, 900, 60), trees).device(pkv).check(pkv)
+    trees = [random_tree(rng, 20, 3), random_tree(rng, 33, 5)]
+    TreeCase(rng, 16, 2, D, 64, [9000, 4001], trees).device(pkv).check(pkv)
+
+
 @pytest.mark.parametrize("D,Hq,Hkv", [(64, 4, 2), (128, 8, 2), (256, 3, 1), (512, 8, 1)])
 @pytest.mark.parametrize("ctx", [0, 1, 2, 7, 8, 55, 63, 64, 65, 120, 126, 127, 128, 129, 191, 255,
                                  256, 257, 1000])
@@ -101,11 +123,12 @@ def test_the_most_rows():
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("D", [64, 128, 256, 512])
-def test_values_of_other_branches_stay_out(value, D):
+@pytest.mark.parametrize("more", [0, 20])
+def test_values_of_other_branches_stay_out(value, D, more):
     """A node whose keys and values are not finite changes nothing for nodes that do not
     see it; the context behind a node's window likewise."""
     rng = rng_of(11, D)
-    par = [-1, 0, 0, 1, 2, 3, 4, 1, 1]
+    par = [-1, 0, 0, 1, 2, 3, 4, 1, 1] + [5] * more
     c = TreeCase(rng, 8, 1, D, 16, [100, 40], [par, par])
     bad = [tree.cache_row(c.table, s, ctx + 4, 16) for s, ctx in ((1, 100), (2, 40))]
     keep = c.kc[:, bad].copy(), c.vc[:, bad].copy()
