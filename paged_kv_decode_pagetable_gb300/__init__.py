@@ -842,8 +842,7 @@ def prefill_attn(q, k, v, block_mask: PrefillBlockMask, scale, out, stream=None)
 
 TREE_MAX = 64
 
-# Each call looks its tensors over in one go (_fits, _fits_i32, _fits_tokens: about 0.3 us a
-# tensor) and only where something does not fit finds out what, and raises, in its _refuse_
+# Each call looks its tensors over in one go (_fits, _fits_i32: about 0.3 us a tensor) and only where something does not fit finds out what, and raises, in its _refuse_
 # function (host time of a call with everything told apart first: append 13.9 us, attention
 # 8.3, verification 10.0, move of 48 caches 41.2).
 
@@ -855,12 +854,6 @@ def _fits(t, dtype, shape, dev) -> bool:
 
 def _fits_i32(t, n, dev) -> bool:
     return (t.dtype is _I32 and t.numel() >= n and t.is_contiguous()
-            and t.get_device() == dev)
-
-
-def _fits_tokens(t, heads, D, dev) -> bool:
-    """bf16 [N][heads][D], the rows possibly apart."""
-    return (t.dtype is _BF16 and t.shape[1:] == (heads, D) and t.stride()[1:] == (D, 1)
             and t.get_device() == dev)
 
 
@@ -935,10 +928,16 @@ def tree_qkv_norm_rope_append(q, k, v, gamma_q, gamma_k, batch_idx, ctx_lens, ro
         rows = (Hkv, n_pages * page_size, D)
         dev = _raw_device() if q.is_cuda else None
         B = row_start.numel() - 1
-        fits = (_fits_tokens(q, Hq, D, dev) and _fits_tokens(k, Hkv, D, dev)
-                and (v is None or (_fits_tokens(v, Hkv, D, dev) and v.shape[0] == N))
-                and k.shape[0] == N and N > 1
-                and _fits(k_cache, _BF16, rows, dev) and _fits(v_cache, _BF16, rows, dev)
+        sq, hq, eq = q.stride()
+        sk, hk, ek = k.stride()
+        fits = (q.dtype is _BF16 and hq == D and eq == 1 and k.dtype is _BF16 and hk == D
+                and ek == 1 and k.shape == (N, Hkv, D) and k.get_device() == dev and N > 1)
+        sv = 0
+        if v is not None:
+            sv, hv, ev = v.stride()
+            fits = (fits and v.dtype is _BF16 and hv == D and ev == 1 and v.shape == (N, Hkv, D)
+                    and v.get_device() == dev)
+        fits = (fits and _fits(k_cache, _BF16, rows, dev) and _fits(v_cache, _BF16, rows, dev)
                 and _fits(q_out, _BF16, (N, Hq, D), dev)
                 and (gamma_q is None or _fits(gamma_q, _BF16, (D,), dev))
                 and (gamma_k is None or _fits(gamma_k, _BF16, (D,), dev))
@@ -949,9 +948,7 @@ def tree_qkv_norm_rope_append(q, k, v, gamma_q, gamma_k, batch_idx, ctx_lens, ro
                 and (err_word is None or _fits_i32(err_word, 1, dev)))
     except (AttributeError, TypeError, ValueError, IndexError):
         fits = False
-    if fits:
-        sq, sk, sv = q.stride()[0], k.stride()[0], 0 if v is None else v.stride()[0]
-    else:
+    if not fits:
         B, N, Hq, Hkv, D, sq, sk, sv, dev = _refuse_append(
             q, k, v, gamma_q, gamma_k, batch_idx, ctx_lens, row_start, parents, dev_table, n_slots,
             max_pages_per_seq, page_size, n_pages, k_cache, v_cache, q_out, err_word)

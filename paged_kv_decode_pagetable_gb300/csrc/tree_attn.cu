@@ -6,32 +6,51 @@
 // behind t (a node's position is ctx + its depth).
 //
 // Bound by reading each key and value of a row's context once for all its nodes and the query
-// heads of a kv head, until nodes x heads reach a few hundred; those "columns" (at most 128 of
-// them a unit, 64 where D > 128) are the N of both products, so that a small tree costs no
-// more arithmetic than it has columns:
+// heads of a kv head, until nodes x heads reach a few hundred. Those "columns" are the N of both
+// products, at most 64 of them a unit of work, or 128 where the rows have more than 64 (and TMEM
+// has room, D <= 256), so that a small tree costs no more arithmetic than it has columns:
 //   S^T = K q^T    M = 128 keys of a tile, N columns, both operands K-major,
 //   O^T = V^T P^T  M = 128 columns of D, N columns, K = the tile's 128 keys, both MN-major: V as
 //                  it lies in the cache, P as the threads write it, a key's columns in a row.
-// In S^T a thread owns a key. Its columns' maxima run across threads, so they are not taken
-// tile by tile: a column keeps a reference, every thread checks that none of its scores passes
-// it by more than 2^8, and only where one does (a unit's first tile, and few others) the maxima
-// are reduced, the references moved and O scaled. The weights' sums are a third product, with ones
-// in V's place: every lane of TMEM has them, and no thread keeps a sum for each column.
+// An MMA with M = 128 takes 42 cycles for 32 columns, 50 for 64, 66 for 128, in either order of
+// the operands; with the queries as M, 32 rows would pay for 128.
+// In S^T a thread owns a key. Its columns' maxima run across threads, so they are not taken tile
+// by tile: a column keeps a reference, every thread checks that none of its scores passes it by
+// more than 2^8, and only where one does (a unit's first tile, and few others) the maxima are
+// reduced, the references moved and O scaled. The weights' sums are a third product, with ones in
+// V's place: every lane of TMEM has them, and no thread keeps a sum for each column. Weights are
+// rounded to bf16 (V's type) and summed as rounded; scores, references and O are fp32.
 //
-// Work: the units' tiles, one more place for each unit's start, lie on one line, cut into equal
-// shares for one persistent CTA an SM from the lengths, on the device. A unit that is cut leaves
-// its parts (O, reference and sum, fp32) in the workspace and a second small kernel joins them
-// in order, so results do not depend on timing and no CTA waits for another.
-//   warps 0-7 (softmax): warp w the keys of TMEM lanes 32 (w % 4) .. and half w / 4 of the
-//     columns; masks, weights, references, a unit's output or part;
-//   warp 8: K and V tiles by TMA, one box a page and 64 columns, into a ring of [128 keys][128
-//     columns of D] in the order in which the MMAs use them up: K(0), K(1), V(0), K(2), V(1) ..;
-//   warp 9: the MMAs, S one tile ahead of P V;
-//   warp 10: a unit's queries by TMA, and which nodes see a key: sets of 64 bits, from the
-//     parents by pointer doubling.
+// Work: the units' tiles, one more place for each unit's start (2 and 3: 40 and 42 us for the
+// rollout batch, not 39), lie on one line, cut into equal shares for one persistent CTA an SM from
+// the lengths, on the device. A unit that is cut leaves its parts (O, reference and sum, fp32) in
+// the workspace and a second small kernel joins them in order, so results do not depend on timing
+// and no CTA waits for another. (Shares that begin at a unit's edge where that is near, to cut
+// fewer: 56 -> 71 us for 64 nodes at D = 512, 39 -> 42 for the rollout batch.) The line is planned
+// from row_start, ctx_lens and batch_idx before the prior kernel has ended.
+//   warps 0-7 (softmax): D <= 128 with 64 columns, two units at a time, four warps each, so that
+//     one unit's start and end overlap the other's tiles; else one unit, its columns in two
+//     halves. Warp w has the keys of TMEM lanes 32 (w % 4) ..: masks, weights, references, a
+//     unit's output or part;
+//   warp 8: K and V tiles by TMA, a box a page and 64 columns, into a ring of 16 KB entries in the
+//     order in which the MMAs use them up: K(0), K(1), V(0), K(2), V(1) ..;
+//   warp 9: a unit's queries by TMA, and which columns see a key: sets of 64 bits, from the
+//     parents by pointer doubling;
+//   warps 10, 11: the MMAs of a unit each, S one tile ahead of P V.
 // Rows of V that no node sees are cleared in shared memory (0 x NaN would reach every column);
 // one that is not finite and seen by some nodes only is cleared too and those nodes' results
-// are NaN, as theirs are: nothing of it reaches the others.
+// are NaN: nothing of it reaches the others.
+//
+// What costs most next to memory is code: a first form with its loops unrolled had 120 KB, a third
+// of its warps' time went into waiting for instructions, and the rollout batch took 70 us. Hence
+// the loops kept as loops, the short waits, and one site of each product.
+//
+// Measured (6769 GB/s measured): 16 rows of 16k to 32k tokens, 8-node chains, 8 heads of 128,
+// 244 us, 0.98 of reading them; 64 rows of 100 to 1024 tokens, trees of 8, 39 us, 0.59: its start
+// (launch, plan, the rings' first fill) and its end (last tiles, join) are 6 us each; 64 rows of
+// 256 to 2048 tokens in a window of 512, trees of 16, one head of 256, 30 us, 0.19, and 16 rows
+// with trees of 64, one head of 512, 56 us, 0.14: they write and read as many bytes in parts as
+// in keys, and at D = 512 every 8 nodes read the keys again; one row of 41 tokens 8.4 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -142,7 +161,8 @@ struct Args {
   float *parts;
   Cut *cuts;
   int32_t *err;
-  int n_slots, max_pages, page_size, log_page, n_pages, window, B, N, Hq, Hkv, G, unit_tokens, box_nodes;
+  int n_slots, max_pages, page_size, log_page, n_pages, window, B, N, Hq, Hkv, G;
+  int unit_tokens, box_nodes;   // nodes of a unit at most, and of a box of queries
   float scale_log2;
 };
 
@@ -600,9 +620,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
               t_mma(to, va + k * (2048 >> 4), pb + k * (2048 >> 4), id, b > 0 || k > 0 ? 1u : add);
             t_commit(empty + 8 * entry[b]);
           }
-          if (c + BT == C::E) {
-            t_commit(pvdone(x));
-          }
+          if (c + BT == C::E) t_commit(pvdone(x));
         }
         __syncwarp();
       }
@@ -703,6 +721,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
           }
         }
         const bool more = __any_sync(0xffffffffu, j[0] >= 0 || j[1] >= 0);
+        __syncwarp();   // all have read
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           path[lane + 32 * q] = v[q];
@@ -1215,7 +1234,9 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
 }
 
 // Units of 128 columns where the rows have more than 64, by the packed nodes a row: the keys of
-// a row are then read half as often. At D = 512 TMEM holds 64.
+// a row are then read half as often (16 rows of 1k to 3k tokens, 8 heads of 128: trees of 64
+// 90 -> 78 us, of 32 58 -> 52; one head of 256, 128 rows of up to 2k tokens, trees of 16 62 -> 55).
+// At D = 512 TMEM holds 64.
 template <int D>
 int launch_for(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, const Args &a,
                void *workspace, cudaStream_t s) {
