@@ -624,10 +624,12 @@ int tree_qkv_norm_rope_append(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf
  * weights enter the product with V as bf16. Table entries that are negative or >= n_pages inside a row's key
  * range set PKV_ERR_PAGE_* (that row's output is then unspecified). Requires
  * D in {64, 128, 256, 512}, 1 <= Hq / Hkv <= 8, page_size a power of two >= 8,
- * scale finite and > 0, 16-byte aligned tensors. The workspace (any contents,
- * paged_tree_attn_workspace(Hq, Hkv, D) bytes, whatever the batch; 0 for sizes
- * the call refuses) holds parts of rows during a call: calls that share one
- * must not overlap on the GPU. A call whose nodes, heads and keys make 2^31
+ * scale finite and > 0, 16-byte aligned tensors. The workspace
+ * (paged_tree_attn_workspace(Hq, Hkv, D) bytes, whatever the batch; 0 for sizes
+ * the call refuses) holds parts of rows during a call and counts them: zero it
+ * once before its first use. Every call leaves its counts zero, except one that
+ * reports PKV_ERR_TIMEOUT, after which it must be zeroed again. Calls that share
+ * one, of whatever shapes, must not overlap on the GPU. A call whose nodes, heads and keys make 2^31
  * tiles of 128 keys or more sets PKV_ERR_POS and computes nothing; a wait for a
  * copy that gives up sets PKV_ERR_TIMEOUT (outputs are then unspecified). */
 int paged_tree_attn(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,

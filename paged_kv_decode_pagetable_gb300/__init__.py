@@ -842,9 +842,10 @@ def prefill_attn(q, k, v, block_mask: PrefillBlockMask, scale, out, stream=None)
 
 TREE_MAX = 64
 
-# Each call looks its tensors over in one go (_fits, _fits_i32: about 0.3 us a tensor) and only where something does not fit finds out what, and raises, in its _refuse_
-# function (host time of a call with everything told apart first: append 13.9 us, attention
-# 8.3, verification 10.0, move of 48 caches 41.2).
+# Each call looks its tensors over in one go (_fits, _fits_i32: about 0.3 us a tensor) and only
+# where something does not fit finds out what, and raises, in its _refuse_ function (with
+# everything told apart first, the binding took 13.9 us for an append, 8.3 for an attention, 10.0
+# for a verification, 41.2 for a move of 48 caches; so 7.5, 4.4, 4.6 and 20.4).
 
 
 def _fits(t, dtype, shape, dev) -> bool:
@@ -931,7 +932,8 @@ def tree_qkv_norm_rope_append(q, k, v, gamma_q, gamma_k, batch_idx, ctx_lens, ro
         sq, hq, eq = q.stride()
         sk, hk, ek = k.stride()
         fits = (q.dtype is _BF16 and hq == D and eq == 1 and k.dtype is _BF16 and hk == D
-                and ek == 1 and k.shape == (N, Hkv, D) and k.get_device() == dev and N > 1)
+                and ek == 1 and k.shape == (N, Hkv, D) and q.get_device() == dev
+                and k.get_device() == dev and N > 1)
         sv = 0
         if v is not None:
             sv, hv, ev = v.stride()
@@ -1003,8 +1005,8 @@ def paged_tree_attn(q, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq, 
                     err_word=None, stream=None) -> None:
     """Attention of every row's tree of drafted tokens (already appended) over the
     paged cache: a node sees the context and its own path. q, out: bf16
-    [N][Hq][D]; workspace: a byte tensor of paged_tree_attn_workspace(Hq, Hkv,
-    D)."""
+    [N][Hq][D]; workspace: a zeroed byte tensor of
+    paged_tree_attn_workspace(Hq, Hkv, D)."""
     try:
         N, Hq, D = q.shape
         Hkv = k_cache.shape[0]

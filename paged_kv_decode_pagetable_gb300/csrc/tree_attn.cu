@@ -24,10 +24,10 @@
 // Work: the units' tiles, one more place for each unit's start (2 and 3: 40 and 42 us for the
 // rollout batch, not 39), lie on one line, cut into equal shares for one persistent CTA an SM from
 // the lengths, on the device. A unit that is cut leaves its parts (O, reference and sum, fp32) in
-// the workspace and a second small kernel joins them in order, so results do not depend on timing
-// and no CTA waits for another. (Shares that begin at a unit's edge where that is near, to cut
-// fewer: 56 -> 71 us for 64 nodes at D = 512, 39 -> 42 for the rollout batch.) The line is planned
-// from row_start, ctx_lens and batch_idx before the prior kernel has ended.
+// the workspace, and whoever writes the last of them, or a second kernel, joins them in their
+// order: results do not depend on timing and no CTA waits for another. (Shares that begin at a unit's edge where that is
+// near, to cut fewer: 56 -> 71 us for 64 nodes at D = 512, 39 -> 42 for the rollout batch.) The
+// line is planned from row_start, ctx_lens and batch_idx before the prior kernel has ended.
 //   warps 0-7 (softmax): D <= 128 with 64 columns, two units at a time, four warps each, so that
 //     one unit's start and end overlap the other's tiles; else one unit, its columns in two
 //     halves. Warp w has the keys of TMEM lanes 32 (w % 4) ..: masks, weights, references, a
@@ -46,11 +46,11 @@
 // the loops kept as loops, the short waits, and one site of each product.
 //
 // Measured (6769 GB/s measured): 16 rows of 16k to 32k tokens, 8-node chains, 8 heads of 128,
-// 244 us, 0.98 of reading them; 64 rows of 100 to 1024 tokens, trees of 8, 39 us, 0.59: its start
+// 240 us, 0.99 of reading them; 64 rows of 100 to 1024 tokens, trees of 8, 37 us, 0.61: its start
 // (launch, plan, the rings' first fill) and its end (last tiles, join) are 6 us each; 64 rows of
-// 256 to 2048 tokens in a window of 512, trees of 16, one head of 256, 30 us, 0.19, and 16 rows
-// with trees of 64, one head of 512, 56 us, 0.14: they write and read as many bytes in parts as
-// in keys, and at D = 512 every 8 nodes read the keys again; one row of 41 tokens 8.4 us.
+// 256 to 2048 tokens in a window of 512, trees of 16, one head of 256, 31 us, 0.19, and 16 rows
+// with trees of 64, one head of 512, 57 us, 0.13: they write and read as many bytes in parts as
+// in keys, and at D = 512 every 8 nodes read the keys again; one row of 41 tokens 4.8 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -70,6 +70,10 @@ constexpr int kMaxCtas = 160;            // CTAs the workspace has room for
 constexpr float kLazyLog2 = 8.f;
 constexpr int kMostPlaces = 0x7fffffff;  // as many and more are reported, not computed
 constexpr float kUnset = 1e30f;          // stands for -reference of a column without one
+constexpr int kFan = 4;                  // parts that are joined at a time
+constexpr int kLevels = 4;               // of joins: 4^4 parts
+static_assert(kMaxCtas <= 256, "levels");
+constexpr size_t kArrivedBytes = sizeof(int) * kLevels * 2 * kMaxCtas;   // their counters
 constexpr int kJoinWarps = 8;            // of a joining CTA
 
 template <int D, int MOST>
@@ -80,6 +84,11 @@ struct Cfg {
   static constexpr int UNITS = D <= 128 && COLS == 64 ? 2 : 1;
   static constexpr int GROUPS = 2 / UNITS;              // groups of four softmax warps a unit
   static constexpr int HALF = COLS / GROUPS;            // columns of a softmax warp, at most
+  // Parts are joined by whoever is the last to write one; where units have two groups, by a second
+  // kernel. A row of 41 tokens 8.4 -> 4.8 us and the rollout batch 38.7 -> 37.4 by the last to
+  // write; but 30 -> 38 us for the window of 512 at D = 256 and 56 -> 61 at D = 512, where one
+  // CTA's few warps would read up to 128 KB a part.
+  static constexpr bool JOINS = UNITS == 2;
   static constexpr int SOFT = 8;                        // softmax warps of all units
   static constexpr int PROD = SOFT, PREP = SOFT + 1, MMA = SOFT + 2;
   static constexpr int THREADS = (SOFT + 2 + UNITS) * 32;
@@ -141,7 +150,8 @@ struct Small {
   float ref[COLS];                  // its reference, -inf: none yet
   float alpha[COLS];                // what a new one scales O and sums by; NaN: poisoned
   long long dst[COLS];              // its place in out, -1: none
-  float red[4][COLS];               // maxima of the four warps of a group
+  float red[kFan][COLS];            // maxima of the four warps of a group; parts' weights
+  int last[2];                      // whether a unit's part was the last of some to arrive
   int pages[2][16];
   int scan[12];
   uint64_t bars[48];
@@ -159,7 +169,8 @@ struct Args {
   const int32_t *table, *batch_idx, *ctx_lens, *row_start, *parents;
   __nv_bfloat16 *out;
   float *parts;
-  Cut *cuts;
+  int *arrived;   // [kLevels][2 kMaxCtas]
+  Cut *cuts;      // [kMaxCtas]
   int32_t *err;
   int n_slots, max_pages, page_size, log_page, n_pages, window, B, N, Hq, Hkv, G;
   int unit_tokens, box_nodes;   // nodes of a unit at most, and of a box of queries
@@ -454,7 +465,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
   const Part &p = line.p;
   // (what the prior kernel may write or read - caches, queries, workspace, output - from here on)
   pkv_wait_prior_grid();
-  if (tid == 0) a.cuts[cta].cols = 0;
+  if (!C::JOINS && tid == 0) a.cuts[cta].cols = 0;
 
   if (warp == C::PROD) {
     // ============================ producer ============================
@@ -783,6 +794,95 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
     const int mine = 32 * quad + lane;          // the column that this thread looks after
     int tiles = 0, segs = 0, seg = 0, g = 0;    // g: ring entries of the parts so far
     bool ok = true, gone = false;
+    // The parts of a unit are joined by fours: who is the last of four to write its own joins them
+    // into the first's place, goes on with four such, and writes the output in the end. In the
+    // parts' order whoever it is; nobody waits.
+    auto join = [&](int cols) {
+      const int first_cta = p.t0 == 0 ? cta : share_of(W, p.start + kStart, ctas);
+      const int parts = share_of(W, p.start + kStart + p.ntiles - 1, ctas) - first_cta + 1;
+      auto place = [&](int i) { return 2 * (first_cta + i) + (i == 0 ? 1 : 0); };
+      int i = cta - first_cta;
+#pragma unroll 1
+      for (int span = 1, level = 0; span < parts; span *= kFan, ++level) {
+        i -= i % (span * kFan);                       // the first of the four
+        const int n = min(kFan, (parts - i + span - 1) / span);
+        if (n == 1) continue;
+        __threadfence();
+        group_sync(sub);
+        if (mine == 0) {
+          int *count = a.arrived + level * 2 * kMaxCtas + place(i);
+          const int last = atomicAdd(count, 1) == n - 1;
+          if (last) *count = 0;                       // as it was
+          s.last[sub] = last;
+        }
+        group_sync(sub);
+        if (!s.last[sub]) return;
+        __threadfence();
+        const bool all = span * kFan >= parts;
+        auto rec = [&](int k) { return a.parts + place(i + k * span) * C::RECORD; };
+        float *to = rec(0);
+        // a thread a column: the parts' weights
+        float ref = -INFINITY, sum = 0.f;
+        if (mine < cols) {
+          float m[kFan];
+#pragma unroll
+          for (int k = 0; k < kFan; ++k) {
+            m[k] = k < n ? __ldcg(rec(k) + C::COLS * D + mine) : -INFINITY;
+            ref = fmaxf(ref, m[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < kFan; ++k) {
+            const float w = m[k] == -INFINITY ? 0.f : exp2f(m[k] - ref);
+            s.red[k][h0 + mine] = w;
+            if (k < n) sum = fmaf(w, __ldcg(rec(k) + C::COLS * (D + 1) + mine), sum);
+          }
+          s.alpha[h0 + mine] = 1.f / sum;
+        }
+        group_sync(sub);
+        constexpr int Q = D / 4, kAhead = 8;   // reads in flight
+#pragma unroll 1
+        for (int j0 = mine; j0 < cols * Q; j0 += kAhead * 128) {
+          float4 y[kAhead];
+#pragma unroll
+          for (int h = 0; h < kAhead; ++h) y[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int k = 0; k < n; ++k) {
+            const float *from = rec(k);
+            float4 v[kAhead];
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h)
+              if (j0 + h * 128 < cols * Q)
+                v[h] = __ldcg(reinterpret_cast<const float4 *>(from + (j0 + h * 128) * 4));
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h) {
+              if (j0 + h * 128 >= cols * Q) break;
+              const float w = s.red[k][h0 + (j0 + h * 128) / Q];
+              y[h].x = fmaf(w, v[h].x, y[h].x);
+              y[h].y = fmaf(w, v[h].y, y[h].y);
+              y[h].z = fmaf(w, v[h].z, y[h].z);
+              y[h].w = fmaf(w, v[h].w, y[h].w);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < kAhead; ++h) {
+            const int j = j0 + h * 128, c = j / Q;
+            if (j >= cols * Q) break;
+            if (all) {
+              const float f = s.alpha[h0 + c];
+              *reinterpret_cast<uint2 *>(a.out + s.dst[h0 + c] + j % Q * 4) =
+                  make_uint2(t_pack(y[h].x * f, y[h].y * f), t_pack(y[h].z * f, y[h].w * f));
+            } else {
+              __stcg(reinterpret_cast<float4 *>(to + j * 4), y[h]);
+            }
+          }
+        }
+        if (!all && mine < cols) {
+          __stcg(to + C::COLS * D + mine, ref);
+          __stcg(to + C::COLS * (D + 1) + mine, sum);
+        }
+        if (all) return;
+      }
+    };
     // A unit, or the part of it that is this CTA's. Loops over chunks of 16 columns stay loops:
     // unrolled, the warps waited for instructions a third of the time.
     auto unit = [&]() {
@@ -1069,7 +1169,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
           }
         }
       }
-      if (warp == 4 * x && lane == 0 && !whole && p.t0 == 0) {
+      if (!C::JOINS && tid == 0 && !whole && p.t0 == 0) {
         // the CTA of the unit's last tile
         const int c = share_of(W, p.start + kStart + p.ntiles - 1, ctas);
         const Cut cut = {p.n0 + p.tok0, cols, p.head, c - cta + 1};
@@ -1080,6 +1180,9 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
       if (lane == 0) {
         t_arrive(ofree(x));
         t_arrive(prepempty + 8 * (seg & 1));
+      }
+      if constexpr (C::JOINS) {
+        if (!whole && !group_any(sub, !ok)) join(cols);
       }
     };
     while (!gone && line.next()) {
@@ -1215,8 +1318,9 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
   const int box_nodes = a.G % 8 == 0 ? 1 : a.G % 4 == 0 ? 2 : a.G % 2 == 0 ? 4 : 8;
   a.unit_tokens = C::COLS / (box_nodes * a.G) * box_nodes;
   a.box_nodes = box_nodes;
-  a.cuts = static_cast<Cut *>(workspace);
-  a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + kMaxCtas * sizeof(Cut));
+  a.arrived = static_cast<int *>(workspace);
+  a.cuts = reinterpret_cast<Cut *>(static_cast<char *>(workspace) + kArrivedBytes);
+  a.parts = reinterpret_cast<float *>(a.cuts + kMaxCtas);
   CUtensorMap tmQ, tmK, tmV;
   const int rows = a.n_pages * a.page_size;
   const int k_box = a.page_size < kTile ? a.page_size : kTile;
@@ -1225,11 +1329,12 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
   if (st == PKV_OK) st = pkv::prefill_atoms_map(&tmK, k, a.Hkv, rows, D, k_box, 1, 1);
   if (st == PKV_OK) st = pkv::prefill_atoms_map(&tmV, v, a.Hkv, rows, D, v_box, 1, 1);
   if (st != PKV_OK) return st;
-  PKV_CUDA_CHECK(pkv::launch_pdl(tree_attn_kernel<D, MOST>, dim3(grid), dim3(C::THREADS), smem_bytes<C>(),
-                                 s, tmQ, tmK, tmV, a));
-  PKV_CUDA_CHECK(pkv::launch_pdl(tree_join_kernel<D, MOST>, dim3(grid, C::COLS / kJoinWarps),
-                                 dim3(kJoinWarps * 32), 0, s, static_cast<const float *>(a.parts),
-                                 static_cast<const Cut *>(a.cuts), a.out, a.Hq, a.G));
+  PKV_CUDA_CHECK(pkv::launch_pdl(tree_attn_kernel<D, MOST>, dim3(grid), dim3(C::THREADS),
+                                 smem_bytes<C>(), s, tmQ, tmK, tmV, a));
+  if constexpr (!C::JOINS)
+    PKV_CUDA_CHECK(pkv::launch_pdl(tree_join_kernel<D, MOST>, dim3(grid, C::COLS / kJoinWarps),
+                                   dim3(kJoinWarps * 32), 0, s, static_cast<const float *>(a.parts),
+                                   static_cast<const Cut *>(a.cuts), a.out, a.Hq, a.G));
   return pkv::ok();
 }
 
@@ -1253,7 +1358,7 @@ extern "C" size_t paged_tree_attn_workspace(int Hq, int Hkv, int D) {
   if ((D != 64 && D != 128 && D != 256 && D != 512) || Hkv < 1 || Hq < Hkv || Hq % Hkv ||
       Hq / Hkv > 8 || Hq > 65535)
     return 0;
-  return kMaxCtas * sizeof(Cut) + 2 * kMaxCtas * record_floats(D) * sizeof(float);
+  return kArrivedBytes + kMaxCtas * sizeof(Cut) + 2 * kMaxCtas * record_floats(D) * sizeof(float);
 }
 
 extern "C" int paged_tree_attn(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,

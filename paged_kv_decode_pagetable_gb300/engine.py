@@ -176,11 +176,16 @@ def decode_layer_step(spec: LayerSpec, pt: PageTable, k_cache, v_cache, q, k, v,
 # --------------------------------------------------------------------------
 
 class TreeWorkspace:
-    """Workspace of paged_tree_attn: sized by the heads alone, any contents."""
+    """Workspace of paged_tree_attn: sized by the heads alone, zeroed once."""
 
     def __init__(self, Hq, Hkv, D, device):
-        self.buf = torch.empty(paged_tree_attn_workspace(Hq, Hkv, D), dtype=torch.uint8,
+        self.buf = torch.zeros(paged_tree_attn_workspace(Hq, Hkv, D), dtype=torch.uint8,
                                device=device)
+
+    def reset(self):
+        """Zeroes it again (on the current stream), as after a call that reported
+        PKV_ERR_TIMEOUT."""
+        self.buf.zero_()
 
 
 def tree_layer_step(spec: LayerSpec, pt: PageTable, k_cache, v_cache, q, k, v, batch_idx, ctx_lens,

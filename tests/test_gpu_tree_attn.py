@@ -196,10 +196,26 @@ def test_results_do_not_depend_on_the_run():
     c = TreeCase(rng, 32, 8, 128, 64, rng.integers(100, 1500, 24),
                  [random_tree(rng, 8, 2) for _ in range(24)]).device(pkv)
     first = c.call(pkv).clone()
-    for i in range(30):
-        c.ws.fill_(i)
+    for _ in range(30):
         c.out.fill_(float("nan"))
         assert torch.equal(c.call(pkv), first)
+
+
+def test_one_workspace_serves_every_shape():
+    """Calls of all shapes in any order on one workspace: each finds its counts zero."""
+    rng = rng_of(22)
+    cases = [TreeCase(rng, Hq, Hkv, D, 64, ctx, [random_tree(rng, n, 2) for n in ns]).device(pkv)
+             for Hq, Hkv, D, ctx, ns in (
+                 (8, 1, 512, [20000], [6]), (32, 8, 128, [3000, 100, 900], [8, 4, 1]),
+                 (8, 1, 256, [7000, 2000], [30, 20]), (2, 2, 64, [9000], [3]),
+                 (8, 1, 128, [40000], [2]), (8, 8, 64, [700, 60], [64, 50]))]
+    want = [c.call(pkv).clone() for c in cases]
+    for c in cases:
+        c.check(pkv)
+    ws = torch.zeros(max(c.ws.nbytes for c in cases), dtype=torch.uint8, device="cuda")
+    for i in rng.integers(0, len(cases), 60):
+        assert torch.equal(cases[i].call(pkv, ws=ws, out=torch.full_like(cases[i].out, 7.0)),
+                           want[i]), i
 
 
 def test_cache_beyond_32_bits():

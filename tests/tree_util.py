@@ -67,7 +67,7 @@ class TreeCase:
                       table=i32(self.table), slots=i32(self.slots), ctx=i32(self.ctx),
                       row_start=i32(self.row_start), parents=i32(self.parents))
         n = pkv.paged_tree_attn_workspace(self.Hq, self.Hkv, self.D)
-        self.ws = torch.full((n,), 255, dtype=torch.uint8, device=dev)   # any contents
+        self.ws = torch.zeros(n, dtype=torch.uint8, device=dev)
         self.out = torch.full((self.N + self.pad, self.Hq, self.D), 7.0, dtype=torch.bfloat16,
                               device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
