@@ -152,7 +152,6 @@ struct Small {
   long long dst[COLS];              // its place in out, -1: none
   float red[kFan][COLS];            // maxima of the four warps of a group; parts' weights
   int last[2];                      // whether a unit's part was the last of some to arrive
-  int pages[2][16];
   int scan[12];
   uint64_t bars[48];
   uint32_t tmem;
@@ -472,56 +471,76 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
     const int k_rows = min(a.page_size, kTile);             // tokens of a K box
     const int v_rows = min(a.page_size, kTile / C::V_HALVES);
     const int per_tile = kTile / k_rows;         // pages of a tile (1 where they are larger)
+    const int v_split = per_tile == 1 ? C::V_HALVES : 1;   // V boxes of a page
     int g = 0;                                   // ring entries so far
     int bits = 0;
     bool ok = true;
-    // room in the next entry, and how many bytes will come
-    auto take = [&](int boxes, int rows) -> int {
-      const int e = g % C::NS;
-      if (g >= C::NS && !wait_for(empty + 8 * e, g / C::NS - 1)) {
-        ok = false;
-        return 0;
+    // Two entries at a time, and like the MMAs issued by one elected lane of a warp that goes
+    // through it as one: with a lane a page an entry took 500 cycles, 16 KB in 0.26 us at most.
+    constexpr int BT = C::E < 2 ? 1 : 2;
+    uint32_t entry[BT];
+    auto take = [&]() {
+#pragma unroll
+      for (int b = 0; b < BT; ++b, ++g) {
+        entry[b] = __shfl_sync(0xffffffffu, g % C::NS, 0);
+        if (g >= C::NS) ok = ok && wait_for(empty + 8 * entry[b], g / C::NS - 1);
       }
-      if (lane == 0) t_expect_tx(full + 8 * e, boxes * rows * 128);
-      __syncwarp();
-      ++g;
-      return e;
     };
-    // a K tile: 64 columns of all its pages [first, last) an entry
-    auto load_k = [&](int which, int head, int j0, int first, int last) {
-      const int in_page = j0 & (a.page_size - 1);   // (pages larger than a tile)
+    // a K tile: 64 columns of its boxes [first, last) an entry; lane i knows box i's row
+    auto load_k = [&](int at_row, int head, int first, int last) {
 #pragma unroll 1
-      for (int at = 0; at < C::E && ok; ++at) {
-        const int e = take(last - first, k_rows);
+      for (int at = 0; at < C::E; at += BT) {
+        take();
         if (!ok) break;
-        if (lane >= first && lane < last)
-          t_tma_4d(sRing + e * C::ENTRY + lane * k_rows * 128, &tmK, 0,
-                   s.pages[which][lane] * a.page_size + in_page, head, at, full + 8 * e);
-        __syncwarp();
+        if (elect_one()) {
+#pragma unroll
+          for (int b = 0; b < BT; ++b)
+            t_expect_tx(full + 8 * entry[b], (last - first) * k_rows * 128);
+        }
+#pragma unroll 1
+        for (int i = first; i < last; ++i) {
+          const int r = __shfl_sync(0xffffffffu, at_row, i);
+          if (elect_one()) {
+#pragma unroll
+            for (int b = 0; b < BT; ++b)
+              t_tma_4d(sRing + entry[b] * C::ENTRY + i * k_rows * 128, &tmK, 0, r, head, at + b,
+                       full + 8 * entry[b]);
+          }
+          __syncwarp();
+        }
       }
     };
-    // a V tile: 128 columns of half its keys an entry, two atoms a page
-    auto load_v = [&](int which, int head, int j0, int first, int last) {
-      const int in_page = j0 & (a.page_size - 1);
+    // a V tile: 128 columns of half its keys an entry, two atoms, in one box where a page has them
+    auto load_v = [&](int at_row, int head, int first, int last) {
       constexpr int AT = D == 64 ? 1 : 2;
-      const int per = kTile / C::V_HALVES / v_rows;   // pages of an entry
+      constexpr int KEYS = kTile / C::V_HALVES;       // of an entry
+      const int per = KEYS / v_rows;                  // boxes (or pairs of them) of an entry
+      const int step = v_rows == KEYS ? AT : 1;       // atoms of a box
 #pragma unroll 1
-      for (int c = 0; c < C::E && ok; ++c) {
-        const int half = c % C::V_HALVES, blk = c / C::V_HALVES;
-        // pages [p0, p0 + per) of the tile; one larger than an entry serves both halves
-        const int p0 = per_tile == 1 ? 0 : half * per;
-        const int lo = max(first, p0), hi = min(last, p0 + per);
-        const int e = take(max(0, hi - lo) * AT, v_rows);
+      for (int c = 0; c < C::E; c += BT) {
+        take();
         if (!ok) break;
-        const int pg = p0 + lane / AT, at = lane % AT;
-        if (pg >= lo && pg < hi)
-          t_tma_4d(sRing + e * C::ENTRY + at * (kTile / C::V_HALVES) * 128 +
-                       (pg - p0) * v_rows * 128,
-                   &tmV, 0,
-                   s.pages[which][pg] * a.page_size + in_page +
-                       (per_tile == 1 ? half * (kTile / C::V_HALVES) : 0),
-                   head, blk * AT + at, full + 8 * e);
-        __syncwarp();
+        if (elect_one()) {
+#pragma unroll
+          for (int b = 0; b < BT; ++b)
+            t_expect_tx(full + 8 * entry[b],
+                        (min(max(last - b * per, 0), per) - min(max(first - b * per, 0), per)) *
+                            AT * v_rows * 128);
+        }
+#pragma unroll 1
+        for (int i = first; i < last; ++i) {
+          const int r = __shfl_sync(0xffffffffu, at_row, i);
+          const int half = i >= per;
+          const uint32_t e = half ? entry[BT - 1] : entry[0];
+          const uint32_t to = sRing + e * C::ENTRY + (i - half * per) * v_rows * 128;
+          if (elect_one()) {
+#pragma unroll 1
+            for (int at = 0; at < AT; at += step)
+              t_tma_4d(to + at * KEYS * 128, &tmV, 0, r, head, c / C::V_HALVES * AT + at,
+                       full + 8 * e);
+          }
+          __syncwarp();
+        }
       }
     };
     while (ok && line.next()) {
@@ -535,32 +554,36 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
       };
       int base = ((p.tile0 + p.t0) * kTile) >> a.log_page;
       int now = fetch(base + lane), then = fetch(base + 32 + lane);
-      int kf = 0, kl = 0;      // pages of the last K tile that are there
+      const int head = __shfl_sync(0xffffffffu, p.head, 0);
+      int vf = 0, vl = 0, v_at = 0;   // of V, a tile behind: its boxes, this lane's one's row
 #pragma unroll 1
       for (int t = p.t0; t <= p.t1 && ok; ++t) {
-        const int pf = kf, pl = kl;
+        int kf = 0, kl = 0, page = 0;
+        const int j0 = (p.tile0 + t) * kTile;
+        const int in_page = j0 & (a.page_size - 1);   // (pages larger than a tile)
         if (t < p.t1) {
-          const int j0 = (p.tile0 + t) * kTile;
           const int page0 = j0 >> a.log_page;
           if (page0 >= base + 32) {
             base += 32;
             now = then;
             then = fetch(base + 32 + lane);
           }
-          kf = max(0, first_page - page0);
-          kl = min(per_tile, last_page - page0 + 1);
-          int page = __shfl_sync(0xffffffffu, now, (page0 - base + lane) & 31);
+          kf = __shfl_sync(0xffffffffu, max(0, first_page - page0), 0);
+          kl = __shfl_sync(0xffffffffu, min(per_tile, last_page - page0 + 1), 0);
+          page = __shfl_sync(0xffffffffu, now, (page0 - base + lane) & 31);
           if (lane >= kf && lane < kl) {
             if (page < 0 || page >= a.n_pages) {
               bits |= page < 0 ? PKV_ERR_PAGE_NEG : PKV_ERR_PAGE_RANGE;
               page = 0;
             }
-            s.pages[t & 1][lane] = page;
           }
-          __syncwarp();
-          load_k(t & 1, p.head, j0, kf, kl);
+          load_k(page * a.page_size + in_page, head, kf, kl);
         }
-        if (t > p.t0 && ok) load_v((t - 1) & 1, p.head, (p.tile0 + t - 1) * kTile, pf, pl);
+        if (t > p.t0 && ok) load_v(v_at, head, vf, vl);
+        vf = kf * v_split;
+        vl = kl * v_split;
+        v_at = __shfl_sync(0xffffffffu, page, lane / v_split) * a.page_size + in_page +
+               lane % v_split * (kTile / C::V_HALVES);
       }
     }
     tree_report(a.err, bits);
@@ -1327,7 +1350,9 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
   const int v_box = a.page_size < kTile / C::V_HALVES ? a.page_size : kTile / C::V_HALVES;
   int st = pkv::prefill_atoms_map(&tmQ, q, a.N, a.Hq, D, a.G, box_nodes, 1);
   if (st == PKV_OK) st = pkv::prefill_atoms_map(&tmK, k, a.Hkv, rows, D, k_box, 1, 1);
-  if (st == PKV_OK) st = pkv::prefill_atoms_map(&tmV, v, a.Hkv, rows, D, v_box, 1, 1);
+  // (two atoms of V in a box where its keys fill an entry)
+  const int v_atoms = D > 64 && v_box == kTile / C::V_HALVES ? 2 : 1;
+  if (st == PKV_OK) st = pkv::prefill_atoms_map(&tmV, v, a.Hkv, rows, D, v_box, 1, v_atoms);
   if (st != PKV_OK) return st;
   PKV_CUDA_CHECK(pkv::launch_pdl(tree_attn_kernel<D, MOST>, dim3(grid), dim3(C::THREADS),
                                  smem_bytes<C>(), s, tmQ, tmK, tmV, a));
