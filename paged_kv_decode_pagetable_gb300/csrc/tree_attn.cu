@@ -90,22 +90,21 @@ struct Cfg {
   // CTA's few warps would read up to 128 KB a part.
   static constexpr bool JOINS = UNITS == 2;
   static constexpr int SOFT = 8;                        // softmax warps of all units
-  static constexpr int PROD = SOFT, PREP = SOFT + 1, MMA = SOFT + 2;
-  static constexpr int THREADS = (SOFT + 2 + UNITS) * 32;
-  // A ring entry: 64 columns of D of a K tile, or 64 keys' 128 columns of a V tile (two atoms
-  // of 64 columns; D = 64: all its keys).
-  static constexpr int ENTRY = kTile * 128;             // bytes
-  static constexpr int E = D / 64;                      // entries of a K tile, and of a V tile
-  static constexpr int BLOCKS = D <= 128 ? 1 : D / 128; // blocks of 128 rows of O^T
-  static constexpr int V_HALVES = D == 64 ? 1 : 2;      // entries of a V tile's block
-  // as many as shared memory holds
-  static constexpr int NS = D == 512                ? 8
-                            : D == 256              ? (COLS == 128 ? 6 : 9)
-                            : D == 128              ? (COLS == 128 ? 8 : 9)
-                            : COLS == 128           ? 9
-                                                    : 10;
+  static constexpr int PROD = SOFT, PREP = SOFT + 2, MMA = SOFT + 3;
+  static constexpr int THREADS = (SOFT + 5) * 32;
+  // A ring entry: 128 columns of D of a K tile in two atoms of 64, or of a V tile, in halves of 64
+  // keys with two atoms each. (D = 64: an atom, all its keys.)
+  static constexpr int ATOM = kTile * 128, ATOMS = D == 64 ? 1 : 2;   // bytes of 64 columns
+  static constexpr int ENTRY = ATOMS * ATOM;
+  static constexpr int E = D == 64 ? 1 : D / 128;       // entries of a K tile, and of a V tile
+  static constexpr int KEYS = kTile / ATOMS;            // of a half of V, one after the other
+  // as many as shared memory holds, in a ring for K and one for V
+  static constexpr int NS = D == 64                   ? (COLS == 128 ? 9 : 10)
+                            : D == 256 && COLS == 128 ? 3
+                                                      : 4;
+  static constexpr int NK = NS / 2, NV = NS - NK;
   static constexpr int Q_ATOM = COLS * 128;
-  static constexpr int Q_BYTES = E * Q_ATOM;
+  static constexpr int Q_BYTES = D / 64 * Q_ATOM;
   static constexpr int P_ATOM = kTile * 128;            // 64 columns of every key
   static constexpr int P_BYTES = COLS / 64 * P_ATOM;
   static constexpr int OFF_Q = NS * ENTRY;              // [UNITS]
@@ -115,7 +114,7 @@ struct Cfg {
   // of a unit: S of two tiles (of one where TMEM has no room), O^T's blocks, the sums of the
   // weights (in every lane)
   static constexpr int SB = D == 256 && COLS == 128 ? 1 : 2;
-  static constexpr int S_COL = 0, O_COL = SB * COLS, L_COL = O_COL + BLOCKS * COLS;
+  static constexpr int S_COL = 0, O_COL = SB * COLS, L_COL = O_COL + E * COLS;
   static constexpr int UNIT_COLS = 512 / UNITS;
   static_assert(L_COL + COLS <= UNIT_COLS, "TMEM");
   static constexpr size_t RECORD = static_cast<size_t>(COLS) * (D + 2);   // floats of a part
@@ -152,7 +151,7 @@ struct Small {
   long long dst[COLS];              // its place in out, -1: none
   float red[kFan][COLS];            // maxima of the four warps of a group; parts' weights
   int last[2];                      // whether a unit's part was the last of some to arrive
-  int scan[12];
+  int scan[16];
   uint64_t bars[48];
   uint32_t tmem;
   Rows rows;
@@ -351,10 +350,10 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
                  sOnes = t_smem(sm + C::OFF_ONES);
   const uint32_t bars = t_smem(s.bars);
   constexpr int U = C::UNITS;
-  // the ring's, then unit x's (S buffer b, preparation b)
+  // the rings', then unit x's (S buffer b, preparation b)
   const uint32_t full = bars, empty = full + 8 * C::NS, drain = empty + 8 * C::NS,
-                 prepfull = drain + 8 * U, prepempty = prepfull + 16, unit0 = prepempty + 16;
-  constexpr int UB = 10;
+                 prepfull = drain + 16, prepempty = prepfull + 16, unit0 = prepempty + 16;
+  constexpr int UB = 9 + 2 * C::E;
   auto sfull = [&](int x, int b) { return unit0 + 8 * (UB * x + b); };
   auto sfree = [&](int x, int b) { return unit0 + 8 * (UB * x + 2 + b); };
   auto pfull = [&](int x) { return unit0 + 8 * (UB * x + 4); };
@@ -362,9 +361,16 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
   auto ofree = [&](int x) { return unit0 + 8 * (UB * x + 6); };
   auto qfull = [&](int x) { return unit0 + 8 * (UB * x + 7); };
   auto qempty = [&](int x) { return unit0 + 8 * (UB * x + 8); };
-  auto turn = [&](int x) { return unit0 + 8 * (UB * x + 9); };
-  static_assert(2 * C::NS + 4 + U + U * UB <= 48, "barriers");
+  // of a masked tile, block by block of 128 columns of V: it is there, it is clean
+  auto vthere = [&](int x, int blk) { return unit0 + 8 * (UB * x + 9 + blk); };
+  auto vclean = [&](int x, int blk) { return unit0 + 8 * (UB * x + 9 + C::E + blk); };
+  static_assert(2 * C::NS + 6 + U * UB <= 48, "barriers");
 
+  if (tid == 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmQ)));
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmK)));
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmV)));
+  }
   if (tid == 0) {
 #pragma unroll 1
     for (int i = 0; i < C::NS; ++i) {
@@ -373,6 +379,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
     }
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
+      t_bar_init(drain + 8 * i, 1);
       t_bar_init(prepfull + 8 * i, 1);
       t_bar_init(prepempty + 8 * i, C::SOFT / U);
     }
@@ -387,8 +394,10 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
       t_bar_init(ofree(x), C::SOFT / U);
       t_bar_init(qfull(x), 1);
       t_bar_init(qempty(x), 1);
-      t_bar_init(turn(x), 1);
-      t_bar_init(drain + 8 * x, 1);
+      for (int b = 0; b < C::E; ++b) {
+        t_bar_init(vthere(x, b), 1);
+        t_bar_init(vclean(x, b), C::SOFT / U);
+      }
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -466,78 +475,66 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
   pkv_wait_prior_grid();
   if (!C::JOINS && tid == 0) a.cuts[cta].cols = 0;
 
-  if (warp == C::PROD) {
-    // ============================ producer ============================
+  // whether some columns do not see some keys of the unit's tile t
+  auto is_masked = [&](int t) {
+    const int j0 = (p.tile0 + t) * kTile;
+    return j0 + kTile > p.ctx || (a.window > 0 && j0 <= p.ctx + p.n - 1 - a.window);
+  };
+  if (warp == C::PROD || warp == C::PROD + 1) {
+    // ==================== producers, of K and of V ====================
+    const bool is_v = warp != C::PROD;
+    const int slots = is_v ? C::NV : C::NK, slot0 = is_v ? C::NK : 0;
     const int k_rows = min(a.page_size, kTile);             // tokens of a K box
-    const int v_rows = min(a.page_size, kTile / C::V_HALVES);
+    const int v_rows = min(a.page_size, C::KEYS);
     const int per_tile = kTile / k_rows;         // pages of a tile (1 where they are larger)
-    const int v_split = per_tile == 1 ? C::V_HALVES : 1;   // V boxes of a page
-    int g = 0;                                   // ring entries so far
+    const int split = is_v && per_tile == 1 ? C::ATOMS : 1;   // boxes of a page
+    int at = 0, round = 0;                       // the next entry, how often the ring has been full
     int bits = 0;
     bool ok = true;
-    // Two entries at a time, and like the MMAs issued by one elected lane of a warp that goes
-    // through it as one: with a lane a page an entry took 500 cycles, 16 KB in 0.26 us at most.
-    constexpr int BT = C::E < 2 ? 1 : 2;
-    uint32_t entry[BT];
-    auto take = [&]() {
-#pragma unroll
-      for (int b = 0; b < BT; ++b, ++g) {
-        entry[b] = __shfl_sync(0xffffffffu, g % C::NS, 0);
-        if (g >= C::NS) ok = ok && wait_for(empty + 8 * entry[b], g / C::NS - 1);
-      }
+    // an entry of so many bytes; its number
+    auto take = [&](int bytes) -> uint32_t {
+      const uint32_t e = __shfl_sync(0xffffffffu, slot0 + at, 0);
+      if (round > 0) ok = wait_for(empty + 8 * e, round - 1);
+      if (ok && elect_one()) t_expect_tx(full + 8 * e, bytes);
+      if (++at == slots) at = 0, ++round;
+      return e;
     };
-    // a K tile: 64 columns of its boxes [first, last) an entry; lane i knows box i's row
+    // a K tile's boxes [first, last); lane i knows box i's row
     auto load_k = [&](int at_row, int head, int first, int last) {
 #pragma unroll 1
-      for (int at = 0; at < C::E; at += BT) {
-        take();
+      for (int c = 0; c < C::E; ++c) {
+        const uint32_t e = take((last - first) * C::ATOMS * k_rows * 128);
         if (!ok) break;
-        if (elect_one()) {
-#pragma unroll
-          for (int b = 0; b < BT; ++b)
-            t_expect_tx(full + 8 * entry[b], (last - first) * k_rows * 128);
-        }
 #pragma unroll 1
         for (int i = first; i < last; ++i) {
           const int r = __shfl_sync(0xffffffffu, at_row, i);
           if (elect_one()) {
 #pragma unroll
-            for (int b = 0; b < BT; ++b)
-              t_tma_4d(sRing + entry[b] * C::ENTRY + i * k_rows * 128, &tmK, 0, r, head, at + b,
-                       full + 8 * entry[b]);
+            for (int b = 0; b < C::ATOMS; ++b)
+              t_tma_4d(sRing + e * C::ENTRY + b * C::ATOM + i * k_rows * 128, &tmK, 0, r, head,
+                       C::ATOMS * c + b, full + 8 * e);
           }
           __syncwarp();
         }
       }
     };
-    // a V tile: 128 columns of half its keys an entry, two atoms, in one box where a page has them
+    // a V tile's; a box has two atoms where its keys are a half's
     auto load_v = [&](int at_row, int head, int first, int last) {
-      constexpr int AT = D == 64 ? 1 : 2;
-      constexpr int KEYS = kTile / C::V_HALVES;       // of an entry
-      const int per = KEYS / v_rows;                  // boxes (or pairs of them) of an entry
-      const int step = v_rows == KEYS ? AT : 1;       // atoms of a box
+      const int per = C::KEYS / v_rows;               // boxes (or pairs of them) of a half
+      const int step = v_rows == C::KEYS ? C::ATOMS : 1;   // atoms of a box
 #pragma unroll 1
-      for (int c = 0; c < C::E; c += BT) {
-        take();
+      for (int c = 0; c < C::E; ++c) {
+        const uint32_t e = take((last - first) * C::ATOMS * v_rows * 128);
         if (!ok) break;
-        if (elect_one()) {
-#pragma unroll
-          for (int b = 0; b < BT; ++b)
-            t_expect_tx(full + 8 * entry[b],
-                        (min(max(last - b * per, 0), per) - min(max(first - b * per, 0), per)) *
-                            AT * v_rows * 128);
-        }
 #pragma unroll 1
         for (int i = first; i < last; ++i) {
           const int r = __shfl_sync(0xffffffffu, at_row, i);
           const int half = i >= per;
-          const uint32_t e = half ? entry[BT - 1] : entry[0];
-          const uint32_t to = sRing + e * C::ENTRY + (i - half * per) * v_rows * 128;
+          const uint32_t to = sRing + e * C::ENTRY + half * C::ATOM + (i - half * per) * v_rows * 128;
           if (elect_one()) {
 #pragma unroll 1
-            for (int at = 0; at < AT; at += step)
-              t_tma_4d(to + at * KEYS * 128, &tmV, 0, r, head, c / C::V_HALVES * AT + at,
-                       full + 8 * e);
+            for (int b = 0; b < C::ATOMS; b += step)
+              t_tma_4d(to + b * C::KEYS * 128, &tmV, 0, r, head, C::ATOMS * c + b, full + 8 * e);
           }
           __syncwarp();
         }
@@ -548,167 +545,173 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
       const int32_t *row = a.table + static_cast<long long>(rows.slot[p.b]) * a.max_pages;
       const int last_page = (p.ctx + p.n - 1) >> a.log_page;
       const int first_page = p.lo >> a.log_page;
+      const int head = __shfl_sync(0xffffffffu, p.head, 0);
       // page numbers 32 at a time, the next ones on their way
       auto fetch = [&](int i) -> int {
         return i >= first_page && i <= last_page ? row[i] : 0;
       };
       int base = ((p.tile0 + p.t0) * kTile) >> a.log_page;
       int now = fetch(base + lane), then = fetch(base + 32 + lane);
-      const int head = __shfl_sync(0xffffffffu, p.head, 0);
-      int vf = 0, vl = 0, v_at = 0;   // of V, a tile behind: its boxes, this lane's one's row
 #pragma unroll 1
-      for (int t = p.t0; t <= p.t1 && ok; ++t) {
-        int kf = 0, kl = 0, page = 0;
-        const int j0 = (p.tile0 + t) * kTile;
-        const int in_page = j0 & (a.page_size - 1);   // (pages larger than a tile)
-        if (t < p.t1) {
-          const int page0 = j0 >> a.log_page;
-          if (page0 >= base + 32) {
-            base += 32;
-            now = then;
-            then = fetch(base + 32 + lane);
-          }
-          kf = __shfl_sync(0xffffffffu, max(0, first_page - page0), 0);
-          kl = __shfl_sync(0xffffffffu, min(per_tile, last_page - page0 + 1), 0);
-          page = __shfl_sync(0xffffffffu, now, (page0 - base + lane) & 31);
-          if (lane >= kf && lane < kl) {
-            if (page < 0 || page >= a.n_pages) {
-              bits |= page < 0 ? PKV_ERR_PAGE_NEG : PKV_ERR_PAGE_RANGE;
-              page = 0;
-            }
-          }
-          load_k(page * a.page_size + in_page, head, kf, kl);
+      for (int t = p.t0; t < p.t1 && ok; ++t) {
+        const int j0 = (p.tile0 + t) * kTile, page0 = j0 >> a.log_page;
+        if (page0 >= base + 32) {
+          base += 32;
+          now = then;
+          then = fetch(base + 32 + lane);
         }
-        if (t > p.t0 && ok) load_v(v_at, head, vf, vl);
-        vf = kf * v_split;
-        vl = kl * v_split;
-        v_at = __shfl_sync(0xffffffffu, page, lane / v_split) * a.page_size + in_page +
-               lane % v_split * (kTile / C::V_HALVES);
+        // boxes [first, last), and lane i knows box i's row
+        const int first = __shfl_sync(0xffffffffu, max(0, first_page - page0) * split, 0);
+        const int last =
+            __shfl_sync(0xffffffffu, min(per_tile, last_page - page0 + 1) * split, 0);
+        int page = __shfl_sync(0xffffffffu, now, (page0 - base + lane / split) & 31);
+        if (lane >= first && lane < last && (page < 0 || page >= a.n_pages)) {
+          bits |= page < 0 ? PKV_ERR_PAGE_NEG : PKV_ERR_PAGE_RANGE;
+          page = 0;
+        }
+        const int at_row = page * a.page_size + (j0 & (a.page_size - 1)) +   // (large pages)
+                           lane % split * C::KEYS;
+        if (is_v) load_v(at_row, head, first, last);
+        else load_k(at_row, head, first, last);
       }
     }
     tree_report(a.err, bits);
     if (!ok) {
       // what is on its way lands before the CTA leaves
 #pragma unroll 1
-      for (int i = max(0, g - C::NS); i < g; ++i) {
+      for (int i = 0; i < slots; ++i) {
+        const int fills = round + (i < at ? 1 : 0);
 #pragma unroll 1
-        for (int k = 0; k < kSpin && !t_test(full + 8 * (i % C::NS), i / C::NS); ++k) {
+        for (int k = 0; k < kSpin && fills && !t_test(full + 8 * (slot0 + i), fills - 1); ++k) {
         }
       }
     }
   } else if (warp >= C::MMA) {
-    // ============================== MMA ===============================
-    // The whole warp goes through the steps and one elected lane issues: so the compiler knows
-    // that descriptors and addresses are the warp's, and an MMA takes 42 to 50 cycles (its A
-    // operand's way from shared memory). Issued under a lane's own branch it took 90 to 150.
-    const int x = warp - C::MMA;     // this warp's units: every U-th
-    int g = 0, tiles = 0, segs = 0, own = 0;
+    // ==================== MMA: a warp for S, one for P V ====================
+    // Of two products one is issued while the other's warp waits: 16 rows with trees of 64, one
+    // head of 512 WIDE us, with one warp for both 57. The whole warp goes through the steps and
+    // one elected lane issues: so the compiler knows that descriptors and addresses are the
+    // warp's, and an MMA takes 42 to 50 cycles (its A operand's way from shared memory). Issued
+    // under a lane's own branch it took 90 to 150.
+    const bool is_pv = warp != C::MMA;
+    const int slots = is_pv ? C::NV : C::NK, slot0 = is_pv ? C::NK : 0;
+    int at = 0, round = 0;                  // as the producers'
+    int segs = 0, done[2] = {0, 0}, masked[2] = {0, 0};   // tiles of each unit, masked ones
     bool ok = true;
-    const uint32_t tx = __shfl_sync(0xffffffffu, tmem + x * C::UNIT_COLS, 0);
-    const uint64_t dQ = t_desc(sQ + x * C::Q_BYTES, 16, 1024);
-    const uint64_t dP = t_desc(sP + x * C::P_BYTES, C::P_ATOM, 1024), dOne = t_desc(sOnes, 0, 0);
-    // the next BT ring entries, once they are there: waits, fences and elections cost more than
-    // issuing the MMAs of one
-    constexpr int BT = C::E < 2 ? 1 : 2;
-    uint32_t entry[BT];
-    auto take = [&]() {
-#pragma unroll
-      for (int b = 0; b < BT; ++b, ++g) {
-        entry[b] = __shfl_sync(0xffffffffu, g % C::NS, 0);
-        ok = ok && wait_for(full + 8 * entry[b], g / C::NS);
-      }
+    // the next entry, once it is there
+    auto take = [&]() -> uint32_t {
+      const uint32_t e = __shfl_sync(0xffffffffu, slot0 + at, 0);
+      ok = ok && wait_for(full + 8 * e, round);
+      if (++at == slots) at = 0, ++round;
       t_fence_after();
+      return e;
     };
-    // P V of a tile, and the weights' sums: a row of ones, 128 times
-    auto do_pv = [&](uint32_t id, int pv, bool first, bool last) {
-      if (U == 2 && last) {   // the unit's last entries: the other unit's turn
-#pragma unroll 1
-        for (int c = 0; c < C::E; ++c)
-          ok = ok && wait_for(full + 8 * ((g + c) % C::NS), (g + c) / C::NS);
-        if (ok && lane == 0) t_arrive(turn(x ^ 1));
-      }
-      ok = ok && wait_for(pfull(x), pv);
-      if (first && own >= 1) ok = ok && wait_for(ofree(x), own - 1);
-      const uint32_t add = !first;
-      t_fence_after();
-      if (ok && elect_one()) {   // (they need no V, which may be on its way)
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          t_mma(tx + C::L_COL, dOne, dP + k * (2048 >> 4), id, k > 0 ? 1u : add);
-      }
-      __syncwarp();
-#pragma unroll 1
-      for (int c = 0; c < C::E && ok; c += BT) {
-        take();
-        if (!ok) break;
-        const uint32_t to = tx + C::O_COL + c / C::V_HALVES * C::COLS;
-        if (elect_one()) {
-#pragma unroll
-          for (int b = 0; b < BT; ++b) {
-            // (D = 64: rows 64 .. 127 of the product repeat rows 0 .. 63)
-            const uint64_t va =
-                t_desc(sRing + entry[b] * C::ENTRY, D == 64 ? 0 : kTile / 2 * 128, 1024);
-            const uint64_t pb = dP + b * (kTile / 2 * 128 >> 4);
-#pragma unroll
-            for (int k = 0; k < kTile / C::V_HALVES / 16; ++k)
-              t_mma(to, va + k * (2048 >> 4), pb + k * (2048 >> 4), id, b > 0 || k > 0 ? 1u : add);
-            t_commit(empty + 8 * entry[b]);
-          }
-          if (c + BT == C::E) t_commit(pvdone(x));
-        }
-        __syncwarp();
-      }
-    };
+    const uint64_t dOne = t_desc(sOnes, 0, 0);
     while (ok && line.next()) {
       if (p.t0 == p.t1) continue;
-      const int seg = segs++;
-      if (seg % U != x) {
-        g += 2 * (p.t1 - p.t0) * C::E;
-        continue;
-      }
-      // An entry's phase is told from the one before only. So a unit begins when all entries
-      // before its own have landed, which the other unit's warp has seen.
-      if (U == 2 && seg > 0 && !wait_for(turn(x), (seg - 1) / 2)) break;
+      const int x = __shfl_sync(0xffffffffu, segs % U, 0), own = segs / U;
+      ++segs;
       const int N = __shfl_sync(0xffffffffu, columns<C::GROUPS>(p.toks * a.G), 0);
-      const uint32_t idS = idesc(N, false), idO = idesc(N, true);
-      if (!wait_for(qfull(x), own)) break;
+      const uint32_t tx = __shfl_sync(0xffffffffu, tmem + x * C::UNIT_COLS, 0);
+      int tiles = x ? done[1] : done[0];
+      if (!is_pv) {
+        const uint64_t dQ = t_desc(sQ + x * C::Q_BYTES, 16, 1024);
+        const uint32_t id = idesc(N, false);
+        ok = wait_for(qfull(x), own);
 #pragma unroll 1
-      for (int t = p.t0; t <= p.t1 && ok; ++t) {
-        if (t < p.t1) {
+        for (int t = p.t0; t < p.t1 && ok; ++t, ++tiles) {
           const int buf = tiles % C::SB;
           if (tiles >= C::SB) ok = wait_for(sfree(x, buf), tiles / C::SB - 1);
           const uint32_t to = __shfl_sync(0xffffffffu, tx + C::S_COL + buf * C::COLS, 0);
 #pragma unroll 1
-          for (int c = 0; c < C::E && ok; c += BT) {
-            take();
+          for (int c = 0; c < C::E && ok; ++c) {
+            const uint32_t e = take();
             if (!ok) break;
             if (elect_one()) {
 #pragma unroll
-              for (int b = 0; b < BT; ++b) {
-                const uint64_t ka = t_desc(sRing + entry[b] * C::ENTRY, 16, 1024);
-                const uint64_t qb = dQ + (c + b) * (C::Q_ATOM >> 4);
+              for (int b = 0; b < C::ATOMS; ++b) {
+                const uint64_t ka = t_desc(sRing + e * C::ENTRY + b * C::ATOM, 16, 1024);
+                const uint64_t qb = dQ + (C::ATOMS * c + b) * (C::Q_ATOM >> 4);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  t_mma(to, ka + k * 2, qb + k * 2, idS, c > 0 || b > 0 || k > 0);
-                t_commit(empty + 8 * entry[b]);
+                  t_mma(to, ka + k * 2, qb + k * 2, id, c > 0 || b > 0 || k > 0);
               }
-              if (c + BT == C::E) {
+              t_commit(empty + 8 * e);
+              if (c + 1 == C::E) {
                 t_commit(sfull(x, buf));
                 if (t == p.t1 - 1) t_commit(qempty(x));
               }
             }
             __syncwarp();
           }
-          ++tiles;
         }
-        if (t > p.t0 && ok)
-          do_pv(idO, tiles - (t < p.t1 ? 2 : 1), t == p.t0 + 1, t == p.t1);
+      } else {
+        const uint64_t dP = t_desc(sP + x * C::P_BYTES, C::P_ATOM, 1024);
+        const uint32_t id = idesc(N, true);
+        int masks = x ? masked[1] : masked[0];
+#pragma unroll 1
+        for (int t = p.t0; t < p.t1 && ok; ++t, ++tiles) {
+          const bool mask = is_masked(t);
+          ok = wait_for(pfull(x), tiles);
+          if (t == p.t0 && own >= 1) ok = ok && wait_for(ofree(x), own - 1);
+          const uint32_t add = t > p.t0;
+          bool ahead = false;
+          uint32_t next = 0;
+          t_fence_after();
+          // the weights' sums: a row of ones, 128 times (they need no V, which may be on its way)
+          if (ok && elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              t_mma(tx + C::L_COL, dOne, dP + k * (2048 >> 4), id, k > 0 ? 1u : add);
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int c = 0; c < C::E && ok; ++c) {
+            if (!ahead) {
+              next = take();
+              if (ok && mask && lane == 0) t_arrive(vthere(x, c));
+            }
+            const uint32_t e = next;
+            // (while a block is looked at, the next one comes)
+            ahead = mask && C::NV >= 2 && c + 1 < C::E;
+            if (ahead) {
+              next = take();
+              if (ok && lane == 0) t_arrive(vthere(x, c + 1));
+            }
+            if (mask) {
+              ok = ok && wait_for(vclean(x, c), masks);
+              t_fence_after();
+            }
+            if (!ok) break;
+            const uint32_t to = tx + C::O_COL + c * C::COLS;
+            if (elect_one()) {
+#pragma unroll
+              for (int b = 0; b < C::ATOMS; ++b) {
+                // (D = 64: rows 64 .. 127 of the product repeat rows 0 .. 63)
+                const uint64_t va = t_desc(sRing + e * C::ENTRY + b * C::ATOM,
+                                           D == 64 ? 0 : C::KEYS * 128, 1024);
+                const uint64_t pb = dP + b * (C::KEYS * 128 >> 4);
+#pragma unroll
+                for (int k = 0; k < C::KEYS / 16; ++k)
+                  t_mma(to, va + k * (2048 >> 4), pb + k * (2048 >> 4), id,
+                        b > 0 || k > 0 ? 1u : add);
+              }
+              t_commit(empty + 8 * e);
+              if (c + 1 == C::E) t_commit(pvdone(x));
+            }
+            __syncwarp();
+          }
+          masks += mask;
+        }
+        if (x) masked[1] = masks;
+        else masked[0] = masks;
       }
-      ++own;
+      if (x) done[1] = tiles;
+      else done[0] = tiles;
     }
     if (elect_one()) {
-      t_commit(drain + 8 * x);
-      t_wait_drain(drain + 8 * x);
+      t_commit(drain + 8 * is_pv);
+      t_wait_drain(drain + 8 * is_pv);
     }
     __syncwarp();
   } else if (warp == C::PREP) {
@@ -719,16 +722,19 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
       if (p.t0 == p.t1) continue;
       const int x = segs % U;
       if (segs >= U && !wait_for(qempty(x), segs / U - 1)) break;
-      if (lane == 0) {
-        const int boxes = (p.toks + a.box_nodes - 1) / a.box_nodes;
+      const int boxes = __shfl_sync(0xffffffffu, (p.toks + a.box_nodes - 1) / a.box_nodes, 0);
+      const int head = __shfl_sync(0xffffffffu, p.head * a.G, 0);
+      const int node = __shfl_sync(0xffffffffu, p.n0 + p.tok0, 0);
+      if (elect_one()) {
         t_expect_tx(qfull(x), boxes * box * (D / 64));
 #pragma unroll 1
         for (int i = 0; i < boxes; ++i)
 #pragma unroll 1
           for (int at = 0; at < D / 64; ++at)
-            t_tma_4d(sQ + x * C::Q_BYTES + at * C::Q_ATOM + i * box, &tmQ, 0, p.head * a.G,
-                     p.n0 + p.tok0 + a.box_nodes * i, at, qfull(x));
+            t_tma_4d(sQ + x * C::Q_BYTES + at * C::Q_ATOM + i * box, &tmQ, 0, head,
+                     node + a.box_nodes * i, at, qfull(x));
       }
+      __syncwarp();
       Prep<C::GROUPS> &w = s.prep[segs & 1];
       if (segs >= 2 && !wait_for(prepempty + 8 * (segs & 1), (segs >> 1) - 1)) break;
       // paths: each node's set of ancestors and itself, twice as far every time
@@ -815,7 +821,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
     const int h0 = sub * C::HALF;               // where the warps' columns are in shared memory
     uint8_t *pbuf = sm + C::OFF_P + x * C::P_BYTES + row * 128;   // this key's row of P
     const int mine = 32 * quad + lane;          // the column that this thread looks after
-    int tiles = 0, segs = 0, seg = 0, g = 0;    // g: ring entries of the parts so far
+    int tiles = 0, segs = 0, seg = 0, masks = 0, g = 0;   // g: where in V's ring
     bool ok = true, gone = false;
     // The parts of a unit are joined by fours: who is the last of four to write its own joins them
     // into the first's place, goes on with four such, and writes the output in the end. In the
@@ -862,7 +868,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
           s.alpha[h0 + mine] = 1.f / sum;
         }
         group_sync(sub);
-        constexpr int Q = D / 4, kAhead = 8;   // reads in flight
+        constexpr int Q = D / 4, kAhead = 4;   // reads in flight
 #pragma unroll 1
         for (int j0 = mine; j0 < cols * Q; j0 += kAhead * 128) {
           float4 y[kAhead];
@@ -912,7 +918,6 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
       const int cols = p.toks * a.G;
       const int hn = columns<C::GROUPS>(cols) / C::GROUPS, c0 = grp * hn;   // this warp's columns
       Prep<C::GROUPS> &w = s.prep[seg & 1];
-      const int nt = p.t1 - p.t0;
       // a group's columns in use
       auto used = [&](int gr) -> uint64_t {
         const int k = min(hn, cols - gr * hn);
@@ -921,11 +926,10 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
       bool any_masked = false;
 #pragma unroll 1
       for (int t = p.t0; t < p.t1; ++t, ++tiles) {
-        const int buf = tiles % C::SB, i = t - p.t0;
+        const int buf = tiles % C::SB;
         const int j0 = (p.tile0 + t) * kTile, j = j0 + row;
-        const bool masked = j0 + kTile > p.ctx ||
-                            (a.window > 0 && j0 <= p.ctx + p.n - 1 - a.window);
-        const bool first = i == 0;
+        const bool masked = is_masked(t);
+        const bool first = t == p.t0;
         uint64_t sees = ~0ull;                  // the columns that see this thread's key
         bool none_sees = false, all_see = true;
         any_masked |= masked;
@@ -998,7 +1002,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
 #pragma unroll 1
               for (int c = 0; c < hn; c += 16) {
 #pragma unroll 1
-                for (int blk = 0; blk <= C::BLOCKS; ++blk) {   // (the last: the sums)
+                for (int blk = 0; blk <= C::E; ++blk) {   // (the last: the sums)
                   uint32_t r[16];
                   const uint32_t at = trow + C::O_COL + blk * C::COLS + c0 + c;
                   t_ld16(at, r);
@@ -1046,34 +1050,32 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
         t_fence_before();
         __syncwarp();
         if (lane == 0) t_arrive(sfree_x + 8 * buf);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        t_fence_before();
+        __syncwarp();
+        if (lane == 0) t_arrive(pfull(x));
         if (masked) {
-          // the tile's V entries: V(i) stands behind K(i + 1) in the ring. Rows seen by no column
-          // are cleared, and those seen by some only if they are not finite
-          const int e0 = g + (2 * i + (i == nt - 1 ? 1 : 2)) * C::E;
+          // Rows of V seen by no column are cleared, and those seen by some only if they are not
+          // finite, block by block between its being there and its product.
           const unsigned none = __ballot_sync(0xffffffffu, none_sees);
           const unsigned part = __ballot_sync(0xffffffffu, !none_sees && !all_see);
-          // a phase is told from the one before only, so the entries' previous tiles have to be
-          // there: they stand at or before K(i) or V(i - 1) in the ring, whose products are done,
-          // but for rings shorter than two tiles, where some are K(i + 1)
           // (a single atom is the first group's)
-          if ((none | part) && (D > 64 || grp == 0)) {
-            if (C::NS < 2 * C::E && i < nt - 1)
-              ok = ok && wait_for(sfull_x + 8 * ((tiles + 1) % C::SB), (tiles + 1) / C::SB);
-            constexpr int KEYS = kTile / C::V_HALVES;    // of an entry
-            // this warp's share of a row of an entry: 8 lanes an atom, both atoms or its group's
-            constexpr int AT = D == 64 || C::GROUPS == 2 ? 1 : 2;
-            constexpr int STEP = 4 / AT;                 // rows at a time
-            const int in = (lane & 7) * 16 +
-                           (D == 64            ? 0
-                            : C::GROUPS == 2 ? grp
-                                             : (lane >> 3) & 1) * KEYS * 128;
-            const int which = lane / (8 * AT);           // of the rows at a time
+          const bool looks = (none | part) && (D > 64 || grp == 0);
+          // this warp's share of a row of an entry: 8 lanes an atom, both atoms or its group's
+          constexpr int AT = D == 64 || C::GROUPS == 2 ? 1 : 2;
+          constexpr int STEP = 4 / AT;                 // rows at a time
+          const int in = (lane & 7) * 16 +
+                         (D == 64            ? 0
+                          : C::GROUPS == 2 ? grp
+                                           : (lane >> 3) & 1) * C::KEYS * 128;
+          const int which = lane / (8 * AT);           // of the rows at a time
 #pragma unroll 1
-            for (int blk = 0; blk < C::BLOCKS; ++blk) {
-              const int n = e0 + blk * C::V_HALVES + 32 * quad / KEYS, e = n % C::NS;
-              ok = ok && wait_for(full + 8 * e, n / C::NS);
-              if (!ok) break;
-              uint8_t *v = sm + e * C::ENTRY + in + (32 * quad % KEYS) * 128;
+          for (int blk = 0; blk < C::E && ok; ++blk) {
+            if (looks) ok = wait_for(vthere(x, blk), masks);
+            if (looks && ok) {
+              const int e = C::NK + (g + (t - p.t0) * C::E + blk) % C::NV;
+              uint8_t *v = sm + e * C::ENTRY + 32 * quad / C::KEYS * C::ATOM + in +
+                           (32 * quad % C::KEYS) * 128;
               unsigned clear = none;
               if (part) {
 #pragma unroll 1
@@ -1123,14 +1125,13 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
                   if (mine_of >> r & 1)
                     *reinterpret_cast<uint4 *>(v + (r + which) * 128) = make_uint4(0, 0, 0, 0);
               }
-              __syncwarp();
             }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) t_arrive(vclean(x, blk));
           }
+          ++masks;
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        t_fence_before();
-        __syncwarp();
-        if (lane == 0) t_arrive(pfull(x));
       }
       ok = ok && wait_for(pvdone_x, tiles - 1);
       t_fence_after();
@@ -1165,7 +1166,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
               if (c0 + c + e < cols) rec[C::COLS * (D + 1) + c0 + c + e] = l[e];
           }
 #pragma unroll 1
-          for (int blk = 0; blk < C::BLOCKS; ++blk) {
+          for (int blk = 0; blk < C::E; ++blk) {
             const int d = blk * 128 + row;
             uint32_t r[16];
             t_ld16(trow + C::O_COL + blk * C::COLS + c0 + c, r);
@@ -1224,11 +1225,11 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
       if (p.t0 == p.t1) continue;
       seg = segs++;
       if (seg % U != x) {
-        g += 2 * (p.t1 - p.t0) * C::E;
+        g = (g + (p.t1 - p.t0) * C::E) % C::NV;
         continue;
       }
       unit();
-      g += 2 * (p.t1 - p.t0) * C::E;
+      g = (g + (p.t1 - p.t0) * C::E) % C::NV;
     }
     if ((gone || !ok) && lane == 0) tree_report(a.err, PKV_ERR_TIMEOUT);
   }
@@ -1255,14 +1256,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   auto rec = [&](int i) -> const float * {
     return parts + (2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * C::RECORD;
   };
-  constexpr int kAhead = C::BLOCKS > 2 ? 2 : 4;
-  float4 v[kAhead][C::BLOCKS];
+  constexpr int kAhead = C::E > 2 ? 2 : 4;
+  float4 v[kAhead][C::E];
   auto read = [&](int i) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
       if (i + j < cut.parts && d < D)
 #pragma unroll
-        for (int b = 0; b < C::BLOCKS; ++b)
+        for (int b = 0; b < C::E; ++b)
           v[j][b] = *reinterpret_cast<const float4 *>(rec(i + j) + col * D + 128 * b + d);
   };
   read(0);
@@ -1275,9 +1276,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (top == -INFINITY) top = 0.f;
-  float4 x[C::BLOCKS];
+  float4 x[C::E];
 #pragma unroll
-  for (int b = 0; b < C::BLOCKS; ++b) x[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int b = 0; b < C::E; ++b) x[b] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = 0; i0 < cut.parts; i0 += 32) {
     if (cut.parts > 32 && i0 + lane < cut.parts) {   // (else they are at hand)
       ref = rec(i0 + lane)[C::COLS * D + col];
@@ -1295,7 +1296,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         const float wj = __shfl_sync(0xffffffffu, w, (i + j) & 31);
         if (i + j < n) {
 #pragma unroll
-          for (int b = 0; b < C::BLOCKS; ++b) {
+          for (int b = 0; b < C::E; ++b) {
             x[b].x = fmaf(wj, v[j][b].x, x[b].x);
             x[b].y = fmaf(wj, v[j][b].y, x[b].y);
             x[b].z = fmaf(wj, v[j][b].z, x[b].z);
@@ -1312,7 +1313,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   __nv_bfloat16 *o = out + (static_cast<long long>(cut.token0 + tok) * Hq + cut.head * G +
                             (col - tok * G)) * D;
 #pragma unroll
-  for (int b = 0; b < C::BLOCKS; ++b)
+  for (int b = 0; b < C::E; ++b)
     *reinterpret_cast<uint2 *>(o + 128 * b + d) =
         make_uint2(t_pack(x[b].x * inv, x[b].y * inv), t_pack(x[b].z * inv, x[b].w * inv));
 }
@@ -1337,9 +1338,15 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
   }
   const int sms = pkv::sm_count();
   const int grid = sms < 1 ? 1 : sms < kMaxCtas ? sms : kMaxCtas;
-  // a Q box is so many nodes that its rows fill whole swizzle atoms of 8
-  const int box_nodes = a.G % 8 == 0 ? 1 : a.G % 4 == 0 ? 2 : a.G % 2 == 0 ? 4 : 8;
-  a.unit_tokens = C::COLS / (box_nodes * a.G) * box_nodes;
+  // A Q box is so many nodes that its rows fill whole swizzle atoms of 8, and as many times as
+  // many as the rows have on average: one box an atom mostly. (A box a node of 8 heads kept 16
+  // rows with trees of 64 at D = 512 waiting 4 us for each unit's queries: BOXES us.)
+  const int least = a.G % 8 == 0 ? 1 : a.G % 4 == 0 ? 2 : a.G % 2 == 0 ? 4 : 8;
+  const int most = C::COLS / (least * a.G);
+  a.unit_tokens = most * least;
+  int times = 1;
+  while (times < most && (most % times || 1LL * times * least * a.B < a.N)) ++times;
+  const int box_nodes = times * least;
   a.box_nodes = box_nodes;
   a.arrived = static_cast<int *>(workspace);
   a.cuts = reinterpret_cast<Cut *>(static_cast<char *>(workspace) + kArrivedBytes);
@@ -1347,11 +1354,11 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
   CUtensorMap tmQ, tmK, tmV;
   const int rows = a.n_pages * a.page_size;
   const int k_box = a.page_size < kTile ? a.page_size : kTile;
-  const int v_box = a.page_size < kTile / C::V_HALVES ? a.page_size : kTile / C::V_HALVES;
+  const int v_box = a.page_size < C::KEYS ? a.page_size : C::KEYS;
   int st = pkv::prefill_atoms_map(&tmQ, q, a.N, a.Hq, D, a.G, box_nodes, 1);
   if (st == PKV_OK) st = pkv::prefill_atoms_map(&tmK, k, a.Hkv, rows, D, k_box, 1, 1);
-  // (two atoms of V in a box where its keys fill an entry)
-  const int v_atoms = D > 64 && v_box == kTile / C::V_HALVES ? 2 : 1;
+  // (two atoms of V in a box where its keys are a half's)
+  const int v_atoms = v_box == C::KEYS ? C::ATOMS : 1;
   if (st == PKV_OK) st = pkv::prefill_atoms_map(&tmV, v, a.Hkv, rows, D, v_box, 1, v_atoms);
   if (st != PKV_OK) return st;
   PKV_CUDA_CHECK(pkv::launch_pdl(tree_attn_kernel<D, MOST>, dim3(grid), dim3(C::THREADS),
