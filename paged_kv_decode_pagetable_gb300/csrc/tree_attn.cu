@@ -967,11 +967,45 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
             for (int e = 0; e < 16; ++e) y[e] = bits & (1u << e) ? y[e] : -INFINITY;
           }
         };
-        // P's place is free once the tile before has been multiplied
-        if (tiles >= 1) {
-          ok = ok && wait_for(pvdone_x, tiles - 1);
-          t_fence_after();
-        }
+        // P's place is free, and O is there, once the tile before has been multiplied. A unit that
+        // is alone has its weights wait for it in registers, so that only their way to shared
+        // memory is between two products (16 rows with trees of 64, eight heads of 128 77 -> 71
+        // us; a row of 41 tokens by units in twos, though, 5.0 -> 5.3: more code).
+        bool at_hand = tiles == 0;
+        auto wait_pv = [&]() {
+          if (!at_hand) {
+            ok = ok && wait_for(pvdone_x, tiles - 1);
+            t_fence_after();
+          }
+          at_hand = true;
+        };
+        uint32_t weights[C::HALF / 2];
+        // of 16 columns, under the references at hand
+        auto weigh = [&](int c, uint32_t *w, float &top) {
+          float y[16];
+          scores(c, y);
+          const float4 *m4 = reinterpret_cast<const float4 *>(s.mneg + h0 + c);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 m = m4[e / 4];
+            fma2(y[e], y[e + 1], y[e], y[e + 1], a.scale_log2, m.x, m.y);
+            fma2(y[e + 2], y[e + 3], y[e + 2], y[e + 3], a.scale_log2, m.z, m.w);
+            top = t_max3(top, y[e], y[e + 1]);
+            top = t_max3(top, y[e + 2], y[e + 3]);
+            w[e / 2] = t_pack(t_ex2(y[e]), t_ex2(y[e + 1]));
+            w[e / 2 + 1] = t_pack(t_ex2(y[e + 2]), t_ex2(y[e + 3]));
+          }
+        };
+        // a key's columns in a row of 128 bytes as the swizzle has them
+        auto put = [&](int c, const uint32_t *w) {
+          const int at = ((c0 + c) & 63) >> 3;
+          uint8_t *to = pbuf + (c0 + c) / 64 * C::P_ATOM;
+          *reinterpret_cast<uint4 *>(to + ((at ^ (row & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4 *>(to + (((at + 1) ^ (row & 7)) << 4)) =
+              make_uint4(w[4], w[5], w[6], w[7]);
+        };
+        if (U == 2) wait_pv();
         // a first tile begins with the columns' maxima, others when a score is out of reach
         for (bool exact = first;;) {
           if (exact) {
@@ -999,6 +1033,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
             }
             group_sync(sub);
             if (!first) {
+              wait_pv();
 #pragma unroll 1
               for (int c = 0; c < hn; c += 16) {
 #pragma unroll 1
@@ -1016,32 +1051,19 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
               t_wait_st();
             }
           }
-          // the weights under the references at hand, a key's columns in a row of 128 bytes as
-          // the swizzle has them
           float top = -INFINITY;
           if (ok) {
+            if constexpr (U == 2) {
 #pragma unroll 1
-            for (int c = 0; c < hn; c += 16) {
-              float y[16];
-              scores(c, y);
-              const float4 *m4 = reinterpret_cast<const float4 *>(s.mneg + h0 + c);
-              uint32_t w[8];
-#pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                const float4 m = m4[e / 4];
-                fma2(y[e], y[e + 1], y[e], y[e + 1], a.scale_log2, m.x, m.y);
-                fma2(y[e + 2], y[e + 3], y[e + 2], y[e + 3], a.scale_log2, m.z, m.w);
-                top = t_max3(top, y[e], y[e + 1]);
-                top = t_max3(top, y[e + 2], y[e + 3]);
-                w[e / 2] = t_pack(t_ex2(y[e]), t_ex2(y[e + 1]));
-                w[e / 2 + 1] = t_pack(t_ex2(y[e + 2]), t_ex2(y[e + 3]));
+              for (int c = 0; c < hn; c += 16) {
+                uint32_t w[8];
+                weigh(c, w, top);
+                put(c, w);
               }
-              const int at = ((c0 + c) & 63) >> 3;
-              uint8_t *to = pbuf + (c0 + c) / 64 * C::P_ATOM;
-              *reinterpret_cast<uint4 *>(to + ((at ^ (row & 7)) << 4)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-              *reinterpret_cast<uint4 *>(to + (((at + 1) ^ (row & 7)) << 4)) =
-                  make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+#pragma unroll
+              for (int c = 0; c < C::HALF; c += 16)
+                if (c < hn) weigh(c, weights + c / 2, top);
             }
           }
           if (exact || !group_any(sub, top > kLazyLog2 || !ok)) break;
@@ -1050,6 +1072,12 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
         t_fence_before();
         __syncwarp();
         if (lane == 0) t_arrive(sfree_x + 8 * buf);
+        wait_pv();
+        if (U == 1 && ok) {
+#pragma unroll
+          for (int c = 0; c < C::HALF; c += 16)
+            if (c < hn) put(c, weights + c / 2);
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         t_fence_before();
         __syncwarp();
