@@ -145,7 +145,8 @@ struct Small {
   static constexpr int COLS = C::UNITS * C::COLS;
   Prep<C::GROUPS> prep[2];
   // of the columns, group g's from g * HALF on (the groups may be at different units)
-  alignas(16) float mneg[COLS];     // a column's reference's negative, kUnset: none yet
+  alignas(16) float mneg[COLS];     // a column's reference's negative, kUnset: none yet; -inf: an
+                                    // unused column, of whatever scores: none is out of its reach
   float ref[COLS];                  // its reference, -inf: none yet
   float alpha[COLS];                // what a new one scales O and sums by; NaN: poisoned
   long long dst[COLS];              // its place in out, -1: none
@@ -652,11 +653,15 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
 #pragma unroll 1
         for (int t = p.t0; t < p.t1 && ok; ++t, ++tiles) {
           const bool mask = is_masked(t);
-          ok = wait_for(pfull(x), tiles);
+          bool ahead = mask;              // whether the next entry has been taken
+          uint32_t next = 0;
+          if (mask) {   // (a masked tile's V is looked at as soon as it is there)
+            next = take();
+            if (ok && lane == 0) t_arrive(vthere(x, 0));
+          }
+          ok = ok && wait_for(pfull(x), tiles);
           if (t == p.t0 && own >= 1) ok = ok && wait_for(ofree(x), own - 1);
           const uint32_t add = t > p.t0;
-          bool ahead = false;
-          uint32_t next = 0;
           t_fence_after();
           // the weights' sums: a row of ones, 128 times (they need no V, which may be on its way)
           if (ok && elect_one()) {
@@ -1006,7 +1011,8 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
               make_uint4(w[4], w[5], w[6], w[7]);
         };
         if (U == 2) wait_pv();
-        // a first tile begins with the columns' maxima, others when a score is out of reach
+        // A first tile begins with the columns' maxima, others when a score is out of reach. (A first
+        // guess without maxima, 2^4 above the first key's scores, gained nothing.)
         for (bool exact = first;;) {
           if (exact) {
             if (group_any(sub, !ok)) {
@@ -1028,7 +1034,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
                                       fmaxf(s.red[2][c], s.red[3][c])) * a.scale_log2;
               const float ref = fmaxf(old, top);
               s.ref[c] = ref;
-              s.mneg[c] = ref == -INFINITY ? kUnset : -ref;
+              s.mneg[c] = c0 + mine >= cols ? -INFINITY : ref == -INFINITY ? kUnset : -ref;
               s.alpha[c] = old == ref ? 1.f : exp2f(old - ref);
             }
             group_sync(sub);

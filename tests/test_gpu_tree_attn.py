@@ -218,6 +218,25 @@ def test_one_workspace_serves_every_shape():
                            want[i]), i
 
 
+@pytest.mark.parametrize("D, G, ns", [(128, 4, [3, 1, 5]), (64, 1, [7, 2]), (128, 8, [11, 13]),
+                                      (256, 8, [1, 9]), (512, 8, [3, 20])])
+def test_unused_columns_change_nothing(D, G, ns):
+    """Columns that a row does not fill hold what was there: results are the same whatever
+    queries the calls before had."""
+    rng = rng_of(23)
+    c = TreeCase(rng, 2 * G, 2, D, 64, [500 + 300 * i for i in range(len(ns))],
+                 [random_tree(rng, n, 2) for n in ns]).device(pkv)
+    full = TreeCase(rng, 2 * G, 2, D, 64, [700] * 8,
+                    [random_tree(rng, 64, 2) for _ in range(8)]).device(pkv)
+    want = None
+    for fill in (0.0, 1e3, -1e3, 3e38, float("inf"), float("nan")):
+        full.t["q"].fill_(fill)
+        full.call(pkv)
+        got = c.call(pkv).clone()
+        want = got if want is None else want
+        assert torch.equal(got, want), fill
+
+
 def test_cache_beyond_32_bits():
     """Rows whose elements lie past 2^32: the last pages of a 9 GB cache."""
     D, ps, P, Hkv = 128, 128, 1 << 17, 2
