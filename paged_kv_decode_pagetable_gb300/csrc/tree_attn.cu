@@ -150,7 +150,7 @@ struct Small {
   float ref[COLS];                  // its reference, -inf: none yet
   float alpha[COLS];                // what a new one scales O and sums by; NaN: poisoned
   long long dst[COLS];              // its place in out, -1: none
-  float red[kFan][COLS];            // maxima of the four warps of a group; parts' weights
+  alignas(16) float red[kFan][COLS];   // maxima of the four warps of a group; parts' weights
   int last[2];                      // whether a unit's part was the last of some to arrive
   int scan[16];
   uint64_t bars[48];
@@ -224,24 +224,11 @@ __device__ __forceinline__ bool group_any(int grp, bool mine) {
 __device__ __forceinline__ void group_sync(int grp) {
   asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + grp) : "memory");
 }
-// The maximum of 16 columns over the 32 lanes: halves of the columns change places until every
-// pair of lanes has one, column_of(lane).
-__device__ __forceinline__ float column_max(float (&x)[16], int lane) {
-#pragma unroll
-  for (int o = 16, n = 8; o >= 2; o >>= 1, n >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (e < n) {
-        const float got = __shfl_xor_sync(0xffffffffu, up ? x[e] : x[e + n], o);
-        x[e] = fmaxf(up ? x[e + n] : x[e], got);
-      }
-    }
-  }
-  return fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
-}
-__device__ __forceinline__ int column_of(int lane) {
-  return (lane & 16 ? 8 : 0) + (lane & 8 ? 4 : 0) + (lane & 4 ? 2 : 0) + (lane & 2 ? 1 : 0);
+// the maximum over the 32 lanes (NaN only where all are)
+__device__ __forceinline__ float lane_max(float x) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // N of a unit's products: a multiple of 16 columns for each group of softmax warps
@@ -1023,8 +1010,14 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
             for (int c = 0; c < hn; c += 16) {
               float y[16];
               scores(c, y);
-              const float v = column_max(y, lane);
-              if (!(lane & 1)) s.red[quad][h0 + c + column_of(lane)] = v;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = lane_max(y[e]);
+              if (lane == 0) {
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                  *reinterpret_cast<float4 *>(&s.red[quad][h0 + c + e]) =
+                      make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+              }
             }
             group_sync(sub);
             if (mine < hn) {
