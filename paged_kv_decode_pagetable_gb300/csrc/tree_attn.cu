@@ -189,10 +189,10 @@ __device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, f
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
 }
-// Waits for completion number k of a barrier's phases, by a whole warp with one answer; false if
-// it gave up, after about two seconds. (A loop of few instructions: the waits are many, and a
-// kernel that does not fit the instruction caches waits for its code instead.)
-__device__ __forceinline__ bool wait_for(uint32_t bar, int k) {
+// Waits for completion number k of a barrier's phases, a lane or a whole warp with one answer;
+// false if it gave up, after about two seconds. (A loop of few instructions: the waits are many,
+// and a kernel that does not fit the instruction caches waits for its code instead.)
+__device__ __forceinline__ bool lane_wait(uint32_t bar, int k) {
   uint32_t done;
   asm volatile(
       "{\n.reg .pred p, q;\n.reg .u32 n;\nmov.u32 n, 0;\n"
@@ -202,7 +202,10 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, int k) {
       : "=r"(done)
       : "r"(bar), "r"(static_cast<uint32_t>(k) & 1u), "n"(1 << 21)
       : "memory");
-  return __all_sync(0xffffffffu, done != 0);
+  return done != 0;
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, int k) {
+  return __all_sync(0xffffffffu, lane_wait(bar, k));
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -576,23 +579,20 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
     }
   } else if (warp >= C::MMA) {
     // ==================== MMA: a warp for S, one for P V ====================
-    // Of two products one is issued while the other's warp waits: 16 rows with trees of 64, one
-    // head of 512 WIDE us, with one warp for both 57. The whole warp goes through the steps and
-    // one elected lane issues: so the compiler knows that descriptors and addresses are the
-    // warp's, and an MMA takes 42 to 50 cycles (its A operand's way from shared memory). Issued
-    // under a lane's own branch it took 90 to 150.
+    // Of two products one is issued while the other's warp waits. A tile is one elected lane's,
+    // its waits too (a vote, an election and an address for each entry of D = 512 took as long as
+    // its products: ELECT us); the warp meets between tiles. Elected, not under a lane's own
+    // branch: so the compiler knows that descriptors and addresses are the warp's, and an MMA
+    // takes 42 to 50 cycles (its A operand's way from shared memory), not 90 to 150.
     const bool is_pv = warp != C::MMA;
-    const int slots = is_pv ? C::NV : C::NK, slot0 = is_pv ? C::NK : 0;
-    int at = 0, round = 0;                  // as the producers'
+    static_assert(C::E == 1 || (C::E % C::NK == 0 && C::E % C::NV == 0), "slots of a tile");
+    int at = 0, round = 0;                  // the next entry, how often the ring has been used up
     int segs = 0, done[2] = {0, 0}, masked[2] = {0, 0};   // tiles of each unit, masked ones
     bool ok = true;
-    // the next entry, once it is there
-    auto take = [&]() -> uint32_t {
-      const uint32_t e = __shfl_sync(0xffffffffu, slot0 + at, 0);
-      ok = ok && wait_for(full + 8 * e, round);
-      if (++at == slots) at = 0, ++round;
-      t_fence_after();
-      return e;
+    // (a tile's entries: the next one, or as many as the ring has, or a multiple)
+    auto used = [&](int slots) {
+      if (C::E > 1) round += C::E / slots;
+      else if (++at == slots) at = 0, ++round;
     };
     const uint64_t dOne = t_desc(sOnes, 0, 0);
     while (ok && line.next()) {
@@ -609,13 +609,16 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
 #pragma unroll 1
         for (int t = p.t0; t < p.t1 && ok; ++t, ++tiles) {
           const int buf = tiles % C::SB;
-          if (tiles >= C::SB) ok = wait_for(sfree(x, buf), tiles / C::SB - 1);
           const uint32_t to = __shfl_sync(0xffffffffu, tx + C::S_COL + buf * C::COLS, 0);
-#pragma unroll 1
-          for (int c = 0; c < C::E && ok; ++c) {
-            const uint32_t e = take();
-            if (!ok) break;
-            if (elect_one()) {
+          const uint32_t slot = __shfl_sync(0xffffffffu, at, 0);
+          if (elect_one()) {
+            ok = tiles < C::SB || lane_wait(sfree(x, buf), tiles / C::SB - 1);
+#pragma unroll
+            for (int c = 0; c < C::E; ++c) {
+              const uint32_t e = C::E > 1 ? c % C::NK : slot;
+              ok = ok && lane_wait(full + 8 * e, round + (C::E > 1 ? c / C::NK : 0));
+              t_fence_after();
+              if (!ok) break;
 #pragma unroll
               for (int b = 0; b < C::ATOMS; ++b) {
                 const uint64_t ka = t_desc(sRing + e * C::ENTRY + b * C::ATOM, 16, 1024);
@@ -625,13 +628,12 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
                   t_mma(to, ka + k * 2, qb + k * 2, id, c > 0 || b > 0 || k > 0);
               }
               t_commit(empty + 8 * e);
-              if (c + 1 == C::E) {
-                t_commit(sfull(x, buf));
-                if (t == p.t1 - 1) t_commit(qempty(x));
-              }
             }
-            __syncwarp();
+            if (ok) t_commit(sfull(x, buf));
+            if (ok && t == p.t1 - 1) t_commit(qempty(x));
           }
+          ok = __all_sync(0xffffffffu, ok);
+          used(C::NK);
         }
       } else {
         const uint64_t dP = t_desc(sP + x * C::P_BYTES, C::P_ATOM, 1024);
@@ -640,43 +642,34 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
 #pragma unroll 1
         for (int t = p.t0; t < p.t1 && ok; ++t, ++tiles) {
           const bool mask = is_masked(t);
-          bool ahead = mask;              // whether the next entry has been taken
-          uint32_t next = 0;
-          if (mask) {   // (a masked tile's V is looked at as soon as it is there)
-            next = take();
-            if (ok && lane == 0) t_arrive(vthere(x, 0));
-          }
-          ok = ok && wait_for(pfull(x), tiles);
-          if (t == p.t0 && own >= 1) ok = ok && wait_for(ofree(x), own - 1);
-          const uint32_t add = t > p.t0;
-          t_fence_after();
-          // the weights' sums: a row of ones, 128 times (they need no V, which may be on its way)
-          if (ok && elect_one()) {
+          const uint32_t slot = C::NK + __shfl_sync(0xffffffffu, at, 0);
+          if (elect_one()) {
+            // a masked tile's V is looked at block by block, as soon as it is there
+            auto there = [&](int c) {
+              const uint32_t e = C::E > 1 ? C::NK + c % C::NV : slot;
+              ok = ok && lane_wait(full + 8 * e, round + (C::E > 1 ? c / C::NV : 0));
+              if (ok && mask) t_arrive(vthere(x, c));
+            };
+            if (mask) there(0);
+            ok = ok && lane_wait(pfull(x), tiles);
+            if (t == p.t0 && own >= 1) ok = ok && lane_wait(ofree(x), own - 1);
+            const uint32_t add = t > p.t0;
+            t_fence_after();
+            // the weights' sums: a row of ones, 128 times (they need no V, which may be on its way)
+            if (ok) {
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              t_mma(tx + C::L_COL, dOne, dP + k * (2048 >> 4), id, k > 0 ? 1u : add);
-          }
-          __syncwarp();
-#pragma unroll 1
-          for (int c = 0; c < C::E && ok; ++c) {
-            if (!ahead) {
-              next = take();
-              if (ok && mask && lane == 0) t_arrive(vthere(x, c));
+              for (int k = 0; k < kTile / 16; ++k)
+                t_mma(tx + C::L_COL, dOne, dP + k * (2048 >> 4), id, k > 0 ? 1u : add);
             }
-            const uint32_t e = next;
-            // (while a block is looked at, the next one comes)
-            ahead = mask && C::NV >= 2 && c + 1 < C::E;
-            if (ahead) {
-              next = take();
-              if (ok && lane == 0) t_arrive(vthere(x, c + 1));
-            }
-            if (mask) {
-              ok = ok && wait_for(vclean(x, c), masks);
+#pragma unroll
+            for (int c = 0; c < C::E; ++c) {
+              if (!mask) there(c);
+              else if (c + 1 < C::E) there(c + 1);
+              if (mask) ok = ok && lane_wait(vclean(x, c), masks);
               t_fence_after();
-            }
-            if (!ok) break;
-            const uint32_t to = tx + C::O_COL + c * C::COLS;
-            if (elect_one()) {
+              if (!ok) break;
+              const uint32_t e = C::E > 1 ? C::NK + c % C::NV : slot;
+              const uint32_t to = tx + C::O_COL + c * C::COLS;
 #pragma unroll
               for (int b = 0; b < C::ATOMS; ++b) {
                 // (D = 64: rows 64 .. 127 of the product repeat rows 0 .. 63)
@@ -689,10 +682,11 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
                         b > 0 || k > 0 ? 1u : add);
               }
               t_commit(empty + 8 * e);
-              if (c + 1 == C::E) t_commit(pvdone(x));
             }
-            __syncwarp();
+            if (ok) t_commit(pvdone(x));
           }
+          ok = __all_sync(0xffffffffu, ok);
+          used(C::NV);
           masks += mask;
         }
         if (x) masked[1] = masks;
