@@ -213,6 +213,11 @@ __device__ __forceinline__ bool elect_one() {
                : "=r"(r));
   return r != 0;
 }
+// reads of TMEM are a whole warp's, which may have come here by the ways of its lanes
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  __syncwarp();
+  t_ld16(taddr, r);
+}
 // barrier of the 128 threads of a group, and whether any of them says yes
 __device__ __forceinline__ bool group_any(int grp, bool mine) {
   uint32_t r;
@@ -397,6 +402,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
     reinterpret_cast<uint32_t *>(sm + C::OFF_ONES)[i] = 0x3f803f80u;
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   if (warp == 0) {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      t_smem(&s.tmem)),
                  "r"(512));
@@ -943,7 +949,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
         // 16 scores of this thread's key, -inf where a node does not see it
         auto scores = [&](int c, float (&y)[16]) {
           uint32_t r[16];
-          t_ld16(scol + c, r);
+          ld16(scol + c, r);
           t_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(r[e]);
@@ -1033,7 +1039,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
                 for (int blk = 0; blk <= C::E; ++blk) {   // (the last: the sums)
                   uint32_t r[16];
                   const uint32_t at = trow + C::O_COL + blk * C::COLS + c0 + c;
-                  t_ld16(at, r);
+                  ld16(at, r);
                   t_wait_ld();
 #pragma unroll
                   for (int e = 0; e < 16; ++e)
@@ -1173,7 +1179,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
           float l[16];
           {
             uint32_t r[16];
-            t_ld16(trow + C::L_COL + c0 + c, r);
+            ld16(trow + C::L_COL + c0 + c, r);
             t_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e) l[e] = __uint_as_float(r[e]) * s.alpha[h0 + c + e];
@@ -1190,7 +1196,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
           for (int blk = 0; blk < C::E; ++blk) {
             const int d = blk * 128 + row;
             uint32_t r[16];
-            t_ld16(trow + C::O_COL + blk * C::COLS + c0 + c, r);
+            ld16(trow + C::O_COL + blk * C::COLS + c0 + c, r);
             t_wait_ld();
             if (D == 64 && quad >= 2) continue;
             if (whole) {
