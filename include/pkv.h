@@ -621,17 +621,19 @@ int tree_qkv_norm_rope_append(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf
  * slot 0 give zeros. Keys and values that a node does not see never reach it,
  * whatever they hold; a value that is not finite and that only some nodes of its
  * row see may make the whole output of those NaN. Scores and sums are fp32, the
- * weights enter the product with V as bf16. Table entries that are negative or >= n_pages inside a row's key
- * range set PKV_ERR_PAGE_* (that row's output is then unspecified). Requires
+ * weights enter the product with V as bf16. Table entries that are negative or
+ * >= n_pages inside a row's key range set PKV_ERR_PAGE_* (that row's output is
+ * then unspecified). Requires
  * D in {64, 128, 256, 512}, 1 <= Hq / Hkv <= 8, page_size a power of two >= 8,
  * scale finite and > 0, 16-byte aligned tensors. The workspace
  * (paged_tree_attn_workspace(Hq, Hkv, D) bytes, whatever the batch; 0 for sizes
  * the call refuses) holds parts of rows during a call and counts them: zero it
  * once before its first use. Every call leaves its counts zero, except one that
  * reports PKV_ERR_TIMEOUT, after which it must be zeroed again. Calls that share
- * one, of whatever shapes, must not overlap on the GPU. A call whose nodes, heads and keys make 2^31
- * tiles of 128 keys or more sets PKV_ERR_POS and computes nothing; a wait for a
- * copy that gives up sets PKV_ERR_TIMEOUT (outputs are then unspecified). */
+ * one, of whatever shapes, must not overlap on the GPU. A call whose nodes,
+ * heads and keys make 2^31 tiles of 128 keys or more sets PKV_ERR_POS and
+ * computes nothing; a wait for a copy that gives up sets PKV_ERR_TIMEOUT
+ * (outputs are then unspecified). */
 int paged_tree_attn(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,
                     const int32_t *dev_table, int n_slots, int max_pages_per_seq,
                     int page_size, int n_pages, const int32_t *batch_idx,

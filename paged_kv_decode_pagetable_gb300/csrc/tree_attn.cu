@@ -12,8 +12,9 @@
 //   S^T = K q^T    M = 128 keys of a tile, N columns, both operands K-major,
 //   O^T = V^T P^T  M = 128 columns of D, N columns, K = the tile's 128 keys, both MN-major: V as
 //                  it lies in the cache, P as the threads write it, a key's columns in a row.
-// An MMA with M = 128 takes 42 cycles for 32 columns, 50 for 64, 66 for 128, in either order of
-// the operands; with the queries as M, 32 rows would pay for 128.
+// An MMA with M = 128 takes 43 cycles for 32 columns, 51 for 64, 67 for 128, in either order of
+// the operands: their way from shared memory at 128 bytes a cycle. With the queries as M, 32 rows
+// would pay for 128.
 // In S^T a thread owns a key. Its columns' maxima run across threads, so they are not taken tile
 // by tile: a column keeps a reference, every thread checks that none of its scores passes it by
 // more than 2^8, and only where one does (a unit's first tile, and few others) the maxima are
@@ -25,21 +26,25 @@
 // rollout batch, not 39), lie on one line, cut into equal shares for one persistent CTA an SM from
 // the lengths, on the device. A unit that is cut leaves its parts (O, reference and sum, fp32) in
 // the workspace, and whoever writes the last of them, or a second kernel, joins them in their
-// order: results do not depend on timing and no CTA waits for another. (Shares that begin at a unit's edge where that is
-// near, to cut fewer: 56 -> 71 us for 64 nodes at D = 512, 39 -> 42 for the rollout batch.) The
-// line is planned from row_start, ctx_lens and batch_idx before the prior kernel has ended.
+// order: results do not depend on timing and no CTA waits for another. (Shares that begin at a
+// unit's edge where that is near, to cut fewer: 56 -> 71 us for 64 nodes at D = 512, 39 -> 42 for
+// the rollout batch.) The line is planned from row_start, ctx_lens and batch_idx before the prior
+// kernel has ended.
 //   warps 0-7 (softmax): D <= 128 with 64 columns, two units at a time, four warps each, so that
 //     one unit's start and end overlap the other's tiles; else one unit, its columns in two
 //     halves. Warp w has the keys of TMEM lanes 32 (w % 4) ..: masks, weights, references, a
 //     unit's output or part;
-//   warp 8: K and V tiles by TMA, a box a page and 64 columns, into a ring of 16 KB entries in the
-//     order in which the MMAs use them up: K(0), K(1), V(0), K(2), V(1) ..;
-//   warp 9: a unit's queries by TMA, and which columns see a key: sets of 64 bits, from the
+//   warps 8, 9: K and V tiles by TMA, each into a ring of its own;
+//   warp 10: a unit's queries by TMA, and which columns see a key: sets of 64 bits, from the
 //     parents by pointer doubling;
-//   warps 10, 11: the MMAs of a unit each, S one tile ahead of P V.
+//   warps 11, 12: the MMAs of S and of P V. With one warp for both, and one ring, each waited
+//     while the other could have been issued; and an entry of 32 KB a barrier, not 16, halves the
+//     waits (16 rows with trees of 64: one head of 512 55 -> 52 us, of 256, up to 8k tokens,
+//     91 -> 82).
 // Rows of V that no node sees are cleared in shared memory (0 x NaN would reach every column);
 // one that is not finite and seen by some nodes only is cleared too and those nodes' results
-// are NaN: nothing of it reaches the others.
+// are NaN: nothing of it reaches the others. So that this is between a tile's arrival and its
+// product, the warp of P V says when a masked tile's V is there and waits until it is clean.
 //
 // What costs most next to memory is code: a first form with its loops unrolled had 120 KB, a third
 // of its warps' time went into waiting for instructions, and the rollout batch took 70 us. Hence
@@ -49,8 +54,10 @@
 // 240 us, 0.99 of reading them; 64 rows of 100 to 1024 tokens, trees of 8, 37 us, 0.61: its start
 // (launch, plan, the rings' first fill) and its end (last tiles, join) are 6 us each; 64 rows of
 // 256 to 2048 tokens in a window of 512, trees of 16, one head of 256, 31 us, 0.19, and 16 rows
-// with trees of 64, one head of 512, 57 us, 0.13: they write and read as many bytes in parts as
-// in keys, and at D = 512 every 8 nodes read the keys again; one row of 41 tokens 4.8 us.
+// with trees of 64, one head of 512, 52 us, 0.15: they write and read as many bytes in parts as
+// in keys, at D = 512 every 8 nodes read the keys again, and a tile's weights, P V and the next
+// one's weights stand behind one another (there is no room for a second P); one row of 41 tokens
+// 4.7 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -85,9 +92,9 @@ struct Cfg {
   static constexpr int GROUPS = 2 / UNITS;              // groups of four softmax warps a unit
   static constexpr int HALF = COLS / GROUPS;            // columns of a softmax warp, at most
   // Parts are joined by whoever is the last to write one; where units have two groups, by a second
-  // kernel. A row of 41 tokens 8.4 -> 4.8 us and the rollout batch 38.7 -> 37.4 by the last to
-  // write; but 30 -> 38 us for the window of 512 at D = 256 and 56 -> 61 at D = 512, where one
-  // CTA's few warps would read up to 128 KB a part.
+  // kernel. By the last to write, a row of 41 tokens went from 8.4 to 4.8 us and the rollout batch
+  // from 38.7 to 37.4; but the window of 512 at D = 256 from 30 to 38 and trees of 64 at D = 512
+  // from 56 to 61, where one CTA's few warps read up to 128 KB a part.
   static constexpr bool JOINS = UNITS == 2;
   static constexpr int SOFT = 8;                        // softmax warps of all units
   static constexpr int PROD = SOFT, PREP = SOFT + 2, MMA = SOFT + 3;
@@ -431,7 +438,8 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
           const int tiles = r.slot == 0 ? 0 : (r.ctx + r.n - 1) / kTile - lo / kTile + 1;
           mine[i] = static_cast<int>(min(static_cast<long long>(kMostPlaces),
                                          static_cast<long long>(tiles + kStart) *
-                                             (a.Hkv * ((r.n + a.unit_tokens - 1) / a.unit_tokens))));
+                                             (a.Hkv * ((r.n + a.unit_tokens - 1) /
+                                                       a.unit_tokens))));
         }
       }
       sum = add_places(sum, mine[i]);
@@ -479,6 +487,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
   };
   if (warp == C::PROD || warp == C::PROD + 1) {
     // ==================== producers, of K and of V ====================
+    // (a warp goes through its boxes as one, and an elected lane issues them, as the MMAs)
     const bool is_v = warp != C::PROD;
     const int slots = is_v ? C::NV : C::NK, slot0 = is_v ? C::NK : 0;
     const int k_rows = min(a.page_size, kTile);             // tokens of a K box
@@ -527,7 +536,8 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
         for (int i = first; i < last; ++i) {
           const int r = __shfl_sync(0xffffffffu, at_row, i);
           const int half = i >= per;
-          const uint32_t to = sRing + e * C::ENTRY + half * C::ATOM + (i - half * per) * v_rows * 128;
+          const uint32_t to =
+              sRing + e * C::ENTRY + half * C::ATOM + (i - half * per) * v_rows * 128;
           if (elect_one()) {
 #pragma unroll 1
             for (int b = 0; b < C::ATOMS; b += step)
@@ -585,11 +595,10 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
     }
   } else if (warp >= C::MMA) {
     // ==================== MMA: a warp for S, one for P V ====================
-    // Of two products one is issued while the other's warp waits. A tile is one elected lane's,
-    // its waits too (a vote, an election and an address for each entry of D = 512 took as long as
-    // its products: ELECT us); the warp meets between tiles. Elected, not under a lane's own
-    // branch: so the compiler knows that descriptors and addresses are the warp's, and an MMA
-    // takes 42 to 50 cycles (its A operand's way from shared memory), not 90 to 150.
+    // A tile is one elected lane's, its waits too: a vote, an election and an address for each
+    // entry took half as long as its products (1 to 2% of every call). Elected, not under a lane's
+    // own branch: so the compiler knows that descriptors and addresses are the warp's; an MMA took
+    // 90 to 150 cycles to issue otherwise. The warp meets between tiles.
     const bool is_pv = warp != C::MMA;
     static_assert(C::E == 1 || (C::E % C::NK == 0 && C::E % C::NV == 0), "slots of a tile");
     int at = 0, round = 0;                  // the next entry, how often the ring has been used up
@@ -998,8 +1007,8 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
               make_uint4(w[4], w[5], w[6], w[7]);
         };
         if (U == 2) wait_pv();
-        // A first tile begins with the columns' maxima, others when a score is out of reach. (A first
-        // guess without maxima, 2^4 above the first key's scores, gained nothing.)
+        // A first tile begins with the columns' maxima, others when a score is out of reach. (A
+        // first guess without maxima, 2^4 above the first key's scores, gained nothing.)
         for (bool exact = first;;) {
           if (exact) {
             if (group_any(sub, !ok)) {
@@ -1167,8 +1176,8 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
       if (mine < hn) {
         const int c = c0 + mine, k = h0 + mine, tok = p.tok0 + c / a.G;
         const bool bad = any_masked && (w.poison[grp][mine >> 5] >> (mine & 31) & 1);
-        s.dst[k] = c < cols ? (static_cast<long long>(p.n0 + tok) * a.Hq + p.head * a.G + c % a.G) * D
-                            : -1;
+        const long long q_row = static_cast<long long>(p.n0 + tok) * a.Hq + p.head * a.G + c % a.G;
+        s.dst[k] = c < cols ? q_row * D : -1;
         s.alpha[k] = bad ? NAN : 1.f;
         if (!whole && c < cols) rec[C::COLS * D + c] = s.ref[k];
       }
@@ -1365,9 +1374,9 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
   }
   const int sms = pkv::sm_count();
   const int grid = sms < 1 ? 1 : sms < kMaxCtas ? sms : kMaxCtas;
-  // A Q box is so many nodes that its rows fill whole swizzle atoms of 8, and as many times as
-  // many as the rows have on average: one box an atom mostly. (A box a node of 8 heads kept 16
-  // rows with trees of 64 at D = 512 waiting 4 us for each unit's queries: BOXES us.)
+  // A Q box is so many nodes that its rows fill whole swizzle atoms of 8, times what the rows have
+  // on average: one box an atom mostly. (A box a node of 8 heads kept 16 rows with trees of 64 at
+  // D = 512 waiting 4 us for each unit's queries: 57 us, now 54.)
   const int least = a.G % 8 == 0 ? 1 : a.G % 4 == 0 ? 2 : a.G % 2 == 0 ? 4 : 8;
   const int most = C::COLS / (least * a.G);
   a.unit_tokens = most * least;
@@ -1399,7 +1408,8 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
 
 // Units of 128 columns where the rows have more than 64, by the packed nodes a row: the keys of
 // a row are then read half as often (16 rows of 1k to 3k tokens, 8 heads of 128: trees of 64
-// 90 -> 78 us, of 32 58 -> 52; one head of 256, 128 rows of up to 2k tokens, trees of 16 62 -> 55).
+// 90 -> 78 us, of 32 58 -> 52, since then 69 and 44; one head of 256, 128 rows of up to 2k tokens,
+// trees of 16 62 -> 55).
 // At D = 512 TMEM holds 64.
 template <int D>
 int launch_for(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, const Args &a,

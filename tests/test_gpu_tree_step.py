@@ -89,7 +89,8 @@ def check_append(c, qo, theta=1e4, rotary=None, v_norm=False):
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (8, 8), (32, 8), (40, 5)])
 def test_append(D, Hq, Hkv):
     rng = np.random.default_rng([21, D, Hq])
-    c = append_case(rng, Hq, Hkv, D, 16, [0, 31, 4000], [random_tree(rng, n, 3) for n in (7, 1, 20)])
+    c = append_case(rng, Hq, Hkv, D, 16, [0, 31, 4000],
+                    [random_tree(rng, n, 3) for n in (7, 1, 20)])
     check_append(c, run_append(c))
 
 
@@ -196,7 +197,8 @@ def verify_case(rng, B, nodes, width, V, sampled):
         if parents[n] >= 0:
             d = q[base[n] + parents[n]].astype(np.float64)
             rank = sum(parents[m] == parents[n] for m in range(base[n], n))
-            tokens[n] = rng.choice(V, p=d / d.sum()) if sampled else np.argsort(-d)[min(rank, V - 1)]
+            tokens[n] = (rng.choice(V, p=d / d.sum()) if sampled
+                         else np.argsort(-d)[min(rank, V - 1)])
     u = rng.random(N).astype(np.float32)
     return p, q if sampled else None, tokens, start, parents, u, rng.random(B).astype(np.float32)
 
@@ -335,8 +337,10 @@ def test_verify_is_the_same_however_rows_are_shared():
 @pytest.mark.parametrize("ps", [8, 64])
 def test_keep_path(shape, dtype, ps):
     rng = np.random.default_rng([41, ps])
-    trees = [random_tree(rng, n, w) for n, w in ((9, 3), (64, 5), (20, 1), (1, 1), (40, 8), (12, 4))]
-    c = TreeCase(rng, 1, 1, 64, ps, [0, 100, 7, 64, 33, 5], trees, slots=[3, 1, 2, 6, 4, 0]).device(pkv)
+    trees = [random_tree(rng, n, w)
+             for n, w in ((9, 3), (64, 5), (20, 1), (1, 1), (40, 8), (12, 4))]
+    c = TreeCase(rng, 1, 1, 64, ps, [0, 100, 7, 64, 33, 5], trees,
+                 slots=[3, 1, 2, 6, 4, 0]).device(pkv)
     path = np.full((6, 64), -1)
     acc = np.zeros(6, int)
     for b, t in enumerate(trees):
@@ -413,7 +417,8 @@ def test_speculative_steps_against_single_ones():
     spec = engine.LayerSpec(head_dim=D, theta=1e4, qk_norm=True)
     tokens = [int(x) for x in rng.integers(0, V, B)]      # the last committed ones
     emb = [wl.randn_bf16(rng, (V, h * D)).cuda() for h in (Hq, Hkv, Hkv)]
-    gains = [(1 + 0.1 * torch.from_numpy(rng.standard_normal(D))).bfloat16().cuda() for _ in range(2)]
+    gains = [(1 + 0.1 * torch.from_numpy(rng.standard_normal(D))).bfloat16().cuda()
+             for _ in range(2)]
     pt, pt1 = (pkv.PageTable(B, ps, 80, 12, device="cuda") for _ in range(2))
     caches = [engine.alloc_cache(Hkv, 80, ps, D, "cuda") for _ in range(2)]
     slots = [pt.assign(1) for _ in range(B)]
@@ -436,7 +441,8 @@ def test_speculative_steps_against_single_ones():
         qo, out = torch.empty_like(qkv[0]), torch.empty_like(qkv[0])
         engine.tree_layer_step(spec, pt, *caches[0], *qkv, bi, cl, rs, parents, qo, out, ws, *gains,
                                err=err)
-        target = torch.softmax(torch.from_numpy(rng.standard_normal((N, V))).float() * 0.5, 1).cuda()
+        target = torch.softmax(
+            torch.from_numpy(rng.standard_normal((N, V))).float() * 0.5, 1).cuda()
         # drafts that the target likes, so that some are accepted
         for n in range(N):
             row = max(b for b in range(B) if start[b] <= n)

@@ -46,7 +46,8 @@ def _outcomes(target, draft, parents, V, sampled):
     grid = (np.arange(16) + 0.5) / 16
     picks = (np.arange(64) + 0.5) / 64
     for toks in itertools.product(range(V), repeat=len(kids)):
-        pr = np.prod([draft[0, t] for t in toks]) if sampled else float(toks == tuple(range(len(kids))))
+        pr = (np.prod([draft[0, t] for t in toks]) if sampled
+              else float(toks == tuple(range(len(kids)))))
         if pr == 0:
             continue
         tokens = np.zeros(len(parents), int)
