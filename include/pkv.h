@@ -623,10 +623,9 @@ int tree_qkv_norm_rope_append(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf
  * row see may make the whole output of those NaN. Scores and sums are fp32, the
  * weights enter the product with V as bf16. Table entries that are negative or
  * >= n_pages inside a row's key range set PKV_ERR_PAGE_* (that row's output is
- * then unspecified). Requires
- * D in {64, 128, 256, 512}, 1 <= Hq / Hkv <= 8, page_size a power of two >= 8,
- * scale finite and > 0, 16-byte aligned tensors. The workspace
- * (paged_tree_attn_workspace(Hq, Hkv, D) bytes, whatever the batch; 0 for sizes
+ * then unspecified). Requires D in {64, 128, 256, 512}, 1 <= Hq / Hkv <= 8,
+ * page_size a power of two >= 8, scale finite and > 0, 16-byte aligned tensors.
+ * The workspace (paged_tree_attn_workspace(Hq, Hkv, D) bytes, whatever the batch; 0 for sizes
  * the call refuses) holds parts of rows during a call and counts them: zero it
  * once before its first use. Every call leaves its counts zero, except one that
  * reports PKV_ERR_TIMEOUT, after which it must be zeroed again. Calls that share

@@ -811,6 +811,9 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
       if (lane == 0) t_arrive(prepfull + 8 * (segs & 1));
       ++segs;
     }
+    // (should the others have given up: what is on its way lands before the CTA leaves)
+#pragma unroll 1
+    for (int i = max(0, segs - U); i < segs; ++i) wait_for(qfull(i % U), i / U);
     tree_report(a.err, bits);
   } else {
     // ============================ softmax =============================

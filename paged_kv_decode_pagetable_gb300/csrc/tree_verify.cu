@@ -178,8 +178,7 @@ __device__ __forceinline__ void read_units(const Row &r, int u, int u1, int V, i
 // Sums of the groups of `size` units that units [u0, u1) make up; returns their sum.
 template <int KIND>
 __device__ __forceinline__ uint64_t sum_units(const Row &r, uint64_t a, Shared &sh, int size,
-                                              int u0,
-                                              int u1, int V, int warp, int lane) {
+                                              int u0, int u1, int V, int warp, int lane) {
   uint64_t total = 0;
   int g = 0;
   for (int first = u0; first < u1; first += size, ++g) {

@@ -310,8 +310,7 @@ def test_graph_replays_follow_the_trees():
     two graphs share a workspace."""
     rng = rng_of(18)
     cases = [TreeCase(rng, 8, 2, 128, 16, ctx, [random_tree(rng, n, 3) for n in ns],
-                      pad=40 - sum(ns),
-                      max_pages=80)
+                      pad=40 - sum(ns), max_pages=80)
              for ctx, ns in (([700, 30, 0], [8, 9, 3]), ([5, 1200, 90], [20, 1, 4]),
                              ([0, 0, 0], [0, 1, 0]), ([900, 100, 333], [13, 13, 14]))]
     P = max(c.P for c in cases)
