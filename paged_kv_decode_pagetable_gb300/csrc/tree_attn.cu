@@ -53,7 +53,7 @@
 // Measured (6769 GB/s measured): 16 rows of 16k to 32k tokens, 8-node chains, 8 heads of 128,
 // 240 us, 0.99 of reading them; 64 rows of 100 to 1024 tokens, trees of 8, 37 us, 0.61: its start
 // (launch, plan, the rings' first fill) and its end (last tiles, join) are 6 us each; 64 rows of
-// 256 to 2048 tokens in a window of 512, trees of 16, one head of 256, 31 us, 0.19, and 16 rows
+// 256 to 2048 tokens in a window of 512, trees of 16, one head of 256, 28 us, 0.21, and 16 rows
 // with trees of 64, one head of 512, 52 us, 0.15: they write and read as many bytes in parts as
 // in keys, at D = 512 every 8 nodes read the keys again, and a tile's weights, P V and the next
 // one's weights stand behind one another (there is no room for a second P); one row of 41 tokens
@@ -1412,12 +1412,16 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
 // Units of 128 columns where the rows have more than 64, by the packed nodes a row: the keys of
 // a row are then read half as often (16 rows of 1k to 3k tokens, 8 heads of 128: trees of 64
 // 90 -> 78 us, of 32 58 -> 52, since then 69 and 44; one head of 256, 128 rows of up to 2k tokens,
-// trees of 16 62 -> 55).
-// At D = 512 TMEM holds 64.
+// trees of 16 62 -> 55). But at D = 256 rows of up to 128 columns in a window of up to 512 are cut
+// into more units, of few tiles either way (trees of 16, 64 rows 31 us by 128, 28 by 64, 8 rows 18.5
+// and 15.6; a window of 1024 35 and 35, of 2048 43 and 47, trees of 64 31 and 32). At D = 512 TMEM
+// holds 64.
 template <int D>
 int launch_for(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, const Args &a,
                void *workspace, cudaStream_t s) {
-  if (D <= 256 && static_cast<long long>(a.N) * a.G > 64LL * a.B)
+  const long long columns = static_cast<long long>(a.N) * a.G;   // of all rows
+  const bool few_tiles = D == 256 && a.window > 0 && a.window <= 512 && columns <= 128LL * a.B;
+  if (D <= 256 && columns > 64LL * a.B && !few_tiles)
     return launch<D, D <= 256 ? 128 : 64>(q, k, v, a, workspace, s);
   return launch<D, 64>(q, k, v, a, workspace, s);
 }

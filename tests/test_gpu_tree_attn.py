@@ -80,6 +80,16 @@ def test_windows(window, D, G):
     TreeCase(rng, G, 1, D, 16, [300, 131, 0, 128], trees, window=window).device(pkv).check(pkv)
 
 
+@pytest.mark.parametrize("window", [1, 300, 511, 512, 513])
+@pytest.mark.parametrize("ns", [(9, 16, 20), (16, 16, 16), (17, 16, 16)])
+def test_units_of_short_windows(window, ns):
+    """Rows of up to and more than 128 columns on both sides of the window that decides how many
+    a unit has."""
+    rng = rng_of(24, window, *ns)
+    trees = [random_tree(rng, n, 3) for n in ns]
+    TreeCase(rng, 8, 1, 256, 64, [2000, 511, 90], trees, window=window).device(pkv).check(pkv)
+
+
 def test_forests_and_empty_and_padding_rows():
     """Several roots, rows without nodes, rows on slot 0, nodes behind the last row."""
     rng = rng_of(6)
