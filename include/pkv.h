@@ -688,6 +688,65 @@ int kv_keep_path(void *const *caches, const int *heads, const int64_t *token_byt
                  const int32_t *accepted, const int32_t *path, int path_cols, int B,
                  int32_t *err_word, void *stream);
 
+/* The four calls with their arguments in one record, for callers to whom every
+ * argument costs (31 of them through Python's ctypes 4.1 us, a record 0.7): the
+ * same arguments in the same order, at their natural alignment. args points to
+ * the record, at any address; the calls return what the plain ones do. */
+typedef struct {
+  const pkv_bf16 *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const pkv_bf16 *gamma_q, *gamma_k;
+  const int32_t *batch_idx, *ctx_lens, *row_start, *parents;
+  float theta, eps;
+  int rotary_dims, v_norm, B, N, Hq, Hkv, D;
+  const int32_t *dev_table;
+  int n_slots, max_pages_per_seq, page_size, n_pages;
+  pkv_bf16 *k_cache, *v_cache, *q_out;
+  int32_t *err_word;
+  void *stream;
+} pkv_tree_append_args;
+typedef struct {
+  const pkv_bf16 *q, *k_cache, *v_cache;
+  const int32_t *dev_table;
+  int n_slots, max_pages_per_seq, page_size, n_pages;
+  const int32_t *batch_idx, *ctx_lens, *row_start, *parents;
+  int window;
+  float scale;
+  int B, N, Hq, Hkv, D;
+  void *workspace;
+  size_t workspace_bytes;
+  pkv_bf16 *out;
+  int32_t *err_word;
+  void *stream;
+} pkv_tree_attn_args;
+typedef struct {
+  const float *target_probs;
+  int64_t target_stride;
+  const float *draft_probs;
+  int64_t draft_stride;
+  const int32_t *tokens, *row_start, *parents;
+  const float *u_accept, *u_pick;
+  int B, N, V, path_cols;
+  int32_t *accepted, *path, *next_token, *err_word;
+  void *stream;
+} pkv_tree_verify_args;
+typedef struct {
+  void *const *caches;
+  const int *heads;
+  const int64_t *token_bytes;
+  int n_caches;
+  const int32_t *dev_table;
+  int n_slots, max_pages_per_seq, page_size, n_pages;
+  const int32_t *batch_idx, *ctx_lens, *accepted, *path;
+  int path_cols, B;
+  int32_t *err_word;
+  void *stream;
+} pkv_keep_path_args;
+int tree_qkv_norm_rope_append_args(const void *args);
+int paged_tree_attn_args(const void *args);
+int tree_verify_args(const void *args);
+int kv_keep_path_args(const void *args);
+
 /* ---------------------------------------------------------------------
  * Utilities
  * ------------------------------------------------------------------- */

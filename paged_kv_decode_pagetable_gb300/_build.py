@@ -16,7 +16,7 @@ LIB = os.path.join(PKG, "libpkv.so")
 SOURCES = ["common.cu", "pagetable.cpp", "kv_append.cu", "kv_append_q8.cu", "kv_copy_pages.cu", "qk_norm_rope.cu",
            "decode_attn.cu", "decode_attn_q8.cu", "decode_attn_noalloc.cu", "prefill_attn.cu", "prefill_tc.cu",
            "prefill_tc_wide.cu", "block_mask_convert.cu", "tree_append.cu", "tree_attn.cu", "tree_verify.cu",
-           "kv_keep_path.cu"]
+           "kv_keep_path.cu", "tree_args.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "-I", os.path.join(ROOT, "include")]

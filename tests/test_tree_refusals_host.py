@@ -134,8 +134,13 @@ A = 1 << 20        # a 16-byte aligned address that nothing follows
 
 
 def raw(fn, order, base, change):
-    args = {**base, **change}
-    return getattr(pkv.load_library(), fn)(*[args[k] for k in order])
+    """The library's answer, the same to the arguments one by one and in a record."""
+    lib, args = pkv.load_library(), [{**base, **change}[k] for k in order]
+    status, said = getattr(lib, fn)(*args), lib.pkv_last_error()
+    record = pkv._RECORDS[fn].pack(*[0 if a is None else a for a in args])
+    assert getattr(lib, fn + "_args")(record) == status
+    assert lib.pkv_last_error() == said
+    return status
 
 
 ATTN = dict(q=A, k=A, v=A, table=A, n_slots=3, max_pages=2, page_size=16, n_pages=4, slots=A,
@@ -200,9 +205,26 @@ def test_verify_of_the_library(change):
 def test_keep_path_of_the_library(change):
     a = {**dict(cache=A, heads=2, bytes=128, n=1, table=A, n_slots=3, max_pages=2, page_size=16,
                 n_pages=4, slots=A, ctx=A, acc=A, path=A, cols=4, B=2), **change}
-    st = pkv.load_library().kv_keep_path(
-        (ctypes.c_void_p * 1)(a["cache"]), (ctypes.c_int * 1)(a["heads"]),
-        (ctypes.c_int64 * 1)(a["bytes"]), a["n"], a["table"], a["n_slots"], a["max_pages"],
-        a["page_size"], a["n_pages"], a["slots"], a["ctx"], a["acc"], a["path"], a["cols"], a["B"],
-        None, None)
-    assert st == pkv.PKV_E_BAD_ARG
+    caches = ((ctypes.c_void_p * 1)(a["cache"]), (ctypes.c_int * 1)(a["heads"]),
+              (ctypes.c_int64 * 1)(a["bytes"]))
+    rest = dict(n=a["n"], table=a["table"], n_slots=a["n_slots"], max_pages=a["max_pages"],
+                page_size=a["page_size"], n_pages=a["n_pages"], slots=a["slots"], ctx=a["ctx"],
+                acc=a["acc"], path=a["path"], cols=a["cols"], B=a["B"], err=None, stream=None)
+    base = {**{i: ctypes.addressof(c) for i, c in enumerate(caches)}, **rest}
+    assert raw("kv_keep_path", list(base), base, {}) == pkv.PKV_E_BAD_ARG
+
+
+@pytest.mark.parametrize("fn", list(pkv._RECORDS))
+def test_a_record_is_needed(fn):
+    assert getattr(pkv.load_library(), fn + "_args")(None) == pkv.PKV_E_BAD_ARG
+
+
+@pytest.mark.parametrize("call,args,change", [
+    (pkv.tree_qkv_norm_rope_append, append_args, dict(rotary_dims=1 << 40)),
+    (pkv.tree_qkv_norm_rope_append, append_args, dict(theta=1e300)),
+    (pkv.paged_tree_attn, attn_args, dict(window=1 << 40)),
+    (pkv.paged_tree_attn, attn_args, dict(window=-(1 << 40))),
+    (pkv.paged_tree_attn, attn_args, dict(scale=1e300))])
+def test_numbers_that_no_argument_holds(call, args, change, monkeypatch):
+    monkeypatch.setattr(pkv, "_on_device", lambda *t: None)
+    refused(call, args(), change)
