@@ -850,8 +850,9 @@ TREE_MAX = 64
 # Each call looks its tensors over in one go (_fits, _fits_i32: about 0.3 us a tensor) and only
 # where something does not fit finds out what, and raises, in its _refuse_ function (with
 # everything told apart first, the binding took 13.9 us for an append, 8.3 for an attention, 10.0
-# for a verification, 41.2 for a move of 48 caches; so 7.5, 4.4, 4.6 and 20.4). The arguments
-# go to the library in a record: one by one, ctypes took 4 us for the append's 31.
+# for a verification, 41.2 for a move of 48 caches; so 6.4, 4.7, 4.8 and 20.3 with the call
+# itself). The arguments go to the library in a record: one by one, ctypes took 2 us longer for
+# the append's 31.
 
 _RECORDS = {
     "tree_qkv_norm_rope_append": struct.Struct("@3P3q6P2f7iP4i5P"),
@@ -862,13 +863,8 @@ _RECORDS = {
 _pack_append, _pack_attn, _pack_verify, _pack_keep = (r.pack for r in _RECORDS.values())
 
 
-def _call(name, fn, pack, *args) -> None:
-    try:
-        status = fn(pack(*args))
-    except (struct.error, OverflowError) as e:
-        raise BadArgError(f"{name}: {e}") from None
-    if status:
-        _check(status, name)
+# what a record does not hold, such as numbers beyond their type's range
+_UNPACKABLE = (struct.error, OverflowError)
 
 
 def _fits(t, dtype, shape, dev) -> bool:
@@ -977,17 +973,22 @@ def tree_qkv_norm_rope_append(q, k, v, gamma_q, gamma_k, batch_idx, ctx_lens, ro
         B, N, Hq, Hkv, D, sq, sk, sv, dev = _refuse_append(
             q, k, v, gamma_q, gamma_k, batch_idx, ctx_lens, row_start, parents, dev_table, n_slots,
             max_pages_per_seq, page_size, n_pages, k_cache, v_cache, q_out, err_word)
-    lib = load_library()
-    _call("tree_qkv_norm_rope_append", lib.tree_qkv_norm_rope_append_args, _pack_append,
-          q.data_ptr(), k.data_ptr(), 0 if v is None else v.data_ptr(), sq, sk, sv,
-          0 if gamma_q is None else gamma_q.data_ptr(),
-          0 if gamma_k is None else gamma_k.data_ptr(),
-          0 if batch_idx is None else batch_idx.data_ptr(), ctx_lens.data_ptr(),
-          row_start.data_ptr(), parents.data_ptr(), float(theta), float(eps),
-          D if rotary_dims is None else int(rotary_dims), 1 if v_norm else 0, B, N, Hq, Hkv, D,
-          dev_table.data_ptr(), n_slots, max_pages_per_seq, page_size, n_pages,
-          k_cache.data_ptr(), v_cache.data_ptr(), q_out.data_ptr(),
-          0 if err_word is None else err_word.data_ptr(), _stream_on(stream, dev) or 0)
+    lib = _lib or load_library()
+    try:
+        status = lib.tree_qkv_norm_rope_append_args(_pack_append(
+            q.data_ptr(), k.data_ptr(), 0 if v is None else v.data_ptr(), sq, sk, sv,
+            0 if gamma_q is None else gamma_q.data_ptr(),
+            0 if gamma_k is None else gamma_k.data_ptr(),
+            0 if batch_idx is None else batch_idx.data_ptr(), ctx_lens.data_ptr(),
+            row_start.data_ptr(), parents.data_ptr(), float(theta), float(eps),
+            D if rotary_dims is None else int(rotary_dims), 1 if v_norm else 0, B, N, Hq, Hkv, D,
+            dev_table.data_ptr(), n_slots, max_pages_per_seq, page_size, n_pages,
+            k_cache.data_ptr(), v_cache.data_ptr(), q_out.data_ptr(),
+            0 if err_word is None else err_word.data_ptr(), _stream_on(stream, dev) or 0))
+    except _UNPACKABLE as e:
+        raise BadArgError(f"tree_qkv_norm_rope_append: {e}") from None
+    if status:
+        _check(status, "tree_qkv_norm_rope_append")
 
 
 def _refuse_append(q, k, v, gamma_q, gamma_k, batch_idx, ctx_lens, row_start, parents, dev_table,
@@ -1048,14 +1049,18 @@ def paged_tree_attn(q, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq, 
         B, N, Hq, Hkv, D, dev = _refuse_attn(
             q, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq, page_size, n_pages,
             batch_idx, ctx_lens, row_start, parents, workspace, out, err_word)
-    lib = load_library()
-    _call("paged_tree_attn", lib.paged_tree_attn_args, _pack_attn, q.data_ptr(),
-          k_cache.data_ptr(), v_cache.data_ptr(), dev_table.data_ptr(), n_slots,
-          max_pages_per_seq, page_size, n_pages,
-          0 if batch_idx is None else batch_idx.data_ptr(), ctx_lens.data_ptr(),
-          row_start.data_ptr(), parents.data_ptr(), int(window), float(scale), B, N, Hq, Hkv, D,
-          workspace.data_ptr(), workspace.nbytes, out.data_ptr(),
-          0 if err_word is None else err_word.data_ptr(), _stream_on(stream, dev) or 0)
+    lib = _lib or load_library()
+    try:
+        status = lib.paged_tree_attn_args(_pack_attn(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), dev_table.data_ptr(), n_slots,
+            max_pages_per_seq, page_size, n_pages, 0 if batch_idx is None else batch_idx.data_ptr(),
+            ctx_lens.data_ptr(), row_start.data_ptr(), parents.data_ptr(), int(window),
+            float(scale), B, N, Hq, Hkv, D, workspace.data_ptr(), workspace.nbytes, out.data_ptr(),
+            0 if err_word is None else err_word.data_ptr(), _stream_on(stream, dev) or 0))
+    except _UNPACKABLE as e:
+        raise BadArgError(f"paged_tree_attn: {e}") from None
+    if status:
+        _check(status, "paged_tree_attn")
 
 
 def _refuse_attn(q, k_cache, v_cache, dev_table, n_slots, max_pages_per_seq, page_size, n_pages,
@@ -1125,12 +1130,18 @@ def tree_verify(target_probs, draft_probs, tokens, row_start, parents, u_accept,
         B, N, V, cols, sp, sq, dev = _refuse_verify(
             target_probs, draft_probs, tokens, row_start, parents, u_accept, u_pick, accepted, path,
             next_token, err_word)
-    lib = load_library()
-    _call("tree_verify", lib.tree_verify_args, _pack_verify, target_probs.data_ptr(), sp,
-          0 if draft_probs is None else draft_probs.data_ptr(), sq, tokens.data_ptr(),
-          row_start.data_ptr(), parents.data_ptr(), u_accept.data_ptr(), u_pick.data_ptr(), B, N,
-          V, cols, accepted.data_ptr(), path.data_ptr(), next_token.data_ptr(),
-          0 if err_word is None else err_word.data_ptr(), _stream_on(stream, dev) or 0)
+    lib = _lib or load_library()
+    try:
+        status = lib.tree_verify_args(_pack_verify(
+            target_probs.data_ptr(), sp, 0 if draft_probs is None else draft_probs.data_ptr(), sq,
+            tokens.data_ptr(), row_start.data_ptr(), parents.data_ptr(), u_accept.data_ptr(),
+            u_pick.data_ptr(), B, N, V, cols, accepted.data_ptr(), path.data_ptr(),
+            next_token.data_ptr(), 0 if err_word is None else err_word.data_ptr(),
+            _stream_on(stream, dev) or 0))
+    except _UNPACKABLE as e:
+        raise BadArgError(f"tree_verify: {e}") from None
+    if status:
+        _check(status, "tree_verify")
 
 
 def _refuse_verify(target_probs, draft_probs, tokens, row_start, parents, u_accept, u_pick,
@@ -1193,13 +1204,18 @@ def kv_keep_path(caches, dev_table, n_slots, max_pages_per_seq, page_size, n_pag
         B, cols, n, ptrs, heads, nbytes, dev = _refuse_keep(
             caches, dev_table, n_slots, max_pages_per_seq, page_size, n_pages, batch_idx, ctx_lens,
             accepted, path, err_word)
-    lib = load_library()
-    _call("kv_keep_path", lib.kv_keep_path_args, _pack_keep, ptrs.buffer_info()[0],
-          heads.buffer_info()[0], nbytes.buffer_info()[0], n, dev_table.data_ptr(), n_slots,
-          max_pages_per_seq, page_size, n_pages,
-          0 if batch_idx is None else batch_idx.data_ptr(), ctx_lens.data_ptr(),
-          accepted.data_ptr(), path.data_ptr(), cols, B,
-          0 if err_word is None else err_word.data_ptr(), _stream_on(stream, dev) or 0)
+    lib = _lib or load_library()
+    try:
+        status = lib.kv_keep_path_args(_pack_keep(
+            ptrs.buffer_info()[0], heads.buffer_info()[0], nbytes.buffer_info()[0], n,
+            dev_table.data_ptr(), n_slots, max_pages_per_seq, page_size, n_pages,
+            0 if batch_idx is None else batch_idx.data_ptr(), ctx_lens.data_ptr(),
+            accepted.data_ptr(), path.data_ptr(), cols, B,
+            0 if err_word is None else err_word.data_ptr(), _stream_on(stream, dev) or 0))
+    except _UNPACKABLE as e:
+        raise BadArgError(f"kv_keep_path: {e}") from None
+    if status:
+        _check(status, "kv_keep_path")
 
 
 _T = torch.Tensor
