@@ -29,8 +29,8 @@
  *     memory that kernel may write, so in-stream order is kept. The decode
  *     attention and the fused step read seq_lens, batch_idx and the page
  *     table BEFORE that wait, to plan their work while earlier kernels
- *     drain, and paged_tree_attn reads row_start, ctx_lens and batch_idx. So
- *     those must be written by copies or by kernels that do
+ *     drain, and paged_tree_attn reads row_start, ctx_lens, batch_idx and the
+ *     page table. So those must be written by copies or by kernels that do
  *     not let their dependents start early (ordinary kernels); none of this
  *     library's kernels writes them.
  *   - Device-side faults are never raised on purpose: an invalid index read

@@ -29,7 +29,8 @@
 // order: results do not depend on timing and no CTA waits for another. (Shares that begin at a
 // unit's edge where that is near, to cut fewer: 56 -> 71 us for 64 nodes at D = 512, 39 -> 42 for
 // the rollout batch.) The line is planned from row_start, ctx_lens and batch_idx before the prior
-// kernel has ended.
+// kernel has ended, and the first tiles, which the table names, are then on their way to L2 (the
+// rollout batch 37.3 -> 36.2 us, one row of 41 tokens 4.6 -> 4.4).
 //   warps 0-7 (softmax): D <= 128 with 64 columns, two units at a time, four warps each, so that
 //     one unit's start and end overlap the other's tiles; else one unit, its columns in two
 //     halves. Warp w has the keys of TMEM lanes 32 (w % 4) ..: masks, weights, references, a
@@ -51,13 +52,13 @@
 // the loops kept as loops, the short waits, and one site of each product.
 //
 // Measured (6769 GB/s measured): 16 rows of 16k to 32k tokens, 8-node chains, 8 heads of 128,
-// 240 us, 0.99 of reading them; 64 rows of 100 to 1024 tokens, trees of 8, 37 us, 0.61: its start
+// 240 us, 0.99 of reading them; 64 rows of 100 to 1024 tokens, trees of 8, 36 us, 0.63: its start
 // (launch, plan, the rings' first fill) and its end (last tiles, join) are 6 us each; 64 rows of
-// 256 to 2048 tokens in a window of 512, trees of 16, one head of 256, 28 us, 0.21, and 16 rows
-// with trees of 64, one head of 512, 52 us, 0.15: they write and read as many bytes in parts as
+// 256 to 2048 tokens in a window of 512, trees of 16, one head of 256, 27 us, 0.21, and 16 rows
+// with trees of 64, one head of 512, 51 us, 0.15: they write and read as many bytes in parts as
 // in keys, at D = 512 every 8 nodes read the keys again, and a tile's weights, P V and the next
 // one's weights stand behind one another (there is no room for a second P); one row of 41 tokens
-// 4.7 us.
+// 4.4 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -173,6 +174,7 @@ constexpr size_t smem_bytes() {
 
 struct Args {
   const int32_t *table, *batch_idx, *ctx_lens, *row_start, *parents;
+  const __nv_bfloat16 *k, *v;   // (what the maps name, for prefetches)
   __nv_bfloat16 *out;
   float *parts;
   int *arrived;   // [kLevels][2 kMaxCtas]
@@ -476,8 +478,10 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
   Line line;
   line.begin(rows, a, x0, x1);
   const Part &p = line.p;
-  // (what the prior kernel may write or read - caches, queries, workspace, output - from here on)
-  pkv_wait_prior_grid();
+  // (what the prior kernel may write or read - caches, queries, workspace, output - from here on;
+  // the producers wait below)
+  const bool producer = warp == C::PROD || warp == C::PROD + 1;
+  if (!producer) pkv_wait_prior_grid();
   if (!C::JOINS && tid == 0) a.cuts[cta].cols = 0;
 
   // whether some columns do not see some keys of the unit's tile t
@@ -485,7 +489,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
     const int j0 = (p.tile0 + t) * kTile;
     return j0 + kTile > p.ctx || (a.window > 0 && j0 <= p.ctx + p.n - 1 - a.window);
   };
-  if (warp == C::PROD || warp == C::PROD + 1) {
+  if (producer) {
     // ==================== producers, of K and of V ====================
     // (a warp goes through its boxes as one, and an elected lane issues them, as the MMAs)
     const bool is_v = warp != C::PROD;
@@ -547,6 +551,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
         }
       }
     };
+    bool waited = false;
     while (ok && line.next()) {
       if (p.t0 == p.t1) continue;
       const int32_t *row = a.table + static_cast<long long>(rows.slot[p.b]) * a.max_pages;
@@ -559,6 +564,25 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
       };
       int base = ((p.tile0 + p.t0) * kTile) >> a.log_page;
       int now = fetch(base + lane), then = fetch(base + 32 + lane);
+      if (!waited) {
+        // The first tiles' way to L2 begins before the prior kernel has ended: nothing is read
+        // that it may still write.
+        constexpr int kRows = D <= 128 ? 32768 / D : kTile;        // of 64 KB, or a tile
+        const int from = ((p.tile0 + p.t0) * kTile) & (a.page_size - 1);   // (large pages)
+        const int n = min(kRows, (p.t1 - p.t0) * kTile), size = min(a.page_size - from, n);
+        if (lane * a.page_size < n && base + lane >= first_page && base + lane <= last_page &&
+            now >= 0 && now < a.n_pages) {
+          const long long at =
+              static_cast<long long>(p.head) * a.n_pages * a.page_size +
+              static_cast<long long>(now) * a.page_size + from;
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                           (is_v ? a.v : a.k) + at * D),
+                       "r"(size * D * 2));
+        }
+        __syncwarp();
+        pkv_wait_prior_grid();
+        waited = true;
+      }
 #pragma unroll 1
       for (int t = p.t0; t < p.t1 && ok; ++t) {
         const int j0 = (p.tile0 + t) * kTile, page0 = j0 >> a.log_page;
@@ -1387,6 +1411,8 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
   while (times < most && (most % times || 1LL * times * least * a.B < a.N)) ++times;
   const int box_nodes = times * least;
   a.box_nodes = box_nodes;
+  a.k = reinterpret_cast<const __nv_bfloat16 *>(k);
+  a.v = reinterpret_cast<const __nv_bfloat16 *>(v);
   a.arrived = static_cast<int *>(workspace);
   a.cuts = reinterpret_cast<Cut *>(static_cast<char *>(workspace) + kArrivedBytes);
   a.parts = reinterpret_cast<float *>(a.cuts + kMaxCtas);
@@ -1413,9 +1439,9 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
 // a row are then read half as often (16 rows of 1k to 3k tokens, 8 heads of 128: trees of 64
 // 90 -> 78 us, of 32 58 -> 52, since then 69 and 44; one head of 256, 128 rows of up to 2k tokens,
 // trees of 16 62 -> 55). But at D = 256 rows of up to 128 columns in a window of up to 512 are cut
-// into more units, of few tiles either way (trees of 16, 64 rows 31 us by 128, 28 by 64, 8 rows 18.5
-// and 15.6; a window of 1024 35 and 35, of 2048 43 and 47, trees of 64 31 and 32). At D = 512 TMEM
-// holds 64.
+// into more units, of few tiles either way (trees of 16, 64 rows 31 us by 128, 28 by 64, 8 rows
+// 18.5 and 15.6; a window of 1024 35 and 35, of 2048 43 and 47, trees of 64 31 and 32). At D = 512
+// TMEM holds 64.
 template <int D>
 int launch_for(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, const Args &a,
                void *workspace, cudaStream_t s) {
