@@ -247,6 +247,40 @@ def test_unused_columns_change_nothing(D, G, ns):
         assert torch.equal(got, want), fill
 
 
+@pytest.mark.parametrize("D", [128, 256])
+def test_lengths_and_trees_written_by_the_kernel_before(D):
+    """What a call reads before the kernel ahead of it has ended may come from that kernel, if it
+    is an ordinary one."""
+    rng = rng_of(25, D)
+    B, n = 24, 9
+    c = TreeCase(rng, 8, 2, D, 32, rng.integers(400, 1500, B),
+                 [random_tree(rng, n, 3) for _ in range(B)]).device(pkv)
+    kinds = []
+    for _ in range(3):
+        ctx = torch.tensor(rng.integers(0, 400, B), dtype=torch.int32, device="cuda")
+        cut = np.sort(rng.integers(0, B * n + 1, B - 1))
+        start = np.concatenate([[0], cut, [B * n]])
+        # rows out of the same packed nodes (one of more than 64 is left as it is), all of them roots
+        start = np.minimum.accumulate(np.minimum(start, np.arange(B + 1) * 60)[::-1])[::-1]
+        kinds.append((ctx, torch.tensor(start.copy(), dtype=torch.int32, device="cuda"),
+                      torch.full((B * n,), -1, dtype=torch.int32, device="cuda")))
+    ctx, start, parents = (x.clone() for x in kinds[0])
+    want = []
+    for k in kinds:
+        torch.cuda.synchronize()
+        out = torch.full_like(c.out, 7.0)
+        want.append(c.call(pkv, ctx=k[0], row_start=k[1], parents=k[2], out=out).clone())
+    outs = [torch.full_like(c.out, 7.0) for _ in range(60)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        for to, value in zip((ctx, start, parents), kinds[i % 3]):
+            torch.add(value, 0, out=to)
+        c.call(pkv, ctx=ctx, row_start=start, parents=parents, out=out)
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        assert torch.equal(out, want[i % 3]), i
+
+
 def test_cache_beyond_32_bits():
     """Rows whose elements lie past 2^32: the last pages of a 9 GB cache."""
     D, ps, P, Hkv = 128, 128, 1 << 17, 2
