@@ -7,8 +7,8 @@
 //
 // Bound by reading each key and value of a row's context once for all its nodes and the query
 // heads of a kv head, until nodes x heads reach a few hundred. Those "columns" are the N of both
-// products, at most 64 of them a unit of work, or 128 where the rows have more than 64 (and TMEM
-// has room, D <= 256), so that a small tree costs no more arithmetic than it has columns:
+// products, at most 64 of them a unit of work, or 128 where the rows have more than 64 (and D <=
+// 128), so that a small tree costs no more arithmetic than it has columns:
 //   S^T = K q^T    M = 128 keys of a tile, N columns, both operands K-major,
 //   O^T = V^T P^T  M = 128 columns of D, N columns, K = the tile's 128 keys, both MN-major: V as
 //                  it lies in the cache, P as the threads write it, a key's columns in a row.
@@ -40,8 +40,7 @@
 //     parents by pointer doubling;
 //   warps 11, 12: the MMAs of S and of P V. With one warp for both, and one ring, each waited
 //     while the other could have been issued; and an entry of 32 KB a barrier, not 16, halves the
-//     waits (16 rows with trees of 64: one head of 512 55 -> 52 us, of 256, up to 8k tokens,
-//     91 -> 82).
+//     waits (16 rows with trees of 64: one head of 512 55 -> 52 us).
 // Rows of V that no node sees are cleared in shared memory (0 x NaN would reach every column);
 // one that is not finite and seen by some nodes only is cleared too and those nodes' results
 // are NaN: nothing of it reaches the others. So that this is between a tile's arrival and its
@@ -107,9 +106,7 @@ struct Cfg {
   static constexpr int E = D == 64 ? 1 : D / 128;       // entries of a K tile, and of a V tile
   static constexpr int KEYS = kTile / ATOMS;            // of a half of V, one after the other
   // as many as shared memory holds, in a ring for K and one for V
-  static constexpr int NS = D == 64                   ? (COLS == 128 ? 9 : 10)
-                            : D == 256 && COLS == 128 ? 3
-                                                      : 4;
+  static constexpr int NS = D == 64 ? (COLS == 128 ? 9 : 10) : 4;
   static constexpr int NK = NS / 2, NV = NS - NK;
   static constexpr int Q_ATOM = COLS * 128;
   static constexpr int Q_BYTES = D / 64 * Q_ATOM;
@@ -119,9 +116,8 @@ struct Cfg {
   static constexpr int OFF_P = OFF_Q + UNITS * Q_BYTES; // [UNITS]
   static constexpr int OFF_ONES = OFF_P + UNITS * P_BYTES;  // one swizzle atom of ones
   static constexpr int OFF_SMALL = OFF_ONES + 1024;
-  // of a unit: S of two tiles (of one where TMEM has no room), O^T's blocks, the sums of the
-  // weights (in every lane)
-  static constexpr int SB = D == 256 && COLS == 128 ? 1 : 2;
+  // of a unit: S of two tiles, O^T's blocks, the sums of the weights (in every lane)
+  static constexpr int SB = 2;
   static constexpr int S_COL = 0, O_COL = SB * COLS, L_COL = O_COL + E * COLS;
   static constexpr int UNIT_COLS = 512 / UNITS;
   static_assert(L_COL + COLS <= UNIT_COLS, "TMEM");
@@ -244,7 +240,7 @@ __device__ __forceinline__ void group_sync(int grp) {
 // the maximum over the 32 lanes (NaN only where all are)
 __device__ __forceinline__ float lane_max(float x) {
   float r;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -1437,22 +1433,18 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
 
 // Units of 128 columns where the rows have more than 64, by the packed nodes a row: the keys of
 // a row are then read half as often (16 rows of 1k to 3k tokens, 8 heads of 128: trees of 64
-// 90 -> 78 us, of 32 58 -> 52, since then 69 and 44; one head of 256, 128 rows of up to 2k tokens,
-// trees of 16 62 -> 55). But at D = 256 rows of up to 128 columns in a window of up to 512 are cut
-// into more units, of few tiles either way (trees of 16, 64 rows 31 us by 128, 28 by 64, 8 rows
-// 18.5 and 15.6; a window of 1024 35 and 35, of 2048 43 and 47, trees of 64 31 and 32). At D = 512
-// TMEM holds 64.
+// 90 -> 78 us, of 32 58 -> 52, since then 69 and 44). At D >= 256 units have 64: at 512 TMEM holds
+// no more, at 256 it would hold one buffer of S and shared memory three entries (16 rows of up to
+// 8k tokens with trees of 64 82 us, not 85, in a window of 512 trees of 16 31, not 28).
 template <int D>
 int launch_for(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, const Args &a,
                void *workspace, cudaStream_t s) {
-  const long long columns = static_cast<long long>(a.N) * a.G;   // of all rows
-  const bool few_tiles = D == 256 && a.window > 0 && a.window <= 512 && columns <= 128LL * a.B;
-  if (D <= 256 && columns > 64LL * a.B && !few_tiles)
-    return launch<D, D <= 256 ? 128 : 64>(q, k, v, a, workspace, s);
+  if (D <= 128 && static_cast<long long>(a.N) * a.G > 64LL * a.B)
+    return launch<D, D <= 128 ? 128 : 64>(q, k, v, a, workspace, s);
   return launch<D, 64>(q, k, v, a, workspace, s);
 }
 
-size_t record_floats(int D) { return static_cast<size_t>(D <= 256 ? 128 : 64) * (D + 2); }
+size_t record_floats(int D) { return static_cast<size_t>(D <= 128 ? 128 : 64) * (D + 2); }
 
 }  // namespace
 

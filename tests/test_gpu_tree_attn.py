@@ -37,8 +37,8 @@ def test_nodes(D, nodes):
 @pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 6, 7, 8])
 @pytest.mark.parametrize("window", [0, 40])
 def test_more_columns_than_64(D, G, window):
-    """Rows of many nodes take units of 128 columns; heads of a node may fall to both halves,
-    rows of few nodes stand beside them."""
+    """Rows of many nodes take units of 128 columns (of 64 at D = 256); heads of a node may fall
+    to both halves, rows of few nodes stand beside them."""
     rng = rng_of(20, D, G, window)
     ns = (64, 64, 61) if G <= 2 else (64, 30, 1, 41)
     trees = [random_tree(rng, n, w) for n, w in zip(ns, (4, 1, 8, 2))]
@@ -83,8 +83,7 @@ def test_windows(window, D, G):
 @pytest.mark.parametrize("window", [1, 300, 511, 512, 513])
 @pytest.mark.parametrize("ns", [(9, 16, 20), (16, 16, 16), (17, 16, 16)])
 def test_units_of_short_windows(window, ns):
-    """Rows of up to and more than 128 columns on both sides of the window that decides how many
-    a unit has."""
+    """Rows of up to and more than 128 columns in windows around a multiple of the tile."""
     rng = rng_of(24, window, *ns)
     trees = [random_tree(rng, n, 3) for n in ns]
     TreeCase(rng, 8, 1, 256, 64, [2000, 511, 90], trees, window=window).device(pkv).check(pkv)
