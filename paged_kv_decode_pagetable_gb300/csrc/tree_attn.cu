@@ -22,9 +22,8 @@
 // V's place: every lane of TMEM has them, and no thread keeps a sum for each column. Weights are
 // rounded to bf16 (V's type) and summed as rounded; scores, references and O are fp32.
 //
-// Work: the units' tiles, one more place for each unit's start (2 and 3: 40 and 42 us for the
-// rollout batch, not 39), lie on one line, cut into equal shares for one persistent CTA an SM from
-// the lengths, on the device. A unit that is cut leaves its parts (O, reference and sum, fp32) in
+// Work: the units' tiles and one or two more places for each unit's start lie on one line, cut into
+// equal shares for one persistent CTA an SM from the lengths, on the device. A unit that is cut leaves its parts (O, reference and sum, fp32) in
 // the workspace, and whoever writes the last of them, or a second kernel, joins them in their
 // order: results do not depend on timing and no CTA waits for another. (Shares that begin at a
 // unit's edge where that is near, to cut fewer: 56 -> 71 us for 64 nodes at D = 512, 39 -> 42 for
@@ -54,7 +53,7 @@
 // 240 us, 0.99 of reading them; 64 rows of 100 to 1024 tokens, trees of 8, 36 us, 0.63: its start
 // (launch, plan, the rings' first fill) and its end (last tiles, join) are 6 us each; 64 rows of
 // 256 to 2048 tokens in a window of 512, trees of 16, one head of 256, 27 us, 0.21, and 16 rows
-// with trees of 64, one head of 512, 51 us, 0.15: they write and read as many bytes in parts as
+// with trees of 64, one head of 512, 48 us, 0.16: they write and read as many bytes in parts as
 // in keys, at D = 512 every 8 nodes read the keys again, and a tile's weights, P V and the next
 // one's weights stand behind one another (there is no room for a second P); one row of 41 tokens
 // 4.4 us.
@@ -72,7 +71,6 @@
 namespace {
 
 constexpr int kTile = 128;               // keys of a tile
-constexpr int kStart = 1;                // places on the line for a unit's start
 constexpr int kMaxCtas = 160;            // CTAs the workspace has room for
 constexpr float kLazyLog2 = 8.f;
 constexpr int kMostPlaces = 0x7fffffff;  // as many and more are reported, not computed
@@ -96,6 +94,11 @@ struct Cfg {
   // from 38.7 to 37.4; but the window of 512 at D = 256 from 30 to 38 and trees of 64 at D = 512
   // from 56 to 61, where one CTA's few warps read up to 128 KB a part.
   static constexpr bool JOINS = UNITS == 2;
+  // Places on the line for a unit's start and end: where units go in twos one's overlap the other's
+  // tiles (2 and 3: 40 and 42 us for the rollout batch, not 39, at the time), else they take as
+  // long as two tiles (16 rows with trees of 64, one head of 512 51 -> 48 us; 64 rows of up to 1k
+  // tokens with trees of 24, eight heads of 128 64 -> 57).
+  static constexpr int START = UNITS == 2 ? 1 : 2;
   static constexpr int SOFT = 8;                        // softmax warps of all units
   static constexpr int PROD = SOFT, PREP = SOFT + 2, MMA = SOFT + 3;
   static constexpr int THREADS = (SOFT + 5) * 32;
@@ -264,6 +267,7 @@ struct Part {
 };
 
 // Goes through a CTA's share of the line, part by part.
+template <int START>
 struct Line {
   const Rows *sm;
   const Args *a;
@@ -293,7 +297,7 @@ struct Line {
       else r = m;
     }
     row(l);
-    const int cost = p.ntiles + kStart, units = (p.n + args.unit_tokens - 1) / args.unit_tokens;
+    const int cost = p.ntiles + START, units = (p.n + args.unit_tokens - 1) / args.unit_tokens;
     const int u = (x0 - s.pre[l]) / cost;
     off = x0 - s.pre[l] - u * cost;
     p.head = u / units;
@@ -302,7 +306,7 @@ struct Line {
   // the next part, in p
   __device__ bool next() {
     if (pos >= end) return false;
-    if (off == p.ntiles + kStart) {   // behind a unit: the next nodes, head or row with nodes
+    if (off == p.ntiles + START) {   // behind a unit: the next nodes, head or row with nodes
       off = 0;
       p.tok0 += a->unit_tokens;
       if (p.tok0 >= p.n) {
@@ -317,9 +321,9 @@ struct Line {
       }
     }
     p.toks = min(a->unit_tokens, p.n - p.tok0);
-    const int to = min(p.ntiles + kStart, off + (end - pos));
-    p.t0 = max(0, off - kStart);
-    p.t1 = max(0, to - kStart);
+    const int to = min(p.ntiles + START, off + (end - pos));
+    p.t0 = max(0, off - START);
+    p.t1 = max(0, to - START);
     p.start = pos - off;
     pos += to - off;
     off = to;
@@ -435,7 +439,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
           const int lo = a.window > 0 ? max(0, r.ctx - a.window + 1) : 0;
           const int tiles = r.slot == 0 ? 0 : (r.ctx + r.n - 1) / kTile - lo / kTile + 1;
           mine[i] = static_cast<int>(min(static_cast<long long>(kMostPlaces),
-                                         static_cast<long long>(tiles + kStart) *
+                                         static_cast<long long>(tiles + C::START) *
                                              (a.Hkv * ((r.n + a.unit_tokens - 1) /
                                                        a.unit_tokens))));
         }
@@ -471,7 +475,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
   const int ctas = min(static_cast<int>(gridDim.x), W);
   const int x0 = cta < ctas ? share(W, cta, ctas) : 0;
   const int x1 = cta < ctas ? share(W, cta + 1, ctas) : 0;
-  Line line;
+  Line<C::START> line;
   line.begin(rows, a, x0, x1);
   const Part &p = line.p;
   // (what the prior kernel may write or read - caches, queries, workspace, output - from here on;
@@ -851,8 +855,8 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
     // into the first's place, goes on with four such, and writes the output in the end. In the
     // parts' order whoever it is; nobody waits.
     auto join = [&](int cols) {
-      const int first_cta = p.t0 == 0 ? cta : share_of(W, p.start + kStart, ctas);
-      const int parts = share_of(W, p.start + kStart + p.ntiles - 1, ctas) - first_cta + 1;
+      const int first_cta = p.t0 == 0 ? cta : share_of(W, p.start + C::START, ctas);
+      const int parts = share_of(W, p.start + C::START + p.ntiles - 1, ctas) - first_cta + 1;
       auto place = [&](int i) { return 2 * (first_cta + i) + (i == 0 ? 1 : 0); };
       int i = cta - first_cta;
 #pragma unroll 1
@@ -1254,7 +1258,7 @@ __global__ void __launch_bounds__(Cfg<D, MOST>::THREADS, 1)
       }
       if (!C::JOINS && tid == 0 && !whole && p.t0 == 0) {
         // the CTA of the unit's last tile
-        const int c = share_of(W, p.start + kStart + p.ntiles - 1, ctas);
+        const int c = share_of(W, p.start + C::START + p.ntiles - 1, ctas);
         const Cut cut = {p.n0 + p.tok0, cols, p.head, c - cta + 1};
         a.cuts[cta] = cut;
       }
@@ -1433,9 +1437,9 @@ int launch(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, Args a, void
 
 // Units of 128 columns where the rows have more than 64, by the packed nodes a row: the keys of
 // a row are then read half as often (16 rows of 1k to 3k tokens, 8 heads of 128: trees of 64
-// 90 -> 78 us, of 32 58 -> 52, since then 69 and 44). At D >= 256 units have 64: at 512 TMEM holds
+// 90 -> 78 us, of 32 58 -> 52, since then 67 and 43). At D >= 256 units have 64: at 512 TMEM holds
 // no more, at 256 it would hold one buffer of S and shared memory three entries (16 rows of up to
-// 8k tokens with trees of 64 82 us, not 85, in a window of 512 trees of 16 31, not 28).
+// 8k tokens with trees of 64 82 us, not 84, in a window of 512 trees of 16 31, not 28).
 template <int D>
 int launch_for(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, const Args &a,
                void *workspace, cudaStream_t s) {
