@@ -23,13 +23,14 @@
 // rounded to bf16 (V's type) and summed as rounded; scores, references and O are fp32.
 //
 // Work: the units' tiles and one or two more places for each unit's start lie on one line, cut into
-// equal shares for one persistent CTA an SM from the lengths, on the device. A unit that is cut leaves its parts (O, reference and sum, fp32) in
-// the workspace, and whoever writes the last of them, or a second kernel, joins them in their
-// order: results do not depend on timing and no CTA waits for another. (Shares that begin at a
-// unit's edge where that is near, to cut fewer: 56 -> 71 us for 64 nodes at D = 512, 39 -> 42 for
-// the rollout batch.) The line is planned from row_start, ctx_lens and batch_idx before the prior
-// kernel has ended, and the first tiles, which the table names, are then on their way to L2 (the
-// rollout batch 37.3 -> 36.2 us, one row of 41 tokens 4.6 -> 4.4).
+// equal shares for one persistent CTA an SM from the lengths, on the device. A unit that is cut
+// leaves its parts (O, reference and sum, fp32) in the workspace, and whoever writes the last of
+// them, or a second kernel, joins them in their order: results do not depend on timing and no CTA
+// waits for another. (Shares that begin at a unit's edge where that is near, to cut fewer: 56 -> 71
+// us for 64 nodes at D = 512, 39 -> 42 for the rollout batch.) The line is planned from row_start,
+// ctx_lens and batch_idx before the prior kernel has ended, and the first tiles, which the table
+// names, are then on their way to L2 (the rollout batch 37.3 -> 36.2 us, one row of 41 tokens 4.6
+// -> 4.4).
 //   warps 0-7 (softmax): D <= 128 with 64 columns, two units at a time, four warps each, so that
 //     one unit's start and end overlap the other's tiles; else one unit, its columns in two
 //     halves. Warp w has the keys of TMEM lanes 32 (w % 4) ..: masks, weights, references, a
