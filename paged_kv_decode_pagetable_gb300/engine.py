@@ -216,12 +216,15 @@ def accept_drafts(pt: PageTable, caches, target_probs, draft_probs, tokens, batc
                   stream=None, table=None):
     """After the last layer: tree_verify, then kv_keep_path on `caches` (K and V of every
     layer). Row b's context is then ctx_lens[b] + 1 + accepted[b] tokens long and its next
-    tree begins with next_token[b]; nothing waits for the GPU."""
+    tree begins with next_token[b]; nothing waits for the GPU. The rows are row_start's: buffers
+    kept for more of them keep what they hold behind, and its tokens stay where they are."""
     table = pt.dev_table if table is None else table
     tree_verify(target_probs, draft_probs, tokens, row_start, parents, u_accept, u_pick, accepted,
                 path, next_token, err, stream=stream)
+    B = row_start.numel() - 1
     kv_keep_path(caches, table, pt.n_slots, pt.max_pages_per_seq, pt.page_size, pt.n_pages,
-                 batch_idx, ctx_lens, accepted, path, err, stream=stream)
+                 batch_idx, ctx_lens, accepted, path if path.shape[0] == B else path[:B], err,
+                 stream=stream)
 
 
 @dataclasses.dataclass
