@@ -678,9 +678,10 @@ int tree_verify(const float *target_probs, int64_t target_stride, const float *d
  * bytes, any element type (for an 8-bit cache: one scale a token, the codes and
  * the scales as caches of their own). caches, heads and token_bytes are host
  * arrays; accepted and path as tree_verify writes them (path: int32 [B]
- * [path_cols]). Table entries out of range set PKV_ERR_PAGE_* and the row is
- * left as it is, in all caches. Any alignment; 16-byte aligned caches and
- * tokens copy fastest. token_bytes <= 2^20. */
+ * [path_cols]). A cache named twice (layers that share one) moves once; caches
+ * that overlap otherwise are refused. Table entries out of range set
+ * PKV_ERR_PAGE_* and the row is left as it is, in all caches. Any alignment;
+ * 16-byte aligned caches and tokens copy fastest. token_bytes <= 2^20. */
 int kv_keep_path(void *const *caches, const int *heads, const int64_t *token_bytes,
                  int n_caches, const int32_t *dev_table, int n_slots,
                  int max_pages_per_seq, int page_size, int n_pages,

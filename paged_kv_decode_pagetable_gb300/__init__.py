@@ -1176,7 +1176,7 @@ def kv_keep_path(caches, dev_table, n_slots, max_pages_per_seq, page_size, n_pag
     """After tree_verify: the accepted nodes' tokens move to the positions behind the
     context, in every head of every cache in `caches` (contiguous device tensors
     [heads][n_pages * page_size][...], any element type, all the layers of a
-    model). The rows are path's: of a path kept for more rows than tree_verify was
+    model; one that is named twice moves once). The rows are path's: of a path kept for more rows than tree_verify was
     given, pass those alone (path[:B]), for the others would move once more."""
     try:
         B, cols = path.shape

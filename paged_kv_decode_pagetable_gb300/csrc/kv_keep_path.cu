@@ -10,6 +10,12 @@
 // caches of 8 heads of 128, one launch, 6.6 us (floor 1.9 us of bytes), 8 rows in two 2.9.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <functional>
+#include <memory>
+#include <new>
+#include <numeric>
+
 #include "pkv_internal.h"
 #include "tree.cuh"
 
@@ -146,12 +152,40 @@ extern "C" int kv_keep_path(void *const *caches, const int *heads, const int64_t
   if (!caches || !heads || !token_bytes || !dev_table || !ctx_lens || !accepted || !path)
     return pkv::fail(PKV_E_BAD_ARG, "%s: NULL pointer", fn);
   const long long rows = static_cast<long long>(page_size) * n_pages;
+  bool ascending = true;   // each behind the one before, as a program mostly has them
+  uintptr_t end = 0;
   for (int c = 0; c < n_caches; ++c) {
     if (!caches[c]) return pkv::fail(PKV_E_BAD_ARG, "%s: NULL cache", fn);
     if (heads[c] < 1 || heads[c] > 65535 || token_bytes[c] < 1 || token_bytes[c] > (1 << 20) ||
         heads[c] * token_bytes[c] > (1LL << 30) ||
         heads[c] * token_bytes[c] >= (1LL << 46) / rows)
       return pkv::fail(PKV_E_BAD_ARG, "%s: cache %d: bad heads or token_bytes", fn, c);
+    const uintptr_t base = reinterpret_cast<uintptr_t>(caches[c]);
+    ascending = ascending && base >= end;
+    end = base + static_cast<uintptr_t>(heads[c] * token_bytes[c] * rows);
+  }
+  // The move is in place and each cache's CTAs know nothing of another's: one that is named again
+  // (layers may share one) is left to the first, what overlaps otherwise is refused.
+  std::unique_ptr<int[]> order;
+  int n_all = n_caches;
+  if (!ascending) {
+    order.reset(new (std::nothrow) int[n_caches]);
+    if (!order) return pkv::fail(PKV_E_BAD_ARG, "%s: no memory for %d caches", fn, n_caches);
+    std::iota(order.get(), order.get() + n_caches, 0);
+    const std::less<const void *> before;
+    std::sort(order.get(), order.get() + n_caches, [&](int x, int y) {
+      return caches[x] == caches[y] ? x < y : before(caches[x], caches[y]);
+    });
+    n_all = 1;
+    for (int i = 1; i < n_caches; ++i) {
+      const int x = order[n_all - 1], y = order[i];   // x: the last that is kept
+      if (caches[x] == caches[y] && heads[x] == heads[y] && token_bytes[x] == token_bytes[y])
+        continue;
+      if (reinterpret_cast<uintptr_t>(caches[y]) - reinterpret_cast<uintptr_t>(caches[x]) <
+          static_cast<uintptr_t>(heads[x] * token_bytes[x] * rows))
+        return pkv::fail(PKV_E_BAD_ARG, "%s: caches %d and %d overlap", fn, x, y);
+      order[n_all++] = y;
+    }
   }
   KeepArgs a;
   a.table = dev_table;
@@ -165,17 +199,18 @@ extern "C" int kv_keep_path(void *const *caches, const int *heads, const int64_t
   a.page_size = page_size;
   a.n_pages = n_pages;
   a.path_cols = path_cols;
-  for (int c0 = 0; c0 < n_caches; c0 += kMaxCaches) {
+  for (int c0 = 0; c0 < n_all; c0 += kMaxCaches) {
     long long blocks = 0;
-    const int n = n_caches - c0 < kMaxCaches ? n_caches - c0 : kMaxCaches;
+    const int n = n_all - c0 < kMaxCaches ? n_all - c0 : kMaxCaches;
     for (int i = 0; i < n; ++i) {
       Cache &k = a.cache[i];
-      k.base = static_cast<unsigned char *>(caches[c0 + i]);
-      const int64_t bytes = token_bytes[c0 + i];
+      const int c = order ? order[c0 + i] : c0 + i;
+      k.base = static_cast<unsigned char *>(caches[c]);
+      const int64_t bytes = token_bytes[c];
       const uintptr_t both = reinterpret_cast<uintptr_t>(k.base) | bytes;
       k.vec = both % 16 == 0 ? 16 : both % 4 == 0 ? 4 : 1;
       k.words.set(static_cast<uint32_t>(bytes / k.vec));
-      k.heads = heads[c0 + i];
+      k.heads = heads[c];
       k.block0 = static_cast<uint32_t>(blocks);
       blocks += (k.heads * static_cast<long long>(k.words.d) + kThreads - 1) / kThreads;
     }
