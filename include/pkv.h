@@ -599,7 +599,7 @@ int paged_decode_attn_noalloc(const pkv_bf16 *q, const pkv_bf16 *k_cache,
  * neither (no norm of q and k). rotary_dims as in qkv_norm_rope. The rotation
  * angle is exact to 2^-24 of a half turn at any position. Rows on slot 0 land
  * in page 0. Requires D in {64, 128, 256, 512}, Hq >= 1, Hkv >= 1, theta
- * finite and > 0, 16-byte aligned tensors. */
+ * finite and >= 2^-56, 16-byte aligned tensors. */
 int tree_qkv_norm_rope_append(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v,
                               int64_t q_stride, int64_t k_stride, int64_t v_stride,
                               const pkv_bf16 *gamma_q, const pkv_bf16 *gamma_k,

@@ -10,9 +10,10 @@
 // forward (norm, rotary, then the paged write), as qkv_norm_rope and kv_append have it.
 //
 // The angle is kept as a fraction of a turn in 64-bit fixed point: with F_i = 2^64
-// theta^(-2i/D) / (2 pi), computed once on the host, position * F_i modulo 2^64 is the exact
-// fraction however far the position (in fp32 the angle of position 30000 is off by 10^-3
-// radians already, more than the output's rounding).
+// theta^(-2i/D) / (2 pi) modulo 2^64, computed once on the host (turns.h), position * F_i modulo
+// 2^64 is the fraction to 2^-29 of a turn however far the position, and its nearest fp32 the angle
+// to 2^-24 of a half turn (in fp32 throughout the angle of position 30000 is off by 10^-3 radians
+// already, more than the output's rounding).
 //
 // Bound by its bytes where there are many nodes, else by latency: row_start, the row's entries,
 // the table and parents behind one another, with q, k and v on their way meanwhile. Measured:
@@ -25,6 +26,7 @@
 
 #include "pkv_internal.h"
 #include "tree.cuh"
+#include "turns.h"
 
 namespace {
 
@@ -198,19 +200,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
 
 template <int D>
 cudaError_t launch(const AppendArgs &a, float theta, int rotary_dims, cudaStream_t s) {
-  // the table of the thread's last theta and rotary_dims (2 us of powers; a model's layers have
-  // one or two of them)
+  // the table of the thread's last theta and rotary_dims (1 to 3 us of products; a model's
+  // layers have one or two of them)
   static thread_local Turns<D> t;
   static thread_local float t_theta = 0.f;
   static thread_local int t_rotary = -1;
   if (theta != t_theta || rotary_dims != t_rotary) {
-    for (int i = 0; i < D / 2; ++i) {
-      double f = i < rotary_dims / 2
-                     ? pow(static_cast<double>(theta), -2.0 * i / D) / (2.0 * M_PI)
-                     : 0.0;
-      f -= floor(f);
-      t.f[i] = f >= 1.0 ? 0 : static_cast<uint64_t>(ldexp(f, 64));
-    }
+    pkv::rotation_turns(theta, rotary_dims / 2, D, t.f);
+    for (int i = rotary_dims / 2; i < D / 2; ++i) t.f[i] = 0;
     t_theta = theta, t_rotary = rotary_dims;
   }
   const int want = (a.Hq + 2 * a.Hkv) * (D / 16);
@@ -239,8 +236,8 @@ extern "C" int tree_qkv_norm_rope_append(
     return pkv::fail(PKV_E_BAD_ARG, "%s: bad table geometry", fn);
   if (rotary_dims < 0 || rotary_dims > D || rotary_dims % 2)
     return pkv::fail(PKV_E_BAD_ARG, "%s: rotary_dims must be even and in [0, D]", fn);
-  if (!(theta > 0.f) || std::isinf(theta))
-    return pkv::fail(PKV_E_BAD_ARG, "%s: theta must be finite and > 0", fn);
+  if (!(theta >= pkv::kLeastTheta) || std::isinf(theta))
+    return pkv::fail(PKV_E_BAD_ARG, "%s: theta must be finite and at least 2^-56", fn);
   if (!(eps >= 0.f)) return pkv::fail(PKV_E_BAD_ARG, "%s: eps must be >= 0", fn);
   if ((gamma_q == nullptr) != (gamma_k == nullptr))
     return pkv::fail(PKV_E_BAD_ARG, "%s: give both gains or neither", fn);
