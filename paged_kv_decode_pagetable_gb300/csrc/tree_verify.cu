@@ -268,8 +268,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyAr
     return;
   }
   // The row's CTAs write into one another's shared memory, which exists once they have started:
-  // each tells the others here and hears of them before its first such write.
-  cluster.barrier_arrive();
+  // each tells the others here and hears of them before its first such write. (Relaxed: nothing
+  // was written for them to see.)
+  asm volatile("barrier.cluster.arrive.relaxed;");
   if (tid < n) {
     int bits = 0;
     const int t = a.tokens[n0 + tid];
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyAr
                          : sum_units<kLater>(r, ak, sh, size, u0, u1, a.V, warp, lane);
     if (lane == 0) sh.warp[warp] = s;
     __syncthreads();
-    if (turn == 0) cluster.barrier_wait();   // (by all threads, as they arrived)
+    if (turn == 0) asm volatile("barrier.cluster.wait;" ::: "memory");   // (all threads arrived)
     if (warp == 0) {
       const uint64_t mine = warp_sum(lane < kWarps ? sh.warp[lane] : 0);
       if (lane < ranks) *cluster.map_shared_rank(&sh.rank[turn & 1][rank], lane) = mine;
