@@ -580,7 +580,7 @@ int paged_decode_attn_noalloc(const pkv_bf16 *q, const pkv_bf16 *k_cache,
  * packed nodes outside every row are neither read nor written. A row whose
  * nodes lie outside [0, N) or are more than PKV_TREE_MAX, a path that does not
  * ascend (PKV_ERR_TREE), a bad slot (PKV_ERR_SLOT) or tokens beyond the table
- * row (PKV_ERR_POS) are reported and the row skipped; a parent that does not
+ * row or 2^31 - 1 (PKV_ERR_POS) are reported and the row skipped; a parent that does not
  * lie before its node is reported (PKV_ERR_TREE) and counts as -1. Rows on
  * slot 0 are padding. B <= 512 (65535 for tree_verify and kv_keep_path). Rows
  * name distinct slots, and pages that a row's nodes fall on must be its own

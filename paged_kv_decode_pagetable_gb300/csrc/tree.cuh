@@ -38,8 +38,9 @@ __device__ __forceinline__ TreeRow tree_row(int b, int N, const int32_t *row_sta
   }
   if (r.n == 0) return r;   // an empty row names nothing else
   if (r.slot < 0 || r.slot >= n_slots) r.bits |= PKV_ERR_SLOT;
+  // (positions are 32-bit numbers, also where a table row has room for more)
   if (r.ctx < 0 || static_cast<long long>(r.ctx) + (n1 - n0) >
-                       static_cast<long long>(max_pages) * page_size)
+                       min(static_cast<long long>(max_pages) * page_size, 0x7fffffffLL))
     r.bits |= PKV_ERR_POS;
   if (r.bits) r.n = 0;
   return r;
