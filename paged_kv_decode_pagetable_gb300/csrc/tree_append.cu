@@ -98,6 +98,15 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
     lo4[j] = hi4[j] = make_uint4(0, 0, 0, 0);
     if (h < heads && node0 + j < a.N) load(node0 + j, h, lo4[j], hi4[j]);
   }
+  if (blockIdx.x == 0 && warp == blockDim.x / 32 - 1) {
+    // rows outside the packed nodes are reported here: no node finds them
+    int bits = 0;
+    for (int i = lane; i < a.B; i += 32) {
+      const int n0 = a.row_start[i], n1 = a.row_start[i + 1];
+      if (n0 < 0 || n1 < n0 || n1 > a.N) bits = PKV_ERR_TREE;
+    }
+    tree_report(a.err, bits);
+  }
   for (int j = warp; j < EACH; j += blockDim.x / 32) {
     const int node = node0 + j;
     int before = 0;   // the node's row: the last that starts at or before it
