@@ -202,8 +202,9 @@ def tree_layer_step(spec: LayerSpec, pt: PageTable, k_cache, v_cache, q, k, v, b
     if spec.gemma_options and not spec.rope:
         raise ValueError("rotary_dims, v_norm and k_eq_v need a rotary layer")
     geometry = (table, pt.n_slots, pt.max_pages_per_seq, pt.page_size, pt.n_pages)
-    tree_qkv_norm_rope_append(q, k, None if spec.k_eq_v else v, gamma_q if spec.qk_norm else None,
-                              gamma_k if spec.qk_norm else None, batch_idx, ctx_lens, row_start,
+    norm = spec.qk_norm and spec.rope     # (decode_layer_step leaves other layers' q and k too)
+    tree_qkv_norm_rope_append(q, k, None if spec.k_eq_v else v, gamma_q if norm else None,
+                              gamma_k if norm else None, batch_idx, ctx_lens, row_start,
                               parents, spec.theta, eps,
                               (spec.rotary_dims or None) if spec.rope else 0, spec.v_norm,
                               *geometry, k_cache, v_cache, q_out, err, stream=stream)
