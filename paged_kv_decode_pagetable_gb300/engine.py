@@ -205,7 +205,7 @@ def tree_layer_step(spec: LayerSpec, pt: PageTable, k_cache, v_cache, q, k, v, b
     norm = spec.qk_norm and spec.rope     # (decode_layer_step leaves other layers' q and k too)
     tree_qkv_norm_rope_append(q, k, None if spec.k_eq_v else v, gamma_q if norm else None,
                               gamma_k if norm else None, batch_idx, ctx_lens, row_start,
-                              parents, spec.theta, eps,
+                              parents, spec.theta if spec.rope else 1.0, eps,
                               (spec.rotary_dims or None) if spec.rope else 0, spec.v_norm,
                               *geometry, k_cache, v_cache, q_out, err, stream=stream)
     paged_tree_attn(q_out, k_cache, v_cache, *geometry, batch_idx, ctx_lens, row_start, parents,

@@ -48,3 +48,16 @@ def test_norm_and_rotation(qk_norm, rope, gains, monkeypatch):
     norm = "qk_norm_rope" in decode and decode["qk_norm_rope"][2] is not None
     assert (gq != 0, gk != 0) == (norm, norm)
     assert rotary == (D if "qk_norm_rope" in decode else 0)
+
+
+@pytest.mark.parametrize("theta", [0.0, float("inf"), -1.0])
+def test_a_layer_without_rotation_needs_no_theta(theta, monkeypatch):
+    spec = engine.LayerSpec(head_dim=D, theta=theta, rope=False)
+    got = {}
+    monkeypatch.setattr(engine, "tree_qkv_norm_rope_append", lambda *a, **k: got.update(a=a))
+    monkeypatch.setattr(engine, "paged_tree_attn", lambda *a, **k: None)
+    pt = type("Geometry", (), dict(dev_table=None, n_slots=3, max_pages_per_seq=2, page_size=16,
+                                   n_pages=4))
+    engine.tree_layer_step(spec, pt, *[None] * 11, type("Workspace", (), dict(buf=None)))
+    theta, rotary = got["a"][9], got["a"][11]
+    assert rotary == 0 and 2.0 ** -56 <= theta < float("inf")
