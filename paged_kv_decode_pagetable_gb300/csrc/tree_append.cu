@@ -17,7 +17,7 @@
 //
 // Bound by its bytes where there are many nodes, else by latency: row_start, the row's entries,
 // the table and parents behind one another, with q, k and v on their way meanwhile. Measured:
-// 1152 nodes of 32 + 8 + 8 heads of 128, 28 MB, 9.2 us (0.45 of 6769 GB/s); 18.5 with a CTA a
+// 1152 nodes of 32 + 8 + 8 heads of 128, 28 MB, 9.1 us (0.45 of 6769 GB/s); 18.5 with a CTA a
 // node, whose 1152 looked their rows up in three waves; 40 nodes 3.8 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

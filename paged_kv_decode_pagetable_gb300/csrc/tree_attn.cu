@@ -20,7 +20,9 @@
 // more than 2^8, and only where one does (a unit's first tile, and few others) the maxima are
 // reduced, the references moved and O scaled. The weights' sums are a third product, with ones in
 // V's place: every lane of TMEM has them, and no thread keeps a sum for each column. Weights are
-// rounded to bf16 (V's type) and summed as rounded; scores, references and O are fp32.
+// rounded to bf16, V's type, for both operands of a product have one (an error of 0.0022 of the
+// outputs' size, not the 0.0017 of rounding those alone), and summed as rounded; scores, references
+// and O are fp32.
 //
 // Work: the units' tiles and one or two more places for each unit's start lie on one line, cut into
 // equal shares for one persistent CTA an SM from the lengths, on the device. A unit that is cut
@@ -51,13 +53,13 @@
 // the loops kept as loops, the short waits, and one site of each product.
 //
 // Measured (6769 GB/s measured): 16 rows of 16k to 32k tokens, 8-node chains, 8 heads of 128,
-// 240 us, 0.99 of reading them; 64 rows of 100 to 1024 tokens, trees of 8, 36 us, 0.63: its start
+// 241 us, 0.99 of reading them; 64 rows of 100 to 1024 tokens, trees of 8, 36 us, 0.64: its start
 // (launch, plan, the rings' first fill) and its end (last tiles, join) are 6 us each; 64 rows of
-// 256 to 2048 tokens in a window of 512, trees of 16, one head of 256, 27 us, 0.21, and 16 rows
+// 256 to 2048 tokens in a window of 512, trees of 16, one head of 256, 26 us, 0.22, and 16 rows
 // with trees of 64, one head of 512, 48 us, 0.16: they write and read as many bytes in parts as
 // in keys, at D = 512 every 8 nodes read the keys again, and a tile's weights, P V and the next
-// one's weights stand behind one another (there is no room for a second P); one row of 41 tokens
-// 4.4 us.
+// one's weights stand behind one another (at 512 there is no room for a second P); one row of 41
+// tokens 4.4 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -98,7 +100,7 @@ struct Cfg {
   // Places on the line for a unit's start and end: where units go in twos one's overlap the other's
   // tiles (2 and 3: 40 and 42 us for the rollout batch, not 39, at the time), else they take as
   // long as two tiles (16 rows with trees of 64, one head of 512 51 -> 48 us; 64 rows of up to 1k
-  // tokens with trees of 24, eight heads of 128 64 -> 57).
+  // tokens with trees of 24, eight heads of 128 64 -> 56).
   static constexpr int START = UNITS == 2 ? 1 : 2;
   static constexpr int SOFT = 8;                        // softmax warps of all units
   static constexpr int PROD = SOFT, PREP = SOFT + 2, MMA = SOFT + 3;
@@ -241,7 +243,8 @@ __device__ __forceinline__ bool group_any(int grp, bool mine) {
 __device__ __forceinline__ void group_sync(int grp) {
   asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + grp) : "memory");
 }
-// the maximum over the 32 lanes (NaN only where all are)
+// the maximum over the 32 lanes (NaN only where all are); volatile, for it names all lanes and must
+// not be moved under the branch of the one that uses it
 __device__ __forceinline__ float lane_max(float x) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));

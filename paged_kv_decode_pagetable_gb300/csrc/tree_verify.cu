@@ -20,10 +20,10 @@
 // over a row is one of the target's V words. A cluster of up to 8 CTAs shares a row: each sums
 // a contiguous part, the sums cross through distributed shared memory, and the warp whose part
 // holds the threshold reads the group of words with it again for the token. Measured (floors at
-// 6769 GB/s): 64 rows of 5 sampled drafts, 151936 words, 19.5 us (11.5), where a row's 4 CTAs meet
-// after each pass; 16 trees of the likeliest tokens, 262144 words, 12.0 us (2.5): a chain of
+// 6769 GB/s): 64 rows of 5 sampled drafts, 151936 words, 20.1 us (11.5), where a row's 4 CTAs meet
+// after each pass; 16 trees of the likeliest tokens, 262144 words, 12.2 us (2.5): a chain of
 // dependent steps down the path, each a few words, then one pass; one row of 3 drafts, 32000
-// words, 6.2 us. With 64-bit conversions for the sums and a search through a warp's whole part the
+// words, 6.5 us. With 64-bit conversions for the sums and a search through a warp's whole part the
 // 64 rows took 44 us.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
